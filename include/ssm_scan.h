@@ -3,7 +3,9 @@
  * (libssmscan.so).
  *
  * The library computes the forward linear recurrence at the core of
- * Mamba-style state-space layers, in two forms:
+ * Mamba-style state-space layers, in two forms (and, further down, a gated
+ * linear recurrence with its gradients and single-token step, 8-bit
+ * activation checkpoints, and the pages of a state cache):
  *
  *   ssm_scan_fwd / ssm_scan_fwd_bf16  -- diagonal A (one decay per channel
  *       and state).  Shape API of selective_scan / selective_scan_seq in
@@ -350,6 +352,125 @@ SSM_API ssm_status_t ssd_chunk_scan_bwd_ex(const void *x, const void *dt, const 
                                            int64_t L, int64_t H, int64_t P, int64_t N,
                                            int bidirectional, int input_bf16,
                                            const ssm_scan_options_t *opts, void *stream);
+
+/*
+ * Gated linear recurrence: one decay per channel and step, set by a gate.
+ *   x, gate_r, gate_i : (Bs, L, ED), fp32 (input_bf16 == 0) or bf16
+ *   lam : (ED) fp32         c : > 0, finite
+ *   s_r = 1 / (1 + e^-gate_r),  s_i = 1 / (1 + e^-gate_i)
+ *   la_t = -c softplus(lam) s_r,  a_t = e^la_t,  m_t = sqrt(1 - e^(2 la_t))
+ *   h_t = a_t h_{t-1} + m_t s_i x_t,   h_{-1} = h0 (0 when NULL)
+ *   y   : (Bs, L, ED), x's type: h_t rounded once; the state itself is fp32
+ *   reset : (Bs, L) bytes or NULL.  A step whose byte is not 0 drops the
+ *           state before it (a_t = 0, m_t = 1), whatever that holds, an
+ *           infinity or NaN included: the first token of a packed sequence.
+ *   h0, h_final : (Bs, ED) fp32 or NULL; h_final = h_{L-1}
+ *   saved : NULL, or what the backward pass needs (every array caller-owned
+ *           and fully written): states, and with x_q != NULL (then all six)
+ *           the 8-bit checkpoints of x, gate_r and gate_i, in the format of
+ *           ckpt8_save for (Bs L) rows of ED columns.
+ * Any Bs in 1..65535 and L, ED >= 1.  Every pointer is aligned to its
+ * element size (SSM_ERR_ALIGNMENT otherwise).
+ */
+#define SSM_GATED_BLOCK 64      /* steps between two kept states */
+typedef struct gated_scan_saved {
+    float *states;              /* (Bs, ceil(L / 64), ED): h before step 0, 64, 128, ... */
+    int8_t *x_q, *r_q, *i_q;    /* (Bs, L, ED) or all NULL */
+    float *x_s, *r_s, *i_s;     /* (ceil(ED / 64), Bs L) or all NULL */
+} gated_scan_saved_t;
+
+SSM_API ssm_status_t gated_scan_fwd(const void *x, const void *gate_r, const void *gate_i,
+                                    const float *lam, float c, const uint8_t *reset,
+                                    const float *h0, void *y, float *h_final,
+                                    const gated_scan_saved_t *saved, int64_t Bs, int64_t L,
+                                    int64_t ED, int input_bf16, void *stream);
+
+/*
+ * Gradients of gated_scan_fwd for dy, the gradient of a loss with respect to
+ * y, and dh_final, the one with respect to h_final (NULL = 0).
+ *   dy : (Bs, L, ED) fp32 or bf16 (io_bf16), as x was;  dh_final : (Bs, ED) fp32
+ *   dx, dgate_r, dgate_i : (Bs, L, ED) of dy's type;  dlam : (ED) fp32
+ *   dh0 : (Bs, ED) fp32 or NULL
+ * `saved` is what the forward call wrote.  With x_q != NULL the gradients are
+ * those at the values that the 8-bit checkpoints stand for, and x, gate_r,
+ * gate_i are not read (may be NULL).  The states inside a block of 64 steps
+ * are recomputed from the one kept at its start.  At a reset step the decay
+ * is the constant 0: no gradient reaches gate_r, lam or an earlier state.
+ * Deterministic (dlam is summed in a fixed order).  Takes stream-ordered
+ * scratch of 4 Bs ED bytes for each part of the time axis that runs at once.
+ * Sizes and alignment as gated_scan_fwd.
+ */
+SSM_API ssm_status_t gated_scan_bwd(const void *x, const void *gate_r, const void *gate_i,
+                                    const float *lam, float c, const uint8_t *reset,
+                                    const void *dy, const float *dh_final,
+                                    const gated_scan_saved_t *saved, void *dx, void *dgate_r,
+                                    void *dgate_i, float *dlam, float *dh0, int64_t Bs, int64_t L,
+                                    int64_t ED, int io_bf16, void *stream);
+
+/*
+ * One step of the gated recurrence for each row of a batch, on states kept in
+ * pages: states[pages[b]] is updated in place and y[b] is the new state.
+ *   x, gate_r, gate_i, y : (Bs, ED);  states : (num_pages, ED) fp32
+ *   pages : (Bs) int32 device array, or NULL (row b uses page b).  A row whose
+ *           page lies outside 0..num_pages-1 is idle: y[b] = 0 and no state
+ *           changes.  No page may be named twice.
+ */
+SSM_API ssm_status_t gated_scan_step(const void *x, const void *gate_r, const void *gate_i,
+                                     const float *lam, float c, float *states,
+                                     const int32_t *pages, void *y, int64_t Bs, int64_t ED,
+                                     int64_t num_pages, int input_bf16, void *stream);
+
+/*
+ * 8-bit activation checkpoints.  x (rows, cols) fp32 or bf16 is kept as
+ * q (rows, cols) int8 and scale (ceil(cols / 64), rows) fp32.  In a group of
+ * 64 columns of one row (the last group may be shorter), with top = max |x|:
+ *   scale = top * fl(1/127),  q = rint(x * fl(127 / top))   (ties to even)
+ * in fp32, each product rounded on its own; a group with top < 2^-100 is kept
+ * as zeros.  ckpt8_load gives q * scale, rounded once to x's type.  A group
+ * that holds a NaN or an infinity reads back as NaN as a whole.
+ */
+SSM_API ssm_status_t ckpt8_save(const void *x, int8_t *q, float *scale, int64_t rows, int64_t cols,
+                                int input_bf16, void *stream);
+SSM_API ssm_status_t ckpt8_load(const int8_t *q, const float *scale, void *x, int64_t rows,
+                                int64_t cols, int output_bf16, void *stream);
+
+/*
+ * Pages of a state cache.  A pool is (layers, num_pages, page_bytes) of any
+ * element type; page p of every layer belongs to one sequence.  A recurrent
+ * state is overwritten at every token, so a forked sequence takes a page of
+ * its own.  used : (num_pages) bytes, 0 = free.  Page lists are int32 device
+ * arrays of n >= 0 entries (n = 0: nothing to do); num_pages <= SSM_MAX_PAGES.
+ *   fork    : for each k, dst[k] = a page that was free, now in use, with
+ *             src[k]'s content (src[k] == -1: zeros, a new sequence).  The
+ *             valid requests take the lowest free pages in their order;
+ *             a request is valid when src[k] is -1 or in use.  dst[k] = -1
+ *             for the others, and once no page is free.
+ *   copy    : page src[k] to page dst[k] (src[k] == -1: zeros); an entry with
+ *             another page outside the pool is skipped.  No page may be
+ *             written twice, or both read and written.
+ *   free    : the listed pages become free; entries outside the pool are
+ *             skipped.
+ *   compact : the pages in use move to 0..n_used-1: the j-th one at or above
+ *             n_used goes to the j-th free page below it, the others stay.
+ *             moved (num_pages) int32 is each page's new number (-1 for a
+ *             free page); pages, a list of page numbers (NULL with n = 0), is
+ *             renumbered in place (negative entries stay, pages that were not
+ *             in use become -1).
+ * fork and compact take stream-ordered scratch of 4 num_pages and
+ * 8 num_pages + 8 bytes.
+ */
+#define SSM_MAX_PAGES (1ll << 24)
+SSM_API ssm_status_t state_pages_fork(void *pool, uint8_t *used, const int32_t *src, int32_t *dst,
+                                      int64_t n, int64_t layers, int64_t num_pages,
+                                      int64_t page_bytes, void *stream);
+SSM_API ssm_status_t state_pages_copy(void *pool, const int32_t *src, const int32_t *dst, int64_t n,
+                                      int64_t layers, int64_t num_pages, int64_t page_bytes,
+                                      void *stream);
+SSM_API ssm_status_t state_pages_free(uint8_t *used, const int32_t *pages, int64_t n,
+                                      int64_t num_pages, void *stream);
+SSM_API ssm_status_t state_pages_compact(void *pool, uint8_t *used, int32_t *moved, int32_t *pages,
+                                         int64_t n, int64_t layers, int64_t num_pages,
+                                         int64_t page_bytes, void *stream);
 
 /*
  * Synchronise `stream` and report whether a kernel of this library running on

@@ -20,7 +20,16 @@ ssd_chunk_scan_fwd(x, dt, A_head, B, C, D=None, chunk=256, bidirectional=False, 
     A_head: (H) fp32; B, C: (Bs, L, N) or (Bs, L, G, N) bf16 (head h reads
     group h // (H // G)); D: (H) fp32.  Returns y (Bs, L, H, P) fp32.
 
-Options (either function; any of them selects the ``*_ex`` C entry point):
+gated_scan_fwd(x, gate_r, gate_i, lam, c=8.0, ...), gated_scan_bwd, gated_scan_step
+    Gated linear recurrence (one decay per channel and step, set by a gate):
+    forward, gradients, and one token for rows whose states lie in pages.
+ckpt8_save(x), ckpt8_load(q, scale, dtype)
+    8-bit activation checkpoints; ``gated_scan_fwd(..., save="8bit")`` keeps
+    its inputs this way and ``gated_scan_bwd`` reads them so.
+state_pages_fork / _copy / _free / _compact
+    The pages of a state cache.
+
+Options (of the selective scans; any of them selects the ``*_ex`` C entry point):
 ``dt_bias`` (ED or H, fp32), ``dt_softplus``, ``dt_limit=(lo, hi)``, ``z``
 (shaped and typed like x), ``h0`` (fp32 initial state, (Bs, ED, N) or
 (Bs, H, P, N)) and ``return_final_state`` (the call then returns
@@ -35,6 +44,9 @@ from . import _build
 
 __all__ = ["ssm_scan_fwd", "ssm_scan_fwd_bf16", "ssd_chunk_scan_fwd", "ssm_check_device_errors",
            "ssm_scan_fwd_plan", "ssm_scan_bwd", "ssd_chunk_scan_bwd", "ScanOptions",
+           "gated_scan_fwd", "gated_scan_bwd", "gated_scan_step", "GatedSaved", "ckpt8_save",
+           "ckpt8_load", "state_pages_fork", "state_pages_copy", "state_pages_free",
+           "state_pages_compact",
            "SsmError", "library", "build", "status_string", "STATUS"]
 
 STATUS = {
@@ -45,6 +57,7 @@ STATUS = {
 # Every symbol include/ssm_scan.h declares, with its ctypes signature.
 _VP = ctypes.c_void_p
 _I64 = ctypes.c_int64
+_F32 = ctypes.c_float
 SIGNATURES = {
     "ssm_scan_fwd": ([_VP] * 7 + [_I64] * 4 + [_VP], ctypes.c_int),
     "ssm_scan_fwd_bf16": ([_VP] * 7 + [_I64] * 4 + [_VP], ctypes.c_int),
@@ -60,6 +73,15 @@ SIGNATURES = {
                               ctypes.c_int),
     "ssd_chunk_scan_fwd_ex": ([_VP] * 7 + [_I64] * 6 + [ctypes.c_int, ctypes.c_int, _VP, _VP],
                               ctypes.c_int),
+    "gated_scan_fwd": ([_VP] * 4 + [_F32] + [_VP] * 5 + [_I64] * 3 + [ctypes.c_int, _VP], ctypes.c_int),
+    "gated_scan_bwd": ([_VP] * 4 + [_F32] + [_VP] * 9 + [_I64] * 3 + [ctypes.c_int, _VP], ctypes.c_int),
+    "gated_scan_step": ([_VP] * 4 + [_F32] + [_VP] * 3 + [_I64] * 3 + [ctypes.c_int, _VP], ctypes.c_int),
+    "ckpt8_save": ([_VP] * 3 + [_I64] * 2 + [ctypes.c_int, _VP], ctypes.c_int),
+    "ckpt8_load": ([_VP] * 3 + [_I64] * 2 + [ctypes.c_int, _VP], ctypes.c_int),
+    "state_pages_fork": ([_VP] * 4 + [_I64] * 4 + [_VP], ctypes.c_int),
+    "state_pages_copy": ([_VP] * 3 + [_I64] * 4 + [_VP], ctypes.c_int),
+    "state_pages_free": ([_VP] * 2 + [_I64] * 2 + [_VP], ctypes.c_int),
+    "state_pages_compact": ([_VP] * 4 + [_I64] * 4 + [_VP], ctypes.c_int),
     "ssm_check_device_errors": ([_VP], ctypes.c_int),
     "ssm_selftest_wait_timeout": ([_VP], ctypes.c_int),
     "ssm_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -113,6 +135,11 @@ def _options(x, channels, state_shape, dev, dt_bias=None, dt_softplus=False, dt_
         hf = torch.empty(state_shape, dtype=torch.float32, device=dev)
         o.h_final = hf.data_ptr()
     return o, hf, keep
+
+
+class GatedSaved(ctypes.Structure):
+    """gated_scan_saved_t of include/ssm_scan.h."""
+    _fields_ = [(n, _VP) for n in ("states", "x_q", "r_q", "i_q", "x_s", "r_s", "i_s")]
 
 
 class SsmError(RuntimeError):
@@ -401,3 +428,308 @@ def ssm_check_device_errors(device=None) -> None:
     st = library().ssm_check_device_errors(_stream(dev))
     if st != 0:
         raise SsmError("ssm_check_device_errors", st)
+
+
+# ---- gated linear recurrence -----------------------------------------------------------
+_BLOCK = 64      # SSM_GATED_BLOCK: steps between kept states; also columns that share an 8-bit scale
+_CKPT8 = ("x_q", "r_q", "i_q", "x_s", "r_s", "i_s")
+
+
+def _call(name, *args):
+    st = getattr(library(), name)(*args)
+    if st != 0:
+        raise SsmError(name, st)
+
+
+def _saved_shapes(Bs, L, ED):
+    q, s = (Bs, L, ED), (-(-ED // _BLOCK), Bs * L)
+    return dict(states=(Bs, -(-L // _BLOCK), ED), x_q=q, r_q=q, i_q=q, x_s=s, r_s=s, i_s=s)
+
+
+def _saved_struct(saved):
+    o = GatedSaved()
+    for k, t in saved.items():
+        setattr(o, k, t.data_ptr())
+    return o
+
+
+def _gated_inputs(x, gate_r, gate_i, lam, ndim):
+    import torch
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    _check(x, "x", (torch.bfloat16, torch.float32), dev, (ndim,))
+    for t, n in ((gate_r, "gate_r"), (gate_i, "gate_i")):
+        if t is None:
+            raise TypeError("%s must be a torch.Tensor" % n)
+        _check(t, n, (x.dtype,), dev, (ndim,))
+        if t.shape != x.shape:
+            raise ValueError("%s must have the shape of x" % n)
+    if lam is None:
+        raise TypeError("lam must be a torch.Tensor")
+    _check(lam, "lam", (torch.float32,), dev, (1,))
+    if lam.shape[0] != x.shape[-1]:
+        raise ValueError("lam must have %d entries" % x.shape[-1])
+    return dev
+
+
+def _check_shape(t, name, dtypes, dev, shape):
+    _check(t, name, dtypes, dev)
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def gated_scan_fwd(x, gate_r, gate_i, lam, c=8.0, reset=None, h0=None, return_final_state=False,
+                   save=None, y=None):
+    """Gated linear recurrence on the current CUDA stream:
+
+        a_t = exp(-c softplus(lam) sigmoid(gate_r)),  h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(gate_i) x_t
+
+    x, gate_r, gate_i: (Bs, L, ED) bf16 or fp32; lam: (ED) fp32; reset: (Bs, L)
+    bool or uint8, true where a sequence starts (the state before it is
+    dropped); h0: (Bs, ED) fp32.  Returns y (Bs, L, ED) in x's type; with
+    ``return_final_state`` also h_final (Bs, ED) fp32; with ``save`` also the
+    dict that ``gated_scan_bwd`` takes: ``save="states"`` keeps the state
+    every 64 steps (the caller keeps x, gate_r, gate_i), ``save="8bit"`` also
+    the 8-bit checkpoints of x, gate_r and gate_i in their place."""
+    import torch
+    dev = _gated_inputs(x, gate_r, gate_i, lam, 3)
+    Bs, L, ED = x.shape
+    _check_shape(reset, "reset", (torch.uint8, torch.bool), dev, (Bs, L))
+    _check_shape(h0, "h0", (torch.float32,), dev, (Bs, ED))
+    if save not in (None, "states", "8bit"):
+        raise ValueError("save must be None, 'states' or '8bit'")
+    if y is None:
+        y = torch.empty_like(x)
+    _check_shape(y, "y", (x.dtype,), dev, x.shape)
+    hf = torch.empty((Bs, ED), dtype=torch.float32, device=dev) if return_final_state else None
+    saved = None
+    if save is not None:
+        shapes = _saved_shapes(Bs, L, ED)
+        keys = ("states",) if save == "states" else ("states",) + _CKPT8
+        saved = {k: torch.empty(shapes[k], dtype=torch.int8 if k.endswith("_q") else torch.float32,
+                                device=dev) for k in keys}
+    _call("gated_scan_fwd", _ptr(x), _ptr(gate_r), _ptr(gate_i), _ptr(lam), float(c), _ptr(reset),
+          _ptr(h0), _ptr(y), _ptr(hf), None if saved is None else ctypes.byref(_saved_struct(saved)),
+          Bs, L, ED, int(x.dtype == torch.bfloat16), _stream(dev))
+    out = (y,) + ((hf,) if return_final_state else ()) + ((saved,) if save is not None else ())
+    return out if len(out) > 1 else y
+
+
+def gated_scan_bwd(x, gate_r, gate_i, lam, dy, saved, c=8.0, reset=None, dh_final=None):
+    """Gradients of ``gated_scan_fwd`` for dy (Bs, L, ED), of x's type:
+    dict(dx, dgate_r, dgate_i) of dy's type, dlam (ED) and dh0 (Bs, ED) fp32.
+    ``saved`` is the forward call's dict; where it holds the 8-bit checkpoints
+    they are read in the place of x, gate_r and gate_i, which may be None.
+    dh_final: (Bs, ED) fp32, the gradient with respect to the final state."""
+    import torch
+    if not isinstance(dy, torch.Tensor):
+        raise TypeError("dy must be a torch.Tensor")
+    dev = dy.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    _check(dy, "dy", (torch.bfloat16, torch.float32), dev, (3,))
+    Bs, L, ED = dy.shape
+    if not isinstance(saved, dict) or "states" not in saved or set(saved) not in (
+            {"states"}, {"states", *_CKPT8}):
+        raise ValueError("saved must be the dict of gated_scan_fwd(..., save='states' or '8bit')")
+    if "x_q" in saved:
+        x = gate_r = gate_i = None
+        _check(lam, "lam", (torch.float32,), dev, (1,))
+        if lam is None or lam.shape[0] != ED:
+            raise ValueError("lam must have %d entries" % ED)
+    else:
+        if _gated_inputs(x, gate_r, gate_i, lam, 3) != dev:
+            raise ValueError("x is on %s, expected %s" % (x.device, dev))
+        if x.dtype != dy.dtype or x.shape != dy.shape:
+            raise ValueError("dy must have the shape and type of x")
+    for k, shape in _saved_shapes(Bs, L, ED).items():
+        if k in saved:
+            if saved[k] is None:
+                raise ValueError("saved[%r] is missing" % k)
+            _check_shape(saved[k], "saved[%r]" % k,
+                         (torch.int8 if k.endswith("_q") else torch.float32,), dev, shape)
+    _check_shape(reset, "reset", (torch.uint8, torch.bool), dev, (Bs, L))
+    _check_shape(dh_final, "dh_final", (torch.float32,), dev, (Bs, ED))
+    g = {k: torch.empty_like(dy) for k in ("dx", "dgate_r", "dgate_i")}
+    g["dlam"] = torch.empty(ED, dtype=torch.float32, device=dev)
+    g["dh0"] = torch.empty((Bs, ED), dtype=torch.float32, device=dev)
+    _call("gated_scan_bwd", _ptr(x), _ptr(gate_r), _ptr(gate_i), _ptr(lam), float(c), _ptr(reset),
+          _ptr(dy), _ptr(dh_final), ctypes.byref(_saved_struct(saved)), _ptr(g["dx"]),
+          _ptr(g["dgate_r"]), _ptr(g["dgate_i"]), _ptr(g["dlam"]), _ptr(g["dh0"]), Bs, L, ED,
+          int(dy.dtype == torch.bfloat16), _stream(dev))
+    return g
+
+
+def gated_scan_step(x, gate_r, gate_i, lam, states, pages=None, c=8.0, y=None):
+    """One token of the gated recurrence for each row of a batch.
+    x, gate_r, gate_i: (Bs, ED) bf16 or fp32; states: (num_pages, ED) fp32,
+    updated in place at row b's page pages[b] ((Bs) int32; None: page b).  A
+    row whose page lies outside the pool is idle: y is 0, no state changes.
+    Returns y (Bs, ED) in x's type."""
+    import torch
+    dev = _gated_inputs(x, gate_r, gate_i, lam, 2)
+    Bs, ED = x.shape
+    if states is None:
+        raise TypeError("states must be a torch.Tensor")
+    _check(states, "states", (torch.float32,), dev, (2,))
+    if states.shape[1] != ED:
+        raise ValueError("states must have %d columns" % ED)
+    _check_shape(pages, "pages", (torch.int32,), dev, (Bs,))
+    if pages is None and states.shape[0] < Bs:
+        raise ValueError("states has fewer pages than x has rows")
+    if y is None:
+        y = torch.empty_like(x)
+    _check_shape(y, "y", (x.dtype,), dev, x.shape)
+    _call("gated_scan_step", _ptr(x), _ptr(gate_r), _ptr(gate_i), _ptr(lam), float(c), _ptr(states),
+          _ptr(pages), _ptr(y), Bs, ED, states.shape[0], int(x.dtype == torch.bfloat16), _stream(dev))
+    return y
+
+
+# ---- 8-bit activation checkpoints ------------------------------------------------------
+def ckpt8_save(x):
+    """(q, scale) of an activation tensor (bf16 or fp32, at least one
+    dimension): q int8 shaped like x, scale fp32 (ceil(cols / 64), rows), where
+    cols is x's last dimension and rows all others; 64 columns of a row share a
+    scale."""
+    import torch
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    _check(x, "x", (torch.bfloat16, torch.float32), dev)
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    cols = x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    q = torch.empty(x.shape, dtype=torch.int8, device=dev)
+    scale = torch.empty((-(-cols // _BLOCK), rows), dtype=torch.float32, device=dev)
+    _call("ckpt8_save", _ptr(x), _ptr(q), _ptr(scale), rows, cols, int(x.dtype == torch.bfloat16),
+          _stream(dev))
+    return q, scale
+
+
+def ckpt8_load(q, scale, dtype=None, out=None):
+    """The values q * scale of ``ckpt8_save``'s result in ``dtype`` (bf16, the
+    default, or fp32), shaped like q."""
+    import torch
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    _check(q, "q", (torch.int8,), dev)
+    if q.dim() < 1:
+        raise ValueError("q must have at least one dimension")
+    cols = q.shape[-1]
+    rows = q.numel() // cols if cols else 0
+    if scale is None:
+        raise TypeError("scale must be a torch.Tensor")
+    _check_shape(scale, "scale", (torch.float32,), dev, (-(-cols // _BLOCK), rows))
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16 if dtype is None else dtype, device=dev)
+    _check_shape(out, "out", (torch.bfloat16, torch.float32) if dtype is None else (dtype,), dev,
+                 q.shape)
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out must be bf16 or fp32")
+    _call("ckpt8_load", _ptr(q), _ptr(scale), _ptr(out), rows, cols, int(out.dtype == torch.bfloat16),
+          _stream(dev))
+    return out
+
+
+# ---- pages of a state cache ------------------------------------------------------------
+def _pool_sizes(pool, page_dim):
+    """(device, layers, pages, bytes of a page of one layer) of a pool."""
+    import torch
+    if not isinstance(pool, torch.Tensor):
+        raise TypeError("pool must be a torch.Tensor")
+    if pool.device.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if not pool.is_contiguous():
+        raise ValueError("pool must be contiguous")
+    if not 0 <= page_dim < pool.dim():
+        raise ValueError("page_dim must name a dimension of pool")
+    shape = pool.shape
+    layers = page = 1
+    for n in shape[:page_dim]:
+        layers *= n
+    for n in shape[page_dim + 1:]:
+        page *= n
+    return pool.device, layers, shape[page_dim], page * pool.element_size()
+
+
+def _page_list(t, name, dev):
+    import torch
+    if t is None:
+        raise TypeError("%s must be a torch.Tensor" % name)
+    _check(t, name, (torch.int32,), dev, (1,))
+
+
+def _used(used, dev, num_pages):
+    import torch
+    if used is None:
+        raise TypeError("used must be a torch.Tensor")
+    _check_shape(used, "used", (torch.uint8, torch.bool), dev, (num_pages,))
+
+
+def state_pages_fork(pool, used, src, page_dim=0):
+    """Give each request of ``src`` (int32 page numbers; -1: a new sequence) a
+    page of its own: the lowest free pages in the requests' order, with a copy
+    of page src[k] of every layer, or zeros.  pool: (..., pages, ...) with its
+    pages along ``page_dim``, the dimensions before it being layers; used:
+    (pages) uint8 or bool, updated in place.  Returns the int32 page numbers,
+    -1 where src[k] is not in use or no page was free."""
+    import torch
+    dev, layers, n_pages, size = _pool_sizes(pool, page_dim)
+    _used(used, dev, n_pages)
+    _page_list(src, "src", dev)
+    dst = torch.empty_like(src)
+    _call("state_pages_fork", _ptr(pool), _ptr(used), _ptr(src), _ptr(dst), src.shape[0], layers,
+          n_pages, size, _stream(dev))
+    return dst
+
+
+def state_pages_copy(pool, src, dst, page_dim=0):
+    """Copy page src[k] to page dst[k] of every layer (src[k] == -1: zeros).
+    An entry with another page outside the pool is skipped.  No page may be
+    written twice, or both read and written."""
+    dev, layers, n_pages, size = _pool_sizes(pool, page_dim)
+    _page_list(src, "src", dev)
+    _page_list(dst, "dst", dev)
+    if src.shape != dst.shape:
+        raise ValueError("src and dst must have the same length")
+    _call("state_pages_copy", _ptr(pool), _ptr(src), _ptr(dst), src.shape[0], layers, n_pages, size,
+          _stream(dev))
+
+
+def state_pages_free(used, pages):
+    """Mark the listed pages free; entries outside the pool are skipped."""
+    import torch
+    if not isinstance(used, torch.Tensor):
+        raise TypeError("used must be a torch.Tensor")
+    dev = used.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    _check(used, "used", (torch.uint8, torch.bool), dev, (1,))
+    _page_list(pages, "pages", dev)
+    _call("state_pages_free", _ptr(used), _ptr(pages), pages.shape[0], used.shape[0], _stream(dev))
+
+
+def state_pages_compact(pool, used, pages=None, page_dim=0):
+    """Move the pages in use to the front of the pool: the j-th one at or
+    above their number goes to the j-th free page below it, the others stay.
+    used is updated in place, and so is ``pages``, a list of page numbers
+    (negative entries stay, pages not in use become -1).  Returns each page's
+    new number ((pages) int32, -1 for a free page)."""
+    import torch
+    dev, layers, n_pages, size = _pool_sizes(pool, page_dim)
+    _used(used, dev, n_pages)
+    if pages is not None:
+        _page_list(pages, "pages", dev)
+    moved = torch.empty(n_pages, dtype=torch.int32, device=dev)
+    _call("state_pages_compact", _ptr(pool), _ptr(used), _ptr(moved), _ptr(pages),
+          0 if pages is None else pages.shape[0], layers, n_pages, size, _stream(dev))
+    return moved

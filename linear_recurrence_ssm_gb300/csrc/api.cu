@@ -3,9 +3,11 @@
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
+#include <float.h>
 #include <limits.h>
 #include <mutex>
 
+#include "gated_scan.cuh"
 #include "ssm_common.cuh"
 
 namespace ssm {
@@ -60,6 +62,42 @@ template <typename Tin>
 cudaError_t launch(const Tin *x, const Tin *dt, const float *A_head, const Tin *Bm, const Tin *Cm,
                    const float *D, float *y, int64_t Bs, int64_t L, int64_t H, int64_t P,
                    int64_t N, bool bidir, int num_sms, const ScanOpts *opt, cudaStream_t st);
+}
+namespace gated {
+template <typename T>
+cudaError_t launch_fwd(const T *x, const T *gr, const T *gi, const float *lam, float c,
+                       const uint8_t *reset, const float *h0, T *y, float *h_final,
+                       const Kept &kept, int64_t Bs, int64_t L, int64_t ED, int num_sms,
+                       cudaStream_t st);
+template <typename T>
+cudaError_t launch_step(const T *x, const T *gr, const T *gi, const float *lam, float c,
+                        float *states, const int32_t *pages, T *y, int64_t Bs, int64_t ED,
+                        int64_t num_pages, cudaStream_t st);
+}
+namespace gated_bwd {
+template <typename T>
+cudaError_t launch(const T *x, const T *gr, const T *gi, const float *lam, float c,
+                   const uint8_t *reset, const T *dy, const float *dh_final,
+                   const gated::Kept &kept, T *dx, T *dr, T *di, float *dlam, float *dh0,
+                   int64_t Bs, int64_t L, int64_t ED, int num_sms, cudaStream_t st);
+}
+namespace ckpt8 {
+template <typename T>
+cudaError_t save(const T *x, int8_t *q, float *scale, int64_t rows, int64_t cols, cudaStream_t st);
+template <typename T>
+cudaError_t load(const int8_t *q, const float *scale, T *x, int64_t rows, int64_t cols,
+                 cudaStream_t st);
+}
+namespace pages {
+cudaError_t copy(void *pool, const int32_t *src, const int32_t *dst, int64_t n, int64_t layers,
+                 int64_t num_pages, int64_t bytes, int num_sms, cudaStream_t st);
+cudaError_t fork(void *pool, uint8_t *used, const int32_t *src, int32_t *dst, int64_t n,
+                 int64_t layers, int64_t num_pages, int64_t bytes, int num_sms, cudaStream_t st);
+cudaError_t free_pages(uint8_t *used, const int32_t *pages, int64_t n, int64_t num_pages,
+                       cudaStream_t st);
+cudaError_t compact(void *pool, uint8_t *used, int32_t *moved, int32_t *pages, int64_t n,
+                    int64_t layers, int64_t num_pages, int64_t bytes, int num_sms,
+                    cudaStream_t st);
 }
 namespace bidir {
 cudaError_t take_device_error(unsigned int *out);
@@ -247,6 +285,120 @@ ssm_status_t ssd_entry(const void *x, const void *dt, const float *A_head, const
                                       A_head, static_cast<const bf *>(B),
                                       static_cast<const bf *>(C), D, y, Bs, L, H, P, N, chunk,
                                       bidirectional != 0, dev.num_sms, st, opts ? &o : nullptr));
+}
+
+bool pages_ok(int64_t n, int64_t num_pages) {
+    return n >= 0 && n <= INT_MAX && num_pages >= 1;
+}
+
+// What a gated forward call writes and a backward call reads; `need` says
+// whether the states must be there.
+ssm_status_t check_saved(const gated_scan_saved_t *saved, bool need, ssm::gated::Kept *out) {
+    *out = ssm::gated::Kept{};
+    if (!saved) return need ? SSM_ERR_INVALID_ARG : SSM_OK;
+    const gated_scan_saved_t &k = *saved;
+    if (!k.states) return SSM_ERR_INVALID_ARG;
+    const bool any = k.x_q || k.r_q || k.i_q || k.x_s || k.r_s || k.i_s;
+    if (any && !(k.x_q && k.r_q && k.i_q && k.x_s && k.r_s && k.i_s)) return SSM_ERR_INVALID_ARG;
+    if (!aligned(k.states, 4) || !aligned(k.x_s, 4) || !aligned(k.r_s, 4) || !aligned(k.i_s, 4))
+        return SSM_ERR_ALIGNMENT;
+    *out = ssm::gated::Kept{k.states, k.x_q, k.r_q, k.i_q, k.x_s, k.r_s, k.i_s};
+    return SSM_OK;
+}
+
+ssm_status_t check_gated_sizes(int64_t Bs, int64_t L, int64_t ED, float c) {
+    if (!sizes_ok({Bs, L, ED, 4}) || !(c > 0.0f) || c > FLT_MAX) return SSM_ERR_INVALID_ARG;
+    if (Bs > 65535 || L > INT_MAX - SSM_GATED_BLOCK || ED > INT_MAX - SSM_GATED_BLOCK)
+        return SSM_ERR_UNSUPPORTED;
+    return SSM_OK;
+}
+
+template <typename T>
+ssm_status_t gated_fwd_entry(const void *x, const void *gr, const void *gi, const float *lam,
+                             float c, const uint8_t *reset, const float *h0, void *y,
+                             float *h_final, const gated_scan_saved_t *saved, int64_t Bs,
+                             int64_t L, int64_t ED, void *stream) {
+    if (!x || !gr || !gi || !lam || !y) return SSM_ERR_INVALID_ARG;
+    ssm_status_t s = check_gated_sizes(Bs, L, ED, c);
+    if (s != SSM_OK) return s;
+    if (!aligned(x, sizeof(T)) || !aligned(gr, sizeof(T)) || !aligned(gi, sizeof(T)) ||
+        !aligned(y, sizeof(T)) || !aligned(lam, 4) || !aligned(h0, 4) || !aligned(h_final, 4))
+        return SSM_ERR_ALIGNMENT;
+    ssm::gated::Kept kept;
+    s = check_saved(saved, false, &kept);
+    if (s != SSM_OK) return s;
+    DeviceInfo dev;
+    s = current_device(&dev);
+    if (s != SSM_OK) return s;
+    return from_cuda(ssm::gated::launch_fwd<T>(
+        static_cast<const T *>(x), static_cast<const T *>(gr), static_cast<const T *>(gi), lam, c,
+        reset, h0, static_cast<T *>(y), h_final, kept, Bs, L, ED, dev.num_sms,
+        static_cast<cudaStream_t>(stream)));
+}
+
+template <typename T>
+ssm_status_t gated_bwd_entry(const void *x, const void *gr, const void *gi, const float *lam,
+                             float c, const uint8_t *reset, const void *dy, const float *dh_final,
+                             const gated_scan_saved_t *saved, void *dx, void *dr, void *di,
+                             float *dlam, float *dh0, int64_t Bs, int64_t L, int64_t ED,
+                             void *stream) {
+    ssm::gated::Kept kept;
+    ssm_status_t s = check_saved(saved, true, &kept);
+    if (s != SSM_OK) return s;
+    if ((!kept.x_q && (!x || !gr || !gi)) || !lam || !dy || !dx || !dr || !di || !dlam)
+        return SSM_ERR_INVALID_ARG;
+    s = check_gated_sizes(Bs, L, ED, c);
+    if (s != SSM_OK) return s;
+    const size_t es = sizeof(T);
+    if (!aligned(x, es) || !aligned(gr, es) || !aligned(gi, es) || !aligned(dy, es) ||
+        !aligned(dx, es) || !aligned(dr, es) || !aligned(di, es) || !aligned(lam, 4) ||
+        !aligned(dh_final, 4) || !aligned(dlam, 4) || !aligned(dh0, 4))
+        return SSM_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    s = current_device(&dev);
+    if (s != SSM_OK) return s;
+    return from_cuda(ssm::gated_bwd::launch<T>(
+        static_cast<const T *>(x), static_cast<const T *>(gr), static_cast<const T *>(gi), lam, c,
+        reset, static_cast<const T *>(dy), dh_final, kept, static_cast<T *>(dx),
+        static_cast<T *>(dr), static_cast<T *>(di), dlam, dh0, Bs, L, ED, dev.num_sms,
+        static_cast<cudaStream_t>(stream)));
+}
+
+template <typename T>
+ssm_status_t gated_step_entry(const void *x, const void *gr, const void *gi, const float *lam,
+                              float c, float *states, const int32_t *pages, void *y, int64_t Bs,
+                              int64_t ED, int64_t num_pages, void *stream) {
+    if (!x || !gr || !gi || !lam || !states || !y) return SSM_ERR_INVALID_ARG;
+    ssm_status_t s = check_gated_sizes(Bs, 1, ED, c);
+    if (s != SSM_OK) return s;
+    if (!pages_ok(Bs, num_pages) || !sizes_ok({num_pages, ED, 4}) || (!pages && num_pages < Bs))
+        return SSM_ERR_INVALID_ARG;
+    if (num_pages > SSM_MAX_PAGES) return SSM_ERR_UNSUPPORTED;
+    if (!aligned(x, sizeof(T)) || !aligned(gr, sizeof(T)) || !aligned(gi, sizeof(T)) ||
+        !aligned(y, sizeof(T)) || !aligned(lam, 4) || !aligned(states, 4) || !aligned(pages, 4))
+        return SSM_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    s = current_device(&dev);
+    if (s != SSM_OK) return s;
+    return from_cuda(ssm::gated::launch_step<T>(
+        static_cast<const T *>(x), static_cast<const T *>(gr), static_cast<const T *>(gi), lam, c,
+        states, pages, static_cast<T *>(y), Bs, ED, num_pages, static_cast<cudaStream_t>(stream)));
+}
+
+ssm_status_t check_ckpt8(const void *x, const void *q, const float *scale, int64_t rows,
+                         int64_t cols, size_t es) {
+    if (!x || !q || !scale || !sizes_ok({rows, cols, 4})) return SSM_ERR_INVALID_ARG;
+    if (rows > INT_MAX || cols > INT_MAX - 64) return SSM_ERR_UNSUPPORTED;
+    return aligned(x, es) && aligned(scale, 4) ? SSM_OK : SSM_ERR_ALIGNMENT;
+}
+
+// Arguments of the calls on a pool and a list of n pages.
+ssm_status_t check_pool(const void *pool, int64_t n, int64_t layers, int64_t num_pages,
+                        int64_t page_bytes, DeviceInfo *dev) {
+    if (!pool || !pages_ok(n, num_pages) || !sizes_ok({layers, num_pages, page_bytes}))
+        return SSM_ERR_INVALID_ARG;
+    if (num_pages > SSM_MAX_PAGES) return SSM_ERR_UNSUPPORTED;
+    return current_device(dev);
 }
 }  // namespace
 
@@ -482,6 +634,111 @@ ssm_status_t ssm_scan_fwd_plan(int64_t Bs, int64_t L, int64_t ED, int64_t N, int
     *lanes_per_channel = p.G;
     *time_segments = p.K;
     return SSM_OK;
+}
+
+ssm_status_t gated_scan_fwd(const void *x, const void *gate_r, const void *gate_i, const float *lam,
+                            float c, const uint8_t *reset, const float *h0, void *y, float *h_final,
+                            const gated_scan_saved_t *saved, int64_t Bs, int64_t L, int64_t ED,
+                            int input_bf16, void *stream) {
+    return input_bf16 ? gated_fwd_entry<__nv_bfloat16>(x, gate_r, gate_i, lam, c, reset, h0, y,
+                                                       h_final, saved, Bs, L, ED, stream)
+                      : gated_fwd_entry<float>(x, gate_r, gate_i, lam, c, reset, h0, y, h_final,
+                                               saved, Bs, L, ED, stream);
+}
+
+ssm_status_t gated_scan_bwd(const void *x, const void *gate_r, const void *gate_i, const float *lam,
+                            float c, const uint8_t *reset, const void *dy, const float *dh_final,
+                            const gated_scan_saved_t *saved, void *dx, void *dgate_r,
+                            void *dgate_i, float *dlam, float *dh0, int64_t Bs, int64_t L,
+                            int64_t ED, int io_bf16, void *stream) {
+    return io_bf16 ? gated_bwd_entry<__nv_bfloat16>(x, gate_r, gate_i, lam, c, reset, dy, dh_final,
+                                                    saved, dx, dgate_r, dgate_i, dlam, dh0, Bs, L,
+                                                    ED, stream)
+                   : gated_bwd_entry<float>(x, gate_r, gate_i, lam, c, reset, dy, dh_final, saved,
+                                            dx, dgate_r, dgate_i, dlam, dh0, Bs, L, ED, stream);
+}
+
+ssm_status_t gated_scan_step(const void *x, const void *gate_r, const void *gate_i, const float *lam,
+                             float c, float *states, const int32_t *pages, void *y, int64_t Bs,
+                             int64_t ED, int64_t num_pages, int input_bf16, void *stream) {
+    return input_bf16 ? gated_step_entry<__nv_bfloat16>(x, gate_r, gate_i, lam, c, states, pages, y,
+                                                        Bs, ED, num_pages, stream)
+                      : gated_step_entry<float>(x, gate_r, gate_i, lam, c, states, pages, y, Bs, ED,
+                                                num_pages, stream);
+}
+
+ssm_status_t ckpt8_save(const void *x, int8_t *q, float *scale, int64_t rows, int64_t cols,
+                        int input_bf16, void *stream) {
+    ssm_status_t s = check_ckpt8(x, q, scale, rows, cols, input_bf16 ? 2 : 4);
+    if (s != SSM_OK) return s;
+    DeviceInfo dev;
+    s = current_device(&dev);
+    if (s != SSM_OK) return s;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return from_cuda(input_bf16 ? ssm::ckpt8::save(static_cast<const __nv_bfloat16 *>(x), q, scale,
+                                                   rows, cols, st)
+                                : ssm::ckpt8::save(static_cast<const float *>(x), q, scale, rows,
+                                                   cols, st));
+}
+
+ssm_status_t ckpt8_load(const int8_t *q, const float *scale, void *x, int64_t rows, int64_t cols,
+                        int output_bf16, void *stream) {
+    ssm_status_t s = check_ckpt8(x, q, scale, rows, cols, output_bf16 ? 2 : 4);
+    if (s != SSM_OK) return s;
+    DeviceInfo dev;
+    s = current_device(&dev);
+    if (s != SSM_OK) return s;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return from_cuda(output_bf16 ? ssm::ckpt8::load(q, scale, static_cast<__nv_bfloat16 *>(x), rows,
+                                                    cols, st)
+                                 : ssm::ckpt8::load(q, scale, static_cast<float *>(x), rows, cols,
+                                                    st));
+}
+
+ssm_status_t state_pages_fork(void *pool, uint8_t *used, const int32_t *src, int32_t *dst, int64_t n,
+                              int64_t layers, int64_t num_pages, int64_t page_bytes, void *stream) {
+    if (!used || (n > 0 && (!src || !dst))) return SSM_ERR_INVALID_ARG;
+    if (!aligned(src, 4) || !aligned(dst, 4)) return SSM_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    const ssm_status_t s = check_pool(pool, n, layers, num_pages, page_bytes, &dev);
+    if (s != SSM_OK || n == 0) return s;
+    return from_cuda(ssm::pages::fork(pool, used, src, dst, n, layers, num_pages, page_bytes,
+                                      dev.num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+ssm_status_t state_pages_copy(void *pool, const int32_t *src, const int32_t *dst, int64_t n,
+                              int64_t layers, int64_t num_pages, int64_t page_bytes, void *stream) {
+    if (n > 0 && (!src || !dst)) return SSM_ERR_INVALID_ARG;
+    if (!aligned(src, 4) || !aligned(dst, 4)) return SSM_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    const ssm_status_t s = check_pool(pool, n, layers, num_pages, page_bytes, &dev);
+    if (s != SSM_OK || n == 0) return s;
+    return from_cuda(ssm::pages::copy(pool, src, dst, n, layers, num_pages, page_bytes, dev.num_sms,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+ssm_status_t state_pages_free(uint8_t *used, const int32_t *pages, int64_t n, int64_t num_pages,
+                              void *stream) {
+    if (!used || (n > 0 && !pages) || !pages_ok(n, num_pages)) return SSM_ERR_INVALID_ARG;
+    if (num_pages > SSM_MAX_PAGES) return SSM_ERR_UNSUPPORTED;
+    if (!aligned(pages, 4)) return SSM_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    const ssm_status_t s = current_device(&dev);
+    if (s != SSM_OK || n == 0) return s;
+    return from_cuda(ssm::pages::free_pages(used, pages, n, num_pages,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+ssm_status_t state_pages_compact(void *pool, uint8_t *used, int32_t *moved, int32_t *pages,
+                                 int64_t n, int64_t layers, int64_t num_pages, int64_t page_bytes,
+                                 void *stream) {
+    if (!used || !moved || (n > 0 && !pages)) return SSM_ERR_INVALID_ARG;
+    if (!aligned(moved, 4) || !aligned(pages, 4)) return SSM_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    const ssm_status_t s = check_pool(pool, n, layers, num_pages, page_bytes, &dev);
+    if (s != SSM_OK) return s;
+    return from_cuda(ssm::pages::compact(pool, used, moved, pages, n, layers, num_pages, page_bytes,
+                                         dev.num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 ssm_status_t ssm_check_device_errors(void *stream) {
