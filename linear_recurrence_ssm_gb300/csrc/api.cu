@@ -308,7 +308,8 @@ ssm_status_t check_saved(const gated_scan_saved_t *saved, bool need, ssm::gated:
 
 ssm_status_t check_gated_sizes(int64_t Bs, int64_t L, int64_t ED, float c) {
     if (!sizes_ok({Bs, L, ED, 4}) || !(c > 0.0f) || c > FLT_MAX) return SSM_ERR_INVALID_ARG;
-    if (Bs > 65535 || L > INT_MAX - SSM_GATED_BLOCK || ED > INT_MAX - SSM_GATED_BLOCK)
+    // room for the tiles behind the end
+    if (Bs > 65535 || L > INT_MAX - 4096 || ED > INT_MAX - 4096)
         return SSM_ERR_UNSUPPORTED;
     return SSM_OK;
 }

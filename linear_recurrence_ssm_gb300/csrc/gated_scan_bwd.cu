@@ -22,7 +22,7 @@ gated_bwd_kernel(const T *__restrict__ x, const T *__restrict__ gr, const T *__r
     constexpr bool ACC = sizeof(T) == 4;
     const int64_t e = int64_t(blockIdx.x) * kGroup + threadIdx.x, b = blockIdx.y;
     if (e >= ED) return;
-    const float k = log_decay(lam[e], c);
+    const float k = decay_rate(lam[e], c);
     const int64_t blocks = (L + kBlock - 1) / kBlock;
     float u = dh_final ? dh_final[b * ED + e] : 0.0f, sum = 0.0f;
     float before[kBlock];
@@ -36,18 +36,21 @@ gated_bwd_kernel(const T *__restrict__ x, const T *__restrict__ gr, const T *__r
         for (int j = 0; j < n; ++j) {
             const int64_t row = b * L + t0 + j;
             before[j] = h;
-            const float xv = get(x, kept.x_q, kept.x_s, row), si = sigmoid<ACC>(get(gi, kept.i_q, kept.i_s, row));
-            const float la = k * sigmoid<ACC>(get(gr, kept.r_q, kept.r_s, row)), a = decay<ACC>(la);
-            const float m = root<ACC>(one_minus_exp(2.0f * la, a));
+            const float xv = get(x, kept.x_q, kept.x_s, row), si = sigmoid2<ACC>(both(get(gi, kept.i_q, kept.i_s, row))).x;
+            float2 a2, w2;
+            decay2<ACC, true>(both(k * sigmoid2<ACC>(both(get(gr, kept.r_q, kept.r_s, row))).x), a2, w2);
+            const float a = a2.x, m = root2<ACC>(one_minus_square(w2)).x;
             h = reset && reset[row] ? si * xv : fmaf(a, h, m * si * xv);
         }
         for (int j = n - 1; j >= 0; --j) {
             const int64_t row = b * L + t0 + j, at = row * ED + e;
-            const float xv = get(x, kept.x_q, kept.x_s, row), si = sigmoid<ACC>(get(gi, kept.i_q, kept.i_s, row));
-            const float sr = sigmoid<ACC>(get(gr, kept.r_q, kept.r_s, row));
-            const float la = k * sr, a = decay<ACC>(la);
+            const float xv = get(x, kept.x_q, kept.x_s, row), si = sigmoid2<ACC>(both(get(gi, kept.i_q, kept.i_s, row))).x;
+            const float sr = sigmoid2<ACC>(both(get(gr, kept.r_q, kept.r_s, row))).x, la = -k * sr;
+            float2 a2, w2;
+            decay2<ACC, true>(both(k * sr), a2, w2);
+            const float a = a2.x;
             const bool cut = reset && reset[row];
-            const float m = cut ? 1.0f : root<ACC>(one_minus_exp(2.0f * la, a));
+            const float m = cut ? 1.0f : root2<ACC>(one_minus_square(w2)).x;
             const float g = to_f32(dy[at]) + u;
             // m -> 0 only together with la, and la / m -> 0
             const float G = cut ? 0.0f : la * g * (a * before[j] - a * a / fmaxf(m, 1e-30f) * si * xv);
