@@ -21,14 +21,8 @@
 namespace ssm {
 namespace gated {
 
-constexpr int kWarps = 8, kSteps = kBlock / kWarps, kThreads = 32 * kWarps;
 constexpr int kStages = 3;
-constexpr int kMaxCluster = 8;
 
-// Bytes from one copied row of 64 channels to the next: words that start one
-// element early (loads of 4 bytes of bf16 rows) need one word more.
-template <typename T, int W>
-constexpr int kPitch = 64 * int(sizeof(T)) + (W == 4 && sizeof(T) == 2 ? 16 : 0);
 template <typename T, int W>
 constexpr int kStageBytes = 3 * kSteps * kPitch<T, W>;
 
@@ -47,70 +41,6 @@ struct FwdArgs {
     int pair_stores;            // y's rows take stores of two elements
 };
 
-// Copies one warp's 8 rows of 64 channels from row0 on, of one tensor.  W is
-// the widest copy that every row's start allows; 2 stands for plain loads of
-// elements, which wait for their data.
-template <typename T, int W>
-__device__ __forceinline__ void copy_rows(uint8_t *to, const T *from, int64_t row0, int n_rows, int e0, int ED) {
-    const int lane = threadIdx.x % 32;
-    if constexpr (W == 16 || (W == 4 && sizeof(T) == 4)) {
-        constexpr int kChunks = 64 * int(sizeof(T)) / W, kPer = W / int(sizeof(T));
-#pragma unroll
-        for (int i = 0; i < kSteps * kChunks / 32; ++i) {
-            const int row = (i * 32 + lane) / kChunks, e = (i * 32 + lane) % kChunks * kPer;
-            const bool in = row < n_rows && e0 + e < ED;
-            const T *src = in ? from + (row0 + row) * ED + e0 + e : from;
-            uint8_t *dst = to + row * kPitch<T, W> + e * int(sizeof(T));
-            if constexpr (W == 16)
-                cp_async16(dst, src, in ? 16 : 0);
-            else
-                cp_async4(dst, src, in ? 4 : 0);
-        }
-    } else if constexpr (W == 4) {
-        // rows of an odd number of bf16: words from the one that holds the row's first element
-#pragma unroll
-        for (int row = 0; row < kSteps; ++row) {
-            const int64_t first = (row0 + row) * ED + e0;
-            const int64_t end = (row0 + row) * ED + ED;     // past the row's last element
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int word = lane + 32 * k;
-                if (word > 32) continue;
-                const int64_t e = (first & ~int64_t(1)) + 2 * word;
-                const bool in = row < n_rows && e < end;
-                // the tensor's last element may be the first half of its word
-                const int bytes = !in ? 0 : (e + 1 < end ? 4 : 2);
-                cp_async4(to + row * kPitch<T, W> + 4 * word, in ? from + e : from, bytes);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int row = 0; row < kSteps; ++row)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int e = lane + 32 * k;
-                T v = T(0.0f);
-                if (row < n_rows && e0 + e < ED) v = from[(row0 + row) * ED + e0 + e];
-                *reinterpret_cast<T *>(to + row * kPitch<T, W> + e * int(sizeof(T))) = v;
-            }
-    }
-}
-
-// The lane's two channels of a copied row.
-template <typename T, int W>
-__device__ __forceinline__ float2 pair_at(const uint8_t *row, uint32_t odd) {
-    const int lane = threadIdx.x % 32;
-    if constexpr (sizeof(T) == 4) return *reinterpret_cast<const float2 *>(row + 8 * lane);
-    uint32_t w = *reinterpret_cast<const uint32_t *>(row + 4 * lane);
-    if (W == 4 && odd) w = __funnelshift_r(w, *reinterpret_cast<const uint32_t *>(row + 4 * lane + 4), 16);
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-
-__device__ __forceinline__ void put2(float *p, float2 v) { *reinterpret_cast<float2 *>(p) = v; }
-__device__ __forceinline__ void put2(__nv_bfloat16 *p, float2 v) {
-    *reinterpret_cast<__nv_bfloat162 *>(p) = __float22bfloat162_rn(v);
-}
-
 struct Pieces {
     float4 warp[2][kWarps][32];              // A of two channels, H of two channels
     float4 block[2][kMaxCluster][32];        // written by the cluster's blocks
@@ -120,21 +50,22 @@ struct Pieces {
 // a_t and b_t of a warp's 8 steps, and their piece (A, H).  bit j of `cut`:
 // step j drops the state before it.
 template <typename T, int W, bool WIDE, bool CUT>
-__device__ __forceinline__ void coefficients(const uint8_t *rows, uint32_t odd, float2 rate, uint32_t cut,
+__device__ __forceinline__ void coefficients(const uint8_t *rows, int64_t row0, int ED, float2 rate, uint32_t cut,
                                              float2 (&a)[kSteps], float2 (&b)[kSteps], float2 &A, float2 &H) {
     constexpr bool ACC = sizeof(T) == 4;
     A = both(1.0f);
     H = both(0.0f);
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) {
-        const uint32_t o = odd >> j & 1;
+        const uint32_t o = shift_of<T, W>(row0 + j, ED);
         const float2 x = pair_at<T, W>(rows + j * kPitch<T, W>, o);
         const float2 sr = sigmoid2<ACC>(pair_at<T, W>(rows + (kSteps + j) * kPitch<T, W>, o));
         const float2 si = sigmoid2<ACC>(pair_at<T, W>(rows + (2 * kSteps + j) * kPitch<T, W>, o));
         float2 w;
         decay2<ACC, WIDE>(mul2(rate, sr), a[j], w);
         const float2 in = mul2(si, x);
-        b[j] = mul2(root2<ACC>(one_minus_square(w)), in);
+        const float2 v = one_minus_square(w);
+        b[j] = mul2(mul2(v, rsqrt2<ACC>(v)), in);
         if (CUT && (cut >> j & 1)) {
             a[j] = both(0.0f);
             b[j] = in;
@@ -150,13 +81,13 @@ __device__ __forceinline__ void coefficients(const uint8_t *rows, uint32_t odd, 
 // Keeps a warp's 8 rows of the three tensors in 8 bits.  The tops of the 24
 // groups end up one in each lane, so that the division is done once.
 template <typename T, int W>
-__device__ __forceinline__ void keep_8bit(const uint8_t *rows, uint32_t odd, const Kept &kept, int64_t row0,
+__device__ __forceinline__ void keep_8bit(const uint8_t *rows, const Kept &kept, int64_t row0,
                                           int n_rows, int e0, int ED, int64_t all_rows) {
     const int lane = threadIdx.x % 32;
     uint32_t mine = 0;
 #pragma unroll
     for (int g = 0; g < 3 * kSteps; ++g) {
-        const float2 v = pair_at<T, W>(rows + g * kPitch<T, W>, odd >> (g % kSteps) & 1);
+        const float2 v = pair_at<T, W>(rows + g * kPitch<T, W>, shift_of<T, W>(row0 + g % kSteps, ED));
         // the order of the bit patterns of |v| is that of the values, NaN on top
         const uint32_t top = __reduce_max_sync(0xffffffffu, max(__float_as_uint(v.x) & 0x7fffffffu,
                                                                 __float_as_uint(v.y) & 0x7fffffffu));
@@ -171,7 +102,7 @@ __device__ __forceinline__ void keep_8bit(const uint8_t *rows, uint32_t odd, con
 #pragma unroll
     for (int g = 0; g < 3 * kSteps; ++g) {
         const int j = g % kSteps;
-        const float2 v = pair_at<T, W>(rows + g * kPitch<T, W>, odd >> j & 1);
+        const float2 v = pair_at<T, W>(rows + g * kPitch<T, W>, shift_of<T, W>(row0 + j, ED));
         const float k = __shfl_sync(0xffffffffu, inv, g);
         const uint32_t n0 = quantised(v.x, k), n1 = quantised(v.y, k);
         if (j < n_rows && e < ED) {
@@ -233,22 +164,19 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p) {
         cp_async_wait<kStages - 1>();
         __syncwarp();
         const uint8_t *rows = mine + turn % kStages * kStageBytes<T, W>;
-        uint32_t cut = 0, odd = 0;
+        uint32_t cut = 0;
         if (RESET) {
             cut = __ballot_sync(0xffffffffu, next_cut != 0);
             next_cut = reset_of(turn + 1);
         }
-        // which rows start in the second half of a word: all of them or none, or every second one
-        if (sizeof(T) == 2 && W == 4) odd = (p.ED & 1) ? (row0 & 1 ? 0x55u : 0xaau) : 0u;
-
-        if (SAVE8 && n > 0) keep_8bit<T, W>(rows, odd, p.kept, row0, n, e0, p.ED, p.rows);
+        if (SAVE8 && n > 0) keep_8bit<T, W>(rows, p.kept, row0, n, e0, p.ED, p.rows);
 
         // steps behind the end leave their piece wrong; nothing after them reads it
         float2 a[kSteps], s[kSteps], A, H;
         if (wide || (RESET && cut))
-            coefficients<T, W, true, RESET>(rows, odd, rate, cut, a, s, A, H);
+            coefficients<T, W, true, RESET>(rows, row0, p.ED, rate, cut, a, s, A, H);
         else
-            coefficients<T, W, false, false>(rows, odd, rate, 0, a, s, A, H);
+            coefficients<T, W, false, false>(rows, row0, p.ED, rate, 0, a, s, A, H);
         __syncwarp();      // all lanes have read before any lane copies over these rows
 
         sh.warp[buf][warp][lane] = make_float4(A.x, A.y, H.x, H.y);
@@ -309,17 +237,9 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p) {
             s[j] = h;
         }
         T *y = p.y + row0 * p.ED + e;
-        if (p.pair_stores) {
 #pragma unroll
-            for (int j = 0; j < kSteps; ++j)
-                if (j < n && in0) put2(y + int64_t(j) * p.ED, s[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < kSteps; ++j) {
-                if (j < n && in0) put(y + int64_t(j) * p.ED, s[j].x);
-                if (j < n && in1) put(y + int64_t(j) * p.ED + 1, s[j].y);
-            }
-        }
+        for (int j = 0; j < kSteps; ++j)
+            if (j < n) put_pair(y + int64_t(j) * p.ED, s[j], p.pair_stores, in0, in1);
         if (p.h_final) {
 #pragma unroll
             for (int j = 0; j < kSteps; ++j)
@@ -349,8 +269,8 @@ gated_step_kernel(const T *__restrict__ x, const T *__restrict__ gr, const T *__
     const float2 s = sigmoid2<ACC>(make_float2(to_f32(gr[at]), to_f32(gi[at])));
     float2 a, w;
     decay2<ACC, true>(both(decay_rate(lam[e], c) * s.x), a, w);
-    const float m = root2<ACC>(one_minus_square(w)).x;
-    const float h = fmaf(a.x, states[page * ED + e], m * s.y * to_f32(x[at]));
+    const float2 v = one_minus_square(w);
+    const float h = fmaf(a.x, states[page * ED + e], v.x * rsqrt2<ACC>(v).x * s.y * to_f32(x[at]));
     states[page * ED + e] = h;
     put(y + at, h);
 }
@@ -389,16 +309,14 @@ cudaError_t launch_fwd(const T *x, const T *gr, const T *gi, const float *lam, f
     const uintptr_t in = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(gr) |
                          reinterpret_cast<uintptr_t>(gi);
     p.pair_stores = ED % 2 == 0 && reinterpret_cast<uintptr_t>(y) % (2 * sizeof(T)) == 0;
-    // Blocks of a cluster share the time axis: as many as fill the GPU with
-    // two blocks an SM, none with less than two tiles.
-    const int64_t chains = (ED + 63) / 64 * Bs, tiles = (L + kBlock - 1) / kBlock;
-    while (p.cluster < kMaxCluster && chains * p.cluster * 2 <= 3 * num_sms && p.cluster * 2 <= tiles) p.cluster *= 2;
-    const bool q_words = !kept.x_q || (reinterpret_cast<uintptr_t>(kept.x_q) | reinterpret_cast<uintptr_t>(kept.r_q) |
-                                       reinterpret_cast<uintptr_t>(kept.i_q)) % 2 == 0;
-    if (ED * int64_t(sizeof(T)) % 16 == 0 && in % 16 == 0 && q_words) return start_fwd<T, 16>(p, Bs, st);
-    if (in % 4 == 0) return start_fwd<T, 4>(p, Bs, st);
-    if constexpr (sizeof(T) == 2) return start_fwd<T, 2>(p, Bs, st);
-    return cudaErrorInvalidValue;
+    p.cluster = cluster_for(Bs, L, ED, num_sms);
+    const uintptr_t q = reinterpret_cast<uintptr_t>(kept.x_q) | reinterpret_cast<uintptr_t>(kept.r_q) |
+                        reinterpret_cast<uintptr_t>(kept.i_q);
+    const int W = widest_copy<T>(in, ED);
+    if (W == 16 && q % 2 == 0) return start_fwd<T, 16>(p, Bs, st);
+    if (W >= 4) return start_fwd<T, 4>(p, Bs, st);
+    if constexpr (sizeof(T) == 2) return start_fwd<T, 1>(p, Bs, st);
+    return cudaErrorInvalidValue;      // fp32 is aligned to its 4 bytes
 }
 
 template <typename T>

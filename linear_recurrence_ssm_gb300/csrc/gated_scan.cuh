@@ -83,12 +83,6 @@ __device__ __forceinline__ float rcp_fast(float v) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
-__device__ __forceinline__ float sqrt_fast(float v) {
-    float r;
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-
 // 1 / (1 + e^-v).  ACC (fp32 tensors) uses the accurate functions; bf16
 // tensors the special-function unit, whose ~2^-22 is far below the 2^-9 of
 // their rounding.
@@ -107,15 +101,20 @@ __device__ __forceinline__ float2 sigmoid2(float2 v) {
 // error 1.2e-8 in exact arithmetic); from 0.7 on 1 - a loses at most one bit.
 // WIDE says that t may exceed 0.7: t <= c softplus(lam), so a warp knows from
 // its channels alone.
-constexpr float kSlow = 0.7f;
-template <bool ACC, bool WIDE>
-__device__ __forceinline__ void decay2(float2 t, float2 &a, float2 &w) {
+// w is kept above kLeast, far below what it adds to, so that t = 0 needs no
+// case of its own where (1 - a^2)^(-1/2) is taken.
+constexpr float kSlow = 0.7f, kLeast = 1e-30f;
+__device__ __forceinline__ float2 slow_loss(float2 t) {
     float2 q = fma2(t, both(-0x1.0f0144p-10f), both(0x1.08671cp-7f));
     q = fma2(q, t, both(-0x1.5491aap-5f));
     q = fma2(q, t, both(0x1.554d72p-3f));
     q = fma2(q, t, both(-0x1.ffffc4p-2f));
     q = fma2(q, t, both(1.0f));
-    w = mul2(q, t);
+    return fma2(q, t, both(kLeast));
+}
+template <bool ACC, bool WIDE>
+__device__ __forceinline__ void decay2(float2 t, float2 &a, float2 &w) {
+    w = slow_loss(t);
     a = fma2(w, both(-1.0f), both(1.0f));
     if (WIDE) {
         float2 e;
@@ -134,9 +133,17 @@ __device__ __forceinline__ void decay2(float2 t, float2 &a, float2 &w) {
 // 1 - a^2
 __device__ __forceinline__ float2 one_minus_square(float2 w) { return mul2(w, fma2(w, both(-1.0f), both(2.0f))); }
 
+// v^(-1/2), for v > 0
 template <bool ACC>
-__device__ __forceinline__ float2 root2(float2 v) {
-    return ACC ? make_float2(sqrtf(v.x), sqrtf(v.y)) : make_float2(sqrt_fast(v.x), sqrt_fast(v.y));
+__device__ __forceinline__ float2 rsqrt2(float2 v) {
+    float2 r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(v.x));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(v.y));
+    if (ACC) {   // one Newton step: r + r (1 - v r^2) / 2
+        const float2 d = fma2(mul2(v, r), mul2(r, both(-1.0f)), both(1.0f));
+        r = fma2(mul2(r, both(0.5f)), d, r);
+    }
+    return r;
 }
 
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
@@ -170,6 +177,128 @@ __device__ __forceinline__ void cp_async4(void *smem_dst, const void *gsrc, int 
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(smem_u32(smem_dst)), "l"(gsrc),
                  "r"(src_bytes)
                  : "memory");
+}
+
+// ---- a warp's rows of a tile ----------------------------------------------------
+// A tile is 64 steps x 64 channels; each of a block's 8 warps owns 8 steps, a
+// lane two channels.  A warp copies its own rows ahead of their use, so no
+// block barrier stands between a copy and its use.
+constexpr int kWarps = 8, kSteps = kBlock / kWarps, kThreads = 32 * kWarps;
+constexpr int kMaxCluster = 8;
+
+// W is the widest copy that every row's start allows: 16 bytes, 4 (rows of
+// narrow elements then start anywhere in their first word, and need one word
+// more), or 1 for plain loads of elements, which wait for their data.
+template <typename T, int W>
+constexpr bool kShifted = W == 4 && sizeof(T) < 4;
+template <typename T, int W>
+constexpr int kPitch = 64 * int(sizeof(T)) + (kShifted<T, W> ? 16 : 0);
+
+template <typename T, int W>
+__device__ __forceinline__ void copy_rows(uint8_t *to, const T *from, int64_t row0, int n_rows, int e0, int ED) {
+    constexpr int kSize = int(sizeof(T));
+    const int lane = threadIdx.x % 32;
+    if constexpr (W == 16 || (W == 4 && kSize == 4)) {
+        constexpr int kChunks = 64 * kSize / W, kPer = W / kSize;
+#pragma unroll
+        for (int i = 0; i < kSteps * kChunks / 32; ++i) {
+            const int row = (i * 32 + lane) / kChunks, e = (i * 32 + lane) % kChunks * kPer;
+            const bool in = row < n_rows && e0 + e < ED;
+            const T *src = in ? from + (row0 + row) * ED + e0 + e : from;
+            uint8_t *dst = to + row * kPitch<T, W> + e * kSize;
+            if constexpr (W == 16)
+                cp_async16(dst, src, in ? 16 : 0);
+            else
+                cp_async4(dst, src, in ? 4 : 0);
+        }
+    } else if constexpr (W == 4) {
+        constexpr int kPer = 4 / kSize, kWords = 64 / kPer + 1;
+#pragma unroll
+        for (int row = 0; row < kSteps; ++row) {
+            const int64_t begin = (row0 + row) * ED, end = begin + ED;
+            // the word that holds the row's first element; the tensor starts on a word
+            const int64_t first = (begin + e0) & ~int64_t(kPer - 1);
+#pragma unroll
+            for (int k = 0; k < (kWords + 31) / 32; ++k) {
+                const int word = lane + 32 * k;
+                if (word >= kWords) continue;
+                const int64_t e = first + kPer * word;
+                const bool in = row < n_rows && e < end;
+                // nothing behind the row's end, which may be the tensor's
+                const int bytes = in ? int(min(int64_t(kPer), end - e)) * kSize : 0;
+                cp_async4(to + row * kPitch<T, W> + 4 * word, in ? from + e : from, bytes);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int row = 0; row < kSteps; ++row)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int e = lane + 32 * k;
+                T v = T(0.0f);
+                if (row < n_rows && e0 + e < ED) v = from[(row0 + row) * ED + e0 + e];
+                *reinterpret_cast<T *>(to + row * kPitch<T, W> + e * kSize) = v;
+            }
+    }
+}
+
+// Elements between a row's first word and its first element.
+template <typename T, int W>
+__device__ __forceinline__ uint32_t shift_of(int64_t row, int ED) {
+    return kShifted<T, W> ? uint32_t(row) * uint32_t(ED) & (4 / uint32_t(sizeof(T)) - 1) : 0;
+}
+
+// The lane's two channels of a copied row (int8: the integers).
+template <typename T, int W>
+__device__ __forceinline__ float2 pair_at(const uint8_t *row, uint32_t shift) {
+    const int lane = threadIdx.x % 32;
+    if constexpr (sizeof(T) == 4) {
+        return *reinterpret_cast<const float2 *>(row + 8 * lane);
+    } else if constexpr (sizeof(T) == 2) {
+        uint32_t w = *reinterpret_cast<const uint32_t *>(row + 4 * lane);
+        if (W == 4 && shift) w = __funnelshift_r(w, *reinterpret_cast<const uint32_t *>(row + 4 * lane + 4), 16);
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    } else {
+        uint32_t w;
+        if (kShifted<T, W>)
+            w = row[2 * lane + shift] | row[2 * lane + shift + 1] << 8;
+        else
+            w = *reinterpret_cast<const uint16_t *>(row + 2 * lane);
+        // 2^23 + (q + 128) as a bit pattern, less 2^23 + 128: exact
+        w ^= 0x8080u;
+        return add2(make_float2(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440)),
+                                __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441))),
+                    both(-8388736.0f));
+    }
+}
+
+__device__ __forceinline__ void put2(float *p, float2 v) { *reinterpret_cast<float2 *>(p) = v; }
+__device__ __forceinline__ void put2(__nv_bfloat16 *p, float2 v) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __float22bfloat162_rn(v);
+}
+// A lane's two channels of one row, as one store where `pairs`.
+template <typename T>
+__device__ __forceinline__ void put_pair(T *p, float2 v, bool pairs, bool in0, bool in1) {
+    if (pairs) {
+        if (in0) put2(p, v);
+    } else {
+        if (in0) put(p, v.x);
+        if (in1) put(p + 1, v.y);
+    }
+}
+
+template <typename T>
+inline int widest_copy(uintptr_t at, int64_t ED) {
+    return ED * int64_t(sizeof(T)) % 16 == 0 && at % 16 == 0 ? 16 : at % 4 == 0 ? 4 : 1;
+}
+
+// Blocks of a cluster take neighbouring tiles of a sequence at once: as many
+// as bring the GPU two blocks an SM, none with less than two tiles.
+inline int cluster_for(int64_t Bs, int64_t L, int64_t ED, int num_sms) {
+    const int64_t chains = (ED + 63) / 64 * Bs, tiles = (L + kBlock - 1) / kBlock;
+    int c = 1;
+    while (c < kMaxCluster && chains * c * 2 <= 3 * num_sms && c * 2 <= tiles) c *= 2;
+    return c;
 }
 
 }  // namespace gated
