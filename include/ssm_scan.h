@@ -396,16 +396,17 @@ SSM_API ssm_status_t gated_scan_fwd(const void *x, const void *gate_r, const voi
  * gate_i are not read (may be NULL).  The states inside a block of 64 steps
  * are recomputed from the one kept at its start.  At a reset step the decay
  * is the constant 0: no gradient reaches gate_r, lam or an earlier state.
- * Deterministic (dlam is summed in a fixed order).  Takes stream-ordered
- * scratch of 4 Bs ED bytes for each part of the time axis that runs at once.
- * Sizes and alignment as gated_scan_fwd.
+ * scratch : min(8, ceil(L / 64)) * Bs * ED floats of the caller's, for dlam's
+ *           partial sums; unspecified afterwards
+ * Deterministic (dlam is summed in a fixed order).  Sizes and alignment as
+ * gated_scan_fwd.
  */
 SSM_API ssm_status_t gated_scan_bwd(const void *x, const void *gate_r, const void *gate_i,
                                     const float *lam, float c, const uint8_t *reset,
                                     const void *dy, const float *dh_final,
                                     const gated_scan_saved_t *saved, void *dx, void *dgate_r,
-                                    void *dgate_i, float *dlam, float *dh0, int64_t Bs, int64_t L,
-                                    int64_t ED, int io_bf16, void *stream);
+                                    void *dgate_i, float *dlam, float *dh0, float *scratch,
+                                    int64_t Bs, int64_t L, int64_t ED, int io_bf16, void *stream);
 
 /*
  * One step of the gated recurrence for each row of a batch, on states kept in

@@ -74,7 +74,7 @@ SIGNATURES = {
     "ssd_chunk_scan_fwd_ex": ([_VP] * 7 + [_I64] * 6 + [ctypes.c_int, ctypes.c_int, _VP, _VP],
                               ctypes.c_int),
     "gated_scan_fwd": ([_VP] * 4 + [_F32] + [_VP] * 5 + [_I64] * 3 + [ctypes.c_int, _VP], ctypes.c_int),
-    "gated_scan_bwd": ([_VP] * 4 + [_F32] + [_VP] * 9 + [_I64] * 3 + [ctypes.c_int, _VP], ctypes.c_int),
+    "gated_scan_bwd": ([_VP] * 4 + [_F32] + [_VP] * 10 + [_I64] * 3 + [ctypes.c_int, _VP], ctypes.c_int),
     "gated_scan_step": ([_VP] * 4 + [_F32] + [_VP] * 3 + [_I64] * 3 + [ctypes.c_int, _VP], ctypes.c_int),
     "ckpt8_save": ([_VP] * 3 + [_I64] * 2 + [ctypes.c_int, _VP], ctypes.c_int),
     "ckpt8_load": ([_VP] * 3 + [_I64] * 2 + [ctypes.c_int, _VP], ctypes.c_int),
@@ -556,10 +556,11 @@ def gated_scan_bwd(x, gate_r, gate_i, lam, dy, saved, c=8.0, reset=None, dh_fina
     g = {k: torch.empty_like(dy) for k in ("dx", "dgate_r", "dgate_i")}
     g["dlam"] = torch.empty(ED, dtype=torch.float32, device=dev)
     g["dh0"] = torch.empty((Bs, ED), dtype=torch.float32, device=dev)
+    scratch = torch.empty(min(8, -(-L // _BLOCK)) * Bs * ED, dtype=torch.float32, device=dev)
     _call("gated_scan_bwd", _ptr(x), _ptr(gate_r), _ptr(gate_i), _ptr(lam), float(c), _ptr(reset),
           _ptr(dy), _ptr(dh_final), ctypes.byref(_saved_struct(saved)), _ptr(g["dx"]),
-          _ptr(g["dgate_r"]), _ptr(g["dgate_i"]), _ptr(g["dlam"]), _ptr(g["dh0"]), Bs, L, ED,
-          int(dy.dtype == torch.bfloat16), _stream(dev))
+          _ptr(g["dgate_r"]), _ptr(g["dgate_i"]), _ptr(g["dlam"]), _ptr(g["dh0"]), _ptr(scratch),
+          Bs, L, ED, int(dy.dtype == torch.bfloat16), _stream(dev))
     return g
 
 

@@ -73,13 +73,16 @@ template <typename T>
 cudaError_t launch_step(const T *x, const T *gr, const T *gi, const float *lam, float c,
                         float *states, const int32_t *pages, T *y, int64_t Bs, int64_t ED,
                         int64_t num_pages, cudaStream_t st);
+cudaError_t take_device_error(unsigned int *out);
 }
 namespace gated_bwd {
 template <typename T>
 cudaError_t launch(const T *x, const T *gr, const T *gi, const float *lam, float c,
                    const uint8_t *reset, const T *dy, const float *dh_final,
                    const gated::Kept &kept, T *dx, T *dr, T *di, float *dlam, float *dh0,
-                   int64_t Bs, int64_t L, int64_t ED, int num_sms, cudaStream_t st);
+                   float *scratch, int64_t Bs, int64_t L, int64_t ED, int num_sms,
+                   cudaStream_t st);
+cudaError_t take_device_error(unsigned int *out);
 }
 namespace ckpt8 {
 template <typename T>
@@ -341,19 +344,20 @@ template <typename T>
 ssm_status_t gated_bwd_entry(const void *x, const void *gr, const void *gi, const float *lam,
                              float c, const uint8_t *reset, const void *dy, const float *dh_final,
                              const gated_scan_saved_t *saved, void *dx, void *dr, void *di,
-                             float *dlam, float *dh0, int64_t Bs, int64_t L, int64_t ED,
-                             void *stream) {
+                             float *dlam, float *dh0, float *scratch, int64_t Bs, int64_t L,
+                             int64_t ED, void *stream) {
     ssm::gated::Kept kept;
     ssm_status_t s = check_saved(saved, true, &kept);
     if (s != SSM_OK) return s;
-    if ((!kept.x_q && (!x || !gr || !gi)) || !lam || !dy || !dx || !dr || !di || !dlam)
+    if ((!kept.x_q && (!x || !gr || !gi)) || !lam || !dy || !dx || !dr || !di || !dlam ||
+        !scratch)
         return SSM_ERR_INVALID_ARG;
     s = check_gated_sizes(Bs, L, ED, c);
     if (s != SSM_OK) return s;
     const size_t es = sizeof(T);
     if (!aligned(x, es) || !aligned(gr, es) || !aligned(gi, es) || !aligned(dy, es) ||
         !aligned(dx, es) || !aligned(dr, es) || !aligned(di, es) || !aligned(lam, 4) ||
-        !aligned(dh_final, 4) || !aligned(dlam, 4) || !aligned(dh0, 4))
+        !aligned(dh_final, 4) || !aligned(dlam, 4) || !aligned(dh0, 4) || !aligned(scratch, 4))
         return SSM_ERR_ALIGNMENT;
     DeviceInfo dev;
     s = current_device(&dev);
@@ -361,7 +365,7 @@ ssm_status_t gated_bwd_entry(const void *x, const void *gr, const void *gi, cons
     return from_cuda(ssm::gated_bwd::launch<T>(
         static_cast<const T *>(x), static_cast<const T *>(gr), static_cast<const T *>(gi), lam, c,
         reset, static_cast<const T *>(dy), dh_final, kept, static_cast<T *>(dx),
-        static_cast<T *>(dr), static_cast<T *>(di), dlam, dh0, Bs, L, ED, dev.num_sms,
+        static_cast<T *>(dr), static_cast<T *>(di), dlam, dh0, scratch, Bs, L, ED, dev.num_sms,
         static_cast<cudaStream_t>(stream)));
 }
 
@@ -650,13 +654,14 @@ ssm_status_t gated_scan_fwd(const void *x, const void *gate_r, const void *gate_
 ssm_status_t gated_scan_bwd(const void *x, const void *gate_r, const void *gate_i, const float *lam,
                             float c, const uint8_t *reset, const void *dy, const float *dh_final,
                             const gated_scan_saved_t *saved, void *dx, void *dgate_r,
-                            void *dgate_i, float *dlam, float *dh0, int64_t Bs, int64_t L,
-                            int64_t ED, int io_bf16, void *stream) {
+                            void *dgate_i, float *dlam, float *dh0, float *scratch, int64_t Bs,
+                            int64_t L, int64_t ED, int io_bf16, void *stream) {
     return io_bf16 ? gated_bwd_entry<__nv_bfloat16>(x, gate_r, gate_i, lam, c, reset, dy, dh_final,
-                                                    saved, dx, dgate_r, dgate_i, dlam, dh0, Bs, L,
-                                                    ED, stream)
+                                                    saved, dx, dgate_r, dgate_i, dlam, dh0, scratch,
+                                                    Bs, L, ED, stream)
                    : gated_bwd_entry<float>(x, gate_r, gate_i, lam, c, reset, dy, dh_final, saved,
-                                            dx, dgate_r, dgate_i, dlam, dh0, Bs, L, ED, stream);
+                                            dx, dgate_r, dgate_i, dlam, dh0, scratch, Bs, L, ED,
+                                            stream);
 }
 
 ssm_status_t gated_scan_step(const void *x, const void *gate_r, const void *gate_i, const float *lam,
@@ -747,10 +752,12 @@ ssm_status_t ssm_check_device_errors(void *stream) {
     ssm_status_t s = current_device(&dev);
     if (s != SSM_OK) return s;
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return SSM_ERR_CUDA;
-    unsigned int flag = 0, flag_bi = 0;
+    unsigned int flag = 0, flag_bi = 0, flag_g = 0, flag_gb = 0;
     if (ssm::ssd::take_device_error(&flag) != cudaSuccess) return SSM_ERR_CUDA;
     if (ssm::bidir::take_device_error(&flag_bi) != cudaSuccess) return SSM_ERR_CUDA;
-    return (flag | flag_bi) ? SSM_ERR_DEVICE_TIMEOUT : SSM_OK;
+    if (ssm::gated::take_device_error(&flag_g) != cudaSuccess) return SSM_ERR_CUDA;
+    if (ssm::gated_bwd::take_device_error(&flag_gb) != cudaSuccess) return SSM_ERR_CUDA;
+    return (flag | flag_bi | flag_g | flag_gb) ? SSM_ERR_DEVICE_TIMEOUT : SSM_OK;
 }
 
 ssm_status_t ssm_selftest_wait_timeout(void *stream) {

@@ -21,7 +21,15 @@
 namespace ssm {
 namespace gated {
 
-constexpr int kStages = 3;
+#ifndef KST
+#define KST 2
+#endif
+#ifndef MINB
+#define MINB 4
+#endif
+constexpr int kWarps = 4, kSteps = kBlock / kWarps, kThreads = 32 * kWarps, kStages = KST;
+
+__device__ unsigned int g_device_error;
 
 template <typename T, int W>
 constexpr int kStageBytes = 3 * kSteps * kPitch<T, W>;
@@ -41,13 +49,18 @@ struct FwdArgs {
     int pair_stores;            // y's rows take stores of two elements
 };
 
-struct Pieces {
-    float4 warp[2][kWarps][32];              // A of two channels, H of two channels
-    float4 block[2][kMaxCluster][32];        // written by the cluster's blocks
-    uint32_t cuts[2][kWarps], block_cut[2][kMaxCluster];
+// Boxes of 64 channels x kSteps rows of x, gate_r, gate_i and y (W = 16).
+struct FwdMaps {
+    CUtensorMap in[3], y;
 };
 
-// a_t and b_t of a warp's 8 steps, and their piece (A, H).  bit j of `cut`:
+struct Shared {
+    float4 warp[2][kWarps][32];     // A of two channels, H of two channels
+    uint64_t full[kWarps][kStages]; // a warp's copies have arrived (W = 16)
+    Exchange ex;
+};
+
+// a_t and b_t of a warp's steps, and their piece (A, H).  bit j of `cut`:
 // step j drops the state before it.
 template <typename T, int W, bool WIDE, bool CUT>
 __device__ __forceinline__ void coefficients(const uint8_t *rows, int64_t row0, int ED, float2 rate, uint32_t cut,
@@ -63,13 +76,12 @@ __device__ __forceinline__ void coefficients(const uint8_t *rows, int64_t row0, 
         const float2 si = sigmoid2<ACC>(pair_at<T, W>(rows + (2 * kSteps + j) * kPitch<T, W>, o));
         float2 w;
         decay2<ACC, WIDE>(mul2(rate, sr), a[j], w);
-        const float2 in = mul2(si, x);
-        const float2 v = one_minus_square(w);
+        const float2 in = mul2(si, x), v = one_minus_square(a[j], w);
         b[j] = mul2(mul2(v, rsqrt2<ACC>(v)), in);
         if (CUT && (cut >> j & 1)) {
             a[j] = both(0.0f);
             b[j] = in;
-            A = both(0.0f);
+            A = both(-0.0f);
             H = in;
         } else {
             A = mul2(A, a[j]);
@@ -78,51 +90,53 @@ __device__ __forceinline__ void coefficients(const uint8_t *rows, int64_t row0, 
     }
 }
 
-// Keeps a warp's 8 rows of the three tensors in 8 bits.  The tops of the 24
-// groups end up one in each lane, so that the division is done once.
+// Keeps a warp's rows of the three tensors in 8 bits, a tensor at a time.
+// The tops of its kSteps groups end up one in each lane, so that the division
+// is done once.
 template <typename T, int W>
-__device__ __forceinline__ void keep_8bit(const uint8_t *rows, const Kept &kept, int64_t row0,
-                                          int n_rows, int e0, int ED, int64_t all_rows) {
-    const int lane = threadIdx.x % 32;
-    uint32_t mine = 0;
+__device__ __forceinline__ void keep_8bit(const uint8_t *rows, const Kept &kept, int64_t row0, int n_rows, int e0,
+                                          int ED, int64_t all_rows, bool pairs) {
+    const int lane = threadIdx.x % 32, e = e0 + 2 * lane;
+#pragma unroll 1
+    for (int k = 0; k < 3; ++k, rows += kSteps * kPitch<T, W>) {
+        uint32_t mine = 0;
 #pragma unroll
-    for (int g = 0; g < 3 * kSteps; ++g) {
-        const float2 v = pair_at<T, W>(rows + g * kPitch<T, W>, shift_of<T, W>(row0 + g % kSteps, ED));
-        // the order of the bit patterns of |v| is that of the values, NaN on top
-        const uint32_t top = __reduce_max_sync(0xffffffffu, max(__float_as_uint(v.x) & 0x7fffffffu,
-                                                                __float_as_uint(v.y) & 0x7fffffffu));
-        if (lane == g) mine = top;
-    }
-    const float top = __uint_as_float(mine), inv = inverse_of(top);
-    if (lane < 3 * kSteps && lane % kSteps < n_rows) {
-        float *s = lane < kSteps ? kept.x_s : lane < 2 * kSteps ? kept.r_s : kept.i_s;
-        s[(e0 / kGroup) * all_rows + row0 + lane % kSteps] = scale_of(top);
-    }
-    const int e = e0 + 2 * lane;
+        for (int j = 0; j < kSteps; ++j) {
+            const float2 v = pair_at<T, W>(rows + j * kPitch<T, W>, shift_of<T, W>(row0 + j, ED));
+            // the order of the bit patterns of |v| is that of the values, NaN on top
+            const uint32_t top = __reduce_max_sync(0xffffffffu, max(__float_as_uint(v.x) & 0x7fffffffu,
+                                                                    __float_as_uint(v.y) & 0x7fffffffu));
+            if (lane == j) mine = top;
+        }
+        const float top = __uint_as_float(mine), inv = inverse_of(top);
+        if (lane < n_rows && lane < kSteps) {
+            float *s = k == 0 ? kept.x_s : k == 1 ? kept.r_s : kept.i_s;
+            s[(e0 / kGroup) * all_rows + row0 + lane] = scale_of(top);
+        }
+        int8_t *q = (k == 0 ? kept.x_q : k == 1 ? kept.r_q : kept.i_q) + row0 * ED + e;
 #pragma unroll
-    for (int g = 0; g < 3 * kSteps; ++g) {
-        const int j = g % kSteps;
-        const float2 v = pair_at<T, W>(rows + g * kPitch<T, W>, shift_of<T, W>(row0 + j, ED));
-        const float k = __shfl_sync(0xffffffffu, inv, g);
-        const uint32_t n0 = quantised(v.x, k), n1 = quantised(v.y, k);
-        if (j < n_rows && e < ED) {
-            int8_t *q = (g < kSteps ? kept.x_q : g < 2 * kSteps ? kept.r_q : kept.i_q) + (row0 + j) * ED + e;
-            if (W == 16) {
-                *reinterpret_cast<uint16_t *>(q) =
-                    uint16_t(__byte_perm(n0, n1, 0x0040));
-            } else {
-                q[0] = int8_t(n0);
-                if (e + 1 < ED) q[1] = int8_t(n1);
+        for (int j = 0; j < kSteps; ++j) {
+            const float2 v = pair_at<T, W>(rows + j * kPitch<T, W>, shift_of<T, W>(row0 + j, ED));
+            const float by = __shfl_sync(0xffffffffu, inv, j);
+            const uint32_t n0 = quantised(v.x, by), n1 = quantised(v.y, by);
+            if (j < n_rows && e < ED) {
+                if (pairs) {
+                    *reinterpret_cast<uint16_t *>(q) = uint16_t(__byte_perm(n0, n1, 0x0040));
+                } else {
+                    q[0] = int8_t(n0);
+                    if (e + 1 < ED) q[1] = int8_t(n1);
+                }
             }
+            q += ED;
         }
     }
 }
 
 template <typename T, int W, bool RESET, bool SAVE8>
-__global__ void __launch_bounds__(kThreads)
-gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p) {
-    extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ Pieces sh;
+__global__ void __launch_bounds__(kThreads, SAVE8 ? 3 : MINB)
+gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ FwdMaps maps) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ Shared sh;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int C = p.cluster, rank = C > 1 ? int(cluster_rank()) : 0;
     const int e0 = int(blockIdx.x) / C * 64, e = e0 + 2 * lane;
@@ -131,16 +145,41 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p) {
     const bool in0 = e < p.ED, in1 = e + 1 < p.ED;
 
     uint8_t *mine = ring + warp * kStages * kStageBytes<T, W>;
+    if (threadIdx.x == 0) {
+        if (C > 1) sh.ex.init();
+        sh.ex.abort = 0;
+    }
+    if (W == 16) {
+        if (lane == 0) {
+            for (int k = 0; k < kStages; ++k) tc::mbar_init(&sh.full[warp][k], 1);
+            tc::mbar_fence_init();
+            tc::fence_proxy_async_smem();
+        }
+    } else if (e0 + 64 > p.ED) {
+        clear_ring(mine, kStages * kStageBytes<T, W>);
+    }
+    __syncthreads();
+
     auto fetch = [&](int turn) {
         const int t = (turn * C + rank) * kBlock + warp * kSteps;
         const int n = min(kSteps, p.L - t);
-        if (turn < turns && n > 0) {
-            uint8_t *to = mine + turn % kStages * kStageBytes<T, W>;
+        uint8_t *to = mine + turn % kStages * kStageBytes<T, W>;
+        if constexpr (W == 16) {
+            if (lane == 0 && turn < turns && n > 0 && !aborted(&sh.ex.abort)) {
+                uint64_t *bar = &sh.full[warp][turn % kStages];
+                tc::mbar_arrive_expect_tx(bar, uint32_t(kStageBytes<T, W>));
 #pragma unroll
-            for (int k = 0; k < 3; ++k)
-                copy_rows<T, W>(to + k * kSteps * kPitch<T, W>, p.in[k], b * p.L + t, n, e0, p.ED);
+                for (int k = 0; k < 3; ++k)
+                    tc::tma_load_3d(to + k * kSteps * kPitch<T, W>, &maps.in[k], bar, e0, t, int(b));
+            }
+        } else {
+            if (turn < turns && n > 0) {
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    copy_rows<T, W, kSteps>(to + k * kSteps * kPitch<T, W>, p.in[k], b * p.L + t, n, e0, p.ED);
+            }
+            cp_async_commit();
         }
-        cp_async_commit();
     };
     auto reset_of = [&](int turn) -> uint32_t {
         const int t = (turn * C + rank) * kBlock + warp * kSteps + lane;
@@ -148,28 +187,31 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p) {
     };
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) fetch(k);
-    if (C > 1) cluster_sync();     // every block runs before another writes to its shared memory
     uint32_t next_cut = RESET ? reset_of(0) : 0;
 
     const float2 rate = make_float2(in0 ? decay_rate(p.lam[e], p.c) : 0.0f, in1 ? decay_rate(p.lam[e + 1], p.c) : 0.0f);
     const bool wide = __any_sync(0xffffffffu, !(fmaxf(rate.x, rate.y) < kSlow));
     float2 carry = both(0.0f);     // the state that enters the cluster's next tiles
     if (p.h0) carry = make_float2(in0 ? p.h0[b * p.ED + e] : 0.0f, in1 ? p.h0[b * p.ED + e + 1] : 0.0f);
+    if (C > 1) cluster_sync();     // every block runs before another writes to its shared memory
 
     for (int turn = 0; turn < turns; ++turn) {
         const int tile = turn * C + rank, t0 = tile * kBlock + warp * kSteps, buf = turn & 1;
         const int n = min(kSteps, p.L - t0);      // <= 0 behind the end
         const int64_t row0 = b * p.L + t0;
-        fetch(turn + kStages - 1);
-        cp_async_wait<kStages - 1>();
-        __syncwarp();
-        const uint8_t *rows = mine + turn % kStages * kStageBytes<T, W>;
+        uint8_t *rows = mine + turn % kStages * kStageBytes<T, W>;
+        if constexpr (W == 16) {
+            if (n > 0) wait_or_abort(&sh.full[warp][turn % kStages], turn / kStages & 1, &sh.ex.abort, &g_device_error);
+        } else {
+            cp_async_wait<kStages - 2>();
+            __syncwarp();
+        }
         uint32_t cut = 0;
         if (RESET) {
             cut = __ballot_sync(0xffffffffu, next_cut != 0);
             next_cut = reset_of(turn + 1);
         }
-        if (SAVE8 && n > 0) keep_8bit<T, W>(rows, p.kept, row0, n, e0, p.ED, p.rows);
+        if (SAVE8 && n > 0) keep_8bit<T, W>(rows, p.kept, row0, n, e0, p.ED, p.rows, W == 16);
 
         // steps behind the end leave their piece wrong; nothing after them reads it
         float2 a[kSteps], s[kSteps], A, H;
@@ -177,51 +219,38 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p) {
             coefficients<T, W, true, RESET>(rows, row0, p.ED, rate, cut, a, s, A, H);
         else
             coefficients<T, W, false, false>(rows, row0, p.ED, rate, 0, a, s, A, H);
-        __syncwarp();      // all lanes have read before any lane copies over these rows
-
         sh.warp[buf][warp][lane] = make_float4(A.x, A.y, H.x, H.y);
-        if (RESET && lane == 0) sh.cuts[buf][warp] = cut;
+        // the stage that the next rows go to was read, and its outputs stored from, a turn ago
+        if (W == 16 && lane == 0) tc::bulk_wait_read0();
+        __syncwarp();
+        fetch(turn + kStages - 1);
         __syncthreads();
 
-        // the pieces before this warp's in its block, and the whole block's
+        // The state that enters this warp's steps: the pieces before its own,
+        // in its block (from 0 with their product where blocks form a cluster),
+        // then in the blocks before.
         float2 h = carry, all = carry;
         if (C == 1) {
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) {
                 if (k == warp) h = all;
-                const float4 v = sh.warp[buf][k][lane];
-                const bool dropped = RESET && sh.cuts[buf][k];
-                const float2 on = fma2(make_float2(v.x, v.y), all, make_float2(v.z, v.w));
-                all = dropped ? make_float2(v.z, v.w) : on;
+                all = after<RESET>(sh.warp[buf][k][lane], all);
             }
         } else {
-            float2 A0 = both(1.0f), H0 = both(0.0f), A1 = A0, H1 = H0;
-            uint32_t cut0 = 0, cut1 = 0;
+            float4 before = make_float4(1.0f, 1.0f, 0.0f, 0.0f), sum = before;
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) {
-                if (k == warp) A0 = A1, H0 = H1, cut0 = cut1;
-                const float4 v = sh.warp[buf][k][lane];
-                const bool dropped = RESET && sh.cuts[buf][k];
-                const float2 on = fma2(make_float2(v.x, v.y), H1, make_float2(v.z, v.w));
-                A1 = mul2(A1, make_float2(v.x, v.y));
-                H1 = dropped ? make_float2(v.z, v.w) : on;
-                if (RESET) cut1 |= sh.cuts[buf][k];
+                if (k == warp) before = sum;
+                sum = joined<RESET>(sum, sh.warp[buf][k][lane]);
             }
-            if (warp < C) {
-                put_remote(&sh.block[buf][rank][lane], warp, make_float4(A1.x, A1.y, H1.x, H1.y));
-                if (RESET && lane == 0) put_remote_u32(&sh.block_cut[buf][rank], warp, cut1);
-            }
-            cluster_sync();
+            sh.ex.send<kWarps>(buf, C, rank, warp, lane, sum);
+            sh.ex.wait(buf, turn >> 1 & 1, &g_device_error);
             for (int k = 0; k < C; ++k) {
                 if (k == rank) h = all;
-                const float4 v = sh.block[buf][k][lane];
-                const bool dropped = RESET && sh.block_cut[buf][k];
-                const float2 on = fma2(make_float2(v.x, v.y), all, make_float2(v.z, v.w));
-                all = dropped ? make_float2(v.z, v.w) : on;
+                all = after<RESET>(sh.ex.piece[buf][k][lane], all);
             }
-            if (p.kept.states && warp == 0 && tile < tiles) carry = h;      // entering the tile
-            const float2 on = fma2(A0, h, H0);
-            h = RESET && cut0 ? H0 : on;
+            if (warp == 0) carry = h;      // entering the tile
+            h = after<RESET>(before, h);
         }
         if (p.kept.states && warp == 0 && tile < tiles) {
             float *k = p.kept.states + (b * tiles + tile) * p.ED + e;
@@ -236,11 +265,23 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p) {
             h = RESET && (cut >> j & 1) ? s[j] : on;
             s[j] = h;
         }
-        T *y = p.y + row0 * p.ED + e;
+        if constexpr (W == 16) {
+            // over the lane's own elements of x, and from there as one box
 #pragma unroll
-        for (int j = 0; j < kSteps; ++j)
-            if (j < n) put_pair(y + int64_t(j) * p.ED, s[j], p.pair_stores, in0, in1);
-        if (p.h_final) {
+            for (int j = 0; j < kSteps; ++j) put2(reinterpret_cast<T *>(rows + j * kPitch<T, W>) + 2 * lane, s[j]);
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && n > 0) {
+                tma_store_3d(&maps.y, rows, e0, t0, int(b));
+                tc::bulk_commit();
+            }
+        } else {
+            T *y = p.y + row0 * p.ED + e;
+#pragma unroll
+            for (int j = 0; j < kSteps; ++j)
+                if (j < n) put_pair(y + int64_t(j) * p.ED, s[j], p.pair_stores, in0, in1);
+        }
+        if (p.h_final && t0 < p.L && t0 + kSteps >= p.L) {
 #pragma unroll
             for (int j = 0; j < kSteps; ++j)
                 if (t0 + j == p.L - 1) {
@@ -249,7 +290,14 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p) {
                 }
         }
     }
-    cp_async_wait<0>();
+    if (W == 16) {
+        if (lane == 0) {
+            tc::bulk_wait_read0();
+            if (aborted(&sh.ex.abort)) linger();
+        }
+    } else {
+        cp_async_wait<0>();
+    }
     if (C > 1) cluster_sync();     // no block leaves while another may still write to it
 }
 
@@ -269,35 +317,29 @@ gated_step_kernel(const T *__restrict__ x, const T *__restrict__ gr, const T *__
     const float2 s = sigmoid2<ACC>(make_float2(to_f32(gr[at]), to_f32(gi[at])));
     float2 a, w;
     decay2<ACC, true>(both(decay_rate(lam[e], c) * s.x), a, w);
-    const float2 v = one_minus_square(w);
+    const float2 v = one_minus_square(a, w);
     const float h = fmaf(a.x, states[page * ED + e], v.x * rsqrt2<ACC>(v).x * s.y * to_f32(x[at]));
     states[page * ED + e] = h;
     put(y + at, h);
 }
 
 template <typename T, int W, bool RESET, bool SAVE8>
-static cudaError_t start_fwd(const FwdArgs<T> &p, int64_t Bs, cudaStream_t st) {
+static cudaError_t start_fwd(const FwdArgs<T> &p, const FwdMaps &maps, int64_t Bs, cudaStream_t st) {
     auto kern = gated_fwd_kernel<T, W, RESET, SAVE8>;
-    const int smem = kWarps * kStages * kStageBytes<T, W>;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned((p.ED + 63) / 64 * p.cluster), unsigned(Bs));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = size_t(smem);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {unsigned(p.cluster), 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    return start_clusters(kern, kWarps * kStages * kStageBytes<T, W>, kThreads, p.ED, p.cluster, Bs, st, p, maps);
 }
 
 template <typename T, int W>
 static cudaError_t start_fwd(const FwdArgs<T> &p, int64_t Bs, cudaStream_t st) {
-    if (p.kept.x_q) return p.reset ? start_fwd<T, W, true, true>(p, Bs, st) : start_fwd<T, W, false, true>(p, Bs, st);
-    return p.reset ? start_fwd<T, W, true, false>(p, Bs, st) : start_fwd<T, W, false, false>(p, Bs, st);
+    FwdMaps maps{};
+    if (W == 16) {
+        for (int k = 0; k < 3; ++k)
+            if (!rows_map(&maps.in[k], p.in[k], Bs, p.L, p.ED, kSteps)) return cudaErrorInvalidValue;
+        if (!rows_map(&maps.y, p.y, Bs, p.L, p.ED, kSteps)) return cudaErrorInvalidValue;
+    }
+    if (p.kept.x_q)
+        return p.reset ? start_fwd<T, W, true, true>(p, maps, Bs, st) : start_fwd<T, W, false, true>(p, maps, Bs, st);
+    return p.reset ? start_fwd<T, W, true, false>(p, maps, Bs, st) : start_fwd<T, W, false, false>(p, maps, Bs, st);
 }
 
 template <typename T>
@@ -305,18 +347,32 @@ cudaError_t launch_fwd(const T *x, const T *gr, const T *gi, const float *lam, f
                        const uint8_t *reset, const float *h0, T *y, float *h_final,
                        const Kept &kept, int64_t Bs, int64_t L, int64_t ED, int num_sms,
                        cudaStream_t st) {
+    auto at = [](const void *q) { return reinterpret_cast<uintptr_t>(q); };
     FwdArgs<T> p{{x, gr, gi}, lam, c, reset, h0, y, h_final, kept, int(L), int(ED), 1, Bs * L, 0};
-    const uintptr_t in = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(gr) |
-                         reinterpret_cast<uintptr_t>(gi);
-    p.pair_stores = ED % 2 == 0 && reinterpret_cast<uintptr_t>(y) % (2 * sizeof(T)) == 0;
-    p.cluster = cluster_for(Bs, L, ED, num_sms);
-    const uintptr_t q = reinterpret_cast<uintptr_t>(kept.x_q) | reinterpret_cast<uintptr_t>(kept.r_q) |
-                        reinterpret_cast<uintptr_t>(kept.i_q);
-    const int W = widest_copy<T>(in, ED);
-    if (W == 16 && q % 2 == 0) return start_fwd<T, 16>(p, Bs, st);
+    p.pair_stores = ED % 2 == 0 && at(y) % (2 * sizeof(T)) == 0;
+    const int W = widest_copy<T>(at(x) | at(gr) | at(gi), ED);
+    const bool boxes = W == 16 && at(y) % 16 == 0 && (at(kept.x_q) | at(kept.r_q) | at(kept.i_q)) % 2 == 0;
+    p.cluster = cluster_for(Bs, L, ED, int64_t(num_sms) * (sizeof(T) == 4 ? 2 : kept.x_q ? 3 : 4), kMaxCluster);
+#ifdef CL
+    p.cluster = CL;
+#endif
+    if (boxes) return start_fwd<T, 16>(p, Bs, st);
     if (W >= 4) return start_fwd<T, 4>(p, Bs, st);
     if constexpr (sizeof(T) == 2) return start_fwd<T, 1>(p, Bs, st);
     return cudaErrorInvalidValue;      // fp32 is aligned to its 4 bytes
+}
+
+// Read and clear this unit's device error word (host side, synchronous).
+cudaError_t take_device_error(unsigned int *out) {
+    unsigned int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_device_error, sizeof(v));
+    if (e != cudaSuccess) return e;
+    if (v) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero));
+    }
+    *out = v;
+    return e;
 }
 
 template <typename T>

@@ -8,14 +8,34 @@
 #pragma once
 
 #include "ssm_common.cuh"
+#include "tc_ptx.cuh"
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <type_traits>
 
 namespace ssm {
 namespace gated {
 
 constexpr int kBlock = SSM_GATED_BLOCK;   // steps between two kept states
 
-// A thread-block cluster's barrier and the address of a variable in another
-// of its blocks' shared memory.
+// Inputs of one pass: the tensors themselves, or their 8-bit checkpoint.
+struct Kept {
+    float *states;                  // (Bs, ceil(L / 64), ED)
+    int8_t *x_q, *r_q, *i_q;        // (Bs, L, ED)
+    float *x_s, *r_s, *i_s;         // (ceil(ED / 64), Bs * L)
+};
+
+// ---- exchange between the blocks of a cluster --------------------------------
+// Each block sends its tile's piece to every block of the cluster, its own
+// included, as asynchronous stores that count towards the receiver's
+// mbarrier: no block waits for its own stores to arrive anywhere, as a
+// cluster barrier would have it do (its release took 1.2 of 7 cycles an
+// instruction).  Two buffers are enough: a block sends for turn s + 2 only
+// after it has received every piece of turn s + 1, and each of those was sent
+// after its sender had read turn s.
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -24,25 +44,79 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void put_remote(const float4 *at, uint32_t rank, float4 v) {
-    uint32_t a;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z),
-                 "f"(v.w)
-                 : "memory");
+
+constexpr int kMaxCluster = 8;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+
+struct Exchange {
+    float4 piece[2][kMaxCluster][32];
+    uint64_t full[2];
+    int abort;      // a wait ran out: this block waits no more, its results are unspecified
+
+    // One thread; a cluster barrier follows.
+    __device__ __forceinline__ void init() {
+        tc::mbar_init(&full[0], 1);
+        tc::mbar_init(&full[1], 1);
+        tc::mbar_fence_init();
+    }
+    // Warp w of WARPS sends to the blocks w, w + WARPS, ...
+    template <int WARPS>
+    __device__ __forceinline__ void send(int buf, int C, int rank, int warp, int lane, float4 v) {
+        if (warp == 0 && lane == 0) tc::mbar_arrive_expect_tx(&full[buf], uint32_t(C) * 32 * 16);
+        for (int k = warp; k < C; k += WARPS) {
+            uint32_t to, bar;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(&piece[buf][rank][lane])), "r"(k));
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(smem_u32(&full[buf])), "r"(k));
+            asm volatile(
+                "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+                "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+                : "memory");
+        }
+    }
+    __device__ __forceinline__ bool arrived(int buf, uint32_t parity) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n"
+            " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(smem_u32(&full[buf])), "r"(parity)
+            : "memory");
+        return ok != 0;
+    }
+    // Every thread; gives up after kWaitLimitNs and then reports in *error.
+    __device__ __forceinline__ void wait(int buf, uint32_t parity, unsigned int *error) {
+        if (arrived(buf, parity)) return;
+        const uint64_t t0 = tc::globaltimer_ns();
+        while (!arrived(buf, parity)) {
+            if (*reinterpret_cast<volatile int *>(&abort)) return;
+            if (tc::globaltimer_ns() - t0 > kWaitLimitNs) {
+                *reinterpret_cast<volatile int *>(&abort) = 1;
+                atomicOr(error, 1u);
+                return;
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ bool aborted(const int *abort) { return *reinterpret_cast<const volatile int *>(abort); }
+// What a block does before it leaves after a wait that ran out: copies into
+// its shared memory may still be in flight, and get the same time again.
+__device__ __forceinline__ void linger() {
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (tc::globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(1000);
+}
+// Waits for a warp's own copies; the same limit.
+__device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, int *abort, unsigned int *error) {
+    if (tc::mbar_wait_bounded(bar, parity, abort, kWaitLimitNs)) return;
+    *reinterpret_cast<volatile int *>(abort) = 1;
+    atomicOr(error, 1u);
 }
 
-// Inputs of one pass: the tensors themselves, or their 8-bit checkpoint.
-struct Kept {
-    float *states;                  // (Bs, ceil(L / 64), ED)
-    int8_t *x_q, *r_q, *i_q;        // (Bs, L, ED)
-    float *x_s, *r_s, *i_s;         // (ceil(ED / 64), Bs * L)
-};
-__device__ __forceinline__ void put_remote_u32(const uint32_t *at, uint32_t rank, uint32_t v) {
-    uint32_t a;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
+// A piece's A carries in its sign whether a step of it dropped the state
+// before (A is then -0): the carried state may be an infinity or NaN, which
+// 0 times it would keep.
+__device__ __forceinline__ bool drops(float A) { return __float_as_int(A) < 0; }
 
 // c softplus(lam); e^lam overflows above 88, where softplus(lam) = lam.
 __device__ __forceinline__ float decay_rate(float lam, float c) {
@@ -95,20 +169,19 @@ __device__ __forceinline__ float2 sigmoid2(float2 v) {
 }
 
 // Decays from t = -la >= 0: a = e^-t and w = 1 - a, w to full relative
-// accuracy, so that 1 - a^2 = w (2 - w) does not cancel for slow decays (a -> 1)
-// and a = 1 - w is rounded once.  For t < 0.7, w = t Q(t) with Q a
-// fifth-degree fit of (1 - e^-t) / t on [0, 0.7] (Chebyshev nodes; relative
-// error 1.2e-8 in exact arithmetic); from 0.7 on 1 - a loses at most one bit.
-// WIDE says that t may exceed 0.7: t <= c softplus(lam), so a warp knows from
+// accuracy, so that 1 - a^2 = w (1 + a) does not cancel for slow decays (a -> 1)
+// and a = 1 - w is rounded once.  For t < 0.4, w = t Q(t) with Q a
+// fourth-degree fit of (1 - e^-t) / t on [0, 0.4] (Chebyshev nodes; relative
+// error 5.2e-8 in exact arithmetic); from 0.4 on 1 - a loses at most two bits.
+// WIDE says that t may exceed 0.4: t <= c softplus(lam), so a warp knows from
 // its channels alone.
 // w is kept above kLeast, far below what it adds to, so that t = 0 needs no
 // case of its own where (1 - a^2)^(-1/2) is taken.
-constexpr float kSlow = 0.7f, kLeast = 1e-30f;
+constexpr float kSlow = 0.4f, kLeast = 1e-30f;
 __device__ __forceinline__ float2 slow_loss(float2 t) {
-    float2 q = fma2(t, both(-0x1.0f0144p-10f), both(0x1.08671cp-7f));
-    q = fma2(q, t, both(-0x1.5491aap-5f));
-    q = fma2(q, t, both(0x1.554d72p-3f));
-    q = fma2(q, t, both(-0x1.ffffc4p-2f));
+    float2 q = fma2(t, both(0x1.cf2208p-8f), both(-0x1.51d0aap-5f));
+    q = fma2(q, t, both(0x1.5535acp-3f));
+    q = fma2(q, t, both(-0x1.ffff38p-2f));
     q = fma2(q, t, both(1.0f));
     return fma2(q, t, both(kLeast));
 }
@@ -130,8 +203,8 @@ __device__ __forceinline__ void decay2(float2 t, float2 &a, float2 &w) {
     }
 }
 
-// 1 - a^2
-__device__ __forceinline__ float2 one_minus_square(float2 w) { return mul2(w, fma2(w, both(-1.0f), both(2.0f))); }
+// 1 - a^2 = w (1 + a)
+__device__ __forceinline__ float2 one_minus_square(float2 a, float2 w) { return fma2(w, a, w); }
 
 // v^(-1/2), for v > 0
 template <bool ACC>
@@ -179,67 +252,81 @@ __device__ __forceinline__ void cp_async4(void *smem_dst, const void *gsrc, int 
                  : "memory");
 }
 
-// ---- a warp's rows of a tile ----------------------------------------------------
-// A tile is 64 steps x 64 channels; each of a block's 8 warps owns 8 steps, a
-// lane two channels.  A warp copies its own rows ahead of their use, so no
-// block barrier stands between a copy and its use.
-constexpr int kWarps = 8, kSteps = kBlock / kWarps, kThreads = 32 * kWarps;
-constexpr int kMaxCluster = 8;
+// ---- pieces of the time axis: h -> A h + H (A of two channels, H of two) -----
+template <bool RESET>
+__device__ __forceinline__ float2 after(float4 piece, float2 h) {
+    const float2 on = fma2(make_float2(piece.x, piece.y), h, make_float2(piece.z, piece.w));
+    return RESET && drops(piece.x) ? make_float2(piece.z, piece.w) : on;
+}
+// One piece, then another.
+template <bool RESET>
+__device__ __forceinline__ float4 joined(float4 first, float4 second) {
+    const float2 A = mul2(make_float2(first.x, first.y), make_float2(second.x, second.y));
+    const float2 H = after<RESET>(second, make_float2(first.z, first.w));
+    // -0 times -0 would lose the sign
+    return RESET && drops(second.x) ? second : make_float4(A.x, A.y, H.x, H.y);
+}
 
-// W is the widest copy that every row's start allows: 16 bytes, 4 (rows of
-// narrow elements then start anywhere in their first word, and need one word
-// more), or 1 for plain loads of elements, which wait for their data.
+// ---- a warp's rows of a tile ----------------------------------------------------
+// A tile is 64 steps x 64 channels; each of a block's warps owns STEPS of the
+// steps, a lane two channels.  A warp copies its own rows ahead of their use,
+// so no block barrier stands between a copy and its use.
+
+// W says how: 16, tensor copies (rows are multiples of 16 bytes); 4, copies of
+// words (rows of narrow elements then start anywhere in their first word, and
+// need one word more); 1, plain loads of elements, which wait for their data.
 template <typename T, int W>
 constexpr bool kShifted = W == 4 && sizeof(T) < 4;
 template <typename T, int W>
 constexpr int kPitch = 64 * int(sizeof(T)) + (kShifted<T, W> ? 16 : 0);
 
-template <typename T, int W>
+template <typename T, int W, int STEPS>
 __device__ __forceinline__ void copy_rows(uint8_t *to, const T *from, int64_t row0, int n_rows, int e0, int ED) {
     constexpr int kSize = int(sizeof(T));
     const int lane = threadIdx.x % 32;
-    if constexpr (W == 16 || (W == 4 && kSize == 4)) {
-        constexpr int kChunks = 64 * kSize / W, kPer = W / kSize;
+    if constexpr (W == 4 && kSize == 4) {
+        const T *src = from + row0 * ED + e0 + lane;
 #pragma unroll
-        for (int i = 0; i < kSteps * kChunks / 32; ++i) {
-            const int row = (i * 32 + lane) / kChunks, e = (i * 32 + lane) % kChunks * kPer;
-            const bool in = row < n_rows && e0 + e < ED;
-            const T *src = in ? from + (row0 + row) * ED + e0 + e : from;
-            uint8_t *dst = to + row * kPitch<T, W> + e * kSize;
-            if constexpr (W == 16)
-                cp_async16(dst, src, in ? 16 : 0);
-            else
-                cp_async4(dst, src, in ? 4 : 0);
-        }
+        for (int row = 0; row < STEPS; ++row)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (row < n_rows && e0 + lane + 32 * k < ED)
+                    cp_async4(to + row * kPitch<T, W> + 4 * lane + 128 * k, src + int64_t(row) * ED + 32 * k, 4);
     } else if constexpr (W == 4) {
         constexpr int kPer = 4 / kSize, kWords = 64 / kPer + 1;
 #pragma unroll
-        for (int row = 0; row < kSteps; ++row) {
+        for (int row = 0; row < STEPS; ++row) {
             const int64_t begin = (row0 + row) * ED, end = begin + ED;
             // the word that holds the row's first element; the tensor starts on a word
             const int64_t first = (begin + e0) & ~int64_t(kPer - 1);
 #pragma unroll
             for (int k = 0; k < (kWords + 31) / 32; ++k) {
                 const int word = lane + 32 * k;
-                if (word >= kWords) continue;
                 const int64_t e = first + kPer * word;
-                const bool in = row < n_rows && e < end;
                 // nothing behind the row's end, which may be the tensor's
-                const int bytes = in ? int(min(int64_t(kPer), end - e)) * kSize : 0;
-                cp_async4(to + row * kPitch<T, W> + 4 * word, in ? from + e : from, bytes);
+                if (word < kWords && row < n_rows && e < end)
+                    cp_async4(to + row * kPitch<T, W> + 4 * word, from + e,
+                              int(min(int64_t(kPer), end - e)) * kSize);
             }
         }
     } else {
 #pragma unroll
-        for (int row = 0; row < kSteps; ++row)
+        for (int row = 0; row < STEPS; ++row)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int e = lane + 32 * k;
-                T v = T(0.0f);
-                if (row < n_rows && e0 + e < ED) v = from[(row0 + row) * ED + e0 + e];
-                *reinterpret_cast<T *>(to + row * kPitch<T, W> + e * kSize) = v;
+                if (row < n_rows && e0 + e < ED)
+                    *reinterpret_cast<T *>(to + row * kPitch<T, W> + e * kSize) = from[(row0 + row) * ED + e0 + e];
             }
     }
+}
+
+// Zeros in a warp's whole ring, before its first copy: columns behind the
+// row's end are never copied to.
+__device__ __forceinline__ void clear_ring(uint8_t *ring, int bytes) {
+    for (int i = threadIdx.x % 32 * 16; i < bytes; i += 32 * 16)
+        *reinterpret_cast<uint4 *>(ring + i) = make_uint4(0, 0, 0, 0);
+    __syncwarp();
 }
 
 // Elements between a row's first word and its first element.
@@ -287,18 +374,79 @@ __device__ __forceinline__ void put_pair(T *p, float2 v, bool pairs, bool in0, b
     }
 }
 
+// ---- tensor copies of boxes of STEPS rows x 64 channels --------------------------
+// The driver's tensor-map encoder.  Only a successful lookup is kept.
+inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> cached{nullptr};
+    PFN_cuTensorMapEncodeTiled_v12000 fn = cached.load(std::memory_order_acquire);
+    if (fn != nullptr) return fn;
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess) {
+        fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+        cached.store(fn, std::memory_order_release);
+    }
+    return fn;
+}
+template <typename T>
+inline bool rows_map(CUtensorMap *m, const T *base, int64_t Bs, int64_t L, int64_t ED, int steps) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {cuuint64_t(ED), cuuint64_t(L), cuuint64_t(Bs)};
+    const cuuint64_t strides[2] = {cuuint64_t(ED) * sizeof(T), cuuint64_t(L) * cuuint64_t(ED) * sizeof(T)};
+    const cuuint32_t box[3] = {64, cuuint32_t(steps), 1}, each[3] = {1, 1, 1};
+    return fn(m, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                 : sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                  : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+              3, const_cast<T *>(base), dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+__device__ __forceinline__ void tma_store_3d(const void *tmap, const void *src, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tmap),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
+// Launches `kern` with a block of `threads` for 64 channels of a sequence and
+// one of its `cluster` shares of the time axis.
+template <typename... Args>
+inline cudaError_t start_clusters(void (*kern)(Args...), int smem, int threads, int64_t ED, int cluster, int64_t Bs,
+                                  cudaStream_t st, const std::decay_t<Args> &...args) {
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned((ED + 63) / 64 * cluster), unsigned(Bs));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {unsigned(cluster), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 template <typename T>
 inline int widest_copy(uintptr_t at, int64_t ED) {
     return ED * int64_t(sizeof(T)) % 16 == 0 && at % 16 == 0 ? 16 : at % 4 == 0 ? 4 : 1;
 }
 
-// Blocks of a cluster take neighbouring tiles of a sequence at once: as many
-// as bring the GPU two blocks an SM, none with less than two tiles.
-inline int cluster_for(int64_t Bs, int64_t L, int64_t ED, int num_sms) {
+// Blocks of a cluster take neighbouring tiles of a sequence at once.  `slots`
+// blocks run at a time.  Fewer chains than slots: as many blocks a chain as
+// fit at once.  More: the size whose last round of blocks is fullest, a larger
+// one (and its exchange) only where it gains 3 % for each block more.
+inline int cluster_for(int64_t Bs, int64_t L, int64_t ED, int64_t slots, int most) {
     const int64_t chains = (ED + 63) / 64 * Bs, tiles = (L + kBlock - 1) / kBlock;
-    int c = 1;
-    while (c < kMaxCluster && chains * c * 2 <= 3 * num_sms && c * 2 <= tiles) c *= 2;
-    return c;
+    int best = 1;
+    double least = 0.0;
+    for (int c = 1; c <= most && c <= tiles; ++c) {
+        const double rounds = double((chains * c + slots - 1) / slots) / c * (1.0 + 0.03 * c);
+        if (c == 1 || rounds < least) best = c, least = rounds;
+    }
+    return best;
 }
 
 }  // namespace gated

@@ -14,11 +14,18 @@
 // from shared memory again, 1 - a^2 is computed again.
 #include "gated_scan.cuh"
 
+#include <algorithm>
+
 namespace ssm {
 namespace gated_bwd {
 using namespace gated;
 
-constexpr int kStages = 2;
+#ifndef BKST
+#define BKST 2
+#endif
+constexpr int kWarps = 8, kSteps = kBlock / kWarps, kThreads = 32 * kWarps, kStages = BKST;
+
+__device__ unsigned int g_device_error;
 
 template <typename T>
 struct BwdArgs {
@@ -37,18 +44,27 @@ struct BwdArgs {
 };
 
 // One stage of a warp's ring: rows of x, gate_r, gate_i (of type K: T, or
-// int8 with their 24 scales), then of dy.
+// int8 with their 24 scales), then of dy.  Boxes of outputs (W = 16) take the
+// places of the three inputs, or of their own behind the ring where those are
+// narrower.
 template <typename T, typename K, int W>
 struct Stage {
     static constexpr int kIn = kSteps * kPitch<K, W>, kDy = 3 * kIn, kScales = kDy + kSteps * kPitch<T, W>;
     static constexpr int kBytes = kScales + (sizeof(K) == 1 ? 128 : 0);
+    static constexpr int kOut = kSteps * kPitch<T, W>, kOwnOut = W == 16 && sizeof(K) < sizeof(T) ? 3 * kOut : 0;
+    static constexpr int kWarpBytes = kStages * kBytes + kOwnOut;
 };
 
-struct Pieces {
-    float4 warp[2][kWarps][32];              // A of two channels, state of two channels
-    float2 adjoint[2][kWarps][32];
-    float4 block[2][kMaxCluster][32];        // A, adjoint; written by the cluster's blocks
-    uint32_t cuts[2][kWarps], block_cut[2][kMaxCluster];
+// Boxes of 64 channels x kSteps rows (W = 16).
+struct BwdMaps {
+    CUtensorMap in[3], dy, out[3];
+};
+
+struct Shared {
+    float4 warp[2][kWarps][32];     // A of two channels, state of two channels
+    float2 adjoint[2][kWarps][32];  // the adjoint of the same piece
+    uint64_t full[kWarps][kStages]; // a warp's copies have arrived (W = 16)
+    Exchange ex;
 };
 
 template <typename T, typename K, int W>
@@ -80,13 +96,13 @@ __device__ __forceinline__ void pieces(const uint8_t *stage, int64_t row0, int E
         float2 w;
         decay2<ACC, GENERAL>(mul2(rate, sr[j]), a[j], w);
         const float2 in = mul2(si[j], input<T, K, W>(stage, 0, j, row0, ED));
-        const float2 v = one_minus_square(w);
+        const float2 v = one_minus_square(a[j], w);
         b[j] = mul2(mul2(v, rsqrt2<ACC>(v)), in);
         if (GENERAL && j >= n) a[j] = both(1.0f), b[j] = both(0.0f);
         if (GENERAL && (cut >> j & 1)) {
             a[j] = both(0.0f);
             b[j] = in;
-            A = both(0.0f);
+            A = both(-0.0f);
             H = in;
         } else {
             A = mul2(A, a[j]);
@@ -102,7 +118,7 @@ __device__ __forceinline__ void pieces(const uint8_t *stage, int64_t row0, int E
 }
 
 template <typename T, typename K, int W, bool GENERAL>
-__device__ __forceinline__ void gradients(const BwdArgs<T> &p, const uint8_t *stage, int64_t row0, float2 rate,
+__device__ __forceinline__ void gradients(const BwdArgs<T> &p, const uint8_t *stage, uint8_t *out, int64_t row0, float2 rate,
                                           uint32_t cut, int n, const float2 (&a)[kSteps], const float2 (&before)[kSteps],
                                           const float2 (&sr)[kSteps], const float2 (&si)[kSteps], float2 u, int e,
                                           bool in0, bool in1, float2 &sum) {
@@ -120,7 +136,7 @@ __device__ __forceinline__ void gradients(const BwdArgs<T> &p, const uint8_t *st
             if (t.x >= kSlow) w.x = 1.0f - a[j].x;
             if (t.y >= kSlow) w.y = 1.0f - a[j].y;
         }
-        const float2 v = one_minus_square(w), over = rsqrt2<ACC>(v);
+        const float2 v = one_minus_square(a[j], w), over = rsqrt2<ACC>(v);
         const float2 in = mul2(si[j], x);
         float2 gm = mul2(g, mul2(v, over));
         // la (a h - (a^2 / m) s_i x) = t a ((a / m) s_i x - h)
@@ -128,9 +144,18 @@ __device__ __forceinline__ void gradients(const BwdArgs<T> &p, const uint8_t *st
                         fma2(mul2(a[j], over), in, mul2(before[j], both(-1.0f))));
         if (dropped) gm = g, G = both(0.0f);
         const float2 dx = mul2(gm, si[j]), q = mul2(dx, x);
-        put_pair(p.dx + at + int64_t(j) * p.ED, dx, p.pair_stores, in0, in1);
-        put_pair(p.di + at + int64_t(j) * p.ED, fma2(mul2(q, both(-1.0f)), si[j], q), p.pair_stores, in0, in1);
-        put_pair(p.dr + at + int64_t(j) * p.ED, fma2(mul2(G, both(-1.0f)), sr[j], G), p.pair_stores, in0, in1);
+        const float2 dr = fma2(mul2(G, both(-1.0f)), sr[j], G), di = fma2(mul2(q, both(-1.0f)), si[j], q);
+        if constexpr (W == 16) {
+            // over the lane's own elements of the inputs
+            T *o = reinterpret_cast<T *>(out + j * kPitch<T, W>) + 2 * (threadIdx.x % 32);
+            put2(o, dx);
+            put2(o + Stage<T, K, W>::kOut / sizeof(T), dr);
+            put2(o + 2 * Stage<T, K, W>::kOut / sizeof(T), di);
+        } else {
+            put_pair(p.dx + at + int64_t(j) * p.ED, dx, p.pair_stores, in0, in1);
+            put_pair(p.dr + at + int64_t(j) * p.ED, dr, p.pair_stores, in0, in1);
+            put_pair(p.di + at + int64_t(j) * p.ED, di, p.pair_stores, in0, in1);
+        }
         sum = add2(sum, G);
         u = mul2(a[j], g);
         if (dropped) u = both(0.0f);
@@ -139,10 +164,10 @@ __device__ __forceinline__ void gradients(const BwdArgs<T> &p, const uint8_t *st
 
 template <typename T, typename K, int W, bool RESET>
 __global__ void __launch_bounds__(kThreads, 2)
-gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p) {
+gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ BwdMaps maps) {
     using S = Stage<T, K, W>;
-    extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ Pieces sh;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ Shared sh;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int C = p.cluster, rank = C > 1 ? int(cluster_rank()) : 0;
     const int e0 = int(blockIdx.x) / C * 64, e = e0 + 2 * lane;
@@ -150,30 +175,55 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p) {
     const int tiles = (p.L + kBlock - 1) / kBlock, turns = (tiles + C - 1) / C;
     const bool in0 = e < p.ED, in1 = e + 1 < p.ED;
 
-    uint8_t *mine = ring + warp * kStages * S::kBytes;
+    uint8_t *mine = ring + warp * S::kWarpBytes;
+    if (threadIdx.x == 0) {
+        if (C > 1) sh.ex.init();
+        sh.ex.abort = 0;
+    }
+    if (W == 16) {
+        if (lane == 0) {
+            for (int k = 0; k < kStages; ++k) tc::mbar_init(&sh.full[warp][k], 1);
+            tc::mbar_fence_init();
+            tc::fence_proxy_async_smem();
+        }
+    } else if (e0 + 64 > p.ED) {
+        clear_ring(mine, kStages * S::kBytes);
+    }
+    __syncthreads();
+
     auto fetch = [&](int turn) {
         const int t = (turn * C + rank) * kBlock + warp * kSteps;
         const int n = min(kSteps, p.L - t);
+        const int64_t row0 = b * p.L + t;
         if (turn >= 0 && n > 0) {
             uint8_t *to = mine + turn % kStages * S::kBytes;
-            const int64_t row0 = b * p.L + t;
-            if constexpr (sizeof(K) == 1) {
-                const int8_t *q[3] = {p.kept.x_q, p.kept.r_q, p.kept.i_q};
+            if constexpr (W == 16) {
+                if (lane == 0 && !aborted(&sh.ex.abort)) {
+                    uint64_t *bar = &sh.full[warp][turn % kStages];
+                    tc::mbar_arrive_expect_tx(bar, uint32_t(S::kScales));
 #pragma unroll
-                for (int k = 0; k < 3; ++k) copy_rows<int8_t, W>(to + k * S::kIn, q[k], row0, n, e0, p.ED);
-                if (lane < 3 * kSteps) {
-                    const float *s = lane < kSteps ? p.kept.x_s : lane < 2 * kSteps ? p.kept.r_s : p.kept.i_s;
-                    const bool in = lane % kSteps < n;
-                    cp_async4(to + S::kScales + 4 * lane,
-                              in ? s + (e0 / kGroup) * p.rows + row0 + lane % kSteps : s, in ? 4 : 0);
+                    for (int k = 0; k < 3; ++k) tc::tma_load_3d(to + k * S::kIn, &maps.in[k], bar, e0, t, int(b));
+                    tc::tma_load_3d(to + S::kDy, &maps.dy, bar, e0, t, int(b));
                 }
             } else {
+                if constexpr (sizeof(K) == 1) {
+                    const int8_t *q[3] = {p.kept.x_q, p.kept.r_q, p.kept.i_q};
 #pragma unroll
-                for (int k = 0; k < 3; ++k) copy_rows<T, W>(to + k * S::kIn, p.in[k], row0, n, e0, p.ED);
+                    for (int k = 0; k < 3; ++k) copy_rows<int8_t, W, kSteps>(to + k * S::kIn, q[k], row0, n, e0, p.ED);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) copy_rows<T, W, kSteps>(to + k * S::kIn, p.in[k], row0, n, e0, p.ED);
+                }
+                copy_rows<T, W, kSteps>(to + S::kDy, p.dy, row0, n, e0, p.ED);
             }
-            copy_rows<T, W>(to + S::kDy, p.dy, row0, n, e0, p.ED);
+            if constexpr (sizeof(K) == 1) {
+                if (lane < 3 * kSteps && lane % kSteps < n) {
+                    const float *s = lane < kSteps ? p.kept.x_s : lane < 2 * kSteps ? p.kept.r_s : p.kept.i_s;
+                    cp_async4(to + S::kScales + 4 * lane, s + (e0 / kGroup) * p.rows + row0 + lane % kSteps, 4);
+                }
+            }
         }
-        cp_async_commit();
+        if (W != 16 || sizeof(K) == 1) cp_async_commit();
     };
     auto reset_of = [&](int turn) -> uint32_t {
         const int t = (turn * C + rank) * kBlock + warp * kSteps + lane;
@@ -196,14 +246,22 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p) {
     float2 carry = both(0.0f), sum = both(0.0f);     // the adjoint that enters the cluster's next tiles from behind
     if (p.dh_final) carry = make_float2(in0 ? p.dh_final[b * p.ED + e] : 0.0f, in1 ? p.dh_final[b * p.ED + e + 1] : 0.0f);
 
+    uint32_t phases = 0;           // bit k: the parity that stage k's next copies complete
+
     for (int turn = turns - 1; turn >= 0; --turn) {
         const int t0 = (turn * C + rank) * kBlock + warp * kSteps, buf = turn & 1;
         const int n = min(kSteps, p.L - t0);      // <= 0 behind the end
         const int64_t row0 = b * p.L + t0;
-        fetch(turn - (kStages - 1));
-        cp_async_wait<kStages - 1>();
-        __syncwarp();
-        const uint8_t *stage = mine + turn % kStages * S::kBytes;
+        uint8_t *stage = mine + turn % kStages * S::kBytes;
+        if (W == 16 && n > 0) {
+            const int k = turn % kStages;
+            wait_or_abort(&sh.full[warp][k], phases >> k & 1, &sh.ex.abort, &g_device_error);
+            phases ^= 1u << k;
+        }
+        if (W != 16 || sizeof(K) == 1) {
+            cp_async_wait<kStages - 2>();
+            __syncwarp();
+        }
         uint32_t cut = 0;
         if (RESET) {
             cut = __ballot_sync(0xffffffffu, next_cut != 0);
@@ -221,48 +279,44 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p) {
 
         sh.warp[buf][warp][lane] = make_float4(A.x, A.y, H.x, H.y);
         sh.adjoint[buf][warp][lane] = U;
-        if (RESET && lane == 0) sh.cuts[buf][warp] = cut;
+        // the stage that the next rows go to was read, and its outputs stored from, a turn ago
+        if (W == 16 && lane == 0) tc::bulk_wait_read0();
+        __syncwarp();
+        fetch(turn - (kStages - 1));
         __syncthreads();
 
-        // the state that enters this warp's steps, the adjoint that enters them from behind
-        float2 u = carry, all = carry, Ab = both(1.0f), A1 = Ab;
-        uint32_t cut0 = 0, cut1 = 0;
-        if (C > 1) all = both(0.0f), u = both(0.0f);
+        // the state that enters this warp's steps, from the one kept
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-            if (k == warp) break;
-            const float4 v = sh.warp[buf][k][lane];
-            const float2 on = fma2(make_float2(v.x, v.y), h, make_float2(v.z, v.w));
-            h = RESET && sh.cuts[buf][k] ? make_float2(v.z, v.w) : on;
-        }
-#pragma unroll
-        for (int k = kWarps - 1; k >= 0; --k) {
-            if (k == warp) u = all, Ab = A1, cut0 = cut1;
+        for (int k = 0; k < kWarps - 1; ++k)
+            if (k < warp) h = after<RESET>(sh.warp[buf][k][lane], h);
+        // the adjoint that enters them from behind: through the warps behind
+        // (from 0 with their product where blocks form a cluster), then the blocks
+        auto behind = [&](int k) {
             const float4 v = sh.warp[buf][k][lane];
             const float2 w = sh.adjoint[buf][k][lane];
-            const float2 on = fma2(make_float2(v.x, v.y), all, w);
-            all = RESET && sh.cuts[buf][k] ? w : on;
-            if (C > 1) {
-                A1 = mul2(A1, make_float2(v.x, v.y));
-                if (RESET) cut1 |= sh.cuts[buf][k];
+            return make_float4(v.x, v.y, w.x, w.y);
+        };
+        float2 u = carry, all = carry;
+        if (C == 1) {
+#pragma unroll
+            for (int k = kWarps - 1; k >= 0; --k) {
+                if (k == warp) u = all;
+                all = after<RESET>(behind(k), all);
             }
-        }
-        if (C > 1) {
-            if (warp < C) {
-                put_remote(&sh.block[buf][rank][lane], warp, make_float4(A1.x, A1.y, all.x, all.y));
-                if (RESET && lane == 0) put_remote_u32(&sh.block_cut[buf][rank], warp, cut1);
+        } else {
+            float4 before = make_float4(1.0f, 1.0f, 0.0f, 0.0f), sum = before;
+#pragma unroll
+            for (int k = kWarps - 1; k >= 0; --k) {
+                if (k == warp) before = sum;
+                sum = joined<RESET>(sum, behind(k));
             }
-            cluster_sync();
-            float2 behind = carry;
-            all = carry;
+            sh.ex.send<kWarps>(buf, C, rank, warp, lane, sum);
+            sh.ex.wait(buf, (turns - 1 - turn) >> 1 & 1, &g_device_error);
             for (int k = C - 1; k >= 0; --k) {
-                if (k == rank) behind = all;
-                const float4 v = sh.block[buf][k][lane];
-                const float2 on = fma2(make_float2(v.x, v.y), all, make_float2(v.z, v.w));
-                all = RESET && sh.block_cut[buf][k] ? make_float2(v.z, v.w) : on;
+                if (k == rank) u = all;
+                all = after<RESET>(sh.ex.piece[buf][k][lane], all);
             }
-            const float2 on = fma2(Ab, behind, u);
-            u = RESET && cut0 ? u : on;
+            u = after<RESET>(before, u);
         }
         carry = all;
 
@@ -272,11 +326,25 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p) {
             h = RESET && (cut >> j & 1) ? s[j] : on;
             s[j] = at;
         }
+        uint8_t *out = S::kOwnOut ? mine + kStages * S::kBytes : stage;
         if (general)
-            gradients<T, K, W, true>(p, stage, row0, rate, cut, n, a, s, sr, si, u, e, in0, in1, sum);
+            gradients<T, K, W, true>(p, stage, out, row0, rate, cut, n, a, s, sr, si, u, e, in0, in1, sum);
         else
-            gradients<T, K, W, false>(p, stage, row0, rate, 0, kSteps, a, s, sr, si, u, e, in0, in1, sum);
-        __syncwarp();      // all lanes have read before any lane copies over this stage
+            gradients<T, K, W, false>(p, stage, out, row0, rate, 0, kSteps, a, s, sr, si, u, e, in0, in1, sum);
+        if (W == 16) {
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && n > 0) {
+                for (int k = 0; k < 3; ++k) tma_store_3d(&maps.out[k], out + k * S::kOut, e0, t0, int(b));
+                tc::bulk_commit();
+            }
+        }
+    }
+    if (W == 16) {
+        if (lane == 0) {
+            tc::bulk_wait_read0();
+            if (aborted(&sh.ex.abort)) linger();
+        }
     }
     cp_async_wait<0>();
     if (p.dh0 && warp == 0 && rank == 0) {
@@ -297,6 +365,19 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p) {
     if (C > 1) cluster_sync();     // no block leaves while another may still write to it
 }
 
+// Read and clear this unit's device error word (host side, synchronous).
+cudaError_t take_device_error(unsigned int *out) {
+    unsigned int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_device_error, sizeof(v));
+    if (e != cudaSuccess) return e;
+    if (v) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero));
+    }
+    *out = v;
+    return e;
+}
+
 // dlam from the blocks' sums, in their order.
 __global__ void __launch_bounds__(256)
 dlam_kernel(const float *__restrict__ part, const float *__restrict__ lam, float *__restrict__ dlam,
@@ -310,63 +391,65 @@ dlam_kernel(const float *__restrict__ part, const float *__restrict__ lam, float
 }
 
 template <typename T, typename K, int W, bool RESET>
-static cudaError_t start(const BwdArgs<T> &p, int64_t Bs, cudaStream_t st) {
-    auto kern = gated_bwd_kernel<T, K, W, RESET>;
-    const int smem = kWarps * kStages * Stage<T, K, W>::kBytes;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned((p.ED + 63) / 64 * p.cluster), unsigned(Bs));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = size_t(smem);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {unsigned(p.cluster), 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+static cudaError_t start(const BwdArgs<T> &p, const BwdMaps &maps, int64_t Bs, cudaStream_t st) {
+    return start_clusters(gated_bwd_kernel<T, K, W, RESET>, kWarps * Stage<T, K, W>::kWarpBytes, kThreads, p.ED,
+                          p.cluster, Bs, st, p, maps);
 }
 
 template <typename T, typename K>
 static cudaError_t start(const BwdArgs<T> &p, int W, int64_t Bs, cudaStream_t st) {
-    if (W == 16) return p.reset ? start<T, K, 16, true>(p, Bs, st) : start<T, K, 16, false>(p, Bs, st);
-    if (W == 4) return p.reset ? start<T, K, 4, true>(p, Bs, st) : start<T, K, 4, false>(p, Bs, st);
+    BwdMaps maps{};
+    if (W == 16) {
+        const K *in[3];
+        if constexpr (sizeof(K) == 1)
+            in[0] = p.kept.x_q, in[1] = p.kept.r_q, in[2] = p.kept.i_q;
+        else
+            in[0] = p.in[0], in[1] = p.in[1], in[2] = p.in[2];
+        T *const out[3] = {p.dx, p.dr, p.di};
+        for (int k = 0; k < 3; ++k)
+            if (!rows_map(&maps.in[k], in[k], Bs, p.L, p.ED, kSteps) ||
+                !rows_map(&maps.out[k], out[k], Bs, p.L, p.ED, kSteps))
+                return cudaErrorInvalidValue;
+        if (!rows_map(&maps.dy, p.dy, Bs, p.L, p.ED, kSteps)) return cudaErrorInvalidValue;
+        return p.reset ? start<T, K, 16, true>(p, maps, Bs, st) : start<T, K, 16, false>(p, maps, Bs, st);
+    }
+    if (W == 4) return p.reset ? start<T, K, 4, true>(p, maps, Bs, st) : start<T, K, 4, false>(p, maps, Bs, st);
     if constexpr (sizeof(K) < 4)
-        return p.reset ? start<T, K, 1, true>(p, Bs, st) : start<T, K, 1, false>(p, Bs, st);
+        return p.reset ? start<T, K, 1, true>(p, maps, Bs, st) : start<T, K, 1, false>(p, maps, Bs, st);
     return cudaErrorInvalidValue;      // fp32 is aligned to its 4 bytes
 }
 
 template <typename T>
 cudaError_t launch(const T *x, const T *gr, const T *gi, const float *lam, float c,
                    const uint8_t *reset, const T *dy, const float *dh_final, const Kept &kept, T *dx,
-                   T *dr, T *di, float *dlam, float *dh0, int64_t Bs, int64_t L, int64_t ED,
-                   int num_sms, cudaStream_t st) {
+                   T *dr, T *di, float *dlam, float *dh0, float *scratch, int64_t Bs, int64_t L,
+                   int64_t ED, int num_sms, cudaStream_t st) {
     auto at = [](const void *q) { return reinterpret_cast<uintptr_t>(q); };
-    BwdArgs<T> p{{x, gr, gi}, lam, c, reset, dy, dh_final, kept, dx, dr, di, nullptr, dh0,
-                 int(L), int(ED), cluster_for(Bs, L, ED, num_sms), Bs * L, 0};
+    BwdArgs<T> p{{x, gr, gi}, lam, c, reset, dy, dh_final, kept, dx, dr, di, scratch, dh0,
+                 int(L), int(ED), cluster_for(Bs, L, ED, int64_t(num_sms) * 2, kMaxCluster), Bs * L, 0};
+#ifdef BCL
+    p.cluster = BCL;
+#endif
     p.pair_stores = ED % 2 == 0 && (at(dx) | at(dr) | at(di)) % (2 * sizeof(T)) == 0;
-    cudaError_t err = cudaMallocAsync(&p.part, size_t(Bs * p.cluster * ED) * sizeof(float), st);
-    if (err != cudaSuccess) return err;
+    int W = widest_copy<T>(at(dy), ED);
+    if (W == 16 && (at(dx) | at(dr) | at(di)) % 16 != 0) W = 4;
+    cudaError_t err;
     if (kept.x_q)
-        err = start<T, int8_t>(p, min(widest_copy<int8_t>(at(kept.x_q) | at(kept.r_q) | at(kept.i_q), ED),
-                                      widest_copy<T>(at(dy), ED)),
-                               Bs, st);
+        err = start<T, int8_t>(p, std::min(W, widest_copy<int8_t>(at(kept.x_q) | at(kept.r_q) | at(kept.i_q), ED)), Bs, st);
     else
-        err = start<T, T>(p, widest_copy<T>(at(x) | at(gr) | at(gi) | at(dy), ED), Bs, st);
+        err = start<T, T>(p, std::min(W, widest_copy<T>(at(x) | at(gr) | at(gi), ED)), Bs, st);
     if (err == cudaSuccess) {
         dlam_kernel<<<unsigned((ED + 255) / 256), 256, 0, st>>>(p.part, lam, dlam, Bs * p.cluster, ED);
         err = cudaGetLastError();
     }
-    const cudaError_t e2 = cudaFreeAsync(p.part, st);
-    return err != cudaSuccess ? err : e2;
+    return err;
 }
 
 #define SSM_GATED_BWD_INSTANTIATE(T)                                                              \
     template cudaError_t launch<T>(const T *, const T *, const T *, const float *, float,         \
                                    const uint8_t *, const T *, const float *, const Kept &, T *,  \
-                                   T *, T *, float *, float *, int64_t, int64_t, int64_t, int,    \
-                                   cudaStream_t);
+                                   T *, T *, float *, float *, float *, int64_t, int64_t, int64_t, \
+                                   int, cudaStream_t);
 SSM_GATED_BWD_INSTANTIATE(float)
 SSM_GATED_BWD_INSTANTIATE(__nv_bfloat16)
 

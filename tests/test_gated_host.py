@@ -26,7 +26,7 @@ def fwd(ptrs=None, c=8.0, keep=None, Bs=2, L=8, ED=4, bf16=1):
 
 
 def bwd(ptrs=None, c=8.0, keep="all", Bs=2, L=8, ED=4, bf16=1):
-    p = ptrs or [P] * 12         # x gate_r gate_i lam | reset dy dh_final | dx dr di dlam dh0
+    p = ptrs or [P] * 13         # x gate_r gate_i lam | reset dy dh_final | dx dr di dlam dh0 scratch
     keep = saved() if keep == "all" else keep
     return lrs.library().gated_scan_bwd(*p[:4], c, *p[4:7], keep, *p[7:], Bs, L, ED, bf16, None)
 
@@ -62,15 +62,15 @@ def test_gated_fwd_refusals():
 
 
 def test_gated_bwd_refusals():
-    for i in (3, 5, 7, 8, 9, 10):
-        assert bwd(swapped(12, i, None)) == INVALID
+    for i in (3, 5, 7, 8, 9, 10, 12):
+        assert bwd(swapped(13, i, None)) == INVALID
     only = dict(x_q=None, r_q=None, i_q=None, x_s=None, r_s=None, i_s=None)
     for i in (0, 1, 2):          # read only without the 8-bit checkpoints
-        assert bwd(swapped(12, i, None), keep=saved(**only)) == INVALID
+        assert bwd(swapped(13, i, None), keep=saved(**only)) == INVALID
     assert bwd(keep=None) == INVALID
     assert bwd(L=0) == INVALID and bwd(Bs=65536) == UNSUPPORTED
-    for i in (3, 5, 6, 7, 8, 9, 10, 11):
-        assert bwd(swapped(12, i, ODD)) == ALIGNMENT
+    for i in (3, 5, 6, 7, 8, 9, 10, 11, 12):
+        assert bwd(swapped(13, i, ODD)) == ALIGNMENT
 
 
 def test_step_refusals():
