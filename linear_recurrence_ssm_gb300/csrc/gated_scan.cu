@@ -24,10 +24,7 @@ namespace gated {
 #ifndef KST
 #define KST 2
 #endif
-#ifndef MINB
-#define MINB 4
-#endif
-constexpr int kWarps = 4, kSteps = kBlock / kWarps, kThreads = 32 * kWarps, kStages = KST;
+constexpr int kSteps = 16, kStages = KST;
 
 __device__ unsigned int g_device_error;
 
@@ -44,7 +41,7 @@ struct FwdArgs {
     T *y;
     float *h_final;
     Kept kept;
-    int L, ED, cluster;
+    int L, ED, warps, cluster;
     int64_t rows;               // Bs * L
     int pair_stores;            // y's rows take stores of two elements
 };
@@ -54,35 +51,53 @@ struct FwdMaps {
     CUtensorMap in[3], y;
 };
 
+// Behind the ring in shared memory; the pieces of ex follow.
+template <int WARPS>
 struct Shared {
-    float4 warp[2][kWarps][32];     // A of two channels, H of two channels
-    uint64_t full[kWarps][kStages]; // a warp's copies have arrived (W = 16)
+    float4 warp[2][WARPS][32];     // A of two channels, H of two channels
+    uint64_t full[WARPS][kStages]; // a warp's copies have arrived (W = 16)
     Exchange ex;
 };
 
 // a_t and b_t of a warp's steps, and their piece (A, H).  bit j of `cut`:
 // step j drops the state before it.
+//
+// Special functions bound this as much as instructions do (a reciprocal or
+// root takes the unit twice as long as an exponential).  With bf16 tensors and
+// slow decays r = (1 + e^-gate_r)^(-1/2) gives both s_r = r^2 and m =
+// (c softplus(lam))^(1/2) r (1 - a^2)^(1/2) / (-la)^(1/2), whose last factor is
+// smooth: one root instead of a reciprocal and a root.
 template <typename T, int W, bool WIDE, bool CUT>
-__device__ __forceinline__ void coefficients(const uint8_t *rows, int64_t row0, int ED, float2 rate, uint32_t cut,
-                                             float2 (&a)[kSteps], float2 (&b)[kSteps], float2 &A, float2 &H) {
+__device__ __forceinline__ void coefficients(const uint8_t *rows, int64_t row0, int ED, float2 rate, float2 root_rate,
+                                             uint32_t cut, float2 (&a)[kSteps], float2 (&b)[kSteps], float2 &A,
+                                             float2 &H) {
     constexpr bool ACC = sizeof(T) == 4;
     A = both(1.0f);
     H = both(0.0f);
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) {
         const uint32_t o = shift_of<T, W>(row0 + j, ED);
-        const float2 x = pair_at<T, W>(rows + j * kPitch<T, W>, o);
-        const float2 sr = sigmoid2<ACC>(pair_at<T, W>(rows + (kSteps + j) * kPitch<T, W>, o));
-        const float2 si = sigmoid2<ACC>(pair_at<T, W>(rows + (2 * kSteps + j) * kPitch<T, W>, o));
-        float2 w;
-        decay2<ACC, WIDE>(mul2(rate, sr), a[j], w);
-        const float2 in = mul2(si, x), v = one_minus_square(a[j], w);
-        b[j] = mul2(mul2(v, rsqrt2<ACC>(v)), in);
+        const float2 gr = pair_at<T, W>(rows + (kSteps + j) * kPitch<T, W>, o);
+        const float2 nsi = nsigmoid2<ACC>(pair_at<T, W>(rows + (2 * kSteps + j) * kPitch<T, W>, o));
+        const float2 nin = mul2(nsi, pair_at<T, W>(rows + j * kPitch<T, W>, o));
+        float2 em;
+        if constexpr (ACC || WIDE) {
+            decay2<ACC, WIDE>(mul2(rate, nsigmoid2<ACC>(gr)), a[j], em);
+            const float2 v = square_less_one(a[j], em);
+            b[j] = mul2(mul2(v, rsqrt_of_minus<ACC>(v)), nin);
+        } else {
+            const float2 s = mul2(gr, both(-SSM_LOG2E));
+            const float2 d = add2(make_float2(ex2(s.x), ex2(s.y)), both(1.0f));
+            const float2 u = mul2(root_rate, make_float2(rsqrt_fast(d.x), rsqrt_fast(d.y)));   // -(-la)^(1/2)
+            const float2 la = mul2(u, mul2(u, both(-1.0f)));
+            decay2<ACC, WIDE>(la, a[j], em);
+            b[j] = mul2(mul2(u, slow_root(la)), nin);
+        }
         if (CUT && (cut >> j & 1)) {
             a[j] = both(0.0f);
-            b[j] = in;
+            b[j] = mul2(nin, both(-1.0f));
             A = both(-0.0f);
-            H = in;
+            H = b[j];
         } else {
             A = mul2(A, a[j]);
             H = fma2(a[j], H, b[j]);
@@ -132,16 +147,17 @@ __device__ __forceinline__ void keep_8bit(const uint8_t *rows, const Kept &kept,
     }
 }
 
-template <typename T, int W, bool RESET, bool SAVE8>
-__global__ void __launch_bounds__(kThreads, SAVE8 ? 3 : MINB)
+template <typename T, int W, int WARPS, bool RESET, bool SAVE8>
+__global__ void __launch_bounds__(32 * WARPS, (SAVE8 ? 12 : 16) / WARPS)
 gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ FwdMaps maps) {
+    constexpr int kTile = WARPS * kSteps;
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ Shared sh;
+    Shared<WARPS> &sh = *reinterpret_cast<Shared<WARPS> *>(ring + WARPS * kStages * kStageBytes<T, W>);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int C = p.cluster, rank = C > 1 ? int(cluster_rank()) : 0;
     const int e0 = int(blockIdx.x) / C * 64, e = e0 + 2 * lane;
     const int64_t b = blockIdx.y;
-    const int tiles = (p.L + kBlock - 1) / kBlock, turns = (tiles + C - 1) / C;
+    const int turns = (p.L + kTile * C - 1) / (kTile * C);
     const bool in0 = e < p.ED, in1 = e + 1 < p.ED;
 
     uint8_t *mine = ring + warp * kStages * kStageBytes<T, W>;
@@ -161,7 +177,7 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
     __syncthreads();
 
     auto fetch = [&](int turn) {
-        const int t = (turn * C + rank) * kBlock + warp * kSteps;
+        const int t = (turn * C + rank) * kTile + warp * kSteps;
         const int n = min(kSteps, p.L - t);
         uint8_t *to = mine + turn % kStages * kStageBytes<T, W>;
         if constexpr (W == 16) {
@@ -182,7 +198,7 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
         }
     };
     auto reset_of = [&](int turn) -> uint32_t {
-        const int t = (turn * C + rank) * kBlock + warp * kSteps + lane;
+        const int t = (turn * C + rank) * kTile + warp * kSteps + lane;
         return lane < kSteps && t < p.L && turn < turns ? p.reset[b * p.L + t] : 0;
     };
 #pragma unroll
@@ -191,19 +207,20 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
 
     const float2 rate = make_float2(in0 ? decay_rate(p.lam[e], p.c) : 0.0f, in1 ? decay_rate(p.lam[e + 1], p.c) : 0.0f);
     const bool wide = __any_sync(0xffffffffu, !(fmaxf(rate.x, rate.y) < kSlow));
+    const float2 root_rate = make_float2(-sqrtf(rate.x), -sqrtf(rate.y));
     float2 carry = both(0.0f);     // the state that enters the cluster's next tiles
     if (p.h0) carry = make_float2(in0 ? p.h0[b * p.ED + e] : 0.0f, in1 ? p.h0[b * p.ED + e + 1] : 0.0f);
     if (C > 1) cluster_sync();     // every block runs before another writes to its shared memory
 
     for (int turn = 0; turn < turns; ++turn) {
-        const int tile = turn * C + rank, t0 = tile * kBlock + warp * kSteps, buf = turn & 1;
+        const int t0 = (turn * C + rank) * kTile + warp * kSteps, buf = turn & 1;
         const int n = min(kSteps, p.L - t0);      // <= 0 behind the end
         const int64_t row0 = b * p.L + t0;
         uint8_t *rows = mine + turn % kStages * kStageBytes<T, W>;
         if constexpr (W == 16) {
             if (n > 0) wait_or_abort(&sh.full[warp][turn % kStages], turn / kStages & 1, &sh.ex.abort, &g_device_error);
         } else {
-            cp_async_wait<kStages - 2>();
+            cp_async_wait<(kStages > 1 ? kStages - 2 : 0)>();
             __syncwarp();
         }
         uint32_t cut = 0;
@@ -216,9 +233,9 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
         // steps behind the end leave their piece wrong; nothing after them reads it
         float2 a[kSteps], s[kSteps], A, H;
         if (wide || (RESET && cut))
-            coefficients<T, W, true, RESET>(rows, row0, p.ED, rate, cut, a, s, A, H);
+            coefficients<T, W, true, RESET>(rows, row0, p.ED, rate, root_rate, cut, a, s, A, H);
         else
-            coefficients<T, W, false, false>(rows, row0, p.ED, rate, 0, a, s, A, H);
+            coefficients<T, W, false, false>(rows, row0, p.ED, rate, root_rate, 0, a, s, A, H);
         sh.warp[buf][warp][lane] = make_float4(A.x, A.y, H.x, H.y);
         // the stage that the next rows go to was read, and its outputs stored from, a turn ago
         if (W == 16 && lane == 0) tc::bulk_wait_read0();
@@ -232,32 +249,31 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
         float2 h = carry, all = carry;
         if (C == 1) {
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
+            for (int k = 0; k < WARPS; ++k) {
                 if (k == warp) h = all;
                 all = after<RESET>(sh.warp[buf][k][lane], all);
             }
         } else {
             float4 before = make_float4(1.0f, 1.0f, 0.0f, 0.0f), sum = before;
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
+            for (int k = 0; k < WARPS; ++k) {
                 if (k == warp) before = sum;
                 sum = joined<RESET>(sum, sh.warp[buf][k][lane]);
             }
-            sh.ex.send<kWarps>(buf, C, rank, warp, lane, sum);
+            sh.ex.send<WARPS>(buf, C, rank, warp, lane, sum);
             sh.ex.wait(buf, turn >> 1 & 1, &g_device_error);
             for (int k = 0; k < C; ++k) {
                 if (k == rank) h = all;
-                all = after<RESET>(sh.ex.piece[buf][k][lane], all);
+                all = after<RESET>(sh.ex.piece(buf, C, k, lane), all);
             }
-            if (warp == 0) carry = h;      // entering the tile
             h = after<RESET>(before, h);
         }
-        if (p.kept.states && warp == 0 && tile < tiles) {
-            float *k = p.kept.states + (b * tiles + tile) * p.ED + e;
-            if (in0) k[0] = carry.x;
-            if (in1) k[1] = carry.y;
-        }
         carry = all;
+        if (p.kept.states && n > 0 && t0 % kBlock == 0) {
+            float *k = p.kept.states + (b * ((p.L + kBlock - 1) / kBlock) + t0 / kBlock) * p.ED + e;
+            if (in0) k[0] = h.x;
+            if (in1) k[1] = h.y;
+        }
 
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) {
@@ -314,19 +330,23 @@ gated_step_kernel(const T *__restrict__ x, const T *__restrict__ gr, const T *__
         put(y + at, 0.0f);
         return;
     }
-    const float2 s = sigmoid2<ACC>(make_float2(to_f32(gr[at]), to_f32(gi[at])));
-    float2 a, w;
-    decay2<ACC, true>(both(decay_rate(lam[e], c) * s.x), a, w);
-    const float2 v = one_minus_square(a, w);
-    const float h = fmaf(a.x, states[page * ED + e], v.x * rsqrt2<ACC>(v).x * s.y * to_f32(x[at]));
+    const float2 s = nsigmoid2<ACC>(make_float2(to_f32(gr[at]), to_f32(gi[at])));
+    float2 a, em;
+    decay2<ACC, true>(both(decay_rate(lam[e], c) * s.x), a, em);
+    const float2 v = square_less_one(a, em);
+    const float h = fmaf(a.x, states[page * ED + e], v.x * rsqrt_of_minus<ACC>(v).x * (s.y * to_f32(x[at])));
     states[page * ED + e] = h;
     put(y + at, h);
 }
 
 template <typename T, int W, bool RESET, bool SAVE8>
 static cudaError_t start_fwd(const FwdArgs<T> &p, const FwdMaps &maps, int64_t Bs, cudaStream_t st) {
-    auto kern = gated_fwd_kernel<T, W, RESET, SAVE8>;
-    return start_clusters(kern, kWarps * kStages * kStageBytes<T, W>, kThreads, p.ED, p.cluster, Bs, st, p, maps);
+    constexpr int kRing = kStages * kStageBytes<T, W>;
+    if (p.warps == 8)
+        return start_clusters(gated_fwd_kernel<T, W, 8, RESET, SAVE8>, 8 * kRing + int(sizeof(Shared<8>)) + exchange_bytes(p.cluster), 256, p.ED,
+                              p.cluster, Bs, st, p, maps);
+    return start_clusters(gated_fwd_kernel<T, W, 4, RESET, SAVE8>, 4 * kRing + int(sizeof(Shared<4>)) + exchange_bytes(p.cluster), 128, p.ED,
+                          p.cluster, Bs, st, p, maps);
 }
 
 template <typename T, int W>
@@ -348,13 +368,16 @@ cudaError_t launch_fwd(const T *x, const T *gr, const T *gi, const float *lam, f
                        const Kept &kept, int64_t Bs, int64_t L, int64_t ED, int num_sms,
                        cudaStream_t st) {
     auto at = [](const void *q) { return reinterpret_cast<uintptr_t>(q); };
-    FwdArgs<T> p{{x, gr, gi}, lam, c, reset, h0, y, h_final, kept, int(L), int(ED), 1, Bs * L, 0};
+    FwdArgs<T> p{{x, gr, gi}, lam, c, reset, h0, y, h_final, kept, int(L), int(ED), 4, 1, Bs * L, 0};
     p.pair_stores = ED % 2 == 0 && at(y) % (2 * sizeof(T)) == 0;
     const int W = widest_copy<T>(at(x) | at(gr) | at(gi), ED);
     const bool boxes = W == 16 && at(y) % 16 == 0 && (at(kept.x_q) | at(kept.r_q) | at(kept.i_q)) % 2 == 0;
     p.cluster = cluster_for(Bs, L, ED, int64_t(num_sms) * (sizeof(T) == 4 ? 2 : kept.x_q ? 3 : 4), kMaxCluster);
 #ifdef CL
     p.cluster = CL;
+#endif
+#ifdef WP
+    p.warps = WP;
 #endif
     if (boxes) return start_fwd<T, 16>(p, Bs, st);
     if (W >= 4) return start_fwd<T, 4>(p, Bs, st);

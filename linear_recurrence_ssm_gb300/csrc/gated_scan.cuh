@@ -10,6 +10,7 @@
 #include "ssm_common.cuh"
 #include "tc_ptx.cuh"
 
+#include <cstdio>
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -47,11 +48,15 @@ __device__ __forceinline__ void cluster_sync() {
 
 constexpr int kMaxCluster = 8;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
+inline int exchange_bytes(int cluster) { return cluster > 1 ? 2 * cluster * 32 * 16 : 0; }
 
-struct Exchange {
-    float4 piece[2][kMaxCluster][32];
+struct alignas(16) Exchange {
     uint64_t full[2];
     int abort;      // a wait ran out: this block waits no more, its results are unspecified
+    // two buffers of C pieces of 32 float4 follow
+    __device__ __forceinline__ float4 &piece(int buf, int C, int from, int lane) {
+        return reinterpret_cast<float4 *>(this + 1)[(buf * C + from) * 32 + lane];
+    }
 
     // One thread; a cluster barrier follows.
     __device__ __forceinline__ void init() {
@@ -65,7 +70,7 @@ struct Exchange {
         if (warp == 0 && lane == 0) tc::mbar_arrive_expect_tx(&full[buf], uint32_t(C) * 32 * 16);
         for (int k = warp; k < C; k += WARPS) {
             uint32_t to, bar;
-            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(&piece[buf][rank][lane])), "r"(k));
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(&piece(buf, C, rank, lane))), "r"(k));
             asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(smem_u32(&full[buf])), "r"(k));
             asm volatile(
                 "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
@@ -157,63 +162,76 @@ __device__ __forceinline__ float rcp_fast(float v) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
-// 1 / (1 + e^-v).  ACC (fp32 tensors) uses the accurate functions; bf16
-// tensors the special-function unit, whose ~2^-22 is far below the 2^-9 of
-// their rounding.
+// -1 / (1 + e^-v): the sign costs nothing here and saves one where 1 - s or
+// -la is wanted.  ACC (fp32 tensors) uses the accurate functions; bf16 tensors
+// the special-function unit, whose ~2^-22 is far below the 2^-9 of their
+// rounding.
 template <bool ACC>
-__device__ __forceinline__ float2 sigmoid2(float2 v) {
-    if (ACC) return make_float2(1.0f / (1.0f + expf(-v.x)), 1.0f / (1.0f + expf(-v.y)));
+__device__ __forceinline__ float2 nsigmoid2(float2 v) {
+    if (ACC) return make_float2(-1.0f / (1.0f + expf(-v.x)), -1.0f / (1.0f + expf(-v.y)));
     const float2 s = mul2(v, both(-SSM_LOG2E));
-    const float2 d = add2(make_float2(ex2(s.x), ex2(s.y)), both(1.0f));
+    const float2 d = fma2(make_float2(ex2(s.x), ex2(s.y)), both(-1.0f), both(-1.0f));
     return make_float2(rcp_fast(d.x), rcp_fast(d.y));
 }
 
-// Decays from t = -la >= 0: a = e^-t and w = 1 - a, w to full relative
-// accuracy, so that 1 - a^2 = w (1 + a) does not cancel for slow decays (a -> 1)
-// and a = 1 - w is rounded once.  For t < 0.4, w = t Q(t) with Q a
-// fourth-degree fit of (1 - e^-t) / t on [0, 0.4] (Chebyshev nodes; relative
-// error 5.2e-8 in exact arithmetic); from 0.4 on 1 - a loses at most two bits.
-// WIDE says that t may exceed 0.4: t <= c softplus(lam), so a warp knows from
-// its channels alone.
-// w is kept above kLeast, far below what it adds to, so that t = 0 needs no
+// Decays from la <= 0: a = e^la and em = a - 1, em to full relative accuracy,
+// so that a^2 - 1 = em (1 + a) does not cancel for slow decays (a -> 1) and
+// a = 1 + em is rounded once.  For la > -0.4, em = la Q(la) with Q a
+// fourth-degree fit of (e^la - 1) / la on [-0.4, 0] (Chebyshev nodes; relative
+// error 5.2e-8 in exact arithmetic); from there on a - 1 loses at most two
+// bits.  WIDE says that la may be below -0.4: |la| <= c softplus(lam), so a
+// warp knows from its channels alone.
+// em is kept below -kLeast, far below what it adds to, so that la = 0 needs no
 // case of its own where (1 - a^2)^(-1/2) is taken.
 constexpr float kSlow = 0.4f, kLeast = 1e-30f;
-__device__ __forceinline__ float2 slow_loss(float2 t) {
-    float2 q = fma2(t, both(0x1.cf2208p-8f), both(-0x1.51d0aap-5f));
-    q = fma2(q, t, both(0x1.5535acp-3f));
-    q = fma2(q, t, both(-0x1.ffff38p-2f));
-    q = fma2(q, t, both(1.0f));
-    return fma2(q, t, both(kLeast));
+__device__ __forceinline__ float2 slow_em1(float2 la) {
+    float2 q = fma2(la, both(0x1.cf2208p-8f), both(0x1.51d0aap-5f));
+    q = fma2(q, la, both(0x1.5535acp-3f));
+    q = fma2(q, la, both(0x1.ffff38p-2f));
+    q = fma2(q, la, both(1.0f));
+    return fma2(q, la, both(-kLeast));
 }
 template <bool ACC, bool WIDE>
-__device__ __forceinline__ void decay2(float2 t, float2 &a, float2 &w) {
-    w = slow_loss(t);
-    a = fma2(w, both(-1.0f), both(1.0f));
+__device__ __forceinline__ void decay2(float2 la, float2 &a, float2 &em) {
+    em = slow_em1(la);
+    a = add2(em, both(1.0f));
     if (WIDE) {
         float2 e;
         if (ACC) {
-            e = make_float2(expf(-t.x), expf(-t.y));
+            e = make_float2(expf(la.x), expf(la.y));
         } else {
-            const float2 s = mul2(t, both(-SSM_LOG2E));
+            const float2 s = mul2(la, both(SSM_LOG2E));
             e = make_float2(ex2(s.x), ex2(s.y));
         }
-        const float2 we = fma2(e, both(-1.0f), both(1.0f));
-        if (t.x >= kSlow) a.x = e.x, w.x = we.x;
-        if (t.y >= kSlow) a.y = e.y, w.y = we.y;
+        const float2 em_e = add2(e, both(-1.0f));
+        if (la.x <= -kSlow) a.x = e.x, em.x = em_e.x;
+        if (la.y <= -kSlow) a.y = e.y, em.y = em_e.y;
     }
 }
 
-// 1 - a^2 = w (1 + a)
-__device__ __forceinline__ float2 one_minus_square(float2 a, float2 w) { return fma2(w, a, w); }
+// a^2 - 1 = em (1 + a)
+__device__ __forceinline__ float2 square_less_one(float2 a, float2 em) { return fma2(em, a, em); }
 
-// v^(-1/2), for v > 0
+// (1 - e^(2 la))^(1/2) / (-la)^(1/2) on [-0.4, 0]: a fourth-degree fit as
+// above, relative error 6.9e-8.
+__device__ __forceinline__ float2 slow_root(float2 la) {
+    float2 q = fma2(la, both(0x1.0ca10cp-6f), both(0x1.65e174p-4f));
+    q = fma2(q, la, both(0x1.2d8d8ap-2f));
+    q = fma2(q, la, both(0x1.6a08fap-1f));
+    return fma2(q, la, both(0x1.6a09e6p+0f));
+}
+
+__device__ __forceinline__ float rsqrt_fast(float v) {
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+// (-v)^(-1/2), for v < 0
 template <bool ACC>
-__device__ __forceinline__ float2 rsqrt2(float2 v) {
-    float2 r;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(v.x));
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(v.y));
-    if (ACC) {   // one Newton step: r + r (1 - v r^2) / 2
-        const float2 d = fma2(mul2(v, r), mul2(r, both(-1.0f)), both(1.0f));
+__device__ __forceinline__ float2 rsqrt_of_minus(float2 v) {
+    float2 r = make_float2(rsqrt_fast(-v.x), rsqrt_fast(-v.y));
+    if (ACC) {   // one Newton step: r + r (1 + v r^2) / 2
+        const float2 d = fma2(mul2(v, r), r, both(1.0f));
         r = fma2(mul2(r, both(0.5f)), d, r);
     }
     return r;
@@ -421,11 +439,19 @@ inline cudaError_t start_clusters(void (*kern)(Args...), int smem, int threads, 
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim = {unsigned(cluster), 1, 1};
+    attr[1].id = cudaLaunchAttributeClusterSchedulingPolicyPreference;
+    attr[1].val.clusterSchedulingPolicyPreference = cudaClusterSchedulingPolicyLoadBalancing;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+#ifdef LB
+    cfg.numAttrs = 2;
+#endif
+#ifdef OCC
+    int nc=0; cudaOccupancyMaxActiveClusters(&nc, kern, &cfg); static int once=0; if(!once++) printf("cluster %d: max active clusters %d (blocks %d)\n", cluster, nc, nc*cluster);
+#endif
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 

@@ -83,27 +83,27 @@ __device__ __forceinline__ float2 upstream(const uint8_t *stage, int j, int64_t 
 // behind the end (j >= n).
 template <typename T, typename K, int W, bool GENERAL>
 __device__ __forceinline__ void pieces(const uint8_t *stage, int64_t row0, int ED, float2 rate, uint32_t cut, int n,
-                                       float2 (&a)[kSteps], float2 (&b)[kSteps], float2 (&sr)[kSteps],
-                                       float2 (&si)[kSteps], float2 &A, float2 &H, float2 &U) {
+                                       float2 (&a)[kSteps], float2 (&b)[kSteps], float2 (&nsr)[kSteps],
+                                       float2 (&nsi)[kSteps], float2 &A, float2 &H, float2 &U) {
     constexpr bool ACC = sizeof(T) == 4;
     A = both(1.0f);
     H = both(0.0f);
     U = both(0.0f);
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) {
-        sr[j] = sigmoid2<ACC>(input<T, K, W>(stage, 1, j, row0, ED));
-        si[j] = sigmoid2<ACC>(input<T, K, W>(stage, 2, j, row0, ED));
-        float2 w;
-        decay2<ACC, GENERAL>(mul2(rate, sr[j]), a[j], w);
-        const float2 in = mul2(si[j], input<T, K, W>(stage, 0, j, row0, ED));
-        const float2 v = one_minus_square(a[j], w);
-        b[j] = mul2(mul2(v, rsqrt2<ACC>(v)), in);
+        nsr[j] = nsigmoid2<ACC>(input<T, K, W>(stage, 1, j, row0, ED));
+        nsi[j] = nsigmoid2<ACC>(input<T, K, W>(stage, 2, j, row0, ED));
+        float2 em;
+        decay2<ACC, GENERAL>(mul2(rate, nsr[j]), a[j], em);
+        const float2 nin = mul2(nsi[j], input<T, K, W>(stage, 0, j, row0, ED));
+        const float2 v = square_less_one(a[j], em);
+        b[j] = mul2(mul2(v, rsqrt_of_minus<ACC>(v)), nin);
         if (GENERAL && j >= n) a[j] = both(1.0f), b[j] = both(0.0f);
         if (GENERAL && (cut >> j & 1)) {
             a[j] = both(0.0f);
-            b[j] = in;
+            b[j] = mul2(nin, both(-1.0f));
             A = both(-0.0f);
-            H = in;
+            H = b[j];
         } else {
             A = mul2(A, a[j]);
             H = fma2(a[j], H, b[j]);
@@ -120,7 +120,7 @@ __device__ __forceinline__ void pieces(const uint8_t *stage, int64_t row0, int E
 template <typename T, typename K, int W, bool GENERAL>
 __device__ __forceinline__ void gradients(const BwdArgs<T> &p, const uint8_t *stage, uint8_t *out, int64_t row0, float2 rate,
                                           uint32_t cut, int n, const float2 (&a)[kSteps], const float2 (&before)[kSteps],
-                                          const float2 (&sr)[kSteps], const float2 (&si)[kSteps], float2 u, int e,
+                                          const float2 (&nsr)[kSteps], const float2 (&nsi)[kSteps], float2 u, int e,
                                           bool in0, bool in1, float2 &sum) {
     constexpr bool ACC = sizeof(T) == 4;
     const int64_t at = row0 * p.ED + e;
@@ -130,21 +130,19 @@ __device__ __forceinline__ void gradients(const BwdArgs<T> &p, const uint8_t *st
         const bool dropped = GENERAL && (cut >> j & 1);
         const float2 g = add2(upstream<T, K, W>(stage, j, row0, p.ED), u);
         const float2 x = input<T, K, W>(stage, 0, j, row0, p.ED);
-        const float2 t = mul2(rate, sr[j]);
-        float2 w = slow_loss(t);
+        const float2 la = mul2(rate, nsr[j]);
+        float2 em = slow_em1(la);
         if (GENERAL) {
-            if (t.x >= kSlow) w.x = 1.0f - a[j].x;
-            if (t.y >= kSlow) w.y = 1.0f - a[j].y;
+            if (la.x <= -kSlow) em.x = a[j].x - 1.0f;
+            if (la.y <= -kSlow) em.y = a[j].y - 1.0f;
         }
-        const float2 v = one_minus_square(a[j], w), over = rsqrt2<ACC>(v);
-        const float2 in = mul2(si[j], x);
-        float2 gm = mul2(g, mul2(v, over));
-        // la (a h - (a^2 / m) s_i x) = t a ((a / m) s_i x - h)
-        float2 G = mul2(mul2(mul2(t, a[j]), g),
-                        fma2(mul2(a[j], over), in, mul2(before[j], both(-1.0f))));
-        if (dropped) gm = g, G = both(0.0f);
-        const float2 dx = mul2(gm, si[j]), q = mul2(dx, x);
-        const float2 dr = fma2(mul2(G, both(-1.0f)), sr[j], G), di = fma2(mul2(q, both(-1.0f)), si[j], q);
+        // v = -m^2 and m's reciprocal; G = la a g (h - (a / m) s_i x)
+        const float2 v = square_less_one(a[j], em), over = rsqrt_of_minus<ACC>(v);
+        float2 ngm = mul2(g, mul2(v, over));
+        float2 G = mul2(mul2(mul2(la, a[j]), g), fma2(mul2(a[j], over), mul2(nsi[j], x), before[j]));
+        if (dropped) ngm = mul2(g, both(-1.0f)), G = both(0.0f);
+        const float2 dx = mul2(ngm, nsi[j]), q = mul2(dx, x);
+        const float2 dr = fma2(G, nsr[j], G), di = fma2(q, nsi[j], q);
         if constexpr (W == 16) {
             // over the lane's own elements of the inputs
             T *o = reinterpret_cast<T *>(out + j * kPitch<T, W>) + 2 * (threadIdx.x % 32);
@@ -167,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ BwdMaps maps) {
     using S = Stage<T, K, W>;
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ Shared sh;
+    Shared &sh = *reinterpret_cast<Shared *>(ring + kWarps * S::kWarpBytes);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int C = p.cluster, rank = C > 1 ? int(cluster_rank()) : 0;
     const int e0 = int(blockIdx.x) / C * 64, e = e0 + 2 * lane;
@@ -270,12 +268,12 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
         float2 h = next_h;
         next_h = kept_of(turn - 1);
 
-        float2 a[kSteps], s[kSteps], sr[kSteps], si[kSteps], A, H, U;
+        float2 a[kSteps], s[kSteps], nsr[kSteps], nsi[kSteps], A, H, U;
         const bool general = wide || n < kSteps || (RESET && cut);
         if (general)
-            pieces<T, K, W, true>(stage, row0, p.ED, rate, cut, n, a, s, sr, si, A, H, U);
+            pieces<T, K, W, true>(stage, row0, p.ED, rate, cut, n, a, s, nsr, nsi, A, H, U);
         else
-            pieces<T, K, W, false>(stage, row0, p.ED, rate, 0, kSteps, a, s, sr, si, A, H, U);
+            pieces<T, K, W, false>(stage, row0, p.ED, rate, 0, kSteps, a, s, nsr, nsi, A, H, U);
 
         sh.warp[buf][warp][lane] = make_float4(A.x, A.y, H.x, H.y);
         sh.adjoint[buf][warp][lane] = U;
@@ -314,7 +312,7 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
             sh.ex.wait(buf, (turns - 1 - turn) >> 1 & 1, &g_device_error);
             for (int k = C - 1; k >= 0; --k) {
                 if (k == rank) u = all;
-                all = after<RESET>(sh.ex.piece[buf][k][lane], all);
+                all = after<RESET>(sh.ex.piece(buf, C, k, lane), all);
             }
             u = after<RESET>(before, u);
         }
@@ -328,9 +326,9 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
         }
         uint8_t *out = S::kOwnOut ? mine + kStages * S::kBytes : stage;
         if (general)
-            gradients<T, K, W, true>(p, stage, out, row0, rate, cut, n, a, s, sr, si, u, e, in0, in1, sum);
+            gradients<T, K, W, true>(p, stage, out, row0, rate, cut, n, a, s, nsr, nsi, u, e, in0, in1, sum);
         else
-            gradients<T, K, W, false>(p, stage, out, row0, rate, 0, kSteps, a, s, sr, si, u, e, in0, in1, sum);
+            gradients<T, K, W, false>(p, stage, out, row0, rate, 0, kSteps, a, s, nsr, nsi, u, e, in0, in1, sum);
         if (W == 16) {
             tc::fence_proxy_async_smem();
             __syncwarp();
@@ -392,8 +390,8 @@ dlam_kernel(const float *__restrict__ part, const float *__restrict__ lam, float
 
 template <typename T, typename K, int W, bool RESET>
 static cudaError_t start(const BwdArgs<T> &p, const BwdMaps &maps, int64_t Bs, cudaStream_t st) {
-    return start_clusters(gated_bwd_kernel<T, K, W, RESET>, kWarps * Stage<T, K, W>::kWarpBytes, kThreads, p.ED,
-                          p.cluster, Bs, st, p, maps);
+    return start_clusters(gated_bwd_kernel<T, K, W, RESET>, kWarps * Stage<T, K, W>::kWarpBytes + int(sizeof(Shared)) + exchange_bytes(p.cluster), kThreads,
+                          p.ED, p.cluster, Bs, st, p, maps);
 }
 
 template <typename T, typename K>
