@@ -396,7 +396,7 @@ SSM_API ssm_status_t gated_scan_fwd(const void *x, const void *gate_r, const voi
  * gate_i are not read (may be NULL).  The states inside a block of 64 steps
  * are recomputed from the one kept at its start.  At a reset step the decay
  * is the constant 0: no gradient reaches gate_r, lam or an earlier state.
- * scratch : min(8, ceil(L / 64)) * Bs * ED floats of the caller's, for dlam's
+ * scratch : min(16, ceil(L / 64)) * Bs * ED floats of the caller's, for dlam's
  *           partial sums; unspecified afterwards
  * Deterministic (dlam is summed in a fixed order).  Sizes and alignment as
  * gated_scan_fwd.

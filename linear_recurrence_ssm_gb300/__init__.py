@@ -556,7 +556,7 @@ def gated_scan_bwd(x, gate_r, gate_i, lam, dy, saved, c=8.0, reset=None, dh_fina
     g = {k: torch.empty_like(dy) for k in ("dx", "dgate_r", "dgate_i")}
     g["dlam"] = torch.empty(ED, dtype=torch.float32, device=dev)
     g["dh0"] = torch.empty((Bs, ED), dtype=torch.float32, device=dev)
-    scratch = torch.empty(min(8, -(-L // _BLOCK)) * Bs * ED, dtype=torch.float32, device=dev)
+    scratch = torch.empty(min(16, -(-L // _BLOCK)) * Bs * ED, dtype=torch.float32, device=dev)
     _call("gated_scan_bwd", _ptr(x), _ptr(gate_r), _ptr(gate_i), _ptr(lam), float(c), _ptr(reset),
           _ptr(dy), _ptr(dh_final), ctypes.byref(_saved_struct(saved)), _ptr(g["dx"]),
           _ptr(g["dgate_r"]), _ptr(g["dgate_i"]), _ptr(g["dlam"]), _ptr(g["dh0"]), _ptr(scratch),

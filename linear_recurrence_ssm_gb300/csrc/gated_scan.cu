@@ -41,14 +41,16 @@ struct FwdArgs {
     T *y;
     float *h_final;
     Kept kept;
-    int L, ED, warps, cluster;
+    int L, ED, cluster;
     int64_t rows;               // Bs * L
     int pair_stores;            // y's rows take stores of two elements
+    float one;                  // 1
 };
 
-// Boxes of 64 channels x kSteps rows of x, gate_r, gate_i and y (W = 16).
+// Boxes of 64 channels x kSteps rows of x, gate_r, gate_i, y and the three
+// checkpoints (W = 16).
 struct FwdMaps {
-    CUtensorMap in[3], y;
+    CUtensorMap in[3], y, q[3];
 };
 
 // Behind the ring in shared memory; the pieces of ex follow.
@@ -56,6 +58,7 @@ template <int WARPS>
 struct Shared {
     float4 warp[2][WARPS][32];     // A of two channels, H of two channels
     uint64_t full[WARPS][kStages]; // a warp's copies have arrived (W = 16)
+    float tops[WARPS][3 * kSteps]; // of the 8-bit groups
     Exchange ex;
 };
 
@@ -105,50 +108,80 @@ __device__ __forceinline__ void coefficients(const uint8_t *rows, int64_t row0, 
     }
 }
 
-// Keeps a warp's rows of the three tensors in 8 bits, a tensor at a time.
-// The tops of its kSteps groups end up one in each lane, so that the division
-// is done once.
+// Keeps a warp's rows of x, gate_r and gate_i in 8 bits.  The tops of its 3
+// kSteps groups go through `tops`, so that one lane divides by each, once.
+// The bytes go to global memory, or (W = 16) to boxes of 64 a row in the place
+// of rows that are not needed any more: gate_i's and gate_r's in gate_i's
+// rows, x's in gate_r's (x's own rows will hold y).
 template <typename T, int W>
-__device__ __forceinline__ void keep_8bit(const uint8_t *rows, const Kept &kept, int64_t row0, int n_rows, int e0,
-                                          int ED, int64_t all_rows, bool pairs) {
+__device__ __forceinline__ uint8_t *box_8bit(uint8_t *rows, int k) {
+    constexpr int kIn = kSteps * kPitch<T, W>;
+    return k == 0 ? rows + kIn : k == 1 ? rows + 2 * kIn + 64 * kSteps : rows + 2 * kIn;
+}
+template <typename T, int W>
+__device__ __forceinline__ void keep_8bit(uint8_t *rows, float *tops, const Kept &kept, int64_t row0, int n_rows,
+                                          int e0, int ED, int64_t all_rows, float one) {
     const int lane = threadIdx.x % 32, e = e0 + 2 * lane;
-#pragma unroll 1
-    for (int k = 0; k < 3; ++k, rows += kSteps * kPitch<T, W>) {
-        uint32_t mine = 0;
+    auto value = [&](int g) {
+        return pair_at<T, W>(rows + g * kPitch<T, W>, shift_of<T, W>(row0 + g % kSteps, ED));
+    };
 #pragma unroll
-        for (int j = 0; j < kSteps; ++j) {
-            const float2 v = pair_at<T, W>(rows + j * kPitch<T, W>, shift_of<T, W>(row0 + j, ED));
+    for (int g = 0; g < 3 * kSteps; g += 4) {
+        float4 top;
+        float *t = &top.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = value(g + i);
             // the order of the bit patterns of |v| is that of the values, NaN on top
-            const uint32_t top = __reduce_max_sync(0xffffffffu, max(__float_as_uint(v.x) & 0x7fffffffu,
-                                                                    __float_as_uint(v.y) & 0x7fffffffu));
-            if (lane == j) mine = top;
+            float m;
+            asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(fabsf(v.x)), "f"(fabsf(v.y)));
+            t[i] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
         }
-        const float top = __uint_as_float(mine), inv = inverse_of(top);
-        if (lane < n_rows && lane < kSteps) {
-            float *s = k == 0 ? kept.x_s : k == 1 ? kept.r_s : kept.i_s;
-            s[(e0 / kGroup) * all_rows + row0 + lane] = scale_of(top);
-        }
+        if (lane == 0) *reinterpret_cast<float4 *>(tops + g) = top;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int g = lane; g < 3 * kSteps; g += 32) {
+        const float top = tops[g];
+        float *s = g < kSteps ? kept.x_s : g < 2 * kSteps ? kept.r_s : kept.i_s;
+        if (g % kSteps < n_rows) s[(e0 / kGroup) * all_rows + row0 + g % kSteps] = scale_of(top);
+        tops[g] = inverse_of(top);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 2; k >= 0; --k) {
+        uint8_t *box = box_8bit<T, W>(rows, k);
         int8_t *q = (k == 0 ? kept.x_q : k == 1 ? kept.r_q : kept.i_q) + row0 * ED + e;
 #pragma unroll
-        for (int j = 0; j < kSteps; ++j) {
-            const float2 v = pair_at<T, W>(rows + j * kPitch<T, W>, shift_of<T, W>(row0 + j, ED));
-            const float by = __shfl_sync(0xffffffffu, inv, j);
-            const uint32_t n0 = quantised(v.x, by), n1 = quantised(v.y, by);
-            if (j < n_rows && e < ED) {
-                if (pairs) {
-                    *reinterpret_cast<uint16_t *>(q) = uint16_t(__byte_perm(n0, n1, 0x0040));
+        for (int j = 0; j < kSteps; j += 4) {
+            const float4 inv = *reinterpret_cast<const float4 *>(tops + k * kSteps + j);
+            float2 n[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // x inv rounded, then to an integer (ties to even) by the
+                // addition of 1.5 2^23: as a multiply-add with a 1 that the
+                // compiler does not know, so that it cannot join it to the product
+                n[i] = fma2(mul2(value(k * kSteps + j + i), both((&inv.x)[i])), both(one), both(12582912.0f));
+            }
+            __syncwarp();      // row j's bytes lie over row j / 2
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t n0 = __float_as_uint(n[i].x), n1 = __float_as_uint(n[i].y);
+                if (W == 16) {
+                    *reinterpret_cast<uint16_t *>(box + 64 * (j + i) + 2 * lane) =
+                        uint16_t(__byte_perm(n0, n1, 0x0040));
                 } else {
-                    q[0] = int8_t(n0);
-                    if (e + 1 < ED) q[1] = int8_t(n1);
+                    if (j + i < n_rows && e < ED) q[0] = int8_t(n0);
+                    if (j + i < n_rows && e + 1 < ED) q[1] = int8_t(n1);
+                    q += ED;
                 }
             }
-            q += ED;
         }
     }
 }
 
 template <typename T, int W, int WARPS, bool RESET, bool SAVE8>
-__global__ void __launch_bounds__(32 * WARPS, (SAVE8 ? 12 : 16) / WARPS)
+__global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
 gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ FwdMaps maps) {
     constexpr int kTile = WARPS * kSteps;
     extern __shared__ __align__(128) uint8_t ring[];
@@ -228,8 +261,6 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
             cut = __ballot_sync(0xffffffffu, next_cut != 0);
             next_cut = reset_of(turn + 1);
         }
-        if (SAVE8 && n > 0) keep_8bit<T, W>(rows, p.kept, row0, n, e0, p.ED, p.rows, W == 16);
-
         // steps behind the end leave their piece wrong; nothing after them reads it
         float2 a[kSteps], s[kSteps], A, H;
         if (wide || (RESET && cut))
@@ -243,11 +274,24 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
         fetch(turn + kStages - 1);
         __syncthreads();
 
+        auto keep = [&] {
+            if (!SAVE8 || n <= 0) return;
+            keep_8bit<T, W>(rows, sh.tops[warp], p.kept, row0, n, e0, p.ED, p.rows, p.one);
+            if (W == 16) {
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    for (int k = 0; k < 3; ++k) tma_store_3d(&maps.q[k], box_8bit<T, W>(rows, k), e0, t0, int(b));
+                    tc::bulk_commit();
+                }
+            }
+        };
         // The state that enters this warp's steps: the pieces before its own,
         // in its block (from 0 with their product where blocks form a cluster),
         // then in the blocks before.
         float2 h = carry, all = carry;
         if (C == 1) {
+            keep();
 #pragma unroll
             for (int k = 0; k < WARPS; ++k) {
                 if (k == warp) h = all;
@@ -260,12 +304,15 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
                 if (k == warp) before = sum;
                 sum = joined<RESET>(sum, sh.warp[buf][k][lane]);
             }
-            sh.ex.send<WARPS>(buf, C, rank, warp, lane, sum);
+            if (threadIdx.x == 0) sh.ex.expect(buf, C);
+            for (int k = warp; k < C; k += WARPS)
+                if (k != rank) sh.ex.send(buf, C, rank, k, sum);
+            keep();      // while the pieces travel
             sh.ex.wait(buf, turn >> 1 & 1, &g_device_error);
-            for (int k = 0; k < C; ++k) {
-                if (k == rank) h = all;
-                all = after<RESET>(sh.ex.piece(buf, C, k, lane), all);
-            }
+            for (int k = 0; k < rank; ++k) all = after<RESET>(sh.ex.piece(buf, C, rank, k)[lane], all);
+            h = all;
+            all = after<RESET>(sum, all);
+            for (int k = rank + 1; k < C; ++k) all = after<RESET>(sh.ex.piece(buf, C, rank, k)[lane], all);
             h = after<RESET>(before, h);
         }
         carry = all;
@@ -339,27 +386,53 @@ gated_step_kernel(const T *__restrict__ x, const T *__restrict__ gr, const T *__
     put(y + at, h);
 }
 
+template <typename T, int W, int WARPS>
+constexpr int kSmem = WARPS * kStages * kStageBytes<T, W> + int(sizeof(Shared<WARPS>));
+
+// The split goes by the sizes and the type alone (the plain kernel's measured
+// turns), so that y is the same, bit for bit, whatever is kept or reset.
+template <typename T>
+static Split split_for(int64_t Bs, int64_t L, int64_t ED, int num_sms) {
+    static std::atomic<int> slots4[kMaxCluster + 1], slots8[kMaxCluster + 1];
+    const double by = sizeof(T) == 4 ? 2.0 : 1.0;
+    const Split with4 = best_split(gated_fwd_kernel<T, 16, 4, false, false>, kSmem<T, 16, 4>, 4, 64, 1.45 * by,
+                                   0.85 * by, 0.07, Bs, L, ED, num_sms, slots4);
+    const Split with8 = best_split(gated_fwd_kernel<T, 16, 8, false, false>, kSmem<T, 16, 8>, 8, 128, 1.7 * by,
+                                   1.55 * by, 0.15, Bs, L, ED, num_sms, slots8);
+    return with8.warps != 0 && (with4.warps == 0 || with8.us < with4.us) ? with8 : with4;
+}
+
 template <typename T, int W, bool RESET, bool SAVE8>
-static cudaError_t start_fwd(const FwdArgs<T> &p, const FwdMaps &maps, int64_t Bs, cudaStream_t st) {
-    constexpr int kRing = kStages * kStageBytes<T, W>;
-    if (p.warps == 8)
-        return start_clusters(gated_fwd_kernel<T, W, 8, RESET, SAVE8>, 8 * kRing + int(sizeof(Shared<8>)) + exchange_bytes(p.cluster), 256, p.ED,
-                              p.cluster, Bs, st, p, maps);
-    return start_clusters(gated_fwd_kernel<T, W, 4, RESET, SAVE8>, 4 * kRing + int(sizeof(Shared<4>)) + exchange_bytes(p.cluster), 128, p.ED,
-                          p.cluster, Bs, st, p, maps);
+static cudaError_t start_fwd(FwdArgs<T> p, const FwdMaps &maps, int64_t Bs, int num_sms, cudaStream_t st) {
+    Split how = split_for<T>(Bs, p.L, p.ED, num_sms);
+    if (how.warps == 0) return cudaErrorInvalidConfiguration;
+#ifdef CL
+    how.cluster = CL; how.warps = WP;
+#endif
+    p.cluster = how.cluster;
+    if (how.warps == 8)
+        return start_clusters(gated_fwd_kernel<T, W, 8, RESET, SAVE8>, kSmem<T, W, 8>, how, p.ED, Bs, st, nullptr, &p,
+                              &maps);
+    return start_clusters(gated_fwd_kernel<T, W, 4, RESET, SAVE8>, kSmem<T, W, 4>, how, p.ED, Bs, st, nullptr, &p,
+                          &maps);
 }
 
 template <typename T, int W>
-static cudaError_t start_fwd(const FwdArgs<T> &p, int64_t Bs, cudaStream_t st) {
+static cudaError_t start_fwd(const FwdArgs<T> &p, int64_t Bs, int num_sms, cudaStream_t st) {
     FwdMaps maps{};
     if (W == 16) {
         for (int k = 0; k < 3; ++k)
             if (!rows_map(&maps.in[k], p.in[k], Bs, p.L, p.ED, kSteps)) return cudaErrorInvalidValue;
         if (!rows_map(&maps.y, p.y, Bs, p.L, p.ED, kSteps)) return cudaErrorInvalidValue;
+        int8_t *const q[3] = {p.kept.x_q, p.kept.r_q, p.kept.i_q};
+        for (int k = 0; k < 3 && q[0]; ++k)
+            if (!rows_map(&maps.q[k], q[k], Bs, p.L, p.ED, kSteps)) return cudaErrorInvalidValue;
     }
     if (p.kept.x_q)
-        return p.reset ? start_fwd<T, W, true, true>(p, maps, Bs, st) : start_fwd<T, W, false, true>(p, maps, Bs, st);
-    return p.reset ? start_fwd<T, W, true, false>(p, maps, Bs, st) : start_fwd<T, W, false, false>(p, maps, Bs, st);
+        return p.reset ? start_fwd<T, W, true, true>(p, maps, Bs, num_sms, st)
+                       : start_fwd<T, W, false, true>(p, maps, Bs, num_sms, st);
+    return p.reset ? start_fwd<T, W, true, false>(p, maps, Bs, num_sms, st)
+                   : start_fwd<T, W, false, false>(p, maps, Bs, num_sms, st);
 }
 
 template <typename T>
@@ -368,20 +441,14 @@ cudaError_t launch_fwd(const T *x, const T *gr, const T *gi, const float *lam, f
                        const Kept &kept, int64_t Bs, int64_t L, int64_t ED, int num_sms,
                        cudaStream_t st) {
     auto at = [](const void *q) { return reinterpret_cast<uintptr_t>(q); };
-    FwdArgs<T> p{{x, gr, gi}, lam, c, reset, h0, y, h_final, kept, int(L), int(ED), 4, 1, Bs * L, 0};
+    FwdArgs<T> p{{x, gr, gi}, lam, c, reset, h0, y, h_final, kept, int(L), int(ED), 1, Bs * L, 0, 1.0f};
     p.pair_stores = ED % 2 == 0 && at(y) % (2 * sizeof(T)) == 0;
     const int W = widest_copy<T>(at(x) | at(gr) | at(gi), ED);
-    const bool boxes = W == 16 && at(y) % 16 == 0 && (at(kept.x_q) | at(kept.r_q) | at(kept.i_q)) % 2 == 0;
-    p.cluster = cluster_for(Bs, L, ED, int64_t(num_sms) * (sizeof(T) == 4 ? 2 : kept.x_q ? 3 : 4), kMaxCluster);
-#ifdef CL
-    p.cluster = CL;
-#endif
-#ifdef WP
-    p.warps = WP;
-#endif
-    if (boxes) return start_fwd<T, 16>(p, Bs, st);
-    if (W >= 4) return start_fwd<T, 4>(p, Bs, st);
-    if constexpr (sizeof(T) == 2) return start_fwd<T, 1>(p, Bs, st);
+    const bool boxes = W == 16 && at(y) % 16 == 0 &&
+                       (!kept.x_q || widest_copy<int8_t>(at(kept.x_q) | at(kept.r_q) | at(kept.i_q), ED) == 16);
+    if (boxes) return start_fwd<T, 16>(p, Bs, num_sms, st);
+    if (W >= 4) return start_fwd<T, 4>(p, Bs, num_sms, st);
+    if constexpr (sizeof(T) == 2) return start_fwd<T, 1>(p, Bs, num_sms, st);
     return cudaErrorInvalidValue;      // fp32 is aligned to its 4 bytes
 }
 

@@ -10,10 +10,10 @@
 #include "ssm_common.cuh"
 #include "tc_ptx.cuh"
 
-#include <cstdio>
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -30,8 +30,8 @@ struct Kept {
 };
 
 // ---- exchange between the blocks of a cluster --------------------------------
-// Each block sends its tile's piece to every block of the cluster, its own
-// included, as asynchronous stores that count towards the receiver's
+// Each block sends its tile's piece to every other block of the cluster, as
+// asynchronous stores that count towards the receiver's
 // mbarrier: no block waits for its own stores to arrive anywhere, as a
 // cluster barrier would have it do (its release took 1.2 of 7 cycles an
 // instruction).  Two buffers are enough: a block sends for turn s + 2 only
@@ -46,37 +46,39 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-inline int exchange_bytes(int cluster) { return cluster > 1 ? 2 * cluster * 32 * 16 : 0; }
+inline int exchange_bytes(int cluster) { return 2 * (cluster - 1) * 32 * 16; }
 
 struct alignas(16) Exchange {
     uint64_t full[2];
     int abort;      // a wait ran out: this block waits no more, its results are unspecified
-    // two buffers of C pieces of 32 float4 follow
-    __device__ __forceinline__ float4 &piece(int buf, int C, int from, int lane) {
-        return reinterpret_cast<float4 *>(this + 1)[(buf * C + from) * 32 + lane];
-    }
 
+    // What block `from` of the others sent to block `at`; C - 1 slots a buffer follow this structure.
+    __device__ __forceinline__ float4 *piece(int buf, int C, int at, int from) {
+        return reinterpret_cast<float4 *>(this + 1) + (buf * (C - 1) + from - (from > at)) * 32;
+    }
     // One thread; a cluster barrier follows.
     __device__ __forceinline__ void init() {
         tc::mbar_init(&full[0], 1);
         tc::mbar_init(&full[1], 1);
         tc::mbar_fence_init();
     }
-    // Warp w of WARPS sends to the blocks w, w + WARPS, ...
-    template <int WARPS>
-    __device__ __forceinline__ void send(int buf, int C, int rank, int warp, int lane, float4 v) {
-        if (warp == 0 && lane == 0) tc::mbar_arrive_expect_tx(&full[buf], uint32_t(C) * 32 * 16);
-        for (int k = warp; k < C; k += WARPS) {
-            uint32_t to, bar;
-            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(&piece(buf, C, rank, lane))), "r"(k));
-            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(smem_u32(&full[buf])), "r"(k));
-            asm volatile(
-                "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
-                "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
-                : "memory");
-        }
+    // One warp: block `rank`'s piece to block k.
+    __device__ __forceinline__ void send(int buf, int C, int rank, int k, float4 v) {
+        uint32_t to, bar;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;"
+            : "=r"(to)
+            : "r"(smem_u32(piece(buf, C, k, rank) + threadIdx.x % 32)), "r"(k));
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(smem_u32(&full[buf])), "r"(k));
+        asm volatile(
+            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+            "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+            : "memory");
+    }
+    // One thread, once a turn: C - 1 pieces will come.
+    __device__ __forceinline__ void expect(int buf, int C) {
+        tc::mbar_arrive_expect_tx(&full[buf], uint32_t(C - 1) * 32 * 16);
     }
     __device__ __forceinline__ bool arrived(int buf, uint32_t parity) {
         uint32_t ok;
@@ -225,6 +227,11 @@ __device__ __forceinline__ float rsqrt_fast(float v) {
     float r;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
+}
+template <bool ACC>
+__device__ __forceinline__ float2 reciprocal_of_minus(float2 v) {
+    if (ACC) return make_float2(-1.0f / v.x, -1.0f / v.y);
+    return make_float2(rcp_fast(-v.x), rcp_fast(-v.y));
 }
 // (-v)^(-1/2), for v < 0
 template <bool ACC>
@@ -427,32 +434,81 @@ __device__ __forceinline__ void tma_store_3d(const void *tmap, const void *src, 
                  : "memory");
 }
 
-// Launches `kern` with a block of `threads` for 64 channels of a sequence and
-// one of its `cluster` shares of the time axis.
+// How a kernel's blocks share the time axis: blocks of `warps` warps, each
+// with 64 channels of a sequence and one of its C shares, C blocks a cluster.
+struct Split {
+    int warps = 0, cluster = 1;
+    double us = 0.0;
+};
+
 template <typename... Args>
-inline cudaError_t start_clusters(void (*kern)(Args...), int smem, int threads, int64_t ED, int cluster, int64_t Bs,
-                                  cudaStream_t st, const std::decay_t<Args> &...args) {
+inline cudaError_t start_clusters(void (*kern)(Args...), int smem, const Split &how, int64_t ED, int64_t Bs,
+                                  cudaStream_t st, int *resident, const std::decay_t<Args> *...args) {
+    const int C = how.cluster;
+    smem += exchange_bytes(C);
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err == cudaSuccess && C > 8)
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned((ED + 63) / 64 * cluster), unsigned(Bs));
-    cfg.blockDim = dim3(threads);
+    cfg.gridDim = dim3(unsigned((ED + 63) / 64 * C), unsigned(Bs));
+    cfg.blockDim = dim3(32 * how.warps);
     cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = st;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {unsigned(cluster), 1, 1};
-    attr[1].id = cudaLaunchAttributeClusterSchedulingPolicyPreference;
-    attr[1].val.clusterSchedulingPolicyPreference = cudaClusterSchedulingPolicyLoadBalancing;
+    attr[0].val.clusterDim = {unsigned(C), 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-#ifdef LB
-    cfg.numAttrs = 2;
-#endif
-#ifdef OCC
-    int nc=0; cudaOccupancyMaxActiveClusters(&nc, kern, &cfg); static int once=0; if(!once++) printf("cluster %d: max active clusters %d (blocks %d)\n", cluster, nc, nc*cluster);
-#endif
-    return cudaLaunchKernelEx(&cfg, kern, args...);
+    if (resident) {      // blocks that run at a time, and no launch
+        int clusters = 0;
+        err = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+        *resident = clusters * C;
+        return err;
+    }
+    return cudaLaunchKernelEx(&cfg, kern, *args...);
+}
+
+constexpr double kStartUs = 3.0;
+
+// Chooses C for one kernel (blocks of `warps` warps, `tile` steps) by the time
+// that its rounds of blocks would take: a block's start, and for each turn (one
+// tile) the turn's own latency or `share` for each block that its SM holds,
+// whichever is longer, and the exchange with each other block of the cluster
+// (measured; microseconds).  cache: blocks that run at a time by C, asked for
+// once.
+template <typename... Args>
+inline Split best_split(void (*kern)(Args...), int smem, int warps, int tile, double latency, double share,
+                        double exchange, int64_t Bs, int64_t L, int64_t ED, int num_sms, std::atomic<int> *cache) {
+    Split best;
+    const int64_t chains = (ED + 63) / 64 * Bs, tiles = (L + tile - 1) / tile;
+    for (int C = 1; C <= kMaxCluster && C <= tiles; ++C) {
+        int slots = cache[C].load(std::memory_order_relaxed);
+        if (slots == 0) {
+            Split one;
+            one.warps = warps;
+            one.cluster = C;
+            slots = -1;
+            if (start_clusters(kern, smem, one, ED, Bs, nullptr, &slots,
+                               static_cast<const std::decay_t<Args> *>(nullptr)...) != cudaSuccess) {
+                cudaGetLastError();
+                slots = -1;
+            }
+            // one cluster less than the driver counts: when all it counts
+            // were asked for (40 of 7), some waited for a second round
+            slots = slots > C ? slots - C : slots > 0 ? slots : -1;
+            cache[C].store(slots, std::memory_order_relaxed);
+        }
+        if (slots < C) continue;
+        auto turn = [&](int64_t blocks) {
+            return std::max(latency, share * double((blocks + num_sms - 1) / num_sms)) + (C - 1) * exchange;
+        };
+        const int64_t blocks = chains * C, full = blocks / slots, rest = blocks % slots;
+        const double us = double((tiles + C - 1) / C) * (double(full) * turn(slots) + (rest ? turn(rest) : 0.0)) +
+                          kStartUs * double(full + (rest ? 1 : 0));
+        if (best.warps == 0 || us < best.us) best.warps = warps, best.cluster = C, best.us = us;
+    }
+    return best;
 }
 
 template <typename T>
@@ -460,20 +516,6 @@ inline int widest_copy(uintptr_t at, int64_t ED) {
     return ED * int64_t(sizeof(T)) % 16 == 0 && at % 16 == 0 ? 16 : at % 4 == 0 ? 4 : 1;
 }
 
-// Blocks of a cluster take neighbouring tiles of a sequence at once.  `slots`
-// blocks run at a time.  Fewer chains than slots: as many blocks a chain as
-// fit at once.  More: the size whose last round of blocks is fullest, a larger
-// one (and its exchange) only where it gains 3 % for each block more.
-inline int cluster_for(int64_t Bs, int64_t L, int64_t ED, int64_t slots, int most) {
-    const int64_t chains = (ED + 63) / 64 * Bs, tiles = (L + kBlock - 1) / kBlock;
-    int best = 1;
-    double least = 0.0;
-    for (int c = 1; c <= most && c <= tiles; ++c) {
-        const double rounds = double((chains * c + slots - 1) / slots) / c * (1.0 + 0.03 * c);
-        if (c == 1 || rounds < least) best = c, least = rounds;
-    }
-    return best;
-}
 
 }  // namespace gated
 }  // namespace ssm

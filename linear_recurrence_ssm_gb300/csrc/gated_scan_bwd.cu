@@ -9,9 +9,9 @@
 // warp's piece of the time axis has two results, that of its states and that
 // of its adjoints u; one exchange a tile carries both.  The states of a tile
 // start from the kept one, so only the adjoint passes between tiles, and
-// between the blocks of a cluster.  a, s_r, s_i and the state before each step
-// stay in registers between the exchange and the gradients; x and dy are read
-// from shared memory again, 1 - a^2 is computed again.
+// between the blocks of a cluster.  a, m, s_r, s_i and the state before each
+// step stay in registers between the exchange and the gradients; x and dy are
+// read from shared memory again.
 #include "gated_scan.cuh"
 
 #include <algorithm>
@@ -61,8 +61,9 @@ struct BwdMaps {
 };
 
 struct Shared {
-    float4 warp[2][kWarps][32];     // A of two channels, state of two channels
-    float2 adjoint[2][kWarps][32];  // the adjoint of the same piece
+    float4 warp[kWarps][32];        // a piece's A of two channels, state of two channels
+    float2 adjoint[kWarps][32];     // its adjoint, then the adjoint that enters it
+    float2 state[kWarps][32];       // the state that enters it
     uint64_t full[kWarps][kStages]; // a warp's copies have arrived (W = 16)
     Exchange ex;
 };
@@ -84,7 +85,7 @@ __device__ __forceinline__ float2 upstream(const uint8_t *stage, int j, int64_t 
 template <typename T, typename K, int W, bool GENERAL>
 __device__ __forceinline__ void pieces(const uint8_t *stage, int64_t row0, int ED, float2 rate, uint32_t cut, int n,
                                        float2 (&a)[kSteps], float2 (&b)[kSteps], float2 (&nsr)[kSteps],
-                                       float2 (&nsi)[kSteps], float2 &A, float2 &H, float2 &U) {
+                                       float2 (&nsi)[kSteps], float2 (&nm)[kSteps], float2 &A, float2 &H, float2 &U) {
     constexpr bool ACC = sizeof(T) == 4;
     A = both(1.0f);
     H = both(0.0f);
@@ -97,7 +98,8 @@ __device__ __forceinline__ void pieces(const uint8_t *stage, int64_t row0, int E
         decay2<ACC, GENERAL>(mul2(rate, nsr[j]), a[j], em);
         const float2 nin = mul2(nsi[j], input<T, K, W>(stage, 0, j, row0, ED));
         const float2 v = square_less_one(a[j], em);
-        b[j] = mul2(mul2(v, rsqrt_of_minus<ACC>(v)), nin);
+        nm[j] = mul2(v, rsqrt_of_minus<ACC>(v));
+        b[j] = mul2(nm[j], nin);
         if (GENERAL && j >= n) a[j] = both(1.0f), b[j] = both(0.0f);
         if (GENERAL && (cut >> j & 1)) {
             a[j] = both(0.0f);
@@ -108,21 +110,17 @@ __device__ __forceinline__ void pieces(const uint8_t *stage, int64_t row0, int E
             A = mul2(A, a[j]);
             H = fma2(a[j], H, b[j]);
         }
-    }
-#pragma unroll
-    for (int j = kSteps - 1; j >= 0; --j) {
-        U = mul2(a[j], add2(upstream<T, K, W>(stage, j, row0, ED), U));
-        if (GENERAL && (cut >> j & 1)) U = both(0.0f);
-        if (GENERAL && j >= n) U = both(0.0f);
+        // U = sum over j of a_0 .. a_j dy_j, up to a dropped state
+        const float2 on = fma2(A, upstream<T, K, W>(stage, j, row0, ED), U);
+        if (!GENERAL || (j < n && !(cut & ((2u << j) - 1)))) U = on;
     }
 }
 
 template <typename T, typename K, int W, bool GENERAL>
 __device__ __forceinline__ void gradients(const BwdArgs<T> &p, const uint8_t *stage, uint8_t *out, int64_t row0, float2 rate,
                                           uint32_t cut, int n, const float2 (&a)[kSteps], const float2 (&before)[kSteps],
-                                          const float2 (&nsr)[kSteps], const float2 (&nsi)[kSteps], float2 u, int e,
+                                          const float2 (&nsr)[kSteps], const float2 (&nsi)[kSteps], const float2 (&nm)[kSteps], float2 u, int e,
                                           bool in0, bool in1, float2 &sum) {
-    constexpr bool ACC = sizeof(T) == 4;
     const int64_t at = row0 * p.ED + e;
 #pragma unroll
     for (int j = kSteps - 1; j >= 0; --j) {
@@ -131,14 +129,9 @@ __device__ __forceinline__ void gradients(const BwdArgs<T> &p, const uint8_t *st
         const float2 g = add2(upstream<T, K, W>(stage, j, row0, p.ED), u);
         const float2 x = input<T, K, W>(stage, 0, j, row0, p.ED);
         const float2 la = mul2(rate, nsr[j]);
-        float2 em = slow_em1(la);
-        if (GENERAL) {
-            if (la.x <= -kSlow) em.x = a[j].x - 1.0f;
-            if (la.y <= -kSlow) em.y = a[j].y - 1.0f;
-        }
-        // v = -m^2 and m's reciprocal; G = la a g (h - (a / m) s_i x)
-        const float2 v = square_less_one(a[j], em), over = rsqrt_of_minus<ACC>(v);
-        float2 ngm = mul2(g, mul2(v, over));
+        // m's reciprocal; G = la a g (h - (a / m) s_i x)
+        const float2 over = reciprocal_of_minus<sizeof(T) == 4>(nm[j]);
+        float2 ngm = mul2(g, nm[j]);
         float2 G = mul2(mul2(mul2(la, a[j]), g), fma2(mul2(a[j], over), mul2(nsi[j], x), before[j]));
         if (dropped) ngm = mul2(g, both(-1.0f)), G = both(0.0f);
         const float2 dx = mul2(ngm, nsi[j]), q = mul2(dx, x);
@@ -229,7 +222,7 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
     };
     auto kept_of = [&](int turn) {
         const int tile = turn * C + rank;
-        if (turn < 0 || tile >= tiles) return both(0.0f);
+        if (turn < 0 || tile >= tiles || warp != 1) return both(0.0f);      // warp 1 folds the states
         const float *k = p.kept.states + (b * tiles + tile) * p.ED + e;
         return make_float2(in0 ? k[0] : 0.0f, in1 ? k[1] : 0.0f);
     };
@@ -268,55 +261,65 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
         float2 h = next_h;
         next_h = kept_of(turn - 1);
 
-        float2 a[kSteps], s[kSteps], nsr[kSteps], nsi[kSteps], A, H, U;
+        float2 a[kSteps], s[kSteps], nsr[kSteps], nsi[kSteps], nm[kSteps], A, H, U;
         const bool general = wide || n < kSteps || (RESET && cut);
         if (general)
-            pieces<T, K, W, true>(stage, row0, p.ED, rate, cut, n, a, s, nsr, nsi, A, H, U);
+            pieces<T, K, W, true>(stage, row0, p.ED, rate, cut, n, a, s, nsr, nsi, nm, A, H, U);
         else
-            pieces<T, K, W, false>(stage, row0, p.ED, rate, 0, kSteps, a, s, nsr, nsi, A, H, U);
+            pieces<T, K, W, false>(stage, row0, p.ED, rate, 0, kSteps, a, s, nsr, nsi, nm, A, H, U);
 
-        sh.warp[buf][warp][lane] = make_float4(A.x, A.y, H.x, H.y);
-        sh.adjoint[buf][warp][lane] = U;
+        sh.warp[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
+        sh.adjoint[warp][lane] = U;
         // the stage that the next rows go to was read, and its outputs stored from, a turn ago
         if (W == 16 && lane == 0) tc::bulk_wait_read0();
         __syncwarp();
         fetch(turn - (kStages - 1));
         __syncthreads();
 
-        // the state that enters this warp's steps, from the one kept
+        // Two warps find what enters each warp's steps: warp 1 the states from
+        // the kept one, warp 0 the adjoints from behind (through the blocks
+        // behind where they form a cluster).  One warp each, because a fold of
+        // eight pieces in every warp was 1/7 of all instructions.
+        if (warp == 1) {
 #pragma unroll
-        for (int k = 0; k < kWarps - 1; ++k)
-            if (k < warp) h = after<RESET>(sh.warp[buf][k][lane], h);
-        // the adjoint that enters them from behind: through the warps behind
-        // (from 0 with their product where blocks form a cluster), then the blocks
-        auto behind = [&](int k) {
-            const float4 v = sh.warp[buf][k][lane];
-            const float2 w = sh.adjoint[buf][k][lane];
-            return make_float4(v.x, v.y, w.x, w.y);
-        };
-        float2 u = carry, all = carry;
-        if (C == 1) {
-#pragma unroll
-            for (int k = kWarps - 1; k >= 0; --k) {
-                if (k == warp) u = all;
-                all = after<RESET>(behind(k), all);
+            for (int k = 0; k < kWarps; ++k) {
+                sh.state[k][lane] = h;
+                if (k + 1 < kWarps) h = after<RESET>(sh.warp[k][lane], h);
             }
-        } else {
-            float4 before = make_float4(1.0f, 1.0f, 0.0f, 0.0f), sum = before;
-#pragma unroll
-            for (int k = kWarps - 1; k >= 0; --k) {
-                if (k == warp) before = sum;
-                sum = joined<RESET>(sum, behind(k));
-            }
-            sh.ex.send<kWarps>(buf, C, rank, warp, lane, sum);
-            sh.ex.wait(buf, (turns - 1 - turn) >> 1 & 1, &g_device_error);
-            for (int k = C - 1; k >= 0; --k) {
-                if (k == rank) u = all;
-                all = after<RESET>(sh.ex.piece(buf, C, k, lane), all);
-            }
-            u = after<RESET>(before, u);
         }
-        carry = all;
+        if (warp == 0) {
+            auto behind = [&](int k) {
+                const float4 v = sh.warp[k][lane];
+                const float2 w = sh.adjoint[k][lane];
+                return make_float4(v.x, v.y, w.x, w.y);
+            };
+            float2 all = carry;
+            if (C > 1) {
+                float4 sum = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int k = kWarps - 1; k >= 0; --k) sum = joined<RESET>(sum, behind(k));
+                if (lane == 0) sh.ex.expect(buf, C);
+                for (int k = 0; k < C; ++k)
+                    if (k != rank) sh.ex.send(buf, C, rank, k, sum);
+                sh.ex.wait(buf, (turns - 1 - turn) >> 1 & 1, &g_device_error);
+                for (int k = C - 1; k > rank; --k) all = after<RESET>(sh.ex.piece(buf, C, rank, k)[lane], all);
+                float2 u = all;
+                all = after<RESET>(sum, all);
+                for (int k = rank - 1; k >= 0; --k) all = after<RESET>(sh.ex.piece(buf, C, rank, k)[lane], all);
+                carry = all;
+                all = u;
+            }
+#pragma unroll
+            for (int k = kWarps - 1; k >= 0; --k) {
+                const float2 w = all;
+                all = after<RESET>(behind(k), all);
+                sh.adjoint[k][lane] = w;     // in the place of the piece that was read
+            }
+            if (C == 1) carry = all;
+        }
+        __syncthreads();
+        h = sh.state[warp][lane];
+        const float2 u = sh.adjoint[warp][lane];
 
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) {      // s: from the steps' inputs to the states before them
@@ -326,9 +329,9 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
         }
         uint8_t *out = S::kOwnOut ? mine + kStages * S::kBytes : stage;
         if (general)
-            gradients<T, K, W, true>(p, stage, out, row0, rate, cut, n, a, s, nsr, nsi, u, e, in0, in1, sum);
+            gradients<T, K, W, true>(p, stage, out, row0, rate, cut, n, a, s, nsr, nsi, nm, u, e, in0, in1, sum);
         else
-            gradients<T, K, W, false>(p, stage, out, row0, rate, 0, kSteps, a, s, nsr, nsi, u, e, in0, in1, sum);
+            gradients<T, K, W, false>(p, stage, out, row0, rate, 0, kSteps, a, s, nsr, nsi, nm, u, e, in0, in1, sum);
         if (W == 16) {
             tc::fence_proxy_async_smem();
             __syncwarp();
@@ -350,7 +353,7 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
         if (in1) p.dh0[b * p.ED + e + 1] = carry.y;
     }
     __syncthreads();
-    float2 *sums = reinterpret_cast<float2 *>(&sh.warp[0][0][0]);
+    float2 *sums = reinterpret_cast<float2 *>(&sh.warp[0][0]);
     sums[warp * 32 + lane] = sum;
     __syncthreads();
     if (warp == 0) {
@@ -389,13 +392,22 @@ dlam_kernel(const float *__restrict__ part, const float *__restrict__ lam, float
 }
 
 template <typename T, typename K, int W, bool RESET>
-static cudaError_t start(const BwdArgs<T> &p, const BwdMaps &maps, int64_t Bs, cudaStream_t st) {
-    return start_clusters(gated_bwd_kernel<T, K, W, RESET>, kWarps * Stage<T, K, W>::kWarpBytes + int(sizeof(Shared)) + exchange_bytes(p.cluster), kThreads,
-                          p.ED, p.cluster, Bs, st, p, maps);
+static cudaError_t start(BwdArgs<T> p, const BwdMaps &maps, int64_t Bs, int num_sms, int *cluster, cudaStream_t st) {
+    constexpr int kSmem = kWarps * Stage<T, K, W>::kWarpBytes + int(sizeof(Shared));
+    auto kern = gated_bwd_kernel<T, K, W, RESET>;
+    static std::atomic<int> slots[kMaxCluster + 1];
+    const double by = sizeof(T) == 4 ? 2.0 : 1.0;
+    Split how = best_split(kern, kSmem, kWarps, kBlock, 2.4 * by, 2.3 * by, 0.1, Bs, p.L, p.ED, num_sms, slots);
+    if (how.warps == 0) return cudaErrorInvalidConfiguration;
+#ifdef BCL
+    how.cluster = BCL;
+#endif
+    *cluster = p.cluster = how.cluster;
+    return start_clusters(kern, kSmem, how, p.ED, Bs, st, nullptr, &p, &maps);
 }
 
 template <typename T, typename K>
-static cudaError_t start(const BwdArgs<T> &p, int W, int64_t Bs, cudaStream_t st) {
+static cudaError_t start(const BwdArgs<T> &p, int W, int64_t Bs, int num_sms, int *cluster, cudaStream_t st) {
     BwdMaps maps{};
     if (W == 16) {
         const K *in[3];
@@ -409,11 +421,14 @@ static cudaError_t start(const BwdArgs<T> &p, int W, int64_t Bs, cudaStream_t st
                 !rows_map(&maps.out[k], out[k], Bs, p.L, p.ED, kSteps))
                 return cudaErrorInvalidValue;
         if (!rows_map(&maps.dy, p.dy, Bs, p.L, p.ED, kSteps)) return cudaErrorInvalidValue;
-        return p.reset ? start<T, K, 16, true>(p, maps, Bs, st) : start<T, K, 16, false>(p, maps, Bs, st);
+        return p.reset ? start<T, K, 16, true>(p, maps, Bs, num_sms, cluster, st)
+                       : start<T, K, 16, false>(p, maps, Bs, num_sms, cluster, st);
     }
-    if (W == 4) return p.reset ? start<T, K, 4, true>(p, maps, Bs, st) : start<T, K, 4, false>(p, maps, Bs, st);
+    if (W == 4) return p.reset ? start<T, K, 4, true>(p, maps, Bs, num_sms, cluster, st)
+                       : start<T, K, 4, false>(p, maps, Bs, num_sms, cluster, st);
     if constexpr (sizeof(K) < 4)
-        return p.reset ? start<T, K, 1, true>(p, maps, Bs, st) : start<T, K, 1, false>(p, maps, Bs, st);
+        return p.reset ? start<T, K, 1, true>(p, maps, Bs, num_sms, cluster, st)
+                       : start<T, K, 1, false>(p, maps, Bs, num_sms, cluster, st);
     return cudaErrorInvalidValue;      // fp32 is aligned to its 4 bytes
 }
 
@@ -424,20 +439,20 @@ cudaError_t launch(const T *x, const T *gr, const T *gi, const float *lam, float
                    int64_t ED, int num_sms, cudaStream_t st) {
     auto at = [](const void *q) { return reinterpret_cast<uintptr_t>(q); };
     BwdArgs<T> p{{x, gr, gi}, lam, c, reset, dy, dh_final, kept, dx, dr, di, scratch, dh0,
-                 int(L), int(ED), cluster_for(Bs, L, ED, int64_t(num_sms) * 2, kMaxCluster), Bs * L, 0};
-#ifdef BCL
-    p.cluster = BCL;
-#endif
+                 int(L), int(ED), 1, Bs * L, 0};
+    int cluster = 1;
     p.pair_stores = ED % 2 == 0 && (at(dx) | at(dr) | at(di)) % (2 * sizeof(T)) == 0;
     int W = widest_copy<T>(at(dy), ED);
     if (W == 16 && (at(dx) | at(dr) | at(di)) % 16 != 0) W = 4;
     cudaError_t err;
     if (kept.x_q)
-        err = start<T, int8_t>(p, std::min(W, widest_copy<int8_t>(at(kept.x_q) | at(kept.r_q) | at(kept.i_q), ED)), Bs, st);
+        err = start<T, int8_t>(p, std::min(W, widest_copy<int8_t>(at(kept.x_q) | at(kept.r_q) | at(kept.i_q), ED)), Bs, num_sms,
+                               &cluster, st);
     else
-        err = start<T, T>(p, std::min(W, widest_copy<T>(at(x) | at(gr) | at(gi), ED)), Bs, st);
+        err = start<T, T>(p, std::min(W, widest_copy<T>(at(x) | at(gr) | at(gi), ED)), Bs, num_sms,
+                               &cluster, st);
     if (err == cudaSuccess) {
-        dlam_kernel<<<unsigned((ED + 255) / 256), 256, 0, st>>>(p.part, lam, dlam, Bs * p.cluster, ED);
+        dlam_kernel<<<unsigned((ED + 255) / 256), 256, 0, st>>>(p.part, lam, dlam, Bs * cluster, ED);
         err = cudaGetLastError();
     }
     return err;
