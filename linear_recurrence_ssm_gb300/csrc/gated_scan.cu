@@ -125,7 +125,7 @@ __device__ __forceinline__ void keep_8bit(uint8_t *rows, float *tops, const Kept
     auto value = [&](int g) {
         return pair_at<T, W>(rows + g * kPitch<T, W>, shift_of<T, W>(row0 + g % kSteps, ED));
     };
-#pragma unroll
+#pragma unroll(W == 16 ? 3 * kSteps / 4 : 1)
     for (int g = 0; g < 3 * kSteps; g += 4) {
         float4 top;
         float *t = &top.x;
@@ -148,11 +148,11 @@ __device__ __forceinline__ void keep_8bit(uint8_t *rows, float *tops, const Kept
         tops[g] = inverse_of(top);
     }
     __syncwarp();
-#pragma unroll
+#pragma unroll(W == 16 ? 3 : 1)
     for (int k = 2; k >= 0; --k) {
         uint8_t *box = box_8bit<T, W>(rows, k);
         int8_t *q = (k == 0 ? kept.x_q : k == 1 ? kept.r_q : kept.i_q) + row0 * ED + e;
-#pragma unroll
+#pragma unroll(W == 16 ? kSteps / 4 : 1)
         for (int j = 0; j < kSteps; j += 4) {
             const float4 inv = *reinterpret_cast<const float4 *>(tops + k * kSteps + j);
             float2 n[4];
@@ -395,10 +395,11 @@ template <typename T>
 static Split split_for(int64_t Bs, int64_t L, int64_t ED, int num_sms) {
     static std::atomic<int> slots4[kMaxCluster + 1], slots8[kMaxCluster + 1];
     const double by = sizeof(T) == 4 ? 2.0 : 1.0;
-    const Split with4 = best_split(gated_fwd_kernel<T, 16, 4, false, false>, kSmem<T, 16, 4>, 4, 64, 1.45 * by,
-                                   0.85 * by, 0.07, Bs, L, ED, num_sms, slots4);
-    const Split with8 = best_split(gated_fwd_kernel<T, 16, 8, false, false>, kSmem<T, 16, 8>, 8, 128, 1.7 * by,
-                                   1.55 * by, 0.15, Bs, L, ED, num_sms, slots8);
+    const Turn of4{1.5 * by, 0.39 * by, 0.3, 0.05}, of8{2.0 * by, 0.85 * by, 0.3, 0.1};
+    const Split with4 = best_split(gated_fwd_kernel<T, 16, 4, false, false>, kSmem<T, 16, 4>, 4, 64, of4, Bs, L, ED,
+                                   num_sms, slots4);
+    const Split with8 = best_split(gated_fwd_kernel<T, 16, 8, false, false>, kSmem<T, 16, 8>, 8, 128, of8, Bs, L, ED,
+                                   num_sms, slots8);
     return with8.warps != 0 && (with4.warps == 0 || with8.us < with4.us) ? with8 : with4;
 }
 
@@ -447,9 +448,7 @@ cudaError_t launch_fwd(const T *x, const T *gr, const T *gi, const float *lam, f
     const bool boxes = W == 16 && at(y) % 16 == 0 &&
                        (!kept.x_q || widest_copy<int8_t>(at(kept.x_q) | at(kept.r_q) | at(kept.i_q), ED) == 16);
     if (boxes) return start_fwd<T, 16>(p, Bs, num_sms, st);
-    if (W >= 4) return start_fwd<T, 4>(p, Bs, num_sms, st);
-    if constexpr (sizeof(T) == 2) return start_fwd<T, 1>(p, Bs, num_sms, st);
-    return cudaErrorInvalidValue;      // fp32 is aligned to its 4 bytes
+    return W >= 8 ? start_fwd<T, 8>(p, Bs, num_sms, st) : start_fwd<T, 1>(p, Bs, num_sms, st);
 }
 
 // Read and clear this unit's device error word (host side, synchronous).

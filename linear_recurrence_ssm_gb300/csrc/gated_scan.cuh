@@ -230,8 +230,9 @@ __device__ __forceinline__ float rsqrt_fast(float v) {
 }
 template <bool ACC>
 __device__ __forceinline__ float2 reciprocal_of_minus(float2 v) {
-    if (ACC) return make_float2(-1.0f / v.x, -1.0f / v.y);
-    return make_float2(rcp_fast(-v.x), rcp_fast(-v.y));
+    float2 r = make_float2(rcp_fast(-v.x), rcp_fast(-v.y));
+    if (ACC) r = fma2(fma2(v, r, both(1.0f)), r, r);     // one Newton step
+    return r;
 }
 // (-v)^(-1/2), for v < 0
 template <bool ACC>
@@ -297,43 +298,31 @@ __device__ __forceinline__ float4 joined(float4 first, float4 second) {
 // steps, a lane two channels.  A warp copies its own rows ahead of their use,
 // so no block barrier stands between a copy and its use.
 
-// W says how: 16, tensor copies (rows are multiples of 16 bytes); 4, copies of
-// words (rows of narrow elements then start anywhere in their first word, and
-// need one word more); 1, plain loads of elements, which wait for their data.
+// W says how: 16, tensor copies (rows are multiples of 16 bytes); 8, copies of
+// 16 bytes from the granule that holds a row's first element, one more than
+// the 64 channels fill; 1, plain loads of elements, which wait for their data
+// (tensors that do not start on 16 bytes).
 template <typename T, int W>
-constexpr bool kShifted = W == 4 && sizeof(T) < 4;
-template <typename T, int W>
-constexpr int kPitch = 64 * int(sizeof(T)) + (kShifted<T, W> ? 16 : 0);
+constexpr int kPitch = 64 * int(sizeof(T)) + (W == 8 ? 16 : 0);
 
 template <typename T, int W, int STEPS>
 __device__ __forceinline__ void copy_rows(uint8_t *to, const T *from, int64_t row0, int n_rows, int e0, int ED) {
     constexpr int kSize = int(sizeof(T));
     const int lane = threadIdx.x % 32;
-    if constexpr (W == 4 && kSize == 4) {
-        const T *src = from + row0 * ED + e0 + lane;
+    if constexpr (W == 8) {
+        constexpr int kChunks = 64 * kSize / 16, kRows = 32 / kChunks;      // of one instruction
+        const uint8_t *base = reinterpret_cast<const uint8_t *>(from);
+        const bool tail = e0 + 64 + 16 / kSize > ED;
+        // The lane's granule `chunk` of a row; nothing behind the row's end, which may be the tensor's.
+        auto copy = [&](int row, int chunk) {
+            const int64_t begin = ((row0 + row) * ED + e0) * kSize, at = (begin & ~int64_t(15)) + 16 * chunk;
+            int bytes = 16;
+            if (tail) bytes = int(max(int64_t(0), min(int64_t(16), begin + int64_t(ED - e0) * kSize - at)));
+            if (row < n_rows && bytes > 0) cp_async16(to + row * kPitch<T, W> + 16 * chunk, base + at, bytes);
+        };
 #pragma unroll
-        for (int row = 0; row < STEPS; ++row)
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                if (row < n_rows && e0 + lane + 32 * k < ED)
-                    cp_async4(to + row * kPitch<T, W> + 4 * lane + 128 * k, src + int64_t(row) * ED + 32 * k, 4);
-    } else if constexpr (W == 4) {
-        constexpr int kPer = 4 / kSize, kWords = 64 / kPer + 1;
-#pragma unroll
-        for (int row = 0; row < STEPS; ++row) {
-            const int64_t begin = (row0 + row) * ED, end = begin + ED;
-            // the word that holds the row's first element; the tensor starts on a word
-            const int64_t first = (begin + e0) & ~int64_t(kPer - 1);
-#pragma unroll
-            for (int k = 0; k < (kWords + 31) / 32; ++k) {
-                const int word = lane + 32 * k;
-                const int64_t e = first + kPer * word;
-                // nothing behind the row's end, which may be the tensor's
-                if (word < kWords && row < n_rows && e < end)
-                    cp_async4(to + row * kPitch<T, W> + 4 * word, from + e,
-                              int(min(int64_t(kPer), end - e)) * kSize);
-            }
-        }
+        for (int i = 0; i < STEPS; i += kRows) copy(i + lane / kChunks, lane % kChunks);
+        if (lane < STEPS) copy(lane, kChunks);
     } else {
 #pragma unroll
         for (int row = 0; row < STEPS; ++row)
@@ -354,10 +343,10 @@ __device__ __forceinline__ void clear_ring(uint8_t *ring, int bytes) {
     __syncwarp();
 }
 
-// Elements between a row's first word and its first element.
+// Bytes between a copied row's first granule and its first element.
 template <typename T, int W>
 __device__ __forceinline__ uint32_t shift_of(int64_t row, int ED) {
-    return kShifted<T, W> ? uint32_t(row) * uint32_t(ED) & (4 / uint32_t(sizeof(T)) - 1) : 0;
+    return W == 8 ? uint32_t(row) * uint32_t(ED) * uint32_t(sizeof(T)) & 15 : 0;
 }
 
 // The lane's two channels of a copied row (int8: the integers).
@@ -365,14 +354,16 @@ template <typename T, int W>
 __device__ __forceinline__ float2 pair_at(const uint8_t *row, uint32_t shift) {
     const int lane = threadIdx.x % 32;
     if constexpr (sizeof(T) == 4) {
-        return *reinterpret_cast<const float2 *>(row + 8 * lane);
+        if (W != 8) return *reinterpret_cast<const float2 *>(row + 8 * lane);
+        const float *p = reinterpret_cast<const float *>(row + shift + 8 * lane);
+        return make_float2(p[0], p[1]);
     } else if constexpr (sizeof(T) == 2) {
-        uint32_t w = *reinterpret_cast<const uint32_t *>(row + 4 * lane);
-        if (W == 4 && shift) w = __funnelshift_r(w, *reinterpret_cast<const uint32_t *>(row + 4 * lane + 4), 16);
+        const uint32_t *p = reinterpret_cast<const uint32_t *>(row + (shift & 12) + 4 * lane);
+        const uint32_t w = W == 8 ? __funnelshift_r(p[0], p[1], 8 * (shift & 2)) : p[0];
         return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     } else {
         uint32_t w;
-        if (kShifted<T, W>)
+        if (W == 8)
             w = row[2 * lane + shift] | row[2 * lane + shift + 1] << 8;
         else
             w = *reinterpret_cast<const uint16_t *>(row + 2 * lane);
@@ -469,17 +460,20 @@ inline cudaError_t start_clusters(void (*kern)(Args...), int smem, const Split &
     return cudaLaunchKernelEx(&cfg, kern, *args...);
 }
 
+// What a turn (one tile of a block) takes, in microseconds: alone on its SM,
+// for each other block there, for an exchange with a cluster of two and for
+// each further block of the cluster.  Measured; a block's start takes kStartUs.
+struct Turn {
+    double alone, shared, exchange, hop;
+};
 constexpr double kStartUs = 3.0;
 
 // Chooses C for one kernel (blocks of `warps` warps, `tile` steps) by the time
-// that its rounds of blocks would take: a block's start, and for each turn (one
-// tile) the turn's own latency or `share` for each block that its SM holds,
-// whichever is longer, and the exchange with each other block of the cluster
-// (measured; microseconds).  cache: blocks that run at a time by C, asked for
-// once.
+// that its rounds of blocks would take.  cache: blocks that run at a time by C,
+// asked for once.
 template <typename... Args>
-inline Split best_split(void (*kern)(Args...), int smem, int warps, int tile, double latency, double share,
-                        double exchange, int64_t Bs, int64_t L, int64_t ED, int num_sms, std::atomic<int> *cache) {
+inline Split best_split(void (*kern)(Args...), int smem, int warps, int tile, const Turn &t,
+                        int64_t Bs, int64_t L, int64_t ED, int num_sms, std::atomic<int> *cache) {
     Split best;
     const int64_t chains = (ED + 63) / 64 * Bs, tiles = (L + tile - 1) / tile;
     for (int C = 1; C <= kMaxCluster && C <= tiles; ++C) {
@@ -501,7 +495,8 @@ inline Split best_split(void (*kern)(Args...), int smem, int warps, int tile, do
         }
         if (slots < C) continue;
         auto turn = [&](int64_t blocks) {
-            return std::max(latency, share * double((blocks + num_sms - 1) / num_sms)) + (C - 1) * exchange;
+            const double others = double((blocks + num_sms - 1) / num_sms - 1);
+            return t.alone + others * t.shared + (C > 1 ? t.exchange + (C - 1) * t.hop : 0.0);
         };
         const int64_t blocks = chains * C, full = blocks / slots, rest = blocks % slots;
         const double us = double((tiles + C - 1) / C) * (double(full) * turn(slots) + (rest ? turn(rest) : 0.0)) +
@@ -513,7 +508,7 @@ inline Split best_split(void (*kern)(Args...), int smem, int warps, int tile, do
 
 template <typename T>
 inline int widest_copy(uintptr_t at, int64_t ED) {
-    return ED * int64_t(sizeof(T)) % 16 == 0 && at % 16 == 0 ? 16 : at % 4 == 0 ? 4 : 1;
+    return at % 16 != 0 ? 1 : ED * int64_t(sizeof(T)) % 16 == 0 ? 16 : 8;
 }
 
 

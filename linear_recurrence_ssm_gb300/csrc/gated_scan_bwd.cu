@@ -110,9 +110,11 @@ __device__ __forceinline__ void pieces(const uint8_t *stage, int64_t row0, int E
             A = mul2(A, a[j]);
             H = fma2(a[j], H, b[j]);
         }
-        // U = sum over j of a_0 .. a_j dy_j, up to a dropped state
-        const float2 on = fma2(A, upstream<T, K, W>(stage, j, row0, ED), U);
-        if (!GENERAL || (j < n && !(cut & ((2u << j) - 1)))) U = on;
+    }
+#pragma unroll
+    for (int j = kSteps - 1; j >= 0; --j) {
+        U = mul2(a[j], add2(upstream<T, K, W>(stage, j, row0, ED), U));
+        if (GENERAL && (j >= n || (cut >> j & 1))) U = both(0.0f);
     }
 }
 
@@ -397,7 +399,8 @@ static cudaError_t start(BwdArgs<T> p, const BwdMaps &maps, int64_t Bs, int num_
     auto kern = gated_bwd_kernel<T, K, W, RESET>;
     static std::atomic<int> slots[kMaxCluster + 1];
     const double by = sizeof(T) == 4 ? 2.0 : 1.0;
-    Split how = best_split(kern, kSmem, kWarps, kBlock, 2.4 * by, 2.3 * by, 0.1, Bs, p.L, p.ED, num_sms, slots);
+    const Turn turn{1.95 * by, 0.92 * by, 0.45, 0.1};
+    Split how = best_split(kern, kSmem, kWarps, kBlock, turn, Bs, p.L, p.ED, num_sms, slots);
     if (how.warps == 0) return cudaErrorInvalidConfiguration;
 #ifdef BCL
     how.cluster = BCL;
@@ -424,12 +427,10 @@ static cudaError_t start(const BwdArgs<T> &p, int W, int64_t Bs, int num_sms, in
         return p.reset ? start<T, K, 16, true>(p, maps, Bs, num_sms, cluster, st)
                        : start<T, K, 16, false>(p, maps, Bs, num_sms, cluster, st);
     }
-    if (W == 4) return p.reset ? start<T, K, 4, true>(p, maps, Bs, num_sms, cluster, st)
-                       : start<T, K, 4, false>(p, maps, Bs, num_sms, cluster, st);
-    if constexpr (sizeof(K) < 4)
-        return p.reset ? start<T, K, 1, true>(p, maps, Bs, num_sms, cluster, st)
+    if (W == 8) return p.reset ? start<T, K, 8, true>(p, maps, Bs, num_sms, cluster, st)
+                               : start<T, K, 8, false>(p, maps, Bs, num_sms, cluster, st);
+    return p.reset ? start<T, K, 1, true>(p, maps, Bs, num_sms, cluster, st)
                        : start<T, K, 1, false>(p, maps, Bs, num_sms, cluster, st);
-    return cudaErrorInvalidValue;      // fp32 is aligned to its 4 bytes
 }
 
 template <typename T>
@@ -443,7 +444,7 @@ cudaError_t launch(const T *x, const T *gr, const T *gi, const float *lam, float
     int cluster = 1;
     p.pair_stores = ED % 2 == 0 && (at(dx) | at(dr) | at(di)) % (2 * sizeof(T)) == 0;
     int W = widest_copy<T>(at(dy), ED);
-    if (W == 16 && (at(dx) | at(dr) | at(di)) % 16 != 0) W = 4;
+    if (W == 16 && (at(dx) | at(dr) | at(di)) % 16 != 0) W = 8;
     cudaError_t err;
     if (kept.x_q)
         err = start<T, int8_t>(p, std::min(W, widest_copy<int8_t>(at(kept.x_q) | at(kept.r_q) | at(kept.i_q), ED)), Bs, num_sms,
