@@ -78,10 +78,10 @@ SIGNATURES = {
     "gated_scan_step": ([_VP] * 4 + [_F32] + [_VP] * 3 + [_I64] * 3 + [ctypes.c_int, _VP], ctypes.c_int),
     "ckpt8_save": ([_VP] * 3 + [_I64] * 2 + [ctypes.c_int, _VP], ctypes.c_int),
     "ckpt8_load": ([_VP] * 3 + [_I64] * 2 + [ctypes.c_int, _VP], ctypes.c_int),
-    "state_pages_fork": ([_VP] * 4 + [_I64] * 4 + [_VP], ctypes.c_int),
+    "state_pages_fork": ([_VP] * 5 + [_I64] * 4 + [_VP], ctypes.c_int),
     "state_pages_copy": ([_VP] * 3 + [_I64] * 4 + [_VP], ctypes.c_int),
     "state_pages_free": ([_VP] * 2 + [_I64] * 2 + [_VP], ctypes.c_int),
-    "state_pages_compact": ([_VP] * 4 + [_I64] * 4 + [_VP], ctypes.c_int),
+    "state_pages_compact": ([_VP] * 5 + [_I64] * 4 + [_VP], ctypes.c_int),
     "ssm_check_device_errors": ([_VP], ctypes.c_int),
     "ssm_selftest_wait_timeout": ([_VP], ctypes.c_int),
     "ssm_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -435,8 +435,16 @@ _BLOCK = 64      # SSM_GATED_BLOCK: steps between kept states; also columns that
 _CKPT8 = ("x_q", "r_q", "i_q", "x_s", "r_s", "i_s")
 
 
-def _call(name, *args):
-    st = getattr(library(), name)(*args)
+def _call(name, dev, *args):
+    """Call a C entry point: tensors become addresses, the stream comes last.
+    These calls are short, so the marshalling is kept lean (addresses as
+    integers, the stream's handle without a Stream object)."""
+    import torch
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(name, dev, *args)
+    args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
+    st = getattr(library(), name)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     if st != 0:
         raise SsmError(name, st)
 
@@ -476,8 +484,10 @@ def _gated_inputs(x, gate_r, gate_i, lam, ndim):
 
 
 def _check_shape(t, name, dtypes, dev, shape):
+    if t is None:
+        return
     _check(t, name, dtypes, dev)
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
@@ -511,9 +521,9 @@ def gated_scan_fwd(x, gate_r, gate_i, lam, c=8.0, reset=None, h0=None, return_fi
         keys = ("states",) if save == "states" else ("states",) + _CKPT8
         saved = {k: torch.empty(shapes[k], dtype=torch.int8 if k.endswith("_q") else torch.float32,
                                 device=dev) for k in keys}
-    _call("gated_scan_fwd", _ptr(x), _ptr(gate_r), _ptr(gate_i), _ptr(lam), float(c), _ptr(reset),
-          _ptr(h0), _ptr(y), _ptr(hf), None if saved is None else ctypes.byref(_saved_struct(saved)),
-          Bs, L, ED, int(x.dtype == torch.bfloat16), _stream(dev))
+    _call("gated_scan_fwd", dev, x, gate_r, gate_i, lam, float(c), reset,
+          h0, y, hf, None if saved is None else ctypes.byref(_saved_struct(saved)),
+          Bs, L, ED, int(x.dtype == torch.bfloat16))
     out = (y,) + ((hf,) if return_final_state else ()) + ((saved,) if save is not None else ())
     return out if len(out) > 1 else y
 
@@ -557,10 +567,10 @@ def gated_scan_bwd(x, gate_r, gate_i, lam, dy, saved, c=8.0, reset=None, dh_fina
     g["dlam"] = torch.empty(ED, dtype=torch.float32, device=dev)
     g["dh0"] = torch.empty((Bs, ED), dtype=torch.float32, device=dev)
     scratch = torch.empty(min(16, -(-L // _BLOCK)) * Bs * ED, dtype=torch.float32, device=dev)
-    _call("gated_scan_bwd", _ptr(x), _ptr(gate_r), _ptr(gate_i), _ptr(lam), float(c), _ptr(reset),
-          _ptr(dy), _ptr(dh_final), ctypes.byref(_saved_struct(saved)), _ptr(g["dx"]),
-          _ptr(g["dgate_r"]), _ptr(g["dgate_i"]), _ptr(g["dlam"]), _ptr(g["dh0"]), _ptr(scratch),
-          Bs, L, ED, int(dy.dtype == torch.bfloat16), _stream(dev))
+    _call("gated_scan_bwd", dev, x, gate_r, gate_i, lam, float(c), reset,
+          dy, dh_final, ctypes.byref(_saved_struct(saved)), g["dx"],
+          g["dgate_r"], g["dgate_i"], g["dlam"], g["dh0"], scratch,
+          Bs, L, ED, int(dy.dtype == torch.bfloat16))
     return g
 
 
@@ -584,8 +594,8 @@ def gated_scan_step(x, gate_r, gate_i, lam, states, pages=None, c=8.0, y=None):
     if y is None:
         y = torch.empty_like(x)
     _check_shape(y, "y", (x.dtype,), dev, x.shape)
-    _call("gated_scan_step", _ptr(x), _ptr(gate_r), _ptr(gate_i), _ptr(lam), float(c), _ptr(states),
-          _ptr(pages), _ptr(y), Bs, ED, states.shape[0], int(x.dtype == torch.bfloat16), _stream(dev))
+    _call("gated_scan_step", dev, x, gate_r, gate_i, lam, float(c), states,
+          pages, y, Bs, ED, states.shape[0], int(x.dtype == torch.bfloat16))
     return y
 
 
@@ -608,8 +618,7 @@ def ckpt8_save(x):
     rows = x.numel() // cols if cols else 0
     q = torch.empty(x.shape, dtype=torch.int8, device=dev)
     scale = torch.empty((-(-cols // _BLOCK), rows), dtype=torch.float32, device=dev)
-    _call("ckpt8_save", _ptr(x), _ptr(q), _ptr(scale), rows, cols, int(x.dtype == torch.bfloat16),
-          _stream(dev))
+    _call("ckpt8_save", dev, x, q, scale, rows, cols, int(x.dtype == torch.bfloat16))
     return q, scale
 
 
@@ -636,8 +645,7 @@ def ckpt8_load(q, scale, dtype=None, out=None):
                  q.shape)
     if out.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out must be bf16 or fp32")
-    _call("ckpt8_load", _ptr(q), _ptr(scale), _ptr(out), rows, cols, int(out.dtype == torch.bfloat16),
-          _stream(dev))
+    _call("ckpt8_load", dev, q, scale, out, rows, cols, int(out.dtype == torch.bfloat16))
     return out
 
 
@@ -688,8 +696,9 @@ def state_pages_fork(pool, used, src, page_dim=0):
     _used(used, dev, n_pages)
     _page_list(src, "src", dev)
     dst = torch.empty_like(src)
-    _call("state_pages_fork", _ptr(pool), _ptr(used), _ptr(src), _ptr(dst), src.shape[0], layers,
-          n_pages, size, _stream(dev))
+    scratch = torch.empty(n_pages, dtype=torch.int32, device=dev)
+    _call("state_pages_fork", dev, pool, used, src, dst, scratch, src.shape[0], layers,
+          n_pages, size)
     return dst
 
 
@@ -702,8 +711,7 @@ def state_pages_copy(pool, src, dst, page_dim=0):
     _page_list(dst, "dst", dev)
     if src.shape != dst.shape:
         raise ValueError("src and dst must have the same length")
-    _call("state_pages_copy", _ptr(pool), _ptr(src), _ptr(dst), src.shape[0], layers, n_pages, size,
-          _stream(dev))
+    _call("state_pages_copy", dev, pool, src, dst, src.shape[0], layers, n_pages, size)
 
 
 def state_pages_free(used, pages):
@@ -716,7 +724,7 @@ def state_pages_free(used, pages):
         raise ValueError("inputs must be CUDA tensors")
     _check(used, "used", (torch.uint8, torch.bool), dev, (1,))
     _page_list(pages, "pages", dev)
-    _call("state_pages_free", _ptr(used), _ptr(pages), pages.shape[0], used.shape[0], _stream(dev))
+    _call("state_pages_free", dev, used, pages, pages.shape[0], used.shape[0])
 
 
 def state_pages_compact(pool, used, pages=None, page_dim=0):
@@ -731,6 +739,7 @@ def state_pages_compact(pool, used, pages=None, page_dim=0):
     if pages is not None:
         _page_list(pages, "pages", dev)
     moved = torch.empty(n_pages, dtype=torch.int32, device=dev)
-    _call("state_pages_compact", _ptr(pool), _ptr(used), _ptr(moved), _ptr(pages),
-          0 if pages is None else pages.shape[0], layers, n_pages, size, _stream(dev))
+    scratch = torch.empty(2 * n_pages + 2, dtype=torch.int32, device=dev)
+    _call("state_pages_compact", dev, pool, used, moved, pages, scratch,
+          0 if pages is None else pages.shape[0], layers, n_pages, size)
     return moved

@@ -1,46 +1,207 @@
 // ckpt8.cu -- 8-bit activation checkpoints: a row's groups of 64 columns, each
 // with a scale of its own (gated_scan.cuh has the rounding rule).
+//
+// Both directions stream: 3 bytes an element of bf16.  Eight lanes share a
+// group (8 elements each, one 16-byte access of bf16), a warp takes 16 rows of
+// one group with four rows in flight a lane, and the eight warps of a block
+// take neighbouring groups, so that a block reads 1 KB of every row and writes
+// 64 bytes of neighbouring scales.  Where rows do not start on vectors, lanes
+// take single elements, a warp a whole group of 64.
 #include "gated_scan.cuh"
 
 namespace ssm {
 namespace ckpt8 {
 using namespace gated;
 
+constexpr int kRows = 16, kWarps = 8;
+
+struct Block {
+    int64_t row0, group;
+};
+// Blocks count through the groups, eight at a time, then the rows.
+__device__ __forceinline__ Block block_of(int64_t groups) {
+    const int64_t across = (groups + kWarps - 1) / kWarps, at = blockIdx.x;
+    return {at / across * kRows, at % across * kWarps + threadIdx.x / 32};
+}
+
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
+    const uint4 w = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(u[i] << 16), v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+}
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
+    uint4 w;
+    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    *reinterpret_cast<uint4 *>(p) = w;
+}
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+// |v| as bits: their order is that of the values, NaN on top
+__device__ __forceinline__ uint32_t size_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// cols is a multiple of 8, x starts on 16 bytes and q on 8.
 template <typename T>
-__global__ void __launch_bounds__(32)
-save_kernel(const T *__restrict__ x, int8_t *__restrict__ q, float *__restrict__ scale, int64_t rows,
-            int64_t cols) {
-    const int64_t row = blockIdx.x, e = int64_t(blockIdx.y) * kGroup + threadIdx.x;
-    float v[2];
-    unsigned top = 0;
-    for (int j = 0; j < 2; ++j) {
-        v[j] = e + 32 * j < cols ? to_f32(x[row * cols + e + 32 * j]) : 0.0f;
-        top = max(top, __float_as_uint(fabsf(v[j])));
+__global__ void __launch_bounds__(32 * kWarps)
+save_vectors_kernel(const T *__restrict__ x, int8_t *__restrict__ q, float *__restrict__ scale, int64_t rows,
+                    int64_t cols) {
+    const Block b = block_of((cols + kGroup - 1) / kGroup);
+    const int lane = threadIdx.x % 32;
+    const int64_t e = b.group * kGroup + lane % 8 * 8;
+    if (b.group * kGroup >= cols) return;
+    float v[kRows / 4][8];
+#pragma unroll
+    for (int i = 0; i < kRows / 4; ++i) {
+        const int64_t row = b.row0 + 4 * i + lane / 8;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] = 0.0f;
+        if (row < rows && e < cols) load8(x + row * cols + e, v[i]);
     }
-    const float t = __uint_as_float(__reduce_max_sync(0xffffffffu, top)), inv = inverse_of(t);
-    for (int j = 0; j < 2; ++j)
-        if (e + 32 * j < cols) q[row * cols + e + 32 * j] = int8_t(quantised(v[j], inv));
-    if (threadIdx.x == 0) scale[blockIdx.y * rows + row] = scale_of(t);
+#pragma unroll
+    for (int i = 0; i < kRows / 4; ++i) {
+        const int64_t row = b.row0 + 4 * i + lane / 8;
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = max(top, size_bits(v[i][k]));
+#pragma unroll
+        for (int d = 1; d < 8; d *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float t = __uint_as_float(top), inv = inverse_of(t);
+        uint32_t n[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) n[k] = quantised(v[i][k], inv);
+        if (row < rows) {
+            uint2 w;
+            w.x = __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410);
+            w.y = __byte_perm(__byte_perm(n[4], n[5], 0x0040), __byte_perm(n[6], n[7], 0x0040), 0x5410);
+            if (e < cols) *reinterpret_cast<uint2 *>(q + row * cols + e) = w;
+            if (lane % 8 == 0) scale[b.group * rows + row] = scale_of(t);
+        }
+    }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256)
-load_kernel(const int8_t *__restrict__ q, const float *__restrict__ scale, T *__restrict__ x, int64_t rows,
-            int64_t cols) {
-    const int64_t e = int64_t(blockIdx.y) * 256 + threadIdx.x, row = blockIdx.x;
-    if (e < cols) put(x + row * cols + e, float(q[row * cols + e]) * scale[e / kGroup * rows + row]);
+__global__ void __launch_bounds__(32 * kWarps)
+load_vectors_kernel(const int8_t *__restrict__ q, const float *__restrict__ scale, T *__restrict__ x, int64_t rows,
+                    int64_t cols) {
+    const Block b = block_of((cols + kGroup - 1) / kGroup);
+    const int lane = threadIdx.x % 32;
+    const int64_t e = b.group * kGroup + lane % 8 * 8;
+    if (e >= cols) return;
+    uint2 w[kRows / 4];
+    float s[kRows / 4];
+#pragma unroll
+    for (int i = 0; i < kRows / 4; ++i) {
+        const int64_t row = b.row0 + 4 * i + lane / 8;
+        if (row >= rows) break;
+        w[i] = *reinterpret_cast<const uint2 *>(q + row * cols + e);
+        s[i] = scale[b.group * rows + row];
+    }
+#pragma unroll
+    for (int i = 0; i < kRows / 4; ++i) {
+        const int64_t row = b.row0 + 4 * i + lane / 8;
+        if (row >= rows) break;
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v[k] = float(int8_t((k < 4 ? w[i].x : w[i].y) >> (k % 4 * 8))) * s[i];
+        store8(x + row * cols + e, v);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kWarps)
+save_elements_kernel(const T *__restrict__ x, int8_t *__restrict__ q, float *__restrict__ scale, int64_t rows,
+                     int64_t cols) {
+    const Block b = block_of((cols + kGroup - 1) / kGroup);
+    const int lane = threadIdx.x % 32;
+    const int64_t e = b.group * kGroup + lane;
+    if (b.group * kGroup >= cols) return;
+    const bool in0 = e < cols, in1 = e + 32 < cols;
+    float v[kRows][2];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int64_t at = (b.row0 + i) * cols + e;
+        const bool in = b.row0 + i < rows;
+        v[i][0] = in && in0 ? to_f32(x[at]) : 0.0f;
+        v[i][1] = in && in1 ? to_f32(x[at + 32]) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const float t = __uint_as_float(__reduce_max_sync(0xffffffffu, max(size_bits(v[i][0]), size_bits(v[i][1]))));
+        const float inv = inverse_of(t);
+        const int64_t at = (b.row0 + i) * cols + e;
+        if (b.row0 + i < rows) {
+            if (in0) q[at] = int8_t(quantised(v[i][0], inv));
+            if (in1) q[at + 32] = int8_t(quantised(v[i][1], inv));
+            if (lane == i) scale[b.group * rows + b.row0 + i] = scale_of(t);
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kWarps)
+load_elements_kernel(const int8_t *__restrict__ q, const float *__restrict__ scale, T *__restrict__ x, int64_t rows,
+                     int64_t cols) {
+    const Block b = block_of((cols + kGroup - 1) / kGroup);
+    const int64_t e = b.group * kGroup + threadIdx.x % 32;
+    if (b.group * kGroup >= cols) return;
+    const bool in0 = e < cols, in1 = e + 32 < cols;
+    int8_t n[kRows][2];
+    float s[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int64_t at = (b.row0 + i) * cols + e;
+        const bool in = b.row0 + i < rows;
+        n[i][0] = in && in0 ? q[at] : 0;
+        n[i][1] = in && in1 ? q[at + 32] : 0;
+        s[i] = in ? scale[b.group * rows + b.row0 + i] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int64_t at = (b.row0 + i) * cols + e;
+        if (b.row0 + i >= rows) break;
+        if (in0) put(x + at, float(n[i][0]) * s[i]);
+        if (in1) put(x + at + 32, float(n[i][1]) * s[i]);
+    }
+}
+
+// The grid's blocks; 0 where there are too many.
+static unsigned blocks_for(int64_t rows, int64_t cols) {
+    const int64_t groups = (cols + kGroup - 1) / kGroup;
+    const int64_t n = (rows + kRows - 1) / kRows * ((groups + kWarps - 1) / kWarps);
+    return n <= 0x7fffffff ? unsigned(n) : 0;
+}
+static bool vectors(const void *x, const void *q, int64_t cols) {
+    return cols % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0 && reinterpret_cast<uintptr_t>(q) % 8 == 0;
 }
 
 template <typename T>
 cudaError_t save(const T *x, int8_t *q, float *scale, int64_t rows, int64_t cols, cudaStream_t st) {
-    save_kernel<T><<<dim3(unsigned(rows), unsigned((cols + kGroup - 1) / kGroup)), 32, 0, st>>>(
-        x, q, scale, rows, cols);
+    const unsigned grid = blocks_for(rows, cols);
+    if (grid == 0) return cudaErrorInvalidConfiguration;
+    if (vectors(x, q, cols))
+        save_vectors_kernel<T><<<grid, 32 * kWarps, 0, st>>>(x, q, scale, rows, cols);
+    else
+        save_elements_kernel<T><<<grid, 32 * kWarps, 0, st>>>(x, q, scale, rows, cols);
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t load(const int8_t *q, const float *scale, T *x, int64_t rows, int64_t cols, cudaStream_t st) {
-    load_kernel<T><<<dim3(unsigned(rows), unsigned((cols + 255) / 256)), 256, 0, st>>>(q, scale, x, rows, cols);
+    const unsigned grid = blocks_for(rows, cols);
+    if (grid == 0) return cudaErrorInvalidConfiguration;
+    if (vectors(x, q, cols))
+        load_vectors_kernel<T><<<grid, 32 * kWarps, 0, st>>>(q, scale, x, rows, cols);
+    else
+        load_elements_kernel<T><<<grid, 32 * kWarps, 0, st>>>(q, scale, x, rows, cols);
     return cudaGetLastError();
 }
 

@@ -364,26 +364,52 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
     if (C > 1) cluster_sync();     // no block leaves while another may still write to it
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256)
+// One token.  A thread takes two channels of kStepRows rows, so that a
+// channel's decay rate is computed once for them and their loads are in
+// flight together; bound by latency (page number, then state) up to some
+// hundred rows.  PAIRS: rows start on pairs of elements.
+constexpr int kStepRows = 4, kStepThreads = 128;
+__device__ __forceinline__ float2 get2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+__device__ __forceinline__ float2 get2(const __nv_bfloat16 *p) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p));
+}
+template <typename T, bool PAIRS>
+__global__ void __launch_bounds__(kStepThreads)
 gated_step_kernel(const T *__restrict__ x, const T *__restrict__ gr, const T *__restrict__ gi,
                   const float *__restrict__ lam, float c, float *__restrict__ states,
-                  const int32_t *__restrict__ pages, T *__restrict__ y, int64_t ED, int64_t num_pages) {
+                  const int32_t *__restrict__ pages, T *__restrict__ y, int64_t Bs, int64_t ED, int64_t num_pages) {
     constexpr bool ACC = sizeof(T) == 4;
-    const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x, b = blockIdx.y;
+    const int64_t e = (int64_t(blockIdx.x) * kStepThreads + threadIdx.x) * 2, b0 = int64_t(blockIdx.y) * kStepRows;
     if (e >= ED) return;
-    const int64_t page = pages ? pages[b] : b, at = b * ED + e;
-    if (page < 0 || page >= num_pages) {
-        put(y + at, 0.0f);
-        return;
+    const bool in1 = PAIRS || e + 1 < ED;
+    auto get = [&](const auto *p) { return PAIRS ? get2(p) : make_float2(to_f32(p[0]), in1 ? to_f32(p[1]) : 0.0f); };
+    float2 v[kStepRows], r[kStepRows], i[kStepRows], h[kStepRows];
+    int64_t at[kStepRows];      // of the state; -1: an idle row, -2: no row
+#pragma unroll
+    for (int k = 0; k < kStepRows; ++k) {
+        at[k] = -2;
+        if (b0 + k >= Bs) continue;
+        const int64_t page = pages ? pages[b0 + k] : b0 + k;
+        at[k] = page >= 0 && page < num_pages ? page * ED + e : -1;
+        const int64_t in = (b0 + k) * ED + e;
+        v[k] = get(x + in), r[k] = get(gr + in), i[k] = get(gi + in);
     }
-    const float2 s = nsigmoid2<ACC>(make_float2(to_f32(gr[at]), to_f32(gi[at])));
-    float2 a, em;
-    decay2<ACC, true>(both(decay_rate(lam[e], c) * s.x), a, em);
-    const float2 v = square_less_one(a, em);
-    const float h = fmaf(a.x, states[page * ED + e], v.x * rsqrt_of_minus<ACC>(v).x * (s.y * to_f32(x[at])));
-    states[page * ED + e] = h;
-    put(y + at, h);
+#pragma unroll
+    for (int k = 0; k < kStepRows; ++k) h[k] = at[k] >= 0 ? get(states + at[k]) : both(0.0f);
+    const float2 rate = make_float2(decay_rate(lam[e], c), in1 ? decay_rate(lam[e + 1], c) : 0.0f);
+#pragma unroll
+    for (int k = 0; k < kStepRows; ++k) {
+        if (at[k] == -2) continue;
+        float2 out = both(0.0f);
+        if (at[k] >= 0) {
+            float2 a, em;
+            decay2<ACC, true>(mul2(rate, nsigmoid2<ACC>(r[k])), a, em);
+            const float2 q = square_less_one(a, em);
+            out = fma2(a, h[k], mul2(mul2(q, rsqrt_of_minus<ACC>(q)), mul2(nsigmoid2<ACC>(i[k]), v[k])));
+            put_pair(states + at[k], out, PAIRS, true, in1);
+        }
+        put_pair(y + (b0 + k) * ED + e, out, PAIRS, true, in1);
+    }
 }
 
 template <typename T, int W, int WARPS>
@@ -468,8 +494,11 @@ template <typename T>
 cudaError_t launch_step(const T *x, const T *gr, const T *gi, const float *lam, float c,
                         float *states, const int32_t *pages, T *y, int64_t Bs, int64_t ED,
                         int64_t num_pages, cudaStream_t st) {
-    const dim3 grid(unsigned((ED + 255) / 256), unsigned(Bs));
-    gated_step_kernel<T><<<grid, 256, 0, st>>>(x, gr, gi, lam, c, states, pages, y, ED, num_pages);
+    auto at = [](const void *q) { return reinterpret_cast<uintptr_t>(q); };
+    const dim3 grid(unsigned((ED + 2 * kStepThreads - 1) / (2 * kStepThreads)), unsigned((Bs + kStepRows - 1) / kStepRows));
+    const bool pairs = ED % 2 == 0 && (at(x) | at(gr) | at(gi) | at(y)) % (2 * sizeof(T)) == 0 && at(states) % 8 == 0;
+    auto kern = pairs ? gated_step_kernel<T, true> : gated_step_kernel<T, false>;
+    kern<<<grid, kStepThreads, 0, st>>>(x, gr, gi, lam, c, states, pages, y, Bs, ED, num_pages);
     return cudaGetLastError();
 }
 

@@ -3,12 +3,19 @@
 // A pool holds (layers, pages, page bytes); page p of every layer belongs to
 // one sequence (a recurrent state is overwritten at every token, so forked
 // sequences cannot share a page).  `used` has one byte for each page.
+//
+// fork and compact are two launches: one block plans (prefix sums over the
+// bytes, 16 pages a thread), then all SMs copy.  The copy is launched early
+// and waits for the plan on the device.
 #include "ssm_common.cuh"
+
+#include <algorithm>
 
 namespace ssm {
 namespace pages {
 
 constexpr int kPlan = 1024;   // threads of the planning kernels' one block
+constexpr int kEach = 16;     // pages a thread looks at in one sweep
 
 // Exclusive prefix sum of v over the block, and the total.
 __device__ __forceinline__ int block_prefix(int v, int *warp_sums, int *total) {
@@ -18,32 +25,56 @@ __device__ __forceinline__ int block_prefix(int v, int *warp_sums, int *total) {
         const int o = __shfl_up_sync(0xffffffffu, s, d);
         if (lane >= d) s += o;
     }
+    __syncthreads();          // the sums of the sweep before have been read
     if (lane == 31) warp_sums[warp] = s;
     __syncthreads();
-    int before = 0, all = 0;
-    for (int w = 0; w < kPlan / 32; ++w) {
-        if (w < warp) before += warp_sums[w];
-        all += warp_sums[w];
+    int w = warp_sums[lane];  // kPlan / 32 = 32 warps
+    for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xffffffffu, w, d);
+        if (lane >= d) w += o;
     }
-    __syncthreads();
-    *total = all;
-    return before + s - v;
+    *total = __shfl_sync(0xffffffffu, w, 31);
+    const int before = __shfl_sync(0xffffffffu, w, (warp + 31) % 32);
+    return (warp ? before : 0) + s - v;
+}
+
+// Bit i: page p0 + i is in use; bits behind the pool's end are 0.
+__device__ __forceinline__ uint32_t use_bits(const uint8_t *used, int64_t p0, int64_t num_pages) {
+    uint32_t bits = 0;
+    if (p0 + kEach <= num_pages && reinterpret_cast<uintptr_t>(used + p0) % 16 == 0) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(used + p0);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            for (int k = 0; k < 4; ++k) bits |= uint32_t((u[i] >> (8 * k) & 0xff) != 0) << (4 * i + k);
+    } else {
+        for (int i = 0; i < kEach && p0 + i < num_pages; ++i) bits |= uint32_t(used[p0 + i] != 0) << i;
+    }
+    return bits;
+}
+// The bits of the pages that the pool has.
+__device__ __forceinline__ uint32_t real_bits(int64_t p0, int64_t num_pages) {
+    const int64_t n = num_pages - p0;
+    return n >= kEach ? (1u << kEach) - 1 : n <= 0 ? 0 : (1u << n) - 1;
 }
 
 // dst[k] for every request: the k-th valid one takes the k-th lowest free
 // page.  The free pages' numbers go through `list` (pages entries).
 __global__ void __launch_bounds__(kPlan)
-fork_plan_kernel(uint8_t *__restrict__ used, const int32_t *__restrict__ src, int32_t *__restrict__ dst,
-                 int32_t *__restrict__ list, int64_t n, int64_t num_pages) {
+fork_plan_kernel(uint8_t *used, const int32_t *__restrict__ src, int32_t *__restrict__ dst, int32_t *list, int64_t n,
+                 int64_t num_pages) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ int sums[kPlan / 32];
     int64_t found = 0;
-    for (int64_t p0 = 0; p0 < num_pages; p0 += kPlan) {
-        const int64_t p = p0 + threadIdx.x;
-        const int is_free = p < num_pages && used[p] == 0;
+    for (int64_t s0 = 0; s0 < num_pages; s0 += kPlan * kEach) {
+        const int64_t p0 = s0 + int64_t(threadIdx.x) * kEach;
+        uint32_t bits = real_bits(p0, num_pages);
+        if (bits) bits &= ~use_bits(used, p0, num_pages);
         int all;
-        const int at = block_prefix(is_free, sums, &all);
-        if (is_free) list[found + at] = int32_t(p);
+        int64_t at = found + block_prefix(__popc(bits), sums, &all);
+        for (; bits; bits &= bits - 1) list[at++] = int32_t(p0 + __ffs(bits) - 1);
         found += all;
+        if (found >= n) break;      // no request needs a later page
     }
     __syncthreads();
     int64_t taken = 0;
@@ -52,8 +83,8 @@ fork_plan_kernel(uint8_t *__restrict__ used, const int32_t *__restrict__ src, in
         const int s = k < n ? src[k] : -2;
         const int valid = s == -1 || (s >= 0 && s < num_pages && used[s] != 0);
         int all;
-        const int at = block_prefix(valid, sums, &all);
-        if (k < n) dst[k] = valid && taken + at < found ? list[taken + at] : -1;
+        const int64_t at = taken + block_prefix(valid, sums, &all);
+        if (k < n) dst[k] = valid && at < found ? list[at] : -1;
         taken += all;
     }
     __syncthreads();
@@ -61,38 +92,40 @@ fork_plan_kernel(uint8_t *__restrict__ used, const int32_t *__restrict__ src, in
 }
 
 // moved[p]: where page p's content is afterwards, -1 for a free page; the
-// moves as (from, to) pairs and their number in list.
+// moves' number, sources and targets in list[0], list + 2 and list + 2 + pages.
 __global__ void __launch_bounds__(kPlan)
-compact_plan_kernel(uint8_t *__restrict__ used, int32_t *__restrict__ moved, int32_t *__restrict__ list,
-                    int32_t *__restrict__ pages, int64_t n, int64_t num_pages) {
+compact_plan_kernel(uint8_t *used, int32_t *moved, int32_t *list, int32_t *pages, int64_t n, int64_t num_pages) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ int sums[kPlan / 32];
-    int64_t live = 0;
-    for (int64_t p0 = 0; p0 < num_pages; p0 += kPlan) {
-        const int64_t p = p0 + threadIdx.x;
-        int all;
-        block_prefix(p < num_pages && used[p] != 0, sums, &all);
-        live += all;
-    }
+    const int64_t per_sweep = int64_t(kPlan) * kEach;
+    int mine = 0, all;
+    for (int64_t p0 = int64_t(threadIdx.x) * kEach; p0 < num_pages; p0 += per_sweep)
+        mine += __popc(use_bits(used, p0, num_pages));
+    block_prefix(mine, sums, &all);
+    const int64_t live = all;
     int32_t *from = list + 2, *to = list + 2 + num_pages;
     int64_t holes = 0, movers = 0;
-    for (int64_t p0 = 0; p0 < num_pages; p0 += kPlan) {
-        const int64_t p = p0 + threadIdx.x;
-        const bool in_use = p < num_pages && used[p] != 0;
-        const int hole = p < live && !in_use, mover = p >= live && in_use;
-        int all;
-        int at = block_prefix(hole, sums, &all);
-        if (hole) to[holes + at] = int32_t(p);
-        holes += all;
-        at = block_prefix(mover, sums, &all);
-        if (mover) from[movers + at] = int32_t(p);
-        movers += all;
-        if (p < num_pages) moved[p] = in_use ? int32_t(p) : -1;
+    for (int64_t s0 = 0; s0 < num_pages; s0 += per_sweep) {
+        const int64_t p0 = s0 + int64_t(threadIdx.x) * kEach;
+        const uint32_t real = real_bits(p0, num_pages), low = real_bits(p0, live);
+        const uint32_t in_use = real ? use_bits(used, p0, num_pages) : 0;
+        uint32_t hole = low & ~in_use, mover = in_use & ~low;
+        // both counts of a sweep fit 16 bits
+        const int at = block_prefix(__popc(hole) << 16 | __popc(mover), sums, &all);
+        int64_t h = holes + (at >> 16), m = movers + (at & 0xffff);
+        for (; hole; hole &= hole - 1) to[h++] = int32_t(p0 + __ffs(hole) - 1);
+        for (uint32_t left = mover; left; left &= left - 1) from[m++] = int32_t(p0 + __ffs(left) - 1);
+        for (int i = 0; i < kEach && p0 + i < num_pages; ++i) {
+            moved[p0 + i] = in_use >> i & 1 ? int32_t(p0 + i) : -1;
+            used[p0 + i] = low >> i & 1;
+        }
+        holes += all >> 16;
+        movers += all & 0xffff;
     }
     __syncthreads();
     if (threadIdx.x == 0) list[0] = int32_t(movers);
     for (int64_t k = threadIdx.x; k < movers; k += kPlan) moved[from[k]] = to[k];
     __syncthreads();
-    for (int64_t p = threadIdx.x; p < num_pages; p += kPlan) used[p] = p < live;
     for (int64_t k = threadIdx.x; k < n; k += kPlan) {
         const int p = pages[k];
         if (p >= 0) pages[k] = p < num_pages ? moved[p] : -1;
@@ -100,20 +133,39 @@ compact_plan_kernel(uint8_t *__restrict__ used, int32_t *__restrict__ moved, int
 }
 
 // Copies page from[k] to page to[k] of every layer; from -1 writes zeros.
-// `count` (device) or `n` says how many.
+// `count` (device) or `n` says how many.  A warp copies 128 words at a time,
+// four loads in flight a lane; the warps walk along a page, then the list,
+// then the layers.
 template <typename V>
 __global__ void __launch_bounds__(256)
-copy_kernel(V *__restrict__ pool, const int32_t *__restrict__ from, const int32_t *__restrict__ to,
-            const int32_t *__restrict__ count, int64_t n, int64_t layers, int64_t num_pages, int64_t words) {
+copy_kernel(V *pool, const int32_t *from, const int32_t *to, const int32_t *count, int64_t n, int64_t layers,
+            int64_t num_pages, int64_t words) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (count) n = *count;
-    const int64_t total = n * layers * words;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
-        const int64_t w = i % words, k = i / words % n, layer = i / words / n;
+    const int lane = threadIdx.x % 32;
+    const int64_t parts = (words + 127) / 128, total = parts * n * layers;
+    for (int64_t u = int64_t(blockIdx.x) * 8 + threadIdx.x / 32; u < total; u += int64_t(gridDim.x) * 8) {
+        int64_t rest, w0, k, layer;
+        if (total <= 0xffffffffll) {      // 32-bit divisions
+            const uint32_t r = uint32_t(u) / uint32_t(parts);
+            rest = r, w0 = int64_t(uint32_t(u) - r * uint32_t(parts)) * 128 + lane;
+            layer = r / uint32_t(n), k = rest - layer * n;
+        } else {
+            rest = u / parts, w0 = u % parts * 128 + lane, layer = rest / n, k = rest % n;
+        }
         const int64_t f = from[k], t = to[k];
         if (t < 0 || t >= num_pages || f < -1 || f >= num_pages) continue;
-        V v{};
-        if (f >= 0) v = pool[(layer * num_pages + f) * words + w];
-        pool[(layer * num_pages + t) * words + w] = v;
+        const V *src = pool + (layer * num_pages + f) * words;
+        V *dst = pool + (layer * num_pages + t) * words;
+        V v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = V{};
+            if (f >= 0 && w0 + 32 * i < words) v[i] = src[w0 + 32 * i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (w0 + 32 * i < words) dst[w0 + 32 * i] = v[i];
     }
 }
 
@@ -125,34 +177,46 @@ free_kernel(uint8_t *__restrict__ used, const int32_t *__restrict__ pages, int64
     if (p >= 0 && p < num_pages) used[p] = 0;
 }
 
-static cudaError_t run_copy(void *pool, const int32_t *from, const int32_t *to, const int32_t *count,
-                            int64_t n, int64_t layers, int64_t num_pages, int64_t bytes, int num_sms,
-                            cudaStream_t st) {
-    const unsigned grid = unsigned(num_sms * 8);
-    if (bytes % 16 == 0 && reinterpret_cast<uintptr_t>(pool) % 16 == 0)
-        copy_kernel<uint4><<<grid, 256, 0, st>>>(static_cast<uint4 *>(pool), from, to, count, n, layers,
-                                                 num_pages, bytes / 16);
-    else
-        copy_kernel<uint8_t><<<grid, 256, 0, st>>>(static_cast<uint8_t *>(pool), from, to, count, n, layers,
-                                                   num_pages, bytes);
-    return cudaGetLastError();
+// `most`: how many pages there can be to copy.  `after_plan`: the kernel
+// before it on the stream is a plan, whose end the copy waits for by itself.
+template <typename V>
+static cudaError_t start_copy(void *pool, const int32_t *from, const int32_t *to, const int32_t *count, int64_t n,
+                              int64_t most, int64_t layers, int64_t num_pages, int64_t bytes, int num_sms,
+                              bool after_plan, cudaStream_t st) {
+    const int64_t words = bytes / int64_t(sizeof(V));
+    const int64_t units = (words + 127) / 128 * most * layers;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(std::min<int64_t>((units + 7) / 8, int64_t(num_sms) * 8)));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = after_plan ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, copy_kernel<V>, static_cast<V *>(pool), from, to, count, n, layers, num_pages,
+                              words);
+}
+
+static cudaError_t run_copy(void *pool, const int32_t *from, const int32_t *to, const int32_t *count, int64_t n,
+                            int64_t most, int64_t layers, int64_t num_pages, int64_t bytes, int num_sms,
+                            bool after_plan, cudaStream_t st) {
+    const uintptr_t all = reinterpret_cast<uintptr_t>(pool) | uintptr_t(bytes);
+    auto start = all % 16 == 0 ? start_copy<uint4> : all % 4 == 0 ? start_copy<uint32_t> : start_copy<uint8_t>;
+    return start(pool, from, to, count, n, most, layers, num_pages, bytes, num_sms, after_plan, st);
 }
 
 cudaError_t copy(void *pool, const int32_t *src, const int32_t *dst, int64_t n, int64_t layers,
                  int64_t num_pages, int64_t bytes, int num_sms, cudaStream_t st) {
-    return run_copy(pool, src, dst, nullptr, n, layers, num_pages, bytes, num_sms, st);
+    return run_copy(pool, src, dst, nullptr, n, n, layers, num_pages, bytes, num_sms, false, st);
 }
 
-cudaError_t fork(void *pool, uint8_t *used, const int32_t *src, int32_t *dst, int64_t n, int64_t layers,
-                 int64_t num_pages, int64_t bytes, int num_sms, cudaStream_t st) {
-    int32_t *list = nullptr;
-    cudaError_t err = cudaMallocAsync(&list, size_t(num_pages) * 4, st);
+cudaError_t fork(void *pool, uint8_t *used, const int32_t *src, int32_t *dst, int32_t *scratch, int64_t n,
+                 int64_t layers, int64_t num_pages, int64_t bytes, int num_sms, cudaStream_t st) {
+    fork_plan_kernel<<<1, kPlan, 0, st>>>(used, src, dst, scratch, n, num_pages);
+    const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
-    fork_plan_kernel<<<1, kPlan, 0, st>>>(used, src, dst, list, n, num_pages);
-    err = cudaGetLastError();
-    if (err == cudaSuccess) err = run_copy(pool, src, dst, nullptr, n, layers, num_pages, bytes, num_sms, st);
-    const cudaError_t e2 = cudaFreeAsync(list, st);
-    return err != cudaSuccess ? err : e2;
+    return run_copy(pool, src, dst, nullptr, n, n, layers, num_pages, bytes, num_sms, true, st);
 }
 
 cudaError_t free_pages(uint8_t *used, const int32_t *pages, int64_t n, int64_t num_pages, cudaStream_t st) {
@@ -160,17 +224,13 @@ cudaError_t free_pages(uint8_t *used, const int32_t *pages, int64_t n, int64_t n
     return cudaGetLastError();
 }
 
-cudaError_t compact(void *pool, uint8_t *used, int32_t *moved, int32_t *pages, int64_t n, int64_t layers,
-                    int64_t num_pages, int64_t bytes, int num_sms, cudaStream_t st) {
-    int32_t *list = nullptr;
-    cudaError_t err = cudaMallocAsync(&list, size_t(num_pages) * 8 + 8, st);
+cudaError_t compact(void *pool, uint8_t *used, int32_t *moved, int32_t *pages, int32_t *scratch, int64_t n,
+                    int64_t layers, int64_t num_pages, int64_t bytes, int num_sms, cudaStream_t st) {
+    compact_plan_kernel<<<1, kPlan, 0, st>>>(used, moved, scratch, pages, n, num_pages);
+    const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
-    compact_plan_kernel<<<1, kPlan, 0, st>>>(used, moved, list, pages, n, num_pages);
-    err = cudaGetLastError();
-    if (err == cudaSuccess)
-        err = run_copy(pool, list + 2, list + 2 + num_pages, list, 0, layers, num_pages, bytes, num_sms, st);
-    const cudaError_t e2 = cudaFreeAsync(list, st);
-    return err != cudaSuccess ? err : e2;
+    return run_copy(pool, scratch + 2, scratch + 2 + num_pages, scratch, 0, num_pages / 2 + 1, layers, num_pages, bytes,
+                    num_sms, true, st);
 }
 
 }  // namespace pages
