@@ -38,6 +38,7 @@ Options (of the selective scans; any of them selects the ``*_ex`` C entry point)
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 from . import _build
@@ -436,17 +437,26 @@ _CKPT8 = ("x_q", "r_q", "i_q", "x_s", "r_s", "i_s")
 
 
 def _call(name, dev, *args):
-    """Call a C entry point: tensors become addresses, the stream comes last.
-    These calls are short, so the marshalling is kept lean (addresses as
-    integers, the stream's handle without a Stream object)."""
+    """Call a C entry point on the current stream of ``dev``.  These calls are
+    short, so the marshalling is kept lean: addresses as integers, the
+    stream's handle without a Stream object."""
     import torch
-    if dev.index != torch.cuda.current_device():
+    index = dev.index
+    if index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _call(name, dev, *args)
-    args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
-    st = getattr(library(), name)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    st = getattr(_lib or library(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
     if st != 0:
         raise SsmError(name, st)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _fits(t, dtype, shape, dev):
+    """The usual case of ``_check_shape``, without its messages."""
+    return t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous()
 
 
 def _saved_shapes(Bs, L, ED):
@@ -466,20 +476,19 @@ def _gated_inputs(x, gate_r, gate_i, lam, ndim):
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
     dev = x.device
-    if dev.type != "cuda":
+    if not x.is_cuda:
         raise ValueError("inputs must be CUDA tensors")
     _check(x, "x", (torch.bfloat16, torch.float32), dev, (ndim,))
+    dtype, shape = x.dtype, x.shape
     for t, n in ((gate_r, "gate_r"), (gate_i, "gate_i")):
-        if t is None:
+        if not isinstance(t, torch.Tensor):
             raise TypeError("%s must be a torch.Tensor" % n)
-        _check(t, n, (x.dtype,), dev, (ndim,))
-        if t.shape != x.shape:
-            raise ValueError("%s must have the shape of x" % n)
-    if lam is None:
+        if not _fits(t, dtype, shape, dev):
+            _check_shape(t, n, (dtype,), dev, shape)
+    if not isinstance(lam, torch.Tensor):
         raise TypeError("lam must be a torch.Tensor")
-    _check(lam, "lam", (torch.float32,), dev, (1,))
-    if lam.shape[0] != x.shape[-1]:
-        raise ValueError("lam must have %d entries" % x.shape[-1])
+    if not _fits(lam, torch.float32, shape[-1:], dev):
+        _check_shape(lam, "lam", (torch.float32,), dev, shape[-1:])
     return dev
 
 
@@ -513,16 +522,18 @@ def gated_scan_fwd(x, gate_r, gate_i, lam, c=8.0, reset=None, h0=None, return_fi
         raise ValueError("save must be None, 'states' or '8bit'")
     if y is None:
         y = torch.empty_like(x)
-    _check_shape(y, "y", (x.dtype,), dev, x.shape)
+    else:
+        _check_shape(y, "y", (x.dtype,), dev, x.shape)
     hf = torch.empty((Bs, ED), dtype=torch.float32, device=dev) if return_final_state else None
     saved = None
     if save is not None:
         shapes = _saved_shapes(Bs, L, ED)
         keys = ("states",) if save == "states" else ("states",) + _CKPT8
-        saved = {k: torch.empty(shapes[k], dtype=torch.int8 if k.endswith("_q") else torch.float32,
+        saved = {k: torch.empty(shapes[k], dtype=torch.int8 if k[1:] == "_q" else torch.float32,
                                 device=dev) for k in keys}
-    _call("gated_scan_fwd", dev, x, gate_r, gate_i, lam, float(c), reset,
-          h0, y, hf, None if saved is None else ctypes.byref(_saved_struct(saved)),
+    _call("gated_scan_fwd", dev, x.data_ptr(), gate_r.data_ptr(), gate_i.data_ptr(), lam.data_ptr(), c,
+          _addr(reset), _addr(h0), y.data_ptr(), _addr(hf),
+          None if saved is None else ctypes.byref(_saved_struct(saved)),
           Bs, L, ED, int(x.dtype == torch.bfloat16))
     out = (y,) + ((hf,) if return_final_state else ()) + ((saved,) if save is not None else ())
     return out if len(out) > 1 else y
@@ -555,22 +566,23 @@ def gated_scan_bwd(x, gate_r, gate_i, lam, dy, saved, c=8.0, reset=None, dh_fina
             raise ValueError("x is on %s, expected %s" % (x.device, dev))
         if x.dtype != dy.dtype or x.shape != dy.shape:
             raise ValueError("dy must have the shape and type of x")
-    for k, shape in _saved_shapes(Bs, L, ED).items():
-        if k in saved:
-            if saved[k] is None:
-                raise ValueError("saved[%r] is missing" % k)
-            _check_shape(saved[k], "saved[%r]" % k,
-                         (torch.int8 if k.endswith("_q") else torch.float32,), dev, shape)
+    shapes = _saved_shapes(Bs, L, ED)
+    for k, t in saved.items():
+        if t is None:
+            raise ValueError("saved[%r] is missing" % k)
+        dtype = torch.int8 if k[1:] == "_q" else torch.float32
+        if not isinstance(t, torch.Tensor) or not _fits(t, dtype, shapes[k], dev):
+            _check_shape(t, "saved[%r]" % k, (dtype,), dev, shapes[k])
     _check_shape(reset, "reset", (torch.uint8, torch.bool), dev, (Bs, L))
     _check_shape(dh_final, "dh_final", (torch.float32,), dev, (Bs, ED))
     g = {k: torch.empty_like(dy) for k in ("dx", "dgate_r", "dgate_i")}
     g["dlam"] = torch.empty(ED, dtype=torch.float32, device=dev)
     g["dh0"] = torch.empty((Bs, ED), dtype=torch.float32, device=dev)
     scratch = torch.empty(min(16, -(-L // _BLOCK)) * Bs * ED, dtype=torch.float32, device=dev)
-    _call("gated_scan_bwd", dev, x, gate_r, gate_i, lam, float(c), reset,
-          dy, dh_final, ctypes.byref(_saved_struct(saved)), g["dx"],
-          g["dgate_r"], g["dgate_i"], g["dlam"], g["dh0"], scratch,
-          Bs, L, ED, int(dy.dtype == torch.bfloat16))
+    _call("gated_scan_bwd", dev, _addr(x), _addr(gate_r), _addr(gate_i), lam.data_ptr(), c, _addr(reset),
+          dy.data_ptr(), _addr(dh_final), ctypes.byref(_saved_struct(saved)), g["dx"].data_ptr(),
+          g["dgate_r"].data_ptr(), g["dgate_i"].data_ptr(), g["dlam"].data_ptr(), g["dh0"].data_ptr(),
+          scratch.data_ptr(), Bs, L, ED, int(dy.dtype == torch.bfloat16))
     return g
 
 
@@ -586,16 +598,20 @@ def gated_scan_step(x, gate_r, gate_i, lam, states, pages=None, c=8.0, y=None):
     if states is None:
         raise TypeError("states must be a torch.Tensor")
     _check(states, "states", (torch.float32,), dev, (2,))
-    if states.shape[1] != ED:
+    num_pages, columns = states.shape
+    if columns != ED:
         raise ValueError("states must have %d columns" % ED)
-    _check_shape(pages, "pages", (torch.int32,), dev, (Bs,))
-    if pages is None and states.shape[0] < Bs:
-        raise ValueError("states has fewer pages than x has rows")
+    if pages is None:
+        if num_pages < Bs:
+            raise ValueError("states has fewer pages than x has rows")
+    else:
+        _check_shape(pages, "pages", (torch.int32,), dev, (Bs,))
     if y is None:
         y = torch.empty_like(x)
-    _check_shape(y, "y", (x.dtype,), dev, x.shape)
-    _call("gated_scan_step", dev, x, gate_r, gate_i, lam, float(c), states,
-          pages, y, Bs, ED, states.shape[0], int(x.dtype == torch.bfloat16))
+    else:
+        _check_shape(y, "y", (x.dtype,), dev, x.shape)
+    _call("gated_scan_step", dev, x.data_ptr(), gate_r.data_ptr(), gate_i.data_ptr(), lam.data_ptr(), c,
+          states.data_ptr(), _addr(pages), y.data_ptr(), Bs, ED, num_pages, int(x.dtype is torch.bfloat16))
     return y
 
 
@@ -618,7 +634,7 @@ def ckpt8_save(x):
     rows = x.numel() // cols if cols else 0
     q = torch.empty(x.shape, dtype=torch.int8, device=dev)
     scale = torch.empty((-(-cols // _BLOCK), rows), dtype=torch.float32, device=dev)
-    _call("ckpt8_save", dev, x, q, scale, rows, cols, int(x.dtype == torch.bfloat16))
+    _call("ckpt8_save", dev, x.data_ptr(), q.data_ptr(), scale.data_ptr(), rows, cols, int(x.dtype == torch.bfloat16))
     return q, scale
 
 
@@ -645,7 +661,7 @@ def ckpt8_load(q, scale, dtype=None, out=None):
                  q.shape)
     if out.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out must be bf16 or fp32")
-    _call("ckpt8_load", dev, q, scale, out, rows, cols, int(out.dtype == torch.bfloat16))
+    _call("ckpt8_load", dev, q.data_ptr(), scale.data_ptr(), out.data_ptr(), rows, cols, int(out.dtype == torch.bfloat16))
     return out
 
 
@@ -655,19 +671,15 @@ def _pool_sizes(pool, page_dim):
     import torch
     if not isinstance(pool, torch.Tensor):
         raise TypeError("pool must be a torch.Tensor")
-    if pool.device.type != "cuda":
+    if not pool.is_cuda:
         raise ValueError("inputs must be CUDA tensors")
     if not pool.is_contiguous():
         raise ValueError("pool must be contiguous")
-    if not 0 <= page_dim < pool.dim():
-        raise ValueError("page_dim must name a dimension of pool")
     shape = pool.shape
-    layers = page = 1
-    for n in shape[:page_dim]:
-        layers *= n
-    for n in shape[page_dim + 1:]:
-        page *= n
-    return pool.device, layers, shape[page_dim], page * pool.element_size()
+    if not 0 <= page_dim < len(shape):
+        raise ValueError("page_dim must name a dimension of pool")
+    return (pool.device, math.prod(shape[:page_dim]), shape[page_dim],
+            math.prod(shape[page_dim + 1:]) * pool.element_size())
 
 
 def _page_list(t, name, dev):
@@ -697,7 +709,8 @@ def state_pages_fork(pool, used, src, page_dim=0):
     _page_list(src, "src", dev)
     dst = torch.empty_like(src)
     scratch = torch.empty(n_pages, dtype=torch.int32, device=dev)
-    _call("state_pages_fork", dev, pool, used, src, dst, scratch, src.shape[0], layers,
+    _call("state_pages_fork", dev, pool.data_ptr(), used.data_ptr(), src.data_ptr(), dst.data_ptr(),
+          scratch.data_ptr(), src.shape[0], layers,
           n_pages, size)
     return dst
 
@@ -711,7 +724,7 @@ def state_pages_copy(pool, src, dst, page_dim=0):
     _page_list(dst, "dst", dev)
     if src.shape != dst.shape:
         raise ValueError("src and dst must have the same length")
-    _call("state_pages_copy", dev, pool, src, dst, src.shape[0], layers, n_pages, size)
+    _call("state_pages_copy", dev, pool.data_ptr(), src.data_ptr(), dst.data_ptr(), src.shape[0], layers, n_pages, size)
 
 
 def state_pages_free(used, pages):
@@ -724,7 +737,7 @@ def state_pages_free(used, pages):
         raise ValueError("inputs must be CUDA tensors")
     _check(used, "used", (torch.uint8, torch.bool), dev, (1,))
     _page_list(pages, "pages", dev)
-    _call("state_pages_free", dev, used, pages, pages.shape[0], used.shape[0])
+    _call("state_pages_free", dev, used.data_ptr(), pages.data_ptr(), pages.shape[0], used.shape[0])
 
 
 def state_pages_compact(pool, used, pages=None, page_dim=0):
@@ -740,6 +753,7 @@ def state_pages_compact(pool, used, pages=None, page_dim=0):
         _page_list(pages, "pages", dev)
     moved = torch.empty(n_pages, dtype=torch.int32, device=dev)
     scratch = torch.empty(2 * n_pages + 2, dtype=torch.int32, device=dev)
-    _call("state_pages_compact", dev, pool, used, moved, pages, scratch,
+    _call("state_pages_compact", dev, pool.data_ptr(), used.data_ptr(), moved.data_ptr(), _addr(pages),
+          scratch.data_ptr(),
           0 if pages is None else pages.shape[0], layers, n_pages, size)
     return moved
