@@ -21,10 +21,11 @@
 namespace ssm {
 namespace gated {
 
-#ifndef KST
-#define KST 2
-#endif
-constexpr int kSteps = 16, kStages = KST;
+constexpr int kSteps = 16;
+// Tiles of a warp's rows in flight or in use.  With fp32 one, so that four
+// blocks of 4 warps fit an SM instead of two; they wait for copies in turn.
+template <typename T>
+constexpr int kStages = sizeof(T) == 4 ? 1 : 2;
 
 __device__ unsigned int g_device_error;
 
@@ -57,7 +58,7 @@ struct FwdMaps {
 template <int WARPS>
 struct Shared {
     float4 warp[2][WARPS][32];     // A of two channels, H of two channels
-    uint64_t full[WARPS][kStages]; // a warp's copies have arrived (W = 16)
+    uint64_t full[WARPS][2];       // a warp's copies have arrived (W = 16)
     float tops[WARPS][3 * kSteps]; // of the 8-bit groups
     Exchange ex;
 };
@@ -183,9 +184,9 @@ __device__ __forceinline__ void keep_8bit(uint8_t *rows, float *tops, const Kept
 template <typename T, int W, int WARPS, bool RESET, bool SAVE8>
 __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
 gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ FwdMaps maps) {
-    constexpr int kTile = WARPS * kSteps;
+    constexpr int kTile = WARPS * kSteps, kDepth = kStages<T>;
     extern __shared__ __align__(128) uint8_t ring[];
-    Shared<WARPS> &sh = *reinterpret_cast<Shared<WARPS> *>(ring + WARPS * kStages * kStageBytes<T, W>);
+    Shared<WARPS> &sh = *reinterpret_cast<Shared<WARPS> *>(ring + WARPS * kDepth * kStageBytes<T, W>);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int C = p.cluster, rank = C > 1 ? int(cluster_rank()) : 0;
     const int e0 = int(blockIdx.x) / C * 64, e = e0 + 2 * lane;
@@ -193,29 +194,29 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
     const int turns = (p.L + kTile * C - 1) / (kTile * C);
     const bool in0 = e < p.ED, in1 = e + 1 < p.ED;
 
-    uint8_t *mine = ring + warp * kStages * kStageBytes<T, W>;
+    uint8_t *mine = ring + warp * kDepth * kStageBytes<T, W>;
     if (threadIdx.x == 0) {
         if (C > 1) sh.ex.init();
         sh.ex.abort = 0;
     }
     if (W == 16) {
         if (lane == 0) {
-            for (int k = 0; k < kStages; ++k) tc::mbar_init(&sh.full[warp][k], 1);
+            for (int k = 0; k < kDepth; ++k) tc::mbar_init(&sh.full[warp][k], 1);
             tc::mbar_fence_init();
             tc::fence_proxy_async_smem();
         }
     } else if (e0 + 64 > p.ED) {
-        clear_ring(mine, kStages * kStageBytes<T, W>);
+        clear_ring(mine, kDepth * kStageBytes<T, W>);
     }
     __syncthreads();
 
     auto fetch = [&](int turn) {
         const int t = (turn * C + rank) * kTile + warp * kSteps;
         const int n = min(kSteps, p.L - t);
-        uint8_t *to = mine + turn % kStages * kStageBytes<T, W>;
+        uint8_t *to = mine + turn % kDepth * kStageBytes<T, W>;
         if constexpr (W == 16) {
             if (lane == 0 && turn < turns && n > 0 && !aborted(&sh.ex.abort)) {
-                uint64_t *bar = &sh.full[warp][turn % kStages];
+                uint64_t *bar = &sh.full[warp][turn % kDepth];
                 tc::mbar_arrive_expect_tx(bar, uint32_t(kStageBytes<T, W>));
 #pragma unroll
                 for (int k = 0; k < 3; ++k)
@@ -235,7 +236,7 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
         return lane < kSteps && t < p.L && turn < turns ? p.reset[b * p.L + t] : 0;
     };
 #pragma unroll
-    for (int k = 0; k < kStages - 1; ++k) fetch(k);
+    for (int k = 0; k < (kDepth > 1 ? kDepth - 1 : 1); ++k) fetch(k);
     uint32_t next_cut = RESET ? reset_of(0) : 0;
 
     const float2 rate = make_float2(in0 ? decay_rate(p.lam[e], p.c) : 0.0f, in1 ? decay_rate(p.lam[e + 1], p.c) : 0.0f);
@@ -249,11 +250,11 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
         const int t0 = (turn * C + rank) * kTile + warp * kSteps, buf = turn & 1;
         const int n = min(kSteps, p.L - t0);      // <= 0 behind the end
         const int64_t row0 = b * p.L + t0;
-        uint8_t *rows = mine + turn % kStages * kStageBytes<T, W>;
+        uint8_t *rows = mine + turn % kDepth * kStageBytes<T, W>;
         if constexpr (W == 16) {
-            if (n > 0) wait_or_abort(&sh.full[warp][turn % kStages], turn / kStages & 1, &sh.ex.abort, &g_device_error);
+            if (n > 0) wait_or_abort(&sh.full[warp][turn % kDepth], turn / kDepth & 1, &sh.ex.abort, &g_device_error);
         } else {
-            cp_async_wait<(kStages > 1 ? kStages - 2 : 0)>();
+            cp_async_wait<(kDepth > 1 ? kDepth - 2 : 0)>();
             __syncwarp();
         }
         uint32_t cut = 0;
@@ -268,10 +269,12 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
         else
             coefficients<T, W, false, false>(rows, row0, p.ED, rate, root_rate, 0, a, s, A, H);
         sh.warp[buf][warp][lane] = make_float4(A.x, A.y, H.x, H.y);
-        // the stage that the next rows go to was read, and its outputs stored from, a turn ago
-        if (W == 16 && lane == 0) tc::bulk_wait_read0();
-        __syncwarp();
-        fetch(turn + kStages - 1);
+        if (kDepth > 1) {
+            // the stage that the next rows go to was read, and its outputs stored from, a turn ago
+            if (W == 16 && lane == 0) tc::bulk_wait_read0();
+            __syncwarp();
+            fetch(turn + kDepth - 1);
+        }
         __syncthreads();
 
         auto keep = [&] {
@@ -344,6 +347,11 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
             for (int j = 0; j < kSteps; ++j)
                 if (j < n) put_pair(y + int64_t(j) * p.ED, s[j], p.pair_stores, in0, in1);
         }
+        if (kDepth == 1) {
+            if (W == 16 && lane == 0) tc::bulk_wait_read0();
+            __syncwarp();
+            fetch(turn + 1);
+        }
         if (p.h_final && t0 < p.L && t0 + kSteps >= p.L) {
 #pragma unroll
             for (int j = 0; j < kSteps; ++j)
@@ -413,7 +421,7 @@ gated_step_kernel(const T *__restrict__ x, const T *__restrict__ gr, const T *__
 }
 
 template <typename T, int W, int WARPS>
-constexpr int kSmem = WARPS * kStages * kStageBytes<T, W> + int(sizeof(Shared<WARPS>));
+constexpr int kSmem = WARPS * kStages<T> * kStageBytes<T, W> + int(sizeof(Shared<WARPS>));
 
 // The split goes by the sizes and the type alone (the plain kernel's measured
 // turns), so that y is the same, bit for bit, whatever is kept or reset.

@@ -164,16 +164,38 @@ __device__ __forceinline__ float rcp_fast(float v) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+// e^v for v <= 88.  bf16 tensors take the special-function unit's exponential
+// of v log2(e) as it is: ~2^-22, far below the 2^-9 of their rounding.  ACC
+// (fp32 tensors) adds what that product's rounding and log2(e)'s own lose,
+// carried to first order.
+template <bool ACC>
+__device__ __forceinline__ float2 exp_pair(float2 v) {
+    const float2 s = mul2(v, both(SSM_LOG2E));
+    const float2 e = make_float2(ex2(s.x), ex2(s.y));
+    if (!ACC) return e;
+    // log2(e) = 0x1.715476p+0 + 0x1.4ae0cp-26 (the next bits)
+    const float2 lost = fma2(v, both(0x1.4ae0cp-26f), fma2(v, both(SSM_LOG2E), mul2(s, both(-1.0f))));
+    return fma2(mul2(e, lost), both(0x1.62e43p-1f), e);      // ln 2
+}
 // -1 / (1 + e^-v): the sign costs nothing here and saves one where 1 - s or
-// -la is wanted.  ACC (fp32 tensors) uses the accurate functions; bf16 tensors
-// the special-function unit, whose ~2^-22 is far below the 2^-9 of their
-// rounding.
+// -la is wanted.
 template <bool ACC>
 __device__ __forceinline__ float2 nsigmoid2(float2 v) {
-    if (ACC) return make_float2(-1.0f / (1.0f + expf(-v.x)), -1.0f / (1.0f + expf(-v.y)));
-    const float2 s = mul2(v, both(-SSM_LOG2E));
-    const float2 d = fma2(make_float2(ex2(s.x), ex2(s.y)), both(-1.0f), both(-1.0f));
-    return make_float2(rcp_fast(d.x), rcp_fast(d.y));
+    if (!ACC) {
+        const float2 s = mul2(v, both(-SSM_LOG2E));
+        const float2 d = fma2(make_float2(ex2(s.x), ex2(s.y)), both(-1.0f), both(-1.0f));
+        return make_float2(rcp_fast(d.x), rcp_fast(d.y));
+    }
+    // e^88 keeps d finite, and its reciprocal is below the smallest normal
+    // number; e^-88 is nothing beside 1
+    float x, y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(v.x), "f"(-88.0f));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(v.y), "f"(-88.0f));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(x), "f"(88.0f));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(y), "f"(88.0f));
+    const float2 d = fma2(exp_pair<true>(make_float2(-x, -y)), both(-1.0f), both(-1.0f));
+    const float2 r = make_float2(rcp_fast(d.x), rcp_fast(d.y));
+    return fma2(fma2(mul2(d, both(-1.0f)), r, both(1.0f)), r, r);      // one Newton step
 }
 
 // Decays from la <= 0: a = e^la and em = a - 1, em to full relative accuracy,
@@ -198,13 +220,7 @@ __device__ __forceinline__ void decay2(float2 la, float2 &a, float2 &em) {
     em = slow_em1(la);
     a = add2(em, both(1.0f));
     if (WIDE) {
-        float2 e;
-        if (ACC) {
-            e = make_float2(expf(la.x), expf(la.y));
-        } else {
-            const float2 s = mul2(la, both(SSM_LOG2E));
-            e = make_float2(ex2(s.x), ex2(s.y));
-        }
+        const float2 e = exp_pair<ACC>(la);
         const float2 em_e = add2(e, both(-1.0f));
         if (la.x <= -kSlow) a.x = e.x, em.x = em_e.x;
         if (la.y <= -kSlow) a.y = e.y, em.y = em_e.y;

@@ -20,10 +20,11 @@ namespace ssm {
 namespace gated_bwd {
 using namespace gated;
 
-#ifndef BKST
-#define BKST 2
-#endif
-constexpr int kWarps = 8, kSteps = kBlock / kWarps, kThreads = 32 * kWarps, kStages = BKST;
+constexpr int kWarps = 8, kSteps = kBlock / kWarps, kThreads = 32 * kWarps;
+// Tiles of a warp's rows in flight or in use.  With fp32 one, so that two
+// blocks fit an SM.
+template <typename T>
+constexpr int kStages = sizeof(T) == 4 ? 1 : 2;
 
 __device__ unsigned int g_device_error;
 
@@ -52,7 +53,7 @@ struct Stage {
     static constexpr int kIn = kSteps * kPitch<K, W>, kDy = 3 * kIn, kScales = kDy + kSteps * kPitch<T, W>;
     static constexpr int kBytes = kScales + (sizeof(K) == 1 ? 128 : 0);
     static constexpr int kOut = kSteps * kPitch<T, W>, kOwnOut = W == 16 && sizeof(K) < sizeof(T) ? 3 * kOut : 0;
-    static constexpr int kWarpBytes = kStages * kBytes + kOwnOut;
+    static constexpr int kDepth = kStages<T>, kWarpBytes = kDepth * kBytes + kOwnOut;
 };
 
 // Boxes of 64 channels x kSteps rows (W = 16).
@@ -64,7 +65,7 @@ struct Shared {
     float4 warp[kWarps][32];        // a piece's A of two channels, state of two channels
     float2 adjoint[kWarps][32];     // its adjoint, then the adjoint that enters it
     float2 state[kWarps][32];       // the state that enters it
-    uint64_t full[kWarps][kStages]; // a warp's copies have arrived (W = 16)
+    uint64_t full[kWarps][2];       // a warp's copies have arrived (W = 16)
     Exchange ex;
 };
 
@@ -159,6 +160,7 @@ template <typename T, typename K, int W, bool RESET>
 __global__ void __launch_bounds__(kThreads, 2)
 gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ BwdMaps maps) {
     using S = Stage<T, K, W>;
+    constexpr int kDepth = S::kDepth;
     extern __shared__ __align__(128) uint8_t ring[];
     Shared &sh = *reinterpret_cast<Shared *>(ring + kWarps * S::kWarpBytes);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -175,12 +177,12 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
     }
     if (W == 16) {
         if (lane == 0) {
-            for (int k = 0; k < kStages; ++k) tc::mbar_init(&sh.full[warp][k], 1);
+            for (int k = 0; k < kDepth; ++k) tc::mbar_init(&sh.full[warp][k], 1);
             tc::mbar_fence_init();
             tc::fence_proxy_async_smem();
         }
     } else if (e0 + 64 > p.ED) {
-        clear_ring(mine, kStages * S::kBytes);
+        clear_ring(mine, kDepth * S::kBytes);
     }
     __syncthreads();
 
@@ -189,10 +191,10 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
         const int n = min(kSteps, p.L - t);
         const int64_t row0 = b * p.L + t;
         if (turn >= 0 && n > 0) {
-            uint8_t *to = mine + turn % kStages * S::kBytes;
+            uint8_t *to = mine + turn % kDepth * S::kBytes;
             if constexpr (W == 16) {
                 if (lane == 0 && !aborted(&sh.ex.abort)) {
-                    uint64_t *bar = &sh.full[warp][turn % kStages];
+                    uint64_t *bar = &sh.full[warp][turn % kDepth];
                     tc::mbar_arrive_expect_tx(bar, uint32_t(S::kScales));
 #pragma unroll
                     for (int k = 0; k < 3; ++k) tc::tma_load_3d(to + k * S::kIn, &maps.in[k], bar, e0, t, int(b));
@@ -229,7 +231,7 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
         return make_float2(in0 ? k[0] : 0.0f, in1 ? k[1] : 0.0f);
     };
 #pragma unroll
-    for (int k = 0; k < kStages - 1; ++k) fetch(turns - 1 - k);
+    for (int k = 0; k < (kDepth > 1 ? kDepth - 1 : 1); ++k) fetch(turns - 1 - k);
     uint32_t next_cut = RESET ? reset_of(turns - 1) : 0;
     float2 next_h = kept_of(turns - 1);
     if (C > 1) cluster_sync();     // every block runs before another writes to its shared memory
@@ -245,14 +247,14 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
         const int t0 = (turn * C + rank) * kBlock + warp * kSteps, buf = turn & 1;
         const int n = min(kSteps, p.L - t0);      // <= 0 behind the end
         const int64_t row0 = b * p.L + t0;
-        uint8_t *stage = mine + turn % kStages * S::kBytes;
+        uint8_t *stage = mine + turn % kDepth * S::kBytes;
         if (W == 16 && n > 0) {
-            const int k = turn % kStages;
+            const int k = turn % kDepth;
             wait_or_abort(&sh.full[warp][k], phases >> k & 1, &sh.ex.abort, &g_device_error);
             phases ^= 1u << k;
         }
         if (W != 16 || sizeof(K) == 1) {
-            cp_async_wait<kStages - 2>();
+            cp_async_wait<(kDepth > 1 ? kDepth - 2 : 0)>();
             __syncwarp();
         }
         uint32_t cut = 0;
@@ -272,10 +274,12 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
 
         sh.warp[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
         sh.adjoint[warp][lane] = U;
-        // the stage that the next rows go to was read, and its outputs stored from, a turn ago
-        if (W == 16 && lane == 0) tc::bulk_wait_read0();
-        __syncwarp();
-        fetch(turn - (kStages - 1));
+        if (kDepth > 1) {
+            // the stage that the next rows go to was read, and its outputs stored from, a turn ago
+            if (W == 16 && lane == 0) tc::bulk_wait_read0();
+            __syncwarp();
+            fetch(turn - (kDepth - 1));
+        }
         __syncthreads();
 
         // Two warps find what enters each warp's steps: warp 1 the states from
@@ -329,7 +333,7 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
             h = RESET && (cut >> j & 1) ? s[j] : on;
             s[j] = at;
         }
-        uint8_t *out = S::kOwnOut ? mine + kStages * S::kBytes : stage;
+        uint8_t *out = S::kOwnOut ? mine + kDepth * S::kBytes : stage;
         if (general)
             gradients<T, K, W, true>(p, stage, out, row0, rate, cut, n, a, s, nsr, nsi, nm, u, e, in0, in1, sum);
         else
@@ -341,6 +345,11 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
                 for (int k = 0; k < 3; ++k) tma_store_3d(&maps.out[k], out + k * S::kOut, e0, t0, int(b));
                 tc::bulk_commit();
             }
+        }
+        if (kDepth == 1) {
+            if (W == 16 && lane == 0) tc::bulk_wait_read0();
+            __syncwarp();
+            fetch(turn - 1);
         }
     }
     if (W == 16) {
