@@ -441,9 +441,6 @@ template <typename T, int W, bool RESET, bool SAVE8>
 static cudaError_t start_fwd(FwdArgs<T> p, const FwdMaps &maps, int64_t Bs, int num_sms, cudaStream_t st) {
     Split how = split_for<T>(Bs, p.L, p.ED, num_sms);
     if (how.warps == 0) return cudaErrorInvalidConfiguration;
-#ifdef CL
-    how.cluster = CL; how.warps = WP;
-#endif
     p.cluster = how.cluster;
     if (how.warps == 8)
         return start_clusters(gated_fwd_kernel<T, W, 8, RESET, SAVE8>, kSmem<T, W, 8>, how, p.ED, Bs, st, nullptr, &p,

@@ -327,14 +327,16 @@ __device__ __forceinline__ void copy_rows(uint8_t *to, const T *from, int64_t ro
     const int lane = threadIdx.x % 32;
     if constexpr (W == 8) {
         constexpr int kChunks = 64 * kSize / 16, kRows = 32 / kChunks;      // of one instruction
-        const uint8_t *base = reinterpret_cast<const uint8_t *>(from);
-        const bool tail = e0 + 64 + 16 / kSize > ED;
+        // offsets from the granule of the first row's first element fit 32 bits (ED < 2^26)
+        const int64_t begin = (row0 * ED + e0) * kSize;
+        const uint8_t *base = reinterpret_cast<const uint8_t *>(from) + (begin & ~int64_t(15));
+        const uint32_t lead = uint32_t(begin) & 15, pitch = uint32_t(ED) * kSize;
+        const int width = min(64, ED - e0) * kSize;
         // The lane's granule `chunk` of a row; nothing behind the row's end, which may be the tensor's.
         auto copy = [&](int row, int chunk) {
-            const int64_t begin = ((row0 + row) * ED + e0) * kSize, at = (begin & ~int64_t(15)) + 16 * chunk;
-            int bytes = 16;
-            if (tail) bytes = int(max(int64_t(0), min(int64_t(16), begin + int64_t(ED - e0) * kSize - at)));
-            if (row < n_rows && bytes > 0) cp_async16(to + row * kPitch<T, W> + 16 * chunk, base + at, bytes);
+            const uint32_t at = lead + uint32_t(row) * pitch, first = at & ~15u;
+            const int bytes = min(16, int(at - first) + width - 16 * chunk);
+            if (row < n_rows && bytes > 0) cp_async16(to + row * kPitch<T, W> + 16 * chunk, base + (first + 16 * chunk), bytes);
         };
 #pragma unroll
         for (int i = 0; i < STEPS; i += kRows) copy(i + lane / kChunks, lane % kChunks);
@@ -524,7 +526,7 @@ inline Split best_split(void (*kern)(Args...), int smem, int warps, int tile, co
 
 template <typename T>
 inline int widest_copy(uintptr_t at, int64_t ED) {
-    return at % 16 != 0 ? 1 : ED * int64_t(sizeof(T)) % 16 == 0 ? 16 : 8;
+    return at % 16 != 0 || ED >= (1 << 26) ? 1 : ED * int64_t(sizeof(T)) % 16 == 0 ? 16 : 8;
 }
 
 

@@ -411,9 +411,6 @@ static cudaError_t start(BwdArgs<T> p, const BwdMaps &maps, int64_t Bs, int num_
     const Turn turn{1.95 * by, 0.92 * by, 0.45, 0.1};
     Split how = best_split(kern, kSmem, kWarps, kBlock, turn, Bs, p.L, p.ED, num_sms, slots);
     if (how.warps == 0) return cudaErrorInvalidConfiguration;
-#ifdef BCL
-    how.cluster = BCL;
-#endif
     *cluster = p.cluster = how.cluster;
     return start_clusters(kern, kSmem, how, p.ED, Bs, st, nullptr, &p, &maps);
 }
