@@ -362,14 +362,12 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
         }
     }
     if (W == 16) {
-        if (lane == 0) {
-            tc::bulk_wait_read0();
-            if (aborted(&sh.ex.abort)) linger();
-        }
+        if (lane == 0) tc::bulk_wait_read0();
     } else {
         cp_async_wait<0>();
     }
     if (C > 1) cluster_sync();     // no block leaves while another may still write to it
+    if (aborted(&sh.ex.abort)) linger();
 }
 
 // One token.  A thread takes two channels of kStepRows rows, so that a

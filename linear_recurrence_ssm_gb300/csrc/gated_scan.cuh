@@ -31,12 +31,11 @@ struct Kept {
 
 // ---- exchange between the blocks of a cluster --------------------------------
 // Each block sends its tile's piece to every other block of the cluster, as
-// asynchronous stores that count towards the receiver's
-// mbarrier: no block waits for its own stores to arrive anywhere, as a
-// cluster barrier would have it do (its release took 1.2 of 7 cycles an
-// instruction).  Two buffers are enough: a block sends for turn s + 2 only
-// after it has received every piece of turn s + 1, and each of those was sent
-// after its sender had read turn s.
+// asynchronous stores that count towards the receiver's mbarrier: no block
+// waits for its own stores to arrive anywhere, as a cluster barrier would have
+// it do (its release took 1.2 of 7 cycles an instruction).  Two buffers are
+// enough: a block sends for turn s + 2 only after it has received every piece
+// of turn s + 1, and each of those was sent after its sender had read turn s.
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -50,6 +49,13 @@ constexpr int kMaxCluster = 16;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 inline int exchange_bytes(int cluster) { return 2 * (cluster - 1) * 32 * 16; }
 
+__device__ __forceinline__ bool aborted(const int *abort) { return *reinterpret_cast<const volatile int *>(abort); }
+// What a block does before it leaves after a wait that ran out: copies and
+// pieces on their way into its shared memory get the same time again.
+__device__ __forceinline__ void linger() {
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (tc::globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(1000);
+}
 struct alignas(16) Exchange {
     uint64_t full[2];
     int abort;      // a wait ran out: this block waits no more, its results are unspecified
@@ -66,6 +72,7 @@ struct alignas(16) Exchange {
     }
     // One warp: block `rank`'s piece to block k.
     __device__ __forceinline__ void send(int buf, int C, int rank, int k, float4 v) {
+        if (aborted(&abort)) return;
         uint32_t to, bar;
         asm("mapa.shared::cluster.u32 %0, %1, %2;"
             : "=r"(to)
@@ -78,6 +85,7 @@ struct alignas(16) Exchange {
     }
     // One thread, once a turn: C - 1 pieces will come.
     __device__ __forceinline__ void expect(int buf, int C) {
+        if (aborted(&abort)) return;      // the phase before may never complete
         tc::mbar_arrive_expect_tx(&full[buf], uint32_t(C - 1) * 32 * 16);
     }
     __device__ __forceinline__ bool arrived(int buf, uint32_t parity) {
@@ -106,13 +114,6 @@ struct alignas(16) Exchange {
     }
 };
 
-__device__ __forceinline__ bool aborted(const int *abort) { return *reinterpret_cast<const volatile int *>(abort); }
-// What a block does before it leaves after a wait that ran out: copies into
-// its shared memory may still be in flight, and get the same time again.
-__device__ __forceinline__ void linger() {
-    const uint64_t t0 = tc::globaltimer_ns();
-    while (tc::globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(1000);
-}
 // Waits for a warp's own copies; the same limit.
 __device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, int *abort, unsigned int *error) {
     if (tc::mbar_wait_bounded(bar, parity, abort, kWaitLimitNs)) return;

@@ -353,10 +353,7 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
         }
     }
     if (W == 16) {
-        if (lane == 0) {
-            tc::bulk_wait_read0();
-            if (aborted(&sh.ex.abort)) linger();
-        }
+        if (lane == 0) tc::bulk_wait_read0();
     }
     cp_async_wait<0>();
     if (p.dh0 && warp == 0 && rank == 0) {
@@ -375,6 +372,7 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
         if (in1) part[1] = s.y;
     }
     if (C > 1) cluster_sync();     // no block leaves while another may still write to it
+    if (aborted(&sh.ex.abort)) linger();
 }
 
 // Read and clear this unit's device error word (host side, synchronous).

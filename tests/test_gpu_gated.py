@@ -240,6 +240,75 @@ def test_unaligned_storage_and_another_stream(cuda_device, dtype):
         near(g[k], g2[k].double().cpu().numpy(), 2e-3, dtype, k)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Bs,L,ED", [(1, 900, 75), (2, 257, 1537), (1, 2100, 40), (3, 640, 129)])
+def test_clusters_and_rows_off_16_bytes(cuda_device, Bs, L, ED, dtype):
+    """Long sequences of few channels (a cluster's blocks share the time axis)
+    whose rows start anywhere, with resets, states and 8-bit checkpoints."""
+    inp, reset, more = case(Bs, L, ED, dtype, seed=L + 3 * ED, resets=True)
+    _, _, saved = check_fwd(inp, reset, more["h0"], dtype, cuda_device, save="8bit")
+    values = {}
+    for k, q in (("x", "x"), ("gate_r", "r"), ("gate_i", "i")):
+        rq, rs = gated.ckpt8(inp[k])
+        assert np.array_equal(saved[q + "_q"].cpu().numpy(), rq)
+        assert np.array_equal(saved[q + "_s"].cpu().numpy(), rs)
+        values[k] = gated.ckpt8_values(rq, rs)
+    check_bwd(inp, reset, more, dtype, cuda_device, saved, values)
+    check_bwd(inp, reset, more, dtype, cuda_device, {"states": saved["states"]})
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("L,ED", [(70, 128), (700, 64)])
+def test_fast_decays(cuda_device, L, ED, dtype):
+    """Decays from almost 1 to below 2^-100 in one block of channels."""
+    inp, reset, more = case(2, L, ED, dtype, seed=L, resets=True)
+    inp["lam"] = torch.linspace(-9.0, 9.0, ED)[torch.randperm(ED, generator=torch.Generator().manual_seed(1))]
+    _, _, saved = check_fwd(inp, reset, more["h0"], dtype, cuda_device)
+    check_bwd(inp, reset, more, dtype, cuda_device, saved)
+
+
+def test_y_does_not_depend_on_what_is_kept(cuda_device):
+    for Bs, L, ED in ((2, 700, 96), (1, 3000, 64), (2, 500, 72)):
+        inp, reset, _ = case(Bs, L, ED, "bf16", seed=L)
+        d = on(inp, cuda_device)
+        y = lrs.gated_scan_fwd(**d)
+        assert torch.equal(y, lrs.gated_scan_fwd(**d, save="states")[0])
+        assert torch.equal(y, lrs.gated_scan_fwd(**d, save="8bit")[0])
+
+
+def test_calls_in_a_cuda_graph(cuda_device):
+    """A token step and a forward-backward pair, captured once and replayed on
+    new values."""
+    inp, _, more = case(3, 200, 128, "bf16", seed=31)
+    d = on(inp, cuda_device)
+    dy = more["dy"].to(cuda_device)
+    tok = {k: v[:, 0].contiguous() if k != "lam" else v for k, v in d.items()}
+    states = torch.zeros(4, 128, device=cuda_device)
+    pages = torch.tensor([2, -1, 0], dtype=torch.int32, device=cuda_device)
+
+    def work():
+        y, saved = lrs.gated_scan_fwd(**d, save="8bit")
+        g = lrs.gated_scan_bwd(None, None, None, d["lam"], dy, saved)
+        return [y, *g.values(), lrs.gated_scan_step(**tok, states=states, pages=pages)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = work()
+    d["x"].mul_(0.5)
+    tok["x"].mul_(2.0)
+    states.fill_(1.0)
+    graph.replay()
+    got = [t.clone() for t in out]
+    states.fill_(1.0)
+    for a, b in zip(got, work()):
+        assert torch.equal(a, b)
+
+
 def test_repeated_calls_are_bitwise_equal(cuda_device):
     inp, reset, more = case(3, 700, 320, "bf16", seed=13, resets=True)
     d, r = on(inp, cuda_device), reset.to(cuda_device)
