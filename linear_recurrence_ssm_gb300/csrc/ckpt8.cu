@@ -20,20 +20,41 @@ struct Block {
 };
 // Blocks count through the groups, eight at a time, then the rows.
 __device__ __forceinline__ Block block_of(int64_t groups) {
-    const int64_t across = (groups + kWarps - 1) / kWarps, at = blockIdx.x;
-    return {at / across * kRows, at % across * kWarps + threadIdx.x / 32};
+    const uint32_t across = uint32_t((groups + kWarps - 1) / kWarps), row = blockIdx.x / across;
+    return {int64_t(row) * kRows, int64_t(blockIdx.x - row * across) * kWarps + threadIdx.x / 32};
 }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
-    const uint4 w = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// |v| as bits: their order is that of the values, NaN on top
+__device__ __forceinline__ uint32_t size_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Eight elements as they are read; the largest's size_bits; one as fp32.
+struct Eight16 {
+    uint32_t w[4];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ uint32_t top() const {
+        uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(u[i] << 16), v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-}
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
+        for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+        return max(m << 16, m & 0xffff0000u);
+    }
+    __device__ __forceinline__ float at(int k) const {
+        return __uint_as_float(k % 2 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+    }
+};
+struct Eight32 {
+    float v[8];
+    __device__ __forceinline__ void load(const float *p) {
+        reinterpret_cast<float4 *>(v)[0] = reinterpret_cast<const float4 *>(p)[0];
+        reinterpret_cast<float4 *>(v)[1] = reinterpret_cast<const float4 *>(p)[1];
+    }
+    __device__ __forceinline__ uint32_t top() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = max(m, size_bits(v[k]));
+        return m;
+    }
+    __device__ __forceinline__ float at(int k) const { return v[k]; }
+};
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
     uint4 w;
     __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&w);
@@ -45,9 +66,6 @@ __device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
     reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
-// |v| as bits: their order is that of the values, NaN on top
-__device__ __forceinline__ uint32_t size_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
 // cols is a multiple of 8, x starts on 16 bytes and q on 8.
 template <typename T>
 __global__ void __launch_bounds__(32 * kWarps)
@@ -57,33 +75,36 @@ save_vectors_kernel(const T *__restrict__ x, int8_t *__restrict__ q, float *__re
     const int lane = threadIdx.x % 32;
     const int64_t e = b.group * kGroup + lane % 8 * 8;
     if (b.group * kGroup >= cols) return;
-    float v[kRows / 4][8];
+    const int64_t first = b.row0 + lane / 8, at = first * cols + e, step = 4 * cols;
+    const int left = int(min(rows - first, int64_t(kRows)));      // rows of this lane: 0, 4, ... below it
+    std::conditional_t<sizeof(T) == 4, Eight32, Eight16> v[kRows / 4];
 #pragma unroll
     for (int i = 0; i < kRows / 4; ++i) {
-        const int64_t row = b.row0 + 4 * i + lane / 8;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][k] = 0.0f;
-        if (row < rows && e < cols) load8(x + row * cols + e, v[i]);
+        v[i] = {};
+        if (4 * i < left && e < cols) v[i].load(x + at + i * step);
     }
+    // lane 8 r + i divides for row 4 i + r
+    uint32_t mine = 0;
 #pragma unroll
     for (int i = 0; i < kRows / 4; ++i) {
-        const int64_t row = b.row0 + 4 * i + lane / 8;
-        uint32_t top = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = max(top, size_bits(v[i][k]));
+        uint32_t top = v[i].top();
 #pragma unroll
         for (int d = 1; d < 8; d *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float t = __uint_as_float(top), inv = inverse_of(t);
+        if (lane % 8 == i) mine = top;
+    }
+    const float t = __uint_as_float(mine), inv = inverse_of(t);
+    if (lane % 8 < kRows / 4 && 4 * (lane % 8) < left)
+        scale[b.group * rows + first + 4 * (lane % 8)] = scale_of(t);
+#pragma unroll
+    for (int i = 0; i < kRows / 4; ++i) {
+        const float by = __shfl_sync(0xffffffffu, inv, (lane & 24) + i);
         uint32_t n[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) n[k] = quantised(v[i][k], inv);
-        if (row < rows) {
-            uint2 w;
-            w.x = __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410);
-            w.y = __byte_perm(__byte_perm(n[4], n[5], 0x0040), __byte_perm(n[6], n[7], 0x0040), 0x5410);
-            if (e < cols) *reinterpret_cast<uint2 *>(q + row * cols + e) = w;
-            if (lane % 8 == 0) scale[b.group * rows + row] = scale_of(t);
-        }
+        for (int k = 0; k < 8; ++k) n[k] = quantised(v[i].at(k), by);
+        uint2 w;
+        w.x = __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410);
+        w.y = __byte_perm(__byte_perm(n[4], n[5], 0x0040), __byte_perm(n[6], n[7], 0x0040), 0x5410);
+        if (4 * i < left && e < cols) *reinterpret_cast<uint2 *>(q + at + i * step) = w;
     }
 }
 
@@ -95,24 +116,24 @@ load_vectors_kernel(const int8_t *__restrict__ q, const float *__restrict__ scal
     const int lane = threadIdx.x % 32;
     const int64_t e = b.group * kGroup + lane % 8 * 8;
     if (e >= cols) return;
+    const int64_t first = b.row0 + lane / 8, at = first * cols + e, step = 4 * cols;
+    const int left = int(min(rows - first, int64_t(kRows)));
     uint2 w[kRows / 4];
     float s[kRows / 4];
 #pragma unroll
     for (int i = 0; i < kRows / 4; ++i) {
-        const int64_t row = b.row0 + 4 * i + lane / 8;
-        if (row >= rows) break;
-        w[i] = *reinterpret_cast<const uint2 *>(q + row * cols + e);
-        s[i] = scale[b.group * rows + row];
+        if (4 * i >= left) break;
+        w[i] = *reinterpret_cast<const uint2 *>(q + at + i * step);
+        s[i] = scale[b.group * rows + first + 4 * i];
     }
 #pragma unroll
     for (int i = 0; i < kRows / 4; ++i) {
-        const int64_t row = b.row0 + 4 * i + lane / 8;
-        if (row >= rows) break;
+        if (4 * i >= left) break;
         float v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             v[k] = float(int8_t((k < 4 ? w[i].x : w[i].y) >> (k % 4 * 8))) * s[i];
-        store8(x + row * cols + e, v);
+        store8(x + at + i * step, v);
     }
 }
 
