@@ -6,7 +6,10 @@
 // one group with four rows in flight a lane, and the eight warps of a block
 // take neighbouring groups, so that a block reads 1 KB of every row and writes
 // 64 bytes of neighbouring scales.  Where rows do not start on vectors, lanes
-// take single elements, a warp a whole group of 64.
+// take single elements, a warp a whole group of 64.  16384 x 2048 bf16: save
+// 20.5 us (5.0 TB/s), load 18.5 us (5.5 TB/s), 15 us of bytes each and 3 us of
+// start.  8 rows a warp measured the same, 4 rows 28.7 us, 32 rows 30.7 us;
+// one division a row instead of one a lane took save from 24.6 to 20.5 us.
 #include "gated_scan.cuh"
 
 namespace ssm {

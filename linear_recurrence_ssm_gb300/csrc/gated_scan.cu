@@ -2,18 +2,32 @@
 //
 // h_t = a_t h_{t-1} + b_t is joined from pieces of the time axis: a piece is
 // the map h -> A h + H with A the product of its decays and H its result from
-// 0.  A warp owns 8 steps of 64 channels (two a lane) and keeps its a_t, b_t
-// in registers; the eight warps of a block form a tile of 64 steps.  Their
-// pieces meet in shared memory, every warp folds those before its own, and
-// then runs its 8 steps again from the state that enters them -- one read of
-// the inputs, one write of the outputs, and no state in between leaves the
-// SM.  Blocks walk along the time axis; where the channels alone cannot fill
-// the GPU, a cluster of blocks takes neighbouring tiles of a sequence at
-// once and its blocks exchange their tiles' pieces through distributed
-// shared memory.
+// 0.  A warp owns 16 steps of 64 channels (two a lane) and keeps its a_t, b_t
+// in registers; the 4 or 8 warps of a block form a tile.  Their pieces meet in
+// shared memory, every warp folds those before its own, and then runs its
+// steps again from the state that enters them -- one read of the inputs, one
+// write of the outputs, and no state in between leaves the SM.  Blocks walk
+// along the time axis; where the channels alone cannot fill the GPU, a cluster
+// of blocks takes neighbouring tiles of a sequence at once and its blocks
+// exchange their tiles' pieces through distributed shared memory.
 //
-// Each warp copies its own rows ahead of their use (cp.async, kStages tiles),
-// so that loads need no barrier; one barrier a tile exchanges the pieces.
+// Each warp copies its own rows ahead of their use (tensor copies of 16 x 64
+// boxes where rows are multiples of 16 bytes), so that loads need no block
+// barrier, and stores its outputs as a box from the place of x's rows; one
+// barrier a tile exchanges the pieces.
+//
+// An element costs 8 bytes (bf16) and 3 exponentials' worth of special
+// functions, so that bytes, instruction issue and the special-function unit
+// lie close together.  What carried it, at Bs=8 L=2048 ED=1536 (bytes: 30 us):
+// one thread a channel 1386 us; tiles joined in shared memory 85; pieces sent
+// by asynchronous stores instead of cluster barriers 60; boxes and 16 steps a
+// warp 48; all four blocks on an SM and clusters of three 43; one root for the
+// gate and the input's factor 41 (4.9 TB/s, 73 % of the measured copy rate).
+// What is left: 576 blocks of 608 places, a start of 3 us and issue slots
+// (448 instructions for 16 x 32 elements, 3.8 warps a scheduler).
+// Bs=1 L=65536 ED=2560 with resets: 308 us for 198 us of bytes; 40 chains fill
+// 10.5 of 16 warps an SM, more blocks a cluster wait for a second round.
+// With the 8-bit checkpoint, Bs=16 L=1000 ED=2560: 110 us for 68 us of bytes.
 #include "gated_scan.cuh"
 
 #include <algorithm>
