@@ -457,12 +457,12 @@ SSM_API ssm_status_t ckpt8_load(const int8_t *q, const float *scale, void *x, in
  *             free page); pages, a list of page numbers (NULL with n = 0), is
  *             renumbered in place (negative entries stay, pages that were not
  *             in use become -1).
- *   scratch : int32 entries of the caller's, unspecified afterwards:
- *             num_pages for fork, 2 num_pages + 2 for compact.
+ *             scratch : 2 num_pages + 2 int32 entries of the caller's,
+ *             unspecified afterwards.
  */
 #define SSM_MAX_PAGES (1ll << 24)
 SSM_API ssm_status_t state_pages_fork(void *pool, uint8_t *used, const int32_t *src, int32_t *dst,
-                                      int32_t *scratch, int64_t n, int64_t layers, int64_t num_pages,
+                                      int64_t n, int64_t layers, int64_t num_pages,
                                       int64_t page_bytes, void *stream);
 SSM_API ssm_status_t state_pages_copy(void *pool, const int32_t *src, const int32_t *dst, int64_t n,
                                       int64_t layers, int64_t num_pages, int64_t page_bytes,

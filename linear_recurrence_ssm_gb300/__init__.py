@@ -79,7 +79,7 @@ SIGNATURES = {
     "gated_scan_step": ([_VP] * 4 + [_F32] + [_VP] * 3 + [_I64] * 3 + [ctypes.c_int, _VP], ctypes.c_int),
     "ckpt8_save": ([_VP] * 3 + [_I64] * 2 + [ctypes.c_int, _VP], ctypes.c_int),
     "ckpt8_load": ([_VP] * 3 + [_I64] * 2 + [ctypes.c_int, _VP], ctypes.c_int),
-    "state_pages_fork": ([_VP] * 5 + [_I64] * 4 + [_VP], ctypes.c_int),
+    "state_pages_fork": ([_VP] * 4 + [_I64] * 4 + [_VP], ctypes.c_int),
     "state_pages_copy": ([_VP] * 3 + [_I64] * 4 + [_VP], ctypes.c_int),
     "state_pages_free": ([_VP] * 2 + [_I64] * 2 + [_VP], ctypes.c_int),
     "state_pages_compact": ([_VP] * 5 + [_I64] * 4 + [_VP], ctypes.c_int),
@@ -464,6 +464,14 @@ def _saved_shapes(Bs, L, ED):
     return dict(states=(Bs, -(-L // _BLOCK), ED), x_q=q, r_q=q, i_q=q, x_s=s, r_s=s, i_s=s)
 
 
+def _new_saved(save, Bs, L, ED, dev):
+    """Empty tensors for what ``gated_scan_fwd`` keeps."""
+    import torch
+    shapes = _saved_shapes(Bs, L, ED)
+    return {k: torch.empty(shapes[k], dtype=torch.int8 if k[1:] == "_q" else torch.float32, device=dev)
+            for k in (("states",) if save == "states" else ("states",) + _CKPT8)}
+
+
 def _saved_struct(saved):
     o = GatedSaved()
     for k, t in saved.items():
@@ -525,12 +533,7 @@ def gated_scan_fwd(x, gate_r, gate_i, lam, c=8.0, reset=None, h0=None, return_fi
     else:
         _check_shape(y, "y", (x.dtype,), dev, x.shape)
     hf = torch.empty((Bs, ED), dtype=torch.float32, device=dev) if return_final_state else None
-    saved = None
-    if save is not None:
-        shapes = _saved_shapes(Bs, L, ED)
-        keys = ("states",) if save == "states" else ("states",) + _CKPT8
-        saved = {k: torch.empty(shapes[k], dtype=torch.int8 if k[1:] == "_q" else torch.float32,
-                                device=dev) for k in keys}
+    saved = _new_saved(save, Bs, L, ED, dev) if save is not None else None
     _call("gated_scan_fwd", dev, x.data_ptr(), gate_r.data_ptr(), gate_i.data_ptr(), lam.data_ptr(), c,
           _addr(reset), _addr(h0), y.data_ptr(), _addr(hf),
           None if saved is None else ctypes.byref(_saved_struct(saved)),
@@ -708,9 +711,7 @@ def state_pages_fork(pool, used, src, page_dim=0):
     _used(used, dev, n_pages)
     _page_list(src, "src", dev)
     dst = torch.empty_like(src)
-    scratch = torch.empty(n_pages, dtype=torch.int32, device=dev)
-    _call("state_pages_fork", dev, pool.data_ptr(), used.data_ptr(), src.data_ptr(), dst.data_ptr(),
-          scratch.data_ptr(), src.shape[0], layers,
+    _call("state_pages_fork", dev, pool.data_ptr(), used.data_ptr(), src.data_ptr(), dst.data_ptr(), src.shape[0], layers,
           n_pages, size)
     return dst
 

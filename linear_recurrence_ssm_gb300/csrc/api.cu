@@ -94,9 +94,8 @@ cudaError_t load(const int8_t *q, const float *scale, T *x, int64_t rows, int64_
 namespace pages {
 cudaError_t copy(void *pool, const int32_t *src, const int32_t *dst, int64_t n, int64_t layers,
                  int64_t num_pages, int64_t bytes, int num_sms, cudaStream_t st);
-cudaError_t fork(void *pool, uint8_t *used, const int32_t *src, int32_t *dst, int32_t *scratch,
-                 int64_t n, int64_t layers, int64_t num_pages, int64_t bytes, int num_sms,
-                 cudaStream_t st);
+cudaError_t fork(void *pool, uint8_t *used, const int32_t *src, int32_t *dst, int64_t n,
+                 int64_t layers, int64_t num_pages, int64_t bytes, int num_sms, cudaStream_t st);
 cudaError_t free_pages(uint8_t *used, const int32_t *pages, int64_t n, int64_t num_pages,
                        cudaStream_t st);
 cudaError_t compact(void *pool, uint8_t *used, int32_t *moved, int32_t *pages, int32_t *scratch,
@@ -702,15 +701,14 @@ ssm_status_t ckpt8_load(const int8_t *q, const float *scale, void *x, int64_t ro
                                                     st));
 }
 
-ssm_status_t state_pages_fork(void *pool, uint8_t *used, const int32_t *src, int32_t *dst,
-                              int32_t *scratch, int64_t n, int64_t layers, int64_t num_pages,
-                              int64_t page_bytes, void *stream) {
-    if (!used || (n > 0 && (!src || !dst || !scratch))) return SSM_ERR_INVALID_ARG;
-    if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(scratch, 4)) return SSM_ERR_ALIGNMENT;
+ssm_status_t state_pages_fork(void *pool, uint8_t *used, const int32_t *src, int32_t *dst, int64_t n,
+                              int64_t layers, int64_t num_pages, int64_t page_bytes, void *stream) {
+    if (!used || (n > 0 && (!src || !dst))) return SSM_ERR_INVALID_ARG;
+    if (!aligned(src, 4) || !aligned(dst, 4)) return SSM_ERR_ALIGNMENT;
     DeviceInfo dev;
     const ssm_status_t s = check_pool(pool, n, layers, num_pages, page_bytes, &dev);
     if (s != SSM_OK || n == 0) return s;
-    return from_cuda(ssm::pages::fork(pool, used, src, dst, scratch, n, layers, num_pages, page_bytes,
+    return from_cuda(ssm::pages::fork(pool, used, src, dst, n, layers, num_pages, page_bytes,
                                       dev.num_sms, static_cast<cudaStream_t>(stream)));
 }
 

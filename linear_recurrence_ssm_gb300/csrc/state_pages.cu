@@ -60,37 +60,43 @@ __device__ __forceinline__ uint32_t real_bits(int64_t p0, int64_t num_pages) {
     return n >= kEach ? (1u << kEach) - 1 : n <= 0 ? 0 : (1u << n) - 1;
 }
 
-// dst[k] for every request: the k-th valid one takes the k-th lowest free
-// page.  The free pages' numbers go through `list` (pages entries).
+// dst[k] for every request: the r-th valid one takes the r-th lowest free page.
+// dst holds the free pages in their order first.  The requests are then
+// answered from the last to the first: r <= k, so nothing is overwritten that
+// is still to be read.
 __global__ void __launch_bounds__(kPlan)
-fork_plan_kernel(uint8_t *used, const int32_t *__restrict__ src, int32_t *__restrict__ dst, int32_t *list, int64_t n,
-                 int64_t num_pages) {
+fork_plan_kernel(uint8_t *used, const int32_t *__restrict__ src, int32_t *dst, int64_t n, int64_t num_pages) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ int sums[kPlan / 32];
     int64_t found = 0;
-    for (int64_t s0 = 0; s0 < num_pages; s0 += kPlan * kEach) {
+    for (int64_t s0 = 0; s0 < num_pages && found < n; s0 += kPlan * kEach) {
         const int64_t p0 = s0 + int64_t(threadIdx.x) * kEach;
         uint32_t bits = real_bits(p0, num_pages);
         if (bits) bits &= ~use_bits(used, p0, num_pages);
         int all;
         int64_t at = found + block_prefix(__popc(bits), sums, &all);
-        for (; bits; bits &= bits - 1) list[at++] = int32_t(p0 + __ffs(bits) - 1);
+        for (; bits && at < n; bits &= bits - 1) dst[at++] = int32_t(p0 + __ffs(bits) - 1);
         found += all;
-        if (found >= n) break;      // no request needs a later page
     }
-    __syncthreads();
-    int64_t taken = 0;
-    for (int64_t k0 = 0; k0 < n; k0 += kPlan) {
-        const int64_t k = k0 + threadIdx.x;
+    auto valid = [&](int64_t k) {
         const int s = k < n ? src[k] : -2;
-        const int valid = s == -1 || (s >= 0 && s < num_pages && used[s] != 0);
-        int all;
-        const int64_t at = taken + block_prefix(valid, sums, &all);
-        if (k < n) dst[k] = valid && at < found ? list[at] : -1;
-        taken += all;
+        return int(s == -1 || (s >= 0 && s < num_pages && used[s] != 0));
+    };
+    int mine = 0, all;
+    for (int64_t k = threadIdx.x; k < n; k += kPlan) mine += valid(k);
+    block_prefix(mine, sums, &all);
+    int64_t left = all;       // valid requests up to this chunk's end
+    for (int64_t k0 = (n - 1) / kPlan * kPlan; k0 >= 0; k0 -= kPlan) {
+        const int64_t k = k0 + threadIdx.x;
+        const int v = valid(k), at = block_prefix(v, sums, &all);
+        left -= all;
+        const int page = v && left + at < found ? dst[left + at] : -1;
+        __syncthreads();
+        if (k < n) dst[k] = page;
     }
     __syncthreads();
-    for (int64_t k = threadIdx.x; k < min(taken, found); k += kPlan) used[list[k]] = 1;
+    for (int64_t k = threadIdx.x; k < n; k += kPlan)
+        if (dst[k] >= 0) used[dst[k]] = 1;
 }
 
 // moved[p]: where page p's content is afterwards, -1 for a free page; the
@@ -213,9 +219,9 @@ cudaError_t copy(void *pool, const int32_t *src, const int32_t *dst, int64_t n, 
     return run_copy(pool, src, dst, nullptr, n, n, layers, num_pages, bytes, num_sms, false, st);
 }
 
-cudaError_t fork(void *pool, uint8_t *used, const int32_t *src, int32_t *dst, int32_t *scratch, int64_t n,
-                 int64_t layers, int64_t num_pages, int64_t bytes, int num_sms, cudaStream_t st) {
-    fork_plan_kernel<<<1, kPlan, 0, st>>>(used, src, dst, scratch, n, num_pages);
+cudaError_t fork(void *pool, uint8_t *used, const int32_t *src, int32_t *dst, int64_t n, int64_t layers,
+                 int64_t num_pages, int64_t bytes, int num_sms, cudaStream_t st) {
+    fork_plan_kernel<<<1, kPlan, 0, st>>>(used, src, dst, n, num_pages);
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     return run_copy(pool, src, dst, nullptr, n, n, layers, num_pages, bytes, num_sms, true, st);

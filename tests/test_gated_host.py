@@ -98,24 +98,25 @@ def test_ckpt8_refusals():
 def test_pages_refusals():
     lib = lrs.library()
     sizes = (3, 1, 8, 64)        # n layers pages bytes
-    for i in range(5):           # the last: scratch
-        assert lib.state_pages_fork(*swapped(5, i, None), *sizes, None) == INVALID
+    for i in range(5):           # compact's last: scratch
+        if i < 4:
+            assert lib.state_pages_fork(*swapped(4, i, None), *sizes, None) == INVALID
         if i < 3:
             assert lib.state_pages_copy(*swapped(3, i, None), *sizes, None) == INVALID
         assert lib.state_pages_compact(*swapped(5, i, None), *sizes, None) == INVALID
     for bad in ((-1, 1, 8, 64), (3, 0, 8, 64), (3, 1, 0, 64), (3, 1, 8, 0), (3, 2 ** 40, 8, 2 ** 40)):
-        assert lib.state_pages_fork(P, P, P, P, P, *bad, None) == INVALID
+        assert lib.state_pages_fork(P, P, P, P, *bad, None) == INVALID
         assert lib.state_pages_copy(P, P, P, *bad, None) == INVALID
         assert lib.state_pages_compact(P, P, P, P, P, *bad, None) == INVALID
-    assert lib.state_pages_fork(P, P, P, P, P, 3, 1, 2 ** 24 + 1, 4, None) == UNSUPPORTED
-    assert lib.state_pages_fork(P, P, ODD, P, P, *sizes, None) == ALIGNMENT
+    assert lib.state_pages_fork(P, P, P, P, 3, 1, 2 ** 24 + 1, 4, None) == UNSUPPORTED
+    assert lib.state_pages_fork(P, P, ODD, P, *sizes, None) == ALIGNMENT
     assert lib.state_pages_copy(P, P, ODD, *sizes, None) == ALIGNMENT
     assert lib.state_pages_compact(P, P, ODD, P, P, *sizes, None) == ALIGNMENT
     assert lib.state_pages_free(P, ODD, 3, 8, None) == ALIGNMENT
     assert lib.state_pages_free(None, P, 3, 8, None) == lib.state_pages_free(P, None, 3, 8, None) == INVALID
     # nothing to do: no list is needed
     assert lib.state_pages_free(P, None, 0, 8, None) == END
-    assert lib.state_pages_fork(P, P, None, None, None, 0, 1, 8, 64, None) == END
+    assert lib.state_pages_fork(P, P, None, None, 0, 1, 8, 64, None) == END
     assert lib.state_pages_copy(P, None, None, 0, 1, 8, 64, None) == END
 
 

@@ -135,6 +135,61 @@ def test_compact_without_a_list_and_of_a_dense_pool(cuda_device):
     assert torch.equal(pool, before) and used.cpu().tolist() == [True] * 20 + [False] * 30
 
 
+@pytest.mark.parametrize("n", [1, 1023, 1024, 1025, 3000])
+@pytest.mark.parametrize("free", [0, 700, 5000])
+def test_fork_of_many_requests(cuda_device, n, free):
+    """Lists longer than the planning block, more requests than free pages,
+    and requests that are not valid in between."""
+    pages = 6000
+    g = torch.Generator().manual_seed(n + free)
+    used = torch.ones(pages, dtype=torch.uint8)
+    used[torch.randperm(pages, generator=g)[:free]] = 0
+    src = torch.randint(-3, pages + 3, (n,), generator=g).to(torch.int32)
+    pool = torch.arange(pages, dtype=torch.float32).view(pages, 1).repeat(1, 4)
+    dev_pool, dev_used = pool.to(cuda_device), used.to(cuda_device)
+    dst = lrs.state_pages_fork(dev_pool, dev_used, src.to(cuda_device))
+    want_used, want_dst = gated.pages_fork(used.tolist(), src.tolist())
+    assert dst.cpu().tolist() == want_dst and dev_used.cpu().tolist() == want_used
+    for s, d in zip(src.tolist(), want_dst):
+        if d >= 0:
+            pool[d] = s if s >= 0 else 0
+    assert torch.equal(dev_pool.cpu(), pool)
+
+
+def test_pages_in_a_cuda_graph(cuda_device):
+    """Free, fork and compact captured once and replayed on another pool."""
+    pool, used = _pool(2, 40, (16,)).to(cuda_device), torch.zeros(40, dtype=torch.uint8, device=cuda_device)
+    ended, src = (torch.zeros(3, dtype=torch.int32, device=cuda_device) for _ in range(2))
+    at = torch.zeros(40, dtype=torch.int32, device=cuda_device)
+
+    def work():
+        lrs.state_pages_free(used, ended)
+        dst = lrs.state_pages_fork(pool, used, src, page_dim=1)
+        return dst, lrs.state_pages_compact(pool, used, at, page_dim=1)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dst, moved = work()
+    got = []
+    for replay in (True, False):
+        pool.copy_(_pool(2, 40, (16,), seed=3))
+        used.copy_(torch.arange(40) % 3 == 0)
+        ended.copy_(torch.tensor([3, 9, 39]))
+        src.copy_(torch.tensor([0, -1, 36]))
+        at.copy_(torch.arange(40))
+        if replay:
+            graph.replay()
+        else:
+            dst, moved = work()
+        got.append([t.clone() for t in (pool, used, at, dst, moved)])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 def test_copy(cuda_device):
     pool = _pool(3, 30, (17,))
     src = torch.tensor([4, -1, 29, 30, 7, -2], dtype=torch.int32)
