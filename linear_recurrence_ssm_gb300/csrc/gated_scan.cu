@@ -58,7 +58,6 @@ struct FwdArgs {
     Kept kept;
     int L, ED, cluster;
     int64_t rows;               // Bs * L
-    int pair_stores;            // y's rows take stores of two elements
     float one;                  // 1
 };
 
@@ -136,7 +135,7 @@ __device__ __forceinline__ uint8_t *box_8bit(uint8_t *rows, int k) {
 template <typename T, int W>
 __device__ __forceinline__ void keep_8bit(uint8_t *rows, float *tops, const Kept &kept, int64_t row0, int n_rows,
                                           int e0, int ED, int64_t all_rows, float one) {
-    const int lane = threadIdx.x % 32, e = e0 + 2 * lane;
+    const int lane = threadIdx.x % 32, e = e0 + first_channel<W>();
     auto value = [&](int g) {
         return pair_at<T, W>(rows + g * kPitch<T, W>, shift_of<T, W>(row0 + g % kSteps, ED));
     };
@@ -187,7 +186,7 @@ __device__ __forceinline__ void keep_8bit(uint8_t *rows, float *tops, const Kept
                         uint16_t(__byte_perm(n0, n1, 0x0040));
                 } else {
                     if (j + i < n_rows && e < ED) q[0] = int8_t(n0);
-                    if (j + i < n_rows && e + 1 < ED) q[1] = int8_t(n1);
+                    if (j + i < n_rows && e + kNext<W> < ED) q[kNext<W>] = int8_t(n1);
                     q += ED;
                 }
             }
@@ -203,10 +202,10 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
     Shared<WARPS> &sh = *reinterpret_cast<Shared<WARPS> *>(ring + WARPS * kDepth * kStageBytes<T, W>);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int C = p.cluster, rank = C > 1 ? int(cluster_rank()) : 0;
-    const int e0 = int(blockIdx.x) / C * 64, e = e0 + 2 * lane;
+    const int e0 = int(blockIdx.x) / C * 64, e = e0 + first_channel<W>();
     const int64_t b = blockIdx.y;
     const int turns = (p.L + kTile * C - 1) / (kTile * C);
-    const bool in0 = e < p.ED, in1 = e + 1 < p.ED;
+    const bool in0 = e < p.ED, in1 = e + kNext<W> < p.ED;
 
     uint8_t *mine = ring + warp * kDepth * kStageBytes<T, W>;
     if (threadIdx.x == 0) {
@@ -253,11 +252,12 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
     for (int k = 0; k < (kDepth > 1 ? kDepth - 1 : 1); ++k) fetch(k);
     uint32_t next_cut = RESET ? reset_of(0) : 0;
 
-    const float2 rate = make_float2(in0 ? decay_rate(p.lam[e], p.c) : 0.0f, in1 ? decay_rate(p.lam[e + 1], p.c) : 0.0f);
+    const float2 rate = make_float2(in0 ? decay_rate(p.lam[e], p.c) : 0.0f,
+                                    in1 ? decay_rate(p.lam[e + kNext<W>], p.c) : 0.0f);
     const bool wide = __any_sync(0xffffffffu, !(fmaxf(rate.x, rate.y) < kSlow));
     const float2 root_rate = make_float2(-sqrtf(rate.x), -sqrtf(rate.y));
     float2 carry = both(0.0f);     // the state that enters the cluster's next tiles
-    if (p.h0) carry = make_float2(in0 ? p.h0[b * p.ED + e] : 0.0f, in1 ? p.h0[b * p.ED + e + 1] : 0.0f);
+    if (p.h0) carry = get_pair<W>(p.h0 + b * p.ED + e, in0, in1);
     if (C > 1) cluster_sync();     // every block runs before another writes to its shared memory
 
     for (int turn = 0; turn < turns; ++turn) {
@@ -334,9 +334,7 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
         }
         carry = all;
         if (p.kept.states && n > 0 && t0 % kBlock == 0) {
-            float *k = p.kept.states + (b * ((p.L + kBlock - 1) / kBlock) + t0 / kBlock) * p.ED + e;
-            if (in0) k[0] = h.x;
-            if (in1) k[1] = h.y;
+            put_pair<W>(p.kept.states + (b * ((p.L + kBlock - 1) / kBlock) + t0 / kBlock) * p.ED + e, h, in0, in1);
         }
 
 #pragma unroll
@@ -359,7 +357,7 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
             T *y = p.y + row0 * p.ED + e;
 #pragma unroll
             for (int j = 0; j < kSteps; ++j)
-                if (j < n) put_pair(y + int64_t(j) * p.ED, s[j], p.pair_stores, in0, in1);
+                if (j < n) put_pair<W>(y + int64_t(j) * p.ED, s[j], in0, in1);
         }
         if (kDepth == 1) {
             if (W == 16 && lane == 0) tc::bulk_wait_read0();
@@ -369,10 +367,7 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
         if (p.h_final && t0 < p.L && t0 + kSteps >= p.L) {
 #pragma unroll
             for (int j = 0; j < kSteps; ++j)
-                if (t0 + j == p.L - 1) {
-                    if (in0) p.h_final[b * p.ED + e] = s[j].x;
-                    if (in1) p.h_final[b * p.ED + e + 1] = s[j].y;
-                }
+                if (t0 + j == p.L - 1) put_pair<W>(p.h_final + b * p.ED + e, s[j], in0, in1);
         }
     }
     if (W == 16) {
@@ -403,6 +398,14 @@ gated_step_kernel(const T *__restrict__ x, const T *__restrict__ gr, const T *__
     if (e >= ED) return;
     const bool in1 = PAIRS || e + 1 < ED;
     auto get = [&](const auto *p) { return PAIRS ? get2(p) : make_float2(to_f32(p[0]), in1 ? to_f32(p[1]) : 0.0f); };
+    auto set = [&](auto *p, float2 v) {
+        if (PAIRS) {
+            put2(p, v);
+        } else {
+            put(p, v.x);
+            if (in1) put(p + 1, v.y);
+        }
+    };
     float2 v[kStepRows], r[kStepRows], i[kStepRows], h[kStepRows];
     int64_t at[kStepRows];      // of the state; -1: an idle row, -2: no row
 #pragma unroll
@@ -426,9 +429,9 @@ gated_step_kernel(const T *__restrict__ x, const T *__restrict__ gr, const T *__
             decay2<ACC, true>(mul2(rate, nsigmoid2<ACC>(r[k])), a, em);
             const float2 q = square_less_one(a, em);
             out = fma2(a, h[k], mul2(mul2(q, rsqrt_of_minus<ACC>(q)), mul2(nsigmoid2<ACC>(i[k]), v[k])));
-            put_pair(states + at[k], out, PAIRS, true, in1);
+            set(states + at[k], out);
         }
-        put_pair(y + (b0 + k) * ED + e, out, PAIRS, true, in1);
+        set(y + (b0 + k) * ED + e, out);
     }
 }
 
@@ -441,7 +444,7 @@ template <typename T>
 static Split split_for(int64_t Bs, int64_t L, int64_t ED, int num_sms) {
     static std::atomic<int> slots4[kMaxCluster + 1], slots8[kMaxCluster + 1];
     const double by = sizeof(T) == 4 ? 2.0 : 1.0;
-    const Turn of4{1.5 * by, 0.39 * by, 0.3, 0.05}, of8{2.0 * by, 0.85 * by, 0.3, 0.1};
+    const Turn of4{1.5 * by, 0.39 * by, 0.3, 0.05, 3.0}, of8{2.0 * by, 0.85 * by, 0.3, 0.1, 3.0};
     const Split with4 = best_split(gated_fwd_kernel<T, 16, 4, false, false>, kSmem<T, 16, 4>, 4, 64, of4, Bs, L, ED,
                                    num_sms, slots4);
     const Split with8 = best_split(gated_fwd_kernel<T, 16, 8, false, false>, kSmem<T, 16, 8>, 8, 128, of8, Bs, L, ED,
@@ -485,8 +488,7 @@ cudaError_t launch_fwd(const T *x, const T *gr, const T *gi, const float *lam, f
                        const Kept &kept, int64_t Bs, int64_t L, int64_t ED, int num_sms,
                        cudaStream_t st) {
     auto at = [](const void *q) { return reinterpret_cast<uintptr_t>(q); };
-    FwdArgs<T> p{{x, gr, gi}, lam, c, reset, h0, y, h_final, kept, int(L), int(ED), 1, Bs * L, 0, 1.0f};
-    p.pair_stores = ED % 2 == 0 && at(y) % (2 * sizeof(T)) == 0;
+    FwdArgs<T> p{{x, gr, gi}, lam, c, reset, h0, y, h_final, kept, int(L), int(ED), 1, Bs * L, 1.0f};
     const int W = widest_copy<T>(at(x) | at(gr) | at(gi), ED);
     const bool boxes = W == 16 && at(y) % 16 == 0 &&
                        (!kept.x_q || widest_copy<int8_t>(at(kept.x_q) | at(kept.r_q) | at(kept.i_q), ED) == 16);

@@ -368,26 +368,32 @@ __device__ __forceinline__ uint32_t shift_of(int64_t row, int ED) {
     return W == 8 ? uint32_t(row) * uint32_t(ED) * uint32_t(sizeof(T)) & 15 : 0;
 }
 
+// A lane's two channels: neighbours where rows are stored as boxes (and read
+// in pairs), else lane and lane + 32, so that every load and store of single
+// elements is of neighbours.
+template <int W>
+constexpr int kNext = W == 16 ? 1 : 32;
+template <int W>
+__device__ __forceinline__ int first_channel() {
+    const int lane = threadIdx.x % 32;
+    return W == 16 ? 2 * lane : lane;
+}
+
 // The lane's two channels of a copied row (int8: the integers).
 template <typename T, int W>
 __device__ __forceinline__ float2 pair_at(const uint8_t *row, uint32_t shift) {
-    const int lane = threadIdx.x % 32;
+    // in bytes and in 32 bits: as T * plus an unsigned index the bf16 gradients took 2 % more
+    const T *p = reinterpret_cast<const T *>(row + shift + int(sizeof(T)) * first_channel<W>());
     if constexpr (sizeof(T) == 4) {
-        if (W != 8) return *reinterpret_cast<const float2 *>(row + 8 * lane);
-        const float *p = reinterpret_cast<const float *>(row + shift + 8 * lane);
-        return make_float2(p[0], p[1]);
+        return W == 16 ? *reinterpret_cast<const float2 *>(p) : make_float2(p[0], p[32]);
     } else if constexpr (sizeof(T) == 2) {
-        const uint32_t *p = reinterpret_cast<const uint32_t *>(row + (shift & 12) + 4 * lane);
-        const uint32_t w = W == 8 ? __funnelshift_r(p[0], p[1], 8 * (shift & 2)) : p[0];
+        if (W != 16) return make_float2(to_f32(p[0]), to_f32(p[32]));
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
         return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     } else {
-        uint32_t w;
-        if (W == 8)
-            w = row[2 * lane + shift] | row[2 * lane + shift + 1] << 8;
-        else
-            w = *reinterpret_cast<const uint16_t *>(row + 2 * lane);
         // 2^23 + (q + 128) as a bit pattern, less 2^23 + 128: exact
-        w ^= 0x8080u;
+        const uint8_t *b = reinterpret_cast<const uint8_t *>(p);
+        const uint32_t w = (W == 16 ? *reinterpret_cast<const uint16_t *>(b) : uint32_t(b[0]) | uint32_t(b[32]) << 8) ^ 0x8080u;
         return add2(make_float2(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440)),
                                 __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441))),
                     both(-8388736.0f));
@@ -398,15 +404,16 @@ __device__ __forceinline__ void put2(float *p, float2 v) { *reinterpret_cast<flo
 __device__ __forceinline__ void put2(__nv_bfloat16 *p, float2 v) {
     *reinterpret_cast<__nv_bfloat162 *>(p) = __float22bfloat162_rn(v);
 }
-// A lane's two channels of one row, as one store where `pairs`.
-template <typename T>
-__device__ __forceinline__ void put_pair(T *p, float2 v, bool pairs, bool in0, bool in1) {
-    if (pairs) {
-        if (in0) put2(p, v);
-    } else {
-        if (in0) put(p, v.x);
-        if (in1) put(p + 1, v.y);
-    }
+// A lane's two channels of one row, element by element.
+template <int W, typename T>
+__device__ __forceinline__ void put_pair(T *p, float2 v, bool in0, bool in1) {
+    if (in0) put(p, v.x);
+    if (in1) put(p + kNext<W>, v.y);
+}
+// The two channels of a vector over the channels.
+template <int W>
+__device__ __forceinline__ float2 get_pair(const float *p, bool in0, bool in1) {
+    return make_float2(in0 ? p[0] : 0.0f, in1 ? p[kNext<W>] : 0.0f);
 }
 
 // ---- tensor copies of boxes of STEPS rows x 64 channels --------------------------
@@ -481,11 +488,10 @@ inline cudaError_t start_clusters(void (*kern)(Args...), int smem, const Split &
 
 // What a turn (one tile of a block) takes, in microseconds: alone on its SM,
 // for each other block there, for an exchange with a cluster of two and for
-// each further block of the cluster.  Measured; a block's start takes kStartUs.
+// each further block of the cluster; and what a block's start takes.  Measured.
 struct Turn {
-    double alone, shared, exchange, hop;
+    double alone, shared, exchange, hop, start;
 };
-constexpr double kStartUs = 3.0;
 
 // Chooses C for one kernel (blocks of `warps` warps, `tile` steps) by the time
 // that its rounds of blocks would take.  cache: blocks that run at a time by C,
@@ -519,7 +525,7 @@ inline Split best_split(void (*kern)(Args...), int smem, int warps, int tile, co
         };
         const int64_t blocks = chains * C, full = blocks / slots, rest = blocks % slots;
         const double us = double((tiles + C - 1) / C) * (double(full) * turn(slots) + (rest ? turn(rest) : 0.0)) +
-                          kStartUs * double(full + (rest ? 1 : 0));
+                          t.start * double(full + (rest ? 1 : 0));
         if (best.warps == 0 || us < best.us) best.warps = warps, best.cluster = C, best.us = us;
     }
     return best;

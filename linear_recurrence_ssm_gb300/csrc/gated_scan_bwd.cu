@@ -52,7 +52,6 @@ struct BwdArgs {
     float *part, *dh0;          // part (Bs * cluster, ED): sums of G
     int L, ED, cluster;
     int64_t rows;               // Bs * L
-    int pair_stores;
 };
 
 // One stage of a warp's ring: rows of x, gate_r, gate_i (of type K: T, or
@@ -157,9 +156,9 @@ __device__ __forceinline__ void gradients(const BwdArgs<T> &p, const uint8_t *st
             put2(o + Stage<T, K, W>::kOut / sizeof(T), dr);
             put2(o + 2 * Stage<T, K, W>::kOut / sizeof(T), di);
         } else {
-            put_pair(p.dx + at + int64_t(j) * p.ED, dx, p.pair_stores, in0, in1);
-            put_pair(p.dr + at + int64_t(j) * p.ED, dr, p.pair_stores, in0, in1);
-            put_pair(p.di + at + int64_t(j) * p.ED, di, p.pair_stores, in0, in1);
+            put_pair<W>(p.dx + at + int64_t(j) * p.ED, dx, in0, in1);
+            put_pair<W>(p.dr + at + int64_t(j) * p.ED, dr, in0, in1);
+            put_pair<W>(p.di + at + int64_t(j) * p.ED, di, in0, in1);
         }
         sum = add2(sum, G);
         u = mul2(a[j], g);
@@ -176,10 +175,10 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
     Shared &sh = *reinterpret_cast<Shared *>(ring + kWarps * S::kWarpBytes);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int C = p.cluster, rank = C > 1 ? int(cluster_rank()) : 0;
-    const int e0 = int(blockIdx.x) / C * 64, e = e0 + 2 * lane;
+    const int e0 = int(blockIdx.x) / C * 64, e = e0 + first_channel<W>();
     const int64_t b = blockIdx.y;
     const int tiles = (p.L + kBlock - 1) / kBlock, turns = (tiles + C - 1) / C;
-    const bool in0 = e < p.ED, in1 = e + 1 < p.ED;
+    const bool in0 = e < p.ED, in1 = e + kNext<W> < p.ED;
 
     uint8_t *mine = ring + warp * S::kWarpBytes;
     if (threadIdx.x == 0) {
@@ -238,8 +237,7 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
     auto kept_of = [&](int turn) {
         const int tile = turn * C + rank;
         if (turn < 0 || tile >= tiles || warp != 1) return both(0.0f);      // warp 1 folds the states
-        const float *k = p.kept.states + (b * tiles + tile) * p.ED + e;
-        return make_float2(in0 ? k[0] : 0.0f, in1 ? k[1] : 0.0f);
+        return get_pair<W>(p.kept.states + (b * tiles + tile) * p.ED + e, in0, in1);
     };
 #pragma unroll
     for (int k = 0; k < (kDepth > 1 ? kDepth - 1 : 1); ++k) fetch(turns - 1 - k);
@@ -247,10 +245,11 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
     float2 next_h = kept_of(turns - 1);
     if (C > 1) cluster_sync();     // every block runs before another writes to its shared memory
 
-    const float2 rate = make_float2(in0 ? decay_rate(p.lam[e], p.c) : 0.0f, in1 ? decay_rate(p.lam[e + 1], p.c) : 0.0f);
+    const float2 rate = make_float2(in0 ? decay_rate(p.lam[e], p.c) : 0.0f,
+                                    in1 ? decay_rate(p.lam[e + kNext<W>], p.c) : 0.0f);
     const bool wide = __any_sync(0xffffffffu, !(fmaxf(rate.x, rate.y) < kSlow));
     float2 carry = both(0.0f), sum = both(0.0f);     // the adjoint that enters the cluster's next tiles from behind
-    if (p.dh_final) carry = make_float2(in0 ? p.dh_final[b * p.ED + e] : 0.0f, in1 ? p.dh_final[b * p.ED + e + 1] : 0.0f);
+    if (p.dh_final) carry = get_pair<W>(p.dh_final + b * p.ED + e, in0, in1);
 
     uint32_t phases = 0;           // bit k: the parity that stage k's next copies complete
 
@@ -367,10 +366,7 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
         if (lane == 0) tc::bulk_wait_read0();
     }
     cp_async_wait<0>();
-    if (p.dh0 && warp == 0 && rank == 0) {
-        if (in0) p.dh0[b * p.ED + e] = carry.x;
-        if (in1) p.dh0[b * p.ED + e + 1] = carry.y;
-    }
+    if (p.dh0 && warp == 0 && rank == 0) put_pair<W>(p.dh0 + b * p.ED + e, carry, in0, in1);
     __syncthreads();
     float2 *sums = reinterpret_cast<float2 *>(&sh.warp[0][0]);
     sums[warp * 32 + lane] = sum;
@@ -378,9 +374,7 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
     if (warp == 0) {
         float2 s = both(0.0f);
         for (int k = 0; k < kWarps; ++k) s = add2(s, sums[k * 32 + lane]);
-        float *part = p.part + (b * C + rank) * p.ED + e;
-        if (in0) part[0] = s.x;
-        if (in1) part[1] = s.y;
+        put_pair<W>(p.part + (b * C + rank) * p.ED + e, s, in0, in1);
     }
     if (C > 1) cluster_sync();     // no block leaves while another may still write to it
     if (aborted(&sh.ex.abort)) linger();
@@ -416,8 +410,7 @@ static cudaError_t start(BwdArgs<T> p, const BwdMaps &maps, int64_t Bs, int num_
     constexpr int kSmem = kWarps * Stage<T, K, W>::kWarpBytes + int(sizeof(Shared));
     auto kern = gated_bwd_kernel<T, K, W, RESET>;
     static std::atomic<int> slots[kMaxCluster + 1];
-    const double by = sizeof(T) == 4 ? 2.0 : 1.0;
-    const Turn turn{1.95 * by, 0.92 * by, 0.45, 0.1};
+    const Turn turn = sizeof(T) == 4 ? Turn{3.9, 0.85, 1.3, 0.2, 8.0} : Turn{1.95, 0.92, 0.45, 0.1, 3.0};
     Split how = best_split(kern, kSmem, kWarps, kBlock, turn, Bs, p.L, p.ED, num_sms, slots);
     if (how.warps == 0) return cudaErrorInvalidConfiguration;
     *cluster = p.cluster = how.cluster;
@@ -455,9 +448,8 @@ cudaError_t launch(const T *x, const T *gr, const T *gi, const float *lam, float
                    int64_t ED, int num_sms, cudaStream_t st) {
     auto at = [](const void *q) { return reinterpret_cast<uintptr_t>(q); };
     BwdArgs<T> p{{x, gr, gi}, lam, c, reset, dy, dh_final, kept, dx, dr, di, scratch, dh0,
-                 int(L), int(ED), 1, Bs * L, 0};
+                 int(L), int(ED), 1, Bs * L};
     int cluster = 1;
-    p.pair_stores = ED % 2 == 0 && (at(dx) | at(dr) | at(di)) % (2 * sizeof(T)) == 0;
     int W = widest_copy<T>(at(dy), ED);
     if (W == 16 && (at(dx) | at(dr) | at(di)) % 16 != 0) W = 8;
     cudaError_t err;
