@@ -56,9 +56,10 @@ struct FwdArgs {
     T *y;
     float *h_final;
     Kept kept;
-    int L, ED, cluster;
+    int L, ED;
     int64_t rows;               // Bs * L
     float one;                  // 1
+    Share share;
 };
 
 // Boxes of 64 channels x kSteps rows of x, gate_r, gate_i, y and the three
@@ -201,13 +202,14 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
     extern __shared__ __align__(128) uint8_t ring[];
     Shared<WARPS> &sh = *reinterpret_cast<Shared<WARPS> *>(ring + WARPS * kDepth * kStageBytes<T, W>);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int C = p.cluster, rank = C > 1 ? int(cluster_rank()) : 0;
+    const int C = p.share.cluster, rank = C > 1 ? int(cluster_rank()) : 0;
     const int e0 = int(blockIdx.x) / C * 64, e = e0 + first_channel<W>();
-    const int64_t b = blockIdx.y;
+    const int64_t b = p.share.first + blockIdx.y;
     const int turns = (p.L + kTile * C - 1) / (kTile * C);
     const bool in0 = e < p.ED, in1 = e + kNext<W> < p.ED;
 
     uint8_t *mine = ring + warp * kDepth * kStageBytes<T, W>;
+    if (p.share.order == 1) let_next_start();
     if (threadIdx.x == 0) {
         if (C > 1) sh.ex.init();
         sh.ex.abort = 0;
@@ -377,6 +379,7 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
     }
     if (C > 1) cluster_sync();     // no block leaves while another may still write to it
     if (aborted(&sh.ex.abort)) linger();
+    wait_for_first(p.share);
 }
 
 // One token.  A thread takes two channels of kStepRows rows, so that a
@@ -453,15 +456,12 @@ static Split split_for(int64_t Bs, int64_t L, int64_t ED, int num_sms) {
 }
 
 template <typename T, int W, bool RESET, bool SAVE8>
-static cudaError_t start_fwd(FwdArgs<T> p, const FwdMaps &maps, int64_t Bs, int num_sms, cudaStream_t st) {
-    Split how = split_for<T>(Bs, p.L, p.ED, num_sms);
+static cudaError_t start_fwd(const FwdArgs<T> &p, const FwdMaps &maps, int64_t Bs, int num_sms, cudaStream_t st) {
+    const Split how = split_for<T>(Bs, p.L, p.ED, num_sms);
     if (how.warps == 0) return cudaErrorInvalidConfiguration;
-    p.cluster = how.cluster;
     if (how.warps == 8)
-        return start_clusters(gated_fwd_kernel<T, W, 8, RESET, SAVE8>, kSmem<T, W, 8>, how, p.ED, Bs, st, nullptr, &p,
-                              &maps);
-    return start_clusters(gated_fwd_kernel<T, W, 4, RESET, SAVE8>, kSmem<T, W, 4>, how, p.ED, Bs, st, nullptr, &p,
-                          &maps);
+        return start_split(gated_fwd_kernel<T, W, 8, RESET, SAVE8>, kSmem<T, W, 8>, how, Bs, p.ED, p, maps, st);
+    return start_split(gated_fwd_kernel<T, W, 4, RESET, SAVE8>, kSmem<T, W, 4>, how, Bs, p.ED, p, maps, st);
 }
 
 template <typename T, int W>
@@ -488,7 +488,7 @@ cudaError_t launch_fwd(const T *x, const T *gr, const T *gi, const float *lam, f
                        const Kept &kept, int64_t Bs, int64_t L, int64_t ED, int num_sms,
                        cudaStream_t st) {
     auto at = [](const void *q) { return reinterpret_cast<uintptr_t>(q); };
-    FwdArgs<T> p{{x, gr, gi}, lam, c, reset, h0, y, h_final, kept, int(L), int(ED), 1, Bs * L, 1.0f};
+    FwdArgs<T> p{{x, gr, gi}, lam, c, reset, h0, y, h_final, kept, int(L), int(ED), Bs * L, 1.0f, {}};
     const int W = widest_copy<T>(at(x) | at(gr) | at(gi), ED);
     const bool boxes = W == 16 && at(y) % 16 == 0 &&
                        (!kept.x_q || widest_copy<int8_t>(at(kept.x_q) | at(kept.r_q) | at(kept.i_q), ED) == 16);

@@ -45,7 +45,7 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 16, kRest = 4;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 inline int exchange_bytes(int cluster) { return 2 * (cluster - 1) * 32 * 16; }
 
@@ -451,39 +451,74 @@ __device__ __forceinline__ void tma_store_3d(const void *tmap, const void *src, 
                  : "memory");
 }
 
-// How a kernel's blocks share the time axis: blocks of `warps` warps, each
-// with 64 channels of a sequence and one of its C shares, C blocks a cluster.
+// How a kernel's blocks share the work: blocks of `warps` warps, each with 64
+// channels of a sequence (a chain) and one of its C shares of the time axis, C
+// blocks a cluster.  Sequences behind the first `first` have clusters of
+// `rest_cluster` blocks, in a launch of their own (0: there are none).
 struct Split {
-    int warps = 0, cluster = 1;
+    int warps = 0, cluster = 1, rest_cluster = 0;
+    int64_t first = 0;
     double us = 0.0;
 };
 
-template <typename... Args>
-inline cudaError_t start_clusters(void (*kern)(Args...), int smem, const Split &how, int64_t ED, int64_t Bs,
-                                  cudaStream_t st, int *resident, const std::decay_t<Args> *...args) {
-    const int C = how.cluster;
+// Which sequences a launch has, in its arguments.
+struct Share {
+    int cluster = 1;      // blocks a cluster
+    int first = 0;        // its first sequence
+    int sums = 0;         // blocks' sums before its first one's
+    int order = 0;        // 1: a launch for the rest follows; 2: it is that one
+};
+// At a block's start: the next launch of this pass may begin once every block
+// of this one has.  The rest needs no result of the first launch.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// At a block's end: what comes after the rest comes after the first launch, too.
+__device__ __forceinline__ void wait_for_first(const Share &s) {
+    if (s.order == 2) wait_for_launch();
+}
+
+// Starts `seqs` sequences in clusters of args.share.cluster blocks.  With
+// `resident`: asks for the blocks that run at a time instead.
+template <typename Args, typename Maps>
+inline cudaError_t start_clusters(void (*kern)(Args, Maps), int smem, int warps, int64_t seqs, int64_t ED, const Args &args,
+                                  const Maps &maps, cudaStream_t st, int *resident = nullptr) {
+    const int C = args.share.cluster;
     smem += exchange_bytes(C);
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err == cudaSuccess && C > 8)
         err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned((ED + 63) / 64 * C), unsigned(Bs));
-    cfg.blockDim = dim3(32 * how.warps);
+    cfg.gridDim = dim3(unsigned((ED + 63) / 64 * C), unsigned(seqs));
+    cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim = {unsigned(C), 1, 1};
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (resident) {      // blocks that run at a time, and no launch
+    cfg.numAttrs = args.share.order == 2 ? 2 : 1;
+    if (resident) {
         int clusters = 0;
         err = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
         *resident = clusters * C;
         return err;
     }
-    return cudaLaunchKernelEx(&cfg, kern, *args...);
+    return cudaLaunchKernelEx(&cfg, kern, args, maps);
+}
+
+// One pass over all sequences.
+template <typename Args, typename Maps>
+inline cudaError_t start_split(void (*kern)(Args, Maps), int smem, const Split &how, int64_t Bs, int64_t ED, Args args,
+                               const Maps &maps, cudaStream_t st) {
+    const bool rest = how.rest_cluster != 0;
+    args.share = {how.cluster, 0, 0, rest ? 1 : 0};
+    const cudaError_t err = start_clusters(kern, smem, how.warps, how.first, ED, args, maps, st);
+    if (err != cudaSuccess || !rest) return err;
+    args.share = {how.rest_cluster, int(how.first), int(how.first) * how.cluster, 2};
+    return start_clusters(kern, smem, how.warps, Bs - how.first, ED, args, maps, st);
 }
 
 // What a turn (one tile of a block) takes, in microseconds: alone on its SM,
@@ -494,39 +529,60 @@ struct Turn {
 };
 
 // Chooses C for one kernel (blocks of `warps` warps, `tile` steps) by the time
-// that its rounds of blocks would take.  cache: blocks that run at a time by C,
-// asked for once.
-template <typename... Args>
-inline Split best_split(void (*kern)(Args...), int smem, int warps, int tile, const Turn &t,
+// that its rounds of blocks would take.  A last round that a few sequences
+// would have for themselves goes to larger clusters, so that it is as short as
+// the GPU is empty; of kRest blocks at most, since a cluster waits until all
+// its places are free (gradients of Bs=32 L=2048 ED=1536 274 us, with the last
+// round by 4 blocks 267, by 6 286, by 8 283).  cache: blocks that run at a time by C, asked for once.
+template <typename Args, typename Maps>
+inline Split best_split(void (*kern)(Args, Maps), int smem, int warps, int tile, const Turn &t,
                         int64_t Bs, int64_t L, int64_t ED, int num_sms, std::atomic<int> *cache) {
-    Split best;
-    const int64_t chains = (ED + 63) / 64 * Bs, tiles = (L + tile - 1) / tile;
-    for (int C = 1; C <= kMaxCluster && C <= tiles; ++C) {
-        int slots = cache[C].load(std::memory_order_relaxed);
-        if (slots == 0) {
-            Split one;
-            one.warps = warps;
-            one.cluster = C;
-            slots = -1;
-            if (start_clusters(kern, smem, one, ED, Bs, nullptr, &slots,
-                               static_cast<const std::decay_t<Args> *>(nullptr)...) != cudaSuccess) {
+    const int64_t groups = (ED + 63) / 64, tiles = (L + tile - 1) / tile;
+    const int widest = int(std::min<int64_t>(kMaxCluster, tiles));
+    int slots[kMaxCluster + 1];
+    for (int C = 1; C <= widest; ++C) {
+        slots[C] = cache[C].load(std::memory_order_relaxed);
+        if (slots[C] == 0) {
+            Args one{};
+            one.share.cluster = C;
+            if (start_clusters(kern, smem, warps, 1, ED, one, Maps{}, nullptr, &slots[C]) != cudaSuccess) {
                 cudaGetLastError();
-                slots = -1;
+                slots[C] = -1;
             }
             // one cluster less than the driver counts: when all it counts
             // were asked for (40 of 7), some waited for a second round
-            slots = slots > C ? slots - C : slots > 0 ? slots : -1;
-            cache[C].store(slots, std::memory_order_relaxed);
+            slots[C] = slots[C] > C ? slots[C] - C : slots[C] > 0 ? slots[C] : -1;
+            cache[C].store(slots[C], std::memory_order_relaxed);
         }
-        if (slots < C) continue;
-        auto turn = [&](int64_t blocks) {
-            const double others = double((blocks + num_sms - 1) / num_sms - 1);
-            return t.alone + others * t.shared + (C > 1 ? t.exchange + (C - 1) * t.hop : 0.0);
-        };
-        const int64_t blocks = chains * C, full = blocks / slots, rest = blocks % slots;
-        const double us = double((tiles + C - 1) / C) * (double(full) * turn(slots) + (rest ? turn(rest) : 0.0)) +
-                          t.start * double(full + (rest ? 1 : 0));
-        if (best.warps == 0 || us < best.us) best.warps = warps, best.cluster = C, best.us = us;
+    }
+    // one round of `blocks` blocks
+    auto round = [&](int C, int64_t blocks) {
+        if (blocks == 0) return 0.0;
+        const double others = double((blocks + num_sms - 1) / num_sms - 1);
+        const double turn = t.alone + others * t.shared + (C > 1 ? t.exchange + (C - 1) * t.hop : 0.0);
+        return double((tiles + C - 1) / C) * turn + t.start;
+    };
+    auto launch = [&](int64_t seqs, int most) {
+        Split best;
+        for (int C = 1; C <= most; ++C) {
+            if (slots[C] < C) continue;
+            const int64_t blocks = seqs * groups * C;
+            const double us = double(blocks / slots[C]) * round(C, slots[C]) + round(C, blocks % slots[C]);
+            if (best.warps == 0 || us < best.us) best.warps = warps, best.cluster = C, best.us = us;
+        }
+        best.first = seqs;
+        return best;
+    };
+    Split best = launch(Bs, widest);
+    for (int C = 1; C <= widest && best.warps != 0; ++C) {
+        if (slots[C] < C) continue;
+        const int64_t rounds = Bs * groups * C / slots[C], first = rounds * slots[C] / (C * groups);
+        if (first == 0 || first == Bs) continue;
+        const double whole = double(rounds) * round(C, slots[C]);
+        if (whole >= best.us) continue;
+        const Split rest = launch(Bs - first, std::min(widest, kRest));
+        const double us = whole + rest.us;
+        if (us < best.us) best.cluster = C, best.first = first, best.rest_cluster = rest.cluster, best.us = us;
     }
     return best;
 }

@@ -49,9 +49,10 @@ struct BwdArgs {
     const float *dh_final;
     Kept kept;
     T *dx, *dr, *di;
-    float *part, *dh0;          // part (Bs * cluster, ED): sums of G
-    int L, ED, cluster;
+    float *part, *dh0;          // part (sequences' clusters' blocks, ED): sums of G
+    int L, ED;
     int64_t rows;               // Bs * L
+    Share share;
 };
 
 // One stage of a warp's ring: rows of x, gate_r, gate_i (of type K: T, or
@@ -174,13 +175,14 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
     extern __shared__ __align__(128) uint8_t ring[];
     Shared &sh = *reinterpret_cast<Shared *>(ring + kWarps * S::kWarpBytes);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int C = p.cluster, rank = C > 1 ? int(cluster_rank()) : 0;
+    const int C = p.share.cluster, rank = C > 1 ? int(cluster_rank()) : 0;
     const int e0 = int(blockIdx.x) / C * 64, e = e0 + first_channel<W>();
-    const int64_t b = blockIdx.y;
+    const int64_t b = p.share.first + blockIdx.y;
     const int tiles = (p.L + kBlock - 1) / kBlock, turns = (tiles + C - 1) / C;
     const bool in0 = e < p.ED, in1 = e + kNext<W> < p.ED;
 
     uint8_t *mine = ring + warp * S::kWarpBytes;
+    let_next_start();      // the rest, or dlam_kernel
     if (threadIdx.x == 0) {
         if (C > 1) sh.ex.init();
         sh.ex.abort = 0;
@@ -374,10 +376,11 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
     if (warp == 0) {
         float2 s = both(0.0f);
         for (int k = 0; k < kWarps; ++k) s = add2(s, sums[k * 32 + lane]);
-        put_pair<W>(p.part + (b * C + rank) * p.ED + e, s, in0, in1);
+        put_pair<W>(p.part + (p.share.sums + int64_t(blockIdx.y) * C + rank) * p.ED + e, s, in0, in1);
     }
     if (C > 1) cluster_sync();     // no block leaves while another may still write to it
     if (aborted(&sh.ex.abort)) linger();
+    wait_for_first(p.share);
 }
 
 // Read and clear this unit's device error word (host side, synchronous).
@@ -399,26 +402,28 @@ dlam_kernel(const float *__restrict__ part, const float *__restrict__ lam, float
             int64_t n, int64_t ED) {
     const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
     if (e >= ED) return;
+    // dla/dlam over la, with la's sign in G
+    const float factor = dlog_decay_over(lam[e]);
+    wait_for_launch();
     float s = 0.0f;
     for (int64_t b = 0; b < n; ++b) s += part[b * ED + e];
-    // dla/dlam over la, with la's sign in G
-    dlam[e] = s * dlog_decay_over(lam[e]);
+    dlam[e] = s * factor;
 }
 
 template <typename T, typename K, int W, bool RESET>
-static cudaError_t start(BwdArgs<T> p, const BwdMaps &maps, int64_t Bs, int num_sms, int *cluster, cudaStream_t st) {
+static cudaError_t start(const BwdArgs<T> &p, const BwdMaps &maps, int64_t Bs, int num_sms, int64_t *sums, cudaStream_t st) {
     constexpr int kSmem = kWarps * Stage<T, K, W>::kWarpBytes + int(sizeof(Shared));
     auto kern = gated_bwd_kernel<T, K, W, RESET>;
     static std::atomic<int> slots[kMaxCluster + 1];
     const Turn turn = sizeof(T) == 4 ? Turn{3.9, 0.85, 1.3, 0.2, 8.0} : Turn{1.95, 0.92, 0.45, 0.1, 3.0};
-    Split how = best_split(kern, kSmem, kWarps, kBlock, turn, Bs, p.L, p.ED, num_sms, slots);
+    const Split how = best_split(kern, kSmem, kWarps, kBlock, turn, Bs, p.L, p.ED, num_sms, slots);
     if (how.warps == 0) return cudaErrorInvalidConfiguration;
-    *cluster = p.cluster = how.cluster;
-    return start_clusters(kern, kSmem, how, p.ED, Bs, st, nullptr, &p, &maps);
+    *sums = how.first * how.cluster + (Bs - how.first) * how.rest_cluster;
+    return start_split(kern, kSmem, how, Bs, p.ED, p, maps, st);
 }
 
 template <typename T, typename K>
-static cudaError_t start(const BwdArgs<T> &p, int W, int64_t Bs, int num_sms, int *cluster, cudaStream_t st) {
+static cudaError_t start(const BwdArgs<T> &p, int W, int64_t Bs, int num_sms, int64_t *sums, cudaStream_t st) {
     BwdMaps maps{};
     if (W == 16) {
         const K *in[3];
@@ -432,13 +437,13 @@ static cudaError_t start(const BwdArgs<T> &p, int W, int64_t Bs, int num_sms, in
                 !rows_map(&maps.out[k], out[k], Bs, p.L, p.ED, kSteps))
                 return cudaErrorInvalidValue;
         if (!rows_map(&maps.dy, p.dy, Bs, p.L, p.ED, kSteps)) return cudaErrorInvalidValue;
-        return p.reset ? start<T, K, 16, true>(p, maps, Bs, num_sms, cluster, st)
-                       : start<T, K, 16, false>(p, maps, Bs, num_sms, cluster, st);
+        return p.reset ? start<T, K, 16, true>(p, maps, Bs, num_sms, sums, st)
+                       : start<T, K, 16, false>(p, maps, Bs, num_sms, sums, st);
     }
-    if (W == 8) return p.reset ? start<T, K, 8, true>(p, maps, Bs, num_sms, cluster, st)
-                               : start<T, K, 8, false>(p, maps, Bs, num_sms, cluster, st);
-    return p.reset ? start<T, K, 1, true>(p, maps, Bs, num_sms, cluster, st)
-                       : start<T, K, 1, false>(p, maps, Bs, num_sms, cluster, st);
+    if (W == 8) return p.reset ? start<T, K, 8, true>(p, maps, Bs, num_sms, sums, st)
+                               : start<T, K, 8, false>(p, maps, Bs, num_sms, sums, st);
+    return p.reset ? start<T, K, 1, true>(p, maps, Bs, num_sms, sums, st)
+                       : start<T, K, 1, false>(p, maps, Bs, num_sms, sums, st);
 }
 
 template <typename T>
@@ -448,20 +453,28 @@ cudaError_t launch(const T *x, const T *gr, const T *gi, const float *lam, float
                    int64_t ED, int num_sms, cudaStream_t st) {
     auto at = [](const void *q) { return reinterpret_cast<uintptr_t>(q); };
     BwdArgs<T> p{{x, gr, gi}, lam, c, reset, dy, dh_final, kept, dx, dr, di, scratch, dh0,
-                 int(L), int(ED), 1, Bs * L};
-    int cluster = 1;
+                 int(L), int(ED), Bs * L, {}};
+    int64_t sums = 0;
     int W = widest_copy<T>(at(dy), ED);
     if (W == 16 && (at(dx) | at(dr) | at(di)) % 16 != 0) W = 8;
     cudaError_t err;
     if (kept.x_q)
         err = start<T, int8_t>(p, std::min(W, widest_copy<int8_t>(at(kept.x_q) | at(kept.r_q) | at(kept.i_q), ED)), Bs, num_sms,
-                               &cluster, st);
+                               &sums, st);
     else
         err = start<T, T>(p, std::min(W, widest_copy<T>(at(x) | at(gr) | at(gi), ED)), Bs, num_sms,
-                               &cluster, st);
+                               &sums, st);
     if (err == cudaSuccess) {
-        dlam_kernel<<<unsigned((ED + 255) / 256), 256, 0, st>>>(p.part, lam, dlam, Bs * cluster, ED);
-        err = cudaGetLastError();
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(unsigned((ED + 255) / 256));
+        cfg.blockDim = dim3(256);
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        err = cudaLaunchKernelEx(&cfg, dlam_kernel, static_cast<const float *>(p.part), lam, dlam, sums, ED);
     }
     return err;
 }

@@ -258,6 +258,25 @@ def test_clusters_and_rows_off_16_bytes(cuda_device, Bs, L, ED, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Bs,L,ED", [(16, 130, 2560), (9, 200, 5001)])
+def test_more_channels_than_fit_at_a_time(cuda_device, Bs, L, ED, dtype):
+    """More than a round of blocks: the last sequences get clusters of their
+    own size, in a second launch."""
+    inp, reset, more = case(Bs, L, ED, dtype, seed=Bs + ED, resets=True)
+    y, hf, saved = check_fwd(inp, reset, more["h0"], dtype, cuda_device, save="8bit")
+    y2, hf2, _ = check_fwd(inp, reset, more["h0"], dtype, cuda_device)
+    assert torch.equal(y, y2) and torch.equal(hf, hf2)
+    values = {}
+    for k, q in (("x", "x"), ("gate_r", "r"), ("gate_i", "i")):
+        rq, rs = gated.ckpt8(inp[k])
+        assert np.array_equal(saved[q + "_q"].cpu().numpy(), rq)
+        assert np.array_equal(saved[q + "_s"].cpu().numpy(), rs)
+        values[k] = gated.ckpt8_values(rq, rs)
+    check_bwd(inp, reset, more, dtype, cuda_device, saved, values)
+    check_bwd(inp, reset, more, dtype, cuda_device, {"states": saved["states"]})
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("L,ED", [(70, 128), (700, 64)])
 def test_fast_decays(cuda_device, L, ED, dtype):
     """Decays from almost 1 to below 2^-100 in one block of channels."""
