@@ -123,36 +123,100 @@ __device__ __forceinline__ void coefficients(const uint8_t *rows, int64_t row0, 
     }
 }
 
-// Keeps a warp's rows of x, gate_r and gate_i in 8 bits.  The tops of its 3
-// kSteps groups go through `tops`, so that one lane divides by each, once.
-// The bytes go to global memory, or (W = 16) to boxes of 64 a row in the place
-// of rows that are not needed any more: gate_i's and gate_r's in gate_i's
-// rows, x's in gate_r's (x's own rows will hold y).
-template <typename T, int W>
+// The largest of N values over lanes that differ in the bits below 2 * BIT, to
+// three values a lane: while there are more, a lane passes half of them on and
+// keeps the other half, from `first` on.  u16x2 or u32, by type.
+template <typename T>
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    if (sizeof(T) == 4) return max(a, b);
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <typename T, int N, int BIT>
+__device__ __forceinline__ void largest(uint32_t *v, int &first) {
+    if constexpr (BIT > 0) {
+        constexpr int kKeep = N > 3 ? N / 2 : N;
+        const bool high = threadIdx.x & BIT;
+#pragma unroll
+        for (int n = 0; n < kKeep; ++n) {
+            const uint32_t own = N > 3 && high ? v[n + kKeep] : v[n], pass = N > 3 && !high ? v[n + kKeep] : v[n];
+            v[n] = larger<T>(own, __shfl_xor_sync(0xffffffffu, pass, BIT));
+        }
+        if (N > 3 && high) first += kKeep;
+        largest<T, kKeep, BIT / 2>(v, first);
+    }
+}
+
+// Where the bytes of x, gate_r and gate_i (k = 0, 1, 2) wait as boxes of 64 a
+// row, in the place of rows that are not needed any more: gate_i's and
+// gate_r's in gate_i's rows, x's in gate_r's (x's own rows will hold y).
+template <typename T>
 __device__ __forceinline__ uint8_t *box_8bit(uint8_t *rows, int k) {
-    constexpr int kIn = kSteps * kPitch<T, W>;
+    constexpr int kIn = kSteps * kPitch<T, 16>;
     return k == 0 ? rows + kIn : k == 1 ? rows + 2 * kIn + 64 * kSteps : rows + 2 * kIn;
 }
+
+// Keeps a warp's rows of x, gate_r and gate_i in 8 bits.  The tops of its 3
+// kSteps groups go through `tops`, so that one lane divides by each, once.
+// Rows that are boxes are read in 16-byte pieces, 8 or 16 lanes a row, and the
+// bytes go to boxes; others are read two channels a lane, and the bytes go to
+// global memory.  At Bs=16 L=1000 ED=2560, two channels a lane and a warp's
+// reduction for each of the 48 tops made it 91 us, pieces make it 84.
 template <typename T, int W>
 __device__ __forceinline__ void keep_8bit(uint8_t *rows, float *tops, const Kept &kept, int64_t row0, int n_rows,
                                           int e0, int ED, int64_t all_rows, float one) {
     const int lane = threadIdx.x % 32, e = e0 + first_channel<W>();
+    constexpr int kLanes = 64 * int(sizeof(T)) / 16, kRows = 32 / kLanes;      // of a row; of one load
+    auto piece = [&](int i) { return *reinterpret_cast<const uint4 *>(rows + 512 * i + 16 * lane); };
     auto value = [&](int g) {
         return pair_at<T, W>(rows + g * kPitch<T, W>, shift_of<T, W>(row0 + g % kSteps, ED));
     };
-#pragma unroll(W == 16 ? 3 * kSteps / 4 : 1)
-    for (int g = 0; g < 3 * kSteps; g += 4) {
-        float4 top;
-        float *t = &top.x;
+    // the order of the bit patterns of |v| is that of the values, NaN on top
+    if constexpr (W == 16) {
+        constexpr int kLoads = 3 * kSteps / kRows, kValues = sizeof(T) == 4 ? kLoads : kLoads / 2;
+        constexpr uint32_t kAbs = sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu;
+        uint32_t v[kValues];
+        auto top_of = [&](int i) {
+            const uint4 w = piece(i);
+            return larger<T>(larger<T>(w.x & kAbs, w.y & kAbs), larger<T>(w.z & kAbs, w.w & kAbs));
+        };
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 v = value(g + i);
-            // the order of the bit patterns of |v| is that of the values, NaN on top
-            float m;
-            asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(fabsf(v.x)), "f"(fabsf(v.y)));
-            t[i] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+        for (int i = 0; i < kValues; ++i) {
+            if (sizeof(T) == 4) {
+                v[i] = top_of(i);
+            } else {      // those of two loads in the halves of a word
+                const uint32_t a = top_of(2 * i), b = top_of(2 * i + 1);
+                v[i] = larger<T>(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+            }
         }
-        if (lane == 0) *reinterpret_cast<float4 *>(tops + g) = top;
+        int first = 0;
+        largest<T, kValues, kLanes / 2>(v, first);
+        constexpr int kEqual = sizeof(T) == 4 ? 2 : 4;      // lanes with the same three values
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+            if (lane % kEqual != n % kEqual) continue;
+            if (sizeof(T) == 4) {
+                tops[(first + n) * kRows + lane / kLanes] = __uint_as_float(v[n]);
+            } else {
+                float *to = tops + 2 * (first + n) * kRows + lane / kLanes;
+                to[0] = __uint_as_float(v[n] << 16);
+                to[kRows] = __uint_as_float(v[n] & 0xffff0000u);
+            }
+        }
+    } else {
+#pragma unroll 1
+        for (int g = 0; g < 3 * kSteps; g += 4) {      // four at a time, for their latency
+            float4 top;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = value(g + i);
+                float m;
+                asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(fabsf(v.x)), "f"(fabsf(v.y)));
+                (&top.x)[i] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+            }
+            if (lane == 0) *reinterpret_cast<float4 *>(tops + g) = top;
+        }
     }
     __syncwarp();
 #pragma unroll
@@ -163,32 +227,63 @@ __device__ __forceinline__ void keep_8bit(uint8_t *rows, float *tops, const Kept
         tops[g] = inverse_of(top);
     }
     __syncwarp();
-#pragma unroll(W == 16 ? 3 : 1)
-    for (int k = 2; k >= 0; --k) {
-        uint8_t *box = box_8bit<T, W>(rows, k);
-        int8_t *q = (k == 0 ? kept.x_q : k == 1 ? kept.r_q : kept.i_q) + row0 * ED + e;
-#pragma unroll(W == 16 ? kSteps / 4 : 1)
-        for (int j = 0; j < kSteps; j += 4) {
-            const float4 inv = *reinterpret_cast<const float4 *>(tops + k * kSteps + j);
-            float2 n[4];
+    // x inv rounded, then to an integer (ties to even) by the addition of
+    // 1.5 2^23: as a multiply-add with a 1 that the compiler does not know, so
+    // that it cannot join it to the product
+    auto quantised2 = [&](float2 v, float inv) {
+        const float2 n = fma2(mul2(v, both(inv)), both(one), both(12582912.0f));
+        return __byte_perm(__float_as_uint(n.x), __float_as_uint(n.y), 0x0040);
+    };
+    if constexpr (W == 16) {
+        constexpr int kLoads = kSteps / kRows;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // x inv rounded, then to an integer (ties to even) by the
-                // addition of 1.5 2^23: as a multiply-add with a 1 that the
-                // compiler does not know, so that it cannot join it to the product
-                n[i] = fma2(mul2(value(k * kSteps + j + i), both((&inv.x)[i])), both(one), both(12582912.0f));
+        for (int k = 2; k >= 0; --k) {
+            uint8_t *box = box_8bit<T>(rows, k);
+#pragma unroll
+            for (int i = 0; i < kLoads; i += 2) {
+                uint32_t q[2][2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint4 w = piece(k * kLoads + i + j);
+                    const float inv = tops[k * kSteps + (i + j) * kRows + lane / kLanes];
+                    if constexpr (sizeof(T) == 4) {
+                        auto two = [&](uint32_t a, uint32_t b) {
+                            return quantised2(make_float2(__uint_as_float(a), __uint_as_float(b)), inv);
+                        };
+                        q[j][0] = __byte_perm(two(w.x, w.y), two(w.z, w.w), 0x5410);
+                    } else {
+                        auto two = [&](uint32_t a) {
+                            return quantised2(make_float2(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u)), inv);
+                        };
+                        q[j][0] = __byte_perm(two(w.x), two(w.y), 0x5410);
+                        q[j][1] = __byte_perm(two(w.z), two(w.w), 0x5410);
+                    }
+                }
+                __syncwarp();      // a load's bytes lie over the same load's rows or earlier ones'
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint8_t *to = box + 64 * kRows * (i + j);
+                    if (sizeof(T) == 4)
+                        *reinterpret_cast<uint32_t *>(to + 4 * lane) = q[j][0];
+                    else
+                        *reinterpret_cast<uint2 *>(to + 8 * lane) = make_uint2(q[j][0], q[j][1]);
+                }
             }
-            __syncwarp();      // row j's bytes lie over row j / 2
+        }
+    } else {
+#pragma unroll 1
+        for (int k = 0; k < 3; ++k) {
+            int8_t *q = (k == 0 ? kept.x_q : k == 1 ? kept.r_q : kept.i_q) + row0 * ED + e;
+#pragma unroll 1
+            for (int j = 0; j < kSteps; j += 4) {
+                const float4 inv = *reinterpret_cast<const float4 *>(tops + k * kSteps + j);
+                uint32_t n[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t n0 = __float_as_uint(n[i].x), n1 = __float_as_uint(n[i].y);
-                if (W == 16) {
-                    *reinterpret_cast<uint16_t *>(box + 64 * (j + i) + 2 * lane) =
-                        uint16_t(__byte_perm(n0, n1, 0x0040));
-                } else {
-                    if (j + i < n_rows && e < ED) q[0] = int8_t(n0);
-                    if (j + i < n_rows && e + kNext<W> < ED) q[kNext<W>] = int8_t(n1);
-                    q += ED;
+                for (int i = 0; i < 4; ++i) n[i] = quantised2(value(k * kSteps + j + i), (&inv.x)[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i, q += ED) {
+                    if (j + i < n_rows && e < ED) q[0] = int8_t(n[i]);
+                    if (j + i < n_rows && e + kNext<W> < ED) q[kNext<W>] = int8_t(n[i] >> 8);
                 }
             }
         }
@@ -300,7 +395,7 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    for (int k = 0; k < 3; ++k) tma_store_3d(&maps.q[k], box_8bit<T, W>(rows, k), e0, t0, int(b));
+                    for (int k = 0; k < 3; ++k) tma_store_3d(&maps.q[k], box_8bit<T>(rows, k), e0, t0, int(b));
                     tc::bulk_commit();
                 }
             }
