@@ -24,10 +24,12 @@
 // warp 48; all four blocks on an SM and clusters of three 43; one root for the
 // gate and the input's factor 41 (4.9 TB/s, 73 % of the measured copy rate).
 // What is left: 576 blocks of 608 places, a start of 3 us and issue slots
-// (448 instructions for 16 x 32 elements, 3.8 warps a scheduler).
-// Bs=1 L=65536 ED=2560 with resets: 308 us for 198 us of bytes; 40 chains fill
+// (997 instructions for 16 steps of 64 channels, 3.5 warps a scheduler).
+// More chains than fit at a time, Bs=16 L=1000 ED=2560 (bytes: 49 us): 68 us
+// in whole rounds, 62 with the last sequence in clusters of four; with the
+// 8-bit checkpoint (bytes: 68 us) 111, 91 and, read in 16-byte pieces, 84.
+// Bs=1 L=65536 ED=2560 with resets: 312 us for 198 us of bytes; 40 chains fill
 // 10.5 of 16 warps an SM, more blocks a cluster wait for a second round.
-// With the 8-bit checkpoint, Bs=16 L=1000 ED=2560: 110 us for 68 us of bytes.
 #include "gated_scan.cuh"
 
 #include <algorithm>

@@ -15,14 +15,17 @@
 //
 // 14 bytes an element (bf16).  At Bs=8 L=2048 ED=1536 (bytes: 52 us): one
 // thread a channel 2072 us; tiles 117; boxes 98; one warp folding the pieces
-// 92; m kept instead of computed twice 85 (4.2 TB/s, 61 % of the measured copy
-// rate).  854 instructions for 8 x 32 lanes of two elements issue in 33 us; 16
-// warps an SM (128 registers) cover them to 47 %, the rest is waiting at the
-// two barriers of a tile (a quarter) and for results.  Doing the work that
+// 92; m kept instead of computed twice 86; dlam's sum launched early 84 (4.2
+// TB/s, 62 % of the measured copy rate).  Left out, the folds of the exchange
+// save 11 us, the copies in 9, those out 7, all three 29: no single one of them
+// bounds it.  856 instructions for 8 x 32 lanes of two elements issue in 33
+// us; 16 warps an SM (128 registers) cover them to 46 %, the rest is waiting at
+// the two barriers of a tile (a quarter) and for results.  Doing the work that
 // does not need the adjoint while it travels was measured slower (88 us), and
-// so was taking the adjoint's sum forwards (86).  From the 8-bit checkpoint,
-// Bs=16 L=1000 ED=2560: 139 us for 68 us of bytes, bound by instructions
-// (1085, the unpacking of bytes among them).
+// so was taking the adjoint's sum forwards (86).  Bs=16 L=1000 ED=2560 (bytes:
+// 85 us): 126 us in whole rounds, 113 with the last sequence in clusters of
+// four; from the 8-bit checkpoint (bytes: 68 us) 139 and 125, bound by
+// instructions (980, the unpacking of bytes among them).
 #include "gated_scan.cuh"
 
 #include <algorithm>
