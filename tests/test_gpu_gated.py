@@ -328,6 +328,36 @@ def test_calls_in_a_cuda_graph(cuda_device):
         assert torch.equal(a, b)
 
 
+def test_what_follows_a_second_launch(cuda_device):
+    """Work behind a pass of two launches sees both, on a stream and in a
+    graph: copies queued right after it, and the next pass on its results."""
+    inp, _, more = case(16, 130, 2560, "bf16", seed=37)
+    d = on(inp, cuda_device)
+    dy = more["dy"].to(cuda_device)
+
+    def work():
+        y, saved = lrs.gated_scan_fwd(**d, save="states")
+        copies = [y.clone()]
+        g = lrs.gated_scan_bwd(d["x"], d["gate_r"], d["gate_i"], d["lam"], dy, saved)
+        copies += [v.clone() for v in g.values()]
+        y2 = lrs.gated_scan_fwd(g["dx"], g["dgate_r"], g["dgate_i"], d["lam"])
+        return copies + [y2, y, *g.values()]
+
+    first = work()
+    torch.cuda.synchronize()
+    for a, b in zip(first[:6], first[7:]):
+        assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = work()
+    for _ in range(3):
+        for t in out:
+            t.fill_(float("nan"))
+        graph.replay()
+        for a, b in zip(out, first):
+            assert torch.equal(a, b)
+
+
 def test_repeated_calls_are_bitwise_equal(cuda_device):
     inp, reset, more = case(3, 700, 320, "bf16", seed=13, resets=True)
     d, r = on(inp, cuda_device), reset.to(cuda_device)
