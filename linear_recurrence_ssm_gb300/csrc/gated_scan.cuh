@@ -528,12 +528,17 @@ struct Turn {
     double alone, shared, exchange, hop, start;
 };
 
+constexpr double kLaunchUs = 1.0;
+
 // Chooses C for one kernel (blocks of `warps` warps, `tile` steps) by the time
 // that its rounds of blocks would take.  A last round that a few sequences
 // would have for themselves goes to larger clusters, so that it is as short as
 // the GPU is empty; of kRest blocks at most, since a cluster waits until all
 // its places are free (gradients of Bs=32 L=2048 ED=1536 274 us, with the last
-// round by 4 blocks 267, by 6 286, by 8 283).  cache: blocks that run at a time by C, asked for once.
+// round by 4 blocks 267, by 6 286, by 8 283).  It has to save kLaunchUs: where
+// the sums were even, two launches took longer (forward of Bs=5 L=4096 ED=2048
+// 72.5 us, in two launches 74.9).  cache: blocks that run at a time by C, asked
+// for once.
 template <typename Args, typename Maps>
 inline Split best_split(void (*kern)(Args, Maps), int smem, int warps, int tile, const Turn &t,
                         int64_t Bs, int64_t L, int64_t ED, int num_sms, std::atomic<int> *cache) {
@@ -581,8 +586,8 @@ inline Split best_split(void (*kern)(Args, Maps), int smem, int warps, int tile,
         const double whole = double(rounds) * round(C, slots[C]);
         if (whole >= best.us) continue;
         const Split rest = launch(Bs - first, std::min(widest, kRest));
-        const double us = whole + rest.us;
-        if (us < best.us) best.cluster = C, best.first = first, best.rest_cluster = rest.cluster, best.us = us;
+        const double us = whole + rest.us + kLaunchUs;
+        if (rest.warps != 0 && us < best.us) best.cluster = C, best.first = first, best.rest_cluster = rest.cluster, best.us = us;
     }
     return best;
 }

@@ -258,7 +258,7 @@ def test_clusters_and_rows_off_16_bytes(cuda_device, Bs, L, ED, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("Bs,L,ED", [(16, 130, 2560), (9, 200, 5001)])
+@pytest.mark.parametrize("Bs,L,ED", [(16, 130, 2560), (20, 150, 1985), (9, 200, 5001)])
 def test_more_channels_than_fit_at_a_time(cuda_device, Bs, L, ED, dtype):
     """More than a round of blocks: the last sequences get clusters of their
     own size, in a second launch."""
