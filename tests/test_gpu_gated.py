@@ -116,6 +116,29 @@ def test_8bit_checkpoints(cuda_device, Bs, L, ED, dtype):
     check_bwd(inp, reset, more, dtype, cuda_device, saved, values)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("ED", [128, 136, 131])
+def test_8bit_checkpoints_of_special_values(cuda_device, ED, dtype):
+    """NaN, infinities, zeros and tiny values: the forward still keeps what
+    ckpt8_save does, bit for bit."""
+    inp, _, _ = case(2, 70, ED, dtype, seed=ED)
+    for k, at in (("x", 0), ("gate_r", 1), ("gate_i", 2)):
+        v = inp[k]
+        v[0, at, 5] = float("nan")
+        v[0, 3 + at, 64] = float("inf")
+        v[1, 6 + at, 63] = -float("inf")
+        v[1, 9 + at] = -0.0
+        v[1, 12 + at] = v[1, 12 + at] * 2.0 ** -105
+        v[1, 15 + at, 7] = 3e38
+        v[0, 69, 1 + at] = -float("nan")
+    d = on(inp, cuda_device)
+    _, saved = lrs.gated_scan_fwd(**d, save="8bit")
+    for k, q in (("x", "x"), ("gate_r", "r"), ("gate_i", "i")):
+        rq, rs = lrs.ckpt8_save(d[k])
+        assert torch.equal(saved[q + "_s"].view(torch.int32).flatten(), rs.view(torch.int32).flatten())
+        assert torch.equal(saved[q + "_q"].flatten(), rq.flatten())
+
+
 def test_gradients_against_differences(cuda_device):
     """Directional differences of the forward kernel itself, in fp32.  With a
     step of 2^-6 the truncation is O(2^-12) of the loss' third derivative and
