@@ -542,19 +542,24 @@ constexpr int kSmem = WARPS * kStages<T> * kStageBytes<T, W> + int(sizeof(Shared
 // turns), so that y is the same, bit for bit, whatever is kept or reset.
 template <typename T>
 static Split split_for(int64_t Bs, int64_t L, int64_t ED, int num_sms) {
-    static std::atomic<int> slots4[kMaxCluster + 1], slots8[kMaxCluster + 1];
+    static Places places4, places8;
     const double by = sizeof(T) == 4 ? 2.0 : 1.0;
     const Turn of4{1.5 * by, 0.39 * by, 0.3, 0.05, 3.0}, of8{2.0 * by, 0.85 * by, 0.3, 0.1, 3.0};
     const Split with4 = best_split(gated_fwd_kernel<T, 16, 4, false, false>, kSmem<T, 16, 4>, 4, 64, of4, Bs, L, ED,
-                                   num_sms, slots4);
+                                   num_sms, places4);
     const Split with8 = best_split(gated_fwd_kernel<T, 16, 8, false, false>, kSmem<T, 16, 8>, 8, 128, of8, Bs, L, ED,
-                                   num_sms, slots8);
+                                   num_sms, places8);
+    if (with4.err != cudaSuccess || with8.err != cudaSuccess) return with4.err != cudaSuccess ? with4 : with8;
     return with8.warps != 0 && (with4.warps == 0 || with8.us < with4.us) ? with8 : with4;
 }
 
 template <typename T, int W, bool RESET, bool SAVE8>
 static cudaError_t start_fwd(const FwdArgs<T> &p, const FwdMaps &maps, int64_t Bs, int num_sms, cudaStream_t st) {
+    static_assert(kSmem<T, W, 4> + exchange_bytes(kMaxCluster) <= 227 * 1024 &&
+                      kSmem<T, W, 8> + exchange_bytes(kMaxCluster) <= 227 * 1024,
+                  "shared memory of one block exceeds 227 KB");
     const Split how = split_for<T>(Bs, p.L, p.ED, num_sms);
+    if (how.err != cudaSuccess) return how.err;
     if (how.warps == 0) return cudaErrorInvalidConfiguration;
     if (how.warps == 8)
         return start_split(gated_fwd_kernel<T, W, 8, RESET, SAVE8>, kSmem<T, W, 8>, how, Bs, p.ED, p, maps, st);

@@ -47,7 +47,7 @@ __device__ __forceinline__ void cluster_sync() {
 
 constexpr int kMaxCluster = 16, kRest = 4;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-inline int exchange_bytes(int cluster) { return 2 * (cluster - 1) * 32 * 16; }
+constexpr int exchange_bytes(int cluster) { return 2 * (cluster - 1) * 32 * 16; }
 
 __device__ __forceinline__ bool aborted(const int *abort) { return *reinterpret_cast<const volatile int *>(abort); }
 // What a block does before it leaves after a wait that ran out: copies and
@@ -459,6 +459,7 @@ struct Split {
     int warps = 0, cluster = 1, rest_cluster = 0;
     int64_t first = 0;
     double us = 0.0;
+    cudaError_t err = cudaSuccess;      // of the questions to the driver; nothing else counts then
 };
 
 // Which sequences a launch has, in its arguments.
@@ -478,13 +479,17 @@ __device__ __forceinline__ void wait_for_first(const Share &s) {
 }
 
 // Starts `seqs` sequences in clusters of args.share.cluster blocks.  With
-// `resident`: asks for the blocks that run at a time instead.
+// `resident`: asks for the blocks that run at a time instead.  The kernel's
+// limit of shared memory is that of the largest cluster whatever this launch
+// takes: the limit belongs to the kernel, and another host thread may set it
+// between this call's setting and its launch.  (A limit alone costs no places.)
 template <typename Args, typename Maps>
 inline cudaError_t start_clusters(void (*kern)(Args, Maps), int smem, int warps, int64_t seqs, int64_t ED, const Args &args,
                                   const Maps &maps, cudaStream_t st, int *resident = nullptr) {
     const int C = args.share.cluster;
+    cudaError_t err =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem + exchange_bytes(kMaxCluster));
     smem += exchange_bytes(C);
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err == cudaSuccess && C > 8)
         err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (err != cudaSuccess) return err;
@@ -530,6 +535,13 @@ struct Turn {
 
 constexpr double kLaunchUs = 1.0;
 
+// Blocks of one kernel that run at a time, by device and C; asked for once.
+// An answer is kept, a failure is not.
+struct Places {
+    static constexpr int kDevices = 64;
+    std::atomic<int> of[kDevices][kMaxCluster + 1];
+};
+
 // Chooses C for one kernel (blocks of `warps` warps, `tile` steps) by the time
 // that its rounds of blocks would take.  A last round that a few sequences
 // would have for themselves goes to larger clusters, so that it is as short as
@@ -537,11 +549,16 @@ constexpr double kLaunchUs = 1.0;
 // its places are free (gradients of Bs=32 L=2048 ED=1536 274 us, with the last
 // round by 4 blocks 267, by 6 286, by 8 283).  It has to save kLaunchUs: where
 // the sums were even, two launches took longer (forward of Bs=5 L=4096 ED=2048
-// 72.5 us, in two launches 74.9).  cache: blocks that run at a time by C, asked
-// for once.
+// 72.5 us, in two launches 74.9).
 template <typename Args, typename Maps>
 inline Split best_split(void (*kern)(Args, Maps), int smem, int warps, int tile, const Turn &t,
-                        int64_t Bs, int64_t L, int64_t ED, int num_sms, std::atomic<int> *cache) {
+                        int64_t Bs, int64_t L, int64_t ED, int num_sms, Places &places) {
+    Split best;
+    int device = 0;
+    best.err = cudaGetDevice(&device);
+    if (best.err == cudaSuccess && device >= Places::kDevices) best.err = cudaErrorInvalidDevice;
+    if (best.err != cudaSuccess) return best;
+    std::atomic<int> *cache = places.of[device];
     const int64_t groups = (ED + 63) / 64, tiles = (L + tile - 1) / tile;
     const int widest = int(std::min<int64_t>(kMaxCluster, tiles));
     int slots[kMaxCluster + 1];
@@ -550,10 +567,8 @@ inline Split best_split(void (*kern)(Args, Maps), int smem, int warps, int tile,
         if (slots[C] == 0) {
             Args one{};
             one.share.cluster = C;
-            if (start_clusters(kern, smem, warps, 1, ED, one, Maps{}, nullptr, &slots[C]) != cudaSuccess) {
-                cudaGetLastError();
-                slots[C] = -1;
-            }
+            best.err = start_clusters(kern, smem, warps, 1, ED, one, Maps{}, nullptr, &slots[C]);
+            if (best.err != cudaSuccess) return best;
             // one cluster less than the driver counts: when all it counts
             // were asked for (40 of 7), some waited for a second round
             slots[C] = slots[C] > C ? slots[C] - C : slots[C] > 0 ? slots[C] : -1;
@@ -578,7 +593,7 @@ inline Split best_split(void (*kern)(Args, Maps), int smem, int warps, int tile,
         best.first = seqs;
         return best;
     };
-    Split best = launch(Bs, widest);
+    best = launch(Bs, widest);
     for (int C = 1; C <= widest && best.warps != 0; ++C) {
         if (slots[C] < C) continue;
         const int64_t rounds = Bs * groups * C / slots[C], first = rounds * slots[C] / (C * groups);

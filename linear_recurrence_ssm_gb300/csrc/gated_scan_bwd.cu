@@ -417,9 +417,11 @@ template <typename T, typename K, int W, bool RESET>
 static cudaError_t start(const BwdArgs<T> &p, const BwdMaps &maps, int64_t Bs, int num_sms, int64_t *sums, cudaStream_t st) {
     constexpr int kSmem = kWarps * Stage<T, K, W>::kWarpBytes + int(sizeof(Shared));
     auto kern = gated_bwd_kernel<T, K, W, RESET>;
-    static std::atomic<int> slots[kMaxCluster + 1];
+    static_assert(kSmem + exchange_bytes(kMaxCluster) <= 227 * 1024, "shared memory of one block exceeds 227 KB");
+    static Places places;
     const Turn turn = sizeof(T) == 4 ? Turn{3.9, 0.85, 1.3, 0.2, 8.0} : Turn{1.95, 0.92, 0.45, 0.1, 3.0};
-    const Split how = best_split(kern, kSmem, kWarps, kBlock, turn, Bs, p.L, p.ED, num_sms, slots);
+    const Split how = best_split(kern, kSmem, kWarps, kBlock, turn, Bs, p.L, p.ED, num_sms, places);
+    if (how.err != cudaSuccess) return how.err;
     if (how.warps == 0) return cudaErrorInvalidConfiguration;
     *sums = how.first * how.cluster + (Bs - how.first) * how.rest_cluster;
     return start_split(kern, kSmem, how, Bs, p.ED, p, maps, st);
