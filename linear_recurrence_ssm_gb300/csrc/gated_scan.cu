@@ -116,13 +116,13 @@ __device__ __forceinline__ void coefficients(const uint8_t *rows, int64_t row0, 
         if (CUT && (cut >> j & 1)) {
             a[j] = both(0.0f);
             b[j] = mul2(nin, both(-1.0f));
-            A = both(-0.0f);
             H = b[j];
         } else {
             A = mul2(A, a[j]);
             H = fma2(a[j], H, b[j]);
         }
     }
+    if (CUT && cut) A = both(-0.0f);      // here, since a NaN gate behind the drop would make it NaN
 }
 
 // The largest of N values over lanes that differ in the bits below 2 * BIT, to

@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <limits.h>
 #include <type_traits>
 
 namespace ssm {
@@ -121,9 +122,10 @@ __device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, in
     atomicOr(error, 1u);
 }
 
-// A piece's A carries in its sign whether a step of it dropped the state
-// before (A is then -0): the carried state may be an infinity or NaN, which
-// 0 times it would keep.
+// A piece's A carries in its first channel's sign whether a step of it dropped
+// the state before, of both channels: the carried state may be an infinity or
+// NaN, which 0 times it would keep.  A is then -0, or a NaN with the sign where
+// a gate behind the drop was NaN; arithmetic makes no NaN with a sign.
 __device__ __forceinline__ bool drops(float A) { return __float_as_int(A) < 0; }
 
 // c softplus(lam); e^lam overflows above 88, where softplus(lam) = lam.
@@ -304,9 +306,10 @@ __device__ __forceinline__ float2 after(float4 piece, float2 h) {
 // One piece, then another.
 template <bool RESET>
 __device__ __forceinline__ float4 joined(float4 first, float4 second) {
-    const float2 A = mul2(make_float2(first.x, first.y), make_float2(second.x, second.y));
+    float2 A = mul2(make_float2(first.x, first.y), make_float2(second.x, second.y));
     const float2 H = after<RESET>(second, make_float2(first.z, first.w));
-    // -0 times -0 would lose the sign
+    // -0 times -0 or NaN would lose the sign
+    if (RESET) A.x = __int_as_float(__float_as_int(A.x) | (__float_as_int(first.x) & INT_MIN));
     return RESET && drops(second.x) ? second : make_float4(A.x, A.y, H.x, H.y);
 }
 

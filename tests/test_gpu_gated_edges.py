@@ -53,3 +53,73 @@ def test_dlam_of_infinite_and_nan_terms(cuda_device):
     assert torch.isinf(dlam[5]) and torch.isnan(dlam[40])
     dlam[5] = dlam[40] = 0
     assert torch.isfinite(dlam).all()
+
+
+# ---- infinities and NaN next to a reset -------------------------------------------------
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("ED,e", [(128, 1), (130, 32)])
+@pytest.mark.parametrize("at", [3, 20, 100])
+@pytest.mark.parametrize("nan", [float("nan"), -float("nan")])
+def test_nan_gate_behind_a_reset(cuda_device, ED, e, at, nan, dtype):
+    """A NaN gate of channel 0 soon after a reset, in the same 8 steps, is
+    channel 0's alone: channel `e` (the one that a lane takes together with it)
+    still drops the infinite state before the reset and, in the gradients, the
+    infinite adjoint behind it.  Bounds as in test_gpu_gated."""
+    L = 300
+    gen = torch.Generator().manual_seed(at + ED)
+    x, r, i, dy = (torch.randn(1, L, ED, generator=gen).to(TYPES[dtype]) for _ in range(4))
+    lam = torch.full((ED,), -4.0)
+    reset = torch.zeros(1, L, dtype=torch.uint8)
+    reset[0, at] = 1
+    r[0, at + 1, 0] = nan
+    others = [k for k in range(ED) if k != 0]
+    dev = [t.to(cuda_device) for t in (r, i, lam, reset)]
+
+    bad = x.clone()
+    bad[0, at - 1, e] = float("inf")
+    y, hf, saved = lrs.gated_scan_fwd(bad.to(cuda_device), *dev[:3], reset=dev[3], return_final_state=True,
+                                      save="states")
+    ref = gated.gated_scan(x, r, i, lam, reset=reset)
+    bound = (16 + L) * 2.0 ** -21 * max(1.0, float(np.max(np.abs(ref[:, :, others]))))
+    got = y.double().cpu().numpy()[0, at:][:, others]
+    want = ref[0, at:][:, others]
+    assert (np.abs(got - want) <= bound + (2.0 ** -8 * np.abs(want) if dtype == "bf16" else 0)).all()
+    assert (np.abs(hf.double().cpu().numpy() - ref[:, -1])[:, others] <= bound).all()
+    assert torch.isnan(y[0, at + 1:, 0]).all()
+
+    dy[0, at + 1, e] = float("inf")
+    x = x.to(cuda_device)
+    _, saved = lrs.gated_scan_fwd(x, *dev[:3], reset=dev[3], save="states")
+    g = lrs.gated_scan_bwd(x, *dev[:3], dy.to(cuda_device), saved, reset=dev[3])
+    for k in ("dx", "dgate_r", "dgate_i"):
+        assert torch.isfinite(g[k][0, :at]).all(), k
+    assert torch.isfinite(g["dh0"]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_nan_gate_without_a_reset(cuda_device, dtype):
+    """A NaN gate (of either sign) or rate of one channel leaves the others
+    alone, also where resets are given, over a cluster's blocks, too."""
+    L, ED = 1500, 128
+    gen = torch.Generator().manual_seed(7)
+    x, r, i, dy = (torch.randn(1, L, ED, generator=gen).to(TYPES[dtype]) for _ in range(4))
+    lam = torch.full((ED,), -4.0)
+    reset = torch.zeros(1, L, dtype=torch.uint8)
+    reset[0, 3] = 1
+    want = [t.to(cuda_device) for t in (x, r, i, lam)]
+    reset = reset.to(cuda_device)
+    r[0, 700, 0], r[0, 900, 2], lam[4] = float("nan"), -float("nan"), -float("nan")
+    got = [t.to(cuda_device) for t in (x, r, i, lam)]
+    dy = dy.to(cuda_device)
+    others = [k for k in range(ED) if k not in (0, 2, 4)]
+
+    def both(inp):
+        y, hf, saved = lrs.gated_scan_fwd(*inp, reset=reset, return_final_state=True, save="states")
+        g = lrs.gated_scan_bwd(*inp, dy, saved, reset=reset)
+        return [t[..., others].float() for t in (y, hf, saved["states"], *g.values())]
+
+    # a NaN rate sends its warp through the general form of the decay: up to
+    # rounding, (16 + L) 2^-21 of the largest value and a neighbouring bf16
+    for a, b in zip(both(got), both(want)):
+        bound = 2 * (16 + L) * 2.0 ** -21 * max(1.0, b.abs().max().item())
+        assert ((a - b).abs() <= bound + (2.0 ** -7 * b.abs() if dtype == "bf16" else 0)).all()
