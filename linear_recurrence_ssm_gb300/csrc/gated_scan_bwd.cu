@@ -153,7 +153,9 @@ __device__ __forceinline__ void gradients(const BwdArgs<T> &p, const uint8_t *st
         float2 G = mul2(mul2(mul2(la, a[j]), g), fma2(mul2(a[j], over), mul2(nsi[j], x), before[j]));
         if (dropped) ngm = mul2(g, both(-1.0f)), G = both(0.0f);
         const float2 dx = mul2(ngm, nsi[j]), q = mul2(dx, x);
-        const float2 dr = fma2(G, nsr[j], G), di = fma2(q, nsi[j], q);
+        float2 dr = fma2(G, nsr[j], G);
+        const float2 di = fma2(q, nsi[j], q);
+        if (dropped) dr = both(0.0f);      // the gate was not used, it may be NaN
         if constexpr (W == 16) {
             // over the lane's own elements of the inputs
             T *o = reinterpret_cast<T *>(out + j * kPitch<T, W>) + 2 * (threadIdx.x % 32);

@@ -123,3 +123,29 @@ def test_nan_gate_without_a_reset(cuda_device, dtype):
     for a, b in zip(both(got), both(want)):
         bound = 2 * (16 + L) * 2.0 ** -21 * max(1.0, b.abs().max().item())
         assert ((a - b).abs() <= bound + (2.0 ** -7 * b.abs() if dtype == "bf16" else 0)).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("gate", [float("nan"), float("inf"), -float("inf")])
+def test_gate_of_a_reset_step_is_not_used(cuda_device, gate, dtype):
+    """A reset step's decay is the constant 0: whatever its gate_r holds, y and
+    the gradients are what they are with another gate, and its own is 0."""
+    Bs, L, ED = 2, 150, 72
+    gen = torch.Generator().manual_seed(11)
+    x, r, i, dy = (torch.randn(Bs, L, ED, generator=gen).to(TYPES[dtype]).to(cuda_device) for _ in range(4))
+    lam = torch.full((ED,), -4.0, device=cuda_device)
+    reset = torch.zeros(Bs, L, dtype=torch.uint8, device=cuda_device)
+    reset[0, 17] = reset[1, 0] = reset[1, 149] = 1
+
+    def both(r):
+        y, hf, saved = lrs.gated_scan_fwd(x, r, i, lam, reset=reset, return_final_state=True, save="states")
+        return y, hf, lrs.gated_scan_bwd(x, r, i, lam, dy, saved, reset=reset)
+
+    y, hf, g = both(r)
+    odd = r.clone()
+    odd[reset != 0] = gate
+    y2, hf2, g2 = both(odd)
+    assert torch.equal(y, y2) and torch.equal(hf, hf2)
+    for k in g:
+        assert torch.equal(g[k], g2[k]), k
+    assert not g2["dgate_r"][reset != 0].any()
