@@ -128,9 +128,12 @@ __device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, in
 // a gate behind the drop was NaN; arithmetic makes no NaN with a sign.
 __device__ __forceinline__ bool drops(float A) { return __float_as_int(A) < 0; }
 
-// c softplus(lam); e^lam overflows above 88, where softplus(lam) = lam.
+// c softplus(lam); e^lam overflows above 88, where softplus(lam) = lam.  Rates
+// above 2^127 are taken as that: an infinite one would make NaN of a gate that
+// is shut (times 0) and of a decay of 0 (its logarithm times it).  NaN stays.
 __device__ __forceinline__ float decay_rate(float lam, float c) {
-    return c * (lam > 20.0f ? lam : log1pf(expf(lam)));
+    const float rate = c * (lam > 20.0f ? lam : log1pf(expf(lam)));
+    return rate > 0x1p127f ? 0x1p127f : rate;
 }
 
 // sigmoid(lam) / softplus(lam): la's derivative with respect to lam, over la.
@@ -223,7 +226,12 @@ __device__ __forceinline__ void decay2(float2 la, float2 &a, float2 &em) {
     em = slow_em1(la);
     a = add2(em, both(1.0f));
     if (WIDE) {
-        const float2 e = exp_pair<ACC>(la);
+        float2 v = la;
+        if (ACC) {      // e^-1000 = 0 in fp32; what log2(e) v loses has to stay finite
+            asm("max.NaN.f32 %0, %1, %2;" : "=f"(v.x) : "f"(la.x), "f"(-1000.0f));
+            asm("max.NaN.f32 %0, %1, %2;" : "=f"(v.y) : "f"(la.y), "f"(-1000.0f));
+        }
+        const float2 e = exp_pair<ACC>(v);
         const float2 em_e = add2(e, both(-1.0f));
         if (la.x <= -kSlow) a.x = e.x, em.x = em_e.x;
         if (la.y <= -kSlow) a.y = e.y, em.y = em_e.y;

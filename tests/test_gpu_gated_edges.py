@@ -149,3 +149,45 @@ def test_gate_of_a_reset_step_is_not_used(cuda_device, gate, dtype):
     for k in g:
         assert torch.equal(g[k], g2[k]), k
     assert not g2["dgate_r"][reset != 0].any()
+
+
+# ---- rates beyond fp32 ------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lam,c", [(2e37, 8.0), (1e38, 8.0), (3e38, 8.0), (float("inf"), 8.0), (30.0, 3e37),
+                                   (1.0, 3e38)])
+def test_rates_beyond_fp32(cuda_device, lam, c, dtype):
+    """c softplus(lam) above the largest fp32 is a decay of 0 where the gate is
+    open, of 1 where it is shut: no NaN, in the scan, its gradients and the
+    step.  A shut gate (-200) has s_r = 0 in fp32, e^-200 in the oracle: la is
+    0 and -1e-48."""
+    Bs, L, ED = 1, 70, 64
+    gen = torch.Generator().manual_seed(5)
+    x, r, i, dy = (torch.randn(Bs, L, ED, generator=gen).to(TYPES[dtype]) for _ in range(4))
+    r[0, 5] = r[0, 40] = r[0, 69] = -200.0
+    h0, dh = torch.randn(Bs, ED, generator=gen), torch.randn(Bs, ED, generator=gen)
+    d = [t.to(cuda_device) for t in (x, r, i, torch.full((ED,), lam))]
+    y, saved = lrs.gated_scan_fwd(*d, c=c, h0=h0.to(cuda_device), save="states")
+    g = lrs.gated_scan_bwd(*d, dy.to(cuda_device), saved, c=c, dh_final=dh.to(cuda_device))
+    big = torch.full((ED,), min(lam, 3e38))
+    ref = gated.gated_scan(x, r, i, big, c, h0=h0)
+    want = gated.gated_scan_bwd(x, r, i, big, dy, saved["states"], c, dh_final=dh)
+
+    def near(got, ref, what):      # as in test_gpu_gated
+        bound = 2 * (16 + L) * 2.0 ** -21 * max(1.0, float(np.max(np.abs(ref))))
+        bound = bound + (2.0 ** -8 * np.abs(ref) if got.dtype == torch.bfloat16 else 0.0)
+        assert (np.abs(got.double().cpu().numpy() - ref) <= bound).all(), what
+
+    near(y, ref, "y")
+    for k in g:
+        near(g[k], want[k], k)
+    states = h0.to(cuda_device)
+    near(lrs.gated_scan_step(*[t[:, 0].contiguous() for t in d[:3]], d[3], states, c=c), ref[:, 0], "step")
+    near(states, ref[:, 0], "state")
+
+
+def test_a_nan_rate_stays(cuda_device):
+    x = torch.randn(1, 40, 64, device=cuda_device)
+    lam = torch.zeros(64, device=cuda_device)
+    lam[7] = float("nan")
+    y = lrs.gated_scan_fwd(x, x, x, lam)
+    assert torch.isnan(y[..., 7]).all() and torch.isfinite(y[..., :7]).all() and torch.isfinite(y[..., 8:]).all()
