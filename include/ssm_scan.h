@@ -493,6 +493,14 @@ SSM_API ssm_status_t ssm_check_device_errors(void *stream);
  */
 SSM_API ssm_status_t ssm_selftest_wait_timeout(void *stream);
 
+/*
+ * The same for the waits of gated_scan_fwd (backward == 0) or gated_scan_bwd:
+ * for a piece that another block of a cluster never sends (copy == 0), or for
+ * a copy that never arrives.  The kernel goes on as the recurrence's do after
+ * such a wait, which must not wait again; it takes 40 ms.
+ */
+SSM_API ssm_status_t gated_selftest_wait_timeout(int backward, int copy, void *stream);
+
 /* Static, human-readable name of a status code. */
 SSM_API const char *ssm_status_string(ssm_status_t status);
 

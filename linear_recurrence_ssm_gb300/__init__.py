@@ -85,6 +85,7 @@ SIGNATURES = {
     "state_pages_compact": ([_VP] * 5 + [_I64] * 4 + [_VP], ctypes.c_int),
     "ssm_check_device_errors": ([_VP], ctypes.c_int),
     "ssm_selftest_wait_timeout": ([_VP], ctypes.c_int),
+    "gated_selftest_wait_timeout": ([ctypes.c_int, ctypes.c_int, _VP], ctypes.c_int),
     "ssm_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "ssm_version": ([], ctypes.c_int),
 }

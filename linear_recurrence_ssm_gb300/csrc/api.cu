@@ -74,6 +74,7 @@ cudaError_t launch_step(const T *x, const T *gr, const T *gi, const float *lam, 
                         float *states, const int32_t *pages, T *y, int64_t Bs, int64_t ED,
                         int64_t num_pages, cudaStream_t st);
 cudaError_t take_device_error(unsigned int *out);
+cudaError_t probe_wait_timeout(bool for_copy, cudaStream_t st);
 }
 namespace gated_bwd {
 template <typename T>
@@ -83,6 +84,7 @@ cudaError_t launch(const T *x, const T *gr, const T *gi, const float *lam, float
                    float *scratch, int64_t Bs, int64_t L, int64_t ED, int num_sms,
                    cudaStream_t st);
 cudaError_t take_device_error(unsigned int *out);
+cudaError_t probe_wait_timeout(bool for_copy, cudaStream_t st);
 }
 namespace ckpt8 {
 template <typename T>
@@ -765,6 +767,15 @@ ssm_status_t ssm_selftest_wait_timeout(void *stream) {
     ssm_status_t s = current_device(&dev);
     if (s != SSM_OK) return s;
     return from_cuda(ssm::ssd::probe_wait_timeout(static_cast<cudaStream_t>(stream)));
+}
+
+ssm_status_t gated_selftest_wait_timeout(int backward, int copy, void *stream) {
+    DeviceInfo dev;
+    ssm_status_t s = current_device(&dev);
+    if (s != SSM_OK) return s;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return from_cuda(backward ? ssm::gated_bwd::probe_wait_timeout(copy != 0, st)
+                              : ssm::gated::probe_wait_timeout(copy != 0, st));
 }
 
 const char *ssm_status_string(ssm_status_t status) {

@@ -598,6 +598,14 @@ cudaError_t launch_fwd(const T *x, const T *gr, const T *gi, const float *lam, f
     return W >= 8 ? start_fwd<T, 8>(p, Bs, num_sms, st) : start_fwd<T, 1>(p, Bs, num_sms, st);
 }
 
+__global__ void __launch_bounds__(32) __cluster_dims__(2, 1, 1) run_out_kernel(bool for_copy) {
+    run_out(for_copy, &g_device_error);
+}
+cudaError_t probe_wait_timeout(bool for_copy, cudaStream_t st) {
+    run_out_kernel<<<2, 32, 0, st>>>(for_copy);
+    return cudaGetLastError();
+}
+
 // Read and clear this unit's device error word (host side, synchronous).
 cudaError_t take_device_error(unsigned int *out) {
     unsigned int v = 0;

@@ -53,9 +53,9 @@ constexpr int exchange_bytes(int cluster) { return 2 * (cluster - 1) * 32 * 16; 
 __device__ __forceinline__ bool aborted(const int *abort) { return *reinterpret_cast<const volatile int *>(abort); }
 // What a block does before it leaves after a wait that ran out: copies and
 // pieces on their way into its shared memory get the same time again.
-__device__ __forceinline__ void linger() {
+__device__ __forceinline__ void linger(uint64_t limit_ns = kWaitLimitNs) {
     const uint64_t t0 = tc::globaltimer_ns();
-    while (tc::globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(1000);
+    while (tc::globaltimer_ns() - t0 < limit_ns) __nanosleep(1000);
 }
 struct alignas(16) Exchange {
     uint64_t full[2];
@@ -100,13 +100,14 @@ struct alignas(16) Exchange {
             : "memory");
         return ok != 0;
     }
-    // Every thread; gives up after kWaitLimitNs and then reports in *error.
-    __device__ __forceinline__ void wait(int buf, uint32_t parity, unsigned int *error) {
+    // Every thread; gives up after limit_ns and then reports in *error.
+    __device__ __forceinline__ void wait(int buf, uint32_t parity, unsigned int *error,
+                                         uint64_t limit_ns = kWaitLimitNs) {
         if (arrived(buf, parity)) return;
         const uint64_t t0 = tc::globaltimer_ns();
         while (!arrived(buf, parity)) {
             if (*reinterpret_cast<volatile int *>(&abort)) return;
-            if (tc::globaltimer_ns() - t0 > kWaitLimitNs) {
+            if (tc::globaltimer_ns() - t0 > limit_ns) {
                 *reinterpret_cast<volatile int *>(&abort) = 1;
                 atomicOr(error, 1u);
                 return;
@@ -116,10 +117,49 @@ struct alignas(16) Exchange {
 };
 
 // Waits for a warp's own copies; the same limit.
-__device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, int *abort, unsigned int *error) {
-    if (tc::mbar_wait_bounded(bar, parity, abort, kWaitLimitNs)) return;
+__device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, int *abort, unsigned int *error,
+                                              uint64_t limit_ns = kWaitLimitNs) {
+    if (tc::mbar_wait_bounded(bar, parity, abort, limit_ns)) return;
     *reinterpret_cast<volatile int *>(abort) = 1;
     atomicOr(error, 1u);
+}
+
+// Self-test of the above, one warp in each of two blocks of a cluster: the
+// first block waits for a piece that the other one never sends (for_copy: for
+// a copy that was never asked for), gives up, and then does what a kernel does
+// in its remaining turns -- which has to wait no more and send nothing.
+__device__ __forceinline__ void run_out(bool for_copy, unsigned int *error) {
+    constexpr uint64_t kLimitNs = 20000000ull;
+    constexpr int kTurns = 100;
+    __shared__ struct {
+        Exchange ex;
+        float4 pieces[exchange_bytes(2) / int(sizeof(float4))];
+        uint64_t copied;
+    } sh;
+    const int rank = int(cluster_rank());
+    if (threadIdx.x == 0) {
+        sh.ex.init();
+        sh.ex.abort = 0;
+        tc::mbar_init(&sh.copied, 1);
+        tc::mbar_fence_init();
+    }
+    __syncwarp();
+    cluster_sync();
+    if (rank == 0) {
+        if (for_copy) wait_or_abort(&sh.copied, 0, &sh.ex.abort, error, kLimitNs);
+        __syncwarp();
+        for (int turn = 0; turn < kTurns; ++turn) {
+            const int buf = turn & 1;
+            if (threadIdx.x == 0) sh.ex.expect(buf, 2);
+            if (turn > 0) sh.ex.send(buf, 2, 0, 1, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+            __syncwarp();
+            sh.ex.wait(buf, turn >> 1 & 1, error, kLimitNs);
+            wait_or_abort(&sh.copied, 0, &sh.ex.abort, error, kLimitNs);
+        }
+        if (aborted(&sh.ex.abort)) linger(kLimitNs);
+    }
+    __syncwarp();
+    cluster_sync();
 }
 
 // A piece's A carries in its first channel's sign whether a step of it dropped

@@ -389,6 +389,14 @@ gated_bwd_kernel(const __grid_constant__ BwdArgs<T> p, const __grid_constant__ B
     wait_for_first(p.share);
 }
 
+__global__ void __launch_bounds__(32) __cluster_dims__(2, 1, 1) run_out_kernel(bool for_copy) {
+    run_out(for_copy, &g_device_error);
+}
+cudaError_t probe_wait_timeout(bool for_copy, cudaStream_t st) {
+    run_out_kernel<<<2, 32, 0, st>>>(for_copy);
+    return cudaGetLastError();
+}
+
 // Read and clear this unit's device error word (host side, synchronous).
 cudaError_t take_device_error(unsigned int *out) {
     unsigned int v = 0;

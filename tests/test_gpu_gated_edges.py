@@ -191,3 +191,34 @@ def test_a_nan_rate_stays(cuda_device):
     lam[7] = float("nan")
     y = lrs.gated_scan_fwd(x, x, x, lam)
     assert torch.isnan(y[..., 7]).all() and torch.isfinite(y[..., :7]).all() and torch.isfinite(y[..., 8:]).all()
+
+
+# ---- waits that run out -----------------------------------------------------------------
+@pytest.mark.parametrize("backward", [0, 1])
+@pytest.mark.parametrize("copy", [0, 1])
+def test_waits_give_up(cuda_device, backward, copy):
+    """A wait that cannot end gives up after its 20 ms, the hundred turns after
+    it wait no more (they would take 2 s), 20 ms more pass for copies under
+    way; the unit's error word is reported once, and the next calls are right."""
+    lib, stream = lrs.library(), torch.cuda.current_stream(cuda_device)
+    assert lib.ssm_check_device_errors(stream.cuda_stream) == 0
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    assert lib.gated_selftest_wait_timeout(backward, copy, stream.cuda_stream) == 0
+    end.record()
+    assert lib.ssm_check_device_errors(stream.cuda_stream) == 5      # SSM_ERR_DEVICE_TIMEOUT
+    assert lib.ssm_check_device_errors(stream.cuda_stream) == 0      # cleared
+    assert 39.0 < start.elapsed_time(end) < 1000.0
+    gen = torch.Generator().manual_seed(1)
+    x, r, i = (torch.randn(1, 700, 64, generator=gen) for _ in range(3))
+    lam = torch.full((64,), -4.0)
+    d = [t.to(cuda_device) for t in (x, r, i, lam)]
+    y, saved = lrs.gated_scan_fwd(*d, save="states")
+    ref = gated.gated_scan(x, r, i, lam)
+    bound = (16 + 700) * 2.0 ** -21 * max(1.0, float(np.max(np.abs(ref))))
+    assert (np.abs(y.double().cpu().numpy() - ref) <= bound).all()
+    g = lrs.gated_scan_bwd(*d, d[0], saved)
+    want = gated.gated_scan_bwd(x, r, i, lam, x, saved["states"])
+    bound = 2 * (16 + 700) * 2.0 ** -21 * max(1.0, float(np.max(np.abs(want["dx"]))))
+    assert (np.abs(g["dx"].double().cpu().numpy() - want["dx"]) <= bound).all()
+    assert lib.ssm_check_device_errors(stream.cuda_stream) == 0
