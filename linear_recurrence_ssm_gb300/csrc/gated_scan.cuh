@@ -251,9 +251,10 @@ __device__ __forceinline__ float2 nsigmoid2(float2 v) {
 // error 5.2e-8 in exact arithmetic); from there on a - 1 loses at most two
 // bits.  WIDE says that la may be below -0.4: |la| <= c softplus(lam), so a
 // warp knows from its channels alone.
-// em is kept below -kLeast, far below what it adds to, so that la = 0 needs no
-// case of its own where (1 - a^2)^(-1/2) is taken.
-constexpr float kSlow = 0.4f, kLeast = 1e-30f;
+// em is kept below -kLeast, so that la = 0 needs no case of its own where
+// (1 - a^2)^(-1/2) is taken (flushed if 1 - a^2 were subnormal): far below what
+// it adds to for every -la above 2^-100, whose m is 2^-50.
+constexpr float kSlow = 0.4f, kLeast = 0x1p-125f;
 __device__ __forceinline__ float2 slow_em1(float2 la) {
     float2 q = fma2(la, both(0x1.cf2208p-8f), both(0x1.51d0aap-5f));
     q = fma2(q, la, both(0x1.5535acp-3f));

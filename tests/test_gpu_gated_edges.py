@@ -222,3 +222,38 @@ def test_waits_give_up(cuda_device, backward, copy):
     bound = 2 * (16 + 700) * 2.0 ** -21 * max(1.0, float(np.max(np.abs(want["dx"]))))
     assert (np.abs(g["dx"].double().cpu().numpy() - want["dx"]) <= bound).all()
     assert lib.ssm_check_device_errors(stream.cuda_stream) == 0
+
+
+# ---- the slowest decays -----------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("fast", [False, True])
+@pytest.mark.parametrize("lam", [-50.0, -65.0, -70.0])
+def test_slowest_decays(cuda_device, lam, fast, dtype):
+    """m = sqrt(1 - a^2) to full relative accuracy as a -> 1: from h0 = 0, y is
+    m's size (1e-11 to 1e-15), and within the usual bound of that, as are the
+    gradients.  `fast` puts fast decays beside them, which are computed in
+    another form."""
+    Bs, L, ED = 1, 70, 64
+    gen = torch.Generator().manual_seed(9)
+    x, r, i, dy = (torch.randn(Bs, L, ED, generator=gen).to(TYPES[dtype]) for _ in range(4))
+    lams = torch.full((ED,), lam)
+    if fast:
+        lams[1::2] = 1.0
+    d = [t.to(cuda_device) for t in (x, r, i, lams)]
+    y, saved = lrs.gated_scan_fwd(*d, save="states")
+    g = lrs.gated_scan_bwd(*d, dy.to(cuda_device), saved)
+    step = lrs.gated_scan_step(*[t[:, 0].contiguous() for t in d[:3]], d[3], torch.zeros(Bs, ED, device=cuda_device))
+    ref = gated.gated_scan(x, r, i, lams)
+    want = gated.gated_scan_bwd(x, r, i, lams, dy, saved["states"])
+    slow = slice(0, ED, 2 if fast else 1)
+
+    def near(got, ref, size, what):
+        got = got.double().cpu().numpy()[..., slow]
+        bound = 2 * (16 + L) * 2.0 ** -21 * np.max(np.abs(size[..., slow]))
+        bound = bound + (2.0 ** -8 * np.abs(ref[..., slow]) if dtype == "bf16" else 0.0)
+        assert (np.abs(got - ref[..., slow]) <= bound).all(), (what, np.max(np.abs(got - ref[..., slow])), np.max(bound))
+
+    near(y, ref, ref, "y")
+    near(step, ref[:, 0], ref[:, 0], "step")
+    for k, size in (("dx", "dx"), ("dgate_i", "dgate_i"), ("dgate_r", "size"), ("dlam", "size_lam"), ("dh0", "dh0")):
+        near(g[k], want[k], want[size], k)
