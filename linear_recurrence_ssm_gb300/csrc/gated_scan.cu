@@ -482,7 +482,9 @@ gated_fwd_kernel(const __grid_constant__ FwdArgs<T> p, const __grid_constant__ F
 // One token.  A thread takes two channels of kStepRows rows, so that a
 // channel's decay rate is computed once for them and their loads are in
 // flight together; bound by latency (page number, then state) up to some
-// hundred rows.  PAIRS: rows start on pairs of elements.
+// hundred rows.  With 2560 channels and the start of a launch, bf16: 256 rows
+// 10 us, 1024 18 us (bytes: 6), 16384 166 us (bytes: 99); fp32: 1024 16 us
+// (bytes: 9), 16384 150 us (bytes: 148).  PAIRS: rows start on pairs of elements.
 constexpr int kStepRows = 4, kStepThreads = 128;
 __device__ __forceinline__ float2 get2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
 __device__ __forceinline__ float2 get2(const __nv_bfloat16 *p) {
@@ -539,7 +541,12 @@ template <typename T, int W, int WARPS>
 constexpr int kSmem = WARPS * kStages<T> * kStageBytes<T, W> + int(sizeof(Shared<WARPS>));
 
 // The split goes by the sizes and the type alone (the plain kernel's measured
-// turns), so that y is the same, bit for bit, whatever is kept or reset.
+// turns), so that y is the same, bit for bit, whatever is kept.  (A reset sends
+// all 16 steps of its warp through the general form of the coefficients, so
+// that steps beside it may differ in their last bits from those without it.)
+// Rows off 16 bytes take the split counted for boxes as well, although their
+// wider pitch lets fewer blocks on an SM: in bf16 three of 4 warps instead of
+// four, one of 8 instead of two, so part of a counted round waits for another.
 template <typename T>
 static Split split_for(int64_t Bs, int64_t L, int64_t ED, int num_sms) {
     static Places places4, places8;

@@ -457,6 +457,14 @@ static cudaError_t start(const BwdArgs<T> &p, const BwdMaps &maps, int64_t Bs, i
     auto kern = gated_bwd_kernel<T, K, W, RESET>;
     static_assert(kSmem + exchange_bytes(kMaxCluster) <= 227 * 1024, "shared memory of one block exceeds 227 KB");
     static Places places;
+    // Fitted to measured passes.  fp32's exchange and hop keep a chain in fewer
+    // blocks: with twice bf16's shared time, its exchange and its hop (0.45,
+    // 0.1) Bs=3 L=1001 ED=1537 took 55.9 us (now 49.8), 8 x 512 x 1536 54.9
+    // (50.9), 16 x 300 x 640 39.6 (33.5), and eleven other shapes within 2 us;
+    // its start only fits the short passes' times (3 gave the same split for
+    // all 14).  8-bit checkpoints take their tensors' type's turns: with turns
+    // longer by a seventh, as their instructions are, nine shapes had the same
+    // split.
     const Turn turn = sizeof(T) == 4 ? Turn{3.9, 0.85, 1.3, 0.2, 8.0} : Turn{1.95, 0.92, 0.45, 0.1, 3.0};
     const Split how = best_split(kern, kSmem, kWarps, kBlock, turn, Bs, p.L, p.ED, num_sms, places);
     if (how.err != cudaSuccess) return how.err;
