@@ -358,7 +358,7 @@ def run(s):
     out = {"y": got[0]}
     if s["r"] is not None:
         out["sum"] = got[1]
-    grads = lrs.rms_norm_bwd(s["dy"], s["x"] if s["r"] is None else got[1], s["weight"], got[-1], ds=s["ds"])
+    grads = lrs.rms_norm_bwd(s["dy"], s["x"], s["weight"], got[-1], residual=s["r"], ds=s["ds"])
     return dict(out, dx=grads["dx"], dweight=grads["dweight"])
 
 
