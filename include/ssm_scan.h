@@ -474,6 +474,110 @@ SSM_API ssm_status_t state_pages_compact(void *pool, uint8_t *used, int32_t *mov
                                          int64_t page_bytes, void *stream);
 
 /*
+ * Gated delta rule: a matrix state (V x K, fp32) per head, corrected at every
+ * step towards the value that its key should give.
+ *   q, k : (Bs, L, G, K)   v : (Bs, L, H, V)   g, beta : (Bs, L, H)
+ *          all fp32 (input_bf16 == 0) or all bf16; head h reads group
+ *          h / (H / G) of q and k
+ *   a_t = e^(g_t)  (g: the log of the decay, <= 0; below -100 the decay is 0
+ *          and drops the state before the step, whatever that holds)
+ *   x_t = v_t - a_t S_{t-1} k_t,   S_t = a_t S_{t-1} + beta_t x_t k_t^T,
+ *   y_t = scale S_t q_t,   S_{-1} = h0 (0 when NULL)
+ *   y   : (Bs, L, H, V), v's type
+ *   h0, h_final : (Bs or n_seq, H, V, K) fp32 or NULL
+ *   offsets, n_seq : NULL and 0, or the starts of n_seq sequences packed into
+ *          one row (Bs == 1), and the end of the last: (n_seq + 1) int32 on
+ *          the device, not decreasing, in 0..L.  A sequence may be empty
+ *          (h_final = h0).  Rows that no sequence covers, before the first or
+ *          behind the last, get 0 in y and in the gradients.  Other offsets
+ *          give unspecified results, but no access outside the arrays.
+ *   states, errors : NULL, or what the backward pass needs (both, fully
+ *          written, v's type): the state before steps 0, 64, 128, ... of each
+ *          sequence, (slots, H, V, K) with slots = Bs ceil(L / 64), packed
+ *          floor(L / 64) + n_seq; and x, (Bs, L, H, V)
+ * The state and every sum are fp32.  bf16 inputs: see the kernels for what the
+ * tensor cores' operands are rounded to.  A NaN or an infinity in a step's
+ * inputs makes the outputs of that head's whole block of 64 steps and of
+ * everything behind it in the same sequence unspecified; no other sequence.
+ * Supported (SSM_ERR_UNSUPPORTED otherwise): K, V <= 256.  G divides H.
+ * Every pointer is aligned to its element size (SSM_ERR_ALIGNMENT).
+ */
+#define SSM_DELTA_BLOCK 64      /* steps between two kept states */
+SSM_API ssm_status_t delta_rule_fwd(const void *q, const void *k, const void *v, const void *g,
+                                    const void *beta, float scale, const int32_t *offsets,
+                                    const float *h0, void *y, float *h_final, void *states,
+                                    void *errors, int64_t Bs, int64_t L, int64_t G, int64_t H,
+                                    int64_t K, int64_t V, int64_t n_seq, int input_bf16,
+                                    void *stream);
+
+/*
+ * Gradients of delta_rule_fwd for dy (v's shape and type) and dh_final (NULL =
+ * 0), from the states and errors that the forward call kept.
+ *   dq, dk : as q, k (a group's is the sum over its heads)   dv : as dy
+ *   dg, dbeta : (Bs, L, H), dy's type   dh0 : as h0, fp32, or NULL
+ *   scratch : delta_rule_bwd_scratch bytes of the caller's, 16-byte aligned;
+ *             unspecified afterwards
+ * Deterministic.  The other rules as delta_rule_fwd.
+ */
+SSM_API int64_t delta_rule_bwd_scratch(int64_t Bs, int64_t L, int64_t G, int64_t H, int64_t K,
+                                       int64_t V, int64_t n_seq, int io_bf16);
+SSM_API ssm_status_t delta_rule_bwd(const void *q, const void *k, const void *g, const void *beta,
+                                    float scale, const int32_t *offsets, const void *dy,
+                                    const float *dh_final, const void *states, const void *errors,
+                                    void *dq, void *dk, void *dv, void *dg, void *dbeta, float *dh0,
+                                    void *scratch, int64_t Bs, int64_t L, int64_t G, int64_t H,
+                                    int64_t K, int64_t V, int64_t n_seq, int io_bf16, void *stream);
+
+/*
+ * One step of the gated delta rule for each row of a batch, on states kept in
+ * pages: states[pages[b]] is updated in place.
+ *   q, k : (Bs, G, K)   v, y : (Bs, H, V)   g, beta : (Bs, H)
+ *   states : (num_pages, H, V, K) fp32
+ *   pages : (Bs) int32 device array, or NULL (row b uses page b).  A row whose
+ *           page lies outside 0..num_pages-1 is idle: y[b] = 0 and no state
+ *           changes.  No page may be named twice.
+ */
+SSM_API ssm_status_t delta_rule_step(const void *q, const void *k, const void *v, const void *g,
+                                     const void *beta, float scale, float *states,
+                                     const int32_t *pages, void *y, int64_t Bs, int64_t G, int64_t H,
+                                     int64_t K, int64_t V, int64_t num_pages, int input_bf16,
+                                     void *stream);
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition:
+ *   s = x + residual (x where that is NULL),  r = (mean of s^2 + eps)^(-1/2),
+ *   y = s r weight          (weight NULL: 1)
+ *   x, residual, sum, y : (rows, cols) fp32 (input_bf16 == 0) or bf16;
+ *   weight : (cols) fp32;  sum = s, with residual != NULL, rounded once
+ *   y_q, y_scale : in the place of y (then NULL), y in 8 bits, in the format of
+ *          ckpt8_save: the fp32 values are rounded once
+ *   rstd : (rows) fp32 or NULL: r, for the gradients
+ * s is fp32 where y is formed from it.  sum may be x or residual; no other
+ * output may overlap an input.  Any sizes >= 1; every pointer is aligned to
+ * its element size.
+ */
+SSM_API ssm_status_t rms_norm_fwd(const void *x, const void *residual, const float *weight, float eps,
+                                  void *sum, void *y, int8_t *y_q, float *y_scale, float *rstd,
+                                  int64_t rows, int64_t cols, int input_bf16, void *stream);
+
+/*
+ * Gradients of rms_norm_fwd for dy and for dsum, the gradient that reaches
+ * s by another way (NULL = 0):
+ *   x, residual : as in the forward call; or residual NULL and its sum in x's
+ *          place, which reads an element less and gives the gradients at s as
+ *          it was rounded
+ *   rstd : what the forward call gave
+ *   dx : the gradient of x, and of the residual   dweight : (cols) fp32 or NULL
+ *   scratch : with dweight, min(rows, 608) rounded up to a multiple of 32, times
+ *             cols floats of the caller's; unspecified afterwards
+ * Deterministic.  No output may overlap an input, but dx may be dsum.
+ */
+SSM_API ssm_status_t rms_norm_bwd(const void *dy, const void *x, const void *residual,
+                                  const float *weight, const float *rstd, const void *dsum, void *dx, float *dweight,
+                                  float *scratch, int64_t rows, int64_t cols, int io_bf16,
+                                  void *stream);
+
+/*
  * Synchronise `stream` and report whether a kernel of this library running on
  * the current device gave up a bounded wait (SSM_ERR_DEVICE_TIMEOUT) since
  * the previous check; the record is cleared by the call.  Kernels never hang

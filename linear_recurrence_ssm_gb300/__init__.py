@@ -28,6 +28,12 @@ ckpt8_save(x), ckpt8_load(q, scale, dtype)
     its inputs this way and ``gated_scan_bwd`` reads them so.
 state_pages_fork / _copy / _free / _compact
     The pages of a state cache.
+delta_rule_fwd(q, k, v, g, beta, ...), delta_rule_bwd, delta_rule_step
+    Gated delta rule (a matrix state per head): forward, gradients, and one
+    token for rows whose states lie in pages.
+rms_norm_fwd(x, weight, residual=None, ...), rms_norm_bwd
+    Root-mean-square norm with the residual's addition, its output in x's type
+    or in 8 bits (``ckpt8_load`` reads it), and its gradients.
 
 Options (of the selective scans; any of them selects the ``*_ex`` C entry point):
 ``dt_bias`` (ED or H, fp32), ``dt_softplus``, ``dt_limit=(lo, hi)``, ``z``
@@ -83,6 +89,12 @@ SIGNATURES = {
     "state_pages_copy": ([_VP] * 3 + [_I64] * 4 + [_VP], ctypes.c_int),
     "state_pages_free": ([_VP] * 2 + [_I64] * 2 + [_VP], ctypes.c_int),
     "state_pages_compact": ([_VP] * 5 + [_I64] * 4 + [_VP], ctypes.c_int),
+    "delta_rule_fwd": ([_VP] * 5 + [_F32] + [_VP] * 6 + [_I64] * 7 + [ctypes.c_int, _VP], ctypes.c_int),
+    "delta_rule_bwd_scratch": ([_I64] * 7 + [ctypes.c_int], _I64),
+    "delta_rule_bwd": ([_VP] * 4 + [_F32] + [_VP] * 12 + [_I64] * 7 + [ctypes.c_int, _VP], ctypes.c_int),
+    "delta_rule_step": ([_VP] * 5 + [_F32] + [_VP] * 3 + [_I64] * 6 + [ctypes.c_int, _VP], ctypes.c_int),
+    "rms_norm_fwd": ([_VP] * 3 + [_F32] + [_VP] * 5 + [_I64] * 2 + [ctypes.c_int, _VP], ctypes.c_int),
+    "rms_norm_bwd": ([_VP] * 9 + [_I64] * 2 + [ctypes.c_int, _VP], ctypes.c_int),
     "ssm_check_device_errors": ([_VP], ctypes.c_int),
     "ssm_selftest_wait_timeout": ([_VP], ctypes.c_int),
     "gated_selftest_wait_timeout": ([ctypes.c_int, ctypes.c_int, _VP], ctypes.c_int),
@@ -759,3 +771,231 @@ def state_pages_compact(pool, used, pages=None, page_dim=0):
           scratch.data_ptr(),
           0 if pages is None else pages.shape[0], layers, n_pages, size)
     return moved
+
+
+# ---- gated delta rule --------------------------------------------------------------------
+def _delta_inputs(q, k, v, g, beta, step):
+    """(device, Bs, L, G, H, K, V) of q, k (Bs, L, G, K), v (Bs, L, H, V) and
+    g, beta (Bs, L, H); without L for a single step.  v may be None, then V is."""
+    import torch
+    for t, n in ((q, "q"), (k, "k"), (g, "g"), (beta, "beta")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % n)
+    if not q.is_cuda:
+        raise ValueError("inputs must be CUDA tensors")
+    dev, dtype = q.device, q.dtype
+    _check(q, "q", (torch.bfloat16, torch.float32), dev, (3 if step else 4,))
+    rows, (G, K) = q.shape[:-2], q.shape[-2:]
+    if g.dim() != len(rows) + 1:
+        raise ValueError("g must have %d dims, got %d" % (len(rows) + 1, g.dim()))
+    H = g.shape[-1]
+    for t, n, shape in ((k, "k", q.shape), (g, "g", (*rows, H)), (beta, "beta", (*rows, H))):
+        if not _fits(t, dtype, shape, dev):
+            _check_shape(t, n, (dtype,), dev, shape)
+    if G < 1 or H % G != 0:
+        raise ValueError("the heads of g (%d) must be a multiple of q's (%d)" % (H, G))
+    V = None
+    if v is not None:
+        if not isinstance(v, torch.Tensor):
+            raise TypeError("v must be a torch.Tensor")
+        V = v.shape[-1] if v.dim() else 0
+        if not _fits(v, dtype, (*rows, H, V), dev):
+            _check_shape(v, "v", (dtype,), dev, (*rows, H, V))
+    return (dev, rows[0], 1 if step else rows[1], G, H, K, V)
+
+
+def _delta_sequences(offsets, Bs, dev):
+    """(sequences, the count that the C entry points take)."""
+    import torch
+    if offsets is None:
+        return Bs, 0
+    if not isinstance(offsets, torch.Tensor):
+        raise TypeError("offsets must be a torch.Tensor")
+    _check(offsets, "offsets", (torch.int32,), dev, (1,))
+    if Bs != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets: (sequences + 1) int32, with a batch of one row")
+    return offsets.shape[0] - 1, offsets.shape[0] - 1
+
+
+def _delta_saved_shapes(Bs, L, H, K, V, n_seq):
+    slots = L // _BLOCK + n_seq if n_seq else Bs * -(-L // _BLOCK)
+    return dict(states=(slots, H, V, K), errors=(Bs, L, H, V))
+
+
+def delta_rule_fwd(q, k, v, g, beta, scale=None, offsets=None, h0=None, return_final_state=False, save=None,
+                   y=None):
+    """Gated delta rule on the current CUDA stream, per head, with a state S (V x K, fp32):
+
+        x_t = v_t - e^g_t S_{t-1} k_t,  S_t = e^g_t S_{t-1} + beta_t x_t k_t^T,  y_t = scale S_t q_t
+
+    q, k: (Bs, L, G, K); v: (Bs, L, H, V); g (the decay's log, <= 0), beta:
+    (Bs, L, H); all bf16 or all fp32; head h reads group h // (H // G).  scale:
+    K ** -0.5 unless given.  offsets: (sequences + 1) int32 starts of sequences
+    packed into a batch of one row (rows outside all of them give 0); h0:
+    (Bs or sequences, H, V, K) fp32.  Returns y, shaped and typed like v; with
+    ``return_final_state`` also h_final, like h0; with ``save="states"`` also
+    the dict that ``delta_rule_bwd`` takes (v itself is not needed there)."""
+    import torch
+    dev, Bs, L, G, H, K, V = _delta_inputs(q, k, v, g, beta, False)
+    if V is None:
+        raise TypeError("v must be a torch.Tensor")
+    n, n_seq = _delta_sequences(offsets, Bs, dev)
+    _check_shape(h0, "h0", (torch.float32,), dev, (n, H, V, K))
+    if save not in (None, "states"):
+        raise ValueError("save must be None or 'states'")
+    if y is None:
+        y = torch.empty_like(v)
+    else:
+        _check_shape(y, "y", (v.dtype,), dev, v.shape)
+    hf = torch.empty((n, H, V, K), dtype=torch.float32, device=dev) if return_final_state else None
+    saved = None
+    if save is not None:
+        saved = {name: torch.empty(shape, dtype=v.dtype, device=dev)
+                 for name, shape in _delta_saved_shapes(Bs, L, H, K, V, n_seq).items()}
+    _call("delta_rule_fwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+          K ** -0.5 if scale is None else scale, _addr(offsets), _addr(h0), y.data_ptr(), _addr(hf),
+          None if saved is None else saved["states"].data_ptr(),
+          None if saved is None else saved["errors"].data_ptr(), Bs, L, G, H, K, V, n_seq,
+          int(v.dtype == torch.bfloat16))
+    out = (y,) + ((hf,) if return_final_state else ()) + ((saved,) if save is not None else ())
+    return out if len(out) > 1 else y
+
+
+def delta_rule_bwd(q, k, g, beta, dy, saved, scale=None, offsets=None, dh_final=None, need_dh0=True):
+    """Gradients of ``delta_rule_fwd`` for dy (shaped and typed like v) and
+    dh_final (like h0; None: 0), from the dict that the forward call saved:
+    dict(dq, dk, dv, dg, dbeta) of the inputs' type and dh0 in fp32 (None
+    without ``need_dh0``).  scale and offsets as in the forward call."""
+    import torch
+    dev, Bs, L, G, H, K, _ = _delta_inputs(q, k, None, g, beta, False)
+    if not isinstance(dy, torch.Tensor):
+        raise TypeError("dy must be a torch.Tensor")
+    V = dy.shape[-1] if dy.dim() else 0
+    if not _fits(dy, q.dtype, (Bs, L, H, V), dev):
+        _check_shape(dy, "dy", (q.dtype,), dev, (Bs, L, H, V))
+    n, n_seq = _delta_sequences(offsets, Bs, dev)
+    if not isinstance(saved, dict) or set(saved) != {"states", "errors"}:
+        raise ValueError("saved must be the dict of delta_rule_fwd(..., save='states')")
+    for name, shape in _delta_saved_shapes(Bs, L, H, K, V, n_seq).items():
+        t = saved[name]
+        if not isinstance(t, torch.Tensor) or not _fits(t, q.dtype, shape, dev):
+            if t is None:
+                raise ValueError("saved[%r] is missing" % name)
+            _check_shape(t, "saved[%r]" % name, (q.dtype,), dev, shape)
+    _check_shape(dh_final, "dh_final", (torch.float32,), dev, (n, H, V, K))
+    out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(dy), dg=torch.empty_like(g),
+               dbeta=torch.empty_like(beta),
+               dh0=torch.empty((n, H, V, K), dtype=torch.float32, device=dev) if need_dh0 else None)
+    bf16 = int(q.dtype == torch.bfloat16)
+    size = library().delta_rule_bwd_scratch(Bs, L, G, H, K, V, n_seq, bf16)
+    scratch = torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
+    _call("delta_rule_bwd", dev, q.data_ptr(), k.data_ptr(), g.data_ptr(), beta.data_ptr(),
+          K ** -0.5 if scale is None else scale, _addr(offsets), dy.data_ptr(), _addr(dh_final),
+          saved["states"].data_ptr(), saved["errors"].data_ptr(), out["dq"].data_ptr(), out["dk"].data_ptr(),
+          out["dv"].data_ptr(), out["dg"].data_ptr(), out["dbeta"].data_ptr(), _addr(out["dh0"]),
+          scratch.data_ptr(), Bs, L, G, H, K, V, n_seq, bf16)
+    return out
+
+
+def delta_rule_step(q, k, v, g, beta, states, pages=None, scale=None, y=None):
+    """One token of the gated delta rule for each row of a batch.  q, k:
+    (Bs, G, K); v: (Bs, H, V); g, beta: (Bs, H); states: (num_pages, H, V, K)
+    fp32, updated in place at row b's page pages[b] ((Bs) int32; None: page
+    b).  A row whose page lies outside the pool is idle: y is 0, no state
+    changes.  Returns y (Bs, H, V) in v's type."""
+    import torch
+    dev, Bs, _, G, H, K, V = _delta_inputs(q, k, v, g, beta, True)
+    if V is None:
+        raise TypeError("v must be a torch.Tensor")
+    if not isinstance(states, torch.Tensor):
+        raise TypeError("states must be a torch.Tensor")
+    _check(states, "states", (torch.float32,), dev, (4,))
+    num_pages = states.shape[0]
+    if states.shape[1:] != (H, V, K):
+        raise ValueError("states must have pages of %s" % ((H, V, K),))
+    if pages is None:
+        if num_pages < Bs:
+            raise ValueError("states has fewer pages than q has rows")
+    else:
+        _check_shape(pages, "pages", (torch.int32,), dev, (Bs,))
+    if y is None:
+        y = torch.empty_like(v)
+    else:
+        _check_shape(y, "y", (v.dtype,), dev, v.shape)
+    _call("delta_rule_step", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+          K ** -0.5 if scale is None else scale, states.data_ptr(), _addr(pages), y.data_ptr(), Bs, G, H, K, V,
+          num_pages, int(v.dtype is torch.bfloat16))
+    return y
+
+
+# ---- root-mean-square norm ---------------------------------------------------------------
+def _norm_input(t, name):
+    """(device, rows, cols) of an activation tensor."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("inputs must be CUDA tensors")
+    _check(t, name, (torch.bfloat16, torch.float32), t.device)
+    if t.dim() < 1:
+        raise ValueError("%s must have at least one dimension" % name)
+    cols = t.shape[-1]
+    return t.device, t.numel() // cols if cols else 0, cols
+
+
+def rms_norm_fwd(x, weight=None, residual=None, eps=1e-6, out="same", save=False):
+    """Root-mean-square norm over the last dimension, with the residual's addition:
+
+        s = x + residual,  y = s (mean(s^2) + eps)^(-1/2) weight
+
+    x, residual: bf16 or fp32, of one shape; weight: (cols) fp32 (None: 1).
+    Returns y in x's type, or with ``out="8bit"`` the pair (q, scale) of
+    ``ckpt8_save``'s format in its place (two entries of the tuple); then s in
+    x's type where there is a residual, and with ``save`` the factors
+    (mean(s^2) + eps)^(-1/2), (rows) fp32, that ``rms_norm_bwd`` takes."""
+    import torch
+    dev, rows, cols = _norm_input(x, "x")
+    if residual is not None and not (isinstance(residual, torch.Tensor) and _fits(residual, x.dtype, x.shape, dev)):
+        _check_shape(residual, "residual", (x.dtype,), dev, x.shape)
+    _check_shape(weight, "weight", (torch.float32,), dev, (cols,))
+    if out not in ("same", "8bit"):
+        raise ValueError("out must be 'same' or '8bit'")
+    y = q = scale = None
+    if out == "same":
+        y = torch.empty_like(x)
+    else:
+        q = torch.empty(x.shape, dtype=torch.int8, device=dev)
+        scale = torch.empty((-(-cols // _BLOCK), rows), dtype=torch.float32, device=dev)
+    s = None if residual is None else torch.empty_like(x)
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev) if save else None
+    _call("rms_norm_fwd", dev, x.data_ptr(), _addr(residual), _addr(weight), eps, _addr(s), _addr(y), _addr(q),
+          _addr(scale), _addr(rstd), rows, cols, int(x.dtype is torch.bfloat16))
+    got = tuple(t for t in (y, q, scale, s, rstd) if t is not None)
+    return got if len(got) > 1 else y
+
+
+def rms_norm_bwd(dy, x, weight, rstd, residual=None, ds=None, need_dweight=True):
+    """Gradients of ``rms_norm_fwd`` for dy (of x's shape and type): dict(dx,
+    dweight).  x, residual: as in the forward call; or the sum that it returned
+    in x's place, without a residual: less to keep and to read, and the
+    gradients at the sum as it was rounded.  rstd: the saved factors; ds: the
+    gradient that reaches s by another way (the residual stream's).  dx is the
+    gradient of x and of the residual; dweight (cols) fp32 (None without a
+    weight or ``need_dweight``)."""
+    import torch
+    dev, rows, cols = _norm_input(dy, "dy")
+    if x is None or rstd is None:
+        raise TypeError("x and rstd must be torch.Tensors")
+    for t, n in ((x, "x"), (residual, "residual"), (ds, "ds")):
+        if t is not None and not (isinstance(t, torch.Tensor) and _fits(t, dy.dtype, dy.shape, dev)):
+            _check_shape(t, n, (dy.dtype,), dev, dy.shape)
+    _check_shape(weight, "weight", (torch.float32,), dev, (cols,))
+    _check_shape(rstd, "rstd", (torch.float32,), dev, (rows,))
+    dx = torch.empty_like(dy)
+    dweight = scratch = None
+    if weight is not None and need_dweight:
+        dweight = torch.empty(cols, dtype=torch.float32, device=dev)
+        scratch = torch.empty(min(-(-rows // 32) * 32, 608) * cols, dtype=torch.float32, device=dev)
+    _call("rms_norm_bwd", dev, dy.data_ptr(), x.data_ptr(), _addr(residual), _addr(weight), rstd.data_ptr(),
+          _addr(ds), dx.data_ptr(), _addr(dweight), _addr(scratch), rows, cols, int(dy.dtype is torch.bfloat16))
+    return dict(dx=dx, dweight=dweight)

@@ -7,6 +7,7 @@
 #include <limits.h>
 #include <mutex>
 
+#include "delta_rule.cuh"
 #include "gated_scan.cuh"
 #include "ssm_common.cuh"
 
@@ -103,6 +104,31 @@ cudaError_t free_pages(uint8_t *used, const int32_t *pages, int64_t n, int64_t n
 cudaError_t compact(void *pool, uint8_t *used, int32_t *moved, int32_t *pages, int32_t *scratch,
                     int64_t n, int64_t layers, int64_t num_pages, int64_t bytes, int num_sms,
                     cudaStream_t st);
+}
+namespace delta {
+namespace general {
+int slices(const Shape &s);
+template <typename T>
+cudaError_t fwd(const FwdArgs<T> &a, cudaStream_t st);
+template <typename T>
+cudaError_t bwd(const BwdArgs<T> &a, cudaStream_t st);
+}
+namespace step {
+template <typename T>
+cudaError_t launch(const T *q, const T *k, const T *v, const T *g, const T *beta, float scale,
+                   float *states, const int32_t *pages, T *y, int64_t Bs, int64_t G, int64_t H,
+                   int64_t K, int64_t V, int64_t num_pages, cudaStream_t st);
+}
+}
+namespace norm {
+template <typename T>
+cudaError_t launch_fwd(const T *x, const T *residual, const float *weight, float eps, T *sum, T *y,
+                       int8_t *q, float *scale, float *rstd, int64_t rows, int64_t cols,
+                       cudaStream_t st);
+template <typename T>
+cudaError_t launch_bwd(const T *dy, const T *s, const T *residual, const float *weight,
+                       const float *rstd, const T *ds, T *dx, float *dweight, float *scratch, int64_t rows, int64_t cols,
+                       cudaStream_t st);
 }
 namespace bidir {
 cudaError_t take_device_error(unsigned int *out);
@@ -407,6 +433,165 @@ ssm_status_t check_pool(const void *pool, int64_t n, int64_t layers, int64_t num
     if (num_pages > SSM_MAX_PAGES) return SSM_ERR_UNSUPPORTED;
     return current_device(dev);
 }
+// The sizes of a call of the gated delta rule; `packed` sequences share one
+// row of the batch.
+ssm_status_t check_delta_sizes(int64_t Bs, int64_t L, int64_t G, int64_t H, int64_t K, int64_t V,
+                               int64_t n_seq, float scale) {
+    if (!sizes_ok({Bs, L, H, V, 4}) || !sizes_ok({Bs, L, G, K, 4}) || !sizes_ok({Bs, L, H, K, 4}) ||
+        !sizes_ok({Bs, H, K, V, 4}) || n_seq < 0 || (n_seq > 0 && Bs != 1) || H % G != 0 ||
+        !(scale >= -FLT_MAX && scale <= FLT_MAX))
+        return SSM_ERR_INVALID_ARG;
+    if (n_seq > 0 && !sizes_ok({n_seq, H, K, V, 4})) return SSM_ERR_INVALID_ARG;
+    // room for the steps behind the end; a block a head and 64 steps in the grid
+    if (K > 256 || V > 256 || L > INT_MAX - 4096 || Bs > INT_MAX / 2 || n_seq > INT_MAX / 2 || H > INT_MAX / 2)
+        return SSM_ERR_UNSUPPORTED;
+    const int64_t slots = n_seq > 0 ? L / 64 + n_seq : Bs * ((L + 63) / 64);
+    if (!sizes_ok({slots, H, K, V, 4})) return SSM_ERR_INVALID_ARG;
+    return slots * H > INT_MAX ? SSM_ERR_UNSUPPORTED : SSM_OK;
+}
+
+ssm::delta::Shape delta_shape(const int32_t *offsets, int64_t Bs, int64_t L, int64_t G, int64_t H,
+                              int64_t K, int64_t V, int64_t n_seq, float scale) {
+    ssm::delta::Shape s{};
+    s.offsets = offsets;
+    s.L = L;
+    s.n = int(offsets ? n_seq : Bs);
+    s.G = int(G), s.H = int(H), s.K = int(K), s.V = int(V);
+    s.scale = scale;
+    return s;
+}
+
+template <typename T>
+ssm_status_t delta_fwd_entry(const void *q, const void *k, const void *v, const void *g,
+                             const void *beta, float scale, const int32_t *offsets,
+                             const float *h0, void *y, float *h_final, void *states, void *errors,
+                             int64_t Bs, int64_t L, int64_t G, int64_t H, int64_t K, int64_t V,
+                             int64_t n_seq, void *stream) {
+    if (!q || !k || !v || !g || !beta || !y || !states != !errors || (n_seq > 0) != (offsets != nullptr))
+        return SSM_ERR_INVALID_ARG;
+    ssm_status_t s = check_delta_sizes(Bs, L, G, H, K, V, n_seq, scale);
+    if (s != SSM_OK) return s;
+    const size_t e = sizeof(T);
+    for (const void *p : {q, k, v, g, beta, static_cast<const void *>(y), static_cast<const void *>(states),
+                          static_cast<const void *>(errors)})
+        if (!aligned(p, e)) return SSM_ERR_ALIGNMENT;
+    if (!aligned(offsets, 4) || !aligned(h0, 4) || !aligned(h_final, 4)) return SSM_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    s = current_device(&dev);
+    if (s != SSM_OK) return s;
+    const ssm::delta::FwdArgs<T> a{delta_shape(offsets, Bs, L, G, H, K, V, n_seq, scale),
+                                   static_cast<const T *>(q), static_cast<const T *>(k),
+                                   static_cast<const T *>(v), static_cast<const T *>(g),
+                                   static_cast<const T *>(beta), h0, static_cast<T *>(y), h_final,
+                                   static_cast<T *>(states), static_cast<T *>(errors)};
+    return from_cuda(ssm::delta::general::fwd(a, static_cast<cudaStream_t>(stream)));
+}
+
+template <typename T>
+ssm_status_t delta_bwd_entry(const void *q, const void *k, const void *g, const void *beta,
+                             float scale, const int32_t *offsets, const void *dy,
+                             const float *dh_final, const void *states, const void *errors,
+                             void *dq, void *dk, void *dv, void *dg, void *dbeta, float *dh0,
+                             void *scratch, int64_t Bs, int64_t L, int64_t G, int64_t H, int64_t K,
+                             int64_t V, int64_t n_seq, void *stream) {
+    if (!q || !k || !g || !beta || !dy || !states || !errors || !dq || !dk || !dv || !dg || !dbeta ||
+        !scratch || (n_seq > 0) != (offsets != nullptr))
+        return SSM_ERR_INVALID_ARG;
+    ssm_status_t s = check_delta_sizes(Bs, L, G, H, K, V, n_seq, scale);
+    if (s != SSM_OK) return s;
+    const size_t e = sizeof(T);
+    for (const void *p : {q, k, g, beta, dy, states, errors, static_cast<const void *>(dq),
+                          static_cast<const void *>(dk), static_cast<const void *>(dv),
+                          static_cast<const void *>(dg), static_cast<const void *>(dbeta)})
+        if (!aligned(p, e)) return SSM_ERR_ALIGNMENT;
+    if (!aligned(offsets, 4) || !aligned(dh_final, 4) || !aligned(dh0, 4) || !aligned(scratch, 16))
+        return SSM_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    s = current_device(&dev);
+    if (s != SSM_OK) return s;
+    const ssm::delta::Shape shape = delta_shape(offsets, Bs, L, G, H, K, V, n_seq, scale);
+    const ssm::delta::Scratch at = ssm::delta::scratch_of(shape, int(e), ssm::delta::general::slices(shape));
+    char *mem = static_cast<char *>(scratch);
+    const ssm::delta::BwdArgs<T> a{shape, static_cast<const T *>(q), static_cast<const T *>(k),
+                                   static_cast<const T *>(g), static_cast<const T *>(beta),
+                                   static_cast<const T *>(dy), dh_final, static_cast<const T *>(states),
+                                   static_cast<const T *>(errors), static_cast<T *>(dq),
+                                   static_cast<T *>(dk), static_cast<T *>(dv), static_cast<T *>(dg),
+                                   static_cast<T *>(dbeta), dh0, reinterpret_cast<T *>(mem + at.ds),
+                                   reinterpret_cast<float *>(mem + at.dbeta),
+                                   reinterpret_cast<float *>(mem + at.dq),
+                                   reinterpret_cast<float *>(mem + at.dk)};
+    return from_cuda(ssm::delta::general::bwd(a, static_cast<cudaStream_t>(stream)));
+}
+
+template <typename T>
+ssm_status_t delta_step_entry(const void *q, const void *k, const void *v, const void *g,
+                              const void *beta, float scale, float *states, const int32_t *pages,
+                              void *y, int64_t Bs, int64_t G, int64_t H, int64_t K, int64_t V,
+                              int64_t num_pages, void *stream) {
+    if (!q || !k || !v || !g || !beta || !states || !y) return SSM_ERR_INVALID_ARG;
+    ssm_status_t s = check_delta_sizes(Bs, 1, G, H, K, V, 0, scale);
+    if (s != SSM_OK) return s;
+    if (!sizes_ok({num_pages, H, K, V, 4}) || (!pages && num_pages < Bs)) return SSM_ERR_INVALID_ARG;
+    if (num_pages > SSM_MAX_PAGES) return SSM_ERR_UNSUPPORTED;
+    const size_t e = sizeof(T);
+    for (const void *p : {q, k, v, g, beta, static_cast<const void *>(y)})
+        if (!aligned(p, e)) return SSM_ERR_ALIGNMENT;
+    if (!aligned(states, 4) || !aligned(pages, 4)) return SSM_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    s = current_device(&dev);
+    if (s != SSM_OK) return s;
+    return from_cuda(ssm::delta::step::launch(static_cast<const T *>(q), static_cast<const T *>(k),
+                                              static_cast<const T *>(v), static_cast<const T *>(g),
+                                              static_cast<const T *>(beta), scale, states, pages,
+                                              static_cast<T *>(y), Bs, G, H, K, V, num_pages,
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+ssm_status_t check_norm(const void *a, const void *b, float eps, int64_t rows, int64_t cols) {
+    if (!a || !b || !sizes_ok({rows, cols, 4}) || !(eps >= 0.0f) || eps > FLT_MAX) return SSM_ERR_INVALID_ARG;
+    return rows > INT_MAX || cols > INT_MAX - 4096 ? SSM_ERR_UNSUPPORTED : SSM_OK;
+}
+
+template <typename T>
+ssm_status_t norm_fwd_entry(const void *x, const void *residual, const float *weight, float eps,
+                            void *sum, void *y, int8_t *y_q, float *y_scale, float *rstd,
+                            int64_t rows, int64_t cols, void *stream) {
+    if (!residual != !sum || !y_q != !y_scale || !y == !y_q) return SSM_ERR_INVALID_ARG;
+    ssm_status_t s = check_norm(x, y ? y : y_q, eps, rows, cols);
+    if (s != SSM_OK) return s;
+    const size_t e = sizeof(T);
+    if (!aligned(x, e) || !aligned(residual, e) || !aligned(sum, e) || !aligned(y, e) || !aligned(weight, 4) ||
+        !aligned(y_scale, 4) || !aligned(rstd, 4))
+        return SSM_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    s = current_device(&dev);
+    if (s != SSM_OK) return s;
+    return from_cuda(ssm::norm::launch_fwd(static_cast<const T *>(x), static_cast<const T *>(residual), weight,
+                                           eps, static_cast<T *>(sum), static_cast<T *>(y), y_q, y_scale, rstd,
+                                           rows, cols, static_cast<cudaStream_t>(stream)));
+}
+
+template <typename T>
+ssm_status_t norm_bwd_entry(const void *dy, const void *x, const void *residual, const float *weight, const float *rstd,
+                            const void *dsum, void *dx, float *dweight, float *scratch, int64_t rows,
+                            int64_t cols, void *stream) {
+    if (!x || !rstd || (dweight && !scratch)) return SSM_ERR_INVALID_ARG;
+    ssm_status_t s = check_norm(dy, dx, 0.0f, rows, cols);
+    if (s != SSM_OK) return s;
+    const size_t e = sizeof(T);
+    if (!aligned(dy, e) || !aligned(x, e) || !aligned(residual, e) || !aligned(dsum, e) || !aligned(dx, e) || !aligned(weight, 4) ||
+        !aligned(rstd, 4) || !aligned(dweight, 4) || !aligned(scratch, 4))
+        return SSM_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    s = current_device(&dev);
+    if (s != SSM_OK) return s;
+    return from_cuda(ssm::norm::launch_bwd(static_cast<const T *>(dy), static_cast<const T *>(x),
+                                           static_cast<const T *>(residual), weight, rstd,
+                                           static_cast<const T *>(dsum), static_cast<T *>(dx), dweight, scratch,
+                                           rows, cols, static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -747,6 +932,68 @@ ssm_status_t state_pages_compact(void *pool, uint8_t *used, int32_t *moved, int3
     if (s != SSM_OK) return s;
     return from_cuda(ssm::pages::compact(pool, used, moved, pages, scratch, n, layers, num_pages, page_bytes,
                                          dev.num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+ssm_status_t delta_rule_fwd(const void *q, const void *k, const void *v, const void *g,
+                            const void *beta, float scale, const int32_t *offsets, const float *h0,
+                            void *y, float *h_final, void *states, void *errors, int64_t Bs,
+                            int64_t L, int64_t G, int64_t H, int64_t K, int64_t V, int64_t n_seq,
+                            int input_bf16, void *stream) {
+    return input_bf16 ? delta_fwd_entry<__nv_bfloat16>(q, k, v, g, beta, scale, offsets, h0, y, h_final,
+                                                       states, errors, Bs, L, G, H, K, V, n_seq, stream)
+                      : delta_fwd_entry<float>(q, k, v, g, beta, scale, offsets, h0, y, h_final, states,
+                                               errors, Bs, L, G, H, K, V, n_seq, stream);
+}
+
+int64_t delta_rule_bwd_scratch(int64_t Bs, int64_t L, int64_t G, int64_t H, int64_t K, int64_t V,
+                               int64_t n_seq, int io_bf16) {
+    if (check_delta_sizes(Bs, L, G, H, K, V, n_seq, 1.0f) != SSM_OK) return 0;
+    // the sequences' offsets are not looked at, only that there are some
+    static const int32_t some = 0;
+    const ssm::delta::Shape s = delta_shape(n_seq > 0 ? &some : nullptr, Bs, L, G, H, K, V, n_seq, 1.0f);
+    return ssm::delta::scratch_of(s, io_bf16 ? 2 : 4, ssm::delta::general::slices(s)).bytes;
+}
+
+ssm_status_t delta_rule_bwd(const void *q, const void *k, const void *g, const void *beta, float scale,
+                            const int32_t *offsets, const void *dy, const float *dh_final,
+                            const void *states, const void *errors, void *dq, void *dk, void *dv,
+                            void *dg, void *dbeta, float *dh0, void *scratch, int64_t Bs, int64_t L,
+                            int64_t G, int64_t H, int64_t K, int64_t V, int64_t n_seq, int io_bf16,
+                            void *stream) {
+    return io_bf16 ? delta_bwd_entry<__nv_bfloat16>(q, k, g, beta, scale, offsets, dy, dh_final, states,
+                                                    errors, dq, dk, dv, dg, dbeta, dh0, scratch, Bs, L, G,
+                                                    H, K, V, n_seq, stream)
+                   : delta_bwd_entry<float>(q, k, g, beta, scale, offsets, dy, dh_final, states, errors,
+                                            dq, dk, dv, dg, dbeta, dh0, scratch, Bs, L, G, H, K, V, n_seq,
+                                            stream);
+}
+
+ssm_status_t delta_rule_step(const void *q, const void *k, const void *v, const void *g,
+                             const void *beta, float scale, float *states, const int32_t *pages,
+                             void *y, int64_t Bs, int64_t G, int64_t H, int64_t K, int64_t V,
+                             int64_t num_pages, int input_bf16, void *stream) {
+    return input_bf16 ? delta_step_entry<__nv_bfloat16>(q, k, v, g, beta, scale, states, pages, y, Bs, G, H,
+                                                        K, V, num_pages, stream)
+                      : delta_step_entry<float>(q, k, v, g, beta, scale, states, pages, y, Bs, G, H, K, V,
+                                                num_pages, stream);
+}
+
+ssm_status_t rms_norm_fwd(const void *x, const void *residual, const float *weight, float eps,
+                          void *sum, void *y, int8_t *y_q, float *y_scale, float *rstd, int64_t rows,
+                          int64_t cols, int input_bf16, void *stream) {
+    return input_bf16 ? norm_fwd_entry<__nv_bfloat16>(x, residual, weight, eps, sum, y, y_q, y_scale, rstd,
+                                                      rows, cols, stream)
+                      : norm_fwd_entry<float>(x, residual, weight, eps, sum, y, y_q, y_scale, rstd, rows,
+                                              cols, stream);
+}
+
+ssm_status_t rms_norm_bwd(const void *dy, const void *x, const void *residual, const float *weight, const float *rstd,
+                          const void *dsum, void *dx, float *dweight, float *scratch, int64_t rows,
+                          int64_t cols, int io_bf16, void *stream) {
+    return io_bf16 ? norm_bwd_entry<__nv_bfloat16>(dy, x, residual, weight, rstd, dsum, dx, dweight, scratch, rows,
+                                                   cols, stream)
+                   : norm_bwd_entry<float>(dy, x, residual, weight, rstd, dsum, dx, dweight, scratch, rows, cols,
+                                           stream);
 }
 
 ssm_status_t ssm_check_device_errors(void *stream) {

@@ -1,0 +1,689 @@
+// delta_general.cu -- the gated delta rule on CUDA cores, in fp32 throughout,
+// for every type and head size (K, V up to 256): the path for fp32 inputs and
+// for sizes without a tensor-core form.
+//
+// A thread block takes one head of one sequence and 32 rows of its state (the
+// rows are independent of one another), and walks the sequence 64 steps at a
+// time with the state in shared memory; the unit triangular system of a block
+// is solved by substitution, 16 rows at a time.
+#include "delta_rule.cuh"
+
+namespace ssm {
+namespace delta {
+namespace general {
+
+constexpr int kSlice = 32, kThreads = 256;
+constexpr int kPairs = kBlock + 4, kRow = kSlice + 4;      // row strides, in floats
+
+__host__ __device__ inline int padded(int K) { return (K + 3) / 4 * 4; }
+__host__ __device__ inline int stride_of(int K) { return padded(K) + 4; }
+
+// `rows` rows of `width` elements, `step` elements apart, as floats; zeros up to 64 x `cols`.
+template <typename T>
+__device__ __forceinline__ void load_tile(float *tile, int stride, const T *src, int64_t step, int rows, int width,
+                                          int cols) {
+    for (int i = threadIdx.x; i < kBlock * cols; i += kThreads) {
+        const int t = i / cols, c = i - t * cols;
+        tile[t * stride + c] = t < rows && c < width ? to_f32(src[t * step + c]) : 0.0f;
+    }
+}
+
+// The 4 x 4 products of this thread's rows ty + 16 i of `a` and tx + 16 j of `b`.
+__device__ __forceinline__ void products(float (&out)[4][4], const float *a, const float *b, int stride, int Kp) {
+    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) out[i / 4][i % 4] = 0.0f;
+    for (int k = 0; k < Kp; k += 4) {
+        float4 u[4], w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            u[i] = *reinterpret_cast<const float4 *>(a + (ty + 16 * i) * stride + k);
+            w[i] = *reinterpret_cast<const float4 *>(b + (tx + 16 * i) * stride + k);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                out[i][j] += u[i].x * w[j].x + u[i].y * w[j].y + u[i].z * w[j].z + u[i].w * w[j].w;
+    }
+}
+
+// Rows t and t + 32 of `a` times four rows v.. of the state: out[i][j] = a_(t + 32 i) . S_(v + j).
+__device__ __forceinline__ void through_state(float (&out)[2][4], const float *a, const float *S, int stride, int Kp,
+                                              int t, int v) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i / 4][i % 4] = 0.0f;
+    for (int k = 0; k < Kp; k += 4) {
+        float4 u[2], w[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) u[i] = *reinterpret_cast<const float4 *>(a + (t + 32 * i) * stride + k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const float4 *>(S + (v + j) * stride + k);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                out[i][j] += u[i].x * w[j].x + u[i].y * w[j].y + u[i].z * w[j].z + u[i].w * w[j].w;
+    }
+}
+
+__device__ __forceinline__ void fma4(float4 &o, float a, const float4 &b) {
+    o.x += a * b.x, o.y += a * b.y, o.z += a * b.z, o.w += a * b.w;
+}
+
+struct Layout {
+    int stride, q, k, s, a, p, w, x, words;
+};
+__host__ __device__ inline Layout layout_of(int K) {
+    Layout l;
+    l.stride = stride_of(K);
+    l.q = 0;
+    l.k = l.q + kBlock * l.stride;
+    l.s = l.k + kBlock * l.stride;
+    l.a = l.s + kSlice * l.stride;
+    l.p = l.a + kBlock * kPairs;
+    l.w = l.p + kBlock * kPairs;
+    l.x = l.w + kBlock * kRow;
+    l.words = l.x + kBlock * kRow;
+    return l;
+}
+
+// Which head, sequence and rows of the state a thread block has.
+struct Work {
+    int seq, head, group, v0, width;
+};
+__device__ __forceinline__ Work work_of(const Shape &s) {
+    const int slices = (s.V + kSlice - 1) / kSlice;
+    const int64_t at = blockIdx.x;
+    Work w;
+    w.v0 = int(at % slices) * kSlice;
+    w.head = int(at / slices % s.H);
+    w.seq = int(at / slices / s.H);
+    w.group = w.head / (s.H / s.G);
+    w.width = min(kSlice, s.V - w.v0);
+    return w;
+}
+
+// Elements [v0, v0 + width) of the rows of `out` (H x V a row) that no sequence covers become 0.
+template <typename T>
+__device__ __forceinline__ void clear_uncovered(const Shape &s, int seq, T *out, int64_t step, int width) {
+    if (!s.offsets || out == nullptr) return;
+    int64_t a = 0, b = 0;
+    for (int part = 0; part < 2; ++part) {
+        if (part == 0) {
+            if (seq != 0) continue;
+            a = 0, b = span_of(s, 0).first;
+        } else {
+            if (seq != s.n - 1) continue;
+            const Span last = span_of(s, s.n - 1);
+            a = last.first + last.len, b = s.L;
+        }
+        for (int64_t i = threadIdx.x; i < (b - a) * width; i += blockDim.x)
+            put(out + (a + i / width) * step + i % width, 0.0f);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdArgs<T> p) {
+    extern __shared__ __align__(16) float mem[];
+    __shared__ Decays d;
+    const Shape &s = p.s;
+    const Layout l = layout_of(s.K);
+    float *Q = mem + l.q, *Kt = mem + l.k, *S = mem + l.s, *A = mem + l.a, *P = mem + l.p, *W = mem + l.w;
+    const int Kp = padded(s.K), tid = threadIdx.x;
+    const Work w = work_of(s);
+    const Span span = span_of(s, w.seq);
+    const int64_t qk_step = int64_t(s.G) * s.K, v_step = int64_t(s.H) * s.V;
+    const int64_t state_at = (int64_t(w.seq) * s.H + w.head) * s.V * s.K + int64_t(w.v0) * s.K;
+
+    for (int i = tid; i < kSlice * Kp; i += kThreads) {
+        const int v = i / Kp, k = i - v * Kp;
+        S[v * l.stride + k] = p.h0 && v < w.width && k < s.K ? p.h0[state_at + int64_t(v) * s.K + k] : 0.0f;
+    }
+    const int t0 = tid / 8, v4 = tid % 8 * 4;
+    for (int c = 0; c < span.blocks; ++c) {
+        const int rows = min(kBlock, span.len - c * kBlock);
+        const int64_t row = span.first + int64_t(c) * kBlock;
+        __syncthreads();
+        load_tile(Q, l.stride, p.q + row * qk_step + int64_t(w.group) * s.K, qk_step, rows, s.K, Kp);
+        load_tile(Kt, l.stride, p.k + row * qk_step + int64_t(w.group) * s.K, qk_step, rows, s.K, Kp);
+        load_tile(W, kRow, p.v + row * v_step + int64_t(w.head) * s.V + w.v0, v_step, rows, w.width, kSlice);
+        if (tid < 32) load_decays(d, p.g + row * s.H + w.head, p.beta + row * s.H + w.head, s.H, rows);
+        __syncthreads();
+        if (p.states) {
+            T *out = p.states + ((span.slot + c) * s.H + w.head) * int64_t(s.V) * s.K + int64_t(w.v0) * s.K;
+            for (int i = tid; i < w.width * s.K; i += kThreads) {
+                const int v = i / s.K, k = i - v * s.K;
+                put(out + i, S[v * l.stride + k]);
+            }
+        }
+        float m[4][4];
+        const int tx = tid % 16, ty = tid / 16;
+        products(m, Kt, Kt, l.stride, Kp);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int t = ty + 16 * (i / 4), r = tx + 16 * (i % 4);
+            A[t * kPairs + r] = r < t ? m[i / 4][i % 4] * d.between(t, r) * d.beta[r] : 0.0f;
+        }
+        products(m, Q, Kt, l.stride, Kp);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int t = ty + 16 * (i / 4), r = tx + 16 * (i % 4);
+            P[t * kPairs + r] = r <= t ? m[i / 4][i % 4] * d.between(t, r) : 0.0f;
+        }
+        float from[2][4], y[2][4];
+        through_state(from, Kt, S, l.stride, Kp, t0, v4);
+        through_state(y, Q, S, l.stride, Kp, t0, v4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int t = t0 + 32 * (i / 4);
+            const float start = d.start(t);
+            // a cut drops the state before it, whatever that holds
+            W[t * kRow + v4 + i % 4] -= start == 0.0f ? 0.0f : start * from[i / 4][i % 4];
+            y[i / 4][i % 4] = start == 0.0f ? 0.0f : start * y[i / 4][i % 4];
+        }
+        __syncthreads();
+        // X from W, 16 rows at a time
+        for (int b = 0; b < kBlock; b += 16) {
+            if (tid < kSlice) {
+                float x[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    x[i] = W[(b + i) * kRow + tid];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (j < i) x[i] -= A[(b + i) * kPairs + b + j] * x[j];
+                    W[(b + i) * kRow + tid] = x[i];
+                }
+            }
+            __syncthreads();
+            for (int i = tid + (b + 16) * kSlice; i < kBlock * kSlice; i += kThreads) {
+                const int t = i / kSlice, v = i % kSlice;
+                float sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sum += A[t * kPairs + b + j] * W[(b + j) * kRow + v];
+                W[t * kRow + v] -= sum;
+            }
+            __syncthreads();
+        }
+        if (p.errors) {
+            T *out = p.errors + row * v_step + int64_t(w.head) * s.V + w.v0;
+            for (int i = tid; i < rows * w.width; i += kThreads) {
+                const int t = i / w.width, v = i - t * w.width;
+                put(out + t * v_step + v, W[t * kRow + v]);
+            }
+            __syncthreads();
+        }
+        for (int i = tid; i < kBlock * kSlice; i += kThreads) W[i / kSlice * kRow + i % kSlice] *= d.beta[i / kSlice];
+        __syncthreads();
+        // outputs of rows t0 and t0 + 32, four columns
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = t0 + 32 * i;
+            float4 o = make_float4(y[i][0], y[i][1], y[i][2], y[i][3]);
+            for (int r = 0; r <= t; ++r) fma4(o, P[t * kPairs + r], *reinterpret_cast<const float4 *>(W + r * kRow + v4));
+            if (t < rows) {
+                T *out = p.y + (row + t) * v_step + int64_t(w.head) * s.V + w.v0 + v4;
+                const float v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (v4 + j < w.width) put(out + j, s.scale * v[j]);
+            }
+        }
+        const float last = d.start(kBlock - 1);
+        __syncthreads();
+        for (int i = tid; i < kBlock * kSlice; i += kThreads) W[i / kSlice * kRow + i % kSlice] *= d.end(i / kSlice);
+        __syncthreads();
+        for (int i = tid; i < kSlice / 4 * (Kp / 4); i += kThreads) {
+            const int v = i % (kSlice / 4) * 4, k = i / (kSlice / 4) * 4;
+            float4 o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                o[j] = *reinterpret_cast<const float4 *>(S + (v + j) * l.stride + k);
+                o[j] = last == 0.0f ? make_float4(0, 0, 0, 0)
+                                    : make_float4(last * o[j].x, last * o[j].y, last * o[j].z, last * o[j].w);
+            }
+            for (int t = 0; t < rows; ++t) {
+                const float4 u = *reinterpret_cast<const float4 *>(W + t * kRow + v);
+                const float4 kk = *reinterpret_cast<const float4 *>(Kt + t * l.stride + k);
+                fma4(o[0], u.x, kk), fma4(o[1], u.y, kk), fma4(o[2], u.z, kk), fma4(o[3], u.w, kk);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<float4 *>(S + (v + j) * l.stride + k) = o[j];
+        }
+    }
+    __syncthreads();
+    if (p.h_final)
+        for (int i = tid; i < w.width * s.K; i += kThreads) {
+            const int v = i / s.K, k = i - v * s.K;
+            p.h_final[state_at + i] = S[v * l.stride + k];
+        }
+    clear_uncovered(s, w.seq, p.y + int64_t(w.head) * s.V + w.v0, v_step, w.width);
+}
+
+// Back along a sequence: dv, the shares of dbeta, the adjoint of every
+// block's last state (into the scratch) and of the first one.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) back_kernel(const BwdArgs<T> p) {
+    extern __shared__ __align__(16) float mem[];
+    __shared__ Decays d;
+    const Shape &s = p.s;
+    const Layout l = layout_of(s.K);
+    float *Q = mem + l.q, *Kt = mem + l.k, *S = mem + l.s, *A = mem + l.a, *P = mem + l.p, *Y = mem + l.w,
+          *Z = mem + l.x;
+    const int Kp = padded(s.K), tid = threadIdx.x;
+    const Work w = work_of(s);
+    const Span span = span_of(s, w.seq);
+    const int64_t qk_step = int64_t(s.G) * s.K, v_step = int64_t(s.H) * s.V;
+    const int64_t state_at = (int64_t(w.seq) * s.H + w.head) * s.V * s.K + int64_t(w.v0) * s.K;
+    const int64_t rows_all = s.offsets ? s.L : s.L * s.n;
+    float *part = p.dbeta_part + int64_t(w.v0 / kSlice) * rows_all * s.H + w.head;
+
+    for (int i = tid; i < kSlice * Kp; i += kThreads) {
+        const int v = i / Kp, k = i - v * Kp;
+        S[v * l.stride + k] =
+            p.dh_final && v < w.width && k < s.K ? p.dh_final[state_at + int64_t(v) * s.K + k] : 0.0f;
+    }
+    const int t0 = tid / 8, v4 = tid % 8 * 4;
+    for (int c = span.blocks - 1; c >= 0; --c) {
+        const int rows = min(kBlock, span.len - c * kBlock);
+        const int64_t row = span.first + int64_t(c) * kBlock;
+        __syncthreads();
+        load_tile(Q, l.stride, p.q + row * qk_step + int64_t(w.group) * s.K, qk_step, rows, s.K, Kp);
+        load_tile(Kt, l.stride, p.k + row * qk_step + int64_t(w.group) * s.K, qk_step, rows, s.K, Kp);
+        load_tile(Y, kRow, p.dy + row * v_step + int64_t(w.head) * s.V + w.v0, v_step, rows, w.width, kSlice);
+        if (tid < 32) load_decays(d, p.g + row * s.H + w.head, p.beta + row * s.H + w.head, s.H, rows);
+        __syncthreads();
+        T *ds = p.ds + ((span.slot + c) * s.H + w.head) * int64_t(s.V) * s.K + int64_t(w.v0) * s.K;
+        for (int i = tid; i < w.width * s.K; i += kThreads) {
+            const int v = i / s.K, k = i - v * s.K;
+            put(ds + i, S[v * l.stride + k]);
+        }
+        float m[4][4];
+        const int tx = tid % 16, ty = tid / 16;
+        products(m, Kt, Kt, l.stride, Kp);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int t = ty + 16 * (i / 4), r = tx + 16 * (i % 4);
+            A[t * kPairs + r] = r < t ? m[i / 4][i % 4] * d.between(t, r) * d.beta[t] : 0.0f;
+        }
+        products(m, Q, Kt, l.stride, Kp);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int t = ty + 16 * (i / 4), r = tx + 16 * (i % 4);
+            P[t * kPairs + r] = r <= t ? s.scale * m[i / 4][i % 4] * d.between(t, r) : 0.0f;
+        }
+        float from[2][4];
+        through_state(from, Kt, S, l.stride, Kp, t0, v4);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = t0 + 32 * i;
+            const float end = d.end(t);
+            float4 o = end == 0.0f ? make_float4(0, 0, 0, 0)
+                                   : make_float4(end * from[i][0], end * from[i][1], end * from[i][2], end * from[i][3]);
+            for (int r = t; r < rows; ++r) fma4(o, P[r * kPairs + t], *reinterpret_cast<const float4 *>(Y + r * kRow + v4));
+            *reinterpret_cast<float4 *>(Z + t * kRow + v4) = o;
+        }
+        __syncthreads();
+        for (int b = kBlock - 16; b >= 0; b -= 16) {
+            if (tid < kSlice) {
+                float x[16];
+#pragma unroll
+                for (int i = 15; i >= 0; --i) {
+                    x[i] = Z[(b + i) * kRow + tid];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (j > i) x[i] -= A[(b + j) * kPairs + b + i] * x[j];
+                    Z[(b + i) * kRow + tid] = x[i];
+                }
+            }
+            __syncthreads();
+            for (int i = tid; i < b * kSlice; i += kThreads) {
+                const int t = i / kSlice, v = i % kSlice;
+                float sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sum += A[(b + j) * kPairs + t] * Z[(b + j) * kRow + v];
+                Z[t * kRow + v] -= sum;
+            }
+            __syncthreads();
+        }
+        // a warp takes a row at a time: dbeta's share, dv, and beta Z in Z's place
+        {
+            const int lane = tid % 32;
+            const T *x = p.errors + row * v_step + int64_t(w.head) * s.V + w.v0;
+            T *dv = p.dv + row * v_step + int64_t(w.head) * s.V + w.v0;
+            for (int t = tid / 32; t < kBlock; t += kThreads / 32) {
+                const float z = Z[t * kRow + lane], bz = d.beta[t] * z;
+                float sum = t < rows && lane < w.width ? z * to_f32(x[t * v_step + lane]) : 0.0f;
+#pragma unroll
+                for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (t < rows) {
+                    if (lane < w.width) put(dv + t * v_step + lane, bz);
+                    if (lane == 0) part[(row + t) * s.H] = sum;
+                }
+                const float start = d.start(t);
+                Z[t * kRow + lane] = -start * bz;
+                Y[t * kRow + lane] *= s.scale * start;
+            }
+        }
+        const float last = d.start(kBlock - 1);
+        __syncthreads();
+        for (int i = tid; i < kSlice / 4 * (Kp / 4); i += kThreads) {
+            const int v = i % (kSlice / 4) * 4, k = i / (kSlice / 4) * 4;
+            float4 o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                o[j] = *reinterpret_cast<const float4 *>(S + (v + j) * l.stride + k);
+                o[j] = last == 0.0f ? make_float4(0, 0, 0, 0)
+                                    : make_float4(last * o[j].x, last * o[j].y, last * o[j].z, last * o[j].w);
+            }
+            for (int t = 0; t < rows; ++t) {
+                float4 u = *reinterpret_cast<const float4 *>(Y + t * kRow + v);
+                float4 kk = *reinterpret_cast<const float4 *>(Q + t * l.stride + k);
+                fma4(o[0], u.x, kk), fma4(o[1], u.y, kk), fma4(o[2], u.z, kk), fma4(o[3], u.w, kk);
+                u = *reinterpret_cast<const float4 *>(Z + t * kRow + v);
+                kk = *reinterpret_cast<const float4 *>(Kt + t * l.stride + k);
+                fma4(o[0], u.x, kk), fma4(o[1], u.y, kk), fma4(o[2], u.z, kk), fma4(o[3], u.w, kk);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<float4 *>(S + (v + j) * l.stride + k) = o[j];
+        }
+    }
+    __syncthreads();
+    if (p.dh0)
+        for (int i = tid; i < w.width * s.K; i += kThreads) {
+            const int v = i / s.K, k = i - v * s.K;
+            p.dh0[state_at + i] = S[v * l.stride + k];
+        }
+    clear_uncovered(s, w.seq, p.dv + int64_t(w.head) * s.V + w.v0, v_step, w.width);
+    if (w.v0 == 0) {
+        clear_uncovered(s, w.seq, p.dg + w.head, s.H, 1);
+        clear_uncovered(s, w.seq, p.dbeta + w.head, s.H, 1);
+        if (w.head < s.G) {
+            clear_uncovered(s, w.seq, p.dq + int64_t(w.head) * s.K, qk_step, s.K);
+            clear_uncovered(s, w.seq, p.dk + int64_t(w.head) * s.K, qk_step, s.K);
+        }
+    }
+}
+
+struct GradLayout {
+    int stride, q, k, dp, da, m, y, u, z, s0, s1, words;
+};
+__host__ __device__ inline GradLayout grad_layout_of(int K) {
+    GradLayout l;
+    l.stride = stride_of(K);
+    l.q = 0;
+    l.k = l.q + kBlock * l.stride;
+    l.dp = l.k + kBlock * l.stride;
+    l.da = l.dp + kBlock * kPairs;
+    l.y = l.da + kBlock * kPairs;
+    l.u = l.y + kBlock * kRow;
+    l.z = l.u + kBlock * kRow;
+    l.s0 = l.z + kBlock * kRow;
+    l.s1 = l.s0 + kSlice * kPairs;
+    l.words = l.s1 + kSlice * kPairs;
+    l.m = l.y;                  // after the slices are done with; 64 x 65
+    return l;
+}
+
+// dq, dk, dg and dbeta of one block of one head.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) grads_kernel(const BwdArgs<T> p) {
+    extern __shared__ __align__(16) float mem[];
+    __shared__ Decays d;
+    __shared__ int found;
+    __shared__ float row_term[kBlock], col_term[kBlock], both_term[kThreads / 32];
+    const Shape &s = p.s;
+    const GradLayout l = grad_layout_of(s.K);
+    float *Q = mem + l.q, *Kt = mem + l.k, *dP = mem + l.dp, *dA = mem + l.da, *Y = mem + l.y, *U = mem + l.u,
+          *Z = mem + l.z, *S0 = mem + l.s0, *S1 = mem + l.s1, *M = mem + l.m;
+    const int Kp = padded(s.K), tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+    const int head = int(blockIdx.x % s.H), group = head / (s.H / s.G);
+    const int64_t slot = blockIdx.x / s.H;
+    // the sequence of this place
+    if (tid == 0) found = -1;
+    __syncthreads();
+    if (s.offsets) {
+        for (int i = tid; i < s.n; i += kThreads) {
+            const Span span = span_of(s, i);
+            if (slot >= span.slot && slot < span.slot + span.blocks) atomicMax(&found, i);
+        }
+    } else if (tid == 0) {
+        found = int(slot / ((s.L + kBlock - 1) / kBlock));
+    }
+    __syncthreads();
+    if (found < 0) return;
+    const Span span = span_of(s, found);
+    const int c = int(slot - span.slot), rows = min(kBlock, span.len - c * kBlock);
+    const int64_t row = span.first + int64_t(c) * kBlock, rows_all = s.offsets ? s.L : s.L * s.n;
+    const int64_t qk_step = int64_t(s.G) * s.K, v_step = int64_t(s.H) * s.V;
+    load_tile(Q, l.stride, p.q + row * qk_step + int64_t(group) * s.K, qk_step, rows, s.K, Kp);
+    load_tile(Kt, l.stride, p.k + row * qk_step + int64_t(group) * s.K, qk_step, rows, s.K, Kp);
+    if (tid < 32) load_decays(d, p.g + row * s.H + head, p.beta + row * s.H + head, s.H, rows);
+    if (tid < kBlock) row_term[tid] = col_term[tid] = 0.0f;
+    const T *st0 = p.states + (slot * s.H + head) * int64_t(s.V) * s.K;
+    const T *st1 = p.ds + (slot * s.H + head) * int64_t(s.V) * s.K;
+
+    // a slice of dY, U = beta x and beta Z = dv
+    const auto load_slice = [&](int v0) {
+        const int width = min(kSlice, s.V - v0);
+        const int64_t at = row * v_step + int64_t(head) * s.V + v0;
+        for (int i = tid; i < kBlock * kSlice; i += kThreads) {
+            const int t = i / kSlice, v = i % kSlice;
+            const bool in = t < rows && v < width;
+            const int64_t o = at + t * v_step + v;
+            Y[t * kRow + v] = in ? s.scale * to_f32(p.dy[o]) : 0.0f;
+            U[t * kRow + v] = in ? d.beta[t] * to_f32(p.errors[o]) : 0.0f;
+            Z[t * kRow + v] = in ? to_f32(p.dv[o]) : 0.0f;
+        }
+    };
+    float gp[4][4] = {}, ga[4][4] = {};
+    for (int v0 = 0; v0 < s.V; v0 += kSlice) {
+        __syncthreads();
+        load_slice(v0);
+        __syncthreads();
+        float m[4][4];
+        products(m, Y, U, kRow, kSlice);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) gp[i / 4][i % 4] += m[i / 4][i % 4];
+        products(m, Z, U, kRow, kSlice);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ga[i / 4][i % 4] -= m[i / 4][i % 4];
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int t = ty + 16 * (i / 4), r = tx + 16 * (i % 4);
+        const float D = d.between(t, r);
+        dP[t * kPairs + r] = r <= t ? gp[i / 4][i % 4] * D : 0.0f;
+        dA[t * kPairs + r] = r < t ? ga[i / 4][i % 4] * D : 0.0f;
+    }
+    float both = 0.0f;
+    // 64 columns of K at a time: what goes through the states, then through the pairs
+    for (int k0 = 0; k0 < Kp; k0 += kBlock) {
+        const int wide = min(kBlock, s.K - k0);
+        float dq[4][4] = {}, dr[4][4] = {}, dc[4][4] = {};      // rows ty + 16 i, columns tx + 16 j
+        for (int v0 = 0; v0 < s.V; v0 += kSlice) {
+            const int width = min(kSlice, s.V - v0);
+            __syncthreads();
+            load_slice(v0);
+            for (int i = tid; i < kSlice * kBlock; i += kThreads) {
+                const int v = i / kBlock, k = i % kBlock;
+                const bool in = v < width && k < wide;
+                const float a = in ? to_f32(st0[int64_t(v0 + v) * s.K + k0 + k]) : 0.0f;
+                const float b = in ? to_f32(st1[int64_t(v0 + v) * s.K + k0 + k]) : 0.0f;
+                S0[v * kPairs + k] = a;
+                S1[v * kPairs + k] = b;
+                both += a * b;
+            }
+            __syncthreads();
+            for (int v = 0; v < width; ++v) {
+                float a[4], b[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) a[j] = S0[v * kPairs + tx + 16 * j], b[j] = S1[v * kPairs + tx + 16 * j];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = ty + 16 * i;
+                    const float y = Y[t * kRow + v], u = U[t * kRow + v], z = Z[t * kRow + v];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) dq[i][j] += y * a[j], dr[i][j] -= z * a[j], dc[i][j] += u * b[j];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = ty + 16 * i;
+            const float start = d.start(t), end = d.end(t);
+            float rt = 0.0f, ct = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = tx + 16 * j;
+                const float qv = k < wide ? Q[t * l.stride + k0 + k] : 0.0f, kv = k < wide ? Kt[t * l.stride + k0 + k] : 0.0f;
+                dq[i][j] = start == 0.0f ? 0.0f : start * dq[i][j];
+                dr[i][j] = start == 0.0f ? 0.0f : start * dr[i][j];
+                dc[i][j] = end == 0.0f ? 0.0f : end * dc[i][j];
+                rt += dq[i][j] * qv + dr[i][j] * kv;
+                ct += dc[i][j] * kv;
+                dr[i][j] += dc[i][j];
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o /= 2) {
+                rt += __shfl_xor_sync(0xffffffffu, rt, o);
+                ct += __shfl_xor_sync(0xffffffffu, ct, o);
+            }
+            if (tx == 0) row_term[t] += rt, col_term[t] += ct;
+        }
+        for (int r = 0; r < rows; ++r) {
+            float kr[4], qr[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = tx + 16 * j;
+                kr[j] = k < wide ? Kt[r * l.stride + k0 + k] : 0.0f;
+                qr[j] = k < wide ? Q[r * l.stride + k0 + k] : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = ty + 16 * i;
+                const float pd = dP[t * kPairs + r], pt = dP[r * kPairs + t];
+                const float ad = dA[t * kPairs + r] + dA[r * kPairs + t];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    dq[i][j] += pd * kr[j];
+                    dr[i][j] += pt * qr[j] + ad * kr[j];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int t = ty + 16 * (i / 4), k = tx + 16 * (i % 4);
+            if (t >= rows || k >= wide) continue;
+            if (s.H > s.G) {
+                const int64_t o = ((row + t) * s.H + head) * s.K + k0 + k;
+                p.dq_head[o] = dq[i / 4][i % 4];
+                p.dk_head[o] = dr[i / 4][i % 4];
+            } else {
+                const int64_t o = ((row + t) * s.H + head) * s.K + k0 + k;
+                put(p.dq + o, dq[i / 4][i % 4]);
+                put(p.dk + o, dr[i / 4][i % 4]);
+            }
+        }
+    }
+    // dg: the pairs' products, their sums along rows up to each step, then down the columns
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) both += __shfl_xor_sync(0xffffffffu, both, o);
+    if (tid % 32 == 0) both_term[tid / 32] = both;
+    float mk[4][4], mq[4][4];
+    products(mq, Q, Kt, l.stride, Kp);
+    products(mk, Kt, Kt, l.stride, Kp);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int t = ty + 16 * (i / 4), r = tx + 16 * (i % 4);
+        M[t * (kBlock + 1) + r] =
+            r < t ? dP[t * kPairs + r] * mq[i / 4][i % 4] + dA[t * kPairs + r] * mk[i / 4][i % 4] : 0.0f;
+    }
+    __syncthreads();
+    if (tid < kBlock) {
+        float sum = 0.0f;
+        for (int r = 0; r < kBlock; ++r) {
+            const float v = M[tid * (kBlock + 1) + r];
+            M[tid * (kBlock + 1) + r] = sum;        // pairs of row tid before step r
+            sum += v;
+        }
+    }
+    __syncthreads();
+    if (tid < rows) {
+        float sum = 0.0f;
+        for (int i = 0; i < kThreads / 32; ++i) sum += both_term[i];
+        const float last = d.start(kBlock - 1);
+        sum = last == 0.0f ? 0.0f : last * sum;
+        for (int r = tid; r < rows; ++r) sum += row_term[r] + M[r * (kBlock + 1) + tid];
+        for (int r = 0; r < tid; ++r) sum += col_term[r];
+        put(p.dg + (row + tid) * s.H + head, sum);
+        const int slices = (s.V + kSlice - 1) / kSlice;
+        float b = 0.0f;
+        for (int i = 0; i < slices; ++i) b += p.dbeta_part[(int64_t(i) * rows_all + row + tid) * s.H + head];
+        put(p.dbeta + (row + tid) * s.H + head, b);
+    }
+}
+
+// dq and dk of a group: the sum of its heads', in their order.  Rows that no
+// sequence covers are 0 (back_kernel) and stay.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) fold_kernel(const BwdArgs<T> p) {
+    const Shape &s = p.s;
+    const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x, row = i / (s.G * s.K);
+    int64_t a = 0, b = s.L * s.n;
+    if (s.offsets) {
+        const Span last = span_of(s, s.n - 1);
+        a = span_of(s, 0).first, b = last.first + last.len;
+    }
+    if (row < a || row >= b) return;
+    const int at = int(i % (s.G * s.K)), group = at / s.K, k = at % s.K, per = s.H / s.G;
+    const int64_t from = (row * s.H + group * per) * s.K + k;
+    float q = 0.0f, kk = 0.0f;
+    for (int h = 0; h < per; ++h) q += p.dq_head[from + int64_t(h) * s.K], kk += p.dk_head[from + int64_t(h) * s.K];
+    put(p.dq + i, q);
+    put(p.dk + i, kk);
+}
+
+int slices(const Shape &s) { return (s.V + kSlice - 1) / kSlice; }
+
+template <typename K>
+static cudaError_t room(K kernel, int words) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, words * 4);
+}
+
+template <typename T>
+cudaError_t fwd(const FwdArgs<T> &a, cudaStream_t st) {
+    const int64_t grid = int64_t(a.s.n) * a.s.H * slices(a.s);
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    // the limit is the largest layout's, whatever this call takes: calls of several threads cannot lower it
+    if (cudaError_t e = room(fwd_kernel<T>, layout_of(256).words)) return e;
+    fwd_kernel<T><<<unsigned(grid), kThreads, layout_of(a.s.K).words * 4, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t bwd(const BwdArgs<T> &a, cudaStream_t st) {
+    const int64_t grid = int64_t(a.s.n) * a.s.H * slices(a.s), blocks = a.s.slots() * a.s.H;
+    const int64_t folds = (a.s.rows() * a.s.G * a.s.K + kThreads - 1) / kThreads;
+    if (grid > 0x7fffffff || blocks > 0x7fffffff || folds > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    if (cudaError_t e = room(back_kernel<T>, layout_of(256).words)) return e;
+    if (cudaError_t e = room(grads_kernel<T>, grad_layout_of(256).words)) return e;
+    back_kernel<T><<<unsigned(grid), kThreads, layout_of(a.s.K).words * 4, st>>>(a);
+    if (cudaError_t e = cudaGetLastError()) return e;
+    grads_kernel<T><<<unsigned(blocks), kThreads, grad_layout_of(a.s.K).words * 4, st>>>(a);
+    if (cudaError_t e = cudaGetLastError()) return e;
+    if (a.s.H > a.s.G) fold_kernel<T><<<unsigned(folds), kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template cudaError_t fwd<float>(const FwdArgs<float> &, cudaStream_t);
+template cudaError_t fwd<__nv_bfloat16>(const FwdArgs<__nv_bfloat16> &, cudaStream_t);
+template cudaError_t bwd<float>(const BwdArgs<float> &, cudaStream_t);
+template cudaError_t bwd<__nv_bfloat16>(const BwdArgs<__nv_bfloat16> &, cudaStream_t);
+
+}  // namespace general
+}  // namespace delta
+}  // namespace ssm
