@@ -495,6 +495,8 @@ SSM_API ssm_status_t state_pages_compact(void *pool, uint8_t *used, int32_t *mov
  *          written, v's type): the state before steps 0, 64, 128, ... of each
  *          sequence, (slots, H, V, K) with slots = Bs ceil(L / 64), packed
  *          floor(L / 64) + n_seq; and x, (Bs, L, H, V)
+ *   scratch : delta_rule_fwd_scratch bytes of the caller's, 16-byte aligned;
+ *          unspecified afterwards
  * The state and every sum are fp32.  bf16 inputs: see the kernels for what the
  * tensor cores' operands are rounded to.  A NaN or an infinity in a step's
  * inputs makes the outputs of that head's whole block of 64 steps and of
@@ -506,9 +508,11 @@ SSM_API ssm_status_t state_pages_compact(void *pool, uint8_t *used, int32_t *mov
 SSM_API ssm_status_t delta_rule_fwd(const void *q, const void *k, const void *v, const void *g,
                                     const void *beta, float scale, const int32_t *offsets,
                                     const float *h0, void *y, float *h_final, void *states,
-                                    void *errors, int64_t Bs, int64_t L, int64_t G, int64_t H,
-                                    int64_t K, int64_t V, int64_t n_seq, int input_bf16,
+                                    void *errors, void *scratch, int64_t Bs, int64_t L, int64_t G,
+                                    int64_t H, int64_t K, int64_t V, int64_t n_seq, int input_bf16,
                                     void *stream);
+SSM_API int64_t delta_rule_fwd_scratch(int64_t Bs, int64_t L, int64_t G, int64_t H, int64_t K,
+                                       int64_t V, int64_t n_seq, int input_bf16);
 
 /*
  * Gradients of delta_rule_fwd for dy (v's shape and type) and dh_final (NULL =

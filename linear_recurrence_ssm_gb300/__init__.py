@@ -89,7 +89,8 @@ SIGNATURES = {
     "state_pages_copy": ([_VP] * 3 + [_I64] * 4 + [_VP], ctypes.c_int),
     "state_pages_free": ([_VP] * 2 + [_I64] * 2 + [_VP], ctypes.c_int),
     "state_pages_compact": ([_VP] * 5 + [_I64] * 4 + [_VP], ctypes.c_int),
-    "delta_rule_fwd": ([_VP] * 5 + [_F32] + [_VP] * 6 + [_I64] * 7 + [ctypes.c_int, _VP], ctypes.c_int),
+    "delta_rule_fwd": ([_VP] * 5 + [_F32] + [_VP] * 7 + [_I64] * 7 + [ctypes.c_int, _VP], ctypes.c_int),
+    "delta_rule_fwd_scratch": ([_I64] * 7 + [ctypes.c_int], _I64),
     "delta_rule_bwd_scratch": ([_I64] * 7 + [ctypes.c_int], _I64),
     "delta_rule_bwd": ([_VP] * 4 + [_F32] + [_VP] * 12 + [_I64] * 7 + [ctypes.c_int, _VP], ctypes.c_int),
     "delta_rule_step": ([_VP] * 5 + [_F32] + [_VP] * 3 + [_I64] * 6 + [ctypes.c_int, _VP], ctypes.c_int),
@@ -852,11 +853,12 @@ def delta_rule_fwd(q, k, v, g, beta, scale=None, offsets=None, h0=None, return_f
     if save is not None:
         saved = {name: torch.empty(shape, dtype=v.dtype, device=dev)
                  for name, shape in _delta_saved_shapes(Bs, L, H, K, V, n_seq).items()}
+    bf16 = int(v.dtype == torch.bfloat16)
+    scratch = torch.empty(library().delta_rule_fwd_scratch(Bs, L, G, H, K, V, n_seq, bf16), dtype=torch.uint8, device=dev)
     _call("delta_rule_fwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
           K ** -0.5 if scale is None else scale, _addr(offsets), _addr(h0), y.data_ptr(), _addr(hf),
           None if saved is None else saved["states"].data_ptr(),
-          None if saved is None else saved["errors"].data_ptr(), Bs, L, G, H, K, V, n_seq,
-          int(v.dtype == torch.bfloat16))
+          None if saved is None else saved["errors"].data_ptr(), scratch.data_ptr(), Bs, L, G, H, K, V, n_seq, bf16)
     out = (y,) + ((hf,) if return_final_state else ()) + ((saved,) if save is not None else ())
     return out if len(out) > 1 else y
 
@@ -888,7 +890,7 @@ def delta_rule_bwd(q, k, g, beta, dy, saved, scale=None, offsets=None, dh_final=
                dh0=torch.empty((n, H, V, K), dtype=torch.float32, device=dev) if need_dh0 else None)
     bf16 = int(q.dtype == torch.bfloat16)
     size = library().delta_rule_bwd_scratch(Bs, L, G, H, K, V, n_seq, bf16)
-    scratch = torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
+    scratch = torch.empty(size, dtype=torch.uint8, device=dev)
     _call("delta_rule_bwd", dev, q.data_ptr(), k.data_ptr(), g.data_ptr(), beta.data_ptr(),
           K ** -0.5 if scale is None else scale, _addr(offsets), dy.data_ptr(), _addr(dh_final),
           saved["states"].data_ptr(), saved["errors"].data_ptr(), out["dq"].data_ptr(), out["dk"].data_ptr(),

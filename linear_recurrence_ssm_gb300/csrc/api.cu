@@ -7,7 +7,7 @@
 #include <limits.h>
 #include <mutex>
 
-#include "delta_rule.cuh"
+#include "delta_mma.cuh"
 #include "gated_scan.cuh"
 #include "ssm_common.cuh"
 
@@ -112,6 +112,12 @@ template <typename T>
 cudaError_t fwd(const FwdArgs<T> &a, cudaStream_t st);
 template <typename T>
 cudaError_t bwd(const BwdArgs<T> &a, cudaStream_t st);
+}
+namespace mma {
+namespace fwd {
+bool fits(const FwdArgs<__nv_bfloat16> &a);
+cudaError_t launch(const FwdArgs<__nv_bfloat16> &a, cudaStream_t st);
+}
 }
 namespace step {
 template <typename T>
@@ -465,9 +471,9 @@ template <typename T>
 ssm_status_t delta_fwd_entry(const void *q, const void *k, const void *v, const void *g,
                              const void *beta, float scale, const int32_t *offsets,
                              const float *h0, void *y, float *h_final, void *states, void *errors,
-                             int64_t Bs, int64_t L, int64_t G, int64_t H, int64_t K, int64_t V,
+                             void *scratch, int64_t Bs, int64_t L, int64_t G, int64_t H, int64_t K, int64_t V,
                              int64_t n_seq, void *stream) {
-    if (!q || !k || !v || !g || !beta || !y || !states != !errors || (n_seq > 0) != (offsets != nullptr))
+    if (!q || !k || !v || !g || !beta || !y || !scratch || !states != !errors || (n_seq > 0) != (offsets != nullptr))
         return SSM_ERR_INVALID_ARG;
     ssm_status_t s = check_delta_sizes(Bs, L, G, H, K, V, n_seq, scale);
     if (s != SSM_OK) return s;
@@ -475,7 +481,8 @@ ssm_status_t delta_fwd_entry(const void *q, const void *k, const void *v, const 
     for (const void *p : {q, k, v, g, beta, static_cast<const void *>(y), static_cast<const void *>(states),
                           static_cast<const void *>(errors)})
         if (!aligned(p, e)) return SSM_ERR_ALIGNMENT;
-    if (!aligned(offsets, 4) || !aligned(h0, 4) || !aligned(h_final, 4)) return SSM_ERR_ALIGNMENT;
+    if (!aligned(offsets, 4) || !aligned(h0, 4) || !aligned(h_final, 4) || !aligned(scratch, 16))
+        return SSM_ERR_ALIGNMENT;
     DeviceInfo dev;
     s = current_device(&dev);
     if (s != SSM_OK) return s;
@@ -483,8 +490,12 @@ ssm_status_t delta_fwd_entry(const void *q, const void *k, const void *v, const 
                                    static_cast<const T *>(q), static_cast<const T *>(k),
                                    static_cast<const T *>(v), static_cast<const T *>(g),
                                    static_cast<const T *>(beta), h0, static_cast<T *>(y), h_final,
-                                   static_cast<T *>(states), static_cast<T *>(errors)};
-    return from_cuda(ssm::delta::general::fwd(a, static_cast<cudaStream_t>(stream)));
+                                   static_cast<T *>(states), static_cast<T *>(errors),
+                                   static_cast<unsigned char *>(scratch)};
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if constexpr (sizeof(T) == 2)
+        if (ssm::delta::mma::fwd::fits(a)) return from_cuda(ssm::delta::mma::fwd::launch(a, st));
+    return from_cuda(ssm::delta::general::fwd(a, st));
 }
 
 template <typename T>
@@ -936,20 +947,27 @@ ssm_status_t state_pages_compact(void *pool, uint8_t *used, int32_t *moved, int3
 
 ssm_status_t delta_rule_fwd(const void *q, const void *k, const void *v, const void *g,
                             const void *beta, float scale, const int32_t *offsets, const float *h0,
-                            void *y, float *h_final, void *states, void *errors, int64_t Bs,
-                            int64_t L, int64_t G, int64_t H, int64_t K, int64_t V, int64_t n_seq,
+                            void *y, float *h_final, void *states, void *errors, void *scratch,
+                            int64_t Bs, int64_t L, int64_t G, int64_t H, int64_t K, int64_t V, int64_t n_seq,
                             int input_bf16, void *stream) {
     return input_bf16 ? delta_fwd_entry<__nv_bfloat16>(q, k, v, g, beta, scale, offsets, h0, y, h_final,
-                                                       states, errors, Bs, L, G, H, K, V, n_seq, stream)
+                                                       states, errors, scratch, Bs, L, G, H, K, V, n_seq, stream)
                       : delta_fwd_entry<float>(q, k, v, g, beta, scale, offsets, h0, y, h_final, states,
-                                               errors, Bs, L, G, H, K, V, n_seq, stream);
+                                               errors, scratch, Bs, L, G, H, K, V, n_seq, stream);
+}
+
+int64_t delta_rule_fwd_scratch(int64_t Bs, int64_t L, int64_t G, int64_t H, int64_t K, int64_t V,
+                               int64_t n_seq, int input_bf16) {
+    if (check_delta_sizes(Bs, L, G, H, K, V, n_seq, 1.0f) != SSM_OK) return 0;
+    static const int32_t some = 0;      // only that there are offsets counts
+    const ssm::delta::Shape s = delta_shape(n_seq > 0 ? &some : nullptr, Bs, L, G, H, K, V, n_seq, 1.0f);
+    return input_bf16 && ssm::delta::mma::fits(s) ? ssm::delta::mma::record_bytes(s) : 16;
 }
 
 int64_t delta_rule_bwd_scratch(int64_t Bs, int64_t L, int64_t G, int64_t H, int64_t K, int64_t V,
                                int64_t n_seq, int io_bf16) {
     if (check_delta_sizes(Bs, L, G, H, K, V, n_seq, 1.0f) != SSM_OK) return 0;
-    // the sequences' offsets are not looked at, only that there are some
-    static const int32_t some = 0;
+    static const int32_t some = 0;      // only that there are offsets counts
     const ssm::delta::Shape s = delta_shape(n_seq > 0 ? &some : nullptr, Bs, L, G, H, K, V, n_seq, 1.0f);
     return ssm::delta::scratch_of(s, io_bf16 ? 2 : 4, ssm::delta::general::slices(s)).bytes;
 }

@@ -1,0 +1,271 @@
+// delta_fwd.cu -- the gated delta rule, forward, bf16, on tensor cores.
+//
+// A thread block takes one head of one sequence and 64 rows of its state, and
+// walks the sequence 64 steps at a time.  Four warps hold 16 rows each, as
+// accumulators in fp32, from the first step to the last:
+//   W^T = V^T - Gam (S K^T),  X^T = W^T - (beta W)^T N^T,  U = beta X
+//   S = Gam_C S + (E U)^T K
+// and hand S and U to four more warps, which form the block's outputs while
+// the chain is at the next one:
+//   Y^T = scale Gam (S Q^T) + U^T P^T.
+// N and P come from pairs_kernel.
+//
+// Operands of the state's own chain (S, beta W, N, E U) go into the tensor
+// cores as two bf16 terms, 16 bits, so that the final state is good to 2^-17
+// an operand (fp32 states come out within 1e-5); K and Q are bf16 as given.
+// What only y sees (S in S Q^T, U and P in U P) is one term: 2^-9 beside y's
+// own rounding.
+#include "delta_mma.cuh"
+
+namespace ssm {
+namespace delta {
+namespace mma {
+namespace fwd {
+
+constexpr int kSlice = 64, kChain = 4, kThreads = 256;
+
+template <int KP>
+struct Layout {
+    static constexpr int tile = kBlock * KP * 2, v = kBlock * kSlice * 2;
+    static constexpr int chain = tile + v + 2 * kTile;              // K, V, N in two terms: two of them
+    static constexpr int outputs = 2 * chain, output = tile + kTile + 1152;      // Q, P, the factors: three of them
+    static constexpr int handed = outputs + 3 * output;
+    static constexpr int state = 16 * KP * 2, u = 16 * kBlock * 2;  // of a warp
+    static constexpr int hand = kChain * (state + 2 * u);           // S, U, X: two of them
+    static constexpr int bytes = handed + 2 * hand;
+    static_assert(sizeof(Factors) <= 1152 && bytes <= 232448, "shared memory");
+};
+
+// 16 columns of the state as a left operand of two terms.
+template <int KP>
+__device__ __forceinline__ void operand(uint32_t (&hi)[4], uint32_t (&lo)[4], const float (&s)[KP / 8][4], int k) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        split(s[2 * k + h][0], s[2 * k + h][1], hi[2 * h], lo[2 * h]);
+        split(s[2 * k + h][2], s[2 * k + h][3], hi[2 * h + 1], lo[2 * h + 1]);
+    }
+}
+
+template <int KP>
+__global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdArgs<bf> p) {
+    extern __shared__ __align__(1024) unsigned char mem[];
+    using L = Layout<KP>;
+    const Shape &s = p.s;
+    const uint32_t base = smem_u32(mem);
+    const int slices = (s.V + kSlice - 1) / kSlice;
+    const int slice = int(blockIdx.x % slices), head = int(blockIdx.x / slices % s.H);
+    const int seq = int(blockIdx.x / slices / s.H), group = head / (s.H / s.G), v0 = slice * kSlice;
+    const Span span = span_of(s, seq);
+    const int64_t qk_step = int64_t(s.G) * s.K, v_step = int64_t(s.H) * s.V;
+    const int tid = threadIdx.x, warp = tid / 32 % kChain, lane = tid % 32;
+    const bool chain = tid < 32 * kChain;
+    const int g = lane / 4, c2 = lane % 4 * 2, mine = v0 + 16 * warp;       // rows mine + g, mine + g + 8 of the state
+    const int width = s.V - mine;                                           // of them, may be below 1 or above 16
+    const int64_t state_at = (int64_t(seq) * s.H + head) * s.V * s.K;
+
+    const auto copy = [&](int c) {
+        const int64_t row = span.first + int64_t(c) * kBlock;
+        const int rows = min(kBlock, span.len - c * kBlock);
+        const uint32_t to = base + c % 2 * L::chain, out = base + L::outputs + c % 3 * L::output;
+        const unsigned char *record = p.scratch + ((span.slot + c) * s.H + head) * kRecord;
+        copy_tile<KP, kThreads>(to, p.k + row * qk_step + int64_t(group) * s.K, qk_step, rows, s.K, tid);
+        copy_tile<kSlice, kThreads>(to + L::tile, p.v + row * v_step + int64_t(head) * s.V + v0, v_step, rows,
+                                    min(kSlice, s.V - v0), tid);
+#pragma unroll
+        for (int i = 0; i < 2 * kTile / 16 / kThreads; ++i)
+            copy16(to + L::tile + L::v + (i * kThreads + tid) * 16, record + (i * kThreads + tid) * 16);
+        copy_tile<KP, kThreads>(out, p.q + row * qk_step + int64_t(group) * s.K, qk_step, rows, s.K, tid);
+        constexpr int rest = (kTile + int(sizeof(Factors))) / 16;
+        for (int i = tid; i < rest; i += kThreads) copy16(out + L::tile + i * 16, record + 2 * kTile + i * 16);
+    };
+    float st[KP / 8][4];
+    if (chain) {
+#pragma unroll
+        for (int n = 0; n < KP / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int v = g + e / 2 * 8, k = 8 * n + c2 + e % 2;
+                st[n][e] = p.h0 && v < width && k < s.K ? p.h0[state_at + int64_t(mine + v) * s.K + k] : 0.0f;
+            }
+    }
+    if (span.blocks > 0) copy(0);
+    cp_async_commit();
+    // the chain is at block c, the outputs at the one before
+    for (int c = 0; c <= span.blocks; ++c) {
+        cp_async_wait<0>();
+        __syncthreads();
+        if (c + 1 < span.blocks) copy(c + 1);
+        cp_async_commit();
+        if (chain) {
+            if (c == span.blocks) break;
+            const uint32_t at = base + c % 2 * L::chain, hand = base + L::handed + c % 2 * L::hand;
+            const uint32_t hand_u = hand + kChain * L::state + warp * L::u, hand_x = hand_u + kChain * L::u;
+            const Factors &f = *reinterpret_cast<const Factors *>(mem + L::outputs + c % 3 * L::output + L::tile + kTile);
+            // S K^T: the pieces of K for the next 16 columns are loaded ahead of the products
+            float w[8][4] = {};
+            {
+                uint32_t b[2][4][4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) load4(b[0][t], four_across<KP>(at, 16 * t, 0));
+#pragma unroll
+                for (int k = 0; k < KP / 16; ++k) {
+                    uint32_t hi[4], lo[4];
+                    operand<KP>(hi, lo, st, k);
+                    store4(four<KP>(hand + warp * L::state, 0, 16 * k), hi);
+                    if (k + 1 < KP / 16)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) load4(b[(k + 1) % 2][t], four_across<KP>(at, 16 * t, 16 * (k + 1)));
+                    across(w, hi, b[k % 2]);
+                    across(w, lo, b[k % 2]);
+                }
+            }
+            // W, beta W as two terms, and X in W's place
+            uint32_t hi[4][4], lo[4][4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                uint32_t v[4];
+                load4t(v, four_across<64>(at + L::tile, 16 * t, 16 * warp));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float2 by = *reinterpret_cast<const float2 *>(f.start + 16 * t + 8 * h + c2);
+                    const float2 beta = *reinterpret_cast<const float2 *>(f.beta + 16 * t + 8 * h + c2);
+                    float(&x)[4] = w[2 * t + h];
+                    x[0] = low(v[2 * h]) - kept(by.x, x[0]);
+                    x[1] = high(v[2 * h]) - kept(by.y, x[1]);
+                    x[2] = low(v[2 * h + 1]) - kept(by.x, x[2]);
+                    x[3] = high(v[2 * h + 1]) - kept(by.y, x[3]);
+                    split(beta.x * x[0], beta.y * x[1], hi[t][2 * h], lo[t][2 * h]);
+                    split(beta.x * x[2], beta.y * x[3], hi[t][2 * h + 1], lo[t][2 * h + 1]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                uint32_t n[4][4], rest[4][4];
+#pragma unroll
+                for (int t = r; t < 4; ++t) {
+                    load4(n[t], four_across<64>(at + L::tile + L::v, 16 * t, 16 * r));
+                    load4(rest[t], four_across<64>(at + L::tile + L::v + kTile, 16 * t, 16 * r));
+                }
+                across(w, hi[r], n, r);
+                across(w, lo[r], n, r);
+                across(w, hi[r], rest, r);
+            }
+            // U for the outputs, E U for the state, X to be kept
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                uint32_t u[4];
+                if (p.errors) store_turned(hand_x, t, w);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float2 beta = *reinterpret_cast<const float2 *>(f.beta + 16 * t + 8 * h + c2);
+                    const float2 end = *reinterpret_cast<const float2 *>(f.end + 16 * t + 8 * h + c2);
+                    const float(&x)[4] = w[2 * t + h];
+                    const float a = beta.x * x[0], b = beta.y * x[1], d = beta.x * x[2], e = beta.y * x[3];
+                    u[2 * h] = pack(a, b);
+                    u[2 * h + 1] = pack(d, e);
+                    split(kept(end.x, a), kept(end.y, b), hi[t][2 * h], lo[t][2 * h]);
+                    split(kept(end.x, d), kept(end.y, e), hi[t][2 * h + 1], lo[t][2 * h + 1]);
+                }
+                store4(four<64>(hand_u, 0, 16 * t), u);
+            }
+            // S
+            const float last = f.last;
+#pragma unroll
+            for (int n = 0; n < KP / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) st[n][e] = kept(last, st[n][e]);
+            add_outer<KP>(st, hi, lo, at);
+        } else if (c > 0) {
+            const int rows = min(kBlock, span.len - (c - 1) * kBlock);
+            const int64_t row = span.first + int64_t(c - 1) * kBlock;
+            const int from = L::outputs + (c - 1) % 3 * L::output;
+            const uint32_t at = base + from;
+            const uint32_t hand = base + L::handed + (c - 1) % 2 * L::hand, hand_s = hand + warp * L::state;
+            const uint32_t hand_u = hand + kChain * L::state + warp * L::u, hand_x = hand_u + kChain * L::u;
+            const Factors &f = *reinterpret_cast<const Factors *>(mem + from + L::tile + kTile);
+            const int64_t out_at = row * v_step + int64_t(head) * s.V + mine;
+            if (p.states) {
+                bf *out = p.states + ((span.slot + c - 1) * s.H + head) * int64_t(s.V) * s.K + int64_t(mine) * s.K;
+#pragma unroll
+                for (int i = 0; i < 16 * KP / 8 / 32; ++i) {
+                    const int v = (i * 32 + lane) / (KP / 8), k = (i * 32 + lane) % (KP / 8) * 8;
+                    const uint4 w = load16(place<KP>(hand_s, v, k));
+                    if (v < width && k < s.K) *reinterpret_cast<uint4 *>(out + int64_t(v) * s.K + k) = w;
+                }
+                write_turned(p.errors + out_at, v_step, rows, width, hand_x);
+                __syncwarp();
+            }
+            float y[8][4] = {};
+            {
+                uint32_t b[2][4][4], a[2][4];
+                load4(a[0], four<KP>(hand_s, 0, 0));
+#pragma unroll
+                for (int t = 0; t < 4; ++t) load4(b[0][t], four_across<KP>(at, 16 * t, 0));
+#pragma unroll
+                for (int k = 0; k < KP / 16; ++k) {
+                    if (k + 1 < KP / 16) {
+                        load4(a[(k + 1) % 2], four<KP>(hand_s, 0, 16 * (k + 1)));
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) load4(b[(k + 1) % 2][t], four_across<KP>(at, 16 * t, 16 * (k + 1)));
+                    }
+                    across(y, a[k % 2], b[k % 2]);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const float2 by = *reinterpret_cast<const float2 *>(f.start_scaled + 8 * t + c2);
+                y[t][0] = kept(by.x, y[t][0]), y[t][1] = kept(by.y, y[t][1]);
+                y[t][2] = kept(by.x, y[t][2]), y[t][3] = kept(by.y, y[t][3]);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                uint32_t u[4], b[4][4];
+                load4(u, four<64>(hand_u, 0, 16 * r));
+#pragma unroll
+                for (int t = r; t < 4; ++t) load4(b[t], four_across<64>(at + L::tile, 16 * t, 16 * r));
+                across(y, u, b, r);
+            }
+            // through shared memory, where X was: 32 bytes of a row are one access
+#pragma unroll
+            for (int t = 0; t < 4; ++t) store_turned(hand_x, t, y);
+            __syncwarp();
+            write_turned(p.y + out_at, v_step, rows, width, hand_x);
+        }
+    }
+    if (chain && p.h_final)
+#pragma unroll
+        for (int n = 0; n < KP / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int v = g + e / 2 * 8, k = 8 * n + c2 + e % 2;
+                if (v < width && k < s.K) p.h_final[state_at + int64_t(mine + v) * s.K + k] = st[n][e];
+            }
+    clear_uncovered(s, seq, p.y + int64_t(head) * s.V + v0, v_step, min(kSlice, s.V - v0));
+}
+
+template <int KP>
+static cudaError_t go(const FwdArgs<bf> &a, cudaStream_t st) {
+    const int64_t grid = int64_t(a.s.n) * a.s.H * ((a.s.V + kSlice - 1) / kSlice);
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    constexpr int bytes = Layout<KP>::bytes;
+    if (cudaError_t e = cudaFuncSetAttribute(fwd_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+    fwd_kernel<KP><<<unsigned(grid), kThreads, bytes, st>>>(a);
+    return cudaGetLastError();
+}
+
+static bool on16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Rows that 16-byte copies can take.
+bool fits(const FwdArgs<bf> &a) {
+    return mma::fits(a.s) && on16(a.q) && on16(a.k) && on16(a.v) && on16(a.y) && on16(a.states) && on16(a.errors);
+}
+
+cudaError_t launch(const FwdArgs<bf> &a, cudaStream_t st) {
+    if (cudaError_t e = make_pairs(a.s, a.q, a.k, a.g, a.beta, a.scratch, st)) return e;
+    return a.s.K <= 64 ? go<64>(a, st) : go<128>(a, st);
+}
+
+}  // namespace fwd
+}  // namespace mma
+}  // namespace delta
+}  // namespace ssm

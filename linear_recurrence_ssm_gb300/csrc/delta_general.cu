@@ -104,25 +104,6 @@ __device__ __forceinline__ Work work_of(const Shape &s) {
     return w;
 }
 
-// Elements [v0, v0 + width) of the rows of `out` (H x V a row) that no sequence covers become 0.
-template <typename T>
-__device__ __forceinline__ void clear_uncovered(const Shape &s, int seq, T *out, int64_t step, int width) {
-    if (!s.offsets || out == nullptr) return;
-    int64_t a = 0, b = 0;
-    for (int part = 0; part < 2; ++part) {
-        if (part == 0) {
-            if (seq != 0) continue;
-            a = 0, b = span_of(s, 0).first;
-        } else {
-            if (seq != s.n - 1) continue;
-            const Span last = span_of(s, s.n - 1);
-            a = last.first + last.len, b = s.L;
-        }
-        for (int64_t i = threadIdx.x; i < (b - a) * width; i += blockDim.x)
-            put(out + (a + i / width) * step + i % width, 0.0f);
-    }
-}
-
 template <typename T>
 __global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdArgs<T> p) {
     extern __shared__ __align__(16) float mem[];
@@ -441,20 +422,9 @@ __global__ void __launch_bounds__(kThreads) grads_kernel(const BwdArgs<T> p) {
     const int Kp = padded(s.K), tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
     const int head = int(blockIdx.x % s.H), group = head / (s.H / s.G);
     const int64_t slot = blockIdx.x / s.H;
-    // the sequence of this place
-    if (tid == 0) found = -1;
-    __syncthreads();
-    if (s.offsets) {
-        for (int i = tid; i < s.n; i += kThreads) {
-            const Span span = span_of(s, i);
-            if (slot >= span.slot && slot < span.slot + span.blocks) atomicMax(&found, i);
-        }
-    } else if (tid == 0) {
-        found = int(slot / ((s.L + kBlock - 1) / kBlock));
-    }
-    __syncthreads();
-    if (found < 0) return;
-    const Span span = span_of(s, found);
+    const int seq = sequence_of(s, slot, &found);
+    if (seq < 0) return;
+    const Span span = span_of(s, seq);
     const int c = int(slot - span.slot), rows = min(kBlock, span.len - c * kBlock);
     const int64_t row = span.first + int64_t(c) * kBlock, rows_all = s.offsets ? s.L : s.L * s.n;
     const int64_t qk_step = int64_t(s.G) * s.K, v_step = int64_t(s.H) * s.V;

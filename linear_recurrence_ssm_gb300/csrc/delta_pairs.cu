@@ -1,0 +1,114 @@
+// delta_pairs.cu -- what the gated delta rule's chains need of each block of
+// 64 steps, apart from the state: the inverse of the block's system and the
+// decayed products of queries and keys (delta_mma.cuh says how it is kept).
+//
+// All blocks at once, a thread block each.  Made apart from the chains, these
+// are shared by the slices of a head's values and by both passes of a long
+// sequence; made by extra warps of the chains' own thread blocks they held the
+// chains up (6.5 us a block of 64 steps instead of the chain's own time).
+#include "delta_mma.cuh"
+
+namespace ssm {
+namespace delta {
+namespace mma {
+
+template <int KP>
+struct PairLayout {
+    static constexpr int tile = kBlock * KP * 2;
+    static constexpr int system = 2 * tile, out = system + kBlock * kPairStride * 4;
+    static constexpr int bytes = out + kRecord;
+};
+
+template <int KP>
+__global__ void __launch_bounds__(kPairThreads, 2)
+pairs_kernel(const Shape s, const bf *q, const bf *k, const bf *g, const bf *beta, unsigned char *records) {
+    extern __shared__ __align__(128) unsigned char mem[];
+    __shared__ Decays d;
+    __shared__ int found;
+    using L = PairLayout<KP>;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int head = int(blockIdx.x % s.H), group = head / (s.H / s.G);
+    const int64_t slot = blockIdx.x / s.H;
+    const int seq = sequence_of(s, slot, &found);
+    if (seq < 0) return;
+    const Span span = span_of(s, seq);
+    const int c = int(slot - span.slot), rows = min(kBlock, span.len - c * kBlock);
+    const int64_t row = span.first + int64_t(c) * kBlock, step = int64_t(s.G) * s.K;
+    const uint32_t base = smem_u32(mem);
+    copy_tile<KP, kPairThreads>(base, k + row * step + int64_t(group) * s.K, step, rows, s.K, tid);
+    copy_tile<KP, kPairThreads>(base + L::tile, q + row * step + int64_t(group) * s.K, step, rows, s.K, tid);
+    cp_async_commit();
+    float *system = reinterpret_cast<float *>(mem + L::system);
+    Factors &f = *reinterpret_cast<Factors *>(mem + L::out + 3 * kTile);
+    if (warp == 7) {
+        load_decays(d, g + row * s.H + head, beta + row * s.H + head, s.H, rows);
+        __syncwarp();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int t = 32 * half + lane;
+            const float start = d.start(t);
+            f.start[t] = start;
+            f.start_scaled[t] = s.scale * start;
+            f.end[t] = d.end(t);
+            f.beta[t] = d.beta[t];
+            if (t == kBlock - 1) f.last = start;
+        }
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    // rows 16 j of K K^T and of Q K^T have j + 1 blocks of 16 x 16: twenty in all, two or three a warp
+    {
+        const int j = warp < 4 ? 3 - warp / 2 : warp < 6 ? 1 : 0;
+        const int first = warp < 6 ? warp % 2 : warp - 6;
+        const uint32_t from = base + first * L::tile;
+        const uint32_t pairs = base + L::out + 2 * kTile;
+        pair_products<KP>(from, base, j, d, [&](int t, int r, float x, float y) {
+            if (first == 0)
+                *reinterpret_cast<float2 *>(system + t * kPairStride + r) = make_float2(r < t ? x : 0.0f, r + 1 < t ? y : 0.0f);
+            else
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(place<64>(pairs, t, r & ~7) + (r & 7) * 2),
+                             "r"(pack(r <= t ? s.scale * x : 0.0f, r + 1 <= t ? s.scale * y : 0.0f))
+                             : "memory");
+        });
+    }
+    __syncthreads();
+    lower_solve(system, d.beta, tid);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int at = i * kPairThreads + tid, t = at / 8, r = at % 8 * 8;
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float a = r + 2 * e < t ? -system[t * kPairStride + r + 2 * e] : 0.0f;
+            const float b = r + 2 * e + 1 < t ? -system[t * kPairStride + r + 2 * e + 1] : 0.0f;
+            split(a, b, h[e], l[e]);
+        }
+        unsigned char *out = mem + L::out + place<64>(0, t, r);
+        *reinterpret_cast<uint4 *>(out) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4 *>(out + kTile) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+    __syncthreads();
+    uint4 *to = reinterpret_cast<uint4 *>(records + (slot * s.H + head) * kRecord);
+    const uint4 *from = reinterpret_cast<const uint4 *>(mem + L::out);
+    for (int i = tid; i < kRecord / 16; i += kPairThreads) to[i] = from[i];
+}
+
+template <int KP>
+static cudaError_t go(const Shape &s, const bf *q, const bf *k, const bf *g, const bf *beta, unsigned char *records,
+                      cudaStream_t st) {
+    const int64_t grid = s.slots() * s.H;
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    constexpr int bytes = PairLayout<KP>::bytes;
+    if (cudaError_t e = cudaFuncSetAttribute(pairs_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+    pairs_kernel<KP><<<unsigned(grid), kPairThreads, bytes, st>>>(s, q, k, g, beta, records);
+    return cudaGetLastError();
+}
+
+cudaError_t make_pairs(const Shape &s, const bf *q, const bf *k, const bf *g, const bf *beta, unsigned char *records,
+                       cudaStream_t st) {
+    return s.K <= 64 ? go<64>(s, q, k, g, beta, records, st) : go<128>(s, q, k, g, beta, records, st);
+}
+
+}  // namespace mma
+}  // namespace delta
+}  // namespace ssm

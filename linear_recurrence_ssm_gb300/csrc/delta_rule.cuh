@@ -57,6 +57,20 @@ __device__ __forceinline__ Span span_of(const Shape &s, int i) {
     return {b, int64_t(b / kBlock) + i, e - b, (e - b + kBlock - 1) / kBlock};
 }
 
+// The sequence whose block has place `slot`, or -1.  All threads of the thread
+// block; `found` is in shared memory.
+__device__ __forceinline__ int sequence_of(const Shape &s, int64_t slot, int *found) {
+    if (!s.offsets) return int(slot / ((s.L + kBlock - 1) / kBlock));
+    if (threadIdx.x == 0) *found = -1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < s.n; i += blockDim.x) {
+        const Span span = span_of(s, i);
+        if (slot >= span.slot && slot < span.slot + span.blocks) atomicMax(found, i);
+    }
+    __syncthreads();
+    return *found;
+}
+
 // The sums of log2 decays inside a block, as two floats: differences of far
 // steps keep their relative accuracy after the exponential.  A decay below
 // e^-100 is 0 in fp32: such a step counts as a cut, adds nothing to the sum,
@@ -73,39 +87,87 @@ struct Decays {
 constexpr float kCut = -100.0f;
 
 // One warp: the running sums of `rows` steps; steps behind them do not decay
-// and write nothing (beta = 0).  `at` is the first step's gate, `stride` the
-// heads of a token.
-template <typename T>
-__device__ __forceinline__ void load_decays(Decays &d, const T *g, const T *beta, int64_t stride, int rows) {
+// and write nothing (beta = 0).  `g` and `beta` start at the first step,
+// `stride` is the heads of a token.  A lane has steps `lane` and `lane + 32`.
+struct Gates {
+    float g[2], beta[2];
+    template <typename T>
+    __device__ __forceinline__ void load(const T *from_g, const T *from_beta, int64_t stride, int rows) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int t = 32 * half + int(threadIdx.x % 32);
+            g[half] = t < rows ? to_f32(from_g[t * stride]) : 0.0f;
+            beta[half] = t < rows ? to_f32(from_beta[t * stride]) : 0.0f;
+        }
+    }
+};
+// A sum of two floats' exact sum and what it leaves over.
+__device__ __forceinline__ void add_to(float &hi, float &lo, float more_hi, float more_lo) {
+    const float s = __fadd_rn(hi, more_hi), b = __fsub_rn(s, hi);
+    lo = __fadd_rn(__fadd_rn(lo, more_lo), __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(more_hi, b)));
+    hi = s;
+}
+__device__ __forceinline__ void sum_decays(Decays &d, const Gates &w) {
     const int lane = threadIdx.x % 32;
-    double sum = 0.0;
+    float sum_hi = 0.0f, sum_lo = 0.0f;
     int cuts = 0;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int t = 32 * half + lane;
-        const float v = t < rows ? to_f32(g[t * stride]) : 0.0f;
-        const bool cut = v < kCut;
-        double w = cut ? 0.0 : double(v) * 1.4426950408889634;
+        const bool cut = w.g[half] < kCut;
+        const float v = cut ? 0.0f : w.g[half];
+        // g log2(e): the constant in two floats, the product's remainder from a fused multiply-add
+        float hi = __fmul_rn(v, 1.44269502162933349609375f);
+        float lo = __fmaf_rn(v, 1.925963033500011e-8f, __fmaf_rn(v, 1.44269502162933349609375f, -hi));
         int c = cut;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
-            const double x = __shfl_up_sync(0xffffffffu, w, o);
-            const int y = __shfl_up_sync(0xffffffffu, c, o);
-            if (lane >= o) w += x, c += y;
+            const float x = __shfl_up_sync(0xffffffffu, hi, o), y = __shfl_up_sync(0xffffffffu, lo, o);
+            const int n = __shfl_up_sync(0xffffffffu, c, o);
+            if (lane >= o) {
+                add_to(hi, lo, x, y);
+                c += n;
+            }
         }
-        w += sum, c += cuts;
-        const float hi = float(w);
+        add_to(hi, lo, sum_hi, sum_lo);
+        c += cuts;
         d.hi[t] = hi;
-        d.lo[t] = float(w - double(hi));
+        d.lo[t] = lo;
         d.cut[t] = c;
-        d.beta[t] = t < rows ? to_f32(beta[t * stride]) : 0.0f;
-        sum = __shfl_sync(0xffffffffu, w, 31);
+        d.beta[t] = w.beta[half];
+        sum_hi = __shfl_sync(0xffffffffu, hi, 31), sum_lo = __shfl_sync(0xffffffffu, lo, 31);
         cuts = __shfl_sync(0xffffffffu, c, 31);
     }
+}
+template <typename T>
+__device__ __forceinline__ void load_decays(Decays &d, const T *g, const T *beta, int64_t stride, int rows) {
+    Gates w;
+    w.load(g, beta, stride, rows);
+    sum_decays(d, w);
 }
 
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16(v); }
+
+// `width` elements of the rows of `out`, `step` elements apart, that no sequence covers become 0: those
+// before the first sequence (its blocks write them) and behind the last.
+template <typename T>
+__device__ __forceinline__ void clear_uncovered(const Shape &s, int seq, T *out, int64_t step, int width) {
+    if (!s.offsets || out == nullptr) return;
+    int64_t a = 0, b = 0;
+    for (int part = 0; part < 2; ++part) {
+        if (part == 0) {
+            if (seq != 0) continue;
+            a = 0, b = span_of(s, 0).first;
+        } else {
+            if (seq != s.n - 1) continue;
+            const Span last = span_of(s, s.n - 1);
+            a = last.first + last.len, b = s.L;
+        }
+        for (int64_t i = threadIdx.x; i < (b - a) * width; i += blockDim.x)
+            put(out + (a + i / width) * step + i % width, 0.0f);
+    }
+}
 
 // What the backward pass keeps between its kernels, one after another in the
 // caller's scratch.
@@ -132,6 +194,7 @@ struct FwdArgs {
     T *y;
     float *h_final;
     T *states, *errors;     // kept for the gradients, or null
+    unsigned char *scratch;
 };
 template <typename T>
 struct BwdArgs {

@@ -18,7 +18,7 @@ def swapped(n, i, value):
 
 
 def fwd(ptrs=None, scale=1.0, Bs=1, L=8, G=2, H=4, K=16, V=8, n=1, bf16=1):
-    p = ptrs or [P] * 11         # q k v g beta | offsets h0 y h_final states errors
+    p = ptrs or [P] * 12         # q k v g beta | offsets h0 y h_final states errors scratch
     return lrs.library().delta_rule_fwd(*p[:5], scale, *p[5:], Bs, L, G, H, K, V, n, bf16, None)
 
 
@@ -32,7 +32,7 @@ def step(ptrs=None, scale=1.0, Bs=2, G=2, H=4, K=16, V=8, pages=4, bf16=1):
     return lrs.library().delta_rule_step(*p[:5], scale, *p[5:], Bs, G, H, K, V, pages, bf16, None)
 
 
-@pytest.mark.parametrize("call,n", [(fwd, 11), (bwd, 16)])
+@pytest.mark.parametrize("call,n", [(fwd, 12), (bwd, 16)])
 def test_sizes(call, n):
     for kw in (dict(L=0), dict(G=0), dict(H=0), dict(K=0), dict(V=-1), dict(Bs=2), dict(n=-1), dict(H=5), dict(G=3),
                dict(scale=float("inf")), dict(scale=float("nan")), dict(L=2 ** 31, H=2 ** 40, G=2 ** 20)):
@@ -45,10 +45,10 @@ def test_sizes(call, n):
 
 
 def test_fwd_pointers():
-    for i in (0, 1, 2, 3, 4, 7, 9, 10):          # states and errors: both or none
-        assert fwd(swapped(11, i, None)) == INVALID
-    for i in range(11):
-        assert fwd(swapped(11, i, ODD)) == ALIGNMENT
+    for i in (0, 1, 2, 3, 4, 7, 9, 10, 11):      # states and errors: both or none
+        assert fwd(swapped(12, i, None)) == INVALID
+    for i in range(12):
+        assert fwd(swapped(12, i, ODD)) == ALIGNMENT
 
 
 def test_bwd_pointers():
@@ -61,7 +61,9 @@ def test_bwd_pointers():
 
 def test_scratch_size():
     lib = lrs.library()
-    assert lib.delta_rule_bwd_scratch(1, 8, 2, 4, 16, 8, 0, 1) > 0
+    for f in (lib.delta_rule_fwd_scratch, lib.delta_rule_bwd_scratch):
+        assert f(1, 8, 2, 4, 16, 8, 0, 1) > 0 and f(1, 8, 2, 4, 17, 9, 3, 0) > 0
+        assert f(1, 8, 3, 4, 16, 8, 0, 1) == f(1, 8, 2, 4, 300, 8, 0, 1) == 0
     assert lib.delta_rule_bwd_scratch(1, 8, 3, 4, 16, 8, 0, 1) == 0          # refused sizes
     assert lib.delta_rule_bwd_scratch(2, 8, 2, 4, 16, 8, 1, 1) == 0
     # a state a block of 64 steps and head at least
