@@ -5,6 +5,7 @@
 
 #include <float.h>
 #include <limits.h>
+#include <algorithm>
 #include <mutex>
 
 #include "delta_mma.cuh"
@@ -107,7 +108,6 @@ cudaError_t compact(void *pool, uint8_t *used, int32_t *moved, int32_t *pages, i
 }
 namespace delta {
 namespace general {
-int slices(const Shape &s);
 template <typename T>
 cudaError_t fwd(const FwdArgs<T> &a, cudaStream_t st);
 template <typename T>
@@ -117,6 +117,10 @@ namespace mma {
 namespace fwd {
 bool fits(const FwdArgs<__nv_bfloat16> &a);
 cudaError_t launch(const FwdArgs<__nv_bfloat16> &a, cudaStream_t st);
+}
+namespace bwd {
+bool fits(const BwdArgs<__nv_bfloat16> &a);
+cudaError_t launch(const BwdArgs<__nv_bfloat16> &a, cudaStream_t st);
 }
 }
 namespace step {
@@ -467,6 +471,17 @@ ssm::delta::Shape delta_shape(const int32_t *offsets, int64_t Bs, int64_t L, int
     return s;
 }
 
+// The scratch of the gradients holds what either path needs.
+ssm::delta::Scratch delta_scratch(const ssm::delta::Shape &s, int elem) {
+    int64_t shares = ssm::delta::general::shares(s), records = 0;
+    if (elem == 2 && ssm::delta::mma::fits_bwd(s)) {
+        const int64_t blocks = s.slots() * s.H;
+        shares = std::max(shares, blocks * ssm::delta::kBlock * ssm::delta::mma::dbeta_parts(s));
+        records = blocks * ssm::delta::mma::kBothRecord;
+    }
+    return ssm::delta::scratch_of(s, elem, shares, records);
+}
+
 template <typename T>
 ssm_status_t delta_fwd_entry(const void *q, const void *k, const void *v, const void *g,
                              const void *beta, float scale, const int32_t *offsets,
@@ -521,7 +536,7 @@ ssm_status_t delta_bwd_entry(const void *q, const void *k, const void *g, const 
     s = current_device(&dev);
     if (s != SSM_OK) return s;
     const ssm::delta::Shape shape = delta_shape(offsets, Bs, L, G, H, K, V, n_seq, scale);
-    const ssm::delta::Scratch at = ssm::delta::scratch_of(shape, int(e), ssm::delta::general::slices(shape));
+    const ssm::delta::Scratch at = delta_scratch(shape, int(e));
     char *mem = static_cast<char *>(scratch);
     const ssm::delta::BwdArgs<T> a{shape, static_cast<const T *>(q), static_cast<const T *>(k),
                                    static_cast<const T *>(g), static_cast<const T *>(beta),
@@ -531,8 +546,12 @@ ssm_status_t delta_bwd_entry(const void *q, const void *k, const void *g, const 
                                    static_cast<T *>(dbeta), dh0, reinterpret_cast<T *>(mem + at.ds),
                                    reinterpret_cast<float *>(mem + at.dbeta),
                                    reinterpret_cast<float *>(mem + at.dq),
-                                   reinterpret_cast<float *>(mem + at.dk)};
-    return from_cuda(ssm::delta::general::bwd(a, static_cast<cudaStream_t>(stream)));
+                                   reinterpret_cast<float *>(mem + at.dk),
+                                   reinterpret_cast<unsigned char *>(mem + at.records)};
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if constexpr (sizeof(T) == 2)
+        if (ssm::delta::mma::bwd::fits(a)) return from_cuda(ssm::delta::mma::bwd::launch(a, st));
+    return from_cuda(ssm::delta::general::bwd(a, st));
 }
 
 template <typename T>
@@ -969,7 +988,7 @@ int64_t delta_rule_bwd_scratch(int64_t Bs, int64_t L, int64_t G, int64_t H, int6
     if (check_delta_sizes(Bs, L, G, H, K, V, n_seq, 1.0f) != SSM_OK) return 0;
     static const int32_t some = 0;      // only that there are offsets counts
     const ssm::delta::Shape s = delta_shape(n_seq > 0 ? &some : nullptr, Bs, L, G, H, K, V, n_seq, 1.0f);
-    return ssm::delta::scratch_of(s, io_bf16 ? 2 : 4, ssm::delta::general::slices(s)).bytes;
+    return delta_scratch(s, io_bf16 ? 2 : 4).bytes;
 }
 
 ssm_status_t delta_rule_bwd(const void *q, const void *k, const void *g, const void *beta, float scale,

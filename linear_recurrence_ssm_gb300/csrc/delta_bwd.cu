@@ -1,0 +1,614 @@
+// delta_bwd.cu -- gradients of the gated delta rule, bf16, on tensor cores.
+//
+// back_kernel walks a sequence from its end with the state's adjoint A (V x K)
+// in four warps' accumulators, 16 rows each, as the forward kernel does:
+//   dU^T = E (A K^T) + dY^T P,  Z^T = dU^T - (beta dU)^T N,  dV = beta Z
+//   A = Gam_C A + (scale Gam dY)^T Q - (Gam beta Z)^T K
+// Four more warps form dY^T P and (scale Gam dY)^T Q, which do not depend on
+// A, one block ahead.  A's own chain uses operands of two bf16 terms (dh0 comes
+// out within 1e-5); it leaves A of every block, dV and shares of dbeta.
+//
+// block_kernel then takes all blocks at once: dQ, dK and dg from the kept states,
+// the adjoints, dY, X and dV.
+#include "delta_mma.cuh"
+
+namespace ssm {
+namespace delta {
+namespace mma {
+namespace bwd {
+
+constexpr int kSlice = 64, kChain = 4, kThreads = 256;
+
+template <int KP>
+struct Layout {
+    static constexpr int tile = kBlock * KP * 2, v = kBlock * kSlice * 2;
+    static constexpr int chain = tile + 2 * kTile + v + 1040;       // K, N in two terms, X, the factors: two of them
+    static constexpr int ahead = tile + v + 2 * kTile + 256;        // Q, dY, P in two terms, scale Gam: two of them
+    static constexpr int at_ahead = 2 * chain, handed = at_ahead + 2 * ahead;
+    static constexpr int u = 16 * kBlock * 4, s = 16 * KP * 4;      // of a warp: dY^T P and (scale Gam dY)^T Q
+    static constexpr int out = handed + kChain * (u + s);
+    static constexpr int out_warp = 16 * 128 * 2;
+    static constexpr int bytes = out + kChain * out_warp;
+    static_assert(sizeof(Factors) <= 1040 && bytes <= 232448, "shared memory");
+};
+
+__device__ __forceinline__ void put_values(uint32_t at, const float (&v)[4]) {
+    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+}
+__device__ __forceinline__ float4 get_values(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
+template <int KP>
+__global__ void __launch_bounds__(kThreads, 1) back_kernel(const BwdArgs<bf> p) {
+    extern __shared__ __align__(1024) unsigned char mem[];
+    using L = Layout<KP>;
+    const Shape &s = p.s;
+    const uint32_t base = smem_u32(mem);
+    const int slices = (s.V + kSlice - 1) / kSlice;
+    const int slice = int(blockIdx.x % slices), head = int(blockIdx.x / slices % s.H);
+    const int seq = int(blockIdx.x / slices / s.H), group = head / (s.H / s.G), v0 = slice * kSlice;
+    const Span span = span_of(s, seq);
+    const int64_t qk_step = int64_t(s.G) * s.K, v_step = int64_t(s.H) * s.V;
+    const int64_t slots = s.offsets ? s.L / kBlock + s.n : (s.L + kBlock - 1) / kBlock * s.n;
+    const int tid = threadIdx.x, warp = tid / 32 % kChain, lane = tid % 32;
+    const bool chain = tid < 32 * kChain;
+    const int g = lane / 4, c2 = lane % 4 * 2, mine = v0 + 16 * warp;
+    const int width = s.V - mine;
+    const int64_t state_at = (int64_t(seq) * s.H + head) * s.V * s.K;
+    const uint32_t hand_u = base + L::handed + warp * (L::u + L::s) + lane * 16, hand_s = hand_u + L::u;
+
+    // for turn i + 1: what the warps ahead need of block blocks - 2 - i, and the chain of the one before
+    const auto copy_ahead = [&](int c, int stage) {
+        const int64_t row = span.first + int64_t(c) * kBlock;
+        const int rows = min(kBlock, span.len - c * kBlock);
+        const uint32_t to = base + L::at_ahead + stage * L::ahead;
+        const unsigned char *record = p.records + ((span.slot + c) * s.H + head) * kBothRecord;
+        copy_tile<KP, kThreads>(to, p.q + row * qk_step + int64_t(group) * s.K, qk_step, rows, s.K, tid);
+        copy_tile<kSlice, kThreads>(to + L::tile, p.dy + row * v_step + int64_t(head) * s.V + v0, v_step, rows,
+                                    min(kSlice, s.V - v0), tid);
+#pragma unroll
+        for (int i = 0; i < kTile / 16 / kThreads; ++i) {
+            const int at = (i * kThreads + tid) * 16;
+            copy16(to + L::tile + L::v + at, record + 2 * kTile + at);
+            copy16(to + L::tile + L::v + kTile + at, record + kRecord + at);
+        }
+        if (tid < 16)
+            copy16(to + L::tile + L::v + 2 * kTile + tid * 16, record + 3 * kTile + offsetof(Factors, start_scaled) + tid * 16);
+    };
+    const auto copy_chain = [&](int c, int stage) {
+        const int64_t row = span.first + int64_t(c) * kBlock;
+        const int rows = min(kBlock, span.len - c * kBlock);
+        const uint32_t to = base + stage * L::chain;
+        const unsigned char *record = p.records + ((span.slot + c) * s.H + head) * kBothRecord;
+        copy_tile<KP, kThreads>(to, p.k + row * qk_step + int64_t(group) * s.K, qk_step, rows, s.K, tid);
+#pragma unroll
+        for (int i = 0; i < 2 * kTile / 16 / kThreads; ++i)
+            copy16(to + L::tile + (i * kThreads + tid) * 16, record + (i * kThreads + tid) * 16);
+        copy_tile<kSlice, kThreads>(to + L::tile + 2 * kTile, p.errors + row * v_step + int64_t(head) * s.V + v0, v_step,
+                                    rows, min(kSlice, s.V - v0), tid);
+        if (tid < int(sizeof(Factors)) / 16)
+            copy16(to + L::tile + 2 * kTile + L::v + tid * 16, record + 3 * kTile + tid * 16);
+    };
+    float st[KP / 8][4], w[8][4];       // the adjoint and dU; of the warps ahead, what they hand over
+#pragma unroll
+    for (int n = 0; n < KP / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int v = g + e / 2 * 8, k = 8 * n + c2 + e % 2;
+            st[n][e] = chain && p.dh_final && v < width && k < s.K ? p.dh_final[state_at + int64_t(mine + v) * s.K + k] : 0.0f;
+        }
+    if (span.blocks > 0) copy_ahead(span.blocks - 1, 0);
+    cp_async_commit();
+    for (int i = 0; i <= span.blocks; ++i) {
+        cp_async_wait<0>();
+        __syncthreads();
+        if (i + 1 < span.blocks) copy_ahead(span.blocks - 2 - i, (i + 1) % 2);
+        if (i < span.blocks) copy_chain(span.blocks - 1 - i, (i + 1) % 2);
+        cp_async_commit();
+        if (!chain) {
+            if (i > 0) {
+#pragma unroll
+                for (int n = 0; n < 8; ++n) put_values(hand_u + n * 512, w[n]);
+#pragma unroll
+                for (int n = 0; n < KP / 8; ++n) put_values(hand_s + n * 512, st[n]);
+                asm volatile("bar.arrive 1, 256;" ::: "memory");
+            }
+            if (i == span.blocks) break;
+            const int from = L::at_ahead + i % 2 * L::ahead;
+            const uint32_t at = base + from, pairs = at + L::tile + L::v;
+            const float *by = reinterpret_cast<const float *>(mem + from + L::tile + L::v + 2 * kTile);
+            uint32_t y[4][4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) load4t(y[t], four_across<64>(at + L::tile, 16 * t, 16 * warp));
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[n][e] = 0.0f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                uint32_t b[4][4], rest[4][4];
+#pragma unroll
+                for (int r = 0; r <= t; ++r) {
+                    load4t(b[r], four<64>(pairs, 16 * t, 16 * r));
+                    load4t(rest[r], four<64>(pairs + kTile, 16 * t, 16 * r));
+                }
+                across_to(w, y[t], b, t);
+                across_to(w, y[t], rest, t);
+            }
+            uint32_t hi[4][4], lo[4][4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float2 f = *reinterpret_cast<const float2 *>(by + 16 * t + 8 * h + c2);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        split(f.x * low(y[t][2 * h + e]), f.y * high(y[t][2 * h + e]), hi[t][2 * h + e], lo[t][2 * h + e]);
+                }
+#pragma unroll
+            for (int n = 0; n < KP / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) st[n][e] = 0.0f;
+            add_outer<KP>(st, hi, lo, at);
+        } else if (i > 0) {
+            const int c = span.blocks - i, rows = min(kBlock, span.len - c * kBlock);
+            const int64_t row = span.first + int64_t(c) * kBlock;
+            const int from = i % 2 * L::chain;
+            const uint32_t at = base + from, room = base + L::out + warp * L::out_warp;
+            const Factors &f = *reinterpret_cast<const Factors *>(mem + from + L::tile + 2 * kTile + L::v);
+            // A K^T
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[n][e] = 0.0f;
+            {
+                uint32_t b[2][4][4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) load4(b[0][t], four_across<KP>(at, 16 * t, 0));
+#pragma unroll
+                for (int k = 0; k < KP / 16; ++k) {
+                    uint32_t hi[4], lo[4];
+                    operand<KP>(hi, lo, st, k);
+                    store4(four<KP>(room, 0, 16 * k), hi);
+                    if (k + 1 < KP / 16)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) load4(b[(k + 1) % 2][t], four_across<KP>(at, 16 * t, 16 * (k + 1)));
+                    across(w, hi, b[k % 2]);
+                    across(w, lo, b[k % 2]);
+                }
+            }
+            __syncwarp();
+            {
+                bf *out = p.ds + ((span.slot + c) * s.H + head) * int64_t(s.V) * s.K + int64_t(mine) * s.K;
+#pragma unroll
+                for (int j = 0; j < 16 * KP / 8 / 32; ++j) {
+                    const int v = (j * 32 + lane) / (KP / 8), k = (j * 32 + lane) % (KP / 8) * 8;
+                    const uint4 x = load16(place<KP>(room, v, k));
+                    if (v < width && k < s.K) *reinterpret_cast<uint4 *>(out + int64_t(v) * s.K + k) = x;
+                }
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            // dU, and beta dU as two terms
+            uint32_t hi[4][4], lo[4][4];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                const float2 end = *reinterpret_cast<const float2 *>(f.end + 8 * n + c2);
+                const float2 beta = *reinterpret_cast<const float2 *>(f.beta + 8 * n + c2);
+                const float4 more = get_values(hand_u + n * 512);
+                w[n][0] = kept(end.x, w[n][0]) + more.x, w[n][1] = kept(end.y, w[n][1]) + more.y;
+                w[n][2] = kept(end.x, w[n][2]) + more.z, w[n][3] = kept(end.y, w[n][3]) + more.w;
+                split(beta.x * w[n][0], beta.y * w[n][1], hi[n / 2][n % 2 * 2], lo[n / 2][n % 2 * 2]);
+                split(beta.x * w[n][2], beta.y * w[n][3], hi[n / 2][n % 2 * 2 + 1], lo[n / 2][n % 2 * 2 + 1]);
+            }
+            // Z
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                uint32_t n[4][4], rest[4][4];
+#pragma unroll
+                for (int r = 0; r <= t; ++r) {
+                    load4t(n[r], four<64>(at + L::tile, 16 * t, 16 * r));
+                    load4t(rest[r], four<64>(at + L::tile + kTile, 16 * t, 16 * r));
+                }
+                across_to(w, hi[t], n, t);
+                across_to(w, lo[t], n, t);
+                across_to(w, hi[t], rest, t);
+            }
+            // shares of dbeta, dV, and -Gam beta Z
+            float *part = p.dbeta_part + (((int64_t(slice) * kChain + warp) * slots + span.slot + c) * s.H + head) * kBlock;
+            __syncwarp();
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                uint32_t x[4];
+                load4t(x, four_across<64>(at + L::tile + 2 * kTile, 16 * t, 16 * warp));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int n = 2 * t + h;
+                    float a = w[n][0] * low(x[2 * h]) + w[n][2] * low(x[2 * h + 1]);
+                    float b = w[n][1] * high(x[2 * h]) + w[n][3] * high(x[2 * h + 1]);
+#pragma unroll
+                    for (int o = 4; o < 32; o *= 2) {
+                        a += __shfl_xor_sync(0xffffffffu, a, o);
+                        b += __shfl_xor_sync(0xffffffffu, b, o);
+                    }
+                    if (g == 0) *reinterpret_cast<float2 *>(part + 8 * n + c2) = make_float2(a, b);
+                    const float2 beta = *reinterpret_cast<const float2 *>(f.beta + 8 * n + c2);
+                    const float2 start = *reinterpret_cast<const float2 *>(f.start + 8 * n + c2);
+                    w[n][0] *= beta.x, w[n][1] *= beta.y, w[n][2] *= beta.x, w[n][3] *= beta.y;
+                    split(kept(-start.x, w[n][0]), kept(-start.y, w[n][1]), hi[t][2 * h], lo[t][2 * h]);
+                    split(kept(-start.x, w[n][2]), kept(-start.y, w[n][3]), hi[t][2 * h + 1], lo[t][2 * h + 1]);
+                }
+                store_turned(room, t, w);
+            }
+            __syncwarp();
+            write_turned(p.dv + row * v_step + int64_t(head) * s.V + mine, v_step, rows, width, room);
+            __syncwarp();
+            // A
+            const float last = f.last;
+#pragma unroll
+            for (int n = 0; n < KP / 8; ++n) {
+                const float4 more = get_values(hand_s + n * 512);
+                st[n][0] = kept(last, st[n][0]) + more.x, st[n][1] = kept(last, st[n][1]) + more.y;
+                st[n][2] = kept(last, st[n][2]) + more.z, st[n][3] = kept(last, st[n][3]) + more.w;
+            }
+            add_outer<KP>(st, hi, lo, at);
+        }
+    }
+    if (chain && p.dh0)
+#pragma unroll
+        for (int n = 0; n < KP / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int v = g + e / 2 * 8, k = 8 * n + c2 + e % 2;
+                if (v < width && k < s.K) p.dh0[state_at + int64_t(mine + v) * s.K + k] = st[n][e];
+            }
+    clear_uncovered(s, seq, p.dv + int64_t(head) * s.V + v0, v_step, min(kSlice, s.V - v0));
+    if (slice == 0) {
+        clear_uncovered(s, seq, p.dg + head, s.H, 1);
+        clear_uncovered(s, seq, p.dbeta + head, s.H, 1);
+        if (head < s.G) {
+            clear_uncovered(s, seq, p.dq + int64_t(head) * s.K, qk_step, s.K);
+            clear_uncovered(s, seq, p.dk + int64_t(head) * s.K, qk_step, s.K);
+        }
+    }
+}
+
+// ---- dQ, dK, dg of a block -------------------------------------------------------------
+template <int KP, int VP>
+struct BlockLayout {
+    static constexpr int qk = kBlock * KP * 2, v = kBlock * 64 * 2, values = VP / 64 * v;
+    static constexpr int states = VP * KP * 2;
+    static constexpr int q = 0, k = q + qk, y = k + qk, x = y + values, dv = x + values, s0 = dv + values, s1 = s0 + states;
+    static constexpr int dp = s1 + states, da = dp + kTile, bytes = da + kTile;
+};
+
+// Warp 2 j + h: rows 16 j; of the pairs, those of the queries (h = 0) or of the
+// keys (h = 1); of dQ and dK, columns h KP / 2 to (h + 1) KP / 2.
+//
+// dg needs, of the pairs' products M = dP P + dAb Ab, the sums over r >= t > s.
+// With their row sums R and column sums C those are sum_{t' < t} (C - R)_t':
+// every M enters once with either sign, in fp32, so nothing is lost but the
+// rounding of the sums.
+template <int KP, int VP>
+__global__ void __launch_bounds__(256, VP == 64 ? 2 : 1) block_kernel(const BwdArgs<bf> p, const int parts) {
+    extern __shared__ __align__(1024) unsigned char mem[];
+    __shared__ Decays d;
+    __shared__ int found;
+    __shared__ float row_term[2][kBlock], col_term[2][kBlock], row_sum[2][kBlock], both_term[8];
+    __shared__ __align__(16) float col_sum[8][kBlock];
+    using L = BlockLayout<KP, VP>;
+    const Shape &s = p.s;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c2 = lane % 4 * 2;
+    const int head = int(blockIdx.x % s.H), group = head / (s.H / s.G);
+    const int64_t slot = blockIdx.x / s.H;
+    const int seq = sequence_of(s, slot, &found);
+    if (seq < 0) return;
+    const Span span = span_of(s, seq);
+    const int c = int(slot - span.slot), rows = min(kBlock, span.len - c * kBlock);
+    const int64_t row = span.first + int64_t(c) * kBlock;
+    const int64_t qk_step = int64_t(s.G) * s.K, v_step = int64_t(s.H) * s.V;
+    const uint32_t base = smem_u32(mem);
+    const int j = warp / 2, h = warp % 2;
+
+    copy_tile<KP, 256>(base + L::q, p.q + row * qk_step + int64_t(group) * s.K, qk_step, rows, s.K, tid);
+    copy_tile<KP, 256>(base + L::k, p.k + row * qk_step + int64_t(group) * s.K, qk_step, rows, s.K, tid);
+    const int64_t v_at = row * v_step + int64_t(head) * s.V;
+#pragma unroll
+    for (int v0 = 0; v0 < VP; v0 += 64) {
+        const int at = v0 / 64 * L::v, width = max(s.V - v0, 0);
+        copy_tile<64, 256>(base + L::y + at, p.dy + v_at + (width > 0 ? v0 : 0), v_step, rows, width, tid);
+        copy_tile<64, 256>(base + L::x + at, p.errors + v_at + (width > 0 ? v0 : 0), v_step, rows, width, tid);
+        copy_tile<64, 256>(base + L::dv + at, p.dv + v_at + (width > 0 ? v0 : 0), v_step, rows, width, tid);
+    }
+    cp_async_commit();
+    {
+        const bf *st0 = p.states + (slot * s.H + head) * int64_t(s.V) * s.K, *st1 = p.ds + (slot * s.H + head) * int64_t(s.V) * s.K;
+#pragma unroll
+        for (int v0 = 0; v0 < VP; v0 += 64) {
+            const int have = min(max(s.V - v0, 0), kBlock), at = have > 0 ? v0 : 0;
+            copy_tile<KP, 256>(base + L::s0 + v0 * KP * 2, st0 + int64_t(at) * s.K, s.K, have, s.K, tid);
+            copy_tile<KP, 256>(base + L::s1 + v0 * KP * 2, st1 + int64_t(at) * s.K, s.K, have, s.K, tid);
+        }
+    }
+    cp_async_commit();
+    if (warp == 0) load_decays(d, p.g + row * s.H + head, p.beta + row * s.H + head, s.H, rows);
+    cp_async_wait<1>();
+    __syncthreads();
+    // pairs: scale beta_s dY_t.x_s D with q_t.k_s, or -beta_s dV_t.x_s D with k_t.k_s
+    {
+        const uint32_t left = base + (h == 0 ? L::y : L::dv), key = base + (h == 0 ? L::q : L::k);
+        const uint32_t out = base + (h == 0 ? L::dp : L::da);
+        const float by = h == 0 ? s.scale : -1.0f;
+        uint32_t fv[VP / 16][4], fk[KP / 16][4];
+#pragma unroll
+        for (int v = 0; v < VP / 16; ++v) load4(fv[v], four<64>(left + v / 4 * L::v, 16 * j, v % 4 * 16));
+#pragma unroll
+        for (int k = 0; k < KP / 16; ++k) load4(fk[k], four<KP>(key, 16 * j, 16 * k));
+        const int t = 16 * j + g;
+        const float hi0 = d.hi[t], lo0 = d.lo[t], hi1 = d.hi[t + 8], lo1 = d.lo[t + 8];
+        const int cut0 = d.cut[t], cut1 = d.cut[t + 8];
+        float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll 1
+        for (int n = 0; n <= j; ++n) {
+            float a[2][4] = {}, m[2][4] = {};
+#pragma unroll
+            for (int v = 0; v < VP / 16; ++v) {
+                uint32_t b[4];
+                load4(b, four_across<64>(base + L::x + v / 4 * L::v, 16 * n, v % 4 * 16));
+                product(a[0], fv[v], b[0], b[1]);
+                product(a[1], fv[v], b[2], b[3]);
+            }
+#pragma unroll
+            for (int k = 0; k < KP / 16; ++k) {
+                uint32_t b[4];
+                load4(b, four_across<KP>(base + L::k, 16 * n, 16 * k));
+                product(m[0], fk[k], b[0], b[1]);
+                product(m[1], fk[k], b[2], b[3]);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 16 * n + 8 * e + c2;
+                const float2 hi = *reinterpret_cast<const float2 *>(d.hi + r), lo = *reinterpret_cast<const float2 *>(d.lo + r);
+                const float2 beta = *reinterpret_cast<const float2 *>(d.beta + r);
+                const int2 cut = *reinterpret_cast<const int2 *>(d.cut + r);
+                // below the diagonal; of the queries, on it as well
+                const float x0 = t >= r + h && cut0 == cut.x ? by * beta.x * a[e][0] * ex2((hi0 - hi.x) + (lo0 - lo.x)) : 0.0f;
+                const float x1 = t >= r + 1 + h && cut0 == cut.y ? by * beta.y * a[e][1] * ex2((hi0 - hi.y) + (lo0 - lo.y)) : 0.0f;
+                const float x2 = t + 8 >= r + h && cut1 == cut.x ? by * beta.x * a[e][2] * ex2((hi1 - hi.x) + (lo1 - lo.x)) : 0.0f;
+                const float x3 = t + 8 >= r + 1 + h && cut1 == cut.y ? by * beta.y * a[e][3] * ex2((hi1 - hi.y) + (lo1 - lo.y)) : 0.0f;
+                const float m0 = t > r ? x0 * m[e][0] : 0.0f, m1 = t > r + 1 ? x1 * m[e][1] : 0.0f;
+                const float m2 = t + 8 > r ? x2 * m[e][2] : 0.0f, m3 = t + 8 > r + 1 ? x3 * m[e][3] : 0.0f;
+                sum0 += m0 + m1, sum1 += m2 + m3;
+                float down0 = m0 + m2, down1 = m1 + m3;
+#pragma unroll
+                for (int o = 4; o < 32; o *= 2) {
+                    down0 += __shfl_xor_sync(0xffffffffu, down0, o);
+                    down1 += __shfl_xor_sync(0xffffffffu, down1, o);
+                }
+                if (g == 0) *reinterpret_cast<float2 *>(&col_sum[warp][r]) = make_float2(down0, down1);
+                const uint32_t w0 = pack(x0, x1), w1 = pack(x2, x3);
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(place<64>(out, t, r & ~7) + (r & 7) * 2), "r"(w0) : "memory");
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(place<64>(out, t + 8, r & ~7) + (r & 7) * 2), "r"(w1) : "memory");
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o *= 2) {
+            sum0 += __shfl_xor_sync(0xffffffffu, sum0, o);
+            sum1 += __shfl_xor_sync(0xffffffffu, sum1, o);
+        }
+        if (lane % 4 == 0) row_sum[h][t] = sum0, row_sum[h][t + 8] = sum1;
+        for (int r = 16 * (j + 1) + lane; r < kBlock; r += 32) col_sum[warp][r] = 0.0f;
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    // <S0, dS>
+    {
+        float both = 0.0f;
+        for (int i = tid; i < VP * KP / 8; i += 256) {
+            const int v = i / (KP / 8), k = i % (KP / 8) * 8;
+            const uint4 a = load16(place<KP>(base + L::s0, v, k)), b = load16(place<KP>(base + L::s1, v, k));
+            both += low(a.x) * low(b.x) + high(a.x) * high(b.x) + low(a.y) * low(b.y) + high(a.y) * high(b.y) +
+                    low(a.z) * low(b.z) + high(a.z) * high(b.z) + low(a.w) * low(b.w) + high(a.w) * high(b.w);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) both += __shfl_xor_sync(0xffffffffu, both, o);
+        if (lane == 0) both_term[warp] = both;
+    }
+    const int t0 = 16 * j + g, t1 = t0 + 8;
+    const float start0 = d.start(t0), start1 = d.start(t1), end0 = d.end(t0), end1 = d.end(t1);
+    float rt0 = 0.0f, rt1 = 0.0f, ct0 = 0.0f, ct1 = 0.0f;
+    constexpr int wide = KP / 2 < 64 ? KP / 2 : 64, tiles = wide / 8;      // columns at a time
+#pragma unroll 1
+    for (int k0 = h * (KP / 2); k0 < (h + 1) * (KP / 2); k0 += wide) {
+        float dq[tiles][4] = {}, dk[tiles][4] = {};
+        // through the state before the block
+#pragma unroll 2
+        for (int v = 0; v < VP / 16; ++v) {
+            uint32_t a[4], z[4], b[tiles / 2][4];
+            load4(a, four<64>(base + L::y + v / 4 * L::v, 16 * j, v % 4 * 16));
+            load4(z, four<64>(base + L::dv + v / 4 * L::v, 16 * j, v % 4 * 16));
+#pragma unroll
+            for (int n = 0; n < tiles / 2; ++n) load4t(b[n], four<KP>(base + L::s0, 16 * v, k0 + 16 * n));
+#pragma unroll
+            for (int n = 0; n < tiles / 2; ++n) {
+                product(dq[2 * n], a, b[n][0], b[n][1]);
+                product(dq[2 * n + 1], a, b[n][2], b[n][3]);
+                product(dk[2 * n], z, b[n][0], b[n][1]);
+                product(dk[2 * n + 1], z, b[n][2], b[n][3]);
+            }
+        }
+        const auto pair_at = [&](uint32_t tile, int t, int k) {
+            uint32_t v;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(place<KP>(tile, t, k & ~7) + (k & 7) * 2) : "memory");
+            return v;
+        };
+#pragma unroll
+        for (int n = 0; n < tiles; ++n) {
+            const int k = k0 + 8 * n + c2;
+            dq[n][0] = kept(s.scale * start0, dq[n][0]), dq[n][1] = kept(s.scale * start0, dq[n][1]);
+            dq[n][2] = kept(s.scale * start1, dq[n][2]), dq[n][3] = kept(s.scale * start1, dq[n][3]);
+            dk[n][0] = kept(-start0, dk[n][0]), dk[n][1] = kept(-start0, dk[n][1]);
+            dk[n][2] = kept(-start1, dk[n][2]), dk[n][3] = kept(-start1, dk[n][3]);
+            const uint32_t q0 = pair_at(base + L::q, t0, k), q1 = pair_at(base + L::q, t1, k);
+            const uint32_t e0 = pair_at(base + L::k, t0, k), e1 = pair_at(base + L::k, t1, k);
+            rt0 += dq[n][0] * low(q0) + dq[n][1] * high(q0) + dk[n][0] * low(e0) + dk[n][1] * high(e0);
+            rt1 += dq[n][2] * low(q1) + dq[n][3] * high(q1) + dk[n][2] * low(e1) + dk[n][3] * high(e1);
+        }
+        // through the pairs: dQ += (dP D) K, dK += (dAb D) K + (dAb D)^T K + (dP D)^T Q
+#pragma unroll 1
+        for (int r = 0; r < 4; ++r) {
+            uint32_t b[tiles / 2][4];
+#pragma unroll
+            for (int n = 0; n < tiles / 2; ++n) load4t(b[n], four<KP>(base + L::k, 16 * r, k0 + 16 * n));
+            if (r <= j) {
+                uint32_t a[4], z[4];
+                load4(a, four<64>(base + L::dp, 16 * j, 16 * r));
+                load4(z, four<64>(base + L::da, 16 * j, 16 * r));
+#pragma unroll
+                for (int n = 0; n < tiles / 2; ++n) {
+                    product(dq[2 * n], a, b[n][0], b[n][1]);
+                    product(dq[2 * n + 1], a, b[n][2], b[n][3]);
+                    product(dk[2 * n], z, b[n][0], b[n][1]);
+                    product(dk[2 * n + 1], z, b[n][2], b[n][3]);
+                }
+            }
+            if (r >= j) {
+                uint32_t a[4], z[4];
+                load4t(z, four_across<64>(base + L::da, 16 * r, 16 * j));
+                load4t(a, four_across<64>(base + L::dp, 16 * r, 16 * j));
+#pragma unroll
+                for (int n = 0; n < tiles / 2; ++n) {
+                    product(dk[2 * n], z, b[n][0], b[n][1]);
+                    product(dk[2 * n + 1], z, b[n][2], b[n][3]);
+                }
+#pragma unroll
+                for (int n = 0; n < tiles / 2; ++n) load4t(b[n], four<KP>(base + L::q, 16 * r, k0 + 16 * n));
+#pragma unroll
+                for (int n = 0; n < tiles / 2; ++n) {
+                    product(dk[2 * n], a, b[n][0], b[n][1]);
+                    product(dk[2 * n + 1], a, b[n][2], b[n][3]);
+                }
+            }
+        }
+        const auto write = [&](bf *whole, float *of_head, const float (&v)[tiles][4]) {
+#pragma unroll
+            for (int n = 0; n < tiles; ++n) {
+                const int k = k0 + 8 * n + c2;
+                if (k >= s.K) continue;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int t = t0 + 8 * e;
+                    if (t >= rows) continue;
+                    const int64_t o = ((row + t) * s.H + head) * s.K + k;
+                    if (s.H > s.G) *reinterpret_cast<float2 *>(of_head + o) = make_float2(v[n][2 * e], v[n][2 * e + 1]);
+                    else *reinterpret_cast<uint32_t *>(whole + o) = pack(v[n][2 * e], v[n][2 * e + 1]);
+                }
+            }
+        };
+        write(p.dq, p.dq_head, dq);
+        // through the adjoint of the state behind the block, in dQ's place
+#pragma unroll
+        for (int n = 0; n < tiles; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dq[n][e] = 0.0f;
+#pragma unroll 2
+        for (int v = 0; v < VP / 16; ++v) {
+            uint32_t a[4], b[tiles / 2][4];
+            load4(a, four<64>(base + L::x + v / 4 * L::v, 16 * j, v % 4 * 16));
+#pragma unroll
+            for (int n = 0; n < tiles / 2; ++n) load4t(b[n], four<KP>(base + L::s1, 16 * v, k0 + 16 * n));
+#pragma unroll
+            for (int n = 0; n < tiles / 2; ++n) {
+                product(dq[2 * n], a, b[n][0], b[n][1]);
+                product(dq[2 * n + 1], a, b[n][2], b[n][3]);
+            }
+        }
+        const float by0 = end0 * d.beta[t0], by1 = end1 * d.beta[t1];
+#pragma unroll
+        for (int n = 0; n < tiles; ++n) {
+            const int k = k0 + 8 * n + c2;
+            const uint32_t e0 = pair_at(base + L::k, t0, k), e1 = pair_at(base + L::k, t1, k);
+            const float a = kept(by0, dq[n][0]), b = kept(by0, dq[n][1]), x = kept(by1, dq[n][2]), y = kept(by1, dq[n][3]);
+            ct0 += a * low(e0) + b * high(e0);
+            ct1 += x * low(e1) + y * high(e1);
+            dk[n][0] += a, dk[n][1] += b, dk[n][2] += x, dk[n][3] += y;
+        }
+        write(p.dk, p.dk_head, dk);
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o *= 2) {
+        rt0 += __shfl_xor_sync(0xffffffffu, rt0, o), rt1 += __shfl_xor_sync(0xffffffffu, rt1, o);
+        ct0 += __shfl_xor_sync(0xffffffffu, ct0, o), ct1 += __shfl_xor_sync(0xffffffffu, ct1, o);
+    }
+    if (lane % 4 == 0) {
+        row_term[h][t0] = rt0, row_term[h][t1] = rt1;
+        col_term[h][t0] = ct0, col_term[h][t1] = ct1;
+    }
+    __syncthreads();
+    if (tid < rows) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += both_term[i];
+        sum = kept(d.start(kBlock - 1), sum);
+        float pairs = 0.0f;
+#pragma unroll 4
+        for (int r = 0; r < kBlock; ++r) {
+            if (r < tid) {
+                float down = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) down += col_sum[i][r];
+                pairs += down - (row_sum[0][r] + row_sum[1][r]);
+                sum += col_term[0][r] + col_term[1][r];
+            } else if (r < rows) {
+                sum += row_term[0][r] + row_term[1][r];
+            }
+        }
+        put(p.dg + (row + tid) * s.H + head, sum + pairs);
+        const int64_t slots = s.offsets ? s.L / kBlock + s.n : (s.L + kBlock - 1) / kBlock * s.n;
+        float b = 0.0f;
+        for (int i = 0; i < parts; ++i) b += p.dbeta_part[((i * slots + slot) * s.H + head) * kBlock + tid];
+        put(p.dbeta + (row + tid) * s.H + head, b);
+    }
+}
+
+static bool on16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+bool fits(const BwdArgs<bf> &a) {
+    return fits_bwd(a.s) && on16(a.q) && on16(a.k) && on16(a.dy) && on16(a.states) && on16(a.errors) && on16(a.dv) &&
+           reinterpret_cast<uintptr_t>(a.dq) % 4 == 0 && reinterpret_cast<uintptr_t>(a.dk) % 4 == 0;
+}
+
+template <int KP>
+static cudaError_t back(const BwdArgs<bf> &a, cudaStream_t st) {
+    const int64_t grid = int64_t(a.s.n) * a.s.H * ((a.s.V + kSlice - 1) / kSlice);
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    constexpr int bytes = Layout<KP>::bytes;
+    if (cudaError_t e = cudaFuncSetAttribute(back_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+    back_kernel<KP><<<unsigned(grid), kThreads, bytes, st>>>(a);
+    return cudaGetLastError();
+}
+template <int KP, int VP>
+static cudaError_t blocks(const BwdArgs<bf> &a, cudaStream_t st) {
+    const int64_t grid = a.s.slots() * a.s.H;
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    constexpr int bytes = BlockLayout<KP, VP>::bytes;
+    if (cudaError_t e = cudaFuncSetAttribute(block_kernel<KP, VP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+    block_kernel<KP, VP><<<unsigned(grid), 256, bytes, st>>>(a, dbeta_parts(a.s));
+    return cudaGetLastError();
+}
+
+cudaError_t launch(const BwdArgs<bf> &a, cudaStream_t st) {
+    if (cudaError_t e = make_pairs(a.s, a.q, a.k, a.g, a.beta, a.records, true, st)) return e;
+    if (cudaError_t e = a.s.K <= 64 ? back<64>(a, st) : back<128>(a, st)) return e;
+    const cudaError_t e = a.s.K <= 64 ? (a.s.V <= 64 ? blocks<64, 64>(a, st) : blocks<64, 128>(a, st))
+                                      : (a.s.V <= 64 ? blocks<128, 64>(a, st) : blocks<128, 128>(a, st));
+    if (e) return e;
+    return a.s.H > a.s.G ? general::fold(a, st) : cudaSuccess;
+}
+
+}  // namespace bwd
+}  // namespace mma
+}  // namespace delta
+}  // namespace ssm

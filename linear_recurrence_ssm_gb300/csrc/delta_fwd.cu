@@ -36,16 +36,6 @@ struct Layout {
     static_assert(sizeof(Factors) <= 1152 && bytes <= 232448, "shared memory");
 };
 
-// 16 columns of the state as a left operand of two terms.
-template <int KP>
-__device__ __forceinline__ void operand(uint32_t (&hi)[4], uint32_t (&lo)[4], const float (&s)[KP / 8][4], int k) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        split(s[2 * k + h][0], s[2 * k + h][1], hi[2 * h], lo[2 * h]);
-        split(s[2 * k + h][2], s[2 * k + h][3], hi[2 * h + 1], lo[2 * h + 1]);
-    }
-}
-
 template <int KP>
 __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdArgs<bf> p) {
     extern __shared__ __align__(1024) unsigned char mem[];
@@ -261,7 +251,7 @@ bool fits(const FwdArgs<bf> &a) {
 }
 
 cudaError_t launch(const FwdArgs<bf> &a, cudaStream_t st) {
-    if (cudaError_t e = make_pairs(a.s, a.q, a.k, a.g, a.beta, a.scratch, st)) return e;
+    if (cudaError_t e = make_pairs(a.s, a.q, a.k, a.g, a.beta, a.scratch, false, st)) return e;
     return a.s.K <= 64 ? go<64>(a, st) : go<128>(a, st);
 }
 

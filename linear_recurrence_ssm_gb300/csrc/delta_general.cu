@@ -617,7 +617,8 @@ __global__ void __launch_bounds__(kThreads) fold_kernel(const BwdArgs<T> p) {
     put(p.dk + i, kk);
 }
 
-int slices(const Shape &s) { return (s.V + kSlice - 1) / kSlice; }
+static int slices(const Shape &s) { return (s.V + kSlice - 1) / kSlice; }
+int64_t shares(const Shape &s) { return int64_t(slices(s)) * s.rows() * s.H; }
 
 template <typename K>
 static cudaError_t room(K kernel, int words) {
@@ -635,20 +636,27 @@ cudaError_t fwd(const FwdArgs<T> &a, cudaStream_t st) {
 }
 
 template <typename T>
+cudaError_t fold(const BwdArgs<T> &a, cudaStream_t st) {
+    const int64_t grid = (a.s.rows() * a.s.G * a.s.K + kThreads - 1) / kThreads;
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    fold_kernel<T><<<unsigned(grid), kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
 cudaError_t bwd(const BwdArgs<T> &a, cudaStream_t st) {
     const int64_t grid = int64_t(a.s.n) * a.s.H * slices(a.s), blocks = a.s.slots() * a.s.H;
-    const int64_t folds = (a.s.rows() * a.s.G * a.s.K + kThreads - 1) / kThreads;
-    if (grid > 0x7fffffff || blocks > 0x7fffffff || folds > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    if (grid > 0x7fffffff || blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     if (cudaError_t e = room(back_kernel<T>, layout_of(256).words)) return e;
     if (cudaError_t e = room(grads_kernel<T>, grad_layout_of(256).words)) return e;
     back_kernel<T><<<unsigned(grid), kThreads, layout_of(a.s.K).words * 4, st>>>(a);
     if (cudaError_t e = cudaGetLastError()) return e;
     grads_kernel<T><<<unsigned(blocks), kThreads, grad_layout_of(a.s.K).words * 4, st>>>(a);
     if (cudaError_t e = cudaGetLastError()) return e;
-    if (a.s.H > a.s.G) fold_kernel<T><<<unsigned(folds), kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return a.s.H > a.s.G ? fold(a, st) : cudaSuccess;
 }
 
+template cudaError_t fold<__nv_bfloat16>(const BwdArgs<__nv_bfloat16> &, cudaStream_t);
 template cudaError_t fwd<float>(const FwdArgs<float> &, cudaStream_t);
 template cudaError_t fwd<__nv_bfloat16>(const FwdArgs<__nv_bfloat16> &, cudaStream_t);
 template cudaError_t bwd<float>(const BwdArgs<float> &, cudaStream_t);

@@ -114,6 +114,26 @@ __device__ __forceinline__ void across(float (&d)[8][4], const uint32_t (&a)[4],
     }
 }
 
+// The same up to column 16 `to`.
+__device__ __forceinline__ void across_to(float (&d)[8][4], const uint32_t (&a)[4], const uint32_t (&b)[4][4], int to) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        if (t > to) continue;
+        product(d[2 * t], a, b[t][0], b[t][1]);
+        product(d[2 * t + 1], a, b[t][2], b[t][3]);
+    }
+}
+
+// 16 columns of the state as a left operand of two terms.
+template <int KP>
+__device__ __forceinline__ void operand(uint32_t (&hi)[4], uint32_t (&lo)[4], const float (&s)[KP / 8][4], int k) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        split(s[2 * k + h][0], s[2 * k + h][1], hi[2 * h], lo[2 * h]);
+        split(s[2 * k + h][2], s[2 * k + h][3], hi[2 * h + 1], lo[2 * h + 1]);
+    }
+}
+
 // The state's 16 rows += (hi + lo) times the 64 x KP tile; a tile's pieces are
 // loaded ahead of the products before them.
 template <int KP>
@@ -286,17 +306,20 @@ __device__ __forceinline__ void lower_solve(float *m, const float *beta, int tid
 }
 
 // What the chains need of a block besides its tokens, made once by
-// pairs_kernel: -N in two bf16 terms and P (with the scale), as 64 x 64 tiles
-// with their pieces exchanged as place<64> does, and the factors.  Blocks of
-// 16 x 16 above P's diagonal are unspecified.
+// pairs_kernel: -N in two bf16 terms, P (with the scale), the factors, and for
+// the gradients P's second term; tiles of 64 x 64 with their pieces exchanged
+// as place<64> does.  Blocks of 16 x 16 above P's diagonal are unspecified.
 constexpr int kTile = kBlock * kBlock * 2;
-constexpr int kRecord = (3 * kTile + int(sizeof(Factors)) + 127) / 128 * 128;
+constexpr int kRecord = (3 * kTile + int(sizeof(Factors)) + 127) / 128 * 128, kBothRecord = kRecord + kTile;
 cudaError_t make_pairs(const Shape &s, const bf *q, const bf *k, const bf *g, const bf *beta, unsigned char *records,
-                       cudaStream_t st);
+                       bool both, cudaStream_t st);
 
 // Sizes whose rows 16-byte copies can take, and whose states fit a warp's registers.
 inline bool fits(const Shape &s) { return s.K <= 128 && s.K % 8 == 0 && s.V % 8 == 0; }
 inline int64_t record_bytes(const Shape &s) { return s.slots() * s.H * kRecord; }
+// ... and whose block fits shared memory.
+inline bool fits_bwd(const Shape &s) { return fits(s) && s.V <= 128; }
+inline int dbeta_parts(const Shape &s) { return (s.V + 63) / 64 * 4; }
 
 }  // namespace mma
 }  // namespace delta

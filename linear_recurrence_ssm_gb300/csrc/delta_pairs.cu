@@ -16,12 +16,12 @@ template <int KP>
 struct PairLayout {
     static constexpr int tile = kBlock * KP * 2;
     static constexpr int system = 2 * tile, out = system + kBlock * kPairStride * 4;
-    static constexpr int bytes = out + kRecord;
+    static constexpr int bytes = out + kBothRecord;
 };
 
 template <int KP>
 __global__ void __launch_bounds__(kPairThreads, 2)
-pairs_kernel(const Shape s, const bf *q, const bf *k, const bf *g, const bf *beta, unsigned char *records) {
+pairs_kernel(const Shape s, const bf *q, const bf *k, const bf *g, const bf *beta, unsigned char *records, const bool both) {
     extern __shared__ __align__(128) unsigned char mem[];
     __shared__ Decays d;
     __shared__ int found;
@@ -65,10 +65,13 @@ pairs_kernel(const Shape s, const bf *q, const bf *k, const bf *g, const bf *bet
         pair_products<KP>(from, base, j, d, [&](int t, int r, float x, float y) {
             if (first == 0)
                 *reinterpret_cast<float2 *>(system + t * kPairStride + r) = make_float2(r < t ? x : 0.0f, r + 1 < t ? y : 0.0f);
-            else
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(place<64>(pairs, t, r & ~7) + (r & 7) * 2),
-                             "r"(pack(r <= t ? s.scale * x : 0.0f, r + 1 <= t ? s.scale * y : 0.0f))
-                             : "memory");
+            else {
+                uint32_t hi, lo;
+                split(r <= t ? s.scale * x : 0.0f, r + 1 <= t ? s.scale * y : 0.0f, hi, lo);
+                const uint32_t at = place<64>(pairs, t, r & ~7) + (r & 7) * 2;
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(hi) : "memory");
+                if (both) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + (kRecord - 2 * kTile)), "r"(lo) : "memory");
+            }
         });
     }
     __syncthreads();
@@ -88,25 +91,26 @@ pairs_kernel(const Shape s, const bf *q, const bf *k, const bf *g, const bf *bet
         *reinterpret_cast<uint4 *>(out + kTile) = make_uint4(l[0], l[1], l[2], l[3]);
     }
     __syncthreads();
-    uint4 *to = reinterpret_cast<uint4 *>(records + (slot * s.H + head) * kRecord);
+    const int size = both ? kBothRecord : kRecord;
+    uint4 *to = reinterpret_cast<uint4 *>(records + (slot * s.H + head) * size);
     const uint4 *from = reinterpret_cast<const uint4 *>(mem + L::out);
-    for (int i = tid; i < kRecord / 16; i += kPairThreads) to[i] = from[i];
+    for (int i = tid; i < size / 16; i += kPairThreads) to[i] = from[i];
 }
 
 template <int KP>
 static cudaError_t go(const Shape &s, const bf *q, const bf *k, const bf *g, const bf *beta, unsigned char *records,
-                      cudaStream_t st) {
+                      bool both, cudaStream_t st) {
     const int64_t grid = s.slots() * s.H;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     constexpr int bytes = PairLayout<KP>::bytes;
     if (cudaError_t e = cudaFuncSetAttribute(pairs_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
-    pairs_kernel<KP><<<unsigned(grid), kPairThreads, bytes, st>>>(s, q, k, g, beta, records);
+    pairs_kernel<KP><<<unsigned(grid), kPairThreads, bytes, st>>>(s, q, k, g, beta, records, both);
     return cudaGetLastError();
 }
 
 cudaError_t make_pairs(const Shape &s, const bf *q, const bf *k, const bf *g, const bf *beta, unsigned char *records,
-                       cudaStream_t st) {
-    return s.K <= 64 ? go<64>(s, q, k, g, beta, records, st) : go<128>(s, q, k, g, beta, records, st);
+                       bool both, cudaStream_t st) {
+    return s.K <= 64 ? go<64>(s, q, k, g, beta, records, both, st) : go<128>(s, q, k, g, beta, records, both, st);
 }
 
 }  // namespace mma

@@ -75,7 +75,7 @@ __device__ __forceinline__ int sequence_of(const Shape &s, int64_t slot, int *fo
 // steps keep their relative accuracy after the exponential.  A decay below
 // e^-100 is 0 in fp32: such a step counts as a cut, adds nothing to the sum,
 // and no pair reaches across it (-infinity is a cut).
-struct Decays {
+struct alignas(16) Decays {
     float hi[kBlock], lo[kBlock], beta[kBlock];
     int cut[kBlock];
     __device__ __forceinline__ float between(int t, int s) const {
@@ -172,17 +172,19 @@ __device__ __forceinline__ void clear_uncovered(const Shape &s, int seq, T *out,
 // What the backward pass keeps between its kernels, one after another in the
 // caller's scratch.
 struct Scratch {
-    int64_t ds, dbeta, dq, dk, bytes;
+    int64_t ds, dbeta, dq, dk, records, bytes;
 };
-inline Scratch scratch_of(const Shape &s, int elem, int slices) {
+// `shares`: floats of dbeta's parts; `records`: bytes.
+inline Scratch scratch_of(const Shape &s, int elem, int64_t shares, int64_t records) {
     const auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
     Scratch r;
     r.ds = 0;
     r.dbeta = up(s.slots() * s.states() * elem);
-    r.dq = r.dbeta + up(int64_t(slices) * s.rows() * s.H * 4);
+    r.dq = r.dbeta + up(shares * 4);
     const int64_t per_head = s.H > s.G ? up(s.rows() * s.H * s.K * 4) : 0;
     r.dk = r.dq + per_head;
-    r.bytes = r.dk + per_head;
+    r.records = r.dk + per_head;
+    r.bytes = r.records + up(records);
     return r;
 }
 
@@ -206,7 +208,13 @@ struct BwdArgs {
     float *dh0;
     T *ds;                  // scratch: the adjoint of every block's last state
     float *dbeta_part, *dq_head, *dk_head;
+    unsigned char *records;
 };
+namespace general {
+int64_t shares(const Shape &s);
+template <typename T>
+cudaError_t fold(const BwdArgs<T> &a, cudaStream_t st);
+}
 
 }  // namespace delta
 }  // namespace ssm
