@@ -334,6 +334,12 @@ __global__ void __launch_bounds__(256, VP == 64 ? 2 : 1) block_kernel(const BwdA
     }
     cp_async_commit();
     if (warp == 0) load_decays(d, p.g + row * s.H + head, p.beta + row * s.H + head, s.H, rows);
+    // dbeta: the shares of the chain's warps
+    float share = 0.0f;
+    if (tid >= 64 && tid < 128) {
+        const int64_t slots = s.offsets ? s.L / kBlock + s.n : (s.L + kBlock - 1) / kBlock * s.n;
+        for (int i = 0; i < parts; ++i) share += p.dbeta_part[((i * slots + slot) * s.H + head) * kBlock + tid - 64];
+    }
     cp_async_wait<1>();
     __syncthreads();
     // pairs: scale beta_s dY_t.x_s D with q_t.k_s, or -beta_s dV_t.x_s D with k_t.k_s
@@ -547,30 +553,38 @@ __global__ void __launch_bounds__(256, VP == 64 ? 2 : 1) block_kernel(const BwdA
         col_term[h][t0] = ct0, col_term[h][t1] = ct1;
     }
     __syncthreads();
-    if (tid < rows) {
-        float sum = 0.0f;
+    // one warp, steps 2 lane and 2 lane + 1: sums over the steps behind and before each
+    if (warp == 0) {
+        float both = both_term[lane % 8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += both_term[i];
-        sum = kept(d.start(kBlock - 1), sum);
-        float pairs = 0.0f;
-#pragma unroll 4
-        for (int r = 0; r < kBlock; ++r) {
-            if (r < tid) {
-                float down = 0.0f;
+        for (int o = 4; o > 0; o /= 2) both += __shfl_xor_sync(0xffffffffu, both, o);
+        both = kept(d.start(kBlock - 1), both);
+        float behind[2], before[2];         // this step's terms
 #pragma unroll
-                for (int i = 0; i < 8; ++i) down += col_sum[i][r];
-                pairs += down - (row_sum[0][r] + row_sum[1][r]);
-                sum += col_term[0][r] + col_term[1][r];
-            } else if (r < rows) {
-                sum += row_term[0][r] + row_term[1][r];
-            }
+        for (int e = 0; e < 2; ++e) {
+            const int t = 2 * lane + e;
+            float down = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) down += col_sum[i][t];
+            behind[e] = row_term[0][t] + row_term[1][t];
+            before[e] = (col_term[0][t] + col_term[1][t]) + (down - (row_sum[0][t] + row_sum[1][t]));
         }
-        put(p.dg + (row + tid) * s.H + head, sum + pairs);
-        const int64_t slots = s.offsets ? s.L / kBlock + s.n : (s.L + kBlock - 1) / kBlock * s.n;
-        float b = 0.0f;
-        for (int i = 0; i < parts; ++i) b += p.dbeta_part[((i * slots + slot) * s.H + head) * kBlock + tid];
-        put(p.dbeta + (row + tid) * s.H + head, b);
+        float up = behind[0] + behind[1], down = before[0] + before[1];
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const float x = __shfl_down_sync(0xffffffffu, up, o), y = __shfl_up_sync(0xffffffffu, down, o);
+            if (lane + o < 32) up += x;
+            if (lane >= o) down += y;
+        }
+        float first = __shfl_up_sync(0xffffffffu, down, 1), last = __shfl_down_sync(0xffffffffu, up, 1);
+        if (lane == 0) first = 0.0f;
+        if (lane == 31) last = 0.0f;
+        const float at[2] = {up + first, behind[1] + last + first + before[0]};
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (2 * lane + e < rows) put(p.dg + (row + 2 * lane + e) * s.H + head, both + at[e]);
     }
+    if (tid >= 64 && tid - 64 < rows) put(p.dbeta + (row + tid - 64) * s.H + head, share);
 }
 
 static bool on16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }

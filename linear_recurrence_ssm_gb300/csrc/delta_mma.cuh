@@ -191,11 +191,12 @@ struct alignas(16) Factors {
 };
 
 // ---- pairs of steps ------------------------------------------------------------
-constexpr int kPairThreads = 256;
+constexpr int kPairThreads = 128;
 constexpr int kPairStride = kBlock + 4;     // floats
 
 // D_ts (a_t . b_s) for rows 16 j.. of `a` and the 16-column blocks 0..j of
-// `b`: `put(t, s, x, y)` takes two neighbours with their decays.
+// `b`: `put(n, h, t, s, x, y)` takes two neighbours of block n with their decays
+// (h: which of the four of a lane).
 template <int KP, typename Put>
 __device__ __forceinline__ void pair_products(uint32_t a, uint32_t b, int j, const Decays &d, Put put) {
     uint32_t fa[KP / 16][4];
@@ -204,7 +205,9 @@ __device__ __forceinline__ void pair_products(uint32_t a, uint32_t b, int j, con
     const int lane = threadIdx.x % 32, c = lane % 4 * 2, t = 16 * j + lane / 4;
     const float hi0 = d.hi[t], lo0 = d.lo[t], hi1 = d.hi[t + 8], lo1 = d.lo[t + 8];
     const int cut0 = d.cut[t], cut1 = d.cut[t + 8];
-    for (int n = 0; n <= j; ++n) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        if (n > j) break;
         float m[2][4] = {};
 #pragma unroll
         for (int k = 0; k < KP / 16; ++k) {
@@ -219,9 +222,9 @@ __device__ __forceinline__ void pair_products(uint32_t a, uint32_t b, int j, con
             const float2 hi = *reinterpret_cast<const float2 *>(d.hi + r), lo = *reinterpret_cast<const float2 *>(d.lo + r);
             const int2 cut = *reinterpret_cast<const int2 *>(d.cut + r);
             // above the diagonal the exponent may be large; put() drops those
-            put(t, r, cut0 == cut.x ? m[h][0] * ex2((hi0 - hi.x) + (lo0 - lo.x)) : 0.0f,
+            put(n, 2 * h, t, r, cut0 == cut.x ? m[h][0] * ex2((hi0 - hi.x) + (lo0 - lo.x)) : 0.0f,
                 cut0 == cut.y ? m[h][1] * ex2((hi0 - hi.y) + (lo0 - lo.y)) : 0.0f);
-            put(t + 8, r, cut1 == cut.x ? m[h][2] * ex2((hi1 - hi.x) + (lo1 - lo.x)) : 0.0f,
+            put(n, 2 * h + 1, t + 8, r, cut1 == cut.x ? m[h][2] * ex2((hi1 - hi.x) + (lo1 - lo.x)) : 0.0f,
                 cut1 == cut.y ? m[h][3] * ex2((hi1 - hi.y) + (lo1 - lo.y)) : 0.0f);
         }
     }
@@ -233,9 +236,9 @@ __device__ __forceinline__ void pair_products(uint32_t a, uint32_t b, int j, con
 // the diagonal blocks is overwritten.  Blocks of 16 by substitution, then
 // pairs of blocks joined:
 //   N21 = (I - N22 beta2) A21 (I - beta1 N11).
-// All in fp32: the errors of a solve feed every later step.  256 threads.
+// All in fp32: the errors of a solve feed every later step.  128 threads.
 __device__ __forceinline__ void lower_solve(float *m, const float *beta, int tid) {
-    if (tid < 128) {
+    {
         const int b = tid / 32 * 16, j = tid % 16;
         float x[16], by[16];        // the column, and beta times it
 #pragma unroll
@@ -261,13 +264,12 @@ __device__ __forceinline__ void lower_solve(float *m, const float *beta, int tid
 #pragma unroll
     for (int size = 16; size <= 32; size *= 2) {
         // four columns of a row of the lower left block; the upper right one holds A21 (I - beta1 N11)
-        const int per = size / 4, pairs = 32 / size;
-        const bool mine = tid < pairs * size * per;
-        const int p = tid / (size * per), t = tid / per % size, c = tid % per * 4;
-        const int first = p * 2 * size, second = first + size;
-        float4 o = make_float4(0, 0, 0, 0);
-        if (mine) {
-            o = *reinterpret_cast<const float4 *>(m + (second + t) * kPairStride + first + c);
+        const int per = size / 4, items = size / 16;
+#pragma unroll
+        for (int i = 0; i < items; ++i) {
+            const int at = i * 128 + tid, p = at / (size * per), t = at / per % size, c = at % per * 4;
+            const int first = p * 2 * size, second = first + size;
+            float4 o = *reinterpret_cast<const float4 *>(m + (second + t) * kPairStride + first + c);
 #pragma unroll
             for (int s = 0; s < size; s += 4) {
                 const float4 a = *reinterpret_cast<const float4 *>(m + (second + t) * kPairStride + first + s);
@@ -286,7 +288,11 @@ __device__ __forceinline__ void lower_solve(float *m, const float *beta, int tid
             *reinterpret_cast<float4 *>(m + (first + t) * kPairStride + second + c) = o;
         }
         __syncthreads();
-        if (mine) {
+#pragma unroll
+        for (int i = 0; i < items; ++i) {
+            const int at = i * 128 + tid, p = at / (size * per), t = at / per % size, c = at % per * 4;
+            const int first = p * 2 * size, second = first + size;
+            float4 o = *reinterpret_cast<const float4 *>(m + (first + t) * kPairStride + second + c);
 #pragma unroll
             for (int s = 0; s < size; s += 4) {
                 const float4 a = *reinterpret_cast<const float4 *>(m + (second + t) * kPairStride + second + s);

@@ -12,18 +12,20 @@ namespace ssm {
 namespace delta {
 namespace mma {
 
+// K, Q and the system; the record is put together where K and Q were.
 template <int KP>
 struct PairLayout {
     static constexpr int tile = kBlock * KP * 2;
-    static constexpr int system = 2 * tile, out = system + kBlock * kPairStride * 4;
-    static constexpr int bytes = out + kBothRecord;
+    static constexpr int system = 2 * tile > kBothRecord ? 2 * tile : (kBothRecord + 15) / 16 * 16;
+    static constexpr int bytes = system + kBlock * kPairStride * 4;
 };
 
 template <int KP>
-__global__ void __launch_bounds__(kPairThreads, 2)
+__global__ void __launch_bounds__(kPairThreads, 4)
 pairs_kernel(const Shape s, const bf *q, const bf *k, const bf *g, const bf *beta, unsigned char *records, const bool both) {
     extern __shared__ __align__(128) unsigned char mem[];
     __shared__ Decays d;
+    __shared__ Factors f;
     __shared__ int found;
     using L = PairLayout<KP>;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -39,8 +41,7 @@ pairs_kernel(const Shape s, const bf *q, const bf *k, const bf *g, const bf *bet
     copy_tile<KP, kPairThreads>(base + L::tile, q + row * step + int64_t(group) * s.K, step, rows, s.K, tid);
     cp_async_commit();
     float *system = reinterpret_cast<float *>(mem + L::system);
-    Factors &f = *reinterpret_cast<Factors *>(mem + L::out + 3 * kTile);
-    if (warp == 7) {
+    if (warp == 0) {
         load_decays(d, g + row * s.H + head, beta + row * s.H + head, s.H, rows);
         __syncwarp();
 #pragma unroll
@@ -56,28 +57,33 @@ pairs_kernel(const Shape s, const bf *q, const bf *k, const bf *g, const bf *bet
     }
     cp_async_wait<0>();
     __syncthreads();
-    // rows 16 j of K K^T and of Q K^T have j + 1 blocks of 16 x 16: twenty in all, two or three a warp
-    {
-        const int j = warp < 4 ? 3 - warp / 2 : warp < 6 ? 1 : 0;
-        const int first = warp < 6 ? warp % 2 : warp - 6;
-        const uint32_t from = base + first * L::tile;
-        const uint32_t pairs = base + L::out + 2 * kTile;
-        pair_products<KP>(from, base, j, d, [&](int t, int r, float x, float y) {
-            if (first == 0)
-                *reinterpret_cast<float2 *>(system + t * kPairStride + r) = make_float2(r < t ? x : 0.0f, r + 1 < t ? y : 0.0f);
-            else {
-                uint32_t hi, lo;
-                split(r <= t ? s.scale * x : 0.0f, r + 1 <= t ? s.scale * y : 0.0f, hi, lo);
-                const uint32_t at = place<64>(pairs, t, r & ~7) + (r & 7) * 2;
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(hi) : "memory");
-                if (both) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + (kRecord - 2 * kTile)), "r"(lo) : "memory");
-            }
-        });
-    }
+    // rows 16 j of K K^T and 16 (3 - j) of Q K^T have five blocks of 16 x 16 together
+    pair_products<KP>(base, base, warp, d, [&](int, int, int t, int r, float x, float y) {
+        *reinterpret_cast<float2 *>(system + t * kPairStride + r) = make_float2(r < t ? x : 0.0f, r + 1 < t ? y : 0.0f);
+    });
+    uint32_t hi[4][4], lo[4][4];
+    pair_products<KP>(base + L::tile, base, 3 - warp, d, [&](int n, int h, int t, int r, float x, float y) {
+        split(r <= t ? s.scale * x : 0.0f, r + 1 <= t ? s.scale * y : 0.0f, hi[n][h], lo[n][h]);
+    });
     __syncthreads();
+    {
+        const int t = 16 * (3 - warp) + lane / 4, c2 = lane % 4 * 2;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            if (n > 3 - warp) break;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                unsigned char *at = mem + place<64>(0, t + h % 2 * 8, 16 * n + h / 2 * 8) + c2 * 2;
+                *reinterpret_cast<uint32_t *>(at + 2 * kTile) = hi[n][h];
+                if (both) *reinterpret_cast<uint32_t *>(at + kRecord) = lo[n][h];
+            }
+        }
+        for (int i = tid; i < int(sizeof(Factors)) / 16; i += kPairThreads)
+            reinterpret_cast<uint4 *>(mem + 3 * kTile)[i] = reinterpret_cast<const uint4 *>(&f)[i];
+    }
     lower_solve(system, d.beta, tid);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
         const int at = i * kPairThreads + tid, t = at / 8, r = at % 8 * 8;
         uint32_t h[4], l[4];
 #pragma unroll
@@ -86,14 +92,14 @@ pairs_kernel(const Shape s, const bf *q, const bf *k, const bf *g, const bf *bet
             const float b = r + 2 * e + 1 < t ? -system[t * kPairStride + r + 2 * e + 1] : 0.0f;
             split(a, b, h[e], l[e]);
         }
-        unsigned char *out = mem + L::out + place<64>(0, t, r);
+        unsigned char *out = mem + place<64>(0, t, r);
         *reinterpret_cast<uint4 *>(out) = make_uint4(h[0], h[1], h[2], h[3]);
         *reinterpret_cast<uint4 *>(out + kTile) = make_uint4(l[0], l[1], l[2], l[3]);
     }
     __syncthreads();
     const int size = both ? kBothRecord : kRecord;
     uint4 *to = reinterpret_cast<uint4 *>(records + (slot * s.H + head) * size);
-    const uint4 *from = reinterpret_cast<const uint4 *>(mem + L::out);
+    const uint4 *from = reinterpret_cast<const uint4 *>(mem);
     for (int i = tid; i < size / 16; i += kPairThreads) to[i] = from[i];
 }
 
