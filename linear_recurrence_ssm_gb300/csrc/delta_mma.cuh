@@ -230,16 +230,74 @@ __device__ __forceinline__ void pair_products(uint32_t a, uint32_t b, int j, con
     }
 }
 
+// c += a b for 16 x 16 floats of rows `stride` apart each, b's two blocks of
+// eight columns: in bf16 matrix products of two terms (lo lo left out), 16
+// bits of either side; from b's column `from` on.  a's column s is scaled by -by_s; LOWER: only what lies
+// below a's (A) or b's (B) diagonal counts.
+template <bool LOWER_A, bool LOWER_B, int N>
+__device__ __forceinline__ void join(float (&c)[N][4], const float *a, const float *by, const float *b, int from = 0) {
+    const int lane = threadIdx.x % 32, g = lane / 4, c2 = lane % 4 * 2;
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float2 f = *reinterpret_cast<const float2 *>(by + 8 * h + c2);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = g + 8 * e, s = 8 * h + c2;
+            float2 v = *reinterpret_cast<const float2 *>(a + t * kPairStride + s);
+            if (LOWER_A) v.x = s < t ? v.x : 0.0f, v.y = s + 1 < t ? v.y : 0.0f;
+            split(-f.x * v.x, -f.y * v.y, hi[2 * h + e], lo[2 * h + e]);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        uint32_t bh[2], bl[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int s = 8 * h + c2, r = from + 8 * n + g;
+            float x = b[s * kPairStride + r], y = b[(s + 1) * kPairStride + r];
+            if (LOWER_B) x = r < s ? x : 0.0f, y = r < s + 1 ? y : 0.0f;
+            split(x, y, bh[h], bl[h]);
+        }
+        product(c[n], hi, bh[0], bh[1]);
+        product(c[n], lo, bh[0], bh[1]);
+        product(c[n], hi, bl[0], bl[1]);
+    }
+}
+template <int N>
+__device__ __forceinline__ void get_block(float (&c)[N][4], const float *from) {
+    const int lane = threadIdx.x % 32, g = lane / 4, c2 = lane % 4 * 2;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float2 v = *reinterpret_cast<const float2 *>(from + (g + 8 * e) * kPairStride + 8 * n + c2);
+            c[n][2 * e] = v.x, c[n][2 * e + 1] = v.y;
+        }
+}
+template <int N>
+__device__ __forceinline__ void put_block(const float (&c)[N][4], float *to) {
+    const int lane = threadIdx.x % 32, g = lane / 4, c2 = lane % 4 * 2;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<float2 *>(to + (g + 8 * e) * kPairStride + 8 * n + c2) = make_float2(c[n][2 * e], c[n][2 * e + 1]);
+}
+
 // N with (I + A beta) N = A for A strictly lower triangular (64 x 64 floats in
 // `m`, zeros on and above the diagonal of its 16 x 16 blocks on the diagonal),
 // so that (I + A beta)^-1 = I - N beta.  N takes A's place; what lies above
-// the diagonal blocks is overwritten.  Blocks of 16 by substitution, then
-// pairs of blocks joined:
-//   N21 = (I - N22 beta2) A21 (I - beta1 N11).
-// All in fp32: the errors of a solve feed every later step.  128 threads.
+// the diagonal blocks is overwritten.  Blocks of 16 by substitution in fp32,
+// then pairs of blocks joined,
+//   N21 = (I - N22 beta2) A21 (I - beta1 N11),
+// in matrix products on 16 bits of either side, which is what the chains take
+// of N; multiply-adds there were bound by their shared-memory operands.  128
+// threads.
 __device__ __forceinline__ void lower_solve(float *m, const float *beta, int tid) {
+    const int warp = tid / 32;
     {
-        const int b = tid / 32 * 16, j = tid % 16;
+        const int b = warp * 16, j = tid % 16;
         float x[16], by[16];        // the column, and beta times it
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -261,54 +319,39 @@ __device__ __forceinline__ void lower_solve(float *m, const float *beta, int tid
             for (int i = 0; i < 16; ++i) m[(b + i) * kPairStride + b + j] = x[i];
     }
     __syncthreads();
-#pragma unroll
-    for (int size = 16; size <= 32; size *= 2) {
-        // four columns of a row of the lower left block; the upper right one holds A21 (I - beta1 N11)
-        const int per = size / 4, items = size / 16;
-#pragma unroll
-        for (int i = 0; i < items; ++i) {
-            const int at = i * 128 + tid, p = at / (size * per), t = at / per % size, c = at % per * 4;
-            const int first = p * 2 * size, second = first + size;
-            float4 o = *reinterpret_cast<const float4 *>(m + (second + t) * kPairStride + first + c);
-#pragma unroll
-            for (int s = 0; s < size; s += 4) {
-                const float4 a = *reinterpret_cast<const float4 *>(m + (second + t) * kPairStride + first + s);
-                const float4 w = *reinterpret_cast<const float4 *>(beta + first + s);
-                const float av[4] = {a.x * w.x, a.y * w.y, a.z * w.z, a.w * w.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float4 n = *reinterpret_cast<const float4 *>(m + (first + s + e) * kPairStride + first + c);
-                    // N11 is strictly lower, but its upper part may hold a smaller pair's left-overs
-                    o.x -= s + e > c ? av[e] * n.x : 0.0f;
-                    o.y -= s + e > c + 1 ? av[e] * n.y : 0.0f;
-                    o.z -= s + e > c + 2 ? av[e] * n.z : 0.0f;
-                    o.w -= s + e > c + 3 ? av[e] * n.w : 0.0f;
-                }
-            }
-            *reinterpret_cast<float4 *>(m + (first + t) * kPairStride + second + c) = o;
-        }
+    {
+        // two pairs of 16: a warp has eight columns of one
+        const int first = warp / 2 * 32, second = first + 16, c = warp % 2 * 8;
+        float *lower = m + second * kPairStride + first, *upper = m + first * kPairStride + second;
+        float o[1][4];
+        get_block(o, lower + c);
+        join<false, true, 1>(o, lower, beta + first, m + first * kPairStride + first, c);
+        put_block(o, upper + c);
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < items; ++i) {
-            const int at = i * 128 + tid, p = at / (size * per), t = at / per % size, c = at % per * 4;
-            const int first = p * 2 * size, second = first + size;
-            float4 o = *reinterpret_cast<const float4 *>(m + (first + t) * kPairStride + second + c);
-#pragma unroll
-            for (int s = 0; s < size; s += 4) {
-                const float4 a = *reinterpret_cast<const float4 *>(m + (second + t) * kPairStride + second + s);
-                const float4 w = *reinterpret_cast<const float4 *>(beta + second + s);
-                const float av[4] = {s < t ? a.x * w.x : 0.0f, s + 1 < t ? a.y * w.y : 0.0f,
-                                     s + 2 < t ? a.z * w.z : 0.0f, s + 3 < t ? a.w * w.w : 0.0f};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float4 n = *reinterpret_cast<const float4 *>(m + (first + s + e) * kPairStride + second + c);
-                    o.x -= av[e] * n.x, o.y -= av[e] * n.y, o.z -= av[e] * n.z, o.w -= av[e] * n.w;
-                }
-            }
-            *reinterpret_cast<float4 *>(m + (second + t) * kPairStride + first + c) = o;
-        }
-        __syncthreads();
+        join<true, false, 1>(o, m + second * kPairStride + second, beta + second, upper + c);
+        put_block(o, lower + c);
     }
+    __syncthreads();
+    {
+        // one pair of 32: a warp has 16 x 16 of it
+        const int t = warp / 2 * 16, c = warp % 2 * 16;
+        float *lower = m + 32 * kPairStride, *upper = m + 32;
+        float o[2][4];
+        get_block(o, lower + t * kPairStride + c);
+        if (c == 0) join<false, true, 2>(o, lower + t * kPairStride, beta, m);
+        else join<false, true, 2>(o, lower + t * kPairStride + 16, beta + 16, m + 16 * kPairStride + 16);
+        if (c == 0) join<false, false, 2>(o, lower + t * kPairStride + 16, beta + 16, m + 16 * kPairStride);
+        put_block(o, upper + t * kPairStride + c);
+        __syncthreads();
+        const float *n22 = m + (32 + t) * kPairStride + 32;
+        if (t == 0) join<true, false, 2>(o, n22, beta + 32, upper + c);
+        else {
+            join<false, false, 2>(o, n22, beta + 32, upper + c);
+            join<true, false, 2>(o, n22 + 16, beta + 48, upper + 16 * kPairStride + c);
+        }
+        put_block(o, lower + t * kPairStride + c);
+    }
+    __syncthreads();
 }
 
 // What the chains need of a block besides its tokens, made once by
