@@ -116,7 +116,7 @@ cudaError_t bwd(const BwdArgs<T> &a, cudaStream_t st);
 namespace mma {
 namespace fwd {
 bool fits(const FwdArgs<__nv_bfloat16> &a);
-cudaError_t launch(const FwdArgs<__nv_bfloat16> &a, cudaStream_t st);
+cudaError_t launch(FwdArgs<__nv_bfloat16> a, cudaStream_t st);
 }
 namespace bwd {
 bool fits(const BwdArgs<__nv_bfloat16> &a);
@@ -506,7 +506,7 @@ ssm_status_t delta_fwd_entry(const void *q, const void *k, const void *v, const 
                                    static_cast<const T *>(v), static_cast<const T *>(g),
                                    static_cast<const T *>(beta), h0, static_cast<T *>(y), h_final,
                                    static_cast<T *>(states), static_cast<T *>(errors),
-                                   static_cast<unsigned char *>(scratch)};
+                                   static_cast<unsigned char *>(scratch), 0, nullptr, nullptr, nullptr};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if constexpr (sizeof(T) == 2)
         if (ssm::delta::mma::fwd::fits(a)) return from_cuda(ssm::delta::mma::fwd::launch(a, st));
@@ -980,7 +980,7 @@ int64_t delta_rule_fwd_scratch(int64_t Bs, int64_t L, int64_t G, int64_t H, int6
     if (check_delta_sizes(Bs, L, G, H, K, V, n_seq, 1.0f) != SSM_OK) return 0;
     static const int32_t some = 0;      // only that there are offsets counts
     const ssm::delta::Shape s = delta_shape(n_seq > 0 ? &some : nullptr, Bs, L, G, H, K, V, n_seq, 1.0f);
-    return input_bf16 && ssm::delta::mma::fits(s) ? ssm::delta::mma::record_bytes(s) : 16;
+    return input_bf16 && ssm::delta::mma::fits(s) ? ssm::delta::mma::fwd_scratch(s).bytes : 16;
 }
 
 int64_t delta_rule_bwd_scratch(int64_t Bs, int64_t L, int64_t G, int64_t H, int64_t K, int64_t V,

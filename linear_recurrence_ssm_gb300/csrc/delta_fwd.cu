@@ -24,7 +24,7 @@ namespace fwd {
 
 constexpr int kSlice = 64, kChain = 4, kThreads = 256;
 
-template <int KP>
+template <int KP, bool CARRY>
 struct Layout {
     static constexpr int tile = kBlock * KP * 2, v = kBlock * kSlice * 2;
     static constexpr int chain = tile + v + 2 * kTile;              // K, V, N in two terms: two of them
@@ -32,41 +32,71 @@ struct Layout {
     static constexpr int handed = outputs + 3 * output;
     static constexpr int state = 16 * KP * 2, u = 16 * kBlock * 2;  // of a warp
     static constexpr int hand = kChain * (state + 2 * u);           // S, U, X: two of them
-    static constexpr int bytes = handed + 2 * hand;
+    static constexpr int bytes = CARRY ? 2 * chain + 2 * 1152 : handed + 2 * hand;
     static_assert(sizeof(Factors) <= 1152 && bytes <= 232448, "shared memory");
 };
 
-template <int KP>
-__global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdArgs<bf> p) {
+// CARRY: no outputs, only what a part adds to a state and what it makes of one
+// (its rows of the identity: 64 rows of K more slices), by the four warps of
+// the chain alone.
+template <int KP, bool CARRY>
+__global__ void __launch_bounds__(CARRY ? 32 * kChain : kThreads, CARRY ? 2 : 1) fwd_kernel(const FwdArgs<bf> p) {
     extern __shared__ __align__(1024) unsigned char mem[];
-    using L = Layout<KP>;
+    __shared__ int found;
+    using L = Layout<KP, CARRY>;
+    constexpr int threads = CARRY ? 32 * kChain : kThreads;
     const Shape &s = p.s;
     const uint32_t base = smem_u32(mem);
-    const int slices = (s.V + kSlice - 1) / kSlice;
+    const int of_values = (s.V + kSlice - 1) / kSlice, slices = CARRY ? of_values + (s.K + kSlice - 1) / kSlice : of_values;
     const int slice = int(blockIdx.x % slices), head = int(blockIdx.x / slices % s.H);
-    const int seq = int(blockIdx.x / slices / s.H), group = head / (s.H / s.G), v0 = slice * kSlice;
-    const Span span = span_of(s, seq);
+    const int group = head / (s.H / s.G);
+    const bool turning = CARRY && slice >= of_values;
+    const int height = turning ? s.K : s.V, v0 = (turning ? slice - of_values : slice) * kSlice;
+    const int64_t index = blockIdx.x / slices / s.H;        // of the sequence, or of the part's place
+    int seq = int(index), part = 0;
+    if (p.part) {
+        seq = part_sequence_of(s, index, p.part, &found);
+        if (seq < 0) return;
+    }
+    Span span = span_of(s, seq);
+    bool last_part = true;
+    if (p.part) {
+        part = int(index - first_part(s, span, seq, p.part));
+        last_part = part + 1 == parts_of(span, p.part);
+        if (CARRY && (last_part || (turning && part == 0 && !p.h0))) return;
+        const int first = part * p.part;
+        span.first += int64_t(first) * kBlock;
+        span.slot += first;
+        span.len = min(span.len - first * kBlock, p.part * kBlock);
+        span.blocks = min(span.blocks - first, p.part);
+    }
+    const float *entering = part == 0 ? p.h0 : p.entering;
+    const int64_t entering_at = ((part == 0 ? int64_t(seq) : index) * s.H + head) * s.V * s.K;
     const int64_t qk_step = int64_t(s.G) * s.K, v_step = int64_t(s.H) * s.V;
     const int tid = threadIdx.x, warp = tid / 32 % kChain, lane = tid % 32;
     const bool chain = tid < 32 * kChain;
     const int g = lane / 4, c2 = lane % 4 * 2, mine = v0 + 16 * warp;       // rows mine + g, mine + g + 8 of the state
-    const int width = s.V - mine;                                           // of them, may be below 1 or above 16
-    const int64_t state_at = (int64_t(seq) * s.H + head) * s.V * s.K;
+    const int width = height - mine;                                        // of them, may be below 1 or above 16
 
     const auto copy = [&](int c) {
         const int64_t row = span.first + int64_t(c) * kBlock;
         const int rows = min(kBlock, span.len - c * kBlock);
-        const uint32_t to = base + c % 2 * L::chain, out = base + L::outputs + c % 3 * L::output;
+        const uint32_t to = base + c % 2 * L::chain;
+        const uint32_t out = base + L::outputs + (CARRY ? c % 2 * 1152 : c % 3 * L::output);
         const unsigned char *record = p.scratch + ((span.slot + c) * s.H + head) * kRecord;
-        copy_tile<KP, kThreads>(to, p.k + row * qk_step + int64_t(group) * s.K, qk_step, rows, s.K, tid);
-        copy_tile<kSlice, kThreads>(to + L::tile, p.v + row * v_step + int64_t(head) * s.V + v0, v_step, rows,
-                                    min(kSlice, s.V - v0), tid);
+        copy_tile<KP, threads>(to, p.k + row * qk_step + int64_t(group) * s.K, qk_step, rows, s.K, tid);
+        copy_tile<kSlice, threads>(to + L::tile, p.v + row * v_step + int64_t(head) * s.V + (turning ? 0 : v0), v_step,
+                                   turning ? 0 : rows, min(kSlice, s.V - v0), tid);
 #pragma unroll
-        for (int i = 0; i < 2 * kTile / 16 / kThreads; ++i)
-            copy16(to + L::tile + L::v + (i * kThreads + tid) * 16, record + (i * kThreads + tid) * 16);
-        copy_tile<KP, kThreads>(out, p.q + row * qk_step + int64_t(group) * s.K, qk_step, rows, s.K, tid);
+        for (int i = 0; i < 2 * kTile / 16 / threads; ++i)
+            copy16(to + L::tile + L::v + (i * threads + tid) * 16, record + (i * threads + tid) * 16);
+        if (CARRY) {
+            if (tid < int(sizeof(Factors)) / 16) copy16(out + tid * 16, record + 3 * kTile + tid * 16);
+            return;
+        }
+        copy_tile<KP, threads>(out, p.q + row * qk_step + int64_t(group) * s.K, qk_step, rows, s.K, tid);
         constexpr int rest = (kTile + int(sizeof(Factors))) / 16;
-        for (int i = tid; i < rest; i += kThreads) copy16(out + L::tile + i * 16, record + 2 * kTile + i * 16);
+        for (int i = tid; i < rest; i += threads) copy16(out + L::tile + i * 16, record + 2 * kTile + i * 16);
     };
     float st[KP / 8][4];
     if (chain) {
@@ -75,13 +105,14 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdArgs<bf> p) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int v = g + e / 2 * 8, k = 8 * n + c2 + e % 2;
-                st[n][e] = p.h0 && v < width && k < s.K ? p.h0[state_at + int64_t(mine + v) * s.K + k] : 0.0f;
+                if (CARRY) st[n][e] = turning && mine + v == k ? 1.0f : 0.0f;
+                else st[n][e] = entering && v < width && k < s.K ? entering[entering_at + int64_t(mine + v) * s.K + k] : 0.0f;
             }
     }
     if (span.blocks > 0) copy(0);
     cp_async_commit();
     // the chain is at block c, the outputs at the one before
-    for (int c = 0; c <= span.blocks; ++c) {
+    for (int c = 0; c < span.blocks + (CARRY ? 0 : 1); ++c) {
         cp_async_wait<0>();
         __syncthreads();
         if (c + 1 < span.blocks) copy(c + 1);
@@ -90,7 +121,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdArgs<bf> p) {
             if (c == span.blocks) break;
             const uint32_t at = base + c % 2 * L::chain, hand = base + L::handed + c % 2 * L::hand;
             const uint32_t hand_u = hand + kChain * L::state + warp * L::u, hand_x = hand_u + kChain * L::u;
-            const Factors &f = *reinterpret_cast<const Factors *>(mem + L::outputs + c % 3 * L::output + L::tile + kTile);
+            const Factors &f = *reinterpret_cast<const Factors *>(
+                mem + L::outputs + (CARRY ? c % 2 * 1152 : c % 3 * L::output + L::tile + kTile));
             // S K^T: the pieces of K for the next 16 columns are loaded ahead of the products
             float w[8][4] = {};
             {
@@ -101,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdArgs<bf> p) {
                 for (int k = 0; k < KP / 16; ++k) {
                     uint32_t hi[4], lo[4];
                     operand<KP>(hi, lo, st, k);
-                    store4(four<KP>(hand + warp * L::state, 0, 16 * k), hi);
+                    if (!CARRY) store4(four<KP>(hand + warp * L::state, 0, 16 * k), hi);
                     if (k + 1 < KP / 16)
 #pragma unroll
                         for (int t = 0; t < 4; ++t) load4(b[(k + 1) % 2][t], four_across<KP>(at, 16 * t, 16 * (k + 1)));
@@ -144,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdArgs<bf> p) {
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 uint32_t u[4];
-                if (p.errors) store_turned(hand_x, t, w);
+                if (!CARRY && p.errors) store_turned(hand_x, t, w);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float2 beta = *reinterpret_cast<const float2 *>(f.beta + 16 * t + 8 * h + c2);
@@ -156,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdArgs<bf> p) {
                     split(kept(end.x, a), kept(end.y, b), hi[t][2 * h], lo[t][2 * h]);
                     split(kept(end.x, d), kept(end.y, e), hi[t][2 * h + 1], lo[t][2 * h + 1]);
                 }
-                store4(four<64>(hand_u, 0, 16 * t), u);
+                if (!CARRY) store4(four<64>(hand_u, 0, 16 * t), u);
             }
             // S
             const float last = f.last;
@@ -165,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdArgs<bf> p) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) st[n][e] = kept(last, st[n][e]);
             add_outer<KP>(st, hi, lo, at);
-        } else if (c > 0) {
+        } else if (!CARRY && c > 0) {
             const int rows = min(kBlock, span.len - (c - 1) * kBlock);
             const int64_t row = span.first + int64_t(c - 1) * kBlock;
             const int from = L::outputs + (c - 1) % 3 * L::output;
@@ -222,24 +254,69 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdArgs<bf> p) {
             write_turned(p.y + out_at, v_step, rows, width, hand_x);
         }
     }
-    if (chain && p.h_final)
+    float *out = CARRY ? (turning ? p.turned : p.added) : last_part ? p.h_final : nullptr;
+    if (chain && out) {
+        out += ((CARRY ? index : int64_t(seq)) * s.H + head) * height * s.K;
 #pragma unroll
         for (int n = 0; n < KP / 8; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int v = g + e / 2 * 8, k = 8 * n + c2 + e % 2;
-                if (v < width && k < s.K) p.h_final[state_at + int64_t(mine + v) * s.K + k] = st[n][e];
+                if (v < width && k < s.K) out[int64_t(mine + v) * s.K + k] = st[n][e];
             }
-    clear_uncovered(s, seq, p.y + int64_t(head) * s.V + v0, v_step, min(kSlice, s.V - v0));
+    }
+    if (!CARRY && part == 0) clear_uncovered(s, seq, p.y + int64_t(head) * s.V + v0, v_step, min(kSlice, s.V - v0));
 }
 
-template <int KP>
-static cudaError_t go(const FwdArgs<bf> &a, cudaStream_t st) {
-    const int64_t grid = int64_t(a.s.n) * a.s.H * ((a.s.V + kSlice - 1) / kSlice);
+// The states that enter a sequence's parts: S_(i + 1) = S_i T_i + B_i, eight
+// rows of one head a thread block.  Rows are independent; T is read from L2.
+constexpr int kJoinRows = 8;
+__global__ void __launch_bounds__(128) join_kernel(const FwdArgs<bf> p) {
+    __shared__ float S[2][kJoinRows][128];
+    const Shape &s = p.s;
+    const int tiles = (s.V + kJoinRows - 1) / kJoinRows, k = threadIdx.x;
+    const int v0 = int(blockIdx.x % tiles) * kJoinRows, head = int(blockIdx.x / tiles % s.H), seq = int(blockIdx.x / tiles / s.H);
+    const Span span = span_of(s, seq);
+    const int parts = parts_of(span, p.part), rows = min(kJoinRows, s.V - v0);
+    const int64_t first = first_part(s, span, seq, p.part);
+    const bool in = k < s.K;
+    for (int v = 0; v < kJoinRows; ++v)
+        S[0][v][k] = p.h0 && in && v < rows ? p.h0[((int64_t(seq) * s.H + head) * s.V + v0 + v) * s.K + k] : 0.0f;
+    for (int i = 0; i + 1 < parts; ++i) {
+        const int64_t at = (first + i) * s.H + head;
+        const float *added = p.added + (at * s.V + v0) * s.K + k, *turned = p.turned + at * s.K * s.K + k;
+        float *out = p.entering + ((at + s.H) * s.V + v0) * s.K + k;
+        const float(&from)[kJoinRows][128] = S[i % 2];
+        float sum[kJoinRows];
+#pragma unroll
+        for (int v = 0; v < kJoinRows; ++v) sum[v] = in && v < rows ? added[v * s.K] : 0.0f;
+        __syncthreads();
+        // the first part starts from h0: nothing was made of it, unless there is one
+        if (in && (i > 0 || p.h0)) {
+#pragma unroll 8
+            for (int m = 0; m < s.K; ++m) {
+                const float t = turned[int64_t(m) * s.K];
+#pragma unroll
+                for (int v = 0; v < kJoinRows; ++v) sum[v] += from[v][m] * t;
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < kJoinRows; ++v) {
+            S[(i + 1) % 2][v][k] = sum[v];
+            if (in && v < rows) out[v * s.K] = sum[v];
+        }
+    }
+}
+
+template <int KP, bool CARRY>
+static cudaError_t go(const FwdArgs<bf> &a, int64_t places, cudaStream_t st) {
+    const int64_t slices = (a.s.V + kSlice - 1) / kSlice + (CARRY ? (a.s.K + kSlice - 1) / kSlice : 0);
+    const int64_t grid = places * a.s.H * slices;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    constexpr int bytes = Layout<KP>::bytes;
-    if (cudaError_t e = cudaFuncSetAttribute(fwd_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
-    fwd_kernel<KP><<<unsigned(grid), kThreads, bytes, st>>>(a);
+    constexpr int bytes = Layout<KP, CARRY>::bytes;
+    if (cudaError_t e = cudaFuncSetAttribute(fwd_kernel<KP, CARRY>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes))
+        return e;
+    fwd_kernel<KP, CARRY><<<unsigned(grid), CARRY ? 32 * kChain : kThreads, bytes, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -250,9 +327,20 @@ bool fits(const FwdArgs<bf> &a) {
     return mma::fits(a.s) && on16(a.q) && on16(a.k) && on16(a.v) && on16(a.y) && on16(a.states) && on16(a.errors);
 }
 
-cudaError_t launch(const FwdArgs<bf> &a, cudaStream_t st) {
+cudaError_t launch(FwdArgs<bf> a, cudaStream_t st) {
     if (cudaError_t e = make_pairs(a.s, a.q, a.k, a.g, a.beta, a.scratch, false, st)) return e;
-    return a.s.K <= 64 ? go<64>(a, st) : go<128>(a, st);
+    const FwdScratch at = fwd_scratch(a.s);
+    const bool wide = a.s.K > 64;
+    a.part = at.part;
+    if (!a.part) return wide ? go<128, false>(a, a.s.n, st) : go<64, false>(a, a.s.n, st);
+    a.added = reinterpret_cast<float *>(a.scratch + at.added);
+    a.turned = reinterpret_cast<float *>(a.scratch + at.turned);
+    a.entering = reinterpret_cast<float *>(a.scratch + at.entering);
+    const int64_t places = part_places(a.s, a.part);
+    if (cudaError_t e = wide ? go<128, true>(a, places, st) : go<64, true>(a, places, st)) return e;
+    join_kernel<<<unsigned((a.s.V + kJoinRows - 1) / kJoinRows * a.s.H * a.s.n), 128, 0, st>>>(a);
+    if (cudaError_t e = cudaGetLastError()) return e;
+    return wide ? go<128, false>(a, places, st) : go<64, false>(a, places, st);
 }
 
 }  // namespace fwd

@@ -57,6 +57,16 @@ __device__ __forceinline__ Span span_of(const Shape &s, int i) {
     return {b, int64_t(b / kBlock) + i, e - b, (e - b + kBlock - 1) / kBlock};
 }
 
+// A long sequence of few heads is taken in parts of `blocks` blocks of 64
+// steps: parts have places as blocks have, and an empty sequence has one part.
+__device__ __forceinline__ int64_t first_part(const Shape &s, const Span &span, int i, int blocks) {
+    if (s.offsets) return span.first / (int64_t(kBlock) * blocks) + i;
+    return int64_t(i) * ((span.blocks + blocks - 1) / blocks);
+}
+__device__ __forceinline__ int parts_of(const Span &span, int blocks) {
+    return max(1, (span.blocks + blocks - 1) / blocks);
+}
+
 // The sequence whose block has place `slot`, or -1.  All threads of the thread
 // block; `found` is in shared memory.
 __device__ __forceinline__ int sequence_of(const Shape &s, int64_t slot, int *found) {
@@ -66,6 +76,23 @@ __device__ __forceinline__ int sequence_of(const Shape &s, int64_t slot, int *fo
     for (int i = threadIdx.x; i < s.n; i += blockDim.x) {
         const Span span = span_of(s, i);
         if (slot >= span.slot && slot < span.slot + span.blocks) atomicMax(found, i);
+    }
+    __syncthreads();
+    return *found;
+}
+
+// The same for a part's place.
+__device__ __forceinline__ int part_sequence_of(const Shape &s, int64_t place, int blocks, int *found) {
+    if (!s.offsets) {
+        const int whole = int((s.L + kBlock - 1) / kBlock);
+        return int(place / ((whole + blocks - 1) / blocks));
+    }
+    if (threadIdx.x == 0) *found = -1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < s.n; i += blockDim.x) {
+        const Span span = span_of(s, i);
+        const int64_t first = first_part(s, span, i, blocks);
+        if (place >= first && place < first + parts_of(span, blocks)) atomicMax(found, i);
     }
     __syncthreads();
     return *found;
@@ -196,7 +223,12 @@ struct FwdArgs {
     T *y;
     float *h_final;
     T *states, *errors;     // kept for the gradients, or null
-    unsigned char *scratch;
+    unsigned char *scratch; // the records of all blocks
+    // sequences in parts of `part` blocks (0: whole): what each part adds to a
+    // state, (places, H, V, K), what it makes of one, (places, H, K, K), and
+    // the states that enter the parts, (places, H, V, K)
+    int part;
+    float *added, *turned, *entering;
 };
 template <typename T>
 struct BwdArgs {

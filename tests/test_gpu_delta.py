@@ -102,6 +102,15 @@ def test_packed(cuda_device, dtype, K, V, offsets):
     check(i, rest, cuda_device, offsets)
 
 
+@pytest.mark.parametrize("K,V", [(128, 64), (64, 128), (40, 24)])
+@pytest.mark.parametrize("Bs,L,offsets,h0", [(1, 2100, None, True), (2, 1537, None, False), (1, 3000, [0, 0, 2000, 2001, 2900], True),
+                                             (1, 2500, [100, 612, 612, 2500], False)])
+def test_long_sequences_of_few_heads(cuda_device, K, V, Bs, L, offsets, h0):
+    """Taken in parts that are joined afterwards."""
+    i, rest = inputs(16, Bs, L, 1, 2, K, V, BF, n=None if offsets is None else len(offsets) - 1, decay=0.02)
+    check(i, rest, cuda_device, offsets, h0=h0)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("h0,dend", [(False, False), (True, False), (False, True)])
 def test_optional_states(cuda_device, dtype, h0, dend):
