@@ -268,45 +268,53 @@ __global__ void __launch_bounds__(CARRY ? 32 * kChain : kThreads, CARRY ? 2 : 1)
     if (!CARRY && part == 0) clear_uncovered(s, seq, p.y + int64_t(head) * s.V + v0, v_step, min(kSlice, s.V - v0));
 }
 
-// The states that enter a sequence's parts: S_(i + 1) = S_i T_i + B_i, eight
-// rows of one head a thread block.  Rows are independent; T is read from L2.
-constexpr int kJoinRows = 8;
-__global__ void __launch_bounds__(128) join_kernel(const FwdArgs<bf> p) {
-    __shared__ float S[2][kJoinRows][128];
+// The states that enter a sequence's parts: S_(i + 1) = S_i T_i + B_i, four
+// rows of one head a thread block.  Rows are independent; T is read from L2, a
+// quarter of its rows by each quarter of the threads.
+constexpr int kJoinRows = 4, kJoinSplit = 4;
+__global__ void __launch_bounds__(128 * kJoinSplit) join_kernel(const FwdArgs<bf> p) {
+    __shared__ float S[kJoinRows][128], shares[kJoinSplit][kJoinRows][128];
     const Shape &s = p.s;
-    const int tiles = (s.V + kJoinRows - 1) / kJoinRows, k = threadIdx.x;
+    const int tiles = (s.V + kJoinRows - 1) / kJoinRows, k = threadIdx.x % 128, quarter = threadIdx.x / 128;
     const int v0 = int(blockIdx.x % tiles) * kJoinRows, head = int(blockIdx.x / tiles % s.H), seq = int(blockIdx.x / tiles / s.H);
     const Span span = span_of(s, seq);
     const int parts = parts_of(span, p.part), rows = min(kJoinRows, s.V - v0);
     const int64_t first = first_part(s, span, seq, p.part);
     const bool in = k < s.K;
-    for (int v = 0; v < kJoinRows; ++v)
-        S[0][v][k] = p.h0 && in && v < rows ? p.h0[((int64_t(seq) * s.H + head) * s.V + v0 + v) * s.K + k] : 0.0f;
+    // this thread's row, column of the result
+    const int mine = quarter;
+    const bool has = in && mine < rows;
+    S[mine][k] = p.h0 && has ? p.h0[((int64_t(seq) * s.H + head) * s.V + v0 + mine) * s.K + k] : 0.0f;
     for (int i = 0; i + 1 < parts; ++i) {
         const int64_t at = (first + i) * s.H + head;
-        const float *added = p.added + (at * s.V + v0) * s.K + k, *turned = p.turned + at * s.K * s.K + k;
-        float *out = p.entering + ((at + s.H) * s.V + v0) * s.K + k;
-        const float(&from)[kJoinRows][128] = S[i % 2];
-        float sum[kJoinRows];
-#pragma unroll
-        for (int v = 0; v < kJoinRows; ++v) sum[v] = in && v < rows ? added[v * s.K] : 0.0f;
+        const float added = has ? p.added[(at * s.V + v0 + mine) * s.K + k] : 0.0f;
+        const float *turned = p.turned + at * s.K * s.K + k;
+        float sum[kJoinRows] = {};
         __syncthreads();
         // the first part starts from h0: nothing was made of it, unless there is one
         if (in && (i > 0 || p.h0)) {
-#pragma unroll 8
-            for (int m = 0; m < s.K; ++m) {
-                const float t = turned[int64_t(m) * s.K];
+            const int each = (s.K + kJoinSplit - 1) / kJoinSplit, to = min((quarter + 1) * each, s.K);
+            for (int m = quarter * each; m < to; m += 16) {
+                float t[16];
 #pragma unroll
-                for (int v = 0; v < kJoinRows; ++v) sum[v] += from[v][m] * t;
+                for (int j = 0; j < 16; ++j) t[j] = m + j < to ? turned[int64_t(m + j) * s.K] : 0.0f;
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+#pragma unroll
+                    for (int v = 0; v < kJoinRows; ++v) sum[v] += S[v][min(m + j, 127)] * t[j];
             }
         }
 #pragma unroll
-        for (int v = 0; v < kJoinRows; ++v) {
-            S[(i + 1) % 2][v][k] = sum[v];
-            if (in && v < rows) out[v * s.K] = sum[v];
-        }
+        for (int v = 0; v < kJoinRows; ++v) shares[quarter][v][k] = sum[v];
+        __syncthreads();
+        float all = added;
+#pragma unroll
+        for (int j = 0; j < kJoinSplit; ++j) all += shares[j][mine][k];
+        S[mine][k] = all;
+        if (has) p.entering[((at + s.H) * s.V + v0 + mine) * s.K + k] = all;
     }
 }
+static_assert(kJoinRows == kJoinSplit, "a row a quarter");
 
 template <int KP, bool CARRY>
 static cudaError_t go(const FwdArgs<bf> &a, int64_t places, cudaStream_t st) {
@@ -338,7 +346,7 @@ cudaError_t launch(FwdArgs<bf> a, cudaStream_t st) {
     a.entering = reinterpret_cast<float *>(a.scratch + at.entering);
     const int64_t places = part_places(a.s, a.part);
     if (cudaError_t e = wide ? go<128, true>(a, places, st) : go<64, true>(a, places, st)) return e;
-    join_kernel<<<unsigned((a.s.V + kJoinRows - 1) / kJoinRows * a.s.H * a.s.n), 128, 0, st>>>(a);
+    join_kernel<<<unsigned((a.s.V + kJoinRows - 1) / kJoinRows * a.s.H * a.s.n), 128 * kJoinSplit, 0, st>>>(a);
     if (cudaError_t e = cudaGetLastError()) return e;
     return wide ? go<128, false>(a, places, st) : go<64, false>(a, places, st);
 }

@@ -5,8 +5,9 @@
 //   dx = ds + r (w dy - s r^2 mean(w dy s)),  dw = sum over rows of dy s r
 //
 // Memory bound: every element is read once and kept in registers between the
-// row's sum and its outputs.  A row takes the lanes that its vectors of eight
-// need at two to four vectors a lane; short rows share a block.
+// row's sum and its outputs.  A row of up to 256 columns takes 8, 16 or 32
+// lanes, a longer one a thread block of as many warps as its vectors of eight
+// need at one to four a thread.
 #include <type_traits>
 
 #include "gated_scan.cuh"
@@ -19,7 +20,7 @@ using gated::quantised;
 using gated::scale_of;
 
 constexpr int kVec = 8;                 // elements of an access
-constexpr int kParts = 608;             // most partial sums of dw
+constexpr int kParts = 608;             // most partial sums of dw: four thread blocks a SM
 
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16(v); }
@@ -49,23 +50,27 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[kVec])
     *reinterpret_cast<uint4 *>(p) = w;
 }
 
-// The sum over the LANES threads that share a row (a block holds 1 or more
-// such groups); every thread of the group gets it.  `mem`: a float a warp.
-template <int LANES>
-__device__ __forceinline__ float row_sum(float v, float *mem) {
+// The sums over the threads that share a row: LANES of a warp, or the whole
+// block (LANES = 0).  `mem`: a float a warp and row; the next call of the same
+// block needs other ones.
+template <int LANES, int ROWS>
+__device__ __forceinline__ void row_sums(float (&v)[ROWS], float (*mem)[ROWS]) {
 #pragma unroll
-    for (int o = (LANES < 32 ? LANES : 32) / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (LANES > 32) {
-        constexpr int warps = LANES > 32 ? LANES / 32 : 1;
-        const int warp = threadIdx.x / 32, first = warp / warps * warps;
-        __syncthreads();
-        if (threadIdx.x % 32 == 0) mem[warp] = v;
-        __syncthreads();
-        v = 0.0f;
+    for (int o = (LANES == 0 ? 32 : LANES) / 2; o > 0; o /= 2)
 #pragma unroll
-        for (int i = 0; i < warps; ++i) v += mem[first + i];
+        for (int r = 0; r < ROWS; ++r) v[r] += __shfl_xor_sync(0xffffffffu, v[r], o);
+    if (LANES == 0) {
+        const int warp = threadIdx.x / 32;
+        if (threadIdx.x % 32 == 0)
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) mem[warp][r] = v[r];
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) v[r] = 0.0f;
+        for (int i = 0; i < int(blockDim.x / 32); ++i)
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) v[r] += mem[i][r];
     }
-    return v;
 }
 
 template <typename T>
@@ -79,20 +84,17 @@ struct FwdArgs {
     float eps;
 };
 
-constexpr int threads_for(int lanes) { return lanes > 256 ? lanes : 256; }
-
 template <typename T, int LANES, int VECS>
-__global__ void __launch_bounds__(threads_for(LANES)) fwd_kernel(const FwdArgs<T> p) {
-    __shared__ float mem[32];
-    constexpr int per_block = threads_for(LANES) / LANES;
-    const int lane = threadIdx.x % LANES;
-    const int64_t row = int64_t(blockIdx.x) * per_block + threadIdx.x / LANES;
+__global__ void __launch_bounds__(LANES ? 256 : 1024) fwd_kernel(const FwdArgs<T> p) {
+    __shared__ float mem[32][1];
+    const int lanes = LANES ? LANES : int(blockDim.x), lane = threadIdx.x % lanes;
+    const int64_t row = int64_t(blockIdx.x) * (blockDim.x / lanes) + threadIdx.x / lanes;
     const bool there = row < p.rows;
     const int64_t at = row * p.cols;
-    float v[VECS][kVec], squares = 0.0f;
+    float v[VECS][kVec], squares[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
-        const int c = (i * LANES + lane) * kVec;
+        const int c = (i * lanes + lane) * kVec;
         if (there && c < p.cols) {
             load8(v[i], p.x + at + c);
             if (p.residual) {
@@ -107,13 +109,14 @@ __global__ void __launch_bounds__(threads_for(LANES)) fwd_kernel(const FwdArgs<T
             for (int e = 0; e < kVec; ++e) v[i][e] = 0.0f;
         }
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) squares += v[i][e] * v[i][e];
+        for (int e = 0; e < kVec; ++e) squares[0] += v[i][e] * v[i][e];
     }
-    const float rstd = 1.0f / sqrtf(row_sum<LANES>(squares, mem) / float(p.cols) + p.eps);
+    row_sums<LANES, 1>(squares, mem);
+    const float rstd = 1.0f / sqrtf(squares[0] / float(p.cols) + p.eps);
     if (there && lane == 0 && p.rstd) p.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
-        const int c = (i * LANES + lane) * kVec;
+        const int c = (i * lanes + lane) * kVec;
         const bool in = there && c < p.cols;
         float w[kVec];
         if (in && p.weight) {
@@ -151,17 +154,18 @@ __global__ void __launch_bounds__(threads_for(LANES)) fwd_kernel(const FwdArgs<T
 // Any width and alignment: a block a row, the sum recomputed for the second pass.
 template <typename T>
 __global__ void __launch_bounds__(256) fwd_elements_kernel(const FwdArgs<T> p) {
-    __shared__ float mem[32];
+    __shared__ float mem[32][1];
     const int64_t row = blockIdx.x, at = row * p.cols;
     const auto value = [&](int64_t c) {
         return to_f32(p.x[at + c]) + (p.residual ? to_f32(p.residual[at + c]) : 0.0f);
     };
-    float squares = 0.0f;
+    float squares[1] = {0.0f};
     for (int64_t c = threadIdx.x; c < p.cols; c += 256) {
         const float v = value(c);
-        squares += v * v;
+        squares[0] += v * v;
     }
-    const float rstd = 1.0f / sqrtf(row_sum<256>(squares, mem) / float(p.cols) + p.eps);
+    row_sums<0, 1>(squares, mem);
+    const float rstd = 1.0f / sqrtf(squares[0] / float(p.cols) + p.eps);
     if (threadIdx.x == 0 && p.rstd) p.rstd[row] = rstd;
     // a warp takes a group of 64 columns at a time; the sum may lie where x or the residual lay
     const int lane = threadIdx.x % 32;
@@ -206,89 +210,143 @@ struct BwdArgs {
     int64_t rows, cols;
 };
 
-// A thread keeps its columns over all rows of its block: dw's partial sums
-// stay in registers.  Each group of LANES threads writes one part.
-template <typename T, int LANES, int VECS>
-__global__ void __launch_bounds__(threads_for(LANES)) bwd_kernel(const BwdArgs<T> p) {
-    __shared__ float mem[32];
-    constexpr int per_block = threads_for(LANES) / LANES;
-    const int lane = threadIdx.x % LANES;
-    const int64_t part = int64_t(blockIdx.x) * per_block + threadIdx.x / LANES, step = int64_t(gridDim.x) * per_block;
+// Eight elements as they lie in memory.
+template <typename T>
+struct Raw {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (auto &x : w) x = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int i = 0; i < int(sizeof(T) / 2); ++i) w[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+    }
+    __device__ __forceinline__ void add_to(float (&v)[kVec]) const {
+        float x[kVec];
+        load8(x, reinterpret_cast<const T *>(w));
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) v[e] += x[e];
+    }
+};
+
+// A thread keeps its columns over all rows of its block, so that dw's partial
+// sums stay in registers; a block writes one part.  ROWS rows at a time, all
+// their loads ahead of the sums; what was read is kept as it was read and
+// unpacked twice, which takes half the registers of its values.
+template <typename T, int LANES, int VECS, int ROWS>
+__global__ void __launch_bounds__(LANES ? 256 : 512, LANES ? 2 : 1) bwd_kernel(const BwdArgs<T> p) {
+    __shared__ float mem[2][32][ROWS];
+    __shared__ float fold[LANES ? 8 : 1][LANES ? LANES * kVec : 1];
+    const int lanes = LANES ? LANES : int(blockDim.x), lane = threadIdx.x % lanes;
+    const int groups = blockDim.x / lanes;              // rows side by side
     const float inv_cols = 1.0f / float(p.cols);
     float dw[VECS][kVec] = {};
-    // groups of a block take the same turns, for the barriers of row_sum
-    for (int64_t row0 = int64_t(blockIdx.x) * per_block; row0 < p.rows; row0 += step) {
-        const int64_t row = row0 + threadIdx.x / LANES, at = row * p.cols;
-        const bool there = row < p.rows;
-        const float rstd = there ? p.rstd[row] : 0.0f;
-        float s[VECS][kVec], d[VECS][kVec], sum = 0.0f;
+    // groups of a block take the same turns, for the barriers of row_sums
+    int turn = 0;
+    for (int64_t row0 = int64_t(blockIdx.x) * groups * ROWS; row0 < p.rows; row0 += int64_t(gridDim.x) * groups * ROWS) {
+        const int64_t row = row0 + threadIdx.x / lanes;         // and row + groups
+        Raw<T> s[ROWS][VECS], d[ROWS][VECS], more[ROWS][VECS], other[ROWS][VECS];
+        float rstd[ROWS], sum[ROWS];
 #pragma unroll
-        for (int i = 0; i < VECS; ++i) {
-            const int c = (i * LANES + lane) * kVec;
-            if (there && c < p.cols) {
-                load8(s[i], p.s + at + c);
-                load8(d[i], p.dy + at + c);
-                if (p.residual) {
-                    float r[kVec];
-                    load8(r, p.residual + at + c);
+        for (int r = 0; r < ROWS; ++r) {
+            const bool there = row + r * groups < p.rows;
+            const int64_t at = (row + r * groups) * p.cols;
+            rstd[r] = there ? p.rstd[row + r * groups] : 0.0f;
 #pragma unroll
-                    for (int e = 0; e < kVec; ++e) s[i][e] += r[e];
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) s[i][e] = d[i][e] = 0.0f;
+            for (int i = 0; i < VECS; ++i) {
+                const int c = (i * lanes + lane) * kVec;
+                const bool in = there && c < p.cols;
+                s[r][i].clear(), d[r][i].clear(), more[r][i].clear(), other[r][i].clear();
+                if (in) s[r][i].load(p.s + at + c), d[r][i].load(p.dy + at + c);
+                if (in && p.residual) other[r][i].load(p.residual + at + c);
+                if (in && p.ds) more[r][i].load(p.ds + at + c);
             }
+        }
+        // s r and w dy of one vector
+        const auto unpack = [&](int r, int i, float (&x)[kVec], float (&y)[kVec], bool first) {
+            const int c = (i * lanes + lane) * kVec;
             float w[kVec];
-            if (p.weight && c < p.cols) {
-                load8(w, p.weight + c);
-            } else {
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) w[e] = 1.0f;
-            }
+            for (int e = 0; e < kVec; ++e) x[e] = y[e] = 0.0f, w[e] = 1.0f;
+            s[r][i].add_to(x);
+            if (p.residual) other[r][i].add_to(x);
+            d[r][i].add_to(y);
+            if (p.weight && c < p.cols) load8(w, p.weight + c);
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
-                s[i][e] *= rstd;
-                dw[i][e] += d[i][e] * s[i][e];
-                d[i][e] *= w[e];
-                sum += d[i][e] * s[i][e];
+                x[e] *= rstd[r];
+                if (first) dw[i][e] += y[e] * x[e];
+                y[e] *= w[e];
+            }
+        };
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            sum[r] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < VECS; ++i) {
+                float x[kVec], y[kVec];
+                unpack(r, i, x, y, true);
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) sum[r] += y[e] * x[e];
             }
         }
-        const float mean = row_sum<LANES>(sum, mem) * inv_cols;
-        if (!there) continue;
+        row_sums<LANES, ROWS>(sum, mem[turn]);
+        turn ^= 1;
 #pragma unroll
-        for (int i = 0; i < VECS; ++i) {
-            const int c = (i * LANES + lane) * kVec;
-            if (c >= p.cols) continue;
-            float o[kVec];
-            if (p.ds) {
-                load8(o, p.ds + at + c);
-            } else {
+        for (int r = 0; r < ROWS; ++r) {
+            if (row + r * groups >= p.rows) break;
+            const int64_t at = (row + r * groups) * p.cols;
+            const float mean = sum[r] * inv_cols;
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) o[e] = 0.0f;
+            for (int i = 0; i < VECS; ++i) {
+                const int c = (i * lanes + lane) * kVec;
+                if (c >= p.cols) continue;
+                float x[kVec], y[kVec], o[kVec];
+                unpack(r, i, x, y, false);
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) o[e] = rstd[r] * (y[e] - x[e] * mean);
+                more[r][i].add_to(o);
+                store8(p.dx + at + c, o);
             }
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) o[e] += rstd * (d[i][e] - s[i][e] * mean);
-            store8(p.dx + at + c, o);
         }
     }
-    if (p.dweight)
+    if (!p.dweight) return;
+    if constexpr (LANES > 0) {
+        // the groups of a warp, then the warps
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+#pragma unroll
+            for (int o = LANES; o < 32; o *= 2) dw[0][e] += __shfl_xor_sync(0xffffffffu, dw[0][e], o);
+            if (threadIdx.x % 32 < LANES) fold[threadIdx.x / 32][(threadIdx.x % 32) * kVec + e] = dw[0][e];
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < p.cols; c += 256) {
+            float v = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v += fold[i][c];
+            p.parts[blockIdx.x * p.cols + c] = v;
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < VECS; ++i) {
-            const int c = (i * LANES + lane) * kVec;
-            if (c < p.cols) store8(p.parts + part * p.cols + c, dw[i]);
+            const int c = (i * lanes + lane) * kVec;
+            if (c < p.cols) store8(p.parts + blockIdx.x * p.cols + c, dw[i]);
         }
+    }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(256) bwd_elements_kernel(const BwdArgs<T> p) {
-    __shared__ float mem[32];
+    __shared__ float mem[32][1];
     const int64_t row = blockIdx.x, at = row * p.cols;
     const float rstd = p.rstd[row];
     const auto value = [&](int64_t c) { return to_f32(p.s[at + c]) + (p.residual ? to_f32(p.residual[at + c]) : 0.0f); };
     const auto wd = [&](int64_t c) { return to_f32(p.dy[at + c]) * (p.weight ? p.weight[c] : 1.0f); };
-    float sum = 0.0f;
-    for (int64_t c = threadIdx.x; c < p.cols; c += 256) sum += wd(c) * (value(c) * rstd);
-    const float mean = row_sum<256>(sum, mem) / float(p.cols);
+    float sum[1] = {0.0f};
+    for (int64_t c = threadIdx.x; c < p.cols; c += 256) sum[0] += wd(c) * (value(c) * rstd);
+    row_sums<0, 1>(sum, mem);
+    const float mean = sum[0] / float(p.cols);
     for (int64_t c = threadIdx.x; c < p.cols; c += 256)
         put(p.dx + at + c, (p.ds ? to_f32(p.ds[at + c]) : 0.0f) +
                                rstd * (wd(c) - value(c) * rstd * mean));
@@ -308,36 +366,38 @@ __global__ void __launch_bounds__(256) weight_elements_kernel(const BwdArgs<T> p
     p.parts[blockIdx.y * p.cols + c] = sum;
 }
 
-// dw from its parts: 32 columns a block, the parts over the warps, joined in
-// their order.
-__global__ void __launch_bounds__(256) weight_kernel(const float *parts, float *dweight, int n, int64_t cols) {
-    __shared__ float mem[8][32];
+// dw from its parts: 32 columns a block, the parts over its 32 warps, joined
+// in their order.
+__global__ void __launch_bounds__(1024) weight_kernel(const float *parts, float *dweight, int n, int64_t cols) {
+    __shared__ float mem[32][33];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int64_t c = int64_t(blockIdx.x) * 32 + lane;
     float sum[4] = {};
     if (c < cols)
-        for (int i = warp; i < n; i += 32)
+        for (int i = warp; i < n; i += 128)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (i + 8 * j < n) sum[j] += parts[int64_t(i + 8 * j) * cols + c];
+                if (i + 32 * j < n) sum[j] += parts[int64_t(i + 32 * j) * cols + c];
     mem[warp][lane] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
     __syncthreads();
-    if (warp == 0 && c < cols) {
-        float v = 0.0f;
+    // warp w has column w
+    float v = mem[lane][warp];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v += mem[i][lane];
-        dweight[c] = v;
-    }
+    for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int64_t mine = int64_t(blockIdx.x) * 32 + warp;
+    if (lane == 0 && mine < cols) dweight[mine] = v;
 }
 
 static bool on16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+// Threads for a row of `vecs` vectors at `each` a thread.
+static unsigned threads_for(int64_t vecs, int each) { return unsigned(((vecs + each - 1) / each + 31) / 32 * 32); }
 
 template <typename T, int LANES, int VECS>
 static cudaError_t go(const FwdArgs<T> &a, cudaStream_t st) {
-    constexpr int per_block = threads_for(LANES) / LANES;
-    const int64_t grid = (a.rows + per_block - 1) / per_block;
+    const unsigned threads = LANES ? 256 : threads_for(a.cols / kVec, VECS), per = LANES ? 256 / LANES : 1;
+    const int64_t grid = (a.rows + per - 1) / per;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    fwd_kernel<T, LANES, VECS><<<unsigned(grid), threads_for(LANES), 0, st>>>(a);
+    fwd_kernel<T, LANES, VECS><<<unsigned(grid), threads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -349,12 +409,9 @@ cudaError_t fwd(const FwdArgs<T> &a, cudaStream_t st) {
         if (vecs <= 8) return go<T, 8, 1>(a, st);
         if (vecs <= 16) return go<T, 16, 1>(a, st);
         if (vecs <= 32) return go<T, 32, 1>(a, st);
-        if (vecs <= 64) return go<T, 64, 1>(a, st);
-        if (vecs <= 128) return go<T, 64, 2>(a, st);
-        if (vecs <= 256) return go<T, 128, 2>(a, st);
-        if (vecs <= 512) return go<T, 256, 2>(a, st);
-        if (vecs <= 1024) return go<T, 256, 4>(a, st);
-        return go<T, 1024, 4>(a, st);
+        if (vecs <= 128) return go<T, 0, 1>(a, st);
+        if (vecs <= 1024) return go<T, 0, 2>(a, st);
+        return go<T, 0, 4>(a, st);
     }
     if (a.rows > 0x7fffffff) return cudaErrorInvalidConfiguration;
     fwd_elements_kernel<T><<<unsigned(a.rows), 256, 0, st>>>(a);
@@ -362,35 +419,29 @@ cudaError_t fwd(const FwdArgs<T> &a, cudaStream_t st) {
 }
 
 static cudaError_t fold(const float *parts, float *dweight, int64_t n, int64_t cols, cudaStream_t st) {
-    weight_kernel<<<unsigned((cols + 31) / 32), 256, 0, st>>>(parts, dweight, int(n), cols);
+    weight_kernel<<<unsigned((cols + 31) / 32), 1024, 0, st>>>(parts, dweight, int(n), cols);
     return cudaGetLastError();
 }
 
-template <typename T, int LANES, int VECS>
+template <typename T, int LANES, int VECS, int ROWS>
 static cudaError_t go(const BwdArgs<T> &a, cudaStream_t st) {
-    constexpr int per_block = threads_for(LANES) / LANES;
-    static_assert(kParts % per_block == 0, "whole blocks of parts");
-    const int64_t blocks = (a.rows + per_block - 1) / per_block;
-    const int64_t grid = blocks < kParts / per_block ? blocks : kParts / per_block;
-    bwd_kernel<T, LANES, VECS><<<unsigned(grid), threads_for(LANES), 0, st>>>(a);
+    const unsigned threads = LANES ? 256 : threads_for(a.cols / kVec, VECS), per = ROWS * (LANES ? 256 / LANES : 1);
+    const int64_t blocks = (a.rows + per - 1) / per, grid = blocks < kParts ? blocks : kParts;
+    bwd_kernel<T, LANES, VECS, ROWS><<<unsigned(grid), threads, 0, st>>>(a);
     if (cudaError_t e = cudaGetLastError()) return e;
-    return a.dweight ? fold(a.parts, a.dweight, grid * per_block, a.cols, st) : cudaSuccess;
+    return a.dweight ? fold(a.parts, a.dweight, grid, a.cols, st) : cudaSuccess;
 }
 
 template <typename T>
 cudaError_t bwd(const BwdArgs<T> &a, cudaStream_t st) {
     const int64_t vecs = a.cols / kVec;
-    if (a.cols % kVec == 0 && vecs <= 2048 && on16(a.dy) && on16(a.s) && on16(a.residual) && on16(a.ds) && on16(a.weight) && on16(a.dx) &&
-        on16(a.parts)) {
-        if (vecs <= 8) return go<T, 8, 1>(a, st);
-        if (vecs <= 16) return go<T, 16, 1>(a, st);
-        if (vecs <= 32) return go<T, 32, 1>(a, st);
-        if (vecs <= 64) return go<T, 64, 1>(a, st);
-        if (vecs <= 128) return go<T, 128, 1>(a, st);
-        if (vecs <= 256) return go<T, 128, 2>(a, st);
-        if (vecs <= 512) return go<T, 256, 2>(a, st);
-        if (vecs <= 1024) return go<T, 512, 2>(a, st);
-        return go<T, 1024, 2>(a, st);
+    if (a.cols % kVec == 0 && vecs <= 1024 && on16(a.dy) && on16(a.s) && on16(a.residual) && on16(a.ds) && on16(a.weight) &&
+        on16(a.dx) && on16(a.parts)) {
+        if (vecs <= 8) return go<T, 8, 1, 2>(a, st);
+        if (vecs <= 16) return go<T, 16, 1, 2>(a, st);
+        if (vecs <= 32) return go<T, 32, 1, 2>(a, st);
+        if (vecs <= 512) return go<T, 0, 1, 2>(a, st);
+        return go<T, 0, 2, 1>(a, st);
     }
     if (a.rows > 0x7fffffff) return cudaErrorInvalidConfiguration;
     bwd_elements_kernel<T><<<unsigned(a.rows), 256, 0, st>>>(a);
