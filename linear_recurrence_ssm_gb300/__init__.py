@@ -44,6 +44,7 @@ Options (of the selective scans; any of them selects the ``*_ex`` C entry point)
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -456,7 +457,7 @@ def _call(name, dev, *args):
     stream's handle without a Stream object."""
     import torch
     index = dev.index
-    if index != torch.cuda.current_device():
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return _call(name, dev, *args)
     st = getattr(_lib or library(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
@@ -779,30 +780,44 @@ def _delta_inputs(q, k, v, g, beta, step):
     """(device, Bs, L, G, H, K, V) of q, k (Bs, L, G, K), v (Bs, L, H, V) and
     g, beta (Bs, L, H); without L for a single step.  v may be None, then V is."""
     import torch
-    for t, n in ((q, "q"), (k, "k"), (g, "g"), (beta, "beta")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("%s must be a torch.Tensor" % n)
+    tensor = torch.Tensor
+    if not (isinstance(q, tensor) and isinstance(k, tensor) and isinstance(g, tensor) and isinstance(beta, tensor)):
+        raise TypeError("q, k, g and beta must be torch.Tensors")
     if not q.is_cuda:
         raise ValueError("inputs must be CUDA tensors")
-    dev, dtype = q.device, q.dtype
-    _check(q, "q", (torch.bfloat16, torch.float32), dev, (3 if step else 4,))
-    rows, (G, K) = q.shape[:-2], q.shape[-2:]
-    if g.dim() != len(rows) + 1:
-        raise ValueError("g must have %d dims, got %d" % (len(rows) + 1, g.dim()))
-    H = g.shape[-1]
-    for t, n, shape in ((k, "k", q.shape), (g, "g", (*rows, H)), (beta, "beta", (*rows, H))):
-        if not _fits(t, dtype, shape, dev):
-            _check_shape(t, n, (dtype,), dev, shape)
+    dev, dtype, shape, heads = q.device, q.dtype, q.shape, g.shape
+    if len(shape) != (3 if step else 4) or dtype not in (torch.bfloat16, torch.float32) or not q.is_contiguous():
+        _check(q, "q", (torch.bfloat16, torch.float32), dev, (3 if step else 4,))
+    if len(heads) != len(shape) - 1:
+        raise ValueError("g must have %d dims, got %d" % (len(shape) - 1, len(heads)))
+    if step:
+        (Bs, G, K), H, L = shape, heads[1], 1
+        gates = (Bs, H)
+    else:
+        (Bs, L, G, K), H = shape, heads[2]
+        gates = (Bs, L, H)
+    if not _fits(k, dtype, shape, dev):
+        _check_shape(k, "k", (dtype,), dev, shape)
+    if not _fits(g, dtype, gates, dev):
+        _check_shape(g, "g", (dtype,), dev, gates)
+    if not _fits(beta, dtype, gates, dev):
+        _check_shape(beta, "beta", (dtype,), dev, gates)
     if G < 1 or H % G != 0:
         raise ValueError("the heads of g (%d) must be a multiple of q's (%d)" % (H, G))
     V = None
     if v is not None:
-        if not isinstance(v, torch.Tensor):
+        if not isinstance(v, tensor):
             raise TypeError("v must be a torch.Tensor")
         V = v.shape[-1] if v.dim() else 0
-        if not _fits(v, dtype, (*rows, H, V), dev):
-            _check_shape(v, "v", (dtype,), dev, (*rows, H, V))
-    return (dev, rows[0], 1 if step else rows[1], G, H, K, V)
+        if not _fits(v, dtype, gates + (V,), dev):
+            _check_shape(v, "v", (dtype,), dev, gates + (V,))
+    return dev, Bs, L, G, H, K, V
+
+
+@functools.lru_cache(maxsize=256)
+def _delta_scratch(backward, *sizes):
+    """Bytes of the scratch that a call of these sizes takes."""
+    return getattr(library(), "delta_rule_bwd_scratch" if backward else "delta_rule_fwd_scratch")(*sizes)
 
 
 def _delta_sequences(offsets, Bs, dev):
@@ -854,7 +869,7 @@ def delta_rule_fwd(q, k, v, g, beta, scale=None, offsets=None, h0=None, return_f
         saved = {name: torch.empty(shape, dtype=v.dtype, device=dev)
                  for name, shape in _delta_saved_shapes(Bs, L, H, K, V, n_seq).items()}
     bf16 = int(v.dtype == torch.bfloat16)
-    scratch = torch.empty(library().delta_rule_fwd_scratch(Bs, L, G, H, K, V, n_seq, bf16), dtype=torch.uint8, device=dev)
+    scratch = torch.empty(_delta_scratch(False, Bs, L, G, H, K, V, n_seq, bf16), dtype=torch.uint8, device=dev)
     _call("delta_rule_fwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
           K ** -0.5 if scale is None else scale, _addr(offsets), _addr(h0), y.data_ptr(), _addr(hf),
           None if saved is None else saved["states"].data_ptr(),
@@ -889,8 +904,7 @@ def delta_rule_bwd(q, k, g, beta, dy, saved, scale=None, offsets=None, dh_final=
                dbeta=torch.empty_like(beta),
                dh0=torch.empty((n, H, V, K), dtype=torch.float32, device=dev) if need_dh0 else None)
     bf16 = int(q.dtype == torch.bfloat16)
-    size = library().delta_rule_bwd_scratch(Bs, L, G, H, K, V, n_seq, bf16)
-    scratch = torch.empty(size, dtype=torch.uint8, device=dev)
+    scratch = torch.empty(_delta_scratch(True, Bs, L, G, H, K, V, n_seq, bf16), dtype=torch.uint8, device=dev)
     _call("delta_rule_bwd", dev, q.data_ptr(), k.data_ptr(), g.data_ptr(), beta.data_ptr(),
           K ** -0.5 if scale is None else scale, _addr(offsets), dy.data_ptr(), _addr(dh_final),
           saved["states"].data_ptr(), saved["errors"].data_ptr(), out["dq"].data_ptr(), out["dk"].data_ptr(),
@@ -911,14 +925,14 @@ def delta_rule_step(q, k, v, g, beta, states, pages=None, scale=None, y=None):
         raise TypeError("v must be a torch.Tensor")
     if not isinstance(states, torch.Tensor):
         raise TypeError("states must be a torch.Tensor")
-    _check(states, "states", (torch.float32,), dev, (4,))
-    num_pages = states.shape[0]
-    if states.shape[1:] != (H, V, K):
+    num_pages = states.shape[0] if states.dim() else 0
+    if not _fits(states, torch.float32, (num_pages, H, V, K), dev):
+        _check(states, "states", (torch.float32,), dev, (4,))
         raise ValueError("states must have pages of %s" % ((H, V, K),))
     if pages is None:
         if num_pages < Bs:
             raise ValueError("states has fewer pages than q has rows")
-    else:
+    elif not (isinstance(pages, torch.Tensor) and _fits(pages, torch.int32, (Bs,), dev)):
         _check_shape(pages, "pages", (torch.int32,), dev, (Bs,))
     if y is None:
         y = torch.empty_like(v)
@@ -938,11 +952,19 @@ def _norm_input(t, name):
         raise TypeError("%s must be a torch.Tensor" % name)
     if not t.is_cuda:
         raise ValueError("inputs must be CUDA tensors")
-    _check(t, name, (torch.bfloat16, torch.float32), t.device)
-    if t.dim() < 1:
+    dev, shape = t.device, t.shape
+    if t.dtype not in (torch.bfloat16, torch.float32) or not t.is_contiguous():
+        _check(t, name, (torch.bfloat16, torch.float32), dev)
+    if not shape:
         raise ValueError("%s must have at least one dimension" % name)
-    cols = t.shape[-1]
-    return t.device, t.numel() // cols if cols else 0, cols
+    cols = shape[-1]
+    return dev, shape[0] if len(shape) == 2 else t.numel() // cols if cols else 0, cols
+
+
+def _norm_weight(weight, cols, dev):
+    import torch
+    if weight is not None and not (isinstance(weight, torch.Tensor) and _fits(weight, torch.float32, (cols,), dev)):
+        _check_shape(weight, "weight", (torch.float32,), dev, (cols,))
 
 
 def rms_norm_fwd(x, weight=None, residual=None, eps=1e-6, out="same", save=False):
@@ -959,7 +981,7 @@ def rms_norm_fwd(x, weight=None, residual=None, eps=1e-6, out="same", save=False
     dev, rows, cols = _norm_input(x, "x")
     if residual is not None and not (isinstance(residual, torch.Tensor) and _fits(residual, x.dtype, x.shape, dev)):
         _check_shape(residual, "residual", (x.dtype,), dev, x.shape)
-    _check_shape(weight, "weight", (torch.float32,), dev, (cols,))
+    _norm_weight(weight, cols, dev)
     if out not in ("same", "8bit"):
         raise ValueError("out must be 'same' or '8bit'")
     y = q = scale = None
@@ -991,8 +1013,9 @@ def rms_norm_bwd(dy, x, weight, rstd, residual=None, ds=None, need_dweight=True)
     for t, n in ((x, "x"), (residual, "residual"), (ds, "ds")):
         if t is not None and not (isinstance(t, torch.Tensor) and _fits(t, dy.dtype, dy.shape, dev)):
             _check_shape(t, n, (dy.dtype,), dev, dy.shape)
-    _check_shape(weight, "weight", (torch.float32,), dev, (cols,))
-    _check_shape(rstd, "rstd", (torch.float32,), dev, (rows,))
+    _norm_weight(weight, cols, dev)
+    if not (isinstance(rstd, torch.Tensor) and _fits(rstd, torch.float32, (rows,), dev)):
+        _check_shape(rstd, "rstd", (torch.float32,), dev, (rows,))
     dx = torch.empty_like(dy)
     dweight = scratch = None
     if weight is not None and need_dweight:

@@ -45,6 +45,7 @@ template <int KP>
 __global__ void __launch_bounds__(kThreads, 1) back_kernel(const BwdArgs<bf> p) {
     extern __shared__ __align__(1024) unsigned char mem[];
     using L = Layout<KP>;
+    let_next_begin();
     const Shape &s = p.s;
     const uint32_t base = smem_u32(mem);
     const int slices = (s.V + kSlice - 1) / kSlice;
@@ -100,6 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1) back_kernel(const BwdArgs<bf> p) 
             const int v = g + e / 2 * 8, k = 8 * n + c2 + e % 2;
             st[n][e] = chain && p.dh_final && v < width && k < s.K ? p.dh_final[state_at + int64_t(mine + v) * s.K + k] : 0.0f;
         }
+    wait_for_last();
     if (span.blocks > 0) copy_ahead(span.blocks - 1, 0);
     cp_async_commit();
     for (int i = 0; i <= span.blocks; ++i) {
@@ -299,6 +301,7 @@ __global__ void __launch_bounds__(256, VP == 64 ? 2 : 1) block_kernel(const BwdA
     __shared__ float row_term[2][kBlock], col_term[2][kBlock], row_sum[2][kBlock], both_term[8];
     __shared__ __align__(16) float col_sum[8][kBlock];
     using L = BlockLayout<KP, VP>;
+    let_next_begin();
     const Shape &s = p.s;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c2 = lane % 4 * 2;
     const int head = int(blockIdx.x % s.H), group = head / (s.H / s.G);
@@ -320,7 +323,12 @@ __global__ void __launch_bounds__(256, VP == 64 ? 2 : 1) block_kernel(const BwdA
         const int at = v0 / 64 * L::v, width = max(s.V - v0, 0);
         copy_tile<64, 256>(base + L::y + at, p.dy + v_at + (width > 0 ? v0 : 0), v_step, rows, width, tid);
         copy_tile<64, 256>(base + L::x + at, p.errors + v_at + (width > 0 ? v0 : 0), v_step, rows, width, tid);
-        copy_tile<64, 256>(base + L::dv + at, p.dv + v_at + (width > 0 ? v0 : 0), v_step, rows, width, tid);
+    }
+    wait_for_last();
+#pragma unroll
+    for (int v0 = 0; v0 < VP; v0 += 64) {
+        const int width = max(s.V - v0, 0);
+        copy_tile<64, 256>(base + L::dv + v0 / 64 * L::v, p.dv + v_at + (width > 0 ? v0 : 0), v_step, rows, width, tid);
     }
     cp_async_commit();
     {
@@ -599,18 +607,16 @@ static cudaError_t back(const BwdArgs<bf> &a, cudaStream_t st) {
     const int64_t grid = int64_t(a.s.n) * a.s.H * ((a.s.V + kSlice - 1) / kSlice);
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     constexpr int bytes = Layout<KP>::bytes;
-    if (cudaError_t e = cudaFuncSetAttribute(back_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
-    back_kernel<KP><<<unsigned(grid), kThreads, bytes, st>>>(a);
-    return cudaGetLastError();
+    if (cudaError_t e = allow<back_kernel<KP>>(bytes)) return e;
+    return launch_behind(back_kernel<KP>, unsigned(grid), kThreads, bytes, st, a);
 }
 template <int KP, int VP>
 static cudaError_t blocks(const BwdArgs<bf> &a, cudaStream_t st) {
     const int64_t grid = a.s.slots() * a.s.H;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     constexpr int bytes = BlockLayout<KP, VP>::bytes;
-    if (cudaError_t e = cudaFuncSetAttribute(block_kernel<KP, VP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
-    block_kernel<KP, VP><<<unsigned(grid), 256, bytes, st>>>(a, dbeta_parts(a.s));
-    return cudaGetLastError();
+    if (cudaError_t e = allow<block_kernel<KP, VP>>(bytes)) return e;
+    return launch_behind(block_kernel<KP, VP>, unsigned(grid), 256, bytes, st, a, dbeta_parts(a.s));
 }
 
 cudaError_t launch(const BwdArgs<bf> &a, cudaStream_t st) {

@@ -45,6 +45,7 @@ __global__ void __launch_bounds__(CARRY ? 32 * kChain : kThreads, CARRY ? 2 : 1)
     __shared__ int found;
     using L = Layout<KP, CARRY>;
     constexpr int threads = CARRY ? 32 * kChain : kThreads;
+    let_next_begin();
     const Shape &s = p.s;
     const uint32_t base = smem_u32(mem);
     const int of_values = (s.V + kSlice - 1) / kSlice, slices = CARRY ? of_values + (s.K + kSlice - 1) / kSlice : of_values;
@@ -98,6 +99,7 @@ __global__ void __launch_bounds__(CARRY ? 32 * kChain : kThreads, CARRY ? 2 : 1)
         constexpr int rest = (kTile + int(sizeof(Factors))) / 16;
         for (int i = tid; i < rest; i += threads) copy16(out + L::tile + i * 16, record + 2 * kTile + i * 16);
     };
+    wait_for_last();
     float st[KP / 8][4];
     if (chain) {
 #pragma unroll
@@ -274,6 +276,8 @@ __global__ void __launch_bounds__(CARRY ? 32 * kChain : kThreads, CARRY ? 2 : 1)
 constexpr int kJoinRows = 4, kJoinSplit = 4;
 __global__ void __launch_bounds__(128 * kJoinSplit) join_kernel(const FwdArgs<bf> p) {
     __shared__ float S[kJoinRows][128], shares[kJoinSplit][kJoinRows][128];
+    let_next_begin();
+    wait_for_last();
     const Shape &s = p.s;
     const int tiles = (s.V + kJoinRows - 1) / kJoinRows, k = threadIdx.x % 128, quarter = threadIdx.x / 128;
     const int v0 = int(blockIdx.x % tiles) * kJoinRows, head = int(blockIdx.x / tiles % s.H), seq = int(blockIdx.x / tiles / s.H);
@@ -322,10 +326,8 @@ static cudaError_t go(const FwdArgs<bf> &a, int64_t places, cudaStream_t st) {
     const int64_t grid = places * a.s.H * slices;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     constexpr int bytes = Layout<KP, CARRY>::bytes;
-    if (cudaError_t e = cudaFuncSetAttribute(fwd_kernel<KP, CARRY>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes))
-        return e;
-    fwd_kernel<KP, CARRY><<<unsigned(grid), CARRY ? 32 * kChain : kThreads, bytes, st>>>(a);
-    return cudaGetLastError();
+    if (cudaError_t e = allow<fwd_kernel<KP, CARRY>>(bytes)) return e;
+    return launch_behind(fwd_kernel<KP, CARRY>, unsigned(grid), CARRY ? 32 * kChain : kThreads, bytes, st, a);
 }
 
 static bool on16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -346,8 +348,9 @@ cudaError_t launch(FwdArgs<bf> a, cudaStream_t st) {
     a.entering = reinterpret_cast<float *>(a.scratch + at.entering);
     const int64_t places = part_places(a.s, a.part);
     if (cudaError_t e = wide ? go<128, true>(a, places, st) : go<64, true>(a, places, st)) return e;
-    join_kernel<<<unsigned((a.s.V + kJoinRows - 1) / kJoinRows * a.s.H * a.s.n), 128 * kJoinSplit, 0, st>>>(a);
-    if (cudaError_t e = cudaGetLastError()) return e;
+    if (cudaError_t e = launch_behind(join_kernel, unsigned((a.s.V + kJoinRows - 1) / kJoinRows * a.s.H * a.s.n),
+                                      128 * kJoinSplit, 0, st, a))
+        return e;
     return wide ? go<128, false>(a, places, st) : go<64, false>(a, places, st);
 }
 

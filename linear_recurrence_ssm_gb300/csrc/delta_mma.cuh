@@ -8,6 +8,8 @@
 // warp's registers, and the warps of the chain never wait for one another.
 #pragma once
 
+#include <atomic>
+
 #include "delta_rule.cuh"
 
 namespace ssm {
@@ -43,6 +45,11 @@ __device__ __forceinline__ void store4t(uint32_t at, const uint32_t (&r)[4]) {
                  "r"(r[1]), "r"(r[2]), "r"(r[3])
                  : "memory");
 }
+
+// A kernel launched behind another one may begin while that one runs: it lets
+// the next one do the same, and waits before it reads what the one before wrote.
+__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Two values as bf16, the first in the low half.
 __device__ __forceinline__ uint32_t pack(float a, float b) {
@@ -362,6 +369,30 @@ constexpr int kTile = kBlock * kBlock * 2;
 constexpr int kRecord = (3 * kTile + int(sizeof(Factors)) + 127) / 128 * 128, kBothRecord = kRecord + kTile;
 cudaError_t make_pairs(const Shape &s, const bf *q, const bf *k, const bf *g, const bf *beta, unsigned char *records,
                        bool both, cudaStream_t st);
+
+// Dynamic shared memory for a kernel, allowed once a device.
+template <auto KERNEL>
+cudaError_t allow(int bytes) {
+    static std::atomic<uint64_t> known{0};
+    int device = 0;
+    if (cudaError_t e = cudaGetDevice(&device)) return e;
+    if (device < 64 && known.load(std::memory_order_acquire) >> device & 1) return cudaSuccess;
+    if (cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+    if (device < 64) known.fetch_or(uint64_t(1) << device, std::memory_order_release);
+    return cudaSuccess;
+}
+// A launch that may begin while the kernel before it in the stream runs.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, int bytes, cudaStream_t st, A... args) {
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(grid), c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = size_t(bytes), c.stream = st;
+    c.attrs = &at, c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
 
 // Sizes whose rows 16-byte copies can take, and whose states fit a warp's registers.
 inline bool fits(const Shape &s) { return s.K <= 128 && s.K % 8 == 0 && s.V % 8 == 0; }

@@ -28,6 +28,7 @@ pairs_kernel(const Shape s, const bf *q, const bf *k, const bf *g, const bf *bet
     __shared__ Factors f;
     __shared__ int found;
     using L = PairLayout<KP>;
+    let_next_begin();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int head = int(blockIdx.x % s.H), group = head / (s.H / s.G);
     const int64_t slot = blockIdx.x / s.H;
@@ -109,7 +110,7 @@ static cudaError_t go(const Shape &s, const bf *q, const bf *k, const bf *g, con
     const int64_t grid = s.slots() * s.H;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     constexpr int bytes = PairLayout<KP>::bytes;
-    if (cudaError_t e = cudaFuncSetAttribute(pairs_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+    if (cudaError_t e = allow<pairs_kernel<KP>>(bytes)) return e;
     pairs_kernel<KP><<<unsigned(grid), kPairThreads, bytes, st>>>(s, q, k, g, beta, records, both);
     return cudaGetLastError();
 }
