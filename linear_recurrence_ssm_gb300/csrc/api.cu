@@ -473,11 +473,11 @@ ssm::delta::Shape delta_shape(const int32_t *offsets, int64_t Bs, int64_t L, int
 
 // The scratch of the gradients holds what either path needs.
 ssm::delta::Scratch delta_scratch(const ssm::delta::Shape &s, int elem) {
-    int64_t shares = ssm::delta::general::shares(s), records = 0;
+    int64_t shares = ssm::delta::general::shares(s), records = ssm::delta::general::made_bytes(s);
     if (elem == 2 && ssm::delta::mma::fits_bwd(s)) {
         const int64_t blocks = s.slots() * s.H;
         shares = std::max(shares, blocks * ssm::delta::kBlock * ssm::delta::mma::dbeta_parts(s));
-        records = blocks * ssm::delta::mma::kBothRecord;
+        records = std::max(records, blocks * ssm::delta::mma::kBothRecord);
     }
     return ssm::delta::scratch_of(s, elem, shares, records);
 }
@@ -980,7 +980,8 @@ int64_t delta_rule_fwd_scratch(int64_t Bs, int64_t L, int64_t G, int64_t H, int6
     if (check_delta_sizes(Bs, L, G, H, K, V, n_seq, 1.0f) != SSM_OK) return 0;
     static const int32_t some = 0;      // only that there are offsets counts
     const ssm::delta::Shape s = delta_shape(n_seq > 0 ? &some : nullptr, Bs, L, G, H, K, V, n_seq, 1.0f);
-    return input_bf16 && ssm::delta::mma::fits(s) ? ssm::delta::mma::fwd_scratch(s).bytes : 16;
+    const int64_t made = ssm::delta::general::made_bytes(s);
+    return input_bf16 && ssm::delta::mma::fits(s) ? std::max(made, ssm::delta::mma::fwd_scratch(s).bytes) : made;
 }
 
 int64_t delta_rule_bwd_scratch(int64_t Bs, int64_t L, int64_t G, int64_t H, int64_t K, int64_t V,

@@ -2,10 +2,12 @@
 // for every type and head size (K, V up to 256): the path for fp32 inputs and
 // for sizes without a tensor-core form.
 //
-// A thread block takes one head of one sequence and 32 rows of its state (the
-// rows are independent of one another), and walks the sequence 64 steps at a
-// time with the state in shared memory; the unit triangular system of a block
-// is solved by substitution, 16 rows at a time.
+// pairs_kernel takes all blocks of 64 steps at once and solves each one's
+// system, N with (I + Ab beta) N = Ab, 16 rows at a time; a thread block of the
+// chains takes one head of one sequence and 32 rows of its state (the rows are
+// independent of one another) with the state in shared memory, and has matrix
+// products left: W = V - Gam K S^T, X = W - N (beta W) and so on.  With the
+// systems solved inside the chain a block of 64 steps took 40 us of it.
 #include "delta_rule.cuh"
 
 namespace ssm {
@@ -18,13 +20,39 @@ constexpr int kPairs = kBlock + 4, kRow = kSlice + 4;      // row strides, in fl
 __host__ __device__ inline int padded(int K) { return (K + 3) / 4 * 4; }
 __host__ __device__ inline int stride_of(int K) { return padded(K) + 4; }
 
-// `rows` rows of `width` elements, `step` elements apart, as floats; zeros up to 64 x `cols`.
+__device__ __forceinline__ void fma4(float4 &o, float a, const float4 &b) {
+    o.x += a * b.x, o.y += a * b.y, o.z += a * b.z, o.w += a * b.w;
+}
+
+// Four elements of a row, `left` of them there.
+template <typename T>
+__device__ __forceinline__ float4 four_of(const T *p, int left, bool vectors) {
+    if (vectors && left >= 4) return to_f32x4(p);
+    return make_float4(left > 0 ? to_f32(p[0]) : 0.0f, left > 1 ? to_f32(p[1]) : 0.0f, left > 2 ? to_f32(p[2]) : 0.0f,
+                       left > 3 ? to_f32(p[3]) : 0.0f);
+}
+template <typename T>
+__device__ __forceinline__ bool on_vectors(const T *p, int64_t step) {
+    return reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0 && step % 4 == 0;
+}
+
+// `rows` rows of `width` elements, `step` elements apart, as floats; zeros up
+// to 64 x `cols` (a multiple of 4).  Sixteen threads take a row.
 template <typename T>
 __device__ __forceinline__ void load_tile(float *tile, int stride, const T *src, int64_t step, int rows, int width,
                                           int cols) {
-    for (int i = threadIdx.x; i < kBlock * cols; i += kThreads) {
-        const int t = i / cols, c = i - t * cols;
-        tile[t * stride + c] = t < rows && c < width ? to_f32(src[t * step + c]) : 0.0f;
+    const bool vectors = on_vectors(src, step);
+    const int col = threadIdx.x % 16 * 4;
+    float4 v[4];
+    for (int c = col; c < cols; c += 64) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = threadIdx.x / 16 + 16 * i;
+            v[i] = t < rows ? four_of(src + t * step + c, width - c, vectors) : make_float4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4 *>(tile + (threadIdx.x / 16 + 16 * i) * stride + c) = v[i];
     }
 }
 
@@ -48,6 +76,10 @@ __device__ __forceinline__ void products(float (&out)[4][4], const float *a, con
     }
 }
 
+// Where row v of the state lies: a thread reads four neighbours, and the eight
+// threads beside it the next ones, which so lie in different banks.
+__device__ __forceinline__ int lies(int v) { return v % 4 * (kSlice / 4) + v / 4; }
+
 // Rows t and t + 32 of `a` times four rows v.. of the state: out[i][j] = a_(t + 32 i) . S_(v + j).
 __device__ __forceinline__ void through_state(float (&out)[2][4], const float *a, const float *S, int stride, int Kp,
                                               int t, int v) {
@@ -58,7 +90,7 @@ __device__ __forceinline__ void through_state(float (&out)[2][4], const float *a
 #pragma unroll
         for (int i = 0; i < 2; ++i) u[i] = *reinterpret_cast<const float4 *>(a + (t + 32 * i) * stride + k);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const float4 *>(S + (v + j) * stride + k);
+        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const float4 *>(S + (j * (kSlice / 4) + v / 4) * stride + k);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -67,9 +99,12 @@ __device__ __forceinline__ void through_state(float (&out)[2][4], const float *a
     }
 }
 
-__device__ __forceinline__ void fma4(float4 &o, float a, const float4 &b) {
-    o.x += a * b.x, o.y += a * b.y, o.z += a * b.z, o.w += a * b.w;
-}
+// What the chains need of a block, in floats: N, P (with the scale), and the
+// decays.
+struct Made {
+    float n[kBlock * kBlock], p[kBlock * kBlock];
+    Decays d;
+};
 
 struct Layout {
     int stride, q, k, s, a, p, w, x, words;
@@ -86,6 +121,87 @@ __host__ __device__ inline Layout layout_of(int K) {
     l.x = l.w + kBlock * kRow;
     l.words = l.x + kBlock * kRow;
     return l;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) pairs_kernel(const Shape s, const T *q, const T *k, const T *g, const T *beta,
+                                                         Made *made) {
+    extern __shared__ __align__(16) float mem[];
+    __shared__ Decays d;
+    __shared__ int found;
+    const int Kp = padded(s.K), stride = stride_of(s.K), tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+    const int wide = stride > kPairs ? stride : kPairs;
+    float *Q = mem, *Kt = Q + kBlock * stride, *A = mem + 2 * kBlock * wide;
+    const int head = int(blockIdx.x % s.H), group = head / (s.H / s.G);
+    const int64_t slot = blockIdx.x / s.H;
+    const int seq = sequence_of(s, slot, &found);
+    if (seq < 0) return;
+    const Span span = span_of(s, seq);
+    const int c = int(slot - span.slot), rows = min(kBlock, span.len - c * kBlock);
+    const int64_t row = span.first + int64_t(c) * kBlock, step = int64_t(s.G) * s.K;
+    Made &out = made[slot * s.H + head];
+    load_tile(Q, stride, q + row * step + int64_t(group) * s.K, step, rows, s.K, Kp);
+    load_tile(Kt, stride, k + row * step + int64_t(group) * s.K, step, rows, s.K, Kp);
+    if (tid < 32) load_decays(d, g + row * s.H + head, beta + row * s.H + head, s.H, rows);
+    __syncthreads();
+    for (int i = tid; i < int(sizeof(Decays) / 4); i += kThreads)
+        reinterpret_cast<float *>(&out.d)[i] = reinterpret_cast<const float *>(&d)[i];
+    float m[4][4];
+    products(m, Q, Kt, stride, Kp);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int t = ty + 16 * (i / 4), r = tx + 16 * (i % 4);
+        out.p[t * kBlock + r] = r <= t ? s.scale * m[i / 4][i % 4] * d.between(t, r) : 0.0f;
+    }
+    products(m, Kt, Kt, stride, Kp);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int t = ty + 16 * (i / 4), r = tx + 16 * (i % 4);
+        A[t * kPairs + r] = r < t ? m[i / 4][i % 4] * d.between(t, r) : 0.0f;
+    }
+    __syncthreads();
+    // N in A's place, a thread a column: N_t = A_t - sum over s < t of A_ts beta_s N_s.  The rows below a block of 16
+    // are brought up to date by all threads; column j of N is 0 down to row j, where A is.
+    float *N = mem;      // in the tiles' place
+    for (int b = 0; b < kBlock; b += 16) {
+        if (tid < kBlock) {
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                x[i] = b == 0 ? A[i * kPairs + tid] : N[(b + i) * kPairs + tid];
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (j < i) x[i] -= A[(b + i) * kPairs + b + j] * (d.beta[b + j] * x[j]);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) N[(b + i) * kPairs + tid] = x[i];
+        }
+        __syncthreads();
+        // four columns of a row
+        for (int i = tid + (b + 16) * 16; i < kBlock * 16; i += kThreads) {
+            const int t = i / 16, r = i % 16 * 4;
+            float4 o = *reinterpret_cast<const float4 *>((b == 0 ? A : N) + t * kPairs + r);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                fma4(o, -A[t * kPairs + b + j] * d.beta[b + j], *reinterpret_cast<const float4 *>(N + (b + j) * kPairs + r));
+            *reinterpret_cast<float4 *>(N + t * kPairs + r) = o;
+        }
+        __syncthreads();
+    }
+    for (int i = tid; i < kBlock * kBlock; i += kThreads) {
+        const int t = i / kBlock, r = i % kBlock;
+        out.n[i] = r < t ? N[t * kPairs + r] : 0.0f;
+    }
+}
+
+// N (or P) and the decays of a block, into shared memory.
+__device__ __forceinline__ void load_pairs(float *tile, const float *from) {
+    for (int i = threadIdx.x; i < kBlock * kBlock / 4; i += kThreads)
+        *reinterpret_cast<float4 *>(tile + i / 16 * kPairs + i % 16 * 4) = reinterpret_cast<const float4 *>(from)[i];
+}
+__device__ __forceinline__ void load_made(Decays &d, const Decays &from) {
+    for (int i = threadIdx.x; i < int(sizeof(Decays) / 16); i += kThreads)
+        reinterpret_cast<float4 *>(&d)[i] = reinterpret_cast<const float4 *>(&from)[i];
 }
 
 // Which head, sequence and rows of the state a thread block has.
@@ -117,10 +233,9 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdArgs<T> p) {
     const int64_t qk_step = int64_t(s.G) * s.K, v_step = int64_t(s.H) * s.V;
     const int64_t state_at = (int64_t(w.seq) * s.H + w.head) * s.V * s.K + int64_t(w.v0) * s.K;
 
-    for (int i = tid; i < kSlice * Kp; i += kThreads) {
-        const int v = i / Kp, k = i - v * Kp;
-        S[v * l.stride + k] = p.h0 && v < w.width && k < s.K ? p.h0[state_at + int64_t(v) * s.K + k] : 0.0f;
-    }
+    for (int v = tid / 32; v < kSlice; v += kThreads / 32)
+        for (int k = tid % 32; k < Kp; k += 32)
+            S[lies(v) * l.stride + k] = p.h0 && v < w.width && k < s.K ? p.h0[state_at + int64_t(v) * s.K + k] : 0.0f;
     const int t0 = tid / 8, v4 = tid % 8 * 4;
     for (int c = 0; c < span.blocks; ++c) {
         const int rows = min(kBlock, span.len - c * kBlock);
@@ -129,70 +244,49 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdArgs<T> p) {
         load_tile(Q, l.stride, p.q + row * qk_step + int64_t(w.group) * s.K, qk_step, rows, s.K, Kp);
         load_tile(Kt, l.stride, p.k + row * qk_step + int64_t(w.group) * s.K, qk_step, rows, s.K, Kp);
         load_tile(W, kRow, p.v + row * v_step + int64_t(w.head) * s.V + w.v0, v_step, rows, w.width, kSlice);
-        if (tid < 32) load_decays(d, p.g + row * s.H + w.head, p.beta + row * s.H + w.head, s.H, rows);
+        const Made &made = reinterpret_cast<const Made *>(p.scratch)[(span.slot + c) * s.H + w.head];
+        load_made(d, made.d);
+        load_pairs(A, made.n);
+        load_pairs(P, made.p);
         __syncthreads();
         if (p.states) {
             T *out = p.states + ((span.slot + c) * s.H + w.head) * int64_t(s.V) * s.K + int64_t(w.v0) * s.K;
-            for (int i = tid; i < w.width * s.K; i += kThreads) {
-                const int v = i / s.K, k = i - v * s.K;
-                put(out + i, S[v * l.stride + k]);
-            }
-        }
-        float m[4][4];
-        const int tx = tid % 16, ty = tid / 16;
-        products(m, Kt, Kt, l.stride, Kp);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int t = ty + 16 * (i / 4), r = tx + 16 * (i % 4);
-            A[t * kPairs + r] = r < t ? m[i / 4][i % 4] * d.between(t, r) * d.beta[r] : 0.0f;
-        }
-        products(m, Q, Kt, l.stride, Kp);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int t = ty + 16 * (i / 4), r = tx + 16 * (i % 4);
-            P[t * kPairs + r] = r <= t ? m[i / 4][i % 4] * d.between(t, r) : 0.0f;
+            for (int v = tid / 32; v < w.width; v += kThreads / 32)
+                for (int k = tid % 32; k < s.K; k += 32) put(out + v * s.K + k, S[lies(v) * l.stride + k]);
         }
         float from[2][4], y[2][4];
         through_state(from, Kt, S, l.stride, Kp, t0, v4);
         through_state(y, Q, S, l.stride, Kp, t0, v4);
+        // W, and beta W beside it
+        float *U = mem + l.x;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int t = t0 + 32 * (i / 4);
-            const float start = d.start(t);
-            // a cut drops the state before it, whatever that holds
-            W[t * kRow + v4 + i % 4] -= start == 0.0f ? 0.0f : start * from[i / 4][i % 4];
-            y[i / 4][i % 4] = start == 0.0f ? 0.0f : start * y[i / 4][i % 4];
+        for (int i = 0; i < 2; ++i) {
+            const int t = t0 + 32 * i;
+            const float start = d.start(t), beta = d.beta[t];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                // a cut drops the state before it, whatever that holds
+                const float v = W[t * kRow + v4 + j] - (start == 0.0f ? 0.0f : start * from[i][j]);
+                from[i][j] = v;
+                U[t * kRow + v4 + j] = beta * v;
+                y[i][j] = start == 0.0f ? 0.0f : s.scale * start * y[i][j];
+            }
         }
         __syncthreads();
-        // X from W, 16 rows at a time
-        for (int b = 0; b < kBlock; b += 16) {
-            if (tid < kSlice) {
-                float x[16];
+        // X
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    x[i] = W[(b + i) * kRow + tid];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (j < i) x[i] -= A[(b + i) * kPairs + b + j] * x[j];
-                    W[(b + i) * kRow + tid] = x[i];
-                }
-            }
-            __syncthreads();
-            for (int i = tid + (b + 16) * kSlice; i < kBlock * kSlice; i += kThreads) {
-                const int t = i / kSlice, v = i % kSlice;
-                float sum = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) sum += A[t * kPairs + b + j] * W[(b + j) * kRow + v];
-                W[t * kRow + v] -= sum;
-            }
-            __syncthreads();
+        for (int i = 0; i < 2; ++i) {
+            const int t = t0 + 32 * i;
+            float4 o = make_float4(from[i][0], from[i][1], from[i][2], from[i][3]);
+#pragma unroll 4
+            for (int r = 0; r < t; ++r) fma4(o, -A[t * kPairs + r], *reinterpret_cast<const float4 *>(U + r * kRow + v4));
+            *reinterpret_cast<float4 *>(W + t * kRow + v4) = o;
         }
+        __syncthreads();
         if (p.errors) {
             T *out = p.errors + row * v_step + int64_t(w.head) * s.V + w.v0;
-            for (int i = tid; i < rows * w.width; i += kThreads) {
-                const int t = i / w.width, v = i - t * w.width;
-                put(out + t * v_step + v, W[t * kRow + v]);
-            }
+            for (int t = tid / 32; t < rows; t += kThreads / 32)
+                if (tid % 32 < w.width) put(out + t * v_step + tid % 32, W[t * kRow + tid % 32]);
             __syncthreads();
         }
         for (int i = tid; i < kBlock * kSlice; i += kThreads) W[i / kSlice * kRow + i % kSlice] *= d.beta[i / kSlice];
@@ -202,13 +296,14 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdArgs<T> p) {
         for (int i = 0; i < 2; ++i) {
             const int t = t0 + 32 * i;
             float4 o = make_float4(y[i][0], y[i][1], y[i][2], y[i][3]);
+#pragma unroll 4
             for (int r = 0; r <= t; ++r) fma4(o, P[t * kPairs + r], *reinterpret_cast<const float4 *>(W + r * kRow + v4));
             if (t < rows) {
                 T *out = p.y + (row + t) * v_step + int64_t(w.head) * s.V + w.v0 + v4;
                 const float v[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (v4 + j < w.width) put(out + j, s.scale * v[j]);
+                    if (v4 + j < w.width) put(out + j, v[j]);
             }
         }
         const float last = d.start(kBlock - 1);
@@ -220,25 +315,24 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdArgs<T> p) {
             float4 o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                o[j] = *reinterpret_cast<const float4 *>(S + (v + j) * l.stride + k);
+                o[j] = *reinterpret_cast<const float4 *>(S + lies(v + j) * l.stride + k);
                 o[j] = last == 0.0f ? make_float4(0, 0, 0, 0)
                                     : make_float4(last * o[j].x, last * o[j].y, last * o[j].z, last * o[j].w);
             }
+#pragma unroll 4
             for (int t = 0; t < rows; ++t) {
                 const float4 u = *reinterpret_cast<const float4 *>(W + t * kRow + v);
                 const float4 kk = *reinterpret_cast<const float4 *>(Kt + t * l.stride + k);
                 fma4(o[0], u.x, kk), fma4(o[1], u.y, kk), fma4(o[2], u.z, kk), fma4(o[3], u.w, kk);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) *reinterpret_cast<float4 *>(S + (v + j) * l.stride + k) = o[j];
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<float4 *>(S + lies(v + j) * l.stride + k) = o[j];
         }
     }
     __syncthreads();
     if (p.h_final)
-        for (int i = tid; i < w.width * s.K; i += kThreads) {
-            const int v = i / s.K, k = i - v * s.K;
-            p.h_final[state_at + i] = S[v * l.stride + k];
-        }
+        for (int v = tid / 32; v < w.width; v += kThreads / 32)
+            for (int k = tid % 32; k < s.K; k += 32) p.h_final[state_at + v * s.K + k] = S[lies(v) * l.stride + k];
     clear_uncovered(s, w.seq, p.y + int64_t(w.head) * s.V + w.v0, v_step, w.width);
 }
 
@@ -260,11 +354,10 @@ __global__ void __launch_bounds__(kThreads) back_kernel(const BwdArgs<T> p) {
     const int64_t rows_all = s.offsets ? s.L : s.L * s.n;
     float *part = p.dbeta_part + int64_t(w.v0 / kSlice) * rows_all * s.H + w.head;
 
-    for (int i = tid; i < kSlice * Kp; i += kThreads) {
-        const int v = i / Kp, k = i - v * Kp;
-        S[v * l.stride + k] =
-            p.dh_final && v < w.width && k < s.K ? p.dh_final[state_at + int64_t(v) * s.K + k] : 0.0f;
-    }
+    for (int v = tid / 32; v < kSlice; v += kThreads / 32)
+        for (int k = tid % 32; k < Kp; k += 32)
+            S[lies(v) * l.stride + k] =
+                p.dh_final && v < w.width && k < s.K ? p.dh_final[state_at + int64_t(v) * s.K + k] : 0.0f;
     const int t0 = tid / 8, v4 = tid % 8 * 4;
     for (int c = span.blocks - 1; c >= 0; --c) {
         const int rows = min(kBlock, span.len - c * kBlock);
@@ -273,62 +366,42 @@ __global__ void __launch_bounds__(kThreads) back_kernel(const BwdArgs<T> p) {
         load_tile(Q, l.stride, p.q + row * qk_step + int64_t(w.group) * s.K, qk_step, rows, s.K, Kp);
         load_tile(Kt, l.stride, p.k + row * qk_step + int64_t(w.group) * s.K, qk_step, rows, s.K, Kp);
         load_tile(Y, kRow, p.dy + row * v_step + int64_t(w.head) * s.V + w.v0, v_step, rows, w.width, kSlice);
-        if (tid < 32) load_decays(d, p.g + row * s.H + w.head, p.beta + row * s.H + w.head, s.H, rows);
+        const Made &made = reinterpret_cast<const Made *>(p.records)[(span.slot + c) * s.H + w.head];
+        load_made(d, made.d);
+        load_pairs(A, made.n);
+        load_pairs(P, made.p);
         __syncthreads();
         T *ds = p.ds + ((span.slot + c) * s.H + w.head) * int64_t(s.V) * s.K + int64_t(w.v0) * s.K;
-        for (int i = tid; i < w.width * s.K; i += kThreads) {
-            const int v = i / s.K, k = i - v * s.K;
-            put(ds + i, S[v * l.stride + k]);
-        }
-        float m[4][4];
-        const int tx = tid % 16, ty = tid / 16;
-        products(m, Kt, Kt, l.stride, Kp);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int t = ty + 16 * (i / 4), r = tx + 16 * (i % 4);
-            A[t * kPairs + r] = r < t ? m[i / 4][i % 4] * d.between(t, r) * d.beta[t] : 0.0f;
-        }
-        products(m, Q, Kt, l.stride, Kp);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int t = ty + 16 * (i / 4), r = tx + 16 * (i % 4);
-            P[t * kPairs + r] = r <= t ? s.scale * m[i / 4][i % 4] * d.between(t, r) : 0.0f;
-        }
+        for (int v = tid / 32; v < w.width; v += kThreads / 32)
+            for (int k = tid % 32; k < s.K; k += 32) put(ds + v * s.K + k, S[lies(v) * l.stride + k]);
         float from[2][4];
         through_state(from, Kt, S, l.stride, Kp, t0, v4);
-        __syncthreads();
+        // dU, and beta dU beside it
+        float4 du[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int t = t0 + 32 * i;
-            const float end = d.end(t);
+            const float end = d.end(t), beta = d.beta[t];
             float4 o = end == 0.0f ? make_float4(0, 0, 0, 0)
                                    : make_float4(end * from[i][0], end * from[i][1], end * from[i][2], end * from[i][3]);
+#pragma unroll 4
             for (int r = t; r < rows; ++r) fma4(o, P[r * kPairs + t], *reinterpret_cast<const float4 *>(Y + r * kRow + v4));
-            *reinterpret_cast<float4 *>(Z + t * kRow + v4) = o;
+            du[i] = o;
+            *reinterpret_cast<float4 *>(Z + t * kRow + v4) = make_float4(beta * o.x, beta * o.y, beta * o.z, beta * o.w);
         }
         __syncthreads();
-        for (int b = kBlock - 16; b >= 0; b -= 16) {
-            if (tid < kSlice) {
-                float x[16];
+        // Z
 #pragma unroll
-                for (int i = 15; i >= 0; --i) {
-                    x[i] = Z[(b + i) * kRow + tid];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (j > i) x[i] -= A[(b + j) * kPairs + b + i] * x[j];
-                    Z[(b + i) * kRow + tid] = x[i];
-                }
-            }
-            __syncthreads();
-            for (int i = tid; i < b * kSlice; i += kThreads) {
-                const int t = i / kSlice, v = i % kSlice;
-                float sum = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) sum += A[(b + j) * kPairs + t] * Z[(b + j) * kRow + v];
-                Z[t * kRow + v] -= sum;
-            }
-            __syncthreads();
+        for (int i = 0; i < 2; ++i) {
+            const int t = t0 + 32 * i;
+#pragma unroll 4
+            for (int r = t + 1; r < rows; ++r)
+                fma4(du[i], -A[r * kPairs + t], *reinterpret_cast<const float4 *>(Z + r * kRow + v4));
         }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) *reinterpret_cast<float4 *>(Z + (t0 + 32 * i) * kRow + v4) = du[i];
+        __syncthreads();
         // a warp takes a row at a time: dbeta's share, dv, and beta Z in Z's place
         {
             const int lane = tid % 32;
@@ -355,10 +428,11 @@ __global__ void __launch_bounds__(kThreads) back_kernel(const BwdArgs<T> p) {
             float4 o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                o[j] = *reinterpret_cast<const float4 *>(S + (v + j) * l.stride + k);
+                o[j] = *reinterpret_cast<const float4 *>(S + lies(v + j) * l.stride + k);
                 o[j] = last == 0.0f ? make_float4(0, 0, 0, 0)
                                     : make_float4(last * o[j].x, last * o[j].y, last * o[j].z, last * o[j].w);
             }
+#pragma unroll 4
             for (int t = 0; t < rows; ++t) {
                 float4 u = *reinterpret_cast<const float4 *>(Y + t * kRow + v);
                 float4 kk = *reinterpret_cast<const float4 *>(Q + t * l.stride + k);
@@ -368,15 +442,13 @@ __global__ void __launch_bounds__(kThreads) back_kernel(const BwdArgs<T> p) {
                 fma4(o[0], u.x, kk), fma4(o[1], u.y, kk), fma4(o[2], u.z, kk), fma4(o[3], u.w, kk);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) *reinterpret_cast<float4 *>(S + (v + j) * l.stride + k) = o[j];
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<float4 *>(S + lies(v + j) * l.stride + k) = o[j];
         }
     }
     __syncthreads();
     if (p.dh0)
-        for (int i = tid; i < w.width * s.K; i += kThreads) {
-            const int v = i / s.K, k = i - v * s.K;
-            p.dh0[state_at + i] = S[v * l.stride + k];
-        }
+        for (int v = tid / 32; v < w.width; v += kThreads / 32)
+            for (int k = tid % 32; k < s.K; k += 32) p.dh0[state_at + v * s.K + k] = S[lies(v) * l.stride + k];
     clear_uncovered(s, w.seq, p.dv + int64_t(w.head) * s.V + w.v0, v_step, w.width);
     if (w.v0 == 0) {
         clear_uncovered(s, w.seq, p.dg + w.head, s.H, 1);
@@ -625,10 +697,24 @@ static cudaError_t room(K kernel, int words) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, words * 4);
 }
 
+int64_t made_bytes(const Shape &s) { return s.slots() * s.H * int64_t(sizeof(Made)); }
+
+template <typename T>
+static cudaError_t make_pairs(const Shape &s, const T *q, const T *k, const T *g, const T *beta, unsigned char *made,
+                              cudaStream_t st) {
+    const int64_t grid = s.slots() * s.H;
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    const auto words = [](int K) { return 2 * kBlock * (stride_of(K) > kPairs ? stride_of(K) : kPairs) + kBlock * kPairs; };
+    if (cudaError_t e = room(pairs_kernel<T>, words(256))) return e;
+    pairs_kernel<T><<<unsigned(grid), kThreads, words(s.K) * 4, st>>>(s, q, k, g, beta, reinterpret_cast<Made *>(made));
+    return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t fwd(const FwdArgs<T> &a, cudaStream_t st) {
     const int64_t grid = int64_t(a.s.n) * a.s.H * slices(a.s);
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    if (cudaError_t e = make_pairs(a.s, a.q, a.k, a.g, a.beta, a.scratch, st)) return e;
     // the limit is the largest layout's, whatever this call takes: calls of several threads cannot lower it
     if (cudaError_t e = room(fwd_kernel<T>, layout_of(256).words)) return e;
     fwd_kernel<T><<<unsigned(grid), kThreads, layout_of(a.s.K).words * 4, st>>>(a);
@@ -647,6 +733,7 @@ template <typename T>
 cudaError_t bwd(const BwdArgs<T> &a, cudaStream_t st) {
     const int64_t grid = int64_t(a.s.n) * a.s.H * slices(a.s), blocks = a.s.slots() * a.s.H;
     if (grid > 0x7fffffff || blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    if (cudaError_t e = make_pairs(a.s, a.q, a.k, a.g, a.beta, a.records, st)) return e;
     if (cudaError_t e = room(back_kernel<T>, layout_of(256).words)) return e;
     if (cudaError_t e = room(grads_kernel<T>, grad_layout_of(256).words)) return e;
     back_kernel<T><<<unsigned(grid), kThreads, layout_of(a.s.K).words * 4, st>>>(a);

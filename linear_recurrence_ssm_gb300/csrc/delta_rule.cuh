@@ -244,6 +244,7 @@ struct BwdArgs {
 };
 namespace general {
 int64_t shares(const Shape &s);
+int64_t made_bytes(const Shape &s);
 template <typename T>
 cudaError_t fold(const BwdArgs<T> &a, cudaStream_t st);
 }
