@@ -32,15 +32,6 @@ struct Layout {
     static_assert(sizeof(Factors) <= 1040 && bytes <= 232448, "shared memory");
 };
 
-__device__ __forceinline__ void put_values(uint32_t at, const float (&v)[4]) {
-    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
-}
-__device__ __forceinline__ float4 get_values(uint32_t at) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
-    return v;
-}
-
 template <int KP>
 __global__ void __launch_bounds__(kThreads, 1) back_kernel(const BwdArgs<bf> p) {
     extern __shared__ __align__(1024) unsigned char mem[];
@@ -174,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) back_kernel(const BwdArgs<bf> p) 
                 for (int k = 0; k < KP / 16; ++k) {
                     uint32_t hi[4], lo[4];
                     operand<KP>(hi, lo, st, k);
-                    store4(four<KP>(room, 0, 16 * k), hi);
+                    store4(four<KP, 16>(room, 0, 16 * k), hi);
                     if (k + 1 < KP / 16)
 #pragma unroll
                         for (int t = 0; t < 4; ++t) load4(b[(k + 1) % 2][t], four_across<KP>(at, 16 * t, 16 * (k + 1)));
@@ -188,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) back_kernel(const BwdArgs<bf> p) 
 #pragma unroll
                 for (int j = 0; j < 16 * KP / 8 / 32; ++j) {
                     const int v = (j * 32 + lane) / (KP / 8), k = (j * 32 + lane) % (KP / 8) * 8;
-                    const uint4 x = load16(place<KP>(room, v, k));
+                    const uint4 x = load16(place<KP, 16>(room, v, k));
                     if (v < width && k < s.K) *reinterpret_cast<uint4 *>(out + int64_t(v) * s.K + k) = x;
                 }
             }
@@ -422,7 +413,8 @@ __global__ void __launch_bounds__(256, VP == 64 ? 2 : 1) block_kernel(const BwdA
         float both = 0.0f;
         for (int i = tid; i < VP * KP / 8; i += 256) {
             const int v = i / (KP / 8), k = i % (KP / 8) * 8;
-            const uint4 a = load16(place<KP>(base + L::s0, v, k)), b = load16(place<KP>(base + L::s1, v, k));
+            const uint32_t at = v / kBlock * (kBlock * KP * 2);
+            const uint4 a = load16(place<KP>(base + L::s0 + at, v % kBlock, k)), b = load16(place<KP>(base + L::s1 + at, v % kBlock, k));
             both += low(a.x) * low(b.x) + high(a.x) * high(b.x) + low(a.y) * low(b.y) + high(a.y) * high(b.y) +
                     low(a.z) * low(b.z) + high(a.z) * high(b.z) + low(a.w) * low(b.w) + high(a.w) * high(b.w);
         }
@@ -444,7 +436,7 @@ __global__ void __launch_bounds__(256, VP == 64 ? 2 : 1) block_kernel(const BwdA
             load4(a, four<64>(base + L::y + v / 4 * L::v, 16 * j, v % 4 * 16));
             load4(z, four<64>(base + L::dv + v / 4 * L::v, 16 * j, v % 4 * 16));
 #pragma unroll
-            for (int n = 0; n < tiles / 2; ++n) load4t(b[n], four<KP>(base + L::s0, 16 * v, k0 + 16 * n));
+            for (int n = 0; n < tiles / 2; ++n) load4t(b[n], four<KP>(base + L::s0 + v / 4 * (kBlock * KP * 2), v % 4 * 16, k0 + 16 * n));
 #pragma unroll
             for (int n = 0; n < tiles / 2; ++n) {
                 product(dq[2 * n], a, b[n][0], b[n][1]);
@@ -532,7 +524,7 @@ __global__ void __launch_bounds__(256, VP == 64 ? 2 : 1) block_kernel(const BwdA
             uint32_t a[4], b[tiles / 2][4];
             load4(a, four<64>(base + L::x + v / 4 * L::v, 16 * j, v % 4 * 16));
 #pragma unroll
-            for (int n = 0; n < tiles / 2; ++n) load4t(b[n], four<KP>(base + L::s1, 16 * v, k0 + 16 * n));
+            for (int n = 0; n < tiles / 2; ++n) load4t(b[n], four<KP>(base + L::s1 + v / 4 * (kBlock * KP * 2), v % 4 * 16, k0 + 16 * n));
 #pragma unroll
             for (int n = 0; n < tiles / 2; ++n) {
                 product(dq[2 * n], a, b[n][0], b[n][1]);

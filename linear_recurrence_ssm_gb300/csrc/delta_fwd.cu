@@ -8,7 +8,10 @@
 // and hand S and U to four more warps, which form the block's outputs while
 // the chain is at the next one:
 //   Y^T = scale Gam (S Q^T) + U^T P^T.
-// N and P come from pairs_kernel.
+// N and P come from pairs_kernel.  One thread asks for the tensor copies of the
+// next block: memory takes its 64 KB slower than warps can ask for them piece by
+// piece (a chain that did so stood still for 1000 of 6300 cycles, its outputs
+// for 3500).
 //
 // Operands of the state's own chain (S, beta W, N, E U) go into the tensor
 // cores as two bf16 terms, 16 bits, so that the final state is good to 2^-17
@@ -28,21 +31,28 @@ template <int KP, bool CARRY>
 struct Layout {
     static constexpr int tile = kBlock * KP * 2, v = kBlock * kSlice * 2;
     static constexpr int chain = tile + v + 2 * kTile;              // K, V, N in two terms: two of them
-    static constexpr int outputs = 2 * chain, output = tile + kTile + 1152;      // Q, P, the factors: three of them
+    static constexpr int outputs = 2 * chain, output = tile + kTile + 2048;      // Q, P, the factors: three of them
     static constexpr int handed = outputs + 3 * output;
     static constexpr int state = 16 * KP * 2, u = 16 * kBlock * 2;  // of a warp
     static constexpr int hand = kChain * (state + 2 * u);           // S, U, X: two of them
-    static constexpr int bytes = CARRY ? 2 * chain + 2 * 1152 : handed + 2 * hand;
-    static_assert(sizeof(Factors) <= 1152 && bytes <= 232448, "shared memory");
+    static constexpr int bytes = CARRY ? 2 * chain + 2 * 2048 : handed + 2 * hand;
+    static_assert(sizeof(Factors) <= 2048 && chain % 1024 == 0 && output % 1024 == 0 && bytes <= 232448 - 1024, "shared memory");
 };
 
 // CARRY: no outputs, only what a part adds to a state and what it makes of one
 // (its rows of the identity: 64 rows of K more slices), by the four warps of
 // the chain alone.
+struct Maps {
+    CUtensorMap q, k, v;
+};
+__device__ unsigned int g_device_error;
+
 template <int KP, bool CARRY>
-__global__ void __launch_bounds__(CARRY ? 32 * kChain : kThreads, CARRY ? 2 : 1) fwd_kernel(const FwdArgs<bf> p) {
+__global__ void __launch_bounds__(CARRY ? 32 * kChain : kThreads, CARRY ? 2 : 1)
+fwd_kernel(const FwdArgs<bf> p, const __grid_constant__ Maps maps) {
     extern __shared__ __align__(1024) unsigned char mem[];
-    __shared__ int found;
+    __shared__ int found, abort;
+    __shared__ __align__(8) uint64_t full[3];
     using L = Layout<KP, CARRY>;
     constexpr int threads = CARRY ? 32 * kChain : kThreads;
     let_next_begin();
@@ -73,32 +83,43 @@ __global__ void __launch_bounds__(CARRY ? 32 * kChain : kThreads, CARRY ? 2 : 1)
     }
     const float *entering = part == 0 ? p.h0 : p.entering;
     const int64_t entering_at = ((part == 0 ? int64_t(seq) : index) * s.H + head) * s.V * s.K;
-    const int64_t qk_step = int64_t(s.G) * s.K, v_step = int64_t(s.H) * s.V;
+    const int64_t v_step = int64_t(s.H) * s.V;
     const int tid = threadIdx.x, warp = tid / 32 % kChain, lane = tid % 32;
     const bool chain = tid < 32 * kChain;
     const int g = lane / 4, c2 = lane % 4 * 2, mine = v0 + 16 * warp;       // rows mine + g, mine + g + 8 of the state
     const int width = height - mine;                                        // of them, may be below 1 or above 16
 
+    // One thread asks for what block c needs: K, V and N for the chain, Q, P and the factors for the outputs.
     const auto copy = [&](int c) {
-        const int64_t row = span.first + int64_t(c) * kBlock;
-        const int rows = min(kBlock, span.len - c * kBlock);
+        const int row = int(span.first + int64_t(c) * kBlock);
         const uint32_t to = base + c % 2 * L::chain;
-        const uint32_t out = base + L::outputs + (CARRY ? c % 2 * 1152 : c % 3 * L::output);
+        const uint32_t out = base + L::outputs + (CARRY ? c % 2 * 2048 : c % 3 * L::output);
         const unsigned char *record = p.scratch + ((span.slot + c) * s.H + head) * kRecord;
-        copy_tile<KP, threads>(to, p.k + row * qk_step + int64_t(group) * s.K, qk_step, rows, s.K, tid);
-        copy_tile<kSlice, threads>(to + L::tile, p.v + row * v_step + int64_t(head) * s.V + (turning ? 0 : v0), v_step,
-                                   turning ? 0 : rows, min(kSlice, s.V - v0), tid);
-#pragma unroll
-        for (int i = 0; i < 2 * kTile / 16 / threads; ++i)
-            copy16(to + L::tile + L::v + (i * threads + tid) * 16, record + (i * threads + tid) * 16);
+        uint64_t *bar = &full[c % 3];
+        constexpr int factors = int(sizeof(Factors));
+        tc::mbar_arrive_expect_tx(bar, L::tile + (turning ? 0 : L::v) + 2 * kTile + (CARRY ? 0 : L::tile + kTile) + factors);
+        boxes<KP>(to, &maps.k, bar, group, row);
+        if (!turning) box(to + L::tile, &maps.v, bar, v0, head, row);
+        bulk(to + L::tile + L::v, record, 2 * kTile, bar);
         if (CARRY) {
-            if (tid < int(sizeof(Factors)) / 16) copy16(out + tid * 16, record + 3 * kTile + tid * 16);
-            return;
+            bulk(out, record + 3 * kTile, factors, bar);
+        } else {
+            boxes<KP>(out, &maps.q, bar, group, row);
+            bulk(out + L::tile, record + 2 * kTile, kTile + factors, bar);
         }
-        copy_tile<KP, threads>(out, p.q + row * qk_step + int64_t(group) * s.K, qk_step, rows, s.K, tid);
-        constexpr int rest = (kTile + int(sizeof(Factors))) / 16;
-        for (int i = tid; i < rest; i += threads) copy16(out + L::tile + i * 16, record + 2 * kTile + i * 16);
     };
+    const bool asks = tid == (CARRY ? 0 : 32 * kChain);
+    if (asks) {
+        abort = 0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) tc::mbar_init(&full[i], 1);
+        tc::mbar_fence_init();
+    }
+    // no values of a part's identity: they are zeros from here on
+    if (turning)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) clear_rows<64>(base + i * L::chain + L::tile, 0, tid, threads);
+    __syncthreads();
     wait_for_last();
     float st[KP / 8][4];
     if (chain) {
@@ -111,20 +132,28 @@ __global__ void __launch_bounds__(CARRY ? 32 * kChain : kThreads, CARRY ? 2 : 1)
                 else st[n][e] = entering && v < width && k < s.K ? entering[entering_at + int64_t(mine + v) * s.K + k] : 0.0f;
             }
     }
-    if (span.blocks > 0) copy(0);
-    cp_async_commit();
+    if (asks && span.blocks > 0) copy(0);
     // the chain is at block c, the outputs at the one before
     for (int c = 0; c < span.blocks + (CARRY ? 0 : 1); ++c) {
-        cp_async_wait<0>();
+        if (c < span.blocks) {
+            wait_for(&full[c % 3], c / 3 & 1, &abort, &g_device_error);
+            const int rows = span.len - c * kBlock;
+            if (rows < kBlock) {
+                const uint32_t to = base + c % 2 * L::chain;
+                clear_rows<KP>(to, rows, tid, threads);
+                clear_rows<64>(to + L::tile, rows, tid, threads);
+                if (!CARRY) clear_rows<KP>(base + L::outputs + c % 3 * L::output, rows, tid, threads);
+            }
+        }
         __syncthreads();
-        if (c + 1 < span.blocks) copy(c + 1);
-        cp_async_commit();
+        if (*reinterpret_cast<volatile int *>(&abort)) break;
+        if (asks && c + 1 < span.blocks) copy(c + 1);
         if (chain) {
             if (c == span.blocks) break;
             const uint32_t at = base + c % 2 * L::chain, hand = base + L::handed + c % 2 * L::hand;
             const uint32_t hand_u = hand + kChain * L::state + warp * L::u, hand_x = hand_u + kChain * L::u;
             const Factors &f = *reinterpret_cast<const Factors *>(
-                mem + L::outputs + (CARRY ? c % 2 * 1152 : c % 3 * L::output + L::tile + kTile));
+                mem + L::outputs + (CARRY ? c % 2 * 2048 : c % 3 * L::output + L::tile + kTile));
             // S K^T: the pieces of K for the next 16 columns are loaded ahead of the products
             float w[8][4] = {};
             {
@@ -135,7 +164,7 @@ __global__ void __launch_bounds__(CARRY ? 32 * kChain : kThreads, CARRY ? 2 : 1)
                 for (int k = 0; k < KP / 16; ++k) {
                     uint32_t hi[4], lo[4];
                     operand<KP>(hi, lo, st, k);
-                    if (!CARRY) store4(four<KP>(hand + warp * L::state, 0, 16 * k), hi);
+                    if (!CARRY) store4(four<KP, 16>(hand + warp * L::state, 0, 16 * k), hi);
                     if (k + 1 < KP / 16)
 #pragma unroll
                         for (int t = 0; t < 4; ++t) load4(b[(k + 1) % 2][t], four_across<KP>(at, 16 * t, 16 * (k + 1)));
@@ -190,7 +219,7 @@ __global__ void __launch_bounds__(CARRY ? 32 * kChain : kThreads, CARRY ? 2 : 1)
                     split(kept(end.x, a), kept(end.y, b), hi[t][2 * h], lo[t][2 * h]);
                     split(kept(end.x, d), kept(end.y, e), hi[t][2 * h + 1], lo[t][2 * h + 1]);
                 }
-                if (!CARRY) store4(four<64>(hand_u, 0, 16 * t), u);
+                if (!CARRY) store4(four<64, 16>(hand_u, 0, 16 * t), u);
             }
             // S
             const float last = f.last;
@@ -213,7 +242,7 @@ __global__ void __launch_bounds__(CARRY ? 32 * kChain : kThreads, CARRY ? 2 : 1)
 #pragma unroll
                 for (int i = 0; i < 16 * KP / 8 / 32; ++i) {
                     const int v = (i * 32 + lane) / (KP / 8), k = (i * 32 + lane) % (KP / 8) * 8;
-                    const uint4 w = load16(place<KP>(hand_s, v, k));
+                    const uint4 w = load16(place<KP, 16>(hand_s, v, k));
                     if (v < width && k < s.K) *reinterpret_cast<uint4 *>(out + int64_t(v) * s.K + k) = w;
                 }
                 write_turned(p.errors + out_at, v_step, rows, width, hand_x);
@@ -222,13 +251,13 @@ __global__ void __launch_bounds__(CARRY ? 32 * kChain : kThreads, CARRY ? 2 : 1)
             float y[8][4] = {};
             {
                 uint32_t b[2][4][4], a[2][4];
-                load4(a[0], four<KP>(hand_s, 0, 0));
+                load4(a[0], four<KP, 16>(hand_s, 0, 0));
 #pragma unroll
                 for (int t = 0; t < 4; ++t) load4(b[0][t], four_across<KP>(at, 16 * t, 0));
 #pragma unroll
                 for (int k = 0; k < KP / 16; ++k) {
                     if (k + 1 < KP / 16) {
-                        load4(a[(k + 1) % 2], four<KP>(hand_s, 0, 16 * (k + 1)));
+                        load4(a[(k + 1) % 2], four<KP, 16>(hand_s, 0, 16 * (k + 1)));
 #pragma unroll
                         for (int t = 0; t < 4; ++t) load4(b[(k + 1) % 2][t], four_across<KP>(at, 16 * t, 16 * (k + 1)));
                     }
@@ -244,7 +273,7 @@ __global__ void __launch_bounds__(CARRY ? 32 * kChain : kThreads, CARRY ? 2 : 1)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 uint32_t u[4], b[4][4];
-                load4(u, four<64>(hand_u, 0, 16 * r));
+                load4(u, four<64, 16>(hand_u, 0, 16 * r));
 #pragma unroll
                 for (int t = r; t < 4; ++t) load4(b[t], four_across<64>(at + L::tile, 16 * t, 16 * r));
                 across(y, u, b, r);
@@ -255,6 +284,11 @@ __global__ void __launch_bounds__(CARRY ? 32 * kChain : kThreads, CARRY ? 2 : 1)
             __syncwarp();
             write_turned(p.y + out_at, v_step, rows, width, hand_x);
         }
+    }
+    if (*reinterpret_cast<volatile int *>(&abort)) {
+        // copies may still be on their way to this block's shared memory
+        if (asks) linger();
+        return;
     }
     float *out = CARRY ? (turning ? p.turned : p.added) : last_part ? p.h_final : nullptr;
     if (chain && out) {
@@ -321,13 +355,13 @@ __global__ void __launch_bounds__(128 * kJoinSplit) join_kernel(const FwdArgs<bf
 static_assert(kJoinRows == kJoinSplit, "a row a quarter");
 
 template <int KP, bool CARRY>
-static cudaError_t go(const FwdArgs<bf> &a, int64_t places, cudaStream_t st) {
+static cudaError_t go(const FwdArgs<bf> &a, const Maps &maps, int64_t places, cudaStream_t st) {
     const int64_t slices = (a.s.V + kSlice - 1) / kSlice + (CARRY ? (a.s.K + kSlice - 1) / kSlice : 0);
     const int64_t grid = places * a.s.H * slices;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     constexpr int bytes = Layout<KP, CARRY>::bytes;
     if (cudaError_t e = allow<fwd_kernel<KP, CARRY>>(bytes)) return e;
-    return launch_behind(fwd_kernel<KP, CARRY>, unsigned(grid), CARRY ? 32 * kChain : kThreads, bytes, st, a);
+    return launch_behind(fwd_kernel<KP, CARRY>, unsigned(grid), CARRY ? 32 * kChain : kThreads, bytes, st, a, maps);
 }
 
 static bool on16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -338,21 +372,27 @@ bool fits(const FwdArgs<bf> &a) {
 }
 
 cudaError_t launch(FwdArgs<bf> a, cudaStream_t st) {
+    Maps maps;
+    if (!map_of(&maps.q, a.q, a.s.rows(), a.s.G, a.s.K) || !map_of(&maps.k, a.k, a.s.rows(), a.s.G, a.s.K) ||
+        !map_of(&maps.v, a.v, a.s.rows(), a.s.H, a.s.V))
+        return cudaErrorInvalidValue;
     if (cudaError_t e = make_pairs(a.s, a.q, a.k, a.g, a.beta, a.scratch, false, st)) return e;
     const FwdScratch at = fwd_scratch(a.s);
     const bool wide = a.s.K > 64;
     a.part = at.part;
-    if (!a.part) return wide ? go<128, false>(a, a.s.n, st) : go<64, false>(a, a.s.n, st);
+    if (!a.part) return wide ? go<128, false>(a, maps, a.s.n, st) : go<64, false>(a, maps, a.s.n, st);
     a.added = reinterpret_cast<float *>(a.scratch + at.added);
     a.turned = reinterpret_cast<float *>(a.scratch + at.turned);
     a.entering = reinterpret_cast<float *>(a.scratch + at.entering);
     const int64_t places = part_places(a.s, a.part);
-    if (cudaError_t e = wide ? go<128, true>(a, places, st) : go<64, true>(a, places, st)) return e;
+    if (cudaError_t e = wide ? go<128, true>(a, maps, places, st) : go<64, true>(a, maps, places, st)) return e;
     if (cudaError_t e = launch_behind(join_kernel, unsigned((a.s.V + kJoinRows - 1) / kJoinRows * a.s.H * a.s.n),
                                       128 * kJoinSplit, 0, st, a))
         return e;
-    return wide ? go<128, false>(a, places, st) : go<64, false>(a, places, st);
+    return wide ? go<128, false>(a, maps, places, st) : go<64, false>(a, maps, places, st);
 }
+
+cudaError_t take_device_error(unsigned int *out) { return take_error(g_device_error, out); }
 
 }  // namespace fwd
 }  // namespace mma

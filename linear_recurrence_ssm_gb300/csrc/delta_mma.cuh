@@ -8,9 +8,13 @@
 // warp's registers, and the warps of the chain never wait for one another.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <atomic>
 
 #include "delta_rule.cuh"
+#include "tc_ptx.cuh"
 
 namespace ssm {
 namespace delta {
@@ -65,25 +69,27 @@ __device__ __forceinline__ void split(float a, float b, uint32_t &hi, uint32_t &
     lo = pack(a - low(hi), b - high(hi));
 }
 
-// Tiles of bf16 in shared memory: rows of WIDTH elements (64 or 128), the
-// 16-byte pieces of a row exchanged by its number, so that eight rows' pieces
-// of one column lie in eight different groups of banks.
-template <int WIDTH>
+// Tiles of bf16 in shared memory, as tensor copies leave them: ROWS rows of 64
+// columns, and for WIDTH = 128 as many again behind them; the 16-byte pieces of
+// a row exchanged by its number, so that eight rows' pieces of one column lie
+// in eight different groups of banks.
+template <int WIDTH, int ROWS = kBlock>
 __device__ __forceinline__ uint32_t place(uint32_t tile, int row, int col) {      // col: a multiple of 8
-    return tile + row * (WIDTH * 2) + (((col >> 3) ^ (row & 7)) << 4);
+    const int half = WIDTH > 64 ? (col >> 6) * (ROWS * 128) : 0;
+    return tile + half + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) << 4);
 }
 // The address that this lane gives for four 8 x 8 pieces: rows r, r + 8 by
 // columns c, c + 8 in the order (r, c), (r + 8, c), (r, c + 8), (r + 8, c + 8).
-template <int WIDTH>
+template <int WIDTH, int ROWS = kBlock>
 __device__ __forceinline__ uint32_t four(uint32_t tile, int r, int c) {
     const int lane = threadIdx.x % 32;
-    return place<WIDTH>(tile, r + (lane & 15), c + (lane >> 4) * 8);
+    return place<WIDTH, ROWS>(tile, r + (lane & 15), c + (lane >> 4) * 8);
 }
 // The same in the order (r, c), (r, c + 8), (r + 8, c), (r + 8, c + 8).
-template <int WIDTH>
+template <int WIDTH, int ROWS = kBlock>
 __device__ __forceinline__ uint32_t four_across(uint32_t tile, int r, int c) {
     const int lane = threadIdx.x % 32;
-    return place<WIDTH>(tile, r + (lane & 7) + (lane >> 4) * 8, c + ((lane >> 3) & 1) * 8);
+    return place<WIDTH, ROWS>(tile, r + (lane & 7) + (lane >> 4) * 8, c + ((lane >> 3) & 1) * 8);
 }
 
 // `rows` rows of `width` elements (a multiple of 8) into a tile of 64 x WIDTH, zeros around them.
@@ -106,6 +112,52 @@ __device__ __forceinline__ uint4 load16(uint32_t at) {
 }
 __device__ __forceinline__ void copy16(uint32_t to, const void *from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(from) : "memory");
+}
+
+__device__ __forceinline__ void put_values(uint32_t at, const float (&v)[4]) {
+    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+}
+__device__ __forceinline__ float4 get_values(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
+// Rows from `rows` on of a 64 x WIDTH tile become 0: a tensor copy brings the
+// next sequence's.
+template <int WIDTH>
+__device__ __forceinline__ void clear_rows(uint32_t tile, int rows, int tid, int threads) {
+    for (int i = tid; i < (kBlock - rows) * WIDTH / 8; i += threads)
+        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(place<WIDTH>(tile, rows + i / (WIDTH / 8), i % (WIDTH / 8) * 8)), "r"(0) : "memory");
+}
+
+// Copies that report to a barrier in shared memory; one thread asks for them.
+__device__ __forceinline__ void box(uint32_t to, const CUtensorMap *map, uint64_t *bar, int col, int head, int row) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(to),
+        "l"(map), "r"(col), "r"(head), "r"(row), "r"(tc::smem_addr(bar))
+        : "memory");
+}
+template <int WIDTH>
+__device__ __forceinline__ void boxes(uint32_t to, const CUtensorMap *map, uint64_t *bar, int head, int row) {
+#pragma unroll
+    for (int c = 0; c < WIDTH; c += 64) box(to + c * kBlock * 2, map, bar, c, head, row);
+}
+__device__ __forceinline__ void bulk(uint32_t to, const void *from, int bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from),
+                 "r"(bytes), "r"(tc::smem_addr(bar))
+                 : "memory");
+}
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+__device__ __forceinline__ void linger() {
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (tc::globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(1000);
+}
+// Waits for a barrier's phase; gives up after the limit, and says so in *abort and *error.
+__device__ __forceinline__ void wait_for(uint64_t *bar, int phase, int *abort, unsigned int *error) {
+    if (tc::mbar_wait_bounded(bar, phase, abort, kWaitLimitNs)) return;
+    *reinterpret_cast<volatile int *>(abort) = 1;
+    atomicOr(error, 1u);
 }
 
 // by v, and 0 for by = 0 whatever v holds.
@@ -381,6 +433,39 @@ cudaError_t allow(int bytes) {
     if (device < 64) known.fetch_or(uint64_t(1) << device, std::memory_order_release);
     return cudaSuccess;
 }
+// Read and clear a unit's error word (host side, synchronous).
+inline cudaError_t take_error(const unsigned int &symbol, unsigned int *out) {
+    unsigned int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, symbol, sizeof(v));
+    if (e == cudaSuccess && v) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(symbol, &zero, sizeof(zero));
+    }
+    *out = v;
+    return e;
+}
+
+// A map of a tensor (rows, heads, cols) for boxes of 64 rows x 64 columns of a
+// head; what lies outside reads as 0.
+inline bool map_of(CUtensorMap *map, const bf *base, int64_t rows, int heads, int cols) {
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> cached{nullptr};
+    PFN_cuTensorMapEncodeTiled_v12000 fn = cached.load(std::memory_order_acquire);
+    if (fn == nullptr) {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return false;
+        fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+        cached.store(fn, std::memory_order_release);
+    }
+    const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(heads), cuuint64_t(rows)};
+    const cuuint64_t strides[2] = {cuuint64_t(cols) * 2, cuuint64_t(cols) * heads * 2};
+    const cuuint32_t box[3] = {64, 1, kBlock}, each[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf *>(base), dims, strides, box, each,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 // A launch that may begin while the kernel before it in the stream runs.
 template <typename... P, typename... A>
 cudaError_t launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, int bytes, cudaStream_t st, A... args) {
@@ -395,7 +480,9 @@ cudaError_t launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads,
 }
 
 // Sizes whose rows 16-byte copies can take, and whose states fit a warp's registers.
-inline bool fits(const Shape &s) { return s.K <= 128 && s.K % 8 == 0 && s.V % 8 == 0; }
+inline bool fits(const Shape &s) {
+    return s.K <= 128 && s.K % 8 == 0 && s.V % 8 == 0 && s.rows() <= 0x7fffffff - kBlock;
+}
 inline int64_t record_bytes(const Shape &s) { return s.slots() * s.H * kRecord; }
 // ... and whose block fits shared memory.
 inline bool fits_bwd(const Shape &s) { return fits(s) && s.V <= 128; }
