@@ -153,26 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) back_kernel(const BwdArgs<bf> p) 
             const uint32_t at = base + from, room = base + L::out + warp * L::out_warp;
             const Factors &f = *reinterpret_cast<const Factors *>(mem + from + L::tile + 2 * kTile + L::v);
             // A K^T
-#pragma unroll
-            for (int n = 0; n < 8; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[n][e] = 0.0f;
-            {
-                uint32_t b[2][4][4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) load4(b[0][t], four_across<KP>(at, 16 * t, 0));
-#pragma unroll
-                for (int k = 0; k < KP / 16; ++k) {
-                    uint32_t hi[4], lo[4];
-                    operand<KP>(hi, lo, st, k);
-                    store4(four<KP, 16>(room, 0, 16 * k), hi);
-                    if (k + 1 < KP / 16)
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) load4(b[(k + 1) % 2][t], four_across<KP>(at, 16 * t, 16 * (k + 1)));
-                    across(w, hi, b[k % 2]);
-                    across(w, lo, b[k % 2]);
-                }
-            }
+            through_tile<KP>(w, st, at, [&](int k, const uint32_t(&hi)[4]) { store4(four<KP, 16>(room, 0, 16 * k), hi); });
             __syncwarp();
             {
                 bf *out = p.ds + ((span.slot + c) * s.H + head) * int64_t(s.V) * s.K + int64_t(mine) * s.K;

@@ -154,24 +154,12 @@ fwd_kernel(const FwdArgs<bf> p, const __grid_constant__ Maps maps) {
             const uint32_t hand_u = hand + kChain * L::state + warp * L::u, hand_x = hand_u + kChain * L::u;
             const Factors &f = *reinterpret_cast<const Factors *>(
                 mem + L::outputs + (CARRY ? c % 2 * 2048 : c % 3 * L::output + L::tile + kTile));
-            // S K^T: the pieces of K for the next 16 columns are loaded ahead of the products
-            float w[8][4] = {};
-            {
-                uint32_t b[2][4][4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) load4(b[0][t], four_across<KP>(at, 16 * t, 0));
-#pragma unroll
-                for (int k = 0; k < KP / 16; ++k) {
-                    uint32_t hi[4], lo[4];
-                    operand<KP>(hi, lo, st, k);
-                    if (!CARRY) store4(four<KP, 16>(hand + warp * L::state, 0, 16 * k), hi);
-                    if (k + 1 < KP / 16)
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) load4(b[(k + 1) % 2][t], four_across<KP>(at, 16 * t, 16 * (k + 1)));
-                    across(w, hi, b[k % 2]);
-                    across(w, lo, b[k % 2]);
-                }
-            }
+            float w[8][4];
+            through_tile<KP>(w, st, at, [&](int k, const uint32_t(&hi)[4]) {
+                if (!CARRY) store4(four<KP, 16>(hand + warp * L::state, 0, 16 * k), hi);
+            });
+            // from here on the tensor cores have room for the outputs
+            if (!CARRY && c > 0) asm volatile("bar.arrive 1, 256;" ::: "memory");
             // W, beta W as two terms, and X in W's place
             uint32_t hi[4][4], lo[4][4];
 #pragma unroll
@@ -248,6 +236,8 @@ fwd_kernel(const FwdArgs<bf> p, const __grid_constant__ Maps maps) {
                 write_turned(p.errors + out_at, v_step, rows, width, hand_x);
                 __syncwarp();
             }
+            // not before the chain is through its first products, which all else waits for
+            if (c < span.blocks) asm volatile("bar.sync 1, 256;" ::: "memory");
             float y[8][4] = {};
             {
                 uint32_t b[2][4][4], a[2][4];

@@ -193,6 +193,44 @@ __device__ __forceinline__ void operand(uint32_t (&hi)[4], uint32_t (&lo)[4], co
     }
 }
 
+// w = st tile^T, 16 x 64: 16 columns of the state at a time, as an operand of
+// two terms whose first term `use` gets as well.  The pieces of the tile and the
+// terms of the next 16 columns are made between the products of these.
+template <int KP, typename Use>
+__device__ __forceinline__ void through_tile(float (&w)[8][4], const float (&st)[KP / 8][4], uint32_t tile, Use use) {
+    uint32_t b[2][4][4], hi[2][4], lo[2][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) load4(b[0][t], four_across<KP>(tile, 16 * t, 0));
+    operand<KP>(hi[0], lo[0], st, 0);
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[n][e] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < KP / 16; ++k) {
+        const int now = k % 2, next = 1 - now;
+        const bool more = k + 1 < KP / 16;
+        if (more)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) load4(b[next][t], four_across<KP>(tile, 16 * t, 16 * (k + 1)));
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            product(w[2 * t], hi[now], b[now][t][0], b[now][t][1]);
+            product(w[2 * t + 1], hi[now], b[now][t][2], b[now][t][3]);
+            if (more) {
+                const float(&s)[4] = st[2 * (k + 1) + t / 2];
+                split(s[t % 2 * 2], s[t % 2 * 2 + 1], hi[next][t], lo[next][t]);
+            }
+        }
+        use(k, hi[now]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            product(w[2 * t], lo[now], b[now][t][0], b[now][t][1]);
+            product(w[2 * t + 1], lo[now], b[now][t][2], b[now][t][3]);
+        }
+    }
+}
+
 // The state's 16 rows += (hi + lo) times the 64 x KP tile; a tile's pieces are
 // loaded ahead of the products before them.
 template <int KP>
