@@ -16,6 +16,8 @@ namespace general {
 
 constexpr int kSlice = 32, kThreads = 256;
 constexpr int kPairs = kBlock + 4, kRow = kSlice + 4;      // row strides, in floats
+// Rows of the state that a thread block of the chains has, SL: 32, or 16 where
+// that leaves SMs without one (a block of 64 steps takes about half as long).
 
 __host__ __device__ inline int padded(int K) { return (K + 3) / 4 * 4; }
 __host__ __device__ inline int stride_of(int K) { return padded(K) + 4; }
@@ -78,21 +80,24 @@ __device__ __forceinline__ void products(float (&out)[4][4], const float *a, con
 
 // Where row v of the state lies: a thread reads four neighbours, and the eight
 // threads beside it the next ones, which so lie in different banks.
-__device__ __forceinline__ int lies(int v) { return v % 4 * (kSlice / 4) + v / 4; }
+template <int SL>
+__device__ __forceinline__ int lies(int v) { return v % 4 * (SL / 4) + v / 4; }
 
-// Rows t and t + 32 of `a` times four rows v.. of the state: out[i][j] = a_(t + 32 i) . S_(v + j).
-__device__ __forceinline__ void through_state(float (&out)[2][4], const float *a, const float *S, int stride, int Kp,
+// Rows t (and t + 32 of 32-row slices) of `a` times four rows v.. of the state: out[i][j] = a_(t + 32 i) . S_(v + j).
+template <int SL, int R>
+__device__ __forceinline__ void through_state(float (&out)[R][4], const float *a, const float *S, int stride, int Kp,
                                               int t, int v) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) out[i / 4][i % 4] = 0.0f;
+    for (int i = 0; i < 4 * R; ++i) out[i / 4][i % 4] = 0.0f;
+#pragma unroll 2
     for (int k = 0; k < Kp; k += 4) {
-        float4 u[2], w[4];
+        float4 u[R], w[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) u[i] = *reinterpret_cast<const float4 *>(a + (t + 32 * i) * stride + k);
+        for (int i = 0; i < R; ++i) u[i] = *reinterpret_cast<const float4 *>(a + (t + 32 * i) * stride + k);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const float4 *>(S + (j * (kSlice / 4) + v / 4) * stride + k);
+        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const float4 *>(S + (j * (SL / 4) + v / 4) * stride + k);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 out[i][j] += u[i].x * w[j].x + u[i].y * w[j].y + u[i].z * w[j].z + u[i].w * w[j].w;
@@ -208,19 +213,20 @@ __device__ __forceinline__ void load_made(Decays &d, const Decays &from) {
 struct Work {
     int seq, head, group, v0, width;
 };
+template <int SL>
 __device__ __forceinline__ Work work_of(const Shape &s) {
-    const int slices = (s.V + kSlice - 1) / kSlice;
+    const int slices = (s.V + SL - 1) / SL;
     const int64_t at = blockIdx.x;
     Work w;
-    w.v0 = int(at % slices) * kSlice;
+    w.v0 = int(at % slices) * SL;
     w.head = int(at / slices % s.H);
     w.seq = int(at / slices / s.H);
     w.group = w.head / (s.H / s.G);
-    w.width = min(kSlice, s.V - w.v0);
+    w.width = min(SL, s.V - w.v0);
     return w;
 }
 
-template <typename T>
+template <typename T, int SL>
 __global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdArgs<T> p) {
     extern __shared__ __align__(16) float mem[];
     __shared__ Decays d;
@@ -228,22 +234,23 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdArgs<T> p) {
     const Layout l = layout_of(s.K);
     float *Q = mem + l.q, *Kt = mem + l.k, *S = mem + l.s, *A = mem + l.a, *P = mem + l.p, *W = mem + l.w;
     const int Kp = padded(s.K), tid = threadIdx.x;
-    const Work w = work_of(s);
+    const Work w = work_of<SL>(s);
+    constexpr int R = SL / 16;      // rows of a thread: t0, t0 + 32
     const Span span = span_of(s, w.seq);
     const int64_t qk_step = int64_t(s.G) * s.K, v_step = int64_t(s.H) * s.V;
     const int64_t state_at = (int64_t(w.seq) * s.H + w.head) * s.V * s.K + int64_t(w.v0) * s.K;
 
-    for (int v = tid / 32; v < kSlice; v += kThreads / 32)
+    for (int v = tid / 32; v < SL; v += kThreads / 32)
         for (int k = tid % 32; k < Kp; k += 32)
-            S[lies(v) * l.stride + k] = p.h0 && v < w.width && k < s.K ? p.h0[state_at + int64_t(v) * s.K + k] : 0.0f;
-    const int t0 = tid / 8, v4 = tid % 8 * 4;
+            S[lies<SL>(v) * l.stride + k] = p.h0 && v < w.width && k < s.K ? p.h0[state_at + int64_t(v) * s.K + k] : 0.0f;
+    const int t0 = tid / (SL / 4), v4 = tid % (SL / 4) * 4;
     for (int c = 0; c < span.blocks; ++c) {
         const int rows = min(kBlock, span.len - c * kBlock);
         const int64_t row = span.first + int64_t(c) * kBlock;
         __syncthreads();
         load_tile(Q, l.stride, p.q + row * qk_step + int64_t(w.group) * s.K, qk_step, rows, s.K, Kp);
         load_tile(Kt, l.stride, p.k + row * qk_step + int64_t(w.group) * s.K, qk_step, rows, s.K, Kp);
-        load_tile(W, kRow, p.v + row * v_step + int64_t(w.head) * s.V + w.v0, v_step, rows, w.width, kSlice);
+        load_tile(W, kRow, p.v + row * v_step + int64_t(w.head) * s.V + w.v0, v_step, rows, w.width, SL);
         const Made &made = reinterpret_cast<const Made *>(p.scratch)[(span.slot + c) * s.H + w.head];
         load_made(d, made.d);
         load_pairs(A, made.n);
@@ -252,15 +259,15 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdArgs<T> p) {
         if (p.states) {
             T *out = p.states + ((span.slot + c) * s.H + w.head) * int64_t(s.V) * s.K + int64_t(w.v0) * s.K;
             for (int v = tid / 32; v < w.width; v += kThreads / 32)
-                for (int k = tid % 32; k < s.K; k += 32) put(out + v * s.K + k, S[lies(v) * l.stride + k]);
+                for (int k = tid % 32; k < s.K; k += 32) put(out + v * s.K + k, S[lies<SL>(v) * l.stride + k]);
         }
-        float from[2][4], y[2][4];
-        through_state(from, Kt, S, l.stride, Kp, t0, v4);
-        through_state(y, Q, S, l.stride, Kp, t0, v4);
+        float from[R][4], y[R][4];
+        through_state<SL, R>(from, Kt, S, l.stride, Kp, t0, v4);
+        through_state<SL, R>(y, Q, S, l.stride, Kp, t0, v4);
         // W, and beta W beside it
         float *U = mem + l.x;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < R; ++i) {
             const int t = t0 + 32 * i;
             const float start = d.start(t), beta = d.beta[t];
 #pragma unroll
@@ -275,7 +282,7 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdArgs<T> p) {
         __syncthreads();
         // X
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < R; ++i) {
             const int t = t0 + 32 * i;
             float4 o = make_float4(from[i][0], from[i][1], from[i][2], from[i][3]);
 #pragma unroll 4
@@ -289,11 +296,11 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdArgs<T> p) {
                 if (tid % 32 < w.width) put(out + t * v_step + tid % 32, W[t * kRow + tid % 32]);
             __syncthreads();
         }
-        for (int i = tid; i < kBlock * kSlice; i += kThreads) W[i / kSlice * kRow + i % kSlice] *= d.beta[i / kSlice];
+        for (int i = tid; i < kBlock * SL; i += kThreads) W[i / SL * kRow + i % SL] *= d.beta[i / SL];
         __syncthreads();
         // outputs of rows t0 and t0 + 32, four columns
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < R; ++i) {
             const int t = t0 + 32 * i;
             float4 o = make_float4(y[i][0], y[i][1], y[i][2], y[i][3]);
 #pragma unroll 4
@@ -308,14 +315,14 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdArgs<T> p) {
         }
         const float last = d.start(kBlock - 1);
         __syncthreads();
-        for (int i = tid; i < kBlock * kSlice; i += kThreads) W[i / kSlice * kRow + i % kSlice] *= d.end(i / kSlice);
+        for (int i = tid; i < kBlock * SL; i += kThreads) W[i / SL * kRow + i % SL] *= d.end(i / SL);
         __syncthreads();
-        for (int i = tid; i < kSlice / 4 * (Kp / 4); i += kThreads) {
-            const int v = i % (kSlice / 4) * 4, k = i / (kSlice / 4) * 4;
+        for (int i = tid; i < SL / 4 * (Kp / 4); i += kThreads) {
+            const int v = i % (SL / 4) * 4, k = i / (SL / 4) * 4;
             float4 o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                o[j] = *reinterpret_cast<const float4 *>(S + lies(v + j) * l.stride + k);
+                o[j] = *reinterpret_cast<const float4 *>(S + lies<SL>(v + j) * l.stride + k);
                 o[j] = last == 0.0f ? make_float4(0, 0, 0, 0)
                                     : make_float4(last * o[j].x, last * o[j].y, last * o[j].z, last * o[j].w);
             }
@@ -326,19 +333,19 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdArgs<T> p) {
                 fma4(o[0], u.x, kk), fma4(o[1], u.y, kk), fma4(o[2], u.z, kk), fma4(o[3], u.w, kk);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) *reinterpret_cast<float4 *>(S + lies(v + j) * l.stride + k) = o[j];
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<float4 *>(S + lies<SL>(v + j) * l.stride + k) = o[j];
         }
     }
     __syncthreads();
     if (p.h_final)
         for (int v = tid / 32; v < w.width; v += kThreads / 32)
-            for (int k = tid % 32; k < s.K; k += 32) p.h_final[state_at + v * s.K + k] = S[lies(v) * l.stride + k];
+            for (int k = tid % 32; k < s.K; k += 32) p.h_final[state_at + v * s.K + k] = S[lies<SL>(v) * l.stride + k];
     clear_uncovered(s, w.seq, p.y + int64_t(w.head) * s.V + w.v0, v_step, w.width);
 }
 
 // Back along a sequence: dv, the shares of dbeta, the adjoint of every
 // block's last state (into the scratch) and of the first one.
-template <typename T>
+template <typename T, int SL>
 __global__ void __launch_bounds__(kThreads) back_kernel(const BwdArgs<T> p) {
     extern __shared__ __align__(16) float mem[];
     __shared__ Decays d;
@@ -347,25 +354,26 @@ __global__ void __launch_bounds__(kThreads) back_kernel(const BwdArgs<T> p) {
     float *Q = mem + l.q, *Kt = mem + l.k, *S = mem + l.s, *A = mem + l.a, *P = mem + l.p, *Y = mem + l.w,
           *Z = mem + l.x;
     const int Kp = padded(s.K), tid = threadIdx.x;
-    const Work w = work_of(s);
+    const Work w = work_of<SL>(s);
+    constexpr int R = SL / 16;      // rows of a thread: t0, t0 + 32
     const Span span = span_of(s, w.seq);
     const int64_t qk_step = int64_t(s.G) * s.K, v_step = int64_t(s.H) * s.V;
     const int64_t state_at = (int64_t(w.seq) * s.H + w.head) * s.V * s.K + int64_t(w.v0) * s.K;
     const int64_t rows_all = s.offsets ? s.L : s.L * s.n;
-    float *part = p.dbeta_part + int64_t(w.v0 / kSlice) * rows_all * s.H + w.head;
+    float *part = p.dbeta_part + int64_t(w.v0 / SL) * rows_all * s.H + w.head;
 
-    for (int v = tid / 32; v < kSlice; v += kThreads / 32)
+    for (int v = tid / 32; v < SL; v += kThreads / 32)
         for (int k = tid % 32; k < Kp; k += 32)
-            S[lies(v) * l.stride + k] =
+            S[lies<SL>(v) * l.stride + k] =
                 p.dh_final && v < w.width && k < s.K ? p.dh_final[state_at + int64_t(v) * s.K + k] : 0.0f;
-    const int t0 = tid / 8, v4 = tid % 8 * 4;
+    const int t0 = tid / (SL / 4), v4 = tid % (SL / 4) * 4;
     for (int c = span.blocks - 1; c >= 0; --c) {
         const int rows = min(kBlock, span.len - c * kBlock);
         const int64_t row = span.first + int64_t(c) * kBlock;
         __syncthreads();
         load_tile(Q, l.stride, p.q + row * qk_step + int64_t(w.group) * s.K, qk_step, rows, s.K, Kp);
         load_tile(Kt, l.stride, p.k + row * qk_step + int64_t(w.group) * s.K, qk_step, rows, s.K, Kp);
-        load_tile(Y, kRow, p.dy + row * v_step + int64_t(w.head) * s.V + w.v0, v_step, rows, w.width, kSlice);
+        load_tile(Y, kRow, p.dy + row * v_step + int64_t(w.head) * s.V + w.v0, v_step, rows, w.width, SL);
         const Made &made = reinterpret_cast<const Made *>(p.records)[(span.slot + c) * s.H + w.head];
         load_made(d, made.d);
         load_pairs(A, made.n);
@@ -373,13 +381,13 @@ __global__ void __launch_bounds__(kThreads) back_kernel(const BwdArgs<T> p) {
         __syncthreads();
         T *ds = p.ds + ((span.slot + c) * s.H + w.head) * int64_t(s.V) * s.K + int64_t(w.v0) * s.K;
         for (int v = tid / 32; v < w.width; v += kThreads / 32)
-            for (int k = tid % 32; k < s.K; k += 32) put(ds + v * s.K + k, S[lies(v) * l.stride + k]);
-        float from[2][4];
-        through_state(from, Kt, S, l.stride, Kp, t0, v4);
+            for (int k = tid % 32; k < s.K; k += 32) put(ds + v * s.K + k, S[lies<SL>(v) * l.stride + k]);
+        float from[R][4];
+        through_state<SL, R>(from, Kt, S, l.stride, Kp, t0, v4);
         // dU, and beta dU beside it
-        float4 du[2];
+        float4 du[R];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < R; ++i) {
             const int t = t0 + 32 * i;
             const float end = d.end(t), beta = d.beta[t];
             float4 o = end == 0.0f ? make_float4(0, 0, 0, 0)
@@ -392,7 +400,7 @@ __global__ void __launch_bounds__(kThreads) back_kernel(const BwdArgs<T> p) {
         __syncthreads();
         // Z
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < R; ++i) {
             const int t = t0 + 32 * i;
 #pragma unroll 4
             for (int r = t + 1; r < rows; ++r)
@@ -400,7 +408,7 @@ __global__ void __launch_bounds__(kThreads) back_kernel(const BwdArgs<T> p) {
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 2; ++i) *reinterpret_cast<float4 *>(Z + (t0 + 32 * i) * kRow + v4) = du[i];
+        for (int i = 0; i < R; ++i) *reinterpret_cast<float4 *>(Z + (t0 + 32 * i) * kRow + v4) = du[i];
         __syncthreads();
         // a warp takes a row at a time: dbeta's share, dv, and beta Z in Z's place
         {
@@ -423,12 +431,12 @@ __global__ void __launch_bounds__(kThreads) back_kernel(const BwdArgs<T> p) {
         }
         const float last = d.start(kBlock - 1);
         __syncthreads();
-        for (int i = tid; i < kSlice / 4 * (Kp / 4); i += kThreads) {
-            const int v = i % (kSlice / 4) * 4, k = i / (kSlice / 4) * 4;
+        for (int i = tid; i < SL / 4 * (Kp / 4); i += kThreads) {
+            const int v = i % (SL / 4) * 4, k = i / (SL / 4) * 4;
             float4 o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                o[j] = *reinterpret_cast<const float4 *>(S + lies(v + j) * l.stride + k);
+                o[j] = *reinterpret_cast<const float4 *>(S + lies<SL>(v + j) * l.stride + k);
                 o[j] = last == 0.0f ? make_float4(0, 0, 0, 0)
                                     : make_float4(last * o[j].x, last * o[j].y, last * o[j].z, last * o[j].w);
             }
@@ -442,13 +450,13 @@ __global__ void __launch_bounds__(kThreads) back_kernel(const BwdArgs<T> p) {
                 fma4(o[0], u.x, kk), fma4(o[1], u.y, kk), fma4(o[2], u.z, kk), fma4(o[3], u.w, kk);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) *reinterpret_cast<float4 *>(S + lies(v + j) * l.stride + k) = o[j];
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<float4 *>(S + lies<SL>(v + j) * l.stride + k) = o[j];
         }
     }
     __syncthreads();
     if (p.dh0)
         for (int v = tid / 32; v < w.width; v += kThreads / 32)
-            for (int k = tid % 32; k < s.K; k += 32) p.dh0[state_at + v * s.K + k] = S[lies(v) * l.stride + k];
+            for (int k = tid % 32; k < s.K; k += 32) p.dh0[state_at + v * s.K + k] = S[lies<SL>(v) * l.stride + k];
     clear_uncovered(s, w.seq, p.dv + int64_t(w.head) * s.V + w.v0, v_step, w.width);
     if (w.v0 == 0) {
         clear_uncovered(s, w.seq, p.dg + w.head, s.H, 1);
@@ -482,7 +490,7 @@ __host__ __device__ inline GradLayout grad_layout_of(int K) {
 
 // dq, dk, dg and dbeta of one block of one head.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) grads_kernel(const BwdArgs<T> p) {
+__global__ void __launch_bounds__(kThreads) grads_kernel(const BwdArgs<T> p, const int shares) {
     extern __shared__ __align__(16) float mem[];
     __shared__ Decays d;
     __shared__ int found;
@@ -662,9 +670,8 @@ __global__ void __launch_bounds__(kThreads) grads_kernel(const BwdArgs<T> p) {
         for (int r = tid; r < rows; ++r) sum += row_term[r] + M[r * (kBlock + 1) + tid];
         for (int r = 0; r < tid; ++r) sum += col_term[r];
         put(p.dg + (row + tid) * s.H + head, sum);
-        const int slices = (s.V + kSlice - 1) / kSlice;
         float b = 0.0f;
-        for (int i = 0; i < slices; ++i) b += p.dbeta_part[(int64_t(i) * rows_all + row + tid) * s.H + head];
+        for (int i = 0; i < shares; ++i) b += p.dbeta_part[(int64_t(i) * rows_all + row + tid) * s.H + head];
         put(p.dbeta + (row + tid) * s.H + head, b);
     }
 }
@@ -689,8 +696,10 @@ __global__ void __launch_bounds__(kThreads) fold_kernel(const BwdArgs<T> p) {
     put(p.dk + i, kk);
 }
 
-static int slices(const Shape &s) { return (s.V + kSlice - 1) / kSlice; }
-int64_t shares(const Shape &s) { return int64_t(slices(s)) * s.rows() * s.H; }
+static int slices(const Shape &s, int rows) { return (s.V + rows - 1) / rows; }
+// 16 rows a thread block where 32 would leave some of the 152 SMs idle.
+static int rows_of(const Shape &s) { return int64_t(s.n) * s.H * slices(s, 32) < 152 ? 16 : 32; }
+int64_t shares(const Shape &s) { return slices(s, rows_of(s)) * s.rows() * s.H; }
 
 template <typename K>
 static cudaError_t room(K kernel, int words) {
@@ -710,15 +719,20 @@ static cudaError_t make_pairs(const Shape &s, const T *q, const T *k, const T *g
     return cudaGetLastError();
 }
 
+template <typename T, int SL>
+static cudaError_t go(const FwdArgs<T> &a, unsigned grid, cudaStream_t st) {
+    // the limit is the largest layout's, whatever this call takes: calls of several threads cannot lower it
+    if (cudaError_t e = room(fwd_kernel<T, SL>, layout_of(256).words)) return e;
+    fwd_kernel<T, SL><<<grid, kThreads, layout_of(a.s.K).words * 4, st>>>(a);
+    return cudaGetLastError();
+}
 template <typename T>
 cudaError_t fwd(const FwdArgs<T> &a, cudaStream_t st) {
-    const int64_t grid = int64_t(a.s.n) * a.s.H * slices(a.s);
+    const int each = rows_of(a.s);
+    const int64_t grid = int64_t(a.s.n) * a.s.H * slices(a.s, each);
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     if (cudaError_t e = make_pairs(a.s, a.q, a.k, a.g, a.beta, a.scratch, st)) return e;
-    // the limit is the largest layout's, whatever this call takes: calls of several threads cannot lower it
-    if (cudaError_t e = room(fwd_kernel<T>, layout_of(256).words)) return e;
-    fwd_kernel<T><<<unsigned(grid), kThreads, layout_of(a.s.K).words * 4, st>>>(a);
-    return cudaGetLastError();
+    return each == 16 ? go<T, 16>(a, unsigned(grid), st) : go<T, 32>(a, unsigned(grid), st);
 }
 
 template <typename T>
@@ -729,16 +743,21 @@ cudaError_t fold(const BwdArgs<T> &a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+template <typename T, int SL>
+static cudaError_t go(const BwdArgs<T> &a, unsigned grid, cudaStream_t st) {
+    if (cudaError_t e = room(back_kernel<T, SL>, layout_of(256).words)) return e;
+    back_kernel<T, SL><<<grid, kThreads, layout_of(a.s.K).words * 4, st>>>(a);
+    return cudaGetLastError();
+}
 template <typename T>
 cudaError_t bwd(const BwdArgs<T> &a, cudaStream_t st) {
-    const int64_t grid = int64_t(a.s.n) * a.s.H * slices(a.s), blocks = a.s.slots() * a.s.H;
+    const int each = rows_of(a.s);
+    const int64_t grid = int64_t(a.s.n) * a.s.H * slices(a.s, each), blocks = a.s.slots() * a.s.H;
     if (grid > 0x7fffffff || blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     if (cudaError_t e = make_pairs(a.s, a.q, a.k, a.g, a.beta, a.records, st)) return e;
-    if (cudaError_t e = room(back_kernel<T>, layout_of(256).words)) return e;
     if (cudaError_t e = room(grads_kernel<T>, grad_layout_of(256).words)) return e;
-    back_kernel<T><<<unsigned(grid), kThreads, layout_of(a.s.K).words * 4, st>>>(a);
-    if (cudaError_t e = cudaGetLastError()) return e;
-    grads_kernel<T><<<unsigned(blocks), kThreads, grad_layout_of(a.s.K).words * 4, st>>>(a);
+    if (cudaError_t e = each == 16 ? go<T, 16>(a, unsigned(grid), st) : go<T, 32>(a, unsigned(grid), st)) return e;
+    grads_kernel<T><<<unsigned(blocks), kThreads, grad_layout_of(a.s.K).words * 4, st>>>(a, slices(a.s, each));
     if (cudaError_t e = cudaGetLastError()) return e;
     return a.s.H > a.s.G ? fold(a, st) : cudaSuccess;
 }
