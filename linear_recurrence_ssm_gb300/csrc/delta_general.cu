@@ -26,6 +26,12 @@ __device__ __forceinline__ void fma4(float4 &o, float a, const float4 &b) {
     o.x += a * b.x, o.y += a * b.y, o.z += a * b.z, o.w += a * b.w;
 }
 
+// What load_tile, load_pairs and load_made asked for has come, for this thread.
+__device__ __forceinline__ void arrived() {
+    cp_async_commit();
+    cp_async_wait<0>();
+}
+
 // Four elements of a row, `left` of them there.
 template <typename T>
 __device__ __forceinline__ float4 four_of(const T *p, int left, bool vectors) {
@@ -45,6 +51,17 @@ __device__ __forceinline__ void load_tile(float *tile, int stride, const T *src,
                                           int cols) {
     const bool vectors = on_vectors(src, step);
     const int col = threadIdx.x % 16 * 4;
+    if constexpr (sizeof(T) == 4)
+        if (vectors && width % 4 == 0) {        // asynchronous: the caller waits
+            for (int c = col; c < cols; c += 64)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = threadIdx.x / 16 + 16 * i;
+                    const bool in = t < rows && c < width;
+                    cp_async16(tile + t * stride + c, in ? src + t * step + c : src, in ? 16 : 0);
+                }
+            return;
+        }
     float4 v[4];
     for (int c = col; c < cols; c += 64) {
 #pragma unroll
@@ -148,6 +165,7 @@ __global__ void __launch_bounds__(kThreads) pairs_kernel(const Shape s, const T 
     load_tile(Q, stride, q + row * step + int64_t(group) * s.K, step, rows, s.K, Kp);
     load_tile(Kt, stride, k + row * step + int64_t(group) * s.K, step, rows, s.K, Kp);
     if (tid < 32) load_decays(d, g + row * s.H + head, beta + row * s.H + head, s.H, rows);
+    arrived();
     __syncthreads();
     for (int i = tid; i < int(sizeof(Decays) / 4); i += kThreads)
         reinterpret_cast<float *>(&out.d)[i] = reinterpret_cast<const float *>(&d)[i];
@@ -202,12 +220,13 @@ __global__ void __launch_bounds__(kThreads) pairs_kernel(const Shape s, const T 
 // N (or P) and the decays of a block, into shared memory.
 __device__ __forceinline__ void load_pairs(float *tile, const float *from) {
     for (int i = threadIdx.x; i < kBlock * kBlock / 4; i += kThreads)
-        *reinterpret_cast<float4 *>(tile + i / 16 * kPairs + i % 16 * 4) = reinterpret_cast<const float4 *>(from)[i];
+        cp_async16(tile + i / 16 * kPairs + i % 16 * 4, from + 4 * i, 16);
 }
 __device__ __forceinline__ void load_made(Decays &d, const Decays &from) {
     for (int i = threadIdx.x; i < int(sizeof(Decays) / 16); i += kThreads)
-        reinterpret_cast<float4 *>(&d)[i] = reinterpret_cast<const float4 *>(&from)[i];
+        cp_async16(reinterpret_cast<float4 *>(&d) + i, reinterpret_cast<const float4 *>(&from) + i, 16);
 }
+
 
 // Which head, sequence and rows of the state a thread block has.
 struct Work {
@@ -255,6 +274,7 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdArgs<T> p) {
         load_made(d, made.d);
         load_pairs(A, made.n);
         load_pairs(P, made.p);
+        arrived();
         __syncthreads();
         if (p.states) {
             T *out = p.states + ((span.slot + c) * s.H + w.head) * int64_t(s.V) * s.K + int64_t(w.v0) * s.K;
@@ -378,6 +398,7 @@ __global__ void __launch_bounds__(kThreads) back_kernel(const BwdArgs<T> p) {
         load_made(d, made.d);
         load_pairs(A, made.n);
         load_pairs(P, made.p);
+        arrived();
         __syncthreads();
         T *ds = p.ds + ((span.slot + c) * s.H + w.head) * int64_t(s.V) * s.K + int64_t(w.v0) * s.K;
         for (int v = tid / 32; v < w.width; v += kThreads / 32)
@@ -512,6 +533,7 @@ __global__ void __launch_bounds__(kThreads) grads_kernel(const BwdArgs<T> p, con
     load_tile(Kt, l.stride, p.k + row * qk_step + int64_t(group) * s.K, qk_step, rows, s.K, Kp);
     if (tid < 32) load_decays(d, p.g + row * s.H + head, p.beta + row * s.H + head, s.H, rows);
     if (tid < kBlock) row_term[tid] = col_term[tid] = 0.0f;
+    arrived();
     const T *st0 = p.states + (slot * s.H + head) * int64_t(s.V) * s.K;
     const T *st1 = p.ds + (slot * s.H + head) * int64_t(s.V) * s.K;
 
