@@ -120,6 +120,7 @@ bool fits(const FwdArgs<__nv_bfloat16> &a);
 cudaError_t launch(FwdArgs<__nv_bfloat16> a, cudaStream_t st);
 }
 namespace bwd {
+cudaError_t take_device_error(unsigned int *out);
 bool fits(const BwdArgs<__nv_bfloat16> &a);
 cudaError_t launch(const BwdArgs<__nv_bfloat16> &a, cudaStream_t st);
 }
@@ -1040,13 +1041,15 @@ ssm_status_t ssm_check_device_errors(void *stream) {
     ssm_status_t s = current_device(&dev);
     if (s != SSM_OK) return s;
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return SSM_ERR_CUDA;
-    unsigned int flag = 0, flag_bi = 0, flag_g = 0, flag_gb = 0, flag_d = 0;
+    unsigned int flag = 0, flag_bi = 0, flag_g = 0, flag_gb = 0, flag_d = 0, flag_dp = 0, flag_db = 0;
     if (ssm::ssd::take_device_error(&flag) != cudaSuccess) return SSM_ERR_CUDA;
     if (ssm::bidir::take_device_error(&flag_bi) != cudaSuccess) return SSM_ERR_CUDA;
     if (ssm::gated::take_device_error(&flag_g) != cudaSuccess) return SSM_ERR_CUDA;
     if (ssm::gated_bwd::take_device_error(&flag_gb) != cudaSuccess) return SSM_ERR_CUDA;
     if (ssm::delta::mma::fwd::take_device_error(&flag_d) != cudaSuccess) return SSM_ERR_CUDA;
-    return (flag | flag_bi | flag_g | flag_gb | flag_d) ? SSM_ERR_DEVICE_TIMEOUT : SSM_OK;
+    if (ssm::delta::mma::take_device_error(&flag_dp) != cudaSuccess) return SSM_ERR_CUDA;
+    if (ssm::delta::mma::bwd::take_device_error(&flag_db) != cudaSuccess) return SSM_ERR_CUDA;
+    return (flag | flag_bi | flag_g | flag_gb | flag_d | flag_dp | flag_db) ? SSM_ERR_DEVICE_TIMEOUT : SSM_OK;
 }
 
 ssm_status_t ssm_selftest_wait_timeout(void *stream) {

@@ -22,18 +22,25 @@ constexpr int kSlice = 64, kChain = 4, kThreads = 256;
 template <int KP>
 struct Layout {
     static constexpr int tile = kBlock * KP * 2, v = kBlock * kSlice * 2;
-    static constexpr int chain = tile + 2 * kTile + v + 1040;       // K, N in two terms, X, the factors: two of them
-    static constexpr int ahead = tile + v + 2 * kTile + 256;        // Q, dY, P in two terms, scale Gam: two of them
+    static constexpr int chain = tile + 2 * kTile + v;              // K, N in two terms, X: two of them
+    static constexpr int ahead = tile + v + 2 * kTile;              // Q, dY, P in two terms: two of them
     static constexpr int at_ahead = 2 * chain, handed = at_ahead + 2 * ahead;
     static constexpr int u = 16 * kBlock * 4, s = 16 * KP * 4;      // of a warp: dY^T P and (scale Gam dY)^T Q
     static constexpr int out = handed + kChain * (u + s);
     static constexpr int out_warp = 16 * 128 * 2;
-    static constexpr int bytes = out + kChain * out_warp;
-    static_assert(sizeof(Factors) <= 1040 && bytes <= 232448, "shared memory");
+    static constexpr int factors = out + kChain * out_warp;         // two of them, and scale Gam of the blocks ahead
+    static constexpr int scaled = factors + 2 * int(sizeof(Factors));
+    static constexpr int bars = scaled + 2 * kBlock * 4;            // two barriers, and whether a wait ran out
+    static constexpr int bytes = bars + 32;
+    static_assert(chain % 1024 == 0 && ahead % 1024 == 0 && bytes <= 232448, "shared memory");
 };
+struct Maps {
+    CUtensorMap q, k, dy, x;
+};
+__device__ unsigned int g_device_error;
 
 template <int KP>
-__global__ void __launch_bounds__(kThreads, 1) back_kernel(const BwdArgs<bf> p) {
+__global__ void __launch_bounds__(kThreads, 1) back_kernel(const BwdArgs<bf> p, const __grid_constant__ Maps maps) {
     extern __shared__ __align__(1024) unsigned char mem[];
     using L = Layout<KP>;
     let_next_begin();
@@ -52,38 +59,40 @@ __global__ void __launch_bounds__(kThreads, 1) back_kernel(const BwdArgs<bf> p) 
     const int64_t state_at = (int64_t(seq) * s.H + head) * s.V * s.K;
     const uint32_t hand_u = base + L::handed + warp * (L::u + L::s) + lane * 16, hand_s = hand_u + L::u;
 
-    // for turn i + 1: what the warps ahead need of block blocks - 2 - i, and the chain of the one before
-    const auto copy_ahead = [&](int c, int stage) {
-        const int64_t row = span.first + int64_t(c) * kBlock;
-        const int rows = min(kBlock, span.len - c * kBlock);
-        const uint32_t to = base + L::at_ahead + stage * L::ahead;
-        const unsigned char *record = p.records + ((span.slot + c) * s.H + head) * kBothRecord;
-        copy_tile<KP, kThreads>(to, p.q + row * qk_step + int64_t(group) * s.K, qk_step, rows, s.K, tid);
-        copy_tile<kSlice, kThreads>(to + L::tile, p.dy + row * v_step + int64_t(head) * s.V + v0, v_step, rows,
-                                    min(kSlice, s.V - v0), tid);
-#pragma unroll
-        for (int i = 0; i < kTile / 16 / kThreads; ++i) {
-            const int at = (i * kThreads + tid) * 16;
-            copy16(to + L::tile + L::v + at, record + 2 * kTile + at);
-            copy16(to + L::tile + L::v + kTile + at, record + kRecord + at);
+    uint64_t *full = reinterpret_cast<uint64_t *>(mem + L::bars);
+    int *abort = reinterpret_cast<int *>(full + 2);
+    // One thread asks for a turn's copies: what the warps ahead need of block blocks - 1 - turn, the chain of the one behind.
+    const auto copy = [&](int turn) {
+        const int ahead = span.blocks - 1 - turn, behind = ahead + 1, stage = turn % 2;
+        uint64_t *bar = &full[stage];
+        const auto record = [&](int c) { return p.records + ((span.slot + c) * s.H + head) * kBothRecord; };
+        constexpr int for_ahead = L::ahead + kBlock * 4, for_chain = L::chain + int(sizeof(Factors));
+        tc::mbar_arrive_expect_tx(bar, (ahead >= 0 ? for_ahead : 0) + (turn > 0 ? for_chain : 0));
+        if (ahead >= 0) {
+            const uint32_t to = base + L::at_ahead + stage * L::ahead;
+            const int row = int(span.first + int64_t(ahead) * kBlock);
+            boxes<KP>(to, &maps.q, bar, group, row);
+            box(to + L::tile, &maps.dy, bar, v0, head, row);
+            bulk(to + L::tile + L::v, record(ahead) + 2 * kTile, kTile, bar);
+            bulk(to + L::tile + L::v + kTile, record(ahead) + kRecord, kTile, bar);
+            bulk(base + L::scaled + stage * kBlock * 4, record(ahead) + 3 * kTile + offsetof(Factors, start_scaled), kBlock * 4, bar);
         }
-        if (tid < 16)
-            copy16(to + L::tile + L::v + 2 * kTile + tid * 16, record + 3 * kTile + offsetof(Factors, start_scaled) + tid * 16);
+        if (turn > 0) {
+            const uint32_t to = base + stage * L::chain;
+            const int row = int(span.first + int64_t(behind) * kBlock);
+            boxes<KP>(to, &maps.k, bar, group, row);
+            bulk(to + L::tile, record(behind), 2 * kTile, bar);
+            box(to + L::tile + 2 * kTile, &maps.x, bar, v0, head, row);
+            bulk(base + L::factors + stage * int(sizeof(Factors)), record(behind) + 3 * kTile, int(sizeof(Factors)), bar);
+        }
     };
-    const auto copy_chain = [&](int c, int stage) {
-        const int64_t row = span.first + int64_t(c) * kBlock;
-        const int rows = min(kBlock, span.len - c * kBlock);
-        const uint32_t to = base + stage * L::chain;
-        const unsigned char *record = p.records + ((span.slot + c) * s.H + head) * kBothRecord;
-        copy_tile<KP, kThreads>(to, p.k + row * qk_step + int64_t(group) * s.K, qk_step, rows, s.K, tid);
-#pragma unroll
-        for (int i = 0; i < 2 * kTile / 16 / kThreads; ++i)
-            copy16(to + L::tile + (i * kThreads + tid) * 16, record + (i * kThreads + tid) * 16);
-        copy_tile<kSlice, kThreads>(to + L::tile + 2 * kTile, p.errors + row * v_step + int64_t(head) * s.V + v0, v_step,
-                                    rows, min(kSlice, s.V - v0), tid);
-        if (tid < int(sizeof(Factors)) / 16)
-            copy16(to + L::tile + 2 * kTile + L::v + tid * 16, record + 3 * kTile + tid * 16);
-    };
+    const bool asks = tid == 32 * kChain;
+    if (asks) {
+        *abort = 0;
+        tc::mbar_init(&full[0], 1), tc::mbar_init(&full[1], 1);
+        tc::mbar_fence_init();
+    }
+    __syncthreads();
     float st[KP / 8][4], w[8][4];       // the adjoint and dU; of the warps ahead, what they hand over
 #pragma unroll
     for (int n = 0; n < KP / 8; ++n)
@@ -93,14 +102,25 @@ __global__ void __launch_bounds__(kThreads, 1) back_kernel(const BwdArgs<bf> p) 
             st[n][e] = chain && p.dh_final && v < width && k < s.K ? p.dh_final[state_at + int64_t(mine + v) * s.K + k] : 0.0f;
         }
     wait_for_last();
-    if (span.blocks > 0) copy_ahead(span.blocks - 1, 0);
-    cp_async_commit();
-    for (int i = 0; i <= span.blocks; ++i) {
-        cp_async_wait<0>();
+    const int turns = span.blocks > 0 ? span.blocks + 1 : 0;
+    if (asks && turns > 0) copy(0);
+    for (int i = 0; i < turns; ++i) {
+        wait_for(&full[i % 2], i / 2 & 1, abort, &g_device_error);
+        const int rows_last = span.len - (span.blocks - 1) * kBlock;
+        if (rows_last < kBlock && i < 2) {
+            // the last block: it is ahead in the first turn, the chain's in the second
+            if (i == 0) {
+                clear_rows<KP>(base + L::at_ahead, rows_last, tid, kThreads);
+                clear_rows<64>(base + L::at_ahead + L::tile, rows_last, tid, kThreads);
+            } else {
+                clear_rows<KP>(base + L::chain, rows_last, tid, kThreads);
+                clear_rows<64>(base + L::chain + L::tile + 2 * kTile, rows_last, tid, kThreads);
+            }
+            tc::fence_proxy_async_smem();
+        }
         __syncthreads();
-        if (i + 1 < span.blocks) copy_ahead(span.blocks - 2 - i, (i + 1) % 2);
-        if (i < span.blocks) copy_chain(span.blocks - 1 - i, (i + 1) % 2);
-        cp_async_commit();
+        if (*reinterpret_cast<volatile int *>(abort)) break;
+        if (asks && i + 1 < turns) copy(i + 1);
         if (!chain) {
             if (i > 0) {
 #pragma unroll
@@ -112,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1) back_kernel(const BwdArgs<bf> p) 
             if (i == span.blocks) break;
             const int from = L::at_ahead + i % 2 * L::ahead;
             const uint32_t at = base + from, pairs = at + L::tile + L::v;
-            const float *by = reinterpret_cast<const float *>(mem + from + L::tile + L::v + 2 * kTile);
+            const float *by = reinterpret_cast<const float *>(mem + L::scaled) + i % 2 * kBlock;
             uint32_t y[4][4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) load4t(y[t], four_across<64>(at + L::tile, 16 * t, 16 * warp));
@@ -151,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) back_kernel(const BwdArgs<bf> p) 
             const int64_t row = span.first + int64_t(c) * kBlock;
             const int from = i % 2 * L::chain;
             const uint32_t at = base + from, room = base + L::out + warp * L::out_warp;
-            const Factors &f = *reinterpret_cast<const Factors *>(mem + from + L::tile + 2 * kTile + L::v);
+            const Factors &f = reinterpret_cast<const Factors *>(mem + L::factors)[i % 2];
             // A K^T
             through_tile<KP>(w, st, at, [&](int k, const uint32_t(&hi)[4]) { store4(four<KP, 16>(room, 0, 16 * k), hi); });
             __syncwarp();
@@ -229,6 +249,10 @@ __global__ void __launch_bounds__(kThreads, 1) back_kernel(const BwdArgs<bf> p) 
             }
             add_outer<KP>(st, hi, lo, at);
         }
+    }
+    if (*reinterpret_cast<volatile int *>(abort)) {
+        if (asks) linger();         // copies may still be on their way
+        return;
     }
     if (chain && p.dh0)
 #pragma unroll
@@ -576,12 +600,12 @@ bool fits(const BwdArgs<bf> &a) {
 }
 
 template <int KP>
-static cudaError_t back(const BwdArgs<bf> &a, cudaStream_t st) {
+static cudaError_t back(const BwdArgs<bf> &a, const Maps &maps, cudaStream_t st) {
     const int64_t grid = int64_t(a.s.n) * a.s.H * ((a.s.V + kSlice - 1) / kSlice);
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     constexpr int bytes = Layout<KP>::bytes;
     if (cudaError_t e = allow<back_kernel<KP>>(bytes)) return e;
-    return launch_behind(back_kernel<KP>, unsigned(grid), kThreads, bytes, st, a);
+    return launch_behind(back_kernel<KP>, unsigned(grid), kThreads, bytes, st, a, maps);
 }
 template <int KP, int VP>
 static cudaError_t blocks(const BwdArgs<bf> &a, cudaStream_t st) {
@@ -593,13 +617,19 @@ static cudaError_t blocks(const BwdArgs<bf> &a, cudaStream_t st) {
 }
 
 cudaError_t launch(const BwdArgs<bf> &a, cudaStream_t st) {
+    Maps maps;
+    if (!map_of(&maps.q, a.q, a.s.rows(), a.s.G, a.s.K) || !map_of(&maps.k, a.k, a.s.rows(), a.s.G, a.s.K) ||
+        !map_of(&maps.dy, a.dy, a.s.rows(), a.s.H, a.s.V) || !map_of(&maps.x, a.errors, a.s.rows(), a.s.H, a.s.V))
+        return cudaErrorInvalidValue;
     if (cudaError_t e = make_pairs(a.s, a.q, a.k, a.g, a.beta, a.records, true, st)) return e;
-    if (cudaError_t e = a.s.K <= 64 ? back<64>(a, st) : back<128>(a, st)) return e;
+    if (cudaError_t e = a.s.K <= 64 ? back<64>(a, maps, st) : back<128>(a, maps, st)) return e;
     const cudaError_t e = a.s.K <= 64 ? (a.s.V <= 64 ? blocks<64, 64>(a, st) : blocks<64, 128>(a, st))
                                       : (a.s.V <= 64 ? blocks<128, 64>(a, st) : blocks<128, 128>(a, st));
     if (e) return e;
     return a.s.H > a.s.G ? general::fold(a, st) : cudaSuccess;
 }
+
+cudaError_t take_device_error(unsigned int *out) { return take_error(g_device_error, out); }
 
 }  // namespace bwd
 }  // namespace mma

@@ -457,6 +457,7 @@ __device__ __forceinline__ void lower_solve(float *m, const float *beta, int tid
 // as place<64> does.  Blocks of 16 x 16 above P's diagonal are unspecified.
 constexpr int kTile = kBlock * kBlock * 2;
 constexpr int kRecord = (3 * kTile + int(sizeof(Factors)) + 127) / 128 * 128, kBothRecord = kRecord + kTile;
+cudaError_t take_device_error(unsigned int *out);
 cudaError_t make_pairs(const Shape &s, const bf *q, const bf *k, const bf *g, const bf *beta, unsigned char *records,
                        bool both, cudaStream_t st);
 

@@ -20,13 +20,20 @@ struct PairLayout {
     static constexpr int bytes = system + kBlock * kPairStride * 4;
 };
 
+struct PairMaps {
+    CUtensorMap q, k;
+};
+__device__ unsigned int g_device_error;
+
 template <int KP>
 __global__ void __launch_bounds__(kPairThreads, 4)
-pairs_kernel(const Shape s, const bf *q, const bf *k, const bf *g, const bf *beta, unsigned char *records, const bool both) {
-    extern __shared__ __align__(128) unsigned char mem[];
+pairs_kernel(const Shape s, const __grid_constant__ PairMaps maps, const bf *g, const bf *beta, unsigned char *records,
+             const bool both) {
+    extern __shared__ __align__(1024) unsigned char mem[];
     __shared__ Decays d;
     __shared__ Factors f;
-    __shared__ int found;
+    __shared__ int found, abort;
+    __shared__ __align__(8) uint64_t full;
     using L = PairLayout<KP>;
     let_next_begin();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -36,11 +43,16 @@ pairs_kernel(const Shape s, const bf *q, const bf *k, const bf *g, const bf *bet
     if (seq < 0) return;
     const Span span = span_of(s, seq);
     const int c = int(slot - span.slot), rows = min(kBlock, span.len - c * kBlock);
-    const int64_t row = span.first + int64_t(c) * kBlock, step = int64_t(s.G) * s.K;
+    const int64_t row = span.first + int64_t(c) * kBlock;
     const uint32_t base = smem_u32(mem);
-    copy_tile<KP, kPairThreads>(base, k + row * step + int64_t(group) * s.K, step, rows, s.K, tid);
-    copy_tile<KP, kPairThreads>(base + L::tile, q + row * step + int64_t(group) * s.K, step, rows, s.K, tid);
-    cp_async_commit();
+    if (tid == 32) {
+        abort = 0;
+        tc::mbar_init(&full, 1);
+        tc::mbar_fence_init();
+        tc::mbar_arrive_expect_tx(&full, 2 * L::tile);
+        boxes<KP>(base, &maps.k, &full, group, int(row));
+        boxes<KP>(base + L::tile, &maps.q, &full, group, int(row));
+    }
     float *system = reinterpret_cast<float *>(mem + L::system);
     if (warp == 0) {
         load_decays(d, g + row * s.H + head, beta + row * s.H + head, s.H, rows);
@@ -56,8 +68,17 @@ pairs_kernel(const Shape s, const bf *q, const bf *k, const bf *g, const bf *bet
             if (t == kBlock - 1) f.last = start;
         }
     }
-    cp_async_wait<0>();
     __syncthreads();
+    wait_for(&full, 0, &abort, &g_device_error);
+    if (*reinterpret_cast<volatile int *>(&abort)) {
+        linger();           // copies may still be on their way
+        return;
+    }
+    if (rows < kBlock) {
+        clear_rows<KP>(base, rows, tid, kPairThreads);
+        clear_rows<KP>(base + L::tile, rows, tid, kPairThreads);
+        __syncthreads();
+    }
     // rows 16 j of K K^T and 16 (3 - j) of Q K^T have five blocks of 16 x 16 together
     pair_products<KP>(base, base, warp, d, [&](int, int, int t, int r, float x, float y) {
         *reinterpret_cast<float2 *>(system + t * kPairStride + r) = make_float2(r < t ? x : 0.0f, r + 1 < t ? y : 0.0f);
@@ -105,20 +126,24 @@ pairs_kernel(const Shape s, const bf *q, const bf *k, const bf *g, const bf *bet
 }
 
 template <int KP>
-static cudaError_t go(const Shape &s, const bf *q, const bf *k, const bf *g, const bf *beta, unsigned char *records,
-                      bool both, cudaStream_t st) {
+static cudaError_t go(const Shape &s, const PairMaps &maps, const bf *g, const bf *beta, unsigned char *records, bool both,
+                      cudaStream_t st) {
     const int64_t grid = s.slots() * s.H;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     constexpr int bytes = PairLayout<KP>::bytes;
     if (cudaError_t e = allow<pairs_kernel<KP>>(bytes)) return e;
-    pairs_kernel<KP><<<unsigned(grid), kPairThreads, bytes, st>>>(s, q, k, g, beta, records, both);
+    pairs_kernel<KP><<<unsigned(grid), kPairThreads, bytes, st>>>(s, maps, g, beta, records, both);
     return cudaGetLastError();
 }
 
 cudaError_t make_pairs(const Shape &s, const bf *q, const bf *k, const bf *g, const bf *beta, unsigned char *records,
                        bool both, cudaStream_t st) {
-    return s.K <= 64 ? go<64>(s, q, k, g, beta, records, both, st) : go<128>(s, q, k, g, beta, records, both, st);
+    PairMaps maps;
+    if (!map_of(&maps.q, q, s.rows(), s.G, s.K) || !map_of(&maps.k, k, s.rows(), s.G, s.K)) return cudaErrorInvalidValue;
+    return s.K <= 64 ? go<64>(s, maps, g, beta, records, both, st) : go<128>(s, maps, g, beta, records, both, st);
 }
+
+cudaError_t take_device_error(unsigned int *out) { return take_error(g_device_error, out); }
 
 }  // namespace mma
 }  // namespace delta
