@@ -282,6 +282,10 @@ struct BlockLayout {
     static constexpr int dp = s1 + states, da = dp + kTile, bytes = da + kTile;
 };
 
+struct BlockMaps {
+    CUtensorMap q, k, dy, x, dv, s0, s1;
+};
+
 // Warp 2 j + h: rows 16 j; of the pairs, those of the queries (h = 0) or of the
 // keys (h = 1); of dQ and dK, columns h KP / 2 to (h + 1) KP / 2.
 //
@@ -290,10 +294,12 @@ struct BlockLayout {
 // every M enters once with either sign, in fp32, so nothing is lost but the
 // rounding of the sums.
 template <int KP, int VP>
-__global__ void __launch_bounds__(256, VP == 64 ? 2 : 1) block_kernel(const BwdArgs<bf> p, const int parts) {
+__global__ void __launch_bounds__(256, VP == 64 ? 2 : 1)
+block_kernel(const BwdArgs<bf> p, const __grid_constant__ BlockMaps maps, const int parts) {
     extern __shared__ __align__(1024) unsigned char mem[];
     __shared__ Decays d;
-    __shared__ int found;
+    __shared__ int found, abort;
+    __shared__ __align__(8) uint64_t full[2];       // the block's rows; the states
     __shared__ float row_term[2][kBlock], col_term[2][kBlock], row_sum[2][kBlock], both_term[8];
     __shared__ __align__(16) float col_sum[8][kBlock];
     using L = BlockLayout<KP, VP>;
@@ -307,36 +313,38 @@ __global__ void __launch_bounds__(256, VP == 64 ? 2 : 1) block_kernel(const BwdA
     const Span span = span_of(s, seq);
     const int c = int(slot - span.slot), rows = min(kBlock, span.len - c * kBlock);
     const int64_t row = span.first + int64_t(c) * kBlock;
-    const int64_t qk_step = int64_t(s.G) * s.K, v_step = int64_t(s.H) * s.V;
     const uint32_t base = smem_u32(mem);
     const int j = warp / 2, h = warp % 2;
 
-    copy_tile<KP, 256>(base + L::q, p.q + row * qk_step + int64_t(group) * s.K, qk_step, rows, s.K, tid);
-    copy_tile<KP, 256>(base + L::k, p.k + row * qk_step + int64_t(group) * s.K, qk_step, rows, s.K, tid);
-    const int64_t v_at = row * v_step + int64_t(head) * s.V;
+    const auto ask_rows = [&](int tile, const CUtensorMap *map) {
 #pragma unroll
-    for (int v0 = 0; v0 < VP; v0 += 64) {
-        const int at = v0 / 64 * L::v, width = max(s.V - v0, 0);
-        copy_tile<64, 256>(base + L::y + at, p.dy + v_at + (width > 0 ? v0 : 0), v_step, rows, width, tid);
-        copy_tile<64, 256>(base + L::x + at, p.errors + v_at + (width > 0 ? v0 : 0), v_step, rows, width, tid);
-    }
-    wait_for_last();
+        for (int v0 = 0; v0 < VP; v0 += 64) box(base + tile + v0 / 64 * L::v, map, &full[0], v0, head, int(row));
+    };
+    const auto ask_states = [&](int tile, const CUtensorMap *map) {
 #pragma unroll
-    for (int v0 = 0; v0 < VP; v0 += 64) {
-        const int width = max(s.V - v0, 0);
-        copy_tile<64, 256>(base + L::dv + v0 / 64 * L::v, p.dv + v_at + (width > 0 ? v0 : 0), v_step, rows, width, tid);
-    }
-    cp_async_commit();
-    {
-        const bf *st0 = p.states + (slot * s.H + head) * int64_t(s.V) * s.K, *st1 = p.ds + (slot * s.H + head) * int64_t(s.V) * s.K;
+        for (int v0 = 0; v0 < VP; v0 += 64)
 #pragma unroll
-        for (int v0 = 0; v0 < VP; v0 += 64) {
-            const int have = min(max(s.V - v0, 0), kBlock), at = have > 0 ? v0 : 0;
-            copy_tile<KP, 256>(base + L::s0 + v0 * KP * 2, st0 + int64_t(at) * s.K, s.K, have, s.K, tid);
-            copy_tile<KP, 256>(base + L::s1 + v0 * KP * 2, st1 + int64_t(at) * s.K, s.K, have, s.K, tid);
-        }
+            for (int k = 0; k < KP; k += 64)
+                box(base + tile + v0 * KP * 2 + k * kBlock * 2, map, &full[1], k, v0, int(slot * s.H + head));
+    };
+    if (tid == 32) {
+        abort = 0;
+        tc::mbar_init(&full[0], 1), tc::mbar_init(&full[1], 1);
+        tc::mbar_fence_init();
+        tc::mbar_arrive_expect_tx(&full[0], 2 * L::qk + 3 * L::values);
+        tc::mbar_arrive_expect_tx(&full[1], 2 * L::states);
+        boxes<KP>(base + L::q, &maps.q, &full[0], group, int(row));
+        boxes<KP>(base + L::k, &maps.k, &full[0], group, int(row));
+        ask_rows(L::y, &maps.dy);
+        ask_rows(L::x, &maps.x);
+        ask_states(L::s0, &maps.s0);
+        // what the chain has written
+        wait_for_last();
+        ask_rows(L::dv, &maps.dv);
+        ask_states(L::s1, &maps.s1);
+    } else {
+        wait_for_last();
     }
-    cp_async_commit();
     if (warp == 0) load_decays(d, p.g + row * s.H + head, p.beta + row * s.H + head, s.H, rows);
     // dbeta: the shares of the chain's warps
     float share = 0.0f;
@@ -344,8 +352,18 @@ __global__ void __launch_bounds__(256, VP == 64 ? 2 : 1) block_kernel(const BwdA
         const int64_t slots = s.offsets ? s.L / kBlock + s.n : (s.L + kBlock - 1) / kBlock * s.n;
         for (int i = 0; i < parts; ++i) share += p.dbeta_part[((i * slots + slot) * s.H + head) * kBlock + tid - 64];
     }
-    cp_async_wait<1>();
     __syncthreads();
+    wait_for(&full[0], 0, &abort, &g_device_error);
+    if (rows < kBlock) {
+        clear_rows<KP>(base + L::q, rows, tid, 256);
+        clear_rows<KP>(base + L::k, rows, tid, 256);
+        for (int v0 = 0; v0 < VP; v0 += 64) {
+            clear_rows<64>(base + L::y + v0 / 64 * L::v, rows, tid, 256);
+            clear_rows<64>(base + L::x + v0 / 64 * L::v, rows, tid, 256);
+            clear_rows<64>(base + L::dv + v0 / 64 * L::v, rows, tid, 256);
+        }
+        __syncthreads();
+    }
     // pairs: scale beta_s dY_t.x_s D with q_t.k_s, or -beta_s dV_t.x_s D with k_t.k_s
     {
         const uint32_t left = base + (h == 0 ? L::y : L::dv), key = base + (h == 0 ? L::q : L::k);
@@ -411,8 +429,12 @@ __global__ void __launch_bounds__(256, VP == 64 ? 2 : 1) block_kernel(const BwdA
         if (lane % 4 == 0) row_sum[h][t] = sum0, row_sum[h][t + 8] = sum1;
         for (int r = 16 * (j + 1) + lane; r < kBlock; r += 32) col_sum[warp][r] = 0.0f;
     }
-    cp_async_wait<0>();
+    wait_for(&full[1], 0, &abort, &g_device_error);
     __syncthreads();
+    if (*reinterpret_cast<volatile int *>(&abort)) {
+        linger();           // copies may still be on their way
+        return;
+    }
     // <S0, dS>
     {
         float both = 0.0f;
@@ -608,12 +630,12 @@ static cudaError_t back(const BwdArgs<bf> &a, const Maps &maps, cudaStream_t st)
     return launch_behind(back_kernel<KP>, unsigned(grid), kThreads, bytes, st, a, maps);
 }
 template <int KP, int VP>
-static cudaError_t blocks(const BwdArgs<bf> &a, cudaStream_t st) {
+static cudaError_t blocks(const BwdArgs<bf> &a, const BlockMaps &maps, cudaStream_t st) {
     const int64_t grid = a.s.slots() * a.s.H;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     constexpr int bytes = BlockLayout<KP, VP>::bytes;
     if (cudaError_t e = allow<block_kernel<KP, VP>>(bytes)) return e;
-    return launch_behind(block_kernel<KP, VP>, unsigned(grid), 256, bytes, st, a, dbeta_parts(a.s));
+    return launch_behind(block_kernel<KP, VP>, unsigned(grid), 256, bytes, st, a, maps, dbeta_parts(a.s));
 }
 
 cudaError_t launch(const BwdArgs<bf> &a, cudaStream_t st) {
@@ -623,8 +645,14 @@ cudaError_t launch(const BwdArgs<bf> &a, cudaStream_t st) {
         return cudaErrorInvalidValue;
     if (cudaError_t e = make_pairs(a.s, a.q, a.k, a.g, a.beta, a.records, true, st)) return e;
     if (cudaError_t e = a.s.K <= 64 ? back<64>(a, maps, st) : back<128>(a, maps, st)) return e;
-    const cudaError_t e = a.s.K <= 64 ? (a.s.V <= 64 ? blocks<64, 64>(a, st) : blocks<64, 128>(a, st))
-                                      : (a.s.V <= 64 ? blocks<128, 64>(a, st) : blocks<128, 128>(a, st));
+    BlockMaps of;
+    of.q = maps.q, of.k = maps.k, of.dy = maps.dy, of.x = maps.x;
+    const int64_t states = a.s.slots() * a.s.H;
+    if (!map_of(&of.dv, a.dv, a.s.rows(), a.s.H, a.s.V) || !map_of(&of.s0, a.states, states, a.s.V, a.s.K, true) ||
+        !map_of(&of.s1, a.ds, states, a.s.V, a.s.K, true))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = a.s.K <= 64 ? (a.s.V <= 64 ? blocks<64, 64>(a, of, st) : blocks<64, 128>(a, of, st))
+                                      : (a.s.V <= 64 ? blocks<128, 64>(a, of, st) : blocks<128, 128>(a, of, st));
     if (e) return e;
     return a.s.H > a.s.G ? general::fold(a, st) : cudaSuccess;
 }

@@ -485,8 +485,9 @@ inline cudaError_t take_error(const unsigned int &symbol, unsigned int *out) {
 }
 
 // A map of a tensor (rows, heads, cols) for boxes of 64 rows x 64 columns of a
-// head; what lies outside reads as 0.
-inline bool map_of(CUtensorMap *map, const bf *base, int64_t rows, int heads, int cols) {
+// head, or (`across`) of 64 heads x 64 columns of a row; what lies outside
+// reads as 0.
+inline bool map_of(CUtensorMap *map, const bf *base, int64_t rows, int heads, int cols, bool across = false) {
     static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> cached{nullptr};
     PFN_cuTensorMapEncodeTiled_v12000 fn = cached.load(std::memory_order_acquire);
     if (fn == nullptr) {
@@ -500,7 +501,7 @@ inline bool map_of(CUtensorMap *map, const bf *base, int64_t rows, int heads, in
     }
     const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(heads), cuuint64_t(rows)};
     const cuuint64_t strides[2] = {cuuint64_t(cols) * 2, cuuint64_t(cols) * heads * 2};
-    const cuuint32_t box[3] = {64, 1, kBlock}, each[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, across ? kBlock : 1u, across ? 1u : kBlock}, each[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf *>(base), dims, strides, box, each,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
