@@ -609,6 +609,9 @@ SSM_API ssm_status_t ssm_selftest_wait_timeout(void *stream);
  */
 SSM_API ssm_status_t gated_selftest_wait_timeout(int backward, int copy, void *stream);
 
+/* The same for the wait of the gated delta rule's kernels for a copy (20 ms). */
+SSM_API ssm_status_t delta_selftest_wait_timeout(void *stream);
+
 /* Static, human-readable name of a status code. */
 SSM_API const char *ssm_status_string(ssm_status_t status);
 

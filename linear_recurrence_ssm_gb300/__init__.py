@@ -100,6 +100,7 @@ SIGNATURES = {
     "ssm_check_device_errors": ([_VP], ctypes.c_int),
     "ssm_selftest_wait_timeout": ([_VP], ctypes.c_int),
     "gated_selftest_wait_timeout": ([ctypes.c_int, ctypes.c_int, _VP], ctypes.c_int),
+    "delta_selftest_wait_timeout": ([_VP], ctypes.c_int),
     "ssm_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "ssm_version": ([], ctypes.c_int),
 }

@@ -115,6 +115,7 @@ cudaError_t bwd(const BwdArgs<T> &a, cudaStream_t st);
 }
 namespace mma {
 namespace fwd {
+cudaError_t probe_wait_timeout(cudaStream_t st);
 cudaError_t take_device_error(unsigned int *out);
 bool fits(const FwdArgs<__nv_bfloat16> &a);
 cudaError_t launch(FwdArgs<__nv_bfloat16> a, cudaStream_t st);
@@ -1066,6 +1067,13 @@ ssm_status_t gated_selftest_wait_timeout(int backward, int copy, void *stream) {
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     return from_cuda(backward ? ssm::gated_bwd::probe_wait_timeout(copy != 0, st)
                               : ssm::gated::probe_wait_timeout(copy != 0, st));
+}
+
+ssm_status_t delta_selftest_wait_timeout(void *stream) {
+    DeviceInfo dev;
+    ssm_status_t s = current_device(&dev);
+    if (s != SSM_OK) return s;
+    return from_cuda(ssm::delta::mma::fwd::probe_wait_timeout(static_cast<cudaStream_t>(stream)));
 }
 
 const char *ssm_status_string(ssm_status_t status) {

@@ -382,6 +382,27 @@ cudaError_t launch(FwdArgs<bf> a, cudaStream_t st) {
     return wide ? go<128, false>(a, maps, places, st) : go<64, false>(a, maps, places, st);
 }
 
+// Self-test of the wait: for a copy that was never asked for.
+__global__ void __launch_bounds__(32) run_out_kernel() {
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ int abort;
+    if (threadIdx.x == 0) {
+        abort = 0;
+        tc::mbar_init(&bar, 1);
+        tc::mbar_fence_init();
+    }
+    __syncthreads();
+    wait_for(&bar, 0, &abort, &g_device_error, 20000000ull);
+    __syncthreads();
+    // what a kernel then does in its remaining turns: it has to wait no more
+    if (*reinterpret_cast<volatile int *>(&abort)) return;
+    linger();
+}
+cudaError_t probe_wait_timeout(cudaStream_t st) {
+    run_out_kernel<<<1, 32, 0, st>>>();
+    return cudaGetLastError();
+}
+
 cudaError_t take_device_error(unsigned int *out) { return take_error(g_device_error, out); }
 
 }  // namespace fwd

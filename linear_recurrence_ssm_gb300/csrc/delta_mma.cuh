@@ -154,8 +154,9 @@ __device__ __forceinline__ void linger() {
     while (tc::globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(1000);
 }
 // Waits for a barrier's phase; gives up after the limit, and says so in *abort and *error.
-__device__ __forceinline__ void wait_for(uint64_t *bar, int phase, int *abort, unsigned int *error) {
-    if (tc::mbar_wait_bounded(bar, phase, abort, kWaitLimitNs)) return;
+__device__ __forceinline__ void wait_for(uint64_t *bar, int phase, int *abort, unsigned int *error,
+                                         uint64_t limit_ns = kWaitLimitNs) {
+    if (tc::mbar_wait_bounded(bar, phase, abort, limit_ns)) return;
     *reinterpret_cast<volatile int *>(abort) = 1;
     atomicOr(error, 1u);
 }
@@ -502,9 +503,13 @@ inline bool map_of(CUtensorMap *map, const bf *base, int64_t rows, int heads, in
     const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(heads), cuuint64_t(rows)};
     const cuuint64_t strides[2] = {cuuint64_t(cols) * 2, cuuint64_t(cols) * heads * 2};
     const cuuint32_t box[3] = {64, across ? kBlock : 1u, across ? 1u : kBlock}, each[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf *>(base), dims, strides, box, each,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const auto encode = [&] {
+        return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf *>(base), dims, strides, box, each,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    // a host thread that has made no call of the runtime yet has no context for the driver's
+    return encode() || (cudaFree(nullptr) == cudaSuccess && encode());
 }
 // A launch that may begin while the kernel before it in the stream runs.
 template <typename... P, typename... A>
