@@ -73,6 +73,26 @@ __device__ __forceinline__ void row_sums(float (&v)[ROWS], float (*mem)[ROWS]) {
     }
 }
 
+// Eight elements as they lie in memory.
+template <typename T>
+struct Raw {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (auto &x : w) x = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int i = 0; i < int(sizeof(T) / 2); ++i) w[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+    }
+    __device__ __forceinline__ void add_to(float (&v)[kVec]) const {
+        float x[kVec];
+        load8(x, reinterpret_cast<const T *>(w));
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) v[e] += x[e];
+    }
+};
+
 template <typename T>
 struct FwdArgs {
     const T *x, *residual;
@@ -92,24 +112,31 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) fwd_kernel(const FwdArgs<T
     const bool there = row < p.rows;
     const int64_t at = row * p.cols;
     float v[VECS][kVec], squares[1] = {0.0f};
+    {
+        // all loads ahead of the first store, which the compiler may not pass
+        Raw<T> x[VECS], r[VECS];
 #pragma unroll
-    for (int i = 0; i < VECS; ++i) {
-        const int c = (i * lanes + lane) * kVec;
-        if (there && c < p.cols) {
-            load8(v[i], p.x + at + c);
-            if (p.residual) {
-                float r[kVec];
-                load8(r, p.residual + at + c);
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) v[i][e] += r[e];
-                store8(p.sum + at + c, v[i]);
+        for (int i = 0; i < VECS; ++i) {
+            const int c = (i * lanes + lane) * kVec;
+            x[i].clear(), r[i].clear();
+            if (there && c < p.cols) {
+                x[i].load(p.x + at + c);
+                if (p.residual) r[i].load(p.residual + at + c);
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) v[i][e] = 0.0f;
         }
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) squares[0] += v[i][e] * v[i][e];
+        for (int i = 0; i < VECS; ++i) {
+            const int c = (i * lanes + lane) * kVec;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) v[i][e] = 0.0f;
+            x[i].add_to(v[i]);
+            if (p.residual) {
+                r[i].add_to(v[i]);
+                if (there && c < p.cols) store8(p.sum + at + c, v[i]);
+            }
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) squares[0] += v[i][e] * v[i][e];
+        }
     }
     row_sums<LANES, 1>(squares, mem);
     const float rstd = 1.0f / sqrtf(squares[0] / float(p.cols) + p.eps);
@@ -208,26 +235,6 @@ struct BwdArgs {
     T *dx;
     float *dweight, *parts;
     int64_t rows, cols;
-};
-
-// Eight elements as they lie in memory.
-template <typename T>
-struct Raw {
-    uint4 w[sizeof(T) / 2];
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (auto &x : w) x = make_uint4(0, 0, 0, 0);
-    }
-    __device__ __forceinline__ void load(const T *p) {
-#pragma unroll
-        for (int i = 0; i < int(sizeof(T) / 2); ++i) w[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
-    }
-    __device__ __forceinline__ void add_to(float (&v)[kVec]) const {
-        float x[kVec];
-        load8(x, reinterpret_cast<const T *>(w));
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) v[e] += x[e];
-    }
 };
 
 // A thread keeps its columns over all rows of its block, so that dw's partial
