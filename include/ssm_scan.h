@@ -572,7 +572,7 @@ SSM_API ssm_status_t rms_norm_fwd(const void *x, const void *residual, const flo
  *          it was rounded
  *   rstd : what the forward call gave
  *   dx : the gradient of x, and of the residual   dweight : (cols) fp32 or NULL
- *   scratch : with dweight, min(rows, 608) * cols floats of the caller's;
+ *   scratch : with dweight, min(rows, 1216) * cols floats of the caller's;
  *             unspecified afterwards
  * Deterministic.  No output may overlap an input, but dx may be dsum.
  */

@@ -1021,7 +1021,7 @@ def rms_norm_bwd(dy, x, weight, rstd, residual=None, ds=None, need_dweight=True)
     dweight = scratch = None
     if weight is not None and need_dweight:
         dweight = torch.empty(cols, dtype=torch.float32, device=dev)
-        scratch = torch.empty(min(rows, 608) * cols, dtype=torch.float32, device=dev)
+        scratch = torch.empty(min(rows, 1216) * cols, dtype=torch.float32, device=dev)
     _call("rms_norm_bwd", dev, dy.data_ptr(), x.data_ptr(), _addr(residual), _addr(weight), rstd.data_ptr(),
           _addr(ds), dx.data_ptr(), _addr(dweight), _addr(scratch), rows, cols, int(dy.dtype is torch.bfloat16))
     return dict(dx=dx, dweight=dweight)

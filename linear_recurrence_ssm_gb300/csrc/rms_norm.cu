@@ -20,7 +20,7 @@ using gated::quantised;
 using gated::scale_of;
 
 constexpr int kVec = 8;                 // elements of an access
-constexpr int kParts = 608;             // most partial sums of dw: four thread blocks a SM
+constexpr int kParts = 1216;            // most partial sums of dw: eight thread blocks a SM (four: 115 against 95 us)
 
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16(v); }
@@ -447,7 +447,7 @@ cudaError_t bwd(const BwdArgs<T> &a, cudaStream_t st) {
         if (vecs <= 8) return go<T, 8, 1, 2>(a, st);
         if (vecs <= 16) return go<T, 16, 1, 2>(a, st);
         if (vecs <= 32) return go<T, 32, 1, 2>(a, st);
-        if (vecs <= 512) return go<T, 0, 1, 2>(a, st);
+        if (vecs <= 512) return go<T, 0, 1, 1>(a, st);
         return go<T, 0, 2, 1>(a, st);
     }
     if (a.rows > 0x7fffffff) return cudaErrorInvalidConfiguration;
