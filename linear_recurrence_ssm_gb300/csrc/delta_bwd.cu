@@ -212,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) back_kernel(const BwdArgs<bf> p, 
             }
             // shares of dbeta, dV, and -Gam beta Z
             float *part = p.dbeta_part + (((int64_t(slice) * kChain + warp) * slots + span.slot + c) * s.H + head) * kBlock;
+            float sums[8][2];
             __syncwarp();
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -220,14 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1) back_kernel(const BwdArgs<bf> p, 
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int n = 2 * t + h;
-                    float a = w[n][0] * low(x[2 * h]) + w[n][2] * low(x[2 * h + 1]);
-                    float b = w[n][1] * high(x[2 * h]) + w[n][3] * high(x[2 * h + 1]);
-#pragma unroll
-                    for (int o = 4; o < 32; o *= 2) {
-                        a += __shfl_xor_sync(0xffffffffu, a, o);
-                        b += __shfl_xor_sync(0xffffffffu, b, o);
-                    }
-                    if (g == 0) *reinterpret_cast<float2 *>(part + 8 * n + c2) = make_float2(a, b);
+                    sums[n][0] = w[n][0] * low(x[2 * h]) + w[n][2] * low(x[2 * h + 1]);
+                    sums[n][1] = w[n][1] * high(x[2 * h]) + w[n][3] * high(x[2 * h + 1]);
                     const float2 beta = *reinterpret_cast<const float2 *>(f.beta + 8 * n + c2);
                     const float2 start = *reinterpret_cast<const float2 *>(f.start + 8 * n + c2);
                     w[n][0] *= beta.x, w[n][1] *= beta.y, w[n][2] *= beta.x, w[n][3] *= beta.y;
@@ -236,6 +231,19 @@ __global__ void __launch_bounds__(kThreads, 1) back_kernel(const BwdArgs<bf> p, 
                 }
                 store_turned(room, t, w);
             }
+            // of the columns' sums over eight lanes each lane keeps those of one n
+#pragma unroll
+            for (int half = 4; half > 0; half /= 2) {
+                const bool upper = (g & half) != 0;
+#pragma unroll
+                for (int n = 0; n < half; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float give = upper ? sums[n][e] : sums[n + half][e];
+                        sums[n][e] = (upper ? sums[n + half][e] : sums[n][e]) + __shfl_xor_sync(0xffffffffu, give, 4 * half);
+                    }
+            }
+            *reinterpret_cast<float2 *>(part + 8 * g + c2) = make_float2(sums[0][0], sums[0][1]);
             __syncwarp();
             write_turned(p.dv + row * v_step + int64_t(head) * s.V + mine, v_step, rows, width, room);
             __syncwarp();

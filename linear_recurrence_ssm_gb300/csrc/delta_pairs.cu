@@ -109,10 +109,11 @@ pairs_kernel(const Shape s, const __grid_constant__ PairMaps maps, const bf *g, 
         const int at = i * kPairThreads + tid, t = at / 8, r = at % 8 * 8;
         uint32_t h[4], l[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float a = r + 2 * e < t ? -system[t * kPairStride + r + 2 * e] : 0.0f;
-            const float b = r + 2 * e + 1 < t ? -system[t * kPairStride + r + 2 * e + 1] : 0.0f;
-            split(a, b, h[e], l[e]);
+        for (int e = 0; e < 4; e += 2) {
+            const int s0 = r + 2 * e;
+            const float4 v = *reinterpret_cast<const float4 *>(system + t * kPairStride + s0);
+            split(s0 < t ? -v.x : 0.0f, s0 + 1 < t ? -v.y : 0.0f, h[e], l[e]);
+            split(s0 + 2 < t ? -v.z : 0.0f, s0 + 3 < t ? -v.w : 0.0f, h[e + 1], l[e + 1]);
         }
         unsigned char *out = mem + place<64>(0, t, r);
         *reinterpret_cast<uint4 *>(out) = make_uint4(h[0], h[1], h[2], h[3]);
