@@ -388,7 +388,7 @@ block_kernel(const BwdArgs<bf> p, const __grid_constant__ BlockMaps maps, const 
         float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll 1
         for (int n = 0; n <= j; ++n) {
-            float a[2][4] = {}, m[2][4] = {};
+            float a[2][4] = {}, m[2][4] = {}, down[4];
 #pragma unroll
             for (int v = 0; v < VP / 16; ++v) {
                 uint32_t b[4];
@@ -417,17 +417,18 @@ block_kernel(const BwdArgs<bf> p, const __grid_constant__ BlockMaps maps, const 
                 const float m0 = t > r ? x0 * m[e][0] : 0.0f, m1 = t > r + 1 ? x1 * m[e][1] : 0.0f;
                 const float m2 = t + 8 > r ? x2 * m[e][2] : 0.0f, m3 = t + 8 > r + 1 ? x3 * m[e][3] : 0.0f;
                 sum0 += m0 + m1, sum1 += m2 + m3;
-                float down0 = m0 + m2, down1 = m1 + m3;
-#pragma unroll
-                for (int o = 4; o < 32; o *= 2) {
-                    down0 += __shfl_xor_sync(0xffffffffu, down0, o);
-                    down1 += __shfl_xor_sync(0xffffffffu, down1, o);
-                }
-                if (g == 0) *reinterpret_cast<float2 *>(&col_sum[warp][r]) = make_float2(down0, down1);
+                down[2 * e] = m0 + m2, down[2 * e + 1] = m1 + m3;
                 const uint32_t w0 = pack(x0, x1), w1 = pack(x2, x3);
                 asm volatile("st.shared.b32 [%0], %1;" ::"r"(place<64>(out, t, r & ~7) + (r & 7) * 2), "r"(w0) : "memory");
                 asm volatile("st.shared.b32 [%0], %1;" ::"r"(place<64>(out, t + 8, r & ~7) + (r & 7) * 2), "r"(w1) : "memory");
             }
+            // of the four columns' sums over the rows, each lane keeps one
+            const bool upper = (g & 4) != 0, odd = (g & 2) != 0;
+            const float of0 = (upper ? down[2] : down[0]) + __shfl_xor_sync(0xffffffffu, upper ? down[0] : down[2], 16);
+            const float of1 = (upper ? down[3] : down[1]) + __shfl_xor_sync(0xffffffffu, upper ? down[1] : down[3], 16);
+            float sum = (odd ? of1 : of0) + __shfl_xor_sync(0xffffffffu, odd ? of0 : of1, 8);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+            if (g % 2 == 0) col_sum[warp][16 * n + 8 * upper + c2 + odd] = sum;
         }
 #pragma unroll
         for (int o = 1; o < 4; o *= 2) {
@@ -480,22 +481,22 @@ block_kernel(const BwdArgs<bf> p, const __grid_constant__ BlockMaps maps, const 
                 product(dk[2 * n + 1], z, b[n][2], b[n][3]);
             }
         }
-        const auto pair_at = [&](uint32_t tile, int t, int k) {
-            uint32_t v;
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(place<KP>(tile, t, k & ~7) + (k & 7) * 2) : "memory");
-            return v;
-        };
 #pragma unroll
-        for (int n = 0; n < tiles; ++n) {
-            const int k = k0 + 8 * n + c2;
-            dq[n][0] = kept(s.scale * start0, dq[n][0]), dq[n][1] = kept(s.scale * start0, dq[n][1]);
-            dq[n][2] = kept(s.scale * start1, dq[n][2]), dq[n][3] = kept(s.scale * start1, dq[n][3]);
-            dk[n][0] = kept(-start0, dk[n][0]), dk[n][1] = kept(-start0, dk[n][1]);
-            dk[n][2] = kept(-start1, dk[n][2]), dk[n][3] = kept(-start1, dk[n][3]);
-            const uint32_t q0 = pair_at(base + L::q, t0, k), q1 = pair_at(base + L::q, t1, k);
-            const uint32_t e0 = pair_at(base + L::k, t0, k), e1 = pair_at(base + L::k, t1, k);
-            rt0 += dq[n][0] * low(q0) + dq[n][1] * high(q0) + dk[n][0] * low(e0) + dk[n][1] * high(e0);
-            rt1 += dq[n][2] * low(q1) + dq[n][3] * high(q1) + dk[n][2] * low(e1) + dk[n][3] * high(e1);
+        for (int m = 0; m < tiles / 2; ++m) {
+            uint32_t qs[4], ks[4];      // rows t0 and t1, columns c2 of tiles 2 m and 2 m + 1
+            load4(qs, four<KP>(base + L::q, 16 * j, k0 + 16 * m));
+            load4(ks, four<KP>(base + L::k, 16 * j, k0 + 16 * m));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int n = 2 * m + e;
+                const uint32_t q0 = qs[2 * e], q1 = qs[2 * e + 1], e0 = ks[2 * e], e1 = ks[2 * e + 1];
+                dq[n][0] = kept(s.scale * start0, dq[n][0]), dq[n][1] = kept(s.scale * start0, dq[n][1]);
+                dq[n][2] = kept(s.scale * start1, dq[n][2]), dq[n][3] = kept(s.scale * start1, dq[n][3]);
+                dk[n][0] = kept(-start0, dk[n][0]), dk[n][1] = kept(-start0, dk[n][1]);
+                dk[n][2] = kept(-start1, dk[n][2]), dk[n][3] = kept(-start1, dk[n][3]);
+                rt0 += dq[n][0] * low(q0) + dq[n][1] * high(q0) + dk[n][0] * low(e0) + dk[n][1] * high(e0);
+                rt1 += dq[n][2] * low(q1) + dq[n][3] * high(q1) + dk[n][2] * low(e1) + dk[n][3] * high(e1);
+            }
         }
         // through the pairs: dQ += (dP D) K, dK += (dAb D) K + (dAb D)^T K + (dP D)^T Q
 #pragma unroll 1
@@ -533,20 +534,27 @@ block_kernel(const BwdArgs<bf> p, const __grid_constant__ BlockMaps maps, const 
                 }
             }
         }
+        // two tiles at a time: a lane takes two of its columns and two of its neighbour's, so
+        // that 32 bytes of a row are one access
         const auto write = [&](bf *whole, float *of_head, const float (&v)[tiles][4]) {
+            const bool odd = lane % 2 != 0;
 #pragma unroll
-            for (int n = 0; n < tiles; ++n) {
-                const int k = k0 + 8 * n + c2;
-                if (k >= s.K) continue;
+            for (int m = 0; m < tiles / 2; ++m)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int t = t0 + 8 * e;
-                    if (t >= rows) continue;
-                    const int64_t o = ((row + t) * s.H + head) * s.K + k;
-                    if (s.H > s.G) *reinterpret_cast<float2 *>(of_head + o) = make_float2(v[n][2 * e], v[n][2 * e + 1]);
-                    else *reinterpret_cast<uint32_t *>(whole + o) = pack(v[n][2 * e], v[n][2 * e + 1]);
+                    const int t = t0 + 8 * e, k = k0 + 16 * m;
+                    const int64_t o = ((row + t) * s.H + head) * s.K;
+                    const float *a = v[2 * m] + 2 * e, *b = v[2 * m + 1] + 2 * e;
+                    if (s.H > s.G) {
+                        if (t < rows && k + c2 < s.K) *reinterpret_cast<float2 *>(of_head + o + k + c2) = make_float2(a[0], a[1]);
+                        if (t < rows && k + 8 + c2 < s.K) *reinterpret_cast<float2 *>(of_head + o + k + 8 + c2) = make_float2(b[0], b[1]);
+                        continue;
+                    }
+                    const uint32_t even = pack(a[0], a[1]), next = pack(b[0], b[1]);
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? even : next, 1);
+                    const int at = k + 8 * odd + (c2 & 4);
+                    if (t < rows && at < s.K) *reinterpret_cast<uint2 *>(whole + o + at) = odd ? make_uint2(got, next) : make_uint2(even, got);
                 }
-            }
         };
         write(p.dq, p.dq_head, dq);
         // through the adjoint of the state behind the block, in dQ's place
@@ -568,13 +576,18 @@ block_kernel(const BwdArgs<bf> p, const __grid_constant__ BlockMaps maps, const 
         }
         const float by0 = end0 * d.beta[t0], by1 = end1 * d.beta[t1];
 #pragma unroll
-        for (int n = 0; n < tiles; ++n) {
-            const int k = k0 + 8 * n + c2;
-            const uint32_t e0 = pair_at(base + L::k, t0, k), e1 = pair_at(base + L::k, t1, k);
-            const float a = kept(by0, dq[n][0]), b = kept(by0, dq[n][1]), x = kept(by1, dq[n][2]), y = kept(by1, dq[n][3]);
-            ct0 += a * low(e0) + b * high(e0);
-            ct1 += x * low(e1) + y * high(e1);
-            dk[n][0] += a, dk[n][1] += b, dk[n][2] += x, dk[n][3] += y;
+        for (int m = 0; m < tiles / 2; ++m) {
+            uint32_t ks[4];
+            load4(ks, four<KP>(base + L::k, 16 * j, k0 + 16 * m));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int n = 2 * m + e;
+                const uint32_t e0 = ks[2 * e], e1 = ks[2 * e + 1];
+                const float a = kept(by0, dq[n][0]), b = kept(by0, dq[n][1]), x = kept(by1, dq[n][2]), y = kept(by1, dq[n][3]);
+                ct0 += a * low(e0) + b * high(e0);
+                ct1 += x * low(e1) + y * high(e1);
+                dk[n][0] += a, dk[n][1] += b, dk[n][2] += x, dk[n][3] += y;
+            }
         }
         write(p.dk, p.dk_head, dk);
     }
