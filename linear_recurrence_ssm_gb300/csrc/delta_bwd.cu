@@ -639,7 +639,7 @@ static bool on16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 
 
 bool fits(const BwdArgs<bf> &a) {
     return fits_bwd(a.s) && on16(a.q) && on16(a.k) && on16(a.dy) && on16(a.states) && on16(a.errors) && on16(a.dv) &&
-           reinterpret_cast<uintptr_t>(a.dq) % 4 == 0 && reinterpret_cast<uintptr_t>(a.dk) % 4 == 0;
+           reinterpret_cast<uintptr_t>(a.dq) % 8 == 0 && reinterpret_cast<uintptr_t>(a.dk) % 8 == 0;
 }
 
 template <int KP>

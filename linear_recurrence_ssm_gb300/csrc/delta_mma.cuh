@@ -92,28 +92,11 @@ __device__ __forceinline__ uint32_t four_across(uint32_t tile, int r, int c) {
     return place<WIDTH, ROWS>(tile, r + (lane & 7) + (lane >> 4) * 8, c + ((lane >> 3) & 1) * 8);
 }
 
-// `rows` rows of `width` elements (a multiple of 8) into a tile of 64 x WIDTH, zeros around them.
-template <int WIDTH, int THREADS>
-__device__ __forceinline__ void copy_tile(uint32_t tile, const bf *src, int64_t step, int rows, int width, int tid) {
-#pragma unroll
-    for (int i = 0; i < kBlock * WIDTH / 8 / THREADS; ++i) {
-        const int at = i * THREADS + tid, row = at / (WIDTH / 8), col = at % (WIDTH / 8) * 8;
-        const bool in = row < rows && col < width;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(place<WIDTH>(tile, row, col)),
-                     "l"(in ? src + row * step + col : src), "r"(in ? 16 : 0)
-                     : "memory");
-    }
-}
-
 __device__ __forceinline__ uint4 load16(uint32_t at) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
     return v;
 }
-__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(from) : "memory");
-}
-
 __device__ __forceinline__ void put_values(uint32_t at, const float (&v)[4]) {
     asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
 }
@@ -532,15 +515,20 @@ inline int64_t record_bytes(const Shape &s) { return s.slots() * s.H * kRecord; 
 // ... and whose block fits shared memory.
 inline bool fits_bwd(const Shape &s) { return fits(s) && s.V <= 128; }
 // Blocks a part, or 0 for whole sequences: a chain is one head's slice of 64
-// values, at most one a SM at a time.  In parts, every block is walked twice
-// more or so (its own 64 rows and the K rows that its turning of the state
-// takes, two thread blocks a SM, then the outputs), so that parts pay where the
-// chains fill a small share of the 152 SMs: measured at 65536 steps of 8 heads
-// of 128 x 128 (16 chains): whole 3.07 ms.
+// values, at most one a SM at a time.  In parts, every block is walked about
+// twice more (its own 64 rows and the K rows that its turning of the state
+// takes, then the outputs), so that parts pay where the chains fill a small
+// share of the 152 SMs.  The bound lies between the sizes measured on either
+// side, calls of one sequence, whole against in parts:
+//   16384 steps, K = V = 128: 8 heads 743 / 287 us, 24 heads 815 / 667, 32 heads 850 / 888
+//   4096 steps,  K = V = 128: 8 heads 194 / 128, 16 heads 203 / 167, 32 heads 220 / 259
+//   16384 steps, K = 128, V = 64: 16 heads 777 / 364, 32 heads 841 / 694
+//   16384 steps, K = V = 64: 32 heads 644 / 445, 64 heads 758 / 764
+// and, of the lengths, 8 heads: 1024 steps 58 / 65, 1536 steps 81 / 71, 2048 steps 103 / 88.
 inline int part_blocks(const Shape &s) {
     const int64_t slices = (s.V + 63) / 64, keys = (s.K + 63) / 64, chains = s.n * int64_t(s.H) * slices;
     const int64_t longest = (s.L + kBlock - 1) / kBlock;
-    if (longest < 24 || chains * (3 * slices + keys) > 152 * 2 * slices) return 0;
+    if (longest < 24 || chains * (3 * slices + keys) > 228 * slices) return 0;
     const int64_t total = s.slots() * s.H * slices, part = (total + 151) / 152;
     return int(part < 8 ? 8 : part);
 }
