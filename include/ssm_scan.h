@@ -499,8 +499,9 @@ SSM_API ssm_status_t state_pages_compact(void *pool, uint8_t *used, int32_t *mov
  *          unspecified afterwards
  * The state and every sum are fp32.  bf16 inputs: see the kernels for what the
  * tensor cores' operands are rounded to.  A NaN or an infinity in a step's
- * inputs makes the outputs of that head's whole block of 64 steps and of
- * everything behind it in the same sequence unspecified; no other sequence.
+ * inputs makes the outputs of that head's whole block of 64 steps unspecified,
+ * and of everything behind it in the same sequence up to a step of a later block
+ * that drops the state; no other sequence.
  * Supported (SSM_ERR_UNSUPPORTED otherwise): K, V <= 256.  G divides H.
  * Every pointer is aligned to its element size (SSM_ERR_ALIGNMENT).
  */
@@ -521,7 +522,9 @@ SSM_API int64_t delta_rule_fwd_scratch(int64_t Bs, int64_t L, int64_t G, int64_t
  *   dg, dbeta : (Bs, L, H), dy's type   dh0 : as h0, fp32, or NULL
  *   scratch : delta_rule_bwd_scratch bytes of the caller's, 16-byte aligned;
  *             unspecified afterwards
- * Deterministic.  The other rules as delta_rule_fwd.
+ * Deterministic.  A NaN or an infinity in the kept states or errors of a block
+ * of 64 steps makes that head's (and its group's) gradients there unspecified.  The other rules as
+ * delta_rule_fwd.
  */
 SSM_API int64_t delta_rule_bwd_scratch(int64_t Bs, int64_t L, int64_t G, int64_t H, int64_t K,
                                        int64_t V, int64_t n_seq, int io_bf16);

@@ -11,7 +11,9 @@
 // N and P come from pairs_kernel.  One thread asks for the tensor copies of the
 // next block: memory takes its 64 KB slower than warps can ask for them piece by
 // piece (a chain that did so stood still for 1000 of 6300 cycles, its outputs
-// for 3500).
+// for 3500).  4 x 4096 steps of 32 heads of 64 x 128 take 196 us, 3.06 a block of
+// 64 steps: the tensor cores are busy 51 % of it, and the rest is the chain's
+// dependent products (S K^T, N beta W, E U K) waiting for one another.
 //
 // Operands of the state's own chain (S, beta W, N, E U) go into the tensor
 // cores as two bf16 terms, 16 bits, so that the final state is good to 2^-17
@@ -65,16 +67,24 @@ fwd_kernel(const FwdArgs<bf> p, const __grid_constant__ Maps maps) {
     const int height = turning ? s.K : s.V, v0 = (turning ? slice - of_values : slice) * kSlice;
     const int64_t index = blockIdx.x / slices / s.H;        // of the sequence, or of the part's place
     int seq = int(index), part = 0;
+    // A grid may not end before the one ahead of it, since the next one waits for
+    // this one alone: blocks without work wait too.
     if (p.part) {
         seq = part_sequence_of(s, index, p.part, &found);
-        if (seq < 0) return;
+        if (seq < 0) {
+            wait_for_last();
+            return;
+        }
     }
     Span span = span_of(s, seq);
     bool last_part = true;
     if (p.part) {
         part = int(index - first_part(s, span, seq, p.part));
         last_part = part + 1 == parts_of(span, p.part);
-        if (CARRY && (last_part || (turning && part == 0 && !p.h0))) return;
+        if (CARRY && (last_part || (turning && part == 0 && !p.h0))) {
+            wait_for_last();
+            return;
+        }
         const int first = part * p.part;
         span.first += int64_t(first) * kBlock;
         span.slot += first;
@@ -179,6 +189,13 @@ fwd_kernel(const FwdArgs<bf> p, const __grid_constant__ Maps maps) {
                     split(beta.x * x[2], beta.y * x[3], hi[t][2 * h + 1], lo[t][2 * h + 1]);
                 }
             }
+            // of a block with a cut: what is not finite in the state stays out of the steps behind it
+            const float last = f.last;
+            unsigned bad = 0;
+            if (last == 0.0f && (bad = not_finite(st)) != 0) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) drop(hi[t], bad, f.start + 16 * t), drop(lo[t], bad, f.start + 16 * t);
+            }
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 uint32_t n[4][4], rest[4][4];
@@ -209,8 +226,17 @@ fwd_kernel(const FwdArgs<bf> p, const __grid_constant__ Maps maps) {
                 }
                 if (!CARRY) store4(four<64, 16>(hand_u, 0, 16 * t), u);
             }
+            if (!CARRY && __any_sync(0xffffffffu, bad)) {
+                __syncwarp();
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    uint32_t u[4];
+                    load4(u, four<64, 16>(hand_u, 0, 16 * t));
+                    drop(u, bad, f.start + 16 * t);
+                    store4(four<64, 16>(hand_u, 0, 16 * t), u);
+                }
+            }
             // S
-            const float last = f.last;
 #pragma unroll
             for (int n = 0; n < KP / 8; ++n)
 #pragma unroll
@@ -318,6 +344,7 @@ __global__ void __launch_bounds__(128 * kJoinSplit) join_kernel(const FwdArgs<bf
         const float added = has ? p.added[(at * s.V + v0 + mine) * s.K + k] : 0.0f;
         const float *turned = p.turned + at * s.K * s.K + k;
         float sum[kJoinRows] = {};
+        uint32_t any = 0;
         __syncthreads();
         // the first part starts from h0: nothing was made of it, unless there is one
         if (in && (i > 0 || p.h0)) {
@@ -327,6 +354,8 @@ __global__ void __launch_bounds__(128 * kJoinSplit) join_kernel(const FwdArgs<bf
 #pragma unroll
                 for (int j = 0; j < 16; ++j) t[j] = m + j < to ? turned[int64_t(m + j) * s.K] : 0.0f;
 #pragma unroll
+                for (int j = 0; j < 16; ++j) any |= __float_as_uint(t[j]) << 1;
+#pragma unroll
                 for (int j = 0; j < 16; ++j)
 #pragma unroll
                     for (int v = 0; v < kJoinRows; ++v) sum[v] += S[v][min(m + j, 127)] * t[j];
@@ -334,10 +363,13 @@ __global__ void __launch_bounds__(128 * kJoinSplit) join_kernel(const FwdArgs<bf
         }
 #pragma unroll
         for (int v = 0; v < kJoinRows; ++v) shares[quarter][v][k] = sum[v];
-        __syncthreads();
+        // a part that makes nothing of a state (a step in it has no decay left) drops it, whatever it holds
+        const bool reaches = __syncthreads_or(any != 0);
         float all = added;
+        if (reaches) {
 #pragma unroll
-        for (int j = 0; j < kJoinSplit; ++j) all += shares[j][mine][k];
+            for (int j = 0; j < kJoinSplit; ++j) all += shares[j][mine][k];
+        }
         S[mine][k] = all;
         if (has) p.entering[((at + s.H) * s.V + v0 + mine) * s.K + k] = all;
     }

@@ -147,6 +147,30 @@ __device__ __forceinline__ void wait_for(uint64_t *bar, int phase, int *abort, u
 // by v, and 0 for by = 0 whatever v holds.
 __device__ __forceinline__ float kept(float by, float v) { return by == 0.0f ? 0.0f : by * v; }
 
+// Whether this lane's rows g and g + 8 of the state hold what is not finite (bits 0 and 1).
+template <int N>
+__device__ __forceinline__ unsigned not_finite(const float (&st)[N][4]) {
+    unsigned bad = 0;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bad |= (__float_as_uint(st[n][e]) & 0x7f800000u) == 0x7f800000u ? 1u << e / 2 : 0u;
+    bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+    return bad | __shfl_xor_sync(0xffffffffu, bad, 2);
+}
+// Those rows become 0 in the packed columns of 16 steps that the state still
+// reaches (`start` above 0): a cut keeps the state out of the steps behind it,
+// but 0 times what it holds may not be 0.
+__device__ __forceinline__ void drop(uint32_t (&w)[4], unsigned bad, const float *start) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float2 by = *reinterpret_cast<const float2 *>(start + 8 * h + threadIdx.x % 4 * 2);
+        const uint32_t keep = (by.x > 0.0f ? 0u : 0xffffu) | (by.y > 0.0f ? 0u : 0xffff0000u);
+        if (bad & 1) w[2 * h] &= keep;
+        if (bad & 2) w[2 * h + 1] &= keep;
+    }
+}
+
 // d += a b for 64 columns (from column 16 `from`) of b.
 __device__ __forceinline__ void across(float (&d)[8][4], const uint32_t (&a)[4], const uint32_t (&b)[4][4], int from = 0) {
 #pragma unroll

@@ -137,3 +137,38 @@ def test_page_calls_on_the_rule_s_pool(cuda_device):
     y = lrs.delta_rule_step(**token(2, slice(2, 4)), states=pool, pages=pages)
     three = {n: torch.stack((w[0, 0], w[2, 1], w[2, 2]))[None] for n, w in i.items()}
     close(y[:1], delta.delta_rule(**three)["y"][:, 2])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 64), (40, 24), (20, 33)])
+@pytest.mark.parametrize("L,at", [(100, 10), (200, 64), (200, 75), (130, 129), (2000, 5), (2000, 1100)])
+def test_a_step_without_decay_left_drops_a_nan_state_wherever_it_lies(cuda_device, dtype, K, V, L, at):
+    i, rest = inputs(10, 2, L, 1, 2, K, V, dtype)
+    i["g"][:, at, 0] = float("-inf")
+    h0 = torch.full_like(rest["h0"], float("nan"))
+    y, hf = lrs.delta_rule_fwd(**cuda(i, cuda_device), h0=h0.to(cuda_device), return_final_state=True)
+    want = delta.delta_rule(**{n: w[:, at:].contiguous() for n, w in i.items()})
+    close(y[:, at:, :1], want["y"][:, :, :1], terms=want["y_terms"][:, :, :1])
+    close(hf[:, 0], want["h_final"][:, 0])
+    # before it, and in the head without such a step, the NaN stands
+    assert torch.isnan(y[:, :at]).all() and torch.isnan(y[:, :, 1]).all() and torch.isnan(hf[:, 1]).all()
+
+
+def test_many_sequences_of_one_part(cuda_device):
+    """So many steps that sequences are taken in parts, and none longer than a part."""
+    i, rest = inputs(11, 1, 2048, 1, 2, 64, 64, BF, n=8)
+    check(i, rest, cuda_device, [256 * n for n in range(9)], h0=False)
+    check(i, rest, cuda_device, [0, 0, 0, 0, 1, 1, 1, 500, 501])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("g", [-101.0, float("-inf")])
+def test_a_token_without_decay_left_drops_a_nan_state(cuda_device, dtype, g):
+    i, _ = inputs(12, 2, 1, 1, 2, 64, 64, dtype)
+    i = {n: w[:, 0].contiguous() for n, w in i.items()}
+    i["g"].fill_(g)
+    pool = torch.full((2, 2, 64, 64), float("nan"), device=cuda_device)
+    y = lrs.delta_rule_step(**cuda(i, cuda_device), states=pool)
+    want, after = delta.delta_rule_step(**i, states=torch.zeros(2, 2, 64, 64), pages=None)
+    close(y, want)
+    close(pool, after)
