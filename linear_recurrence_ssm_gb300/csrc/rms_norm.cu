@@ -8,6 +8,8 @@
 // row's sum and its outputs.  A row of up to 256 columns takes 8, 16 or 32
 // lanes, a longer one a thread block of as many warps as its vectors of eight
 // need at one to four a thread.
+#include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "gated_scan.cuh"
@@ -20,7 +22,7 @@ using gated::quantised;
 using gated::scale_of;
 
 constexpr int kVec = 8;                 // elements of an access
-constexpr int kParts = 1216;            // most partial sums of dw: eight thread blocks a SM (four: 115 against 95 us)
+constexpr int kParts = 1216;            // most partial sums of dw
 
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16(v); }
@@ -240,9 +242,12 @@ struct BwdArgs {
 // A thread keeps its columns over all rows of its block, so that dw's partial
 // sums stay in registers; a block writes one part.  ROWS rows at a time, all
 // their loads ahead of the sums; what was read is kept as it was read and
-// unpacked twice, which takes half the registers of its values.
+// unpacked twice, which takes half the registers of its values.  A block a row
+// is held to 64 registers: more rows in flight on a SM are worth more than none
+// spilled (16384 x 2560 bf16 without the residual, dw included: 77 us, with 71
+// registers 91; 8192 x 4096: 65 and 92).
 template <typename T, int LANES, int VECS, int ROWS>
-__global__ void __launch_bounds__(LANES ? 256 : 512, LANES ? 2 : 1) bwd_kernel(const BwdArgs<T> p) {
+__global__ void __launch_bounds__(LANES ? 256 : 512, LANES || VECS == 1 ? 2 : 1) bwd_kernel(const BwdArgs<T> p) {
     __shared__ float mem[2][32][ROWS];
     __shared__ float fold[LANES ? 8 : 1][LANES ? LANES * kVec : 1];
     const int lanes = LANES ? LANES : int(blockDim.x), lane = threadIdx.x % lanes;
@@ -413,10 +418,12 @@ cudaError_t fwd(const FwdArgs<T> &a, cudaStream_t st) {
     const int64_t vecs = a.cols / kVec;
     if (a.cols % kVec == 0 && vecs <= 4096 && on16(a.x) && on16(a.residual) && on16(a.weight) && on16(a.sum) &&
         on16(a.y) && reinterpret_cast<uintptr_t>(a.q) % 8 == 0) {
+        // lanes of a warp up to 256 columns (bf16, 100000 x 256 with a residual: 38 us, as a block a row
+        // 58; 400000 x 64: 37 and 210); then two vectors a thread (16384 x 2048 to 8 bits: 37.5, one
+        // 43.6; 32768 x 1024: 37.5 and 42.6), four where 1024 threads would not do otherwise
         if (vecs <= 8) return go<T, 8, 1>(a, st);
         if (vecs <= 16) return go<T, 16, 1>(a, st);
         if (vecs <= 32) return go<T, 32, 1>(a, st);
-        if (vecs <= 128) return go<T, 0, 1>(a, st);
         if (vecs <= 1024) return go<T, 0, 2>(a, st);
         return go<T, 0, 4>(a, st);
     }
@@ -430,10 +437,31 @@ static cudaError_t fold(const float *parts, float *dweight, int64_t n, int64_t c
     return cudaGetLastError();
 }
 
+// The blocks of `threads` that run at a time, at most kParts: a kernel of as many
+// has no last round that leaves SMs idle, and the fewest partial sums (with two
+// vectors a thread, 16384 x 2560: 1216 blocks 90 us, as many as run 84).
+template <auto KERNEL>
+static cudaError_t at_a_time(unsigned threads, int *blocks) {
+    static std::atomic<int> known[17];          // by warps; the same on every GPU of this kind
+    std::atomic<int> &kept = known[threads / 32];
+    *blocks = kept.load(std::memory_order_relaxed);
+    if (*blocks) return cudaSuccess;
+    int device = 0, sms = 0, each = 0;
+    if (cudaError_t e = cudaGetDevice(&device)) return e;
+    if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device)) return e;
+    if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&each, KERNEL, int(threads), 0)) return e;
+    *blocks = std::min(std::max(sms * each, 1), kParts);
+    kept.store(*blocks, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
 template <typename T, int LANES, int VECS, int ROWS>
 static cudaError_t go(const BwdArgs<T> &a, cudaStream_t st) {
     const unsigned threads = LANES ? 256 : threads_for(a.cols / kVec, VECS), per = ROWS * (LANES ? 256 / LANES : 1);
-    const int64_t blocks = (a.rows + per - 1) / per, grid = blocks < kParts ? blocks : kParts;
+    const int64_t blocks = (a.rows + per - 1) / per;
+    int most = 0;
+    if (cudaError_t e = at_a_time<bwd_kernel<T, LANES, VECS, ROWS>>(threads, &most)) return e;
+    const int64_t grid = blocks < most ? blocks : most;
     bwd_kernel<T, LANES, VECS, ROWS><<<unsigned(grid), threads, 0, st>>>(a);
     if (cudaError_t e = cudaGetLastError()) return e;
     return a.dweight ? fold(a.parts, a.dweight, grid, a.cols, st) : cudaSuccess;
@@ -444,6 +472,9 @@ cudaError_t bwd(const BwdArgs<T> &a, cudaStream_t st) {
     const int64_t vecs = a.cols / kVec;
     if (a.cols % kVec == 0 && vecs <= 1024 && on16(a.dy) && on16(a.s) && on16(a.residual) && on16(a.ds) && on16(a.weight) &&
         on16(a.dx) && on16(a.parts)) {
+        // lanes of a warp up to 256 columns (bf16, 100000 x 256: 53 us, as a block a row 98); then one
+        // vector a thread (16384 x 2048: 61, two 66; 8192 x 4096: 65 and 67), two where 512 threads would
+        // not do otherwise
         if (vecs <= 8) return go<T, 8, 1, 2>(a, st);
         if (vecs <= 16) return go<T, 16, 1, 2>(a, st);
         if (vecs <= 32) return go<T, 32, 1, 2>(a, st);

@@ -172,3 +172,40 @@ def test_a_token_without_decay_left_drops_a_nan_state(cuda_device, dtype, g):
     want, after = delta.delta_rule_step(**i, states=torch.zeros(2, 2, 64, 64), pages=None)
     close(y, want)
     close(pool, after)
+
+
+def test_parts_on_another_stream_and_in_a_graph(cuda_device):
+    """A long sequence of few heads: four kernels that begin while the one before runs."""
+    i, rest = inputs(13, 1, 2500, 1, 2, 128, 64, BF, n=3)
+    c, h0 = cuda(i, cuda_device), rest["h0"].to(cuda_device)
+    o = torch.tensor([0, 700, 700, 2490], dtype=torch.int32, device=cuda_device)
+    call = lambda: lrs.delta_rule_fwd(**c, offsets=o, h0=h0, return_final_state=True)  # noqa: E731
+    first = call()
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(other):
+        second = [call() for _ in range(3)]
+    other.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        third = call()
+    for _ in range(3):
+        for t in third:
+            t.fill_(float("nan"))
+        graph.replay()
+    torch.cuda.synchronize()
+    for out in (*second, third):
+        assert all(torch.equal(a, b) for a, b in zip(first, out))
+
+
+@pytest.mark.parametrize("offsets", [[0, 2400, 100, 2000, 10 ** 9], [-5, 2500, 0, 2500, 0], [2000, 1500, 1000, 500, 0]])
+def test_bad_offsets_of_long_sequences_touch_nothing_outside(cuda_device, offsets):
+    i, rest = inputs(14, 1, 2500, 1, 2, 64, 64, BF, n=4)
+    o = torch.tensor(offsets, dtype=torch.int32, device=cuda_device)
+    c = cuda(i, cuda_device)
+    room = torch.full((4096 + 2500 * 2 * 64 + 4096,), 7.0, dtype=BF, device=cuda_device)
+    lrs.delta_rule_fwd(**c, offsets=o, h0=rest["h0"].to(cuda_device), return_final_state=True,
+                       y=room[4096:-4096].view(1, 2500, 2, 64))
+    torch.cuda.synchronize()
+    assert torch.all(room[:4096] == 7.0) and torch.all(room[-4096:] == 7.0)
+    lrs.ssm_check_device_errors()
