@@ -12,8 +12,9 @@
 // the adjoints, dY, X and dV.
 //
 // 4 x 4096 steps of 32 heads of 64 x 128: the chain 264 us (tensor cores 47 %, its
-// products wait for one another), the blocks 301 (issue 41 %, shared memory 60 %:
-// seven operands of 8 to 16 KB are read by eight warps each).
+// products wait for one another), the blocks 301 (issue 43 %, shared memory 48 %,
+// tensor cores 33 %; barriers are a fifth of the stalls: two thread blocks of eight
+// warps are all that a SM's shared memory holds).
 #include "delta_mma.cuh"
 
 namespace ssm {
