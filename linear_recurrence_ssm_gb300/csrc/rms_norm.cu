@@ -67,11 +67,13 @@ __device__ __forceinline__ void row_sums(float (&v)[ROWS], float (*mem)[ROWS]) {
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) mem[warp][r] = v[r];
         __syncthreads();
+        const int lane = threadIdx.x % 32;
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) v[r] = 0.0f;
-        for (int i = 0; i < int(blockDim.x / 32); ++i)
+        for (int r = 0; r < ROWS; ++r) {
+            v[r] = lane < int(blockDim.x / 32) ? mem[lane][r] : 0.0f;
 #pragma unroll
-            for (int r = 0; r < ROWS; ++r) v[r] += mem[i][r];
+            for (int o = 16; o > 0; o /= 2) v[r] += __shfl_xor_sync(0xffffffffu, v[r], o);
+        }
     }
 }
 
@@ -243,9 +245,8 @@ struct BwdArgs {
 // sums stay in registers; a block writes one part.  ROWS rows at a time, all
 // their loads ahead of the sums; what was read is kept as it was read and
 // unpacked twice, which takes half the registers of its values.  A block a row
-// is held to 64 registers: more rows in flight on a SM are worth more than none
-// spilled (16384 x 2560 bf16 without the residual, dw included: 77 us, with 71
-// registers 91; 8192 x 4096: 65 and 92).
+// is held to 64 registers, for more rows in flight on a SM (fp32, 16384 x 2560
+// without the residual, dw included: 102 us, with 79 registers 115).
 template <typename T, int LANES, int VECS, int ROWS>
 __global__ void __launch_bounds__(LANES ? 256 : 512, LANES || VECS == 1 ? 2 : 1) bwd_kernel(const BwdArgs<T> p) {
     __shared__ float mem[2][32][ROWS];
@@ -348,6 +349,108 @@ __global__ void __launch_bounds__(LANES ? 256 : 512, LANES || VECS == 1 ? 2 : 1)
     }
 }
 
+// The same for bf16 rows of a whole block: what the next row holds is on its
+// way to shared memory, a thread's own pieces to its own places, so that no
+// barrier but the row's sum is needed, and values are unpacked once.  16384 x
+// 2560 with the residual and ds: 75 us, from registers 89 (3 and 4 rows on their
+// way: 76, 82); without them 56 and 78.  fp32 rows have twice the bytes in
+// flight for the same instructions and gain nothing: 102 from registers, 136 so.
+using bf = __nv_bfloat16;
+constexpr int kStages = 2;
+
+template <int VECS>
+__global__ void __launch_bounds__(512, VECS == 1 ? 2 : 1) bwd_ring_kernel(const BwdArgs<bf> p) {
+    extern __shared__ uint4 ring[];
+    __shared__ float mem[2][32][1];
+    const int tid = threadIdx.x, threads = blockDim.x;
+    const int of_tensor = VECS * threads, tensors = 2 + (p.residual != nullptr) + (p.ds != nullptr);
+    const float inv_cols = 1.0f / float(p.cols);
+    float w[VECS][kVec], dw[VECS][kVec] = {};
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+        const int c = (i * threads + tid) * kVec;
+        if (p.weight && c < p.cols) {
+            load8(w[i], p.weight + c);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) w[i][e] = 1.0f;
+        }
+    }
+    const auto ask = [&](int stage, int64_t row) {
+        uint32_t to = smem_u32(ring + stage * tensors * of_tensor + tid);
+        const auto tensor = [&](const bf *from) {
+#pragma unroll
+            for (int i = 0; i < VECS; ++i) {
+                const int c = (i * threads + tid) * kVec;
+                if (row < p.rows && c < p.cols)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to + i * threads * 16),
+                                 "l"(from + row * p.cols + c)
+                                 : "memory");
+            }
+            to += of_tensor * 16;
+        };
+        tensor(p.s), tensor(p.dy);
+        if (p.residual) tensor(p.residual);
+        if (p.ds) tensor(p.ds);
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
+    };
+    const int64_t step = gridDim.x;
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) ask(i, blockIdx.x + i * step);
+    int stage = 0, turn = 0;
+    float rstd = p.rstd[blockIdx.x];
+    for (int64_t row = blockIdx.x; row < p.rows; row += step) {
+        ask(stage == 0 ? kStages - 1 : stage - 1, row + (kStages - 1) * step);
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 1) : "memory");
+        const uint4 *at = ring + stage * tensors * of_tensor + tid;
+        const auto take = [&](int tensor, int i) {
+            Raw<bf> v;
+            v.w[0] = at[tensor * of_tensor + i * threads];
+            return v;
+        };
+        float x[VECS][kVec], y[VECS][kVec], sum[1] = {0.0f};       // s r, and w dy
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) x[i][e] = y[i][e] = 0.0f;
+            if ((i * threads + tid) * kVec < p.cols) {
+                take(0, i).add_to(x[i]);
+                if (p.residual) take(2, i).add_to(x[i]);
+                take(1, i).add_to(y[i]);
+            }
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                x[i][e] *= rstd;
+                dw[i][e] += y[i][e] * x[i][e];
+                y[i][e] *= w[i][e];
+                sum[0] += y[i][e] * x[i][e];
+            }
+        }
+        const float next = row + step < p.rows ? p.rstd[row + step] : 0.0f;
+        row_sums<0, 1>(sum, mem[turn]);
+        turn ^= 1;
+        const float mean = sum[0] * inv_cols;
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) {
+            const int c = (i * threads + tid) * kVec;
+            if (c >= p.cols) continue;
+            float o[kVec];
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) o[e] = rstd * (y[i][e] - x[i][e] * mean);
+            if (p.ds) take(tensors - 1, i).add_to(o);
+            store8(p.dx + row * p.cols + c, o);
+        }
+        rstd = next;
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    if (!p.dweight) return;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+        const int c = (i * threads + tid) * kVec;
+        if (c < p.cols) store8(p.parts + blockIdx.x * p.cols + c, dw[i]);
+    }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(256) bwd_elements_kernel(const BwdArgs<T> p) {
     __shared__ float mem[32][1];
@@ -438,18 +541,18 @@ static cudaError_t fold(const float *parts, float *dweight, int64_t n, int64_t c
 }
 
 // The blocks of `threads` that run at a time, at most kParts: a kernel of as many
-// has no last round that leaves SMs idle, and the fewest partial sums (with two
-// vectors a thread, 16384 x 2560: 1216 blocks 90 us, as many as run 84).
+// has no last round that leaves SMs idle, and the fewest partial sums (fp32, two
+// vectors a thread, 4096 x 8192: 1216 blocks 118 us, as many as run 101).
 template <auto KERNEL>
-static cudaError_t at_a_time(unsigned threads, int *blocks) {
-    static std::atomic<int> known[17];          // by warps; the same on every GPU of this kind
-    std::atomic<int> &kept = known[threads / 32];
+static cudaError_t at_a_time(unsigned threads, int bytes, int tensors, int *blocks) {
+    static std::atomic<int> known[5][17];       // by tensors and warps; the same on every GPU of this kind
+    std::atomic<int> &kept = known[tensors][threads / 32];
     *blocks = kept.load(std::memory_order_relaxed);
     if (*blocks) return cudaSuccess;
     int device = 0, sms = 0, each = 0;
     if (cudaError_t e = cudaGetDevice(&device)) return e;
     if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device)) return e;
-    if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&each, KERNEL, int(threads), 0)) return e;
+    if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&each, KERNEL, int(threads), size_t(bytes))) return e;
     *blocks = std::min(std::max(sms * each, 1), kParts);
     kept.store(*blocks, std::memory_order_relaxed);
     return cudaSuccess;
@@ -460,9 +563,32 @@ static cudaError_t go(const BwdArgs<T> &a, cudaStream_t st) {
     const unsigned threads = LANES ? 256 : threads_for(a.cols / kVec, VECS), per = ROWS * (LANES ? 256 / LANES : 1);
     const int64_t blocks = (a.rows + per - 1) / per;
     int most = 0;
-    if (cudaError_t e = at_a_time<bwd_kernel<T, LANES, VECS, ROWS>>(threads, &most)) return e;
+    if (cudaError_t e = at_a_time<bwd_kernel<T, LANES, VECS, ROWS>>(threads, 0, 0, &most)) return e;
     const int64_t grid = blocks < most ? blocks : most;
     bwd_kernel<T, LANES, VECS, ROWS><<<unsigned(grid), threads, 0, st>>>(a);
+    if (cudaError_t e = cudaGetLastError()) return e;
+    return a.dweight ? fold(a.parts, a.dweight, grid, a.cols, st) : cudaSuccess;
+}
+
+template <int VECS>
+static cudaError_t go_ring(const BwdArgs<bf> &a, cudaStream_t st) {
+    const unsigned threads = threads_for(a.cols / kVec, VECS);
+    const int tensors = 2 + (a.residual != nullptr) + (a.ds != nullptr);
+    constexpr int each = VECS * 16 * kStages;       // bytes of a thread and tensor
+    static_assert(512 * 4 * each <= 232448 - 1024, "shared memory");
+    static std::atomic<uint64_t> allowed{0};        // by device: the limit of the widest rows
+    int device = 0;
+    if (cudaError_t e = cudaGetDevice(&device)) return e;
+    if (device >= 64 || !(allowed.load(std::memory_order_acquire) >> device & 1)) {
+        if (cudaError_t e = cudaFuncSetAttribute(bwd_ring_kernel<VECS>, cudaFuncAttributeMaxDynamicSharedMemorySize, 512 * 4 * each))
+            return e;
+        if (device < 64) allowed.fetch_or(uint64_t(1) << device, std::memory_order_release);
+    }
+    const int bytes = int(threads) * tensors * each;
+    int most = 0;
+    if (cudaError_t e = at_a_time<bwd_ring_kernel<VECS>>(threads, bytes, tensors, &most)) return e;
+    const int64_t grid = a.rows < most ? a.rows : most;
+    bwd_ring_kernel<VECS><<<unsigned(grid), threads, bytes, st>>>(a);
     if (cudaError_t e = cudaGetLastError()) return e;
     return a.dweight ? fold(a.parts, a.dweight, grid, a.cols, st) : cudaSuccess;
 }
@@ -473,13 +599,13 @@ cudaError_t bwd(const BwdArgs<T> &a, cudaStream_t st) {
     if (a.cols % kVec == 0 && vecs <= 1024 && on16(a.dy) && on16(a.s) && on16(a.residual) && on16(a.ds) && on16(a.weight) &&
         on16(a.dx) && on16(a.parts)) {
         // lanes of a warp up to 256 columns (bf16, 100000 x 256: 53 us, as a block a row 98); then one
-        // vector a thread (16384 x 2048: 61, two 66; 8192 x 4096: 65 and 67), two where 512 threads would
-        // not do otherwise
+        // vector a thread (fp32, 16384 x 2560: 102, two 100; 65536 x 512: 99 and 101), two where 512
+        // threads would not do otherwise
         if (vecs <= 8) return go<T, 8, 1, 2>(a, st);
         if (vecs <= 16) return go<T, 16, 1, 2>(a, st);
         if (vecs <= 32) return go<T, 32, 1, 2>(a, st);
-        if (vecs <= 512) return go<T, 0, 1, 1>(a, st);
-        return go<T, 0, 2, 1>(a, st);
+        if constexpr (sizeof(T) == 2) return vecs <= 512 ? go_ring<1>(a, st) : go_ring<2>(a, st);
+        else return vecs <= 512 ? go<T, 0, 1, 1>(a, st) : go<T, 0, 2, 1>(a, st);
     }
     if (a.rows > 0x7fffffff) return cudaErrorInvalidConfiguration;
     bwd_elements_kernel<T><<<unsigned(a.rows), 256, 0, st>>>(a);
@@ -502,7 +628,6 @@ cudaError_t launch_bwd(const T *dy, const T *s, const T *residual, const float *
     return bwd(BwdArgs<T>{dy, s, residual, ds, weight, rstd, dx, dweight, scratch, rows, cols}, st);
 }
 
-using bf = __nv_bfloat16;
 template cudaError_t launch_fwd<float>(const float *, const float *, const float *, float, float *, float *, int8_t *,
                                        float *, float *, int64_t, int64_t, cudaStream_t);
 template cudaError_t launch_fwd<bf>(const bf *, const bf *, const float *, float, bf *, bf *, int8_t *, float *,
