@@ -398,7 +398,7 @@ cudaError_t launch(FwdArgs<bf> a, cudaStream_t st) {
     if (!map_of(&maps.q, a.q, a.s.rows(), a.s.G, a.s.K) || !map_of(&maps.k, a.k, a.s.rows(), a.s.G, a.s.K) ||
         !map_of(&maps.v, a.v, a.s.rows(), a.s.H, a.s.V))
         return cudaErrorInvalidValue;
-    if (cudaError_t e = make_pairs(a.s, a.q, a.k, a.g, a.beta, a.scratch, false, st)) return e;
+    if (cudaError_t e = make_pairs(a.s, maps.q, maps.k, a.g, a.beta, a.scratch, false, st)) return e;
     const FwdScratch at = fwd_scratch(a.s);
     const bool wide = a.s.K > 64;
     a.part = at.part;

@@ -466,8 +466,8 @@ __device__ __forceinline__ void lower_solve(float *m, const float *beta, int tid
 constexpr int kTile = kBlock * kBlock * 2;
 constexpr int kRecord = (3 * kTile + int(sizeof(Factors)) + 127) / 128 * 128, kBothRecord = kRecord + kTile;
 cudaError_t take_device_error(unsigned int *out);
-cudaError_t make_pairs(const Shape &s, const bf *q, const bf *k, const bf *g, const bf *beta, unsigned char *records,
-                       bool both, cudaStream_t st);
+cudaError_t make_pairs(const Shape &s, const CUtensorMap &q, const CUtensorMap &k, const bf *g, const bf *beta,
+                       unsigned char *records, bool both, cudaStream_t st);
 
 // Dynamic shared memory for a kernel, allowed once a device.
 template <auto KERNEL>

@@ -139,10 +139,9 @@ static cudaError_t go(const Shape &s, const PairMaps &maps, const bf *g, const b
     return cudaGetLastError();
 }
 
-cudaError_t make_pairs(const Shape &s, const bf *q, const bf *k, const bf *g, const bf *beta, unsigned char *records,
-                       bool both, cudaStream_t st) {
-    PairMaps maps;
-    if (!map_of(&maps.q, q, s.rows(), s.G, s.K) || !map_of(&maps.k, k, s.rows(), s.G, s.K)) return cudaErrorInvalidValue;
+cudaError_t make_pairs(const Shape &s, const CUtensorMap &q, const CUtensorMap &k, const bf *g, const bf *beta,
+                       unsigned char *records, bool both, cudaStream_t st) {
+    const PairMaps maps{q, k};
     return s.K <= 64 ? go<64>(s, maps, g, beta, records, both, st) : go<128>(s, maps, g, beta, records, both, st);
 }
 
