@@ -523,8 +523,9 @@ SSM_API int64_t delta_rule_fwd_scratch(int64_t Bs, int64_t L, int64_t G, int64_t
  *   scratch : delta_rule_bwd_scratch bytes of the caller's, 16-byte aligned;
  *             unspecified afterwards
  * Deterministic.  A NaN or an infinity in the kept states or errors of a block
- * of 64 steps makes that head's (and its group's) gradients there unspecified.  The other rules as
- * delta_rule_fwd.
+ * of 64 steps makes that head's (and its group's) gradients there unspecified,
+ * one in dy or dh_final those of that head's sequence up to the end of its block.
+ * The other rules as delta_rule_fwd.
  */
 SSM_API int64_t delta_rule_bwd_scratch(int64_t Bs, int64_t L, int64_t G, int64_t H, int64_t K,
                                        int64_t V, int64_t n_seq, int io_bf16);
