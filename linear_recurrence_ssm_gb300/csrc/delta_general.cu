@@ -7,7 +7,11 @@
 // chains takes one head of one sequence and 32 rows of its state (the rows are
 // independent of one another) with the state in shared memory, and has matrix
 // products left: W = V - Gam K S^T, X = W - N (beta W) and so on.  With the
-// systems solved inside the chain a block of 64 steps took 40 us of it.
+// systems solved inside the chain a block of 64 steps took 40 us of it.  A chain
+// alone is latency: a head of 64 x 64 takes 6.6 us a block forward and 12 back
+// (30217 steps: 3.1 and 5.7 ms), of loads for the block that wait for the one
+// before and of operands from shared memory (8.8 us a block forward before K and Q
+// shared the reads of the state and N and P were read by 16 bytes).
 #include "delta_rule.cuh"
 
 namespace ssm {
@@ -100,25 +104,55 @@ __device__ __forceinline__ void products(float (&out)[4][4], const float *a, con
 template <int SL>
 __device__ __forceinline__ int lies(int v) { return v % 4 * (SL / 4) + v / 4; }
 
-// Rows t (and t + 32 of 32-row slices) of `a` times four rows v.. of the state: out[i][j] = a_(t + 32 i) . S_(v + j).
-template <int SL, int R>
-__device__ __forceinline__ void through_state(float (&out)[R][4], const float *a, const float *S, int stride, int Kp,
-                                              int t, int v) {
+// Rows t (and t + 32 of 32-row slices) of each of N matrices times four rows v..
+// of the state: out[n][i][j] = a[n]_(t + 32 i) . S_(v + j).
+template <int SL, int R, int N>
+__device__ __forceinline__ void through_state(float (&out)[N][R][4], const float *const (&a)[N], const float *S, int stride,
+                                              int Kp, int t, int v) {
 #pragma unroll
-    for (int i = 0; i < 4 * R; ++i) out[i / 4][i % 4] = 0.0f;
+    for (int i = 0; i < 4 * R * N; ++i) out[i / (4 * R)][i / 4 % R][i % 4] = 0.0f;
 #pragma unroll 2
     for (int k = 0; k < Kp; k += 4) {
-        float4 u[R], w[4];
-#pragma unroll
-        for (int i = 0; i < R; ++i) u[i] = *reinterpret_cast<const float4 *>(a + (t + 32 * i) * stride + k);
+        float4 w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const float4 *>(S + (j * (SL / 4) + v / 4) * stride + k);
 #pragma unroll
-        for (int i = 0; i < R; ++i)
+        for (int n = 0; n < N; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                out[i][j] += u[i].x * w[j].x + u[i].y * w[j].y + u[i].z * w[j].z + u[i].w * w[j].w;
+            for (int i = 0; i < R; ++i) {
+                const float4 u = *reinterpret_cast<const float4 *>(a[n] + (t + 32 * i) * stride + k);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) out[n][i][j] += u.x * w[j].x + u.y * w[j].y + u.z * w[j].z + u.w * w[j].w;
+            }
     }
+}
+
+// Four rows of the state and this many of its columns are a thread's in the
+// state's sums: as many threads for 16 rows as for 32.
+template <int SL>
+constexpr int kColumns = SL / 8;
+template <int N>
+__device__ __forceinline__ void get(float (&v)[N], const float *p) {
+    if constexpr (N == 4) {
+        const float4 w = *reinterpret_cast<const float4 *>(p);
+        v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+    } else {
+        const float2 w = *reinterpret_cast<const float2 *>(p);
+        v[0] = w.x, v[1] = w.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ void set(float *p, const float (&v)[N]) {
+    if constexpr (N == 4) *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+}
+// o += u_t k_t^T
+template <int N>
+__device__ __forceinline__ void outer(float (&o)[4][N], const float4 &u, const float *k) {
+    float kk[N];
+    get(kk, k);
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[0][e] += u.x * kk[e], o[1][e] += u.y * kk[e], o[2][e] += u.z * kk[e], o[3][e] += u.w * kk[e];
 }
 
 // What the chains need of a block, in floats: N, P (with the scale), and the
@@ -236,6 +270,22 @@ __device__ __forceinline__ int behind_cut(const Decays &d, int t) {
     return t;
 }
 
+// o += sign sum over r from `from` up to (not with) `to` of a_r x_r; a starts on 16 bytes.
+template <int SIGN>
+__device__ __forceinline__ void add_rows(float4 &o, const float *a, const float *x, int from, int to) {
+    int r = from;
+    for (; r < to && r % 4; ++r) fma4(o, SIGN * a[r], *reinterpret_cast<const float4 *>(x + r * kRow));
+#pragma unroll 4
+    for (; r + 4 <= to; r += 4) {
+        const float4 w = *reinterpret_cast<const float4 *>(a + r);
+        fma4(o, SIGN * w.x, *reinterpret_cast<const float4 *>(x + r * kRow));
+        fma4(o, SIGN * w.y, *reinterpret_cast<const float4 *>(x + (r + 1) * kRow));
+        fma4(o, SIGN * w.z, *reinterpret_cast<const float4 *>(x + (r + 2) * kRow));
+        fma4(o, SIGN * w.w, *reinterpret_cast<const float4 *>(x + (r + 3) * kRow));
+    }
+    for (; r < to; ++r) fma4(o, SIGN * a[r], *reinterpret_cast<const float4 *>(x + r * kRow));
+}
+
 // Which head, sequence and rows of the state a thread block has.
 struct Work {
     int seq, head, group, v0, width;
@@ -289,9 +339,9 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdArgs<T> p) {
             for (int v = tid / 32; v < w.width; v += kThreads / 32)
                 for (int k = tid % 32; k < s.K; k += 32) put(out + v * s.K + k, S[lies<SL>(v) * l.stride + k]);
         }
-        float from[R][4], y[R][4];
-        through_state<SL, R>(from, Kt, S, l.stride, Kp, t0, v4);
-        through_state<SL, R>(y, Q, S, l.stride, Kp, t0, v4);
+        float both[2][R][4];
+        through_state<SL, R, 2>(both, {Kt, Q}, S, l.stride, Kp, t0, v4);
+        float(&from)[R][4] = both[0], (&y)[R][4] = both[1];
         // W, and beta W beside it
         float *U = mem + l.x;
 #pragma unroll
@@ -313,8 +363,7 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdArgs<T> p) {
         for (int i = 0; i < R; ++i) {
             const int t = t0 + 32 * i;
             float4 o = make_float4(from[i][0], from[i][1], from[i][2], from[i][3]);
-#pragma unroll 4
-            for (int r = behind_cut(d, t); r < t; ++r) fma4(o, -A[t * kPairs + r], *reinterpret_cast<const float4 *>(U + r * kRow + v4));
+            add_rows<-1>(o, A + t * kPairs, U + v4, behind_cut(d, t), t);
             *reinterpret_cast<float4 *>(W + t * kRow + v4) = o;
         }
         __syncthreads();
@@ -331,8 +380,7 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdArgs<T> p) {
         for (int i = 0; i < R; ++i) {
             const int t = t0 + 32 * i;
             float4 o = make_float4(y[i][0], y[i][1], y[i][2], y[i][3]);
-#pragma unroll 4
-            for (int r = behind_cut(d, t); r <= t; ++r) fma4(o, P[t * kPairs + r], *reinterpret_cast<const float4 *>(W + r * kRow + v4));
+            add_rows<1>(o, P + t * kPairs, W + v4, behind_cut(d, t), t + 1);
             if (t < rows) {
                 T *out = p.y + (row + t) * v_step + int64_t(w.head) * s.V + w.v0 + v4;
                 const float v[4] = {o.x, o.y, o.z, o.w};
@@ -346,23 +394,19 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdArgs<T> p) {
         __syncthreads();
         for (int i = tid; i < kBlock * SL; i += kThreads) W[i / SL * kRow + i % SL] *= d.end(i / SL);
         __syncthreads();
-        for (int i = tid; i < SL / 4 * (Kp / 4); i += kThreads) {
-            const int v = i % (SL / 4) * 4, k = i / (SL / 4) * 4;
-            float4 o[4];
+        for (int i = tid; i < SL / 4 * (Kp / kColumns<SL>); i += kThreads) {
+            const int v = i % (SL / 4) * 4, k = i / (SL / 4) * kColumns<SL>;
+            float o[4][kColumns<SL>];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                o[j] = *reinterpret_cast<const float4 *>(S + lies<SL>(v + j) * l.stride + k);
-                o[j] = last == 0.0f ? make_float4(0, 0, 0, 0)
-                                    : make_float4(last * o[j].x, last * o[j].y, last * o[j].z, last * o[j].w);
+                get(o[j], S + lies<SL>(v + j) * l.stride + k);
+#pragma unroll
+                for (int e = 0; e < kColumns<SL>; ++e) o[j][e] = last == 0.0f ? 0.0f : last * o[j][e];
             }
 #pragma unroll 4
-            for (int t = first; t < rows; ++t) {
-                const float4 u = *reinterpret_cast<const float4 *>(W + t * kRow + v);
-                const float4 kk = *reinterpret_cast<const float4 *>(Kt + t * l.stride + k);
-                fma4(o[0], u.x, kk), fma4(o[1], u.y, kk), fma4(o[2], u.z, kk), fma4(o[3], u.w, kk);
-            }
+            for (int t = first; t < rows; ++t) outer(o, *reinterpret_cast<const float4 *>(W + t * kRow + v), Kt + t * l.stride + k);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) *reinterpret_cast<float4 *>(S + lies<SL>(v + j) * l.stride + k) = o[j];
+            for (int j = 0; j < 4; ++j) set(S + lies<SL>(v + j) * l.stride + k, o[j]);
         }
     }
     __syncthreads();
@@ -412,8 +456,9 @@ __global__ void __launch_bounds__(kThreads) back_kernel(const BwdArgs<T> p) {
         T *ds = p.ds + ((span.slot + c) * s.H + w.head) * int64_t(s.V) * s.K + int64_t(w.v0) * s.K;
         for (int v = tid / 32; v < w.width; v += kThreads / 32)
             for (int k = tid % 32; k < s.K; k += 32) put(ds + v * s.K + k, S[lies<SL>(v) * l.stride + k]);
-        float from[R][4];
-        through_state<SL, R>(from, Kt, S, l.stride, Kp, t0, v4);
+        float of_keys[1][R][4];
+        through_state<SL, R, 1>(of_keys, {Kt}, S, l.stride, Kp, t0, v4);
+        const float(&from)[R][4] = of_keys[0];
         // dU, and beta dU beside it
         float4 du[R];
 #pragma unroll
@@ -461,26 +506,22 @@ __global__ void __launch_bounds__(kThreads) back_kernel(const BwdArgs<T> p) {
         }
         const float last = d.start(kBlock - 1);
         __syncthreads();
-        for (int i = tid; i < SL / 4 * (Kp / 4); i += kThreads) {
-            const int v = i % (SL / 4) * 4, k = i / (SL / 4) * 4;
-            float4 o[4];
+        for (int i = tid; i < SL / 4 * (Kp / kColumns<SL>); i += kThreads) {
+            const int v = i % (SL / 4) * 4, k = i / (SL / 4) * kColumns<SL>;
+            float o[4][kColumns<SL>];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                o[j] = *reinterpret_cast<const float4 *>(S + lies<SL>(v + j) * l.stride + k);
-                o[j] = last == 0.0f ? make_float4(0, 0, 0, 0)
-                                    : make_float4(last * o[j].x, last * o[j].y, last * o[j].z, last * o[j].w);
+                get(o[j], S + lies<SL>(v + j) * l.stride + k);
+#pragma unroll
+                for (int e = 0; e < kColumns<SL>; ++e) o[j][e] = last == 0.0f ? 0.0f : last * o[j][e];
             }
 #pragma unroll 4
             for (int t = 0; t < rows; ++t) {
-                float4 u = *reinterpret_cast<const float4 *>(Y + t * kRow + v);
-                float4 kk = *reinterpret_cast<const float4 *>(Q + t * l.stride + k);
-                fma4(o[0], u.x, kk), fma4(o[1], u.y, kk), fma4(o[2], u.z, kk), fma4(o[3], u.w, kk);
-                u = *reinterpret_cast<const float4 *>(Z + t * kRow + v);
-                kk = *reinterpret_cast<const float4 *>(Kt + t * l.stride + k);
-                fma4(o[0], u.x, kk), fma4(o[1], u.y, kk), fma4(o[2], u.z, kk), fma4(o[3], u.w, kk);
+                outer(o, *reinterpret_cast<const float4 *>(Y + t * kRow + v), Q + t * l.stride + k);
+                outer(o, *reinterpret_cast<const float4 *>(Z + t * kRow + v), Kt + t * l.stride + k);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) *reinterpret_cast<float4 *>(S + lies<SL>(v + j) * l.stride + k) = o[j];
+            for (int j = 0; j < 4; ++j) set(S + lies<SL>(v + j) * l.stride + k, o[j]);
         }
     }
     __syncthreads();
