@@ -502,7 +502,8 @@ SSM_API ssm_status_t state_pages_compact(void *pool, uint8_t *used, int32_t *mov
  * inputs makes the outputs of that head's whole block of 64 steps unspecified,
  * and of everything behind it in the same sequence up to a step of a later block
  * that drops the state; no other sequence.
- * Supported (SSM_ERR_UNSUPPORTED otherwise): K, V <= 256.  G divides H.
+ * Supported (SSM_ERR_UNSUPPORTED otherwise): K, V <= 256.  G divides H.  No
+ * output may overlap an input or another output.
  * Every pointer is aligned to its element size (SSM_ERR_ALIGNMENT).
  */
 #define SSM_DELTA_BLOCK 64      /* steps between two kept states */
@@ -543,7 +544,7 @@ SSM_API ssm_status_t delta_rule_bwd(const void *q, const void *k, const void *g,
  *   states : (num_pages, H, V, K) fp32
  *   pages : (Bs) int32 device array, or NULL (row b uses page b).  A row whose
  *           page lies outside 0..num_pages-1 is idle: y[b] = 0 and no state
- *           changes.  No page may be named twice.
+ *           changes.  No page may be named twice.  y may not overlap an input.
  */
 SSM_API ssm_status_t delta_rule_step(const void *q, const void *k, const void *v, const void *g,
                                      const void *beta, float scale, float *states,
