@@ -494,7 +494,9 @@ SSM_API ssm_status_t state_pages_compact(void *pool, uint8_t *used, int32_t *mov
  *   states, errors : NULL, or what the backward pass needs (both, fully
  *          written, v's type): the state before steps 0, 64, 128, ... of each
  *          sequence, (slots, H, V, K) with slots = Bs ceil(L / 64), packed
- *          floor(L / 64) + n_seq; and x, (Bs, L, H, V)
+ *          floor(L / 64) + n_seq, sequence i's from slot floor(offsets[i] / 64)
+ *          + i on; and x, (Bs, L, H, V).  Slots that no sequence needs and
+ *          rows of x that none covers are 0.
  *   scratch : delta_rule_fwd_scratch bytes of the caller's, 16-byte aligned;
  *          unspecified afterwards
  * The state and every sum are fp32.  bf16 inputs: see the kernels for what the

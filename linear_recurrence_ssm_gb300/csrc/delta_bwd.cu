@@ -672,7 +672,7 @@ cudaError_t launch(const BwdArgs<bf> &a, cudaStream_t st) {
     if (!map_of(&maps.q, a.q, a.s.rows(), a.s.G, a.s.K) || !map_of(&maps.k, a.k, a.s.rows(), a.s.G, a.s.K) ||
         !map_of(&maps.dy, a.dy, a.s.rows(), a.s.H, a.s.V) || !map_of(&maps.x, a.errors, a.s.rows(), a.s.H, a.s.V))
         return cudaErrorInvalidValue;
-    if (cudaError_t e = make_pairs(a.s, maps.q, maps.k, a.g, a.beta, a.records, true, st)) return e;
+    if (cudaError_t e = make_pairs(a.s, maps.q, maps.k, a.g, a.beta, a.records, true, nullptr, st)) return e;
     if (cudaError_t e = a.s.K <= 64 ? back<64>(a, maps, st) : back<128>(a, maps, st)) return e;
     BlockMaps of;
     of.q = maps.q, of.k = maps.k, of.dy = maps.dy, of.x = maps.x;

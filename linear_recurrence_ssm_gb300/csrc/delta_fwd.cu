@@ -317,7 +317,10 @@ fwd_kernel(const FwdArgs<bf> p, const __grid_constant__ Maps maps) {
                 if (v < width && k < s.K) out[int64_t(mine + v) * s.K + k] = st[n][e];
             }
     }
-    if (!CARRY && part == 0) clear_uncovered(s, seq, p.y + int64_t(head) * s.V + v0, v_step, min(kSlice, s.V - v0));
+    if (!CARRY && part == 0) {
+        clear_uncovered(s, seq, p.y + int64_t(head) * s.V + v0, v_step, min(kSlice, s.V - v0));
+        if (p.errors) clear_uncovered(s, seq, p.errors + int64_t(head) * s.V + v0, v_step, min(kSlice, s.V - v0));
+    }
 }
 
 // The states that enter a sequence's parts: S_(i + 1) = S_i T_i + B_i, four
@@ -398,7 +401,7 @@ cudaError_t launch(FwdArgs<bf> a, cudaStream_t st) {
     if (!map_of(&maps.q, a.q, a.s.rows(), a.s.G, a.s.K) || !map_of(&maps.k, a.k, a.s.rows(), a.s.G, a.s.K) ||
         !map_of(&maps.v, a.v, a.s.rows(), a.s.H, a.s.V))
         return cudaErrorInvalidValue;
-    if (cudaError_t e = make_pairs(a.s, maps.q, maps.k, a.g, a.beta, a.scratch, false, st)) return e;
+    if (cudaError_t e = make_pairs(a.s, maps.q, maps.k, a.g, a.beta, a.scratch, false, a.states, st)) return e;
     const FwdScratch at = fwd_scratch(a.s);
     const bool wide = a.s.K > 64;
     a.part = at.part;

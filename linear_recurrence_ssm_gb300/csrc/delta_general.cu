@@ -181,7 +181,7 @@ __host__ __device__ inline Layout layout_of(int K) {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) pairs_kernel(const Shape s, const T *q, const T *k, const T *g, const T *beta,
-                                                         Made *made) {
+                                                         Made *made, T *states) {
     extern __shared__ __align__(16) float mem[];
     __shared__ Decays d;
     __shared__ int found;
@@ -191,7 +191,10 @@ __global__ void __launch_bounds__(kThreads) pairs_kernel(const Shape s, const T 
     const int head = int(blockIdx.x % s.H), group = head / (s.H / s.G);
     const int64_t slot = blockIdx.x / s.H;
     const int seq = sequence_of(s, slot, &found);
-    if (seq < 0) return;
+    if (seq < 0) {
+        if (states) clear_state(s, slot, head, states);
+        return;
+    }
     const Span span = span_of(s, seq);
     const int c = int(slot - span.slot), rows = min(kBlock, span.len - c * kBlock);
     const int64_t row = span.first + int64_t(c) * kBlock, step = int64_t(s.G) * s.K;
@@ -414,6 +417,7 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const FwdArgs<T> p) {
         for (int v = tid / 32; v < w.width; v += kThreads / 32)
             for (int k = tid % 32; k < s.K; k += 32) p.h_final[state_at + v * s.K + k] = S[lies<SL>(v) * l.stride + k];
     clear_uncovered(s, w.seq, p.y + int64_t(w.head) * s.V + w.v0, v_step, w.width);
+    if (p.errors) clear_uncovered(s, w.seq, p.errors + int64_t(w.head) * s.V + w.v0, v_step, w.width);
 }
 
 // Back along a sequence: dv, the shares of dbeta, the adjoint of every
@@ -784,12 +788,12 @@ int64_t made_bytes(const Shape &s) { return s.slots() * s.H * int64_t(sizeof(Mad
 
 template <typename T>
 static cudaError_t make_pairs(const Shape &s, const T *q, const T *k, const T *g, const T *beta, unsigned char *made,
-                              cudaStream_t st) {
+                              T *states, cudaStream_t st) {
     const int64_t grid = s.slots() * s.H;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     const auto words = [](int K) { return 2 * kBlock * (stride_of(K) > kPairs ? stride_of(K) : kPairs) + kBlock * kPairs; };
     if (cudaError_t e = room(pairs_kernel<T>, words(256))) return e;
-    pairs_kernel<T><<<unsigned(grid), kThreads, words(s.K) * 4, st>>>(s, q, k, g, beta, reinterpret_cast<Made *>(made));
+    pairs_kernel<T><<<unsigned(grid), kThreads, words(s.K) * 4, st>>>(s, q, k, g, beta, reinterpret_cast<Made *>(made), states);
     return cudaGetLastError();
 }
 
@@ -805,7 +809,7 @@ cudaError_t fwd(const FwdArgs<T> &a, cudaStream_t st) {
     const int each = rows_of(a.s);
     const int64_t grid = int64_t(a.s.n) * a.s.H * slices(a.s, each);
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    if (cudaError_t e = make_pairs(a.s, a.q, a.k, a.g, a.beta, a.scratch, st)) return e;
+    if (cudaError_t e = make_pairs(a.s, a.q, a.k, a.g, a.beta, a.scratch, a.states, st)) return e;
     return each == 16 ? go<T, 16>(a, unsigned(grid), st) : go<T, 32>(a, unsigned(grid), st);
 }
 
@@ -828,7 +832,7 @@ cudaError_t bwd(const BwdArgs<T> &a, cudaStream_t st) {
     const int each = rows_of(a.s);
     const int64_t grid = int64_t(a.s.n) * a.s.H * slices(a.s, each), blocks = a.s.slots() * a.s.H;
     if (grid > 0x7fffffff || blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    if (cudaError_t e = make_pairs(a.s, a.q, a.k, a.g, a.beta, a.records, st)) return e;
+    if (cudaError_t e = make_pairs<T>(a.s, a.q, a.k, a.g, a.beta, a.records, nullptr, st)) return e;
     if (cudaError_t e = room(grads_kernel<T>, grad_layout_of(256).words)) return e;
     if (cudaError_t e = each == 16 ? go<T, 16>(a, unsigned(grid), st) : go<T, 32>(a, unsigned(grid), st)) return e;
     grads_kernel<T><<<unsigned(blocks), kThreads, grad_layout_of(a.s.K).words * 4, st>>>(a, slices(a.s, each));

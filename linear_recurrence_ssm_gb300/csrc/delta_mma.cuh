@@ -466,8 +466,9 @@ __device__ __forceinline__ void lower_solve(float *m, const float *beta, int tid
 constexpr int kTile = kBlock * kBlock * 2;
 constexpr int kRecord = (3 * kTile + int(sizeof(Factors)) + 127) / 128 * 128, kBothRecord = kRecord + kTile;
 cudaError_t take_device_error(unsigned int *out);
+// `states`: of the kept ones, those of places that no block has become 0 (null: none are kept).
 cudaError_t make_pairs(const Shape &s, const CUtensorMap &q, const CUtensorMap &k, const bf *g, const bf *beta,
-                       unsigned char *records, bool both, cudaStream_t st);
+                       unsigned char *records, bool both, bf *states, cudaStream_t st);
 
 // Dynamic shared memory for a kernel, allowed once a device.
 template <auto KERNEL>

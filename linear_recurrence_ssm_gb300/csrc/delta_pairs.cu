@@ -30,7 +30,7 @@ __device__ unsigned int g_device_error;
 template <int KP>
 __global__ void __launch_bounds__(kPairThreads, 4)
 pairs_kernel(const Shape s, const __grid_constant__ PairMaps maps, const bf *g, const bf *beta, unsigned char *records,
-             const bool both) {
+             const bool both, bf *states) {
     extern __shared__ __align__(1024) unsigned char mem[];
     __shared__ Decays d;
     __shared__ Factors f;
@@ -42,7 +42,10 @@ pairs_kernel(const Shape s, const __grid_constant__ PairMaps maps, const bf *g, 
     const int head = int(blockIdx.x % s.H), group = head / (s.H / s.G);
     const int64_t slot = blockIdx.x / s.H;
     const int seq = sequence_of(s, slot, &found);
-    if (seq < 0) return;
+    if (seq < 0) {
+        if (states) clear_state(s, slot, head, states);
+        return;
+    }
     const Span span = span_of(s, seq);
     const int c = int(slot - span.slot), rows = min(kBlock, span.len - c * kBlock);
     const int64_t row = span.first + int64_t(c) * kBlock;
@@ -130,19 +133,20 @@ pairs_kernel(const Shape s, const __grid_constant__ PairMaps maps, const bf *g, 
 
 template <int KP>
 static cudaError_t go(const Shape &s, const PairMaps &maps, const bf *g, const bf *beta, unsigned char *records, bool both,
-                      cudaStream_t st) {
+                      bf *states, cudaStream_t st) {
     const int64_t grid = s.slots() * s.H;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     constexpr int bytes = PairLayout<KP>::bytes;
     if (cudaError_t e = allow<pairs_kernel<KP>>(bytes)) return e;
-    pairs_kernel<KP><<<unsigned(grid), kPairThreads, bytes, st>>>(s, maps, g, beta, records, both);
+    pairs_kernel<KP><<<unsigned(grid), kPairThreads, bytes, st>>>(s, maps, g, beta, records, both, states);
     return cudaGetLastError();
 }
 
 cudaError_t make_pairs(const Shape &s, const CUtensorMap &q, const CUtensorMap &k, const bf *g, const bf *beta,
-                       unsigned char *records, bool both, cudaStream_t st) {
+                       unsigned char *records, bool both, bf *states, cudaStream_t st) {
     const PairMaps maps{q, k};
-    return s.K <= 64 ? go<64>(s, maps, g, beta, records, both, st) : go<128>(s, maps, g, beta, records, both, st);
+    return s.K <= 64 ? go<64>(s, maps, g, beta, records, both, states, st)
+                     : go<128>(s, maps, g, beta, records, both, states, st);
 }
 
 cudaError_t take_device_error(unsigned int *out) { return take_error(g_device_error, out); }

@@ -180,7 +180,7 @@ __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bf
 // before the first sequence (its blocks write them) and behind the last.
 template <typename T>
 __device__ __forceinline__ void clear_uncovered(const Shape &s, int seq, T *out, int64_t step, int width) {
-    if (!s.offsets || out == nullptr) return;
+    if (!s.offsets) return;
     int64_t a = 0, b = 0;
     for (int part = 0; part < 2; ++part) {
         if (part == 0) {
@@ -194,6 +194,13 @@ __device__ __forceinline__ void clear_uncovered(const Shape &s, int seq, T *out,
         for (int64_t i = threadIdx.x; i < (b - a) * width; i += blockDim.x)
             put(out + (a + i / width) * step + i % width, 0.0f);
     }
+}
+
+// The kept state of a place that no block has becomes 0.
+template <typename T>
+__device__ __forceinline__ void clear_state(const Shape &s, int64_t slot, int head, T *states) {
+    T *out = states + (slot * s.H + head) * int64_t(s.V) * s.K;
+    for (int i = threadIdx.x; i < s.V * s.K; i += blockDim.x) put(out + i, 0.0f);
 }
 
 // What the backward pass keeps between its kernels, one after another in the
