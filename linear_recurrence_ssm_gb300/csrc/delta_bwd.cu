@@ -302,10 +302,11 @@ struct BlockMaps {
 // Warp 2 j + h: rows 16 j; of the pairs, those of the queries (h = 0) or of the
 // keys (h = 1); of dQ and dK, columns h KP / 2 to (h + 1) KP / 2.
 //
-// dg needs, of the pairs' products M = dP P + dAb Ab, the sums over r >= t > s.
-// With their row sums R and column sums C those are sum_{t' < t} (C - R)_t':
-// every M enters once with either sign, in fp32, so nothing is lost but the
-// rounding of the sums.
+// dg needs, of the pairs' products M = dP P + dAb Ab, the sums over r >= t > s:
+// a row's sums up to each column (over four lanes and the blocks of 16 columns),
+// and those of the rows from t on.  Pairs on one side of step t never enter:
+// differences of whole rows' and columns' sums would leave their rounding, 2^-24
+// of everything in the block, where little or nothing crosses a step.
 template <int KP, int VP>
 __global__ void __launch_bounds__(256, VP == 64 ? 2 : 1)
 block_kernel(const BwdArgs<bf> p, const __grid_constant__ BlockMaps maps, const int parts) {
@@ -313,8 +314,8 @@ block_kernel(const BwdArgs<bf> p, const __grid_constant__ BlockMaps maps, const 
     __shared__ Decays d;
     __shared__ int found, abort;
     __shared__ __align__(8) uint64_t full[2];       // the block's rows; the states
-    __shared__ float row_term[2][kBlock], col_term[2][kBlock], row_sum[2][kBlock], both_term[8];
-    __shared__ __align__(16) float col_sum[8][kBlock];
+    __shared__ float row_term[2][kBlock], col_term[2][kBlock], both_term[8];
+    __shared__ float across_sum[8][kBlock];
     using L = BlockLayout<KP, VP>;
     let_next_begin();
     const Shape &s = p.s;
@@ -393,7 +394,7 @@ block_kernel(const BwdArgs<bf> p, const __grid_constant__ BlockMaps maps, const 
         const int t = 16 * j + g;
         const float hi0 = d.hi[t], lo0 = d.lo[t], hi1 = d.hi[t + 8], lo1 = d.lo[t + 8];
         const int cut0 = d.cut[t], cut1 = d.cut[t + 8];
-        float sum0 = 0.0f, sum1 = 0.0f;
+        float before0 = 0.0f, before1 = 0.0f;       // of rows t and t + 8, M's columns up to here
 #pragma unroll 1
         for (int n = 0; n <= j; ++n) {
             float a[2][4] = {}, m[2][4] = {}, down[4];
@@ -424,8 +425,18 @@ block_kernel(const BwdArgs<bf> p, const __grid_constant__ BlockMaps maps, const 
                 const float x3 = t + 8 >= r + 1 + h && cut1 == cut.y ? by * beta.y * a[e][3] * ex2((hi1 - hi.y) + (lo1 - lo.y)) : 0.0f;
                 const float m0 = t > r ? x0 * m[e][0] : 0.0f, m1 = t > r + 1 ? x1 * m[e][1] : 0.0f;
                 const float m2 = t + 8 > r ? x2 * m[e][2] : 0.0f, m3 = t + 8 > r + 1 ? x3 * m[e][3] : 0.0f;
-                sum0 += m0 + m1, sum1 += m2 + m3;
-                down[2 * e] = m0 + m2, down[2 * e + 1] = m1 + m3;
+                // what the lanes before this one have in their two columns, and what all four have
+                float up0 = m0 + m1, up1 = m2 + m3, left0 = 0.0f, left1 = 0.0f;
+#pragma unroll
+                for (int o = 1; o < 4; o *= 2) {
+                    const float x = __shfl_xor_sync(0xffffffffu, up0, o), y = __shfl_xor_sync(0xffffffffu, up1, o);
+                    if (lane & o) left0 += x, left1 += y;
+                    up0 += x, up1 += y;
+                }
+                left0 += before0, left1 += before1;
+                down[2 * e] = (t >= r ? left0 : 0.0f) + (t + 8 >= r ? left1 : 0.0f);
+                down[2 * e + 1] = (t > r ? left0 + m0 : 0.0f) + (t + 8 > r ? left1 + m2 : 0.0f);
+                before0 += up0, before1 += up1;
                 const uint32_t w0 = pack(x0, x1), w1 = pack(x2, x3);
                 asm volatile("st.shared.b32 [%0], %1;" ::"r"(place<64>(out, t, r & ~7) + (r & 7) * 2), "r"(w0) : "memory");
                 asm volatile("st.shared.b32 [%0], %1;" ::"r"(place<64>(out, t + 8, r & ~7) + (r & 7) * 2), "r"(w1) : "memory");
@@ -436,15 +447,9 @@ block_kernel(const BwdArgs<bf> p, const __grid_constant__ BlockMaps maps, const 
             const float of1 = (upper ? down[3] : down[1]) + __shfl_xor_sync(0xffffffffu, upper ? down[1] : down[3], 16);
             float sum = (odd ? of1 : of0) + __shfl_xor_sync(0xffffffffu, odd ? of0 : of1, 8);
             sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-            if (g % 2 == 0) col_sum[warp][16 * n + 8 * upper + c2 + odd] = sum;
+            if (g % 2 == 0) across_sum[warp][16 * n + 8 * upper + c2 + odd] = sum;
         }
-#pragma unroll
-        for (int o = 1; o < 4; o *= 2) {
-            sum0 += __shfl_xor_sync(0xffffffffu, sum0, o);
-            sum1 += __shfl_xor_sync(0xffffffffu, sum1, o);
-        }
-        if (lane % 4 == 0) row_sum[h][t] = sum0, row_sum[h][t + 8] = sum1;
-        for (int r = 16 * (j + 1) + lane; r < kBlock; r += 32) col_sum[warp][r] = 0.0f;
+        for (int r = 16 * (j + 1) + lane; r < kBlock; r += 32) across_sum[warp][r] = 0.0f;
     }
     wait_for(&full[1], 0, &abort, &g_device_error);
     __syncthreads();
@@ -615,15 +620,15 @@ block_kernel(const BwdArgs<bf> p, const __grid_constant__ BlockMaps maps, const 
 #pragma unroll
         for (int o = 4; o > 0; o /= 2) both += __shfl_xor_sync(0xffffffffu, both, o);
         both = kept(d.start(kBlock - 1), both);
-        float behind[2], before[2];         // this step's terms
+        float behind[2], before[2], crossing[2];        // this step's terms
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int t = 2 * lane + e;
-            float down = 0.0f;
+            crossing[e] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) down += col_sum[i][t];
+            for (int i = 0; i < 8; ++i) crossing[e] += across_sum[i][t];
             behind[e] = row_term[0][t] + row_term[1][t];
-            before[e] = (col_term[0][t] + col_term[1][t]) + (down - (row_sum[0][t] + row_sum[1][t]));
+            before[e] = col_term[0][t] + col_term[1][t];
         }
         float up = behind[0] + behind[1], down = before[0] + before[1];
 #pragma unroll
@@ -635,7 +640,7 @@ block_kernel(const BwdArgs<bf> p, const __grid_constant__ BlockMaps maps, const 
         float first = __shfl_up_sync(0xffffffffu, down, 1), last = __shfl_down_sync(0xffffffffu, up, 1);
         if (lane == 0) first = 0.0f;
         if (lane == 31) last = 0.0f;
-        const float at[2] = {up + first, behind[1] + last + first + before[0]};
+        const float at[2] = {crossing[0] + up + first, crossing[1] + behind[1] + last + first + before[0]};
 #pragma unroll
         for (int e = 0; e < 2; ++e)
             if (2 * lane + e < rows) put(p.dg + (row + 2 * lane + e) * s.H + head, both + at[e]);
