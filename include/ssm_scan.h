@@ -497,8 +497,8 @@ SSM_API ssm_status_t state_pages_compact(void *pool, uint8_t *used, int32_t *mov
  *          floor(L / 64) + n_seq, sequence i's from slot floor(offsets[i] / 64)
  *          + i on; and x, (Bs, L, H, V).  Slots that no sequence needs and
  *          rows of x that none covers are 0.
- *   scratch : delta_rule_fwd_scratch bytes of the caller's, 16-byte aligned;
- *          unspecified afterwards
+ *   scratch : delta_rule_fwd_scratch bytes (0 for sizes that are refused) of
+ *          the caller's, 16-byte aligned; unspecified afterwards
  * The state and every sum are fp32.  bf16 inputs: see the kernels for what the
  * tensor cores' operands are rounded to.  A NaN or an infinity in a step's
  * inputs makes the outputs of that head's whole block of 64 steps unspecified,

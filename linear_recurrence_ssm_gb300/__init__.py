@@ -821,6 +821,10 @@ def _delta_scratch(backward, *sizes):
     return getattr(library(), "delta_rule_bwd_scratch" if backward else "delta_rule_fwd_scratch")(*sizes)
 
 
+def _delta_scale(scale, K):
+    return max(K, 1) ** -0.5 if scale is None else scale       # heads of no columns are the C call's to refuse
+
+
 def _delta_sequences(offsets, Bs, dev):
     """(sequences, the count that the C entry points take)."""
     import torch
@@ -872,7 +876,7 @@ def delta_rule_fwd(q, k, v, g, beta, scale=None, offsets=None, h0=None, return_f
     bf16 = int(v.dtype == torch.bfloat16)
     scratch = torch.empty(_delta_scratch(False, Bs, L, G, H, K, V, n_seq, bf16), dtype=torch.uint8, device=dev)
     _call("delta_rule_fwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-          K ** -0.5 if scale is None else scale, _addr(offsets), _addr(h0), y.data_ptr(), _addr(hf),
+          _delta_scale(scale, K), _addr(offsets), _addr(h0), y.data_ptr(), _addr(hf),
           None if saved is None else saved["states"].data_ptr(),
           None if saved is None else saved["errors"].data_ptr(), scratch.data_ptr(), Bs, L, G, H, K, V, n_seq, bf16)
     out = (y,) + ((hf,) if return_final_state else ()) + ((saved,) if save is not None else ())
@@ -907,7 +911,7 @@ def delta_rule_bwd(q, k, g, beta, dy, saved, scale=None, offsets=None, dh_final=
     bf16 = int(q.dtype == torch.bfloat16)
     scratch = torch.empty(_delta_scratch(True, Bs, L, G, H, K, V, n_seq, bf16), dtype=torch.uint8, device=dev)
     _call("delta_rule_bwd", dev, q.data_ptr(), k.data_ptr(), g.data_ptr(), beta.data_ptr(),
-          K ** -0.5 if scale is None else scale, _addr(offsets), dy.data_ptr(), _addr(dh_final),
+          _delta_scale(scale, K), _addr(offsets), dy.data_ptr(), _addr(dh_final),
           saved["states"].data_ptr(), saved["errors"].data_ptr(), out["dq"].data_ptr(), out["dk"].data_ptr(),
           out["dv"].data_ptr(), out["dg"].data_ptr(), out["dbeta"].data_ptr(), _addr(out["dh0"]),
           scratch.data_ptr(), Bs, L, G, H, K, V, n_seq, bf16)
@@ -940,7 +944,7 @@ def delta_rule_step(q, k, v, g, beta, states, pages=None, scale=None, y=None):
     else:
         _check_shape(y, "y", (v.dtype,), dev, v.shape)
     _call("delta_rule_step", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-          K ** -0.5 if scale is None else scale, states.data_ptr(), _addr(pages), y.data_ptr(), Bs, G, H, K, V,
+          _delta_scale(scale, K), states.data_ptr(), _addr(pages), y.data_ptr(), Bs, G, H, K, V,
           num_pages, int(v.dtype is torch.bfloat16))
     return y
 

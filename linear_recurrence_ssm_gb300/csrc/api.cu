@@ -491,10 +491,11 @@ ssm_status_t delta_fwd_entry(const void *q, const void *k, const void *v, const 
                              const float *h0, void *y, float *h_final, void *states, void *errors,
                              void *scratch, int64_t Bs, int64_t L, int64_t G, int64_t H, int64_t K, int64_t V,
                              int64_t n_seq, void *stream) {
-    if (!q || !k || !v || !g || !beta || !y || !scratch || !states != !errors || (n_seq > 0) != (offsets != nullptr))
+    if (!q || !k || !v || !g || !beta || !y || !states != !errors || (n_seq > 0) != (offsets != nullptr))
         return SSM_ERR_INVALID_ARG;
     ssm_status_t s = check_delta_sizes(Bs, L, G, H, K, V, n_seq, scale);
     if (s != SSM_OK) return s;
+    if (!scratch) return SSM_ERR_INVALID_ARG;       // of no size for sizes that are refused
     const size_t e = sizeof(T);
     for (const void *p : {q, k, v, g, beta, static_cast<const void *>(y), static_cast<const void *>(states),
                           static_cast<const void *>(errors)})
@@ -524,10 +525,11 @@ ssm_status_t delta_bwd_entry(const void *q, const void *k, const void *g, const 
                              void *scratch, int64_t Bs, int64_t L, int64_t G, int64_t H, int64_t K,
                              int64_t V, int64_t n_seq, void *stream) {
     if (!q || !k || !g || !beta || !dy || !states || !errors || !dq || !dk || !dv || !dg || !dbeta ||
-        !scratch || (n_seq > 0) != (offsets != nullptr))
+        (n_seq > 0) != (offsets != nullptr))
         return SSM_ERR_INVALID_ARG;
     ssm_status_t s = check_delta_sizes(Bs, L, G, H, K, V, n_seq, scale);
     if (s != SSM_OK) return s;
+    if (!scratch) return SSM_ERR_INVALID_ARG;
     const size_t e = sizeof(T);
     for (const void *p : {q, k, g, beta, dy, states, errors, static_cast<const void *>(dq),
                           static_cast<const void *>(dk), static_cast<const void *>(dv),
