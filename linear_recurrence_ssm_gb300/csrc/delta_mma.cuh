@@ -516,8 +516,10 @@ inline bool map_of(CUtensorMap *map, const bf *base, int64_t rows, int heads, in
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
-    // a host thread that has made no call of the runtime yet has no context for the driver's
-    return encode() || (cudaFree(nullptr) == cudaSuccess && encode());
+    // A host thread that has made no call of the runtime yet has no context for the driver's.  Setting the
+    // device that it has gives it one, and unlike an allocation's call may be made while a graph is captured.
+    int device = 0;
+    return encode() || (cudaGetDevice(&device) == cudaSuccess && cudaSetDevice(device) == cudaSuccess && encode());
 }
 // A launch that may begin while the kernel before it in the stream runs.
 template <typename... P, typename... A>
