@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "gated_scan.cuh"
+#include "kept_by_device.cuh"
 
 namespace ssm {
 namespace norm {
@@ -545,17 +546,14 @@ static cudaError_t fold(const float *parts, float *dweight, int64_t n, int64_t c
 // vectors a thread, 4096 x 8192: 1216 blocks 118 us, as many as run 101).
 template <auto KERNEL>
 static cudaError_t at_a_time(unsigned threads, int bytes, int tensors, int *blocks) {
-    static std::atomic<int> known[5][17];       // by tensors and warps; the same on every GPU of this kind
-    std::atomic<int> &kept = known[tensors][threads / 32];
-    *blocks = kept.load(std::memory_order_relaxed);
-    if (*blocks) return cudaSuccess;
-    int device = 0, sms = 0, each = 0;
-    if (cudaError_t e = cudaGetDevice(&device)) return e;
-    if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device)) return e;
-    if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&each, KERNEL, int(threads), size_t(bytes))) return e;
-    *blocks = std::min(std::max(sms * each, 1), kParts);
-    kept.store(*blocks, std::memory_order_relaxed);
-    return cudaSuccess;
+    static KeptByDevice<5 * 17> kept;       // by tensors and warps
+    return kept.get(tensors * 17 + int(threads) / 32, blocks, [&](int device, int *most) {
+        int sms = 0, each = 0;
+        if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device)) return e;
+        if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&each, KERNEL, int(threads), size_t(bytes))) return e;
+        *most = std::min(std::max(sms * each, 1), kParts);
+        return cudaSuccess;
+    });
 }
 
 template <typename T, int LANES, int VECS, int ROWS>
