@@ -335,14 +335,22 @@ __device__ __forceinline__ void pair_products(uint32_t a, uint32_t b, int j, con
     }
 }
 
+// Two values as the sum of three bf16 each: all 24 bits.
+__device__ __forceinline__ void split3(float a, float b, uint32_t (&t)[3]) {
+    t[0] = pack(a, b);
+    a -= low(t[0]), b -= high(t[0]);
+    t[1] = pack(a, b);
+    t[2] = pack(a - low(t[1]), b - high(t[1]));
+}
+
 // c += a b for 16 x 16 floats of rows `stride` apart each, b's two blocks of
-// eight columns: in bf16 matrix products of two terms (lo lo left out), 16
-// bits of either side; from b's column `from` on.  a's column s is scaled by -by_s; LOWER: only what lies
-// below a's (A) or b's (B) diagonal counts.
+// eight columns, in bf16 matrix products of three terms that leave out what is
+// below 2^-24 of a product; from b's column `from` on.  a's column s is scaled by
+// -by_s; LOWER: only what lies below a's (A) or b's (B) diagonal counts.
 template <bool LOWER_A, bool LOWER_B, int N>
 __device__ __forceinline__ void join(float (&c)[N][4], const float *a, const float *by, const float *b, int from = 0) {
     const int lane = threadIdx.x % 32, g = lane / 4, c2 = lane % 4 * 2;
-    uint32_t hi[4], lo[4];
+    uint32_t at[3][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const float2 f = *reinterpret_cast<const float2 *>(by + 8 * h + c2);
@@ -351,22 +359,26 @@ __device__ __forceinline__ void join(float (&c)[N][4], const float *a, const flo
             const int t = g + 8 * e, s = 8 * h + c2;
             float2 v = *reinterpret_cast<const float2 *>(a + t * kPairStride + s);
             if (LOWER_A) v.x = s < t ? v.x : 0.0f, v.y = s + 1 < t ? v.y : 0.0f;
-            split(-f.x * v.x, -f.y * v.y, hi[2 * h + e], lo[2 * h + e]);
+            uint32_t w[3];
+            split3(-f.x * v.x, -f.y * v.y, w);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) at[i][2 * h + e] = w[i];
         }
     }
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        uint32_t bh[2], bl[2];
+        uint32_t bt[2][3];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int s = 8 * h + c2, r = from + 8 * n + g;
             float x = b[s * kPairStride + r], y = b[(s + 1) * kPairStride + r];
             if (LOWER_B) x = r < s ? x : 0.0f, y = r < s + 1 ? y : 0.0f;
-            split(x, y, bh[h], bl[h]);
+            split3(x, y, bt[h]);
         }
-        product(c[n], hi, bh[0], bh[1]);
-        product(c[n], lo, bh[0], bh[1]);
-        product(c[n], hi, bl[0], bl[1]);
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+#pragma unroll
+            for (int j = 0; i + j < 3; ++j) product(c[n], at[i], bt[0][j], bt[1][j]);
     }
 }
 template <int N>
@@ -396,9 +408,10 @@ __device__ __forceinline__ void put_block(const float (&c)[N][4], float *to) {
 // the diagonal blocks is overwritten.  Blocks of 16 by substitution in fp32,
 // then pairs of blocks joined,
 //   N21 = (I - N22 beta2) A21 (I - beta1 N11),
-// in matrix products on 16 bits of either side, which is what the chains take
-// of N; multiply-adds there were bound by their shared-memory operands.  128
-// threads.
+// in matrix products on all 24 bits of either side: the chains take 16 bits of N,
+// but with beta near 2 and keys alike what is joined cancels (on 16 bits N was off
+// by 2e-4, and the state with it).  Multiply-adds there were bound by their
+// shared-memory operands.  128 threads.
 __device__ __forceinline__ void lower_solve(float *m, const float *beta, int tid) {
     const int warp = tid / 32;
     {
