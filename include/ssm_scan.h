@@ -499,8 +499,12 @@ SSM_API ssm_status_t state_pages_compact(void *pool, uint8_t *used, int32_t *mov
  *          rows of x that none covers are 0.
  *   scratch : delta_rule_fwd_scratch bytes (0 for sizes that are refused) of
  *          the caller's, 16-byte aligned; unspecified afterwards
- * The state and every sum are fp32.  bf16 inputs: see the kernels for what the
- * tensor cores' operands are rounded to.  A NaN or an infinity in a step's
+ * The state and every sum are fp32, and with fp32 inputs so is all work.  bf16
+ * inputs: the tensor cores' operands are the state's in 16 bits (h_final comes
+ * out within about 1e-5), for y alone in 8 (y is off by twice its own rounding,
+ * 3.4e-3 in the 2-norm, and so are dq, dk and dg); K, V that they do not take
+ * (K > 128 or no multiple of 8, V no multiple of 8, gradients of V > 128) are
+ * computed as fp32.  A NaN or an infinity in a step's
  * inputs makes the outputs of that head's whole block of 64 steps unspecified,
  * and of everything behind it in the same sequence up to a step of a later block
  * that drops the state; no other sequence.
@@ -564,8 +568,8 @@ SSM_API ssm_status_t delta_rule_step(const void *q, const void *k, const void *v
  *          ckpt8_save: the fp32 values are rounded once
  *   rstd : (rows) fp32 or NULL: r, for the gradients
  * s is fp32 where y is formed from it.  sum may be x or residual; no other
- * output may overlap an input.  Any sizes >= 1; every pointer is aligned to
- * its element size.
+ * output may overlap an input.  rows < 2^31 and cols < 2^31 - 4096
+ * (SSM_ERR_UNSUPPORTED otherwise); every pointer is aligned to its element size.
  */
 SSM_API ssm_status_t rms_norm_fwd(const void *x, const void *residual, const float *weight, float eps,
                                   void *sum, void *y, int8_t *y_q, float *y_scale, float *rstd,

@@ -6,14 +6,19 @@
 //   A = Gam_C A + (scale Gam dY)^T Q - (Gam beta Z)^T K
 // Four more warps form dY^T P and (scale Gam dY)^T Q, which do not depend on
 // A, one block ahead.  A's own chain uses operands of two bf16 terms (dh0 comes
-// out within 1e-5); it leaves A of every block, dV and shares of dbeta.
+// out as the forward pass's final state does); it leaves A of every block, dV and
+// shares of dbeta (Z in fp32 times the kept X).
 //
 // block_kernel then takes all blocks at once: dQ, dK and dg from the kept states,
-// the adjoints, dY, X and dV.
+// the adjoints, dY, X and dV.  Those are bf16, A and dV rounded once for it, and so
+// are dP D and dAb D as operands of the last products: up to 2^-8 of a term, as
+// dq, dk and dg themselves are rounded (3.4e-3 in the 2-norm where that rounding
+// gives 1.7e-3).  Two terms of each would double its products, and A and dV in
+// fp32 take half as much memory again.
 //
-// 4 x 4096 steps of 32 heads of 64 x 128: the chain 264 us (tensor cores 47 %, its
-// products wait for one another), the blocks 301 (issue 43 %, shared memory 48 %,
-// tensor cores 33 %; barriers are a fifth of the stalls: two thread blocks of eight
+// 4 x 4096 steps of 32 heads of 64 x 128: the chain 267 us (tensor cores 47 %, its
+// products wait for one another), the blocks 307 (issue 44 %, shared memory 47 %,
+// tensor cores 32 %; barriers are a fifth of the stalls: two thread blocks of eight
 // warps are all that a SM's shared memory holds).
 #include "delta_mma.cuh"
 

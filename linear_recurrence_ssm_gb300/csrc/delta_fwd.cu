@@ -11,15 +11,22 @@
 // N and P come from pairs_kernel.  One thread asks for the tensor copies of the
 // next block: memory takes its 64 KB slower than warps can ask for them piece by
 // piece (a chain that did so stood still for 1000 of 6300 cycles, its outputs
-// for 3500).  4 x 4096 steps of 32 heads of 64 x 128 take 196 us, 3.06 a block of
+// for 3500).  4 x 4096 steps of 32 heads of 64 x 128 take 201 us, 3.1 a block of
 // 64 steps: the tensor cores are busy 51 % of it, and the rest is the chain's
 // dependent products (S K^T, N beta W, E U K) waiting for one another.
 //
 // Operands of the state's own chain (S, beta W, N, E U) go into the tensor
-// cores as two bf16 terms, 16 bits, so that the final state is good to 2^-17
-// an operand (fp32 states come out within 1e-5); K and Q are bf16 as given.
-// What only y sees (S in S Q^T, U and P in U P) is one term: 2^-9 beside y's
-// own rounding.
+// cores as two bf16 terms, 16 bits, without the low terms' product: 2^-17 of an
+// operand.  States of 200 steps come out within 1.4e-5 of the 64-bit ones for
+// beta up to 1, also where keys are all the same; for beta near 2 and keys alike,
+// where sums over N cancel, within 3e-5 (beta 1.9, keys 0.2 apart) and 1.3e-4
+// (beta 2, keys all the same; fp32 there 7e-6).  All 24 bits would cost twice
+// the chain's products.  K and Q are bf16 as given.
+// What y alone sees (S in S Q^T, U and P in U P) is one term, rounded by up to
+// 2^-8 of itself as y is: y comes out within 3.4e-3 in the 2-norm where its own
+// rounding gives 1.7e-3, and two terms would double the outputs' products.
+// What is kept for the gradients (S before a block, x) is rounded once to the
+// inputs' type, half of what fp32 would have to be kept and read.
 #include "delta_mma.cuh"
 
 namespace ssm {

@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(kThreads) fold_kernel(const BwdArgs<T> p) {
 }
 
 static int slices(const Shape &s, int rows) { return (s.V + rows - 1) / rows; }
-// 16 rows a thread block where 32 would leave some of the 152 SMs idle (3 x 333
+// 16 rows a thread block where 32 would leave some of a GB300's 152 SMs idle (3 x 333
 // steps of 5 heads of 40 x 96, forward and back: 284 us with 32, 257 with 16; with
 // the SMs full, 32 rows read K and Q half as often).
 static int rows_of(const Shape &s) { return int64_t(s.n) * s.H * slices(s, 32) < 152 ? 16 : 32; }

@@ -410,8 +410,8 @@ __device__ __forceinline__ void put_block(const float (&c)[N][4], float *to) {
 //   N21 = (I - N22 beta2) A21 (I - beta1 N11),
 // in matrix products on all 24 bits of either side: the chains take 16 bits of N,
 // but with beta near 2 and keys alike what is joined cancels (on 16 bits N was off
-// by 2e-4, and the state with it).  Multiply-adds there were bound by their
-// shared-memory operands.  128 threads.
+// by 2e-4, the state by 1.2e-3; 8192 blocks took 131 us in place of 139).
+// Multiply-adds there were bound by their shared-memory operands.  128 threads.
 __device__ __forceinline__ void lower_solve(float *m, const float *beta, int tid) {
     const int warp = tid / 32;
     {
@@ -558,7 +558,8 @@ inline bool fits_bwd(const Shape &s) { return fits(s) && s.V <= 128; }
 // values, at most one a SM at a time.  In parts, every block is walked about
 // twice more (its own 64 rows and the K rows that its turning of the state
 // takes, then the outputs), so that parts pay where the chains fill a small
-// share of the 152 SMs.  The bound lies between the sizes measured on either
+// share of the SMs, 152 as on every GB300 (the size functions follow the same
+// rule and need no device; results are right whatever a GPU has).  The bound lies between the sizes measured on either
 // side, calls of one sequence, whole against in parts:
 //   16384 steps, K = V = 128: 8 heads 743 / 287 us, 24 heads 815 / 667, 32 heads 850 / 888
 //   4096 steps,  K = V = 128: 8 heads 194 / 128, 16 heads 203 / 167, 32 heads 220 / 259

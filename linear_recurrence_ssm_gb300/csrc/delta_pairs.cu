@@ -6,8 +6,8 @@
 // are shared by the slices of a head's values and by both passes of a long
 // sequence; made by extra warps of the chains' own thread blocks they held the
 // chains up (6.5 us a block of 64 steps instead of the chain's own time).  8192
-// blocks of K = 128 take 131 us, with P's second term 142: shared memory's
-// accesses, 60 % of what it can serve, and the solves' barriers.
+// blocks of K = 128 take 139 us, with P's second term 149: shared memory's
+// accesses, 57 % of what it can serve, and the solves' barriers.
 #include "delta_mma.cuh"
 
 namespace ssm {
