@@ -501,13 +501,13 @@ SSM_API ssm_status_t state_pages_compact(void *pool, uint8_t *used, int32_t *mov
  *          the caller's, 16-byte aligned; unspecified afterwards
  * The state and every sum are fp32, and with fp32 inputs so is all work.  bf16
  * inputs: the tensor cores' operands are the state's in 16 bits (h_final comes
- * out within about 1e-5), for y alone in 8 (y is off by twice its own rounding,
- * 3.4e-3 in the 2-norm, and so are dq, dk and dg); K, V that they do not take
- * (K > 128 or no multiple of 8, V no multiple of 8, gradients of V > 128) are
- * computed as fp32.  A NaN or an infinity in a step's
- * inputs makes the outputs of that head's whole block of 64 steps unspecified,
- * and of everything behind it in the same sequence up to a step of a later block
- * that drops the state; no other sequence.
+ * out within about 1e-5), for y alone in 8 (y is off by about twice its own
+ * rounding, 3.4e-3 to 4e-3 in the 2-norm, and so are dq, dk and dg); heads that
+ * they do not take (K > 128 or no multiple of 8, V no multiple of 8, gradients
+ * of V > 128) are computed in fp32.
+ * A NaN or an infinity in a step's inputs makes the outputs of that head's whole
+ * block of 64 steps unspecified, and of everything behind it in the same
+ * sequence up to a step of a later block that drops the state; no other sequence.
  * Supported (SSM_ERR_UNSUPPORTED otherwise): K, V <= 256.  G divides H.  No
  * output may overlap an input or another output.
  * Every pointer is aligned to its element size (SSM_ERR_ALIGNMENT).

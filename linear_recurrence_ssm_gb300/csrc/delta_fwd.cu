@@ -23,8 +23,8 @@
 // (beta 2, keys all the same; fp32 there 7e-6).  All 24 bits would cost twice
 // the chain's products.  K and Q are bf16 as given.
 // What y alone sees (S in S Q^T, U and P in U P) is one term, rounded by up to
-// 2^-8 of itself as y is: y comes out within 3.4e-3 in the 2-norm where its own
-// rounding gives 1.7e-3, and two terms would double the outputs' products.
+// 2^-8 of itself as y is: y comes out within 3.4e-3 to 4e-3 in the 2-norm where
+// its own rounding gives 1.7e-3, and two terms would double the outputs' products.
 // What is kept for the gradients (S before a block, x) is rounded once to the
 // inputs' type, half of what fp32 would have to be kept and read.
 #include "delta_mma.cuh"

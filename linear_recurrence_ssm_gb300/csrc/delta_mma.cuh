@@ -559,8 +559,9 @@ inline bool fits_bwd(const Shape &s) { return fits(s) && s.V <= 128; }
 // twice more (its own 64 rows and the K rows that its turning of the state
 // takes, then the outputs), so that parts pay where the chains fill a small
 // share of the SMs, 152 as on every GB300 (the size functions follow the same
-// rule and need no device; results are right whatever a GPU has).  The bound lies between the sizes measured on either
-// side, calls of one sequence, whole against in parts:
+// rule and need no device; results are right whatever a GPU has).  The bound lies
+// between the sizes measured on either side, calls of one sequence, whole against
+// in parts:
 //   16384 steps, K = V = 128: 8 heads 743 / 287 us, 24 heads 815 / 667, 32 heads 850 / 888
 //   4096 steps,  K = V = 128: 8 heads 194 / 128, 16 heads 203 / 167, 32 heads 220 / 259
 //   16384 steps, K = 128, V = 64: 16 heads 777 / 364, 32 heads 841 / 694
